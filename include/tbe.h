@@ -323,6 +323,139 @@ int tbe_per_sample_weight_grad(tbe_handle* h, const void* indices, const void* o
                                int32_t index_dtype, int64_t num_indices, int32_t batch_size,
                                const float* grad_out, float* grad_weights, void* stream);
 
+/* ------------------------------------------- attention over user histories */
+
+/* Operators on ragged runs of looked-up rows.  A user's history is a run of
+ * tokens (events); a batch holds B histories one after another, history b
+ * being tokens [offsets[b], offsets[b+1]) of N (CSR, as the lookups' batch:
+ * B+1 offsets, int32 or int64, from 0 to N, never decreasing).
+ *
+ * With H query heads and Hk key-value heads (H a multiple of Hk; query head h
+ * reads key-value head h / (H/Hk)), tokens i and j of one history and the
+ * distance d = i - j:
+ *   visible(i, j):  0 <= d  and  (window == 0  or  d < window  or  j < sinks)
+ *   logit_ij = scale * q_i . k_j + bias[bucket(d), h]
+ *   p_ij = exp(logit_ij) / sum over visible j' of exp(logit_ij')
+ *   out_i = sum over visible j of p_ij v_j
+ * bucket(d) is the last bucket whose first distance is <= d.  The bias table
+ * [buckets, H] is learned: the backward call gives its gradient.
+ *
+ * dtype: fp32, fp16 or bf16, of q, k, v, bias, out, the upstream gradient,
+ * the gradients and the cache alike.  Logits, softmax statistics and sums are
+ * fp32; results are rounded once to dtype.  With 16-bit types the softmax
+ * weights and the logits' gradients are rounded to dtype where they enter a
+ * tensor-core product (their sums stay fp32), as the operands of every
+ * 16-bit matrix product are.  fp16 gradients below fp16's range are lost, as
+ * always in fp16: scale the loss.
+ *
+ * A row with no visible key (every visible bias entry -inf, or an empty
+ * cache) gives 0 and has zero gradients.  Keys and values of a history's
+ * own tokens are expected to be finite; what lies outside a history or
+ * behind a cache's length is never used, whatever its bits are.
+ *
+ * Results are deterministic: every sum has a fixed order.
+ *
+ * Limits: N < 2^30; B < 2^24; head_dim in [1, 256]; H <= 1024; sinks <= 128;
+ * at most 256 buckets with first distances <= 65535; at most 2^31 - 1
+ * (tile, head) pairs, with ceil(N/32) + B tiles at most.  A handle follows
+ * the rules of tbe_handle: one device, one stream at a time. */
+typedef struct {
+    int32_t dtype;    /* tbe_dtype */
+    int32_t heads;    /* H */
+    int32_t kv_heads; /* Hk */
+    int32_t head_dim; /* D */
+    int32_t window;   /* newest tokens seen, the query's own included; 0: all */
+    int32_t sinks;    /* first tokens that stay visible */
+    float scale;
+    int32_t num_buckets;          /* 0: no bias */
+    const int32_t* bucket_starts; /* host [num_buckets]: first distance of each
+                                     bucket, rising, beginning with 0 */
+} tbe_attention_config;
+
+/* Rows of a token operand: the D elements of (token, head) are consecutive
+ * and start at data + token*token_stride + head*head_stride (strides in
+ * elements, >= 0).  The fastest path wants 16-byte aligned rows and
+ * D*sizeof(dtype) a multiple of 16. */
+typedef struct {
+    const void* data; /* device */
+    int64_t token_stride;
+    int64_t head_stride;
+} tbe_rows;
+
+/* A paged cache: the row of (page, token of the page, key-value head) starts
+ * at data + page*page_stride + token*token_stride + head*head_stride. */
+typedef struct {
+    void* data; /* device */
+    int64_t page_stride;
+    int64_t token_stride;
+    int64_t head_stride;
+} tbe_pages;
+
+typedef struct tbe_attention tbe_attention;
+
+/* Creates a handle (a device block of 16 bytes, the buckets' map and their
+ * first distances).  Errors: INVALID_ARG, UNSUPPORTED (limits), NO_MEMORY,
+ * CUDA. */
+int tbe_attention_create(const tbe_attention_config* config, tbe_attention** out);
+void tbe_attention_destroy(tbe_attention* h);
+
+/* Bytes of workspace of a forward call (backward = 0) or a backward call
+ * (backward = 1, enough for the forward too) of N tokens in B histories; 0
+ * for arguments outside the limits. */
+size_t tbe_attention_workspace_bytes(const tbe_attention* h, int64_t num_tokens, int32_t batch_size,
+                                     int32_t backward);
+
+/* out: device dtype [N, H, D], contiguous.  lse: device fp32 [H, N], kept for
+ * the backward call: log2 of each row's sum of 2^(logit * log2 e); -inf for a
+ * row that sees nothing.  bias: device dtype [buckets, H] contiguous, or
+ * NULL where num_buckets is 0.  A history with malformed offsets is left
+ * out (TBE_ERR_BAD_OFFSETS by tbe_attention_get_error). */
+int tbe_attention_forward(tbe_attention* h, const tbe_rows* q, const tbe_rows* k, const tbe_rows* v,
+                          const void* bias, const void* offsets, int32_t index_dtype, int64_t num_tokens,
+                          int32_t batch_size, void* out, float* lse, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/* Gradients from the forward call's out and lse and the upstream gradient
+ * grad_out: grad_q [N, H, D], grad_k and grad_v [N, Hk, D] (contiguous, fully
+ * written where the offsets are well formed; a shared key-value head's
+ * gradient is the sum over its query heads), grad_bias [buckets, H] (written,
+ * not added to; NULL where num_buckets is 0). */
+int tbe_attention_backward(tbe_attention* h, const tbe_rows* q, const tbe_rows* k, const tbe_rows* v,
+                           const void* bias, const void* offsets, int32_t index_dtype, int64_t num_tokens,
+                           int32_t batch_size, const void* out, const float* lse, const tbe_rows* grad_out,
+                           void* grad_q, void* grad_k, void* grad_v, void* grad_bias, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/* Writes new tokens' keys and values into the cache.  The new tokens of
+ * history b are [offsets[b], offsets[b+1]) of N; the first goes to position
+ * before[b] (device int32 [B]: the tokens that the cache holds already).
+ * block_table: device int32 [B, table_width]; page block_table[b, j /
+ * page_size] holds token j.  A position or page out of range is skipped and
+ * reported as TBE_ERR_INDEX_OOB by tbe_attention_get_error.  Needs
+ * table_width * page_size < 2^31. */
+int tbe_attention_append(tbe_attention* h, const tbe_rows* k, const tbe_rows* v, const void* offsets,
+                         int32_t index_dtype, int64_t num_tokens, int32_t batch_size, const int32_t* before,
+                         const tbe_pages* k_pages, const tbe_pages* v_pages, int32_t num_pages,
+                         int32_t page_size, const int32_t* block_table, int32_t table_width, void* stream);
+
+/* Attention of each history's newest token over its cache: q holds one token
+ * per history, lengths (device int32 [B]) the tokens in the cache with the
+ * newest (its distance to token j is lengths[b] - 1 - j).  out: device dtype
+ * [B, H, D], contiguous.  Histories longer than a chunk are split over CTAs
+ * and joined; max_length (an upper bound of the lengths; 0: table_width *
+ * page_size) only sizes the chunks and the workspace: a length above
+ * table_width * page_size or below 0 gives zeros, and one above max_length is
+ * refused in the same way (TBE_ERR_INDEX_OOB by tbe_attention_get_error). */
+size_t tbe_attention_decode_workspace_bytes(const tbe_attention* h, int32_t batch_size, int64_t max_length);
+int tbe_attention_decode(tbe_attention* h, const tbe_rows* q, const tbe_pages* k_pages,
+                         const tbe_pages* v_pages, int32_t num_pages, int32_t page_size,
+                         const int32_t* block_table, int32_t table_width, const int32_t* lengths,
+                         int32_t batch_size, int64_t max_length, const void* bias, void* out, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
+/* As tbe_get_error, for an attention handle. */
+int tbe_attention_get_error(tbe_attention* h, void* stream);
+
 /* ------------------------------------------------------------- diagnostics */
 
 /* Synchronises `stream`, returns the first device-detected error since the

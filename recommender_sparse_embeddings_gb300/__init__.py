@@ -11,6 +11,7 @@ call raises; there is no other implementation to fall back on.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import re
 from typing import List, Optional, Sequence
@@ -68,6 +69,22 @@ class WorkspaceLayout(ctypes.Structure):
                 ("num_unique", ctypes.c_uint64), ("total_bytes", ctypes.c_uint64)]
 
 
+class _AttentionConfig(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("window", ctypes.c_int32), ("sinks", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("num_buckets", ctypes.c_int32),
+                ("bucket_starts", ctypes.POINTER(ctypes.c_int32))]
+
+
+class _Rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class _Pages(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
 _lib = None
 
 
@@ -85,6 +102,7 @@ def load_library():
             f"{LIB_PATH} is missing: build it first (python -c 'import __graft_entry__ as g; g.build()')")
     lib = ctypes.CDLL(LIB_PATH)
     P, i32, i64, u32, f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint32, ctypes.c_float
+    R, G = ctypes.POINTER(_Rows), ctypes.POINTER(_Pages)
     sig = {
         "tbe_create": ([ctypes.POINTER(_Table), i32, i32, u32, ctypes.POINTER(P)], ctypes.c_int),
         "tbe_destroy": ([P], None),
@@ -100,6 +118,17 @@ def load_library():
                                           ctypes.c_size_t, P], ctypes.c_int),
         "tbe_backward_sgd_noalloc": ([P, P, P, i32, i64, i32, P, P, f32, P], ctypes.c_int),
         "tbe_per_sample_weight_grad": ([P, P, P, i32, i64, i32, P, P, P], ctypes.c_int),
+        "tbe_attention_create": ([ctypes.POINTER(_AttentionConfig), ctypes.POINTER(P)], ctypes.c_int),
+        "tbe_attention_destroy": ([P], None),
+        "tbe_attention_workspace_bytes": ([P, i64, i32, i32], ctypes.c_size_t),
+        "tbe_attention_forward": ([P, R, R, R, P, P, i32, i64, i32, P, P, P, ctypes.c_size_t, P], ctypes.c_int),
+        "tbe_attention_backward": ([P, R, R, R, P, P, i32, i64, i32, P, P, R, P, P, P, P, P, ctypes.c_size_t, P],
+                                   ctypes.c_int),
+        "tbe_attention_append": ([P, R, R, P, i32, i64, i32, P, G, G, i32, i32, P, i32, P], ctypes.c_int),
+        "tbe_attention_decode_workspace_bytes": ([P, i32, i64], ctypes.c_size_t),
+        "tbe_attention_decode": ([P, R, G, G, i32, i32, P, i32, P, i32, i64, P, P, P, ctypes.c_size_t, P],
+                                 ctypes.c_int),
+        "tbe_attention_get_error": ([P, P], ctypes.c_int),
         "tbe_get_error": ([P, P], ctypes.c_int),
         "tbe_strerror": ([ctypes.c_int], ctypes.c_char_p),
         "tbe_last_cuda_error": ([], ctypes.c_int),
@@ -330,6 +359,258 @@ def tbe_get_error(h: Handle, stream=None) -> int:
     return int(load_library().tbe_get_error(h.ptr, _stream(stream)))
 
 
+# ------------------------------------------------- attention over histories
+
+
+class AttentionHandle:
+    """A created attention handle; ``close()`` (or garbage collection) calls
+    tbe_attention_destroy."""
+
+    def __init__(self, ptr: ctypes.c_void_p, heads: int, kv_heads: int, head_dim: int, dtype: torch.dtype,
+                 buckets: int):
+        self._ptr = ptr
+        self.heads, self.kv_heads, self.head_dim = heads, kv_heads, head_dim
+        self.dtype, self.buckets = dtype, buckets
+
+    @property
+    def ptr(self):
+        if self._ptr is None:
+            raise RuntimeError("handle already destroyed")
+        return self._ptr
+
+    def close(self):
+        if self._ptr is not None and _lib is not None:
+            _lib.tbe_attention_destroy(self._ptr)
+        self._ptr = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def tbe_relative_buckets(num_buckets: int, max_distance: int) -> List[int]:
+    """First distance of each bucket of a learned relative position bias: one
+    distance per bucket in the first half, then growing by a constant factor;
+    distances of max_distance and more share the last bucket."""
+    if num_buckets < 1 or max_distance < num_buckets:
+        raise ValueError("needs 1 <= num_buckets <= max_distance")
+    single = max(1, num_buckets // 2)
+    starts = list(range(min(single, num_buckets)))
+    wide = num_buckets - single
+    for i in range(wide):
+        at = max_distance if i == wide - 1 else math.ceil(
+            single * (max_distance / single) ** (i / (wide - 1)) - 1e-9)
+        starts.append(max(starts[-1] + 1, at))
+    return starts
+
+
+def tbe_attention_create(heads: int, kv_heads: int, head_dim: int, dtype: torch.dtype, window: int = 0,
+                         sinks: int = 0, bucket_starts: Optional[Sequence[int]] = None,
+                         scale: Optional[float] = None) -> AttentionHandle:
+    """Attention over ragged histories: each token sees the ``window`` newest
+    tokens up to itself (0: all) and the first ``sinks``; ``bucket_starts``
+    (see tbe_relative_buckets) adds a learned bias by distance; ``scale``
+    defaults to head_dim ** -0.5."""
+    if dtype not in _DTYPES:
+        raise ValueError("dtype must be fp32, fp16 or bf16")
+    lib = load_library()
+    n = 0 if bucket_starts is None else len(bucket_starts)
+    starts = (ctypes.c_int32 * max(n, 1))(*(bucket_starts or ()))
+    cfg = _AttentionConfig(_DTYPES[dtype], heads, kv_heads, head_dim, window, sinks,
+                           head_dim ** -0.5 if scale is None else scale, n, starts)
+    out = ctypes.c_void_p()
+    _check(lib.tbe_attention_create(ctypes.byref(cfg), ctypes.byref(out)), "tbe_attention_create")
+    return AttentionHandle(out, heads, kv_heads, head_dim, dtype, n)
+
+
+def tbe_attention_destroy(h: AttentionHandle):
+    h.close()
+
+
+def _rows(h: AttentionHandle, t: torch.Tensor, tokens: int, heads: int, name: str) -> _Rows:
+    if t.dim() != 3 or t.shape[0] != tokens or t.shape[1] != heads or t.shape[2] != h.head_dim:
+        raise ValueError(f"{name}: expected [{tokens}, {heads}, {h.head_dim}], got {list(t.shape)}")
+    if t.dtype != h.dtype:
+        raise ValueError(f"{name}: expected {h.dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    st = t.stride()
+    if st[2] != 1 and h.head_dim > 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return _Rows(t.data_ptr(), st[0], st[1])
+
+
+def _pages(h: AttentionHandle, t: torch.Tensor, name: str) -> _Pages:
+    if t.dim() != 4 or t.shape[2] != h.kv_heads or t.shape[3] != h.head_dim:
+        raise ValueError(f"{name}: expected [pages, page size, {h.kv_heads}, {h.head_dim}], got {list(t.shape)}")
+    if t.dtype != h.dtype:
+        raise ValueError(f"{name}: expected {h.dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    st = t.stride()
+    if st[3] != 1 and h.head_dim > 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return _Pages(t.data_ptr(), st[0], st[1], st[2])
+
+
+def _bias(h: AttentionHandle, bias: Optional[torch.Tensor]):
+    if (bias is None) != (h.buckets == 0):
+        raise ValueError("bias must be given exactly where the handle has buckets")
+    if bias is None:
+        return None
+    if tuple(bias.shape) != (h.buckets, h.heads) or bias.dtype != h.dtype:
+        raise ValueError(f"bias: expected {h.dtype} [{h.buckets}, {h.heads}]")
+    return _ptr(bias)
+
+
+def _offsets(offsets: torch.Tensor) -> int:
+    if offsets.dim() != 1 or offsets.numel() < 1 or offsets.dtype not in (torch.int32, torch.int64):
+        raise ValueError("offsets must be a 1-D int32 or int64 tensor of B+1 entries")
+    return TBE_I64 if offsets.dtype == torch.int64 else TBE_I32
+
+
+def _result(t: Optional[torch.Tensor], shape, dtype, device, name: str) -> torch.Tensor:
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise ValueError(f"{name}: expected {dtype} {list(shape)}")
+    return t
+
+
+def _int32(t: torch.Tensor, shape, name: str):
+    if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected int32 {list(shape)}")
+    return _ptr(t)
+
+
+def tbe_attention_workspace_bytes(h: AttentionHandle, num_tokens: int, batch_size: int,
+                                  backward: bool = False) -> int:
+    return int(load_library().tbe_attention_workspace_bytes(h.ptr, num_tokens, batch_size, int(backward)))
+
+
+def make_attention_workspace(h: AttentionHandle, num_tokens: int, batch_size: int, backward: bool = False,
+                             device=None) -> torch.Tensor:
+    """Workspace of forward calls (``backward``: of both) up to this size."""
+    n = tbe_attention_workspace_bytes(h, num_tokens, batch_size, backward)
+    if n == 0:
+        raise TBEError(TBE_ERR_UNSUPPORTED, "tbe_attention_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def tbe_attention_forward(h: AttentionHandle, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                          offsets: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                          out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                          workspace: Optional[torch.Tensor] = None, stream=None):
+    """q [N, H, D], k and v [N, Hk, D] of the batch's histories (strided rows
+    are fine), offsets [B+1]; returns (out [N, H, D], lse [H, N])."""
+    n, b = int(q.shape[0]), offsets.numel() - 1
+    rq, rk, rv = _rows(h, q, n, h.heads, "q"), _rows(h, k, n, h.kv_heads, "k"), _rows(h, v, n, h.kv_heads, "v")
+    it, pb = _offsets(offsets), _bias(h, bias)
+    out = _result(out, (n, h.heads, h.head_dim), h.dtype, q.device, "out")
+    lse = _result(lse, (h.heads, n), torch.float32, q.device, "lse")
+    if workspace is None:
+        workspace = make_attention_workspace(h, n, b, False, q.device)
+    rc = load_library().tbe_attention_forward(h.ptr, rq, rk, rv, pb, _ptr(offsets), it, n, b, _ptr(out), _ptr(lse),
+                                              _ptr(workspace), workspace.numel(), _stream(stream))
+    _check(rc, "tbe_attention_forward")
+    return out, lse
+
+
+def tbe_attention_backward(h: AttentionHandle, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                           offsets: torch.Tensor, out: torch.Tensor, lse: torch.Tensor, grad_out: torch.Tensor,
+                           bias: Optional[torch.Tensor] = None, grad_q: Optional[torch.Tensor] = None,
+                           grad_k: Optional[torch.Tensor] = None, grad_v: Optional[torch.Tensor] = None,
+                           grad_bias: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                           stream=None):
+    """Gradients (grad_q, grad_k, grad_v, grad_bias) from a forward call's out
+    and lse and the upstream gradient; grad_bias is None without buckets."""
+    n, b, d = int(q.shape[0]), offsets.numel() - 1, h.head_dim
+    rq, rk, rv = _rows(h, q, n, h.heads, "q"), _rows(h, k, n, h.kv_heads, "k"), _rows(h, v, n, h.kv_heads, "v")
+    rg = _rows(h, grad_out, n, h.heads, "grad_out")
+    it, pb = _offsets(offsets), _bias(h, bias)
+    _result(out, (n, h.heads, d), h.dtype, q.device, "out")
+    _result(lse, (h.heads, n), torch.float32, q.device, "lse")
+    grad_q = _result(grad_q, (n, h.heads, d), h.dtype, q.device, "grad_q")
+    grad_k = _result(grad_k, (n, h.kv_heads, d), h.dtype, q.device, "grad_k")
+    grad_v = _result(grad_v, (n, h.kv_heads, d), h.dtype, q.device, "grad_v")
+    if h.buckets:
+        grad_bias = _result(grad_bias, (h.buckets, h.heads), h.dtype, q.device, "grad_bias")
+    elif grad_bias is not None:
+        raise ValueError("grad_bias without buckets")
+    if workspace is None:
+        workspace = make_attention_workspace(h, n, b, True, q.device)
+    rc = load_library().tbe_attention_backward(
+        h.ptr, rq, rk, rv, pb, _ptr(offsets), it, n, b, _ptr(out), _ptr(lse), rg, _ptr(grad_q), _ptr(grad_k),
+        _ptr(grad_v), _ptr(grad_bias), _ptr(workspace), workspace.numel(), _stream(stream))
+    _check(rc, "tbe_attention_backward")
+    return grad_q, grad_k, grad_v, grad_bias
+
+
+def _cache(h: AttentionHandle, k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: torch.Tensor, b: int):
+    if k_pages.shape != v_pages.shape:
+        raise ValueError("k_pages and v_pages must have one shape")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, width]")
+    width = int(block_table.shape[1])
+    return (_pages(h, k_pages, "k_pages"), _pages(h, v_pages, "v_pages"), int(k_pages.shape[0]),
+            int(k_pages.shape[1]), _int32(block_table, (b, width), "block_table"), width)
+
+
+def tbe_attention_append(h: AttentionHandle, k: torch.Tensor, v: torch.Tensor, offsets: torch.Tensor,
+                         before: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                         block_table: torch.Tensor, stream=None):
+    """Writes new tokens' keys and values ([N, Hk, D], ragged by offsets) into
+    the paged cache ([pages, page size, Hk, D]) behind the ``before`` tokens
+    each history holds already; block_table [B, width] names its pages."""
+    n, b = int(k.shape[0]), offsets.numel() - 1
+    rk, rv = _rows(h, k, n, h.kv_heads, "k"), _rows(h, v, n, h.kv_heads, "v")
+    it = _offsets(offsets)
+    kp, vp, pages, size, table, width = _cache(h, k_pages, v_pages, block_table, b)
+    rc = load_library().tbe_attention_append(h.ptr, rk, rv, _ptr(offsets), it, n, b, _int32(before, (b,), "before"),
+                                             kp, vp, pages, size, table, width, _stream(stream))
+    _check(rc, "tbe_attention_append")
+
+
+def tbe_attention_decode_workspace_bytes(h: AttentionHandle, batch_size: int, max_length: int) -> int:
+    return int(load_library().tbe_attention_decode_workspace_bytes(h.ptr, batch_size, max_length))
+
+
+def make_attention_decode_workspace(h: AttentionHandle, batch_size: int, max_length: int,
+                                    device=None) -> torch.Tensor:
+    n = tbe_attention_decode_workspace_bytes(h, batch_size, max_length)
+    if n == 0:
+        raise TBEError(TBE_ERR_UNSUPPORTED, "tbe_attention_decode_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def tbe_attention_decode(h: AttentionHandle, q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                         block_table: torch.Tensor, lengths: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                         max_length: Optional[int] = None, out: Optional[torch.Tensor] = None,
+                         workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Attention of each history's newest token (q [B, H, D]) over its paged
+    cache of ``lengths`` tokens (the newest included); max_length, an upper
+    bound of them, defaults to the block table's room."""
+    b = int(q.shape[0])
+    rq, pb = _rows(h, q, b, h.heads, "q"), _bias(h, bias)
+    kp, vp, pages, size, table, width = _cache(h, k_pages, v_pages, block_table, b)
+    most = width * size if max_length is None else int(max_length)
+    out = _result(out, (b, h.heads, h.head_dim), h.dtype, q.device, "out")
+    if workspace is None:
+        workspace = make_attention_decode_workspace(h, b, most, q.device)
+    rc = load_library().tbe_attention_decode(h.ptr, rq, kp, vp, pages, size, table, width,
+                                             _int32(lengths, (b,), "lengths"), b, most, pb, _ptr(out),
+                                             _ptr(workspace), workspace.numel(), _stream(stream))
+    _check(rc, "tbe_attention_decode")
+    return out
+
+
+def tbe_attention_get_error(h: AttentionHandle, stream=None) -> int:
+    return int(load_library().tbe_attention_get_error(h.ptr, _stream(stream)))
+
+
 __all__ = [n for n in dir() if n.startswith("tbe_") or n.startswith("TBE_")] + [
     "Handle", "TBEError", "WorkspaceLayout", "load_library", "declared_functions",
-    "make_workspace", "library_path"]
+    "make_workspace", "library_path", "AttentionHandle", "make_attention_workspace",
+    "make_attention_decode_workspace"]

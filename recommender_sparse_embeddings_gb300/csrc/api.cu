@@ -12,8 +12,18 @@
 #include "tbe_internal.cuh"
 
 namespace tbe {
+
 cudaError_t launch_forward_schedule(TableDesc* tabs, int T, int B, cudaStream_t s);
+
+// The last failing CUDA call of this host thread, for tbe_last_cuda_error.
+static thread_local cudaError_t g_last_cuda_error = cudaSuccess;
+
+int cuda_fail(cudaError_t e) {
+    g_last_cuda_error = e;
+    return TBE_ERR_CUDA;
 }
+
+}  // namespace tbe
 
 using namespace tbe;
 
@@ -276,13 +286,6 @@ int check_batch(const tbe_handle* h, const void* indices, const void* offsets, i
     return TBE_OK;
 }
 
-// The last failing CUDA call of this host thread, for tbe_last_cuda_error.
-thread_local cudaError_t g_last_cuda_error = cudaSuccess;
-
-int cuda_fail(cudaError_t e) {
-    g_last_cuda_error = e;
-    return TBE_ERR_CUDA;
-}
 
 int cuda_status(cudaError_t e) { return e == cudaSuccess ? TBE_OK : cuda_fail(e); }
 

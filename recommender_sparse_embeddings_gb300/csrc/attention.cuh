@@ -1,0 +1,203 @@
+// Attention over ragged user histories: what its kernels share.
+//
+// A history is a run of L tokens; query i and key j of one history, with
+// distance d = i - j, see each other when
+//     0 <= d  and  (d < window  or  j < sinks)
+// and their logit is scale * q_i . k_j + bias[bucket(d)].  All kernels work
+// in base 2: logits are multiplied by log2(e) so that the softmax's
+// exponential is one ex2, and the saved statistic is
+//     lse_i = log2 sum_j 2^(logit_ij * log2 e).
+#pragma once
+
+#include <float.h>
+#include <limits.h>
+
+#include "tbe_internal.cuh"
+
+namespace tbe {
+
+constexpr float kLog2e = 1.4426950408889634f;
+// Limits of a handle (decode keeps the buckets of eight heads in shared memory).
+constexpr int kMaxBuckets = 256;
+constexpr int kMaxDistance = 65535;
+constexpr int kMaxSinks = 128;
+constexpr int kMaxHeadDim = 256;
+
+// Rows of one tensor operand: row (token, head) starts at
+// data + token * token_stride + head * head_stride (elements).
+struct Rows {
+    const void* data;
+    int64_t token_stride;
+    int64_t head_stride;
+};
+
+// One tile of one history (a work item of the forward and backward kernels).
+struct AttnItem {
+    int32_t start;  // the history's first token in the batch
+    int32_t len;    // its tokens
+    int32_t tile;   // the tile's number, counted from the history's start
+    int32_t tiles;  // tiles of the history
+};
+
+// First words of the handle's device block; the bucket map follows.
+struct AttnBlock {
+    uint32_t error;  // sticky ERR_* bits
+    uint32_t pad[3];
+    // uint16_t bucket_of[far + 1]
+};
+
+struct AttnShape {
+    int32_t dtype;
+    int32_t H, Hk, G;  // query heads, key-value heads, query heads per key-value head
+    int32_t D;
+    int32_t window;  // INT_MAX / 2 where every earlier token is visible
+    int32_t sinks;
+    int32_t buckets;  // 0: no bias
+    int32_t far;      // first distance of the last bucket
+    float scale;
+    const uint16_t* bucket_of;  // device [far + 1]
+    const int32_t* starts;      // device [buckets + 1], ending with INT_MAX
+    uint32_t* error;            // device
+};
+
+struct AttnForward {
+    AttnShape s;
+    Rows q, k, v;
+    const void* bias;  // [buckets, H] of dtype, or null
+    void* out;         // [N, H, D]
+    float* lse;        // [H, N]
+    int64_t N;
+    const AttnItem* items;
+    const int32_t* n_items;
+    int32_t vec;  // rows are 16-byte aligned and D * element size is a multiple of 16
+};
+
+struct AttnBackward {
+    AttnShape s;
+    Rows q, k, v, g;
+    const void* bias;
+    const void* out;   // [N, H, D]
+    const float* lse;  // [H, N]
+    void* gq;          // [N, H, D]
+    void* gk;          // [N, Hk, D]
+    void* gv;          // [N, Hk, D]
+    float* delta;      // workspace [H, N]: g_i . out_i
+    float* bias_part;  // workspace [items, H, buckets]
+    int64_t N;
+    const AttnItem* items;
+    const int32_t* n_items;
+    int32_t vec;
+};
+
+// Division by a number fixed per launch, for x < 2^31: with c = ceil(log2 n)
+// and m = ceil(2^(31 + c) / n) < 2^32, the error x * (m - 2^(31+c)/n) / 2^(31+c)
+// is below x / 2^(31+c) <= 1 / n, so x * m >> (31 + c) is the floor.
+struct FastDiv {
+    uint32_t n, m, s;
+};
+
+inline FastDiv make_fast_div(uint32_t n) {
+    uint32_t c = 0;
+    while ((uint64_t(1) << c) < n) ++c;
+    const uint64_t p = uint64_t(1) << (31 + c);
+    return FastDiv{n, (uint32_t)((p + n - 1) / n), 31 + c};
+}
+
+__host__ __device__ __forceinline__ uint32_t fast_div(uint32_t x, FastDiv d) {
+    return (uint32_t)(((uint64_t)x * d.m) >> d.s);
+}
+
+struct AttnDecode {
+    AttnShape s;
+    Rows q;            // token = history of the batch
+    const void* kp;    // pages: row (page, token, head)
+    const void* vp;
+    int64_t k_page, k_token, k_head, v_page, v_token, v_head;  // strides (elements)
+    const int32_t* table;  // [B, width]
+    const int32_t* lengths;
+    const void* bias;
+    void* out;  // [B, H, D]
+    float* part;  // workspace [B, H, splits, D + 2] (D sums, max, sum of weights)
+    int32_t width, num_pages, B, chunk, splits;
+    int64_t max_length;
+    FastDiv page;
+    int32_t vec;
+};
+
+struct AttnAppend {
+    int32_t Hk, D, e;  // e: element bytes
+    Rows k, v;
+    const void* offsets;
+    int32_t index64;
+    const int32_t* before;
+    void* kp;
+    void* vp;
+    int64_t k_page, k_token, k_head, v_page, v_token, v_head;
+    const int32_t* table;
+    int32_t width, num_pages, B;
+    int64_t N;
+    FastDiv page;
+    uint32_t* error;
+    int32_t vec;
+};
+
+// 2^x by the special-function unit (relative error about 2^-22; 2^-inf = 0).
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// A bias entry in base 2.  The product of a type's lowest finite value with
+// log2(e) leaves fp32's range; it is held at fp32's lowest instead, so a row
+// whose visible keys all carry it keeps equal weights (an entry of -inf
+// stays -inf and hides its keys).
+__device__ __forceinline__ float bias_base2(float b) {
+    const float x = b * kLog2e;
+    return (x < -FLT_MAX && b >= -FLT_MAX) ? -FLT_MAX : x;
+}
+
+__device__ __forceinline__ bool attn_visible(int d, int j, int window, int sinks) {
+    return d >= 0 && (d < window || j < sinks);
+}
+
+// Whether key j is the only one that query i can see.  Its weight is 1
+// whatever the logit, so the logit's gradient is exactly 0, which dp - delta,
+// two sums of the same products in different orders, would miss by rounding.
+__device__ __forceinline__ bool attn_lone(int i, int j, int window, int sinks) {
+    return i == j && (i == 0 || (window == 1 && sinks == 0));
+}
+
+__device__ __forceinline__ int attn_bucket(const AttnShape& s, int d) {
+    return d >= s.far ? s.buckets - 1 : (int)__ldg(s.bucket_of + d);
+}
+
+template <int DT>
+struct Elem;
+template <>
+struct Elem<DT_F32> {
+    using type = float;
+};
+template <>
+struct Elem<DT_F16> {
+    using type = __half;
+};
+template <>
+struct Elem<DT_BF16> {
+    using type = __nv_bfloat16;
+};
+
+// Launchers (each returns the launch's status).
+cudaError_t launch_attn_items(const void* offsets, int index64, int64_t N, int B, int tile, AttnItem* items,
+                              int64_t capacity, int32_t* n_items, uint32_t* error, cudaStream_t s);
+cudaError_t launch_attn_forward_simt(const AttnForward& p, int64_t max_items, cudaStream_t s);
+cudaError_t launch_attn_backward_simt(const AttnBackward& p, int64_t max_items, cudaStream_t s);
+cudaError_t launch_attn_bias_reduce(const AttnBackward& p, void* grad_bias, cudaStream_t s);
+cudaError_t launch_attn_append(const AttnAppend& p, cudaStream_t s);
+cudaError_t launch_attn_decode(const AttnDecode& p, cudaStream_t s);
+cudaError_t attn_simt_configure(int optin_smem);
+int attn_simt_tile(int D);
+// query heads one decode CTA takes at once
+int attn_decode_heads(int G);
+
+}  // namespace tbe

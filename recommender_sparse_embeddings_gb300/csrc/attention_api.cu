@@ -1,0 +1,404 @@
+// C ABI of the attention operators: argument checks, the handle, the
+// workspaces' layout and the order of launches.  Declarations and contracts
+// are in include/tbe.h.
+#include <algorithm>
+#include <new>
+#include <vector>
+
+#include <nvtx3/nvToolsExt.h>
+
+#include "../../include/tbe.h"
+#include "attention.cuh"
+
+namespace tbe {
+int cuda_fail(cudaError_t e);
+}
+
+using namespace tbe;
+
+struct tbe_attention {
+    int device = 0;
+    int num_sms = 0;
+    AttnShape s{};
+    void* dev = nullptr;
+};
+
+namespace {
+
+struct CallRange {
+    explicit CallRange(const char* name) { nvtxRangePushA(name); }
+    ~CallRange() { nvtxRangePop(); }
+    CallRange(const CallRange&) = delete;
+    CallRange& operator=(const CallRange&) = delete;
+};
+
+size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
+
+int status(cudaError_t e) { return e == cudaSuccess ? TBE_OK : cuda_fail(e); }
+
+bool on_device(const tbe_attention* h) {
+    int d = -1;
+    return cudaGetDevice(&d) == cudaSuccess && d == h->device;
+}
+
+bool aligned16(const void* p) { return (uintptr_t)p % 16 == 0; }
+
+bool vec_rows(const tbe_attention* h, const tbe_rows& r) {
+    const int e = elem_bytes(h->s.dtype);
+    return aligned16(r.data) && r.token_stride * e % 16 == 0 && r.head_stride * e % 16 == 0 && h->s.D * e % 16 == 0;
+}
+
+bool vec_pages(const tbe_attention* h, const tbe_pages& r) {
+    const int e = elem_bytes(h->s.dtype);
+    return aligned16(r.data) && r.page_stride * e % 16 == 0 && r.token_stride * e % 16 == 0 &&
+           r.head_stride * e % 16 == 0 && h->s.D * e % 16 == 0;
+}
+
+bool rows_ok(const tbe_rows* r, int64_t n) {
+    return r && (n == 0 || r->data) && r->token_stride >= 0 && r->head_stride >= 0;
+}
+
+bool pages_ok(const tbe_pages* r) {
+    return r && r->data && r->page_stride >= 0 && r->token_stride >= 0 && r->head_stride >= 0;
+}
+
+Rows as_rows(const tbe_rows& r) { return Rows{r.data, r.token_stride, r.head_stride}; }
+
+bool batch_within_limits(const tbe_attention* h, int64_t N, int64_t B) {
+    if (N >= (int64_t(1) << 30) || B >= (int64_t(1) << 24)) return false;
+    return ((N + 31) / 32 + B) * h->s.H < (int64_t(1) << 31);
+}
+
+int check_batch(const tbe_attention* h, const void* offsets, int32_t index_dtype, int64_t N, int32_t B) {
+    if (!h || !on_device(h)) return TBE_ERR_INVALID_ARG;
+    if (index_dtype != TBE_I32 && index_dtype != TBE_I64) return TBE_ERR_INVALID_ARG;
+    if (N < 0 || B < 0 || !offsets || (B == 0 && N > 0)) return TBE_ERR_INVALID_ARG;
+    return batch_within_limits(h, N, B) ? TBE_OK : TBE_ERR_UNSUPPORTED;
+}
+
+struct Layout {
+    size_t n_items, items, delta, bias_part, total;
+    int64_t capacity;
+};
+
+// Laid out for the smallest tile any path of the handle's head_dim takes.
+Layout make_layout(const tbe_attention* h, int64_t N, int64_t B, bool backward) {
+    Layout L{};
+    L.capacity = N / attn_simt_tile(h->s.D) + B;
+    size_t o = 0;
+    auto take = [&](size_t bytes) {
+        const size_t at = o;
+        o = align_up(o + bytes);
+        return at;
+    };
+    L.n_items = take(sizeof(int32_t));
+    L.items = take(sizeof(AttnItem) * (size_t)L.capacity);
+    if (backward) {
+        L.delta = take(sizeof(float) * (size_t)N * h->s.H);
+        L.bias_part = take(sizeof(float) * (size_t)L.capacity * h->s.H * h->s.buckets);
+    }
+    L.total = o;
+    return L;
+}
+
+template <typename T>
+T* at(void* base, size_t offset) {
+    return reinterpret_cast<T*>(static_cast<char*>(base) + offset);
+}
+
+// Rows of a cache that a query sees at most.
+int64_t visible_most(const tbe_attention* h, int64_t max_length) {
+    return std::min<int64_t>(max_length, (int64_t)h->s.window + h->s.sinks);
+}
+
+struct Split {
+    int chunk, splits;
+};
+
+// Visible rows a decode CTA takes.  Whole histories where they are short or
+// there are many; else chunks of at least 256 rows (the join reads D + 2
+// floats per chunk and head, under 2 % of a chunk's rows), small enough that
+// the batch makes about 16 CTAs per SM, so that histories of uneven length
+// leave no SM idle.
+Split decode_split(const tbe_attention* h, int64_t B, int64_t max_length) {
+    const int64_t most = std::max<int64_t>(1, visible_most(h, max_length));
+    const int gt = attn_decode_heads(h->s.G);
+    const int64_t rows = std::max<int64_t>(1, B * h->s.Hk * ((h->s.G + gt - 1) / gt));
+    int64_t chunk = most * rows / ((int64_t)h->num_sms * 16);
+    chunk = std::max<int64_t>(256, (chunk + 63) / 64 * 64);
+    const int64_t splits = (most + chunk - 1) / chunk;
+    return Split{(int)std::min<int64_t>(chunk, INT_MAX / 2), (int)splits};
+}
+
+}  // namespace
+
+extern "C" {
+
+int tbe_attention_create(const tbe_attention_config* c, tbe_attention** out) {
+    CallRange range("tbe_attention_create");
+    if (!out) return TBE_ERR_INVALID_ARG;
+    *out = nullptr;
+    if (!c) return TBE_ERR_INVALID_ARG;
+    if (c->dtype != TBE_F32 && c->dtype != TBE_F16 && c->dtype != TBE_BF16) return TBE_ERR_INVALID_ARG;
+    if (c->heads <= 0 || c->kv_heads <= 0 || c->heads % c->kv_heads != 0 || c->head_dim <= 0 || c->window < 0 ||
+        c->sinks < 0 || c->num_buckets < 0 || !(c->scale - c->scale == 0.f))
+        return TBE_ERR_INVALID_ARG;
+    if (c->num_buckets > 0) {
+        if (!c->bucket_starts || c->bucket_starts[0] != 0) return TBE_ERR_INVALID_ARG;
+        if (c->num_buckets > kMaxBuckets) return TBE_ERR_UNSUPPORTED;
+        for (int b = 1; b < c->num_buckets; ++b)
+            if (c->bucket_starts[b] <= c->bucket_starts[b - 1]) return TBE_ERR_INVALID_ARG;
+        if (c->bucket_starts[c->num_buckets - 1] > kMaxDistance) return TBE_ERR_UNSUPPORTED;
+    }
+    if (c->head_dim > kMaxHeadDim || c->sinks > kMaxSinks || c->heads > 1024) return TBE_ERR_UNSUPPORTED;
+
+    tbe_attention* h = new (std::nothrow) tbe_attention();
+    if (!h) return TBE_ERR_NO_MEMORY;
+    AttnShape& s = h->s;
+    s.dtype = c->dtype;
+    s.H = c->heads;
+    s.Hk = c->kv_heads;
+    s.G = c->heads / c->kv_heads;
+    s.D = c->head_dim;
+    s.window = c->window == 0 ? INT_MAX / 2 : std::min(c->window, INT_MAX / 2);
+    s.sinks = c->sinks;
+    s.buckets = c->num_buckets;
+    s.scale = c->scale;
+    s.far = s.buckets > 0 ? c->bucket_starts[s.buckets - 1] : 0;
+    int optin = 0;
+    cudaError_t e = cudaGetDevice(&h->device);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, h->device);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, h->device);
+    if (e == cudaSuccess) e = attn_simt_configure(optin);
+    if (e != cudaSuccess) {
+        delete h;
+        return cuda_fail(e);
+    }
+    // device block: the error word, the buckets' first distances (one more,
+    // INT_MAX, ends the last), the bucket of every distance up to `far`
+    const size_t starts_at = sizeof(AttnBlock), map_at = starts_at + sizeof(int32_t) * (s.buckets + 1);
+    const size_t bytes = map_at + sizeof(uint16_t) * (s.far + 1);
+    try {
+        std::vector<unsigned char> img(bytes, 0);
+        int32_t* starts = reinterpret_cast<int32_t*>(img.data() + starts_at);
+        uint16_t* map = reinterpret_cast<uint16_t*>(img.data() + map_at);
+        for (int b = 0; b < s.buckets; ++b) starts[b] = c->bucket_starts[b];
+        starts[s.buckets] = INT_MAX;
+        for (int d = 0, b = 0; s.buckets > 0 && d <= s.far; ++d) {
+            while (starts[b + 1] <= d) ++b;
+            map[d] = (uint16_t)b;
+        }
+        e = cudaMalloc(&h->dev, bytes);
+        if (e == cudaSuccess) e = cudaMemcpy(h->dev, img.data(), bytes, cudaMemcpyHostToDevice);
+    } catch (const std::bad_alloc&) {
+        delete h;
+        return TBE_ERR_NO_MEMORY;
+    }
+    if (e != cudaSuccess) {
+        if (h->dev) cudaFree(h->dev);
+        delete h;
+        return e == cudaErrorMemoryAllocation ? TBE_ERR_NO_MEMORY : cuda_fail(e);
+    }
+    s.error = &static_cast<AttnBlock*>(h->dev)->error;
+    s.starts = at<int32_t>(h->dev, starts_at);
+    s.bucket_of = at<uint16_t>(h->dev, map_at);
+    *out = h;
+    return TBE_OK;
+}
+
+void tbe_attention_destroy(tbe_attention* h) {
+    if (!h) return;
+    if (h->dev) cudaFree(h->dev);
+    delete h;
+}
+
+size_t tbe_attention_workspace_bytes(const tbe_attention* h, int64_t N, int32_t B, int32_t backward) {
+    if (!h || N < 0 || B < 0 || !batch_within_limits(h, N, B)) return 0;
+    return make_layout(h, N, B, backward != 0).total;
+}
+
+int tbe_attention_forward(tbe_attention* h, const tbe_rows* q, const tbe_rows* k, const tbe_rows* v, const void* bias,
+                          const void* offsets, int32_t index_dtype, int64_t N, int32_t B, void* out, float* lse,
+                          void* workspace, size_t workspace_bytes, void* stream) {
+    CallRange range("tbe_attention_forward");
+    int rc = check_batch(h, offsets, index_dtype, N, B);
+    if (rc) return rc;
+    if (!rows_ok(q, N) || !rows_ok(k, N) || !rows_ok(v, N)) return TBE_ERR_INVALID_ARG;
+    if ((bias != nullptr) != (h->s.buckets > 0) || (N > 0 && (!out || !lse)) || !workspace)
+        return TBE_ERR_INVALID_ARG;
+    const Layout L = make_layout(h, N, B, false);
+    if (workspace_bytes < L.total) return TBE_ERR_WORKSPACE_TOO_SMALL;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    AttnForward p{};
+    p.s = h->s;
+    p.q = as_rows(*q);
+    p.k = as_rows(*k);
+    p.v = as_rows(*v);
+    p.bias = bias;
+    p.out = out;
+    p.lse = lse;
+    p.N = N;
+    p.items = at<AttnItem>(workspace, L.items);
+    p.n_items = at<int32_t>(workspace, L.n_items);
+    p.vec = vec_rows(h, *q) && vec_rows(h, *k) && vec_rows(h, *v) && aligned16(out);
+    const int tile = attn_simt_tile(h->s.D);
+    const int64_t most = N / tile + B;
+    rc = status(launch_attn_items(offsets, index_dtype == TBE_I64, N, B, tile, at<AttnItem>(workspace, L.items), most,
+                                  at<int32_t>(workspace, L.n_items), h->s.error, s));
+    if (rc || N == 0) return rc;
+    return status(launch_attn_forward_simt(p, most, s));
+}
+
+int tbe_attention_backward(tbe_attention* h, const tbe_rows* q, const tbe_rows* k, const tbe_rows* v, const void* bias,
+                           const void* offsets, int32_t index_dtype, int64_t N, int32_t B, const void* out,
+                           const float* lse, const tbe_rows* grad_out, void* grad_q, void* grad_k, void* grad_v,
+                           void* grad_bias, void* workspace, size_t workspace_bytes, void* stream) {
+    CallRange range("tbe_attention_backward");
+    int rc = check_batch(h, offsets, index_dtype, N, B);
+    if (rc) return rc;
+    if (!rows_ok(q, N) || !rows_ok(k, N) || !rows_ok(v, N) || !rows_ok(grad_out, N)) return TBE_ERR_INVALID_ARG;
+    if ((bias != nullptr) != (h->s.buckets > 0) || (grad_bias != nullptr) != (h->s.buckets > 0) || !workspace)
+        return TBE_ERR_INVALID_ARG;
+    if (N > 0 && (!out || !lse || !grad_q || !grad_k || !grad_v)) return TBE_ERR_INVALID_ARG;
+    const Layout L = make_layout(h, N, B, true);
+    if (workspace_bytes < L.total) return TBE_ERR_WORKSPACE_TOO_SMALL;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    AttnBackward p{};
+    p.s = h->s;
+    p.q = as_rows(*q);
+    p.k = as_rows(*k);
+    p.v = as_rows(*v);
+    p.g = as_rows(*grad_out);
+    p.bias = bias;
+    p.out = out;
+    p.lse = lse;
+    p.gq = grad_q;
+    p.gk = grad_k;
+    p.gv = grad_v;
+    p.delta = at<float>(workspace, L.delta);
+    p.bias_part = at<float>(workspace, L.bias_part);
+    p.N = N;
+    p.items = at<AttnItem>(workspace, L.items);
+    p.n_items = at<int32_t>(workspace, L.n_items);
+    p.vec = vec_rows(h, *q) && vec_rows(h, *k) && vec_rows(h, *v) && vec_rows(h, *grad_out) && aligned16(out) &&
+            aligned16(grad_q) && aligned16(grad_k) && aligned16(grad_v);
+    const int tile = attn_simt_tile(h->s.D);
+    const int64_t most = N / tile + B;
+    rc = status(launch_attn_items(offsets, index_dtype == TBE_I64, N, B, tile, at<AttnItem>(workspace, L.items), most,
+                                  at<int32_t>(workspace, L.n_items), h->s.error, s));
+    if (rc) return rc;
+    if (N > 0) rc = status(launch_attn_backward_simt(p, most, s));
+    if (rc || !bias) return rc;
+    return status(launch_attn_bias_reduce(p, grad_bias, s));
+}
+
+int tbe_attention_append(tbe_attention* h, const tbe_rows* k, const tbe_rows* v, const void* offsets,
+                         int32_t index_dtype, int64_t N, int32_t B, const int32_t* before, const tbe_pages* k_pages,
+                         const tbe_pages* v_pages, int32_t num_pages, int32_t page_size, const int32_t* block_table,
+                         int32_t table_width, void* stream) {
+    CallRange range("tbe_attention_append");
+    const int rc = check_batch(h, offsets, index_dtype, N, B);
+    if (rc) return rc;
+    if (!rows_ok(k, N) || !rows_ok(v, N) || !pages_ok(k_pages) || !pages_ok(v_pages)) return TBE_ERR_INVALID_ARG;
+    if (num_pages < 0 || page_size <= 0 || table_width < 0 || (B > 0 && (!before || (table_width > 0 && !block_table))))
+        return TBE_ERR_INVALID_ARG;
+    if ((int64_t)table_width * page_size >= (int64_t(1) << 31)) return TBE_ERR_UNSUPPORTED;
+    if (N == 0) return TBE_OK;
+    AttnAppend p{};
+    p.Hk = h->s.Hk;
+    p.D = h->s.D;
+    p.e = elem_bytes(h->s.dtype);
+    p.k = as_rows(*k);
+    p.v = as_rows(*v);
+    p.offsets = offsets;
+    p.index64 = index_dtype == TBE_I64;
+    p.before = before;
+    p.kp = k_pages->data;
+    p.vp = v_pages->data;
+    p.k_page = k_pages->page_stride;
+    p.k_token = k_pages->token_stride;
+    p.k_head = k_pages->head_stride;
+    p.v_page = v_pages->page_stride;
+    p.v_token = v_pages->token_stride;
+    p.v_head = v_pages->head_stride;
+    p.table = block_table;
+    p.width = table_width;
+    p.num_pages = num_pages;
+    p.B = B;
+    p.N = N;
+    p.page = make_fast_div((uint32_t)page_size);
+    p.error = h->s.error;
+    p.vec = vec_rows(h, *k) && vec_rows(h, *v) && vec_pages(h, *k_pages) && vec_pages(h, *v_pages);
+    return status(launch_attn_append(p, static_cast<cudaStream_t>(stream)));
+}
+
+size_t tbe_attention_decode_workspace_bytes(const tbe_attention* h, int32_t B, int64_t max_length) {
+    if (!h || B < 0 || max_length < 0 || max_length >= (int64_t(1) << 31)) return 0;
+    const Split sp = decode_split(h, B, max_length);
+    return align_up(sizeof(float) * (size_t)B * h->s.H * sp.splits * (h->s.D + 2)) + 256;
+}
+
+int tbe_attention_decode(tbe_attention* h, const tbe_rows* q, const tbe_pages* k_pages, const tbe_pages* v_pages,
+                         int32_t num_pages, int32_t page_size, const int32_t* block_table, int32_t table_width,
+                         const int32_t* lengths, int32_t B, int64_t max_length, const void* bias, void* out,
+                         void* workspace, size_t workspace_bytes, void* stream) {
+    CallRange range("tbe_attention_decode");
+    if (!h || !on_device(h)) return TBE_ERR_INVALID_ARG;
+    if (B < 0 || max_length < 0 || num_pages < 0 || page_size <= 0 || table_width < 0) return TBE_ERR_INVALID_ARG;
+    if (!rows_ok(q, B) || !pages_ok(k_pages) || !pages_ok(v_pages)) return TBE_ERR_INVALID_ARG;
+    if ((bias != nullptr) != (h->s.buckets > 0) || !workspace) return TBE_ERR_INVALID_ARG;
+    if (B > 0 && (!lengths || !out || (table_width > 0 && !block_table))) return TBE_ERR_INVALID_ARG;
+    if ((int64_t)table_width * page_size >= (int64_t(1) << 31) || B >= (1 << 24)) return TBE_ERR_UNSUPPORTED;
+    const int64_t room = (int64_t)table_width * page_size;
+    const int64_t most = max_length == 0 ? room : std::min(max_length, room);
+    const Split sp = decode_split(h, B, most);
+    const int gt = attn_decode_heads(h->s.G);
+    if ((int64_t)sp.splits * ((h->s.G + gt - 1) / gt) * h->s.Hk * B >= (int64_t(1) << 31) ||
+        (int64_t)B * h->s.H >= (int64_t(1) << 31))
+        return TBE_ERR_UNSUPPORTED;
+    if (workspace_bytes < sizeof(float) * (size_t)B * h->s.H * sp.splits * (h->s.D + 2))
+        return TBE_ERR_WORKSPACE_TOO_SMALL;
+    if (B == 0) return TBE_OK;
+    AttnDecode p{};
+    p.s = h->s;
+    p.q = as_rows(*q);
+    p.kp = k_pages->data;
+    p.vp = v_pages->data;
+    p.k_page = k_pages->page_stride;
+    p.k_token = k_pages->token_stride;
+    p.k_head = k_pages->head_stride;
+    p.v_page = v_pages->page_stride;
+    p.v_token = v_pages->token_stride;
+    p.v_head = v_pages->head_stride;
+    p.table = block_table;
+    p.lengths = lengths;
+    p.bias = bias;
+    p.out = out;
+    p.part = static_cast<float*>(workspace);
+    p.width = table_width;
+    p.num_pages = num_pages;
+    p.B = B;
+    p.chunk = sp.chunk;
+    p.splits = sp.splits;
+    p.max_length = most;
+    p.page = make_fast_div((uint32_t)page_size);
+    p.vec = vec_rows(h, *q) && vec_pages(h, *k_pages) && vec_pages(h, *v_pages);
+    return status(launch_attn_decode(p, static_cast<cudaStream_t>(stream)));
+}
+
+int tbe_attention_get_error(tbe_attention* h, void* stream) {
+    if (!h || !on_device(h)) return TBE_ERR_INVALID_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    uint32_t bits = 0;
+    cudaError_t e = cudaMemcpyAsync(&bits, h->s.error, sizeof bits, cudaMemcpyDeviceToHost, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    if (e == cudaSuccess) e = cudaMemsetAsync(h->s.error, 0, sizeof(uint32_t), s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    if (e != cudaSuccess) return cuda_fail(e);
+    if (bits & ERR_TIMEOUT) return TBE_ERR_TIMEOUT;
+    if (bits & ERR_OFFSETS) return TBE_ERR_BAD_OFFSETS;
+    if (bits & ERR_OOB) return TBE_ERR_INDEX_OOB;
+    return TBE_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,382 @@
+// The serving form: new tokens' keys and values go to a paged cache, and one
+// new token per history attends to its cache.
+//
+// The cache of history b is the pages table[b][0], table[b][1], ...; token j
+// is row j % page of page table[b][j / page].  Only the visible rows are
+// read: the first `sinks` and the newest `window`.  What a page holds beyond
+// a history's length is never loaded, whatever its bits are.
+#include "attention.cuh"
+
+namespace tbe {
+
+namespace {
+
+constexpr int kAppendThreads = 256;
+
+// One warp per new token: finds its history by bisection of the offsets,
+// then copies the token's key and value rows into its page.
+template <typename I>
+__global__ void __launch_bounds__(kAppendThreads) attn_append_kernel(const AttnAppend p) {
+    const int64_t t = (int64_t)blockIdx.x * (kAppendThreads / 32) + threadIdx.x / 32;
+    const int lane = threadIdx.x % 32;
+    if (t >= p.N) return;
+    const I* off = static_cast<const I*>(p.offsets);
+    int lo = 0, hi = p.B - 1;  // the last history that starts at or before t
+    while (lo < hi) {
+        const int mid = lo + (hi - lo + 1) / 2;
+        if ((int64_t)off[mid] <= t)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    const int64_t from = (int64_t)off[lo], to = (int64_t)off[lo + 1];
+    if (from < 0 || t < from || t >= to) {
+        if (lane == 0) atomicOr(p.error, ERR_OFFSETS);
+        return;
+    }
+    const int64_t pos = (int64_t)p.before[lo] + (t - from);
+    if (p.before[lo] < 0 || pos >= (int64_t)p.width * p.page.n) {
+        if (lane == 0) atomicOr(p.error, ERR_OOB);
+        return;
+    }
+    const uint32_t pg = fast_div((uint32_t)pos, p.page);
+    const int row = (int)((uint32_t)pos - pg * p.page.n);
+    const int32_t page = p.table[(int64_t)lo * p.width + pg];
+    if (page < 0 || page >= p.num_pages) {
+        if (lane == 0) atomicOr(p.error, ERR_OOB);
+        return;
+    }
+    const char* ks = static_cast<const char*>(p.k.data) + t * p.k.token_stride * p.e;
+    const char* vs = static_cast<const char*>(p.v.data) + t * p.v.token_stride * p.e;
+    char* kd = static_cast<char*>(p.kp) + (page * p.k_page + row * p.k_token) * p.e;
+    char* vd = static_cast<char*>(p.vp) + (page * p.v_page + row * p.v_token) * p.e;
+    const int bytes = p.D * p.e, unit = p.vec ? 16 : p.e, per = bytes / unit;
+    for (int c = lane; c < p.Hk * per; c += 32) {
+        const int h = c / per, x = c % per * unit;
+        const char* a = ks + h * p.k.head_stride * p.e + x;
+        const char* b = vs + h * p.v.head_stride * p.e + x;
+        char* ka = kd + h * p.k_head * p.e + x;
+        char* vb = vd + h * p.v_head * p.e + x;
+        if (p.vec) {
+            *reinterpret_cast<uint4*>(ka) = __ldg(reinterpret_cast<const uint4*>(a));
+            *reinterpret_cast<uint4*>(vb) = __ldg(reinterpret_cast<const uint4*>(b));
+        } else if (p.e == 4) {
+            *reinterpret_cast<uint32_t*>(ka) = __ldg(reinterpret_cast<const uint32_t*>(a));
+            *reinterpret_cast<uint32_t*>(vb) = __ldg(reinterpret_cast<const uint32_t*>(b));
+        } else {
+            *reinterpret_cast<uint16_t*>(ka) = __ldg(reinterpret_cast<const uint16_t*>(a));
+            *reinterpret_cast<uint16_t*>(vb) = __ldg(reinterpret_cast<const uint16_t*>(b));
+        }
+    }
+}
+
+constexpr int kWarps = 4;
+
+// The visible rows of a cache of len tokens, as one range [0, sinks + len - lo):
+// index x is token x below `sinks` and token lo + x - sinks from there on.
+struct Visible {
+    int sinks, lo, count;
+};
+
+__device__ __forceinline__ Visible visible_rows(const AttnShape& s, int len) {
+    const int lo = len > s.window ? len - s.window : 0;
+    const int sinks = tmin(s.sinks, lo);
+    return Visible{sinks, lo, sinks + len - lo};
+}
+
+__device__ __forceinline__ int cache_length(const AttnDecode& p, int b) {
+    const int len = __ldg(p.lengths + b);
+    return len < 0 || (int64_t)len > p.max_length ? -1 : len;
+}
+
+template <int DT, int NV>
+__device__ __forceinline__ void load_vecs(uint4 (&u)[NV], const typename Elem<DT>::type* row, int col, int step, int D,
+                                          int vec) {
+    using E = typename Elem<DT>::type;
+    constexpr int V = 16 / sizeof(E);
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+        const int c = col + n * step;
+        u[n] = make_uint4(0, 0, 0, 0);
+        if (vec) {
+            if (c < D) u[n] = __ldg(reinterpret_cast<const uint4*>(row + c));
+        } else {
+            E e[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) e[i] = c + i < D ? row[c + i] : E(0.f);
+            u[n] = *reinterpret_cast<uint4*>(e);
+        }
+    }
+}
+
+// One CTA: `chunk` visible rows of one history for GT query heads of one
+// key-value head.  LPR lanes hold one row (16 bytes each, NV times); each
+// such group of lanes runs its own softmax over its rows, U rows a step, and
+// the groups are joined at the end.
+template <int DT, int GT, int LPR, int NV>
+__global__ void __launch_bounds__(kWarps * 32) attn_decode_kernel(const AttnDecode p) {
+    using E = typename Elem<DT>::type;
+    constexpr int V = 16 / sizeof(E), RPW = 32 / LPR, U = GT > 4 ? 2 : 4, STEP = kWarps * RPW * U;
+    constexpr int W = V * NV;
+    extern __shared__ float dsm[];
+    __shared__ float stat[kWarps][GT][2];
+    const int hchunks = (p.s.G + GT - 1) / GT;
+    uint32_t x = blockIdx.x;
+    const int split = (int)(x % p.splits);
+    x /= p.splits;
+    const int hc = (int)(x % hchunks);
+    x /= hchunks;
+    const int kvh = (int)(x % p.s.Hk), b = (int)(x / p.s.Hk);
+    const int g0 = hc * GT, gn = tmin(GT, p.s.G - g0), head0 = kvh * p.s.G + g0;
+    const int len = cache_length(p, b);
+    if (len < 0 && threadIdx.x == 0 && split == 0) atomicOr(p.s.error, ERR_OOB);
+    const Visible vis = visible_rows(p.s, tmax(len, 0));
+    if (split > 0 && split * p.chunk >= vis.count) return;
+    const int begin = split * p.chunk, end = tmin(vis.count, begin + p.chunk);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, sub = lane / LPR;
+    const int col = lane % LPR * V;
+    constexpr int cstep = LPR * V;
+    const float c2 = p.s.scale * kLog2e;
+
+    if (p.bias) {
+        for (int i = threadIdx.x; i < GT * p.s.buckets; i += kWarps * 32) {
+            const int g = i / p.s.buckets, k = i % p.s.buckets;
+            dsm[i] = g < gn ? bias_base2(load_elem<DT>(p.bias, (int64_t)k * p.s.H + head0 + g)) : 0.f;
+        }
+        __syncthreads();
+    }
+    float q[GT][W], o[GT][W], m[GT], l[GT];
+#pragma unroll
+    for (int g = 0; g < GT; ++g) {
+        m[g] = -INFINITY;
+        l[g] = 0.f;
+        uint4 u[NV];
+        if (g < gn) {
+            const E* row = static_cast<const E*>(p.q.data) + b * p.q.token_stride + (head0 + g) * p.q.head_stride;
+            load_vecs<DT, NV>(u, row, col, cstep, p.s.D, p.vec);
+        } else {
+#pragma unroll
+            for (int n = 0; n < NV; ++n) u[n] = make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int n = 0; n < NV; ++n) unpack16<DT>(u[n], &q[g][n * V]);
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            q[g][i] *= c2;
+            o[g][i] = 0.f;
+        }
+    }
+    const E* kbase = static_cast<const E*>(p.kp) + kvh * p.k_head;
+    const E* vbase = static_cast<const E*>(p.vp) + kvh * p.v_head;
+    const int32_t* table = p.table + (int64_t)b * p.width;
+
+    for (int x0 = begin; x0 < end; x0 += STEP) {
+        uint4 kr[U][NV], vr[U][NV];
+        int dist[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int xi = x0 + (u * kWarps + warp) * RPW + sub;
+            const int j = xi < vis.sinks ? xi : vis.lo + xi - vis.sinks;
+            dist[u] = -1;
+#pragma unroll
+            for (int n = 0; n < NV; ++n) kr[u][n] = vr[u][n] = make_uint4(0, 0, 0, 0);
+            if (xi < end) {
+                const uint32_t pg = fast_div((uint32_t)j, p.page);
+                const int row = (int)((uint32_t)j - pg * p.page.n);
+                const int32_t page = __ldg(table + pg);
+                if (page >= 0 && page < p.num_pages) {
+                    dist[u] = len - 1 - j;
+                    load_vecs<DT, NV>(kr[u], kbase + page * p.k_page + row * p.k_token, col, cstep, p.s.D, p.vec);
+                    load_vecs<DT, NV>(vr[u], vbase + page * p.v_page + row * p.v_token, col, cstep, p.s.D, p.vec);
+                } else {
+                    atomicOr(p.s.error, ERR_OOB);
+                }
+            }
+        }
+        float s[U][GT];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float f[W];
+#pragma unroll
+            for (int n = 0; n < NV; ++n) unpack16<DT>(kr[u][n], &f[n * V]);
+#pragma unroll
+            for (int g = 0; g < GT; ++g) {
+                float t = 0.f;
+#pragma unroll
+                for (int i = 0; i < W; ++i) t = fmaf(q[g][i], f[i], t);
+#pragma unroll
+                for (int w = LPR / 2; w > 0; w >>= 1) t += __shfl_xor_sync(0xffffffffu, t, w);
+                s[u][g] = t;
+            }
+            if (p.bias) {
+                const int bk = dist[u] >= 0 ? attn_bucket(p.s, dist[u]) : 0;
+#pragma unroll
+                for (int g = 0; g < GT; ++g) s[u][g] += dsm[g * p.s.buckets + bk];
+            }
+        }
+#pragma unroll
+        for (int g = 0; g < GT; ++g) {
+            float top = m[g];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (dist[u] < 0) s[u][g] = -INFINITY;
+                top = fmaxf(top, s[u][g]);
+            }
+            const float safe = top == -INFINITY ? 0.f : top;
+            const float keep = ex2(m[g] - safe);
+            m[g] = top;
+            float sum = 0.f;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                s[u][g] = ex2(s[u][g] - safe);
+                sum += s[u][g];
+            }
+            l[g] = l[g] * keep + sum;
+#pragma unroll
+            for (int i = 0; i < W; ++i) o[g][i] *= keep;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float f[W];
+#pragma unroll
+            for (int n = 0; n < NV; ++n) unpack16<DT>(vr[u][n], &f[n * V]);
+#pragma unroll
+            for (int g = 0; g < GT; ++g)
+#pragma unroll
+                for (int i = 0; i < W; ++i) o[g][i] = fmaf(s[u][g], f[i], o[g][i]);
+        }
+    }
+    // join the warp's groups, then the CTA's warps
+    float* osm = dsm + (p.bias ? GT * p.s.buckets : 0);  // [kWarps][GT][LPR * W]
+#pragma unroll
+    for (int g = 0; g < GT; ++g) {
+        float top = m[g];
+#pragma unroll
+        for (int w = LPR; w < 32; w <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+        const float keep = ex2(m[g] - (top == -INFINITY ? 0.f : top));
+        float sum = l[g] * keep;
+#pragma unroll
+        for (int w = LPR; w < 32; w <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            float t = o[g][i] * keep;
+#pragma unroll
+            for (int w = LPR; w < 32; w <<= 1) t += __shfl_xor_sync(0xffffffffu, t, w);
+            if (sub == 0) osm[(warp * GT + g) * (LPR * W) + col + (i / V) * cstep + i % V] = t;
+        }
+        if (lane == 0) {
+            stat[warp][g][0] = top;
+            stat[warp][g][1] = sum;
+        }
+    }
+    __syncthreads();
+    const bool whole = vis.count <= p.chunk;
+    for (int i = threadIdx.x; i < gn * p.s.D; i += kWarps * 32) {
+        const int g = i / p.s.D, d = i % p.s.D;
+        float top = -INFINITY, sum = 0.f, t = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, stat[w][g][0]);
+        const float safe = top == -INFINITY ? 0.f : top;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float keep = ex2(stat[w][g][0] - safe);
+            sum += stat[w][g][1] * keep;
+            t += osm[(w * GT + g) * (LPR * W) + d] * keep;
+        }
+        const int64_t row = (int64_t)b * p.s.H + head0 + g;
+        if (whole) {
+            store_elem<DT>(p.out, row * p.s.D + d, sum == 0.f ? 0.f : t / sum);  // an empty cache gives zeros
+        } else {
+            float* to = p.part + (row * p.splits + split) * (p.s.D + 2);
+            to[d] = t;
+            if (d == 0) {
+                to[p.s.D] = top;
+                to[p.s.D + 1] = sum;
+            }
+        }
+    }
+}
+
+// Joins the chunks of one history and head: the partial sums scaled to the
+// largest of their maxima, added in the chunks' order.
+template <int DT>
+__global__ void __launch_bounds__(128) attn_decode_join_kernel(const AttnDecode p) {
+    const int b = (int)(blockIdx.x / p.s.H);
+    const int len = cache_length(p, b);
+    const Visible vis = visible_rows(p.s, tmax(len, 0));
+    if (vis.count <= p.chunk) return;  // written by its one CTA
+    const int n = (vis.count + p.chunk - 1) / p.chunk;
+    const float* part = p.part + (int64_t)blockIdx.x * p.splits * (p.s.D + 2);
+    const int ld = p.s.D + 2;
+    float top = -INFINITY;
+    for (int i = 0; i < n; ++i) top = fmaxf(top, part[i * ld + p.s.D]);
+    const float safe = top == -INFINITY ? 0.f : top;
+    for (int d = threadIdx.x; d < p.s.D; d += 128) {
+        float sum = 0.f, t = 0.f;
+        for (int i = 0; i < n; ++i) {
+            const float keep = ex2(part[i * ld + p.s.D] - safe);
+            sum += part[i * ld + p.s.D + 1] * keep;
+            t += part[i * ld + d] * keep;
+        }
+        store_elem<DT>(p.out, (int64_t)blockIdx.x * p.s.D + d, sum == 0.f ? 0.f : t / sum);
+    }
+}
+
+template <int DT, int GT, int LPR, int NV>
+cudaError_t decode(const AttnDecode& p, cudaStream_t s) {
+    constexpr int W = 16 / sizeof(typename Elem<DT>::type) * NV;
+    const int64_t grid = (int64_t)p.splits * ((p.s.G + GT - 1) / GT) * p.s.Hk * p.B;
+    const size_t smem = sizeof(float) * ((p.bias ? (size_t)GT * p.s.buckets : 0) + (size_t)kWarps * GT * LPR * W);
+    attn_decode_kernel<DT, GT, LPR, NV><<<(unsigned)grid, kWarps * 32, smem, s>>>(p);
+    return cudaGetLastError();
+}
+
+template <int DT, int GT>
+cudaError_t decode_dim(const AttnDecode& p, cudaStream_t s) {
+    constexpr int V = 16 / sizeof(typename Elem<DT>::type);
+    const int lanes = (p.s.D + V - 1) / V;
+    if (lanes <= 4) return decode<DT, GT, 4, 1>(p, s);
+    if (lanes <= 8) return decode<DT, GT, 8, 1>(p, s);
+    if (lanes <= 16) return decode<DT, GT, 16, 1>(p, s);
+    if constexpr (DT == DT_F32) {
+        if (lanes <= 32) return decode<DT, GT, 32, 1>(p, s);
+        return decode<DT, GT, 32, 2>(p, s);
+    } else {
+        return decode<DT, GT, 32, 1>(p, s);
+    }
+}
+
+template <int DT>
+cudaError_t decode_type(const AttnDecode& p, cudaStream_t s) {
+    cudaError_t e;
+    switch (attn_decode_heads(p.s.G)) {
+        case 1: e = decode_dim<DT, 1>(p, s); break;
+        case 2: e = decode_dim<DT, 2>(p, s); break;
+        case 4: e = decode_dim<DT, 4>(p, s); break;
+        default: e = decode_dim<DT, 8>(p, s); break;
+    }
+    if (e != cudaSuccess || p.splits == 1) return e;
+    attn_decode_join_kernel<DT><<<(unsigned)(p.B * p.s.H), 128, 0, s>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+int attn_decode_heads(int G) { return G <= 1 ? 1 : G <= 2 ? 2 : G <= 4 ? 4 : 8; }
+
+cudaError_t launch_attn_append(const AttnAppend& p, cudaStream_t s) {
+    const unsigned grid = (unsigned)((p.N + kAppendThreads / 32 - 1) / (kAppendThreads / 32));
+    if (p.index64)
+        attn_append_kernel<int64_t><<<grid, kAppendThreads, 0, s>>>(p);
+    else
+        attn_append_kernel<int32_t><<<grid, kAppendThreads, 0, s>>>(p);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_attn_decode(const AttnDecode& p, cudaStream_t s) {
+    if (p.s.dtype == DT_F32) return decode_type<DT_F32>(p, s);
+    if (p.s.dtype == DT_F16) return decode_type<DT_F16>(p, s);
+    return decode_type<DT_BF16>(p, s);
+}
+
+}  // namespace tbe

@@ -1,0 +1,615 @@
+// Attention over ragged histories, fp32 arithmetic on the FMA units: the
+// path of fp32 tensors and of rows the tensor-core kernels do not take.
+//
+// One CTA takes one tile of T tokens of one history and one head, holds its
+// rows in shared memory as fp32 and walks the visible tiles of the other
+// side once.  256 threads form a 16 x 16 grid; a thread holds an R x R block
+// of logits (R = T / 16; rows ty*R + r, columns tx + 16 c) and an R x D/16
+// block of each accumulator, so a step of four products reads 2R 16-byte
+// words of shared memory for 4 R^2 FMAs (R = 4: 64): FMA-bound.
+// T = 64 up to head_dim 128, 32 above (the tiles must fit 227 KB).
+#include <type_traits>
+
+#include "attention.cuh"
+
+namespace tbe {
+
+namespace {
+
+constexpr int kThreads = 256;
+static_assert(kMaxBuckets <= kThreads, "a thread per bucket");
+
+template <int T, int DP>
+struct Tile {
+    static constexpr int LD = DP + 4;  // row stride: the 16 rows a warp reads fall on distinct banks
+    static constexpr int PLD = T + 4;
+    static constexpr size_t bytes = sizeof(float) * T * LD;
+    static constexpr size_t pbytes = sizeof(float) * T * PLD;
+};
+
+// Rows [first, first + T) of a history (zeros from `len` on, and beyond
+// column D) into a shared tile as fp32.
+template <int DT, int T, int DP>
+__device__ __forceinline__ void load_tile(float* dst, const Rows& r, int64_t token0, int head, int first, int len,
+                                          int D, int vec) {
+    using E = typename Elem<DT>::type;
+    constexpr int V = 16 / sizeof(E);
+    constexpr int LD = Tile<T, DP>::LD;
+    const E* base = static_cast<const E*>(r.data) + head * r.head_stride;
+    if (vec) {
+        for (int c = threadIdx.x; c < T * (DP / V); c += kThreads) {
+            const int row = c / (DP / V), col = c % (DP / V) * V;
+            float f[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) f[i] = 0.f;
+            if (first + row < len && col < D) {
+                const E* p = base + (token0 + first + row) * r.token_stride + col;
+                unpack16<DT>(__ldg(reinterpret_cast<const uint4*>(p)), f);
+            }
+#pragma unroll
+            for (int i = 0; i < V; i += 4)
+                *reinterpret_cast<float4*>(dst + row * LD + col + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+        }
+    } else {
+        for (int c = threadIdx.x; c < T * DP; c += kThreads) {
+            const int row = c / DP, col = c % DP;
+            float f = 0.f;
+            if (first + row < len && col < D) f = load_elem<DT>(base, (token0 + first + row) * r.token_stride + col);
+            dst[row * LD + col] = f;
+        }
+    }
+}
+
+// acc[r][c] += sum_d a[ty*R + r][d] * b[tx + 16 c][d]
+template <int T, int DP>
+__device__ __forceinline__ void dot_tile(float (&acc)[T / 16][T / 16], const float* a, const float* b, int tx, int ty) {
+    constexpr int R = T / 16, LD = Tile<T, DP>::LD;
+#pragma unroll 4
+    for (int d = 0; d < DP; d += 4) {
+        float4 x[R], y[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) x[r] = *reinterpret_cast<const float4*>(a + (ty * R + r) * LD + d);
+#pragma unroll
+        for (int c = 0; c < R; ++c) y[c] = *reinterpret_cast<const float4*>(b + (tx + 16 * c) * LD + d);
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int c = 0; c < R; ++c) {
+                acc[r][c] = fmaf(x[r].x, y[c].x, acc[r][c]);
+                acc[r][c] = fmaf(x[r].y, y[c].y, acc[r][c]);
+                acc[r][c] = fmaf(x[r].z, y[c].z, acc[r][c]);
+                acc[r][c] = fmaf(x[r].w, y[c].w, acc[r][c]);
+            }
+    }
+}
+
+// acc[r][u] (columns 64 u + 4 tx ..) += sum_j p[ty*R + r][j] * b[j][column]
+template <int T, int DP>
+__device__ __forceinline__ void mul_tile(float4 (&acc)[T / 16][DP / 64], const float* p, const float* b, int tx,
+                                         int ty) {
+    constexpr int R = T / 16, LD = Tile<T, DP>::LD, PLD = Tile<T, DP>::PLD, U = DP / 64;
+#pragma unroll 2
+    for (int j = 0; j < T; j += 4) {
+        float w[R][4];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const float4 x = *reinterpret_cast<const float4*>(p + (ty * R + r) * PLD + j);
+            w[r][0] = x.x;
+            w[r][1] = x.y;
+            w[r][2] = x.z;
+            w[r][3] = x.w;
+        }
+#pragma unroll
+        for (int jj = 0; jj < 4; ++jj)
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const float4 y = *reinterpret_cast<const float4*>(b + (j + jj) * LD + u * 64 + tx * 4);
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    acc[r][u].x = fmaf(w[r][jj], y.x, acc[r][u].x);
+                    acc[r][u].y = fmaf(w[r][jj], y.y, acc[r][u].y);
+                    acc[r][u].z = fmaf(w[r][jj], y.z, acc[r][u].z);
+                    acc[r][u].w = fmaf(w[r][jj], y.w, acc[r][u].w);
+                }
+            }
+    }
+}
+
+template <int DT, int T, int DP>
+__device__ __forceinline__ void store_rows(void* out, const float4 (&acc)[T / 16][DP / 64], const float (&mul)[T / 16],
+                                           int64_t token0, int heads, int head, int first, int len, int D, int tx,
+                                           int ty) {
+    constexpr int R = T / 16, U = DP / 64;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int row = first + ty * R + r;
+        if (row >= len) continue;
+        const int64_t at = ((token0 + row) * heads + head) * D;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int col = u * 64 + tx * 4;
+            const float f[4] = {acc[r][u].x, acc[r][u].y, acc[r][u].z, acc[r][u].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (col + i < D) store_elem<DT>(out, at + col + i, f[i] * mul[r]);
+        }
+    }
+}
+
+// The key tiles a query tile sees: [0, sink_tiles) and [lo, hi).
+template <int T>
+__device__ __forceinline__ void key_tiles(const AttnShape& s, int tile, int& sink_tiles, int& lo) {
+    const int64_t first = (int64_t)tile * T - s.window + 1;  // first key the tile's first query sees
+    lo = first > 0 ? (int)(first / T) : 0;
+    sink_tiles = s.sinks > 0 ? tmin((s.sinks + T - 1) / T, lo) : 0;
+}
+
+// The bias of every distance the tile pair can have, in base 2:
+// bt[x] belongs to distance base + x - (T - 1), x in [0, 2T - 1).
+template <int DT, int T>
+__device__ __forceinline__ void load_bias(float* bt, const AttnShape& s, const void* bias, int head, int base) {
+    for (int x = threadIdx.x; x < 2 * T - 1; x += kThreads) {
+        const int d = base + x - (T - 1);
+        bt[x] = d >= 0 ? bias_base2(load_elem<DT>(bias, (int64_t)attn_bucket(s, d) * s.H + head)) : 0.f;
+    }
+}
+
+template <int DT, int T, int DP>
+__global__ void __launch_bounds__(kThreads) attn_fwd_simt_kernel(const AttnForward p) {
+    constexpr int R = T / 16, U = DP / 64, PLD = Tile<T, DP>::PLD;
+    extern __shared__ __align__(16) float sm[];
+    float* qs = sm;
+    float* ks = qs + Tile<T, DP>::bytes / 4;
+    float* vs = ks + Tile<T, DP>::bytes / 4;
+    float* ps = vs + Tile<T, DP>::bytes / 4;
+    float* bt = ps + Tile<T, DP>::pbytes / 4;
+    const int64_t w = blockIdx.x / p.s.H;
+    const int head = (int)(blockIdx.x % p.s.H);
+    if (w >= *p.n_items) return;
+    const AttnItem it = p.items[w];
+    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16, kvh = head / p.s.G;
+    const int first = it.tile * T;
+    const float c2 = p.s.scale * kLog2e;
+    load_tile<DT, T, DP>(qs, p.q, it.start, head, first, it.len, p.s.D, p.vec);
+    float4 o[R][U];
+    float m[R], l[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        m[r] = -INFINITY;
+        l[r] = 0.f;
+#pragma unroll
+        for (int u = 0; u < U; ++u) o[r][u] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    int sink_tiles, lo;
+    key_tiles<T>(p.s, it.tile, sink_tiles, lo);
+    const int steps = sink_tiles + it.tile + 1 - lo;
+    for (int st = 0; st < steps; ++st) {
+        const int kt = st < sink_tiles ? st : lo + st - sink_tiles;
+        __syncthreads();
+        load_tile<DT, T, DP>(ks, p.k, it.start, kvh, kt * T, it.len, p.s.D, p.vec);
+        load_tile<DT, T, DP>(vs, p.v, it.start, kvh, kt * T, it.len, p.s.D, p.vec);
+        if (p.bias) load_bias<DT, T>(bt, p.s, p.bias, head, (it.tile - kt) * T);
+        __syncthreads();
+        float s[R][R];
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int c = 0; c < R; ++c) s[r][c] = 0.f;
+        dot_tile<T, DP>(s, qs, ks, tx, ty);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int i = first + ty * R + r;
+            float top = m[r];
+#pragma unroll
+            for (int c = 0; c < R; ++c) {
+                const int jj = tx + 16 * c, j = kt * T + jj;
+                float x = s[r][c] * c2;
+                if (p.bias) x += bt[ty * R + r - jj + T - 1];
+                s[r][c] = attn_visible(i - j, j, p.s.window, p.s.sinks) ? x : -INFINITY;
+                top = fmaxf(top, s[r][c]);
+            }
+#pragma unroll
+            for (int o2 = 8; o2 > 0; o2 >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o2, 16));
+            const float safe = top == -INFINITY ? 0.f : top;  // no visible key yet
+            const float keep = ex2(m[r] - safe);
+            m[r] = top;
+            float sum = 0.f;
+#pragma unroll
+            for (int c = 0; c < R; ++c) {
+                const float e = ex2(s[r][c] - safe);
+                sum += e;
+                ps[(ty * R + r) * PLD + tx + 16 * c] = e;
+            }
+#pragma unroll
+            for (int o2 = 8; o2 > 0; o2 >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o2, 16);
+            l[r] = l[r] * keep + sum;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                o[r][u].x *= keep;
+                o[r][u].y *= keep;
+                o[r][u].z *= keep;
+                o[r][u].w *= keep;
+            }
+        }
+        __syncwarp();  // a warp reads only the rows of ps that it wrote
+        mul_tile<T, DP>(o, ps, vs, tx, ty);
+    }
+    float inv[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        inv[r] = l[r] == 0.f ? 0.f : 1.f / l[r];  // a row that sees nothing is zero
+        const int row = first + ty * R + r;
+        if (tx == 0 && row < it.len) p.lse[(int64_t)head * p.N + it.start + row] = m[r] + log2f(l[r]);
+    }
+    store_rows<DT, T, DP>(p.out, o, inv, it.start, p.s.H, head, first, it.len, p.s.D, tx, ty);
+}
+
+// dq of one query tile, delta of its rows, and the tile's share of the bias
+// gradient.  The bias gradient adds ds along diagonals (one distance each) in
+// a fixed order: a thread per diagonal of the tile pair, then a thread per
+// bucket over the bucket's diagonals, so results do not vary between runs.
+template <int DT, int T, int DP>
+__global__ void __launch_bounds__(kThreads) attn_dq_simt_kernel(const AttnBackward p) {
+    constexpr int R = T / 16, U = DP / 64, PLD = Tile<T, DP>::PLD;
+    extern __shared__ __align__(16) float sm[];
+    float* qs = sm;
+    float* gs = qs + Tile<T, DP>::bytes / 4;
+    float* ks = gs + Tile<T, DP>::bytes / 4;
+    float* vs = ks + Tile<T, DP>::bytes / 4;
+    float* ps = vs + Tile<T, DP>::bytes / 4;
+    float* bt = ps + Tile<T, DP>::pbytes / 4;
+    float* diag = bt + 2 * T;
+    const int64_t w = blockIdx.x / p.s.H;
+    const int head = (int)(blockIdx.x % p.s.H);
+    if (w >= *p.n_items) return;
+    const AttnItem it = p.items[w];
+    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16, kvh = head / p.s.G;
+    const int first = it.tile * T;
+    const float c2 = p.s.scale * kLog2e;
+    load_tile<DT, T, DP>(qs, p.q, it.start, head, first, it.len, p.s.D, p.vec);
+    load_tile<DT, T, DP>(gs, p.g, it.start, head, first, it.len, p.s.D, p.vec);
+    const Rows orows{p.out, (int64_t)p.s.H * p.s.D, p.s.D};
+    load_tile<DT, T, DP>(ks, orows, it.start, head, first, it.len, p.s.D, p.vec);
+    __syncthreads();
+    float4 acc[R][U];
+    float lse[R], delta[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int row = ty * R + r;
+        float t = 0.f;
+        for (int d = tx; d < DP; d += 16) t = fmaf(gs[row * Tile<T, DP>::LD + d], ks[row * Tile<T, DP>::LD + d], t);
+#pragma unroll
+        for (int o2 = 8; o2 > 0; o2 >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o2, 16);
+        delta[r] = t;
+        lse[r] = INFINITY;
+        if (first + row < it.len) {
+            const int64_t at = (int64_t)head * p.N + it.start + first + row;
+            const float x = p.lse[at];
+            lse[r] = x == -INFINITY ? INFINITY : x;  // a row that sees nothing: all its weights 2^-inf
+            if (tx == 0) p.delta[at] = t;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) acc[r][u] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    float mine = 0.f;  // bias gradient of bucket threadIdx.x
+    int sink_tiles, lo;
+    key_tiles<T>(p.s, it.tile, sink_tiles, lo);
+    const int steps = sink_tiles + it.tile + 1 - lo;
+    for (int st = 0; st < steps; ++st) {
+        const int kt = st < sink_tiles ? st : lo + st - sink_tiles;
+        const int base = (it.tile - kt) * T;
+        __syncthreads();
+        load_tile<DT, T, DP>(ks, p.k, it.start, kvh, kt * T, it.len, p.s.D, p.vec);
+        load_tile<DT, T, DP>(vs, p.v, it.start, kvh, kt * T, it.len, p.s.D, p.vec);
+        if (p.bias) load_bias<DT, T>(bt, p.s, p.bias, head, base);
+        __syncthreads();
+        float s[R][R], dp[R][R];
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int c = 0; c < R; ++c) s[r][c] = dp[r][c] = 0.f;
+        dot_tile<T, DP>(s, qs, ks, tx, ty);
+        dot_tile<T, DP>(dp, gs, vs, tx, ty);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int i = first + ty * R + r;
+#pragma unroll
+            for (int c = 0; c < R; ++c) {
+                const int jj = tx + 16 * c, j = kt * T + jj;
+                float x = s[r][c] * c2;
+                if (p.bias) x += bt[ty * R + r - jj + T - 1];
+                const bool seen = i < it.len && attn_visible(i - j, j, p.s.window, p.s.sinks) &&
+                                  !attn_lone(i, j, p.s.window, p.s.sinks);
+                ps[(ty * R + r) * PLD + jj] = seen ? ex2(x - lse[r]) * (dp[r][c] - delta[r]) : 0.f;
+            }
+        }
+        __syncthreads();
+        mul_tile<T, DP>(acc, ps, ks, tx, ty);
+        if (p.bias) {
+            for (int x = threadIdx.x; x < 2 * T - 1; x += kThreads) {
+                const int off = x - (T - 1);  // row - column
+                float t = 0.f;
+                for (int j = tmax(0, -off); j < tmin(T, T - off); ++j) t += ps[(j + off) * PLD + j];
+                diag[x] = t;
+            }
+            __syncthreads();
+            if (threadIdx.x < p.s.buckets) {
+                const int from = tmax(__ldg(p.s.starts + threadIdx.x), tmax(0, base - (T - 1)));
+                const int to = tmin(__ldg(p.s.starts + threadIdx.x + 1), base + T);
+                for (int d = from; d < to; ++d) mine += diag[d - base + T - 1];
+            }
+        }
+    }
+    float mul[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) mul[r] = p.s.scale;
+    store_rows<DT, T, DP>(p.gq, acc, mul, it.start, p.s.H, head, first, it.len, p.s.D, tx, ty);
+    if (p.bias && threadIdx.x < p.s.buckets) p.bias_part[(w * p.s.H + head) * p.s.buckets + threadIdx.x] = mine;
+}
+
+// dk and dv of one key tile and key-value head: the sums over the group's
+// query heads and the visible query tiles, in a fixed order.  Here the
+// logits' rows are keys and their columns queries.
+template <int DT, int T, int DP>
+__global__ void __launch_bounds__(kThreads) attn_dkv_simt_kernel(const AttnBackward p) {
+    constexpr int R = T / 16, U = DP / 64, PLD = Tile<T, DP>::PLD;
+    extern __shared__ __align__(16) float sm[];
+    float* ks = sm;
+    float* vs = ks + Tile<T, DP>::bytes / 4;
+    float* qs = vs + Tile<T, DP>::bytes / 4;
+    float* gs = qs + Tile<T, DP>::bytes / 4;
+    float* ps = gs + Tile<T, DP>::bytes / 4;
+    float* bt = ps + Tile<T, DP>::pbytes / 4;
+    float* ls = bt + 2 * T;
+    float* de = ls + T;
+    const int64_t w = blockIdx.x / p.s.Hk;
+    const int kvh = (int)(blockIdx.x % p.s.Hk);
+    if (w >= *p.n_items) return;
+    const AttnItem it = p.items[w];
+    const int kt = it.tiles - 1 - it.tile;  // the first tiles are seen most: they start first
+    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+    const int first = kt * T;
+    const float c2 = p.s.scale * kLog2e;
+    load_tile<DT, T, DP>(ks, p.k, it.start, kvh, first, it.len, p.s.D, p.vec);
+    load_tile<DT, T, DP>(vs, p.v, it.start, kvh, first, it.len, p.s.D, p.vec);
+    float4 dk[R][U], dv[R][U];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int u = 0; u < U; ++u) dk[r][u] = dv[r][u] = make_float4(0.f, 0.f, 0.f, 0.f);
+    // last query that sees a key of the tile: window - 1 tokens after its last key, or the last of all for sinks
+    const int64_t last = first < p.s.sinks ? it.len - 1 : tmin<int64_t>(it.len - 1, (int64_t)first + T - 1 + p.s.window - 1);
+    const int qt_end = (int)(last / T) + 1;
+    for (int g = 0; g < p.s.G; ++g) {
+        const int head = kvh * p.s.G + g;
+        for (int qt = kt; qt < qt_end; ++qt) {
+            __syncthreads();
+            load_tile<DT, T, DP>(qs, p.q, it.start, head, qt * T, it.len, p.s.D, p.vec);
+            load_tile<DT, T, DP>(gs, p.g, it.start, head, qt * T, it.len, p.s.D, p.vec);
+            if (p.bias) load_bias<DT, T>(bt, p.s, p.bias, head, (qt - kt) * T);
+            if (threadIdx.x < T) {
+                const int i = qt * T + threadIdx.x;
+                float x = INFINITY, y = 0.f;
+                if (i < it.len) {
+                    x = p.lse[(int64_t)head * p.N + it.start + i];
+                    y = p.delta[(int64_t)head * p.N + it.start + i];
+                    if (x == -INFINITY) x = INFINITY;
+                }
+                ls[threadIdx.x] = x;
+                de[threadIdx.x] = y;
+            }
+            __syncthreads();
+            float s[R][R], dp[R][R];
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int c = 0; c < R; ++c) s[r][c] = dp[r][c] = 0.f;
+            dot_tile<T, DP>(s, ks, qs, tx, ty);
+            dot_tile<T, DP>(dp, vs, gs, tx, ty);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const int j = first + ty * R + r;
+#pragma unroll
+                for (int c = 0; c < R; ++c) {
+                    const int ii = tx + 16 * c, i = qt * T + ii;
+                    float x = s[r][c] * c2;
+                    if (p.bias) x += bt[ii - (ty * R + r) + T - 1];
+                    const bool seen = i < it.len && attn_visible(i - j, j, p.s.window, p.s.sinks);
+                    const float e = seen ? ex2(x - ls[ii]) : 0.f;
+                    ps[(ty * R + r) * PLD + ii] = e;
+                    const bool live = seen && !attn_lone(i, j, p.s.window, p.s.sinks);
+                    s[r][c] = live ? e * (dp[r][c] - de[ii]) : 0.f;
+                }
+            }
+            __syncwarp();  // a warp reads only the rows of ps that it wrote
+            mul_tile<T, DP>(dv, ps, gs, tx, ty);
+            __syncwarp();
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int c = 0; c < R; ++c) ps[(ty * R + r) * PLD + tx + 16 * c] = s[r][c];
+            __syncwarp();
+            mul_tile<T, DP>(dk, ps, qs, tx, ty);
+        }
+    }
+    float one[R], mul[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        one[r] = 1.f;
+        mul[r] = p.s.scale;
+    }
+    store_rows<DT, T, DP>(p.gv, dv, one, it.start, p.s.Hk, kvh, first, it.len, p.s.D, tx, ty);
+    store_rows<DT, T, DP>(p.gk, dk, mul, it.start, p.s.Hk, kvh, first, it.len, p.s.D, tx, ty);
+}
+
+// Work items of the batch, and the offsets' check: histories of n tiles of
+// `tile` tokens, each history's last tile first.  One CTA; 1024 histories a
+// pass.  A history whose offsets are not ordered within [0, N] gets no item.
+template <typename I>
+__global__ void __launch_bounds__(1024) attn_items_kernel(const I* __restrict__ off, int64_t N, int B, int tile,
+                                                          AttnItem* __restrict__ items, int64_t capacity,
+                                                          int32_t* n_items, uint32_t* error) {
+    __shared__ int32_t warp_sum[32];
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    int64_t base = 0;
+    for (int b0 = 0; b0 < B; b0 += 1024) {
+        const int b = b0 + threadIdx.x;
+        int64_t lo = 0, hi = 0;
+        if (b < B) {
+            lo = (int64_t)off[b];
+            hi = (int64_t)off[b + 1];
+            const bool bad = lo < 0 || hi < lo || hi > N;
+            if (bad || (b == 0 && lo != 0) || (b == B - 1 && hi != N)) atomicOr(error, ERR_OFFSETS);
+            if (bad) hi = lo = 0;
+        }
+        const int n = (int)((hi - lo + tile - 1) / tile);
+        int incl = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int t = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += t;
+        }
+        if (lane == 31) warp_sum[warp] = incl;
+        __syncthreads();
+        int before = 0, all = 0;
+        for (int k = 0; k < 32; ++k) {
+            if (k < warp) before += warp_sum[k];
+            all += warp_sum[k];
+        }
+        __syncthreads();
+        const int64_t at = base + before + incl - n;
+        for (int k = 0; k < 32; ++k) {  // the warp writes its histories' items one history after another
+            const int nk = __shfl_sync(0xffffffffu, n, k);
+            const int64_t ak = __shfl_sync(0xffffffffu, at, k);
+            const int sk = (int)__shfl_sync(0xffffffffu, lo, k);
+            const int lk = (int)(__shfl_sync(0xffffffffu, hi, k)) - sk;
+            for (int t = lane; t < nk; t += 32)
+                if (ak + t < capacity) items[ak + t] = AttnItem{sk, lk, nk - 1 - t, nk};
+        }
+        base += all;
+    }
+    if (threadIdx.x == 0) *n_items = (int32_t)tmin<int64_t>(base, capacity);
+}
+
+// grad_bias[bucket, head] = the items' shares added up in a fixed order: a
+// warp per (bucket, head), its lanes over the items, then a tree.
+template <int DT>
+__global__ void __launch_bounds__(256) attn_bias_reduce_kernel(const float* __restrict__ part,
+                                                               const int32_t* __restrict__ n_items, int H,
+                                                               int buckets, void* grad_bias) {
+    const int pair = blockIdx.x * 8 + threadIdx.x / 32, lane = threadIdx.x % 32;
+    if (pair >= H * buckets) return;
+    const int head = pair / buckets, b = pair % buckets;
+    const int n = *n_items;
+    float t = 0.f;
+    for (int w = lane; w < n; w += 32) t += part[((int64_t)w * H + head) * buckets + b];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    if (lane == 0) store_elem<DT>(grad_bias, (int64_t)b * H + head, t);
+}
+
+template <int T, int DP>
+constexpr size_t fwd_smem() {
+    return 3 * Tile<T, DP>::bytes + Tile<T, DP>::pbytes + sizeof(float) * 2 * T;
+}
+template <int T, int DP>
+constexpr size_t bwd_smem() {
+    return 4 * Tile<T, DP>::bytes + Tile<T, DP>::pbytes + sizeof(float) * 4 * T;
+}
+
+template <typename K>
+cudaError_t allow(K kernel, size_t bytes, int optin) {
+    if (bytes > (size_t)optin) return cudaErrorInvalidConfiguration;
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
+template <int DT, int T, int DP>
+cudaError_t configure(int optin) {
+    cudaError_t e = allow(attn_fwd_simt_kernel<DT, T, DP>, fwd_smem<T, DP>(), optin);
+    if (e == cudaSuccess) e = allow(attn_dq_simt_kernel<DT, T, DP>, bwd_smem<T, DP>(), optin);
+    if (e == cudaSuccess) e = allow(attn_dkv_simt_kernel<DT, T, DP>, bwd_smem<T, DP>(), optin);
+    return e;
+}
+
+template <int DT, int T, int DP>
+cudaError_t forward(const AttnForward& p, int64_t n, cudaStream_t s) {
+    attn_fwd_simt_kernel<DT, T, DP><<<(unsigned)(n * p.s.H), kThreads, fwd_smem<T, DP>(), s>>>(p);
+    return cudaGetLastError();
+}
+
+template <int DT, int T, int DP>
+cudaError_t backward(const AttnBackward& p, int64_t n, cudaStream_t s) {
+    attn_dq_simt_kernel<DT, T, DP><<<(unsigned)(n * p.s.H), kThreads, bwd_smem<T, DP>(), s>>>(p);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    attn_dkv_simt_kernel<DT, T, DP><<<(unsigned)(n * p.s.Hk), kThreads, bwd_smem<T, DP>(), s>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+int attn_simt_tile(int D) { return D <= 128 ? 64 : 32; }
+
+cudaError_t attn_simt_configure(int optin) {
+    cudaError_t e = cudaSuccess;
+    auto all = [&](auto dt) {
+        constexpr int DT = decltype(dt)::value;
+        if (e == cudaSuccess) e = configure<DT, 64, 64>(optin);
+        if (e == cudaSuccess) e = configure<DT, 64, 128>(optin);
+        if (e == cudaSuccess) e = configure<DT, 32, 256>(optin);
+    };
+    all(std::integral_constant<int, DT_F32>{});
+    all(std::integral_constant<int, DT_F16>{});
+    all(std::integral_constant<int, DT_BF16>{});
+    return e;
+}
+
+#define ATTN_BY_TYPE_AND_DIM(CALL)                                          \
+    do {                                                                    \
+        const int D = p.s.D;                                                \
+        if (p.s.dtype == DT_F32) {                                          \
+            if (D <= 64) return CALL<DT_F32, 64, 64>(p, max_items, s);      \
+            if (D <= 128) return CALL<DT_F32, 64, 128>(p, max_items, s);    \
+            return CALL<DT_F32, 32, 256>(p, max_items, s);                  \
+        } else if (p.s.dtype == DT_F16) {                                   \
+            if (D <= 64) return CALL<DT_F16, 64, 64>(p, max_items, s);      \
+            if (D <= 128) return CALL<DT_F16, 64, 128>(p, max_items, s);    \
+            return CALL<DT_F16, 32, 256>(p, max_items, s);                  \
+        } else {                                                            \
+            if (D <= 64) return CALL<DT_BF16, 64, 64>(p, max_items, s);     \
+            if (D <= 128) return CALL<DT_BF16, 64, 128>(p, max_items, s);   \
+            return CALL<DT_BF16, 32, 256>(p, max_items, s);                 \
+        }                                                                   \
+    } while (0)
+
+cudaError_t launch_attn_forward_simt(const AttnForward& p, int64_t max_items, cudaStream_t s) {
+    ATTN_BY_TYPE_AND_DIM(forward);
+}
+
+cudaError_t launch_attn_backward_simt(const AttnBackward& p, int64_t max_items, cudaStream_t s) {
+    ATTN_BY_TYPE_AND_DIM(backward);
+}
+
+cudaError_t launch_attn_items(const void* offsets, int index64, int64_t N, int B, int tile, AttnItem* items,
+                              int64_t capacity, int32_t* n_items, uint32_t* error, cudaStream_t s) {
+    if (index64)
+        attn_items_kernel<int64_t><<<1, 1024, 0, s>>>(static_cast<const int64_t*>(offsets), N, B, tile, items, capacity,
+                                                      n_items, error);
+    else
+        attn_items_kernel<int32_t><<<1, 1024, 0, s>>>(static_cast<const int32_t*>(offsets), N, B, tile, items, capacity,
+                                                      n_items, error);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_attn_bias_reduce(const AttnBackward& p, void* grad_bias, cudaStream_t s) {
+    const int grid = (p.s.H * p.s.buckets + 7) / 8;
+    if (p.s.dtype == DT_F32)
+        attn_bias_reduce_kernel<DT_F32><<<grid, 256, 0, s>>>(p.bias_part, p.n_items, p.s.H, p.s.buckets, grad_bias);
+    else if (p.s.dtype == DT_F16)
+        attn_bias_reduce_kernel<DT_F16><<<grid, 256, 0, s>>>(p.bias_part, p.n_items, p.s.H, p.s.buckets, grad_bias);
+    else
+        attn_bias_reduce_kernel<DT_BF16><<<grid, 256, 0, s>>>(p.bias_part, p.n_items, p.s.H, p.s.buckets, grad_bias);
+    return cudaGetLastError();
+}
+
+}  // namespace tbe
