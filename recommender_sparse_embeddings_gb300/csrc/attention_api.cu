@@ -62,6 +62,11 @@ bool pages_ok(const tbe_pages* r) {
     return r && r->data && r->page_stride >= 0 && r->token_stride >= 0 && r->head_stride >= 0;
 }
 
+// The tensor-core kernels take 16-bit rows of up to 128 columns that are
+// 16-byte aligned; they hold tiles of 128 tokens.
+constexpr int kMmaTile = 128;
+bool takes_mma(const tbe_attention* h, bool vec) { return vec && h->s.dtype != TBE_F32 && h->s.D <= 128; }
+
 Rows as_rows(const tbe_rows& r) { return Rows{r.data, r.token_stride, r.head_stride}; }
 
 bool batch_within_limits(const tbe_attention* h, int64_t N, int64_t B) {
@@ -170,6 +175,8 @@ int tbe_attention_create(const tbe_attention_config* c, tbe_attention** out) {
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, h->device);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, h->device);
     if (e == cudaSuccess) e = attn_simt_configure(optin);
+    if (e == cudaSuccess) e = attn_forward_mma_configure();
+    if (e == cudaSuccess) e = attn_backward_mma_configure();
     if (e != cudaSuccess) {
         delete h;
         return cuda_fail(e);
@@ -241,12 +248,13 @@ int tbe_attention_forward(tbe_attention* h, const tbe_rows* q, const tbe_rows* k
     p.items = at<AttnItem>(workspace, L.items);
     p.n_items = at<int32_t>(workspace, L.n_items);
     p.vec = vec_rows(h, *q) && vec_rows(h, *k) && vec_rows(h, *v) && aligned16(out);
-    const int tile = attn_simt_tile(h->s.D);
+    const bool mma = takes_mma(h, p.vec);
+    const int tile = mma ? kMmaTile : attn_simt_tile(h->s.D);
     const int64_t most = N / tile + B;
     rc = status(launch_attn_items(offsets, index_dtype == TBE_I64, N, B, tile, at<AttnItem>(workspace, L.items), most,
                                   at<int32_t>(workspace, L.n_items), h->s.error, s));
     if (rc || N == 0) return rc;
-    return status(launch_attn_forward_simt(p, most, s));
+    return status(mma ? launch_attn_forward_mma(p, most, s) : launch_attn_forward_simt(p, most, s));
 }
 
 int tbe_attention_backward(tbe_attention* h, const tbe_rows* q, const tbe_rows* k, const tbe_rows* v, const void* bias,
@@ -282,12 +290,13 @@ int tbe_attention_backward(tbe_attention* h, const tbe_rows* q, const tbe_rows* 
     p.n_items = at<int32_t>(workspace, L.n_items);
     p.vec = vec_rows(h, *q) && vec_rows(h, *k) && vec_rows(h, *v) && vec_rows(h, *grad_out) && aligned16(out) &&
             aligned16(grad_q) && aligned16(grad_k) && aligned16(grad_v);
-    const int tile = attn_simt_tile(h->s.D);
+    const bool mma = takes_mma(h, p.vec);
+    const int tile = mma ? kMmaTile : attn_simt_tile(h->s.D);
     const int64_t most = N / tile + B;
     rc = status(launch_attn_items(offsets, index_dtype == TBE_I64, N, B, tile, at<AttnItem>(workspace, L.items), most,
                                   at<int32_t>(workspace, L.n_items), h->s.error, s));
     if (rc) return rc;
-    if (N > 0) rc = status(launch_attn_backward_simt(p, most, s));
+    if (N > 0) rc = status(mma ? launch_attn_backward_mma(p, most, s) : launch_attn_backward_simt(p, most, s));
     if (rc || !bias) return rc;
     return status(launch_attn_bias_reduce(p, grad_bias, s));
 }

@@ -1,0 +1,675 @@
+// Attention over ragged histories on the tensor cores (tcgen05), backward.
+//
+// Two kernels, each summing its gradients inside one CTA in a fixed order
+// (no atomics, no fp32 copies of the gradients in memory), at the price of
+// recomputing the logits twice (seven products instead of five):
+//
+// dq (128 queries of one head; key blocks of 64):
+//   S = Q K^T, dP = G V^T, dS = P (dP - delta), dQ += dS K
+//   and the bias gradient: dS summed by bucket of the distance.
+// dkv (128 keys of one key-value head; query blocks of 64, over the group's
+// heads), transposed so that P^T and dS^T are products' first operands and
+// stay in tensor memory:
+//   S^T = K Q^T, dP^T = V G^T, dV += P^T G, dK += dS^T Q
+//
+// A thread owns one row of S (a query in dq, a key in dkv).  head_dim <= 64:
+// one warpgroup and one set of score buffers, two CTAs per SM that fill each
+// other's gaps (256 TMEM columns each).  Above: one CTA per SM (shared
+// memory), two warpgroups that take the blocks in turn, each with its own
+// score buffers, so one block's products run beside the other's arithmetic.
+//
+// P and dS are rounded to the 16-bit type where they enter a product; the
+// bias gradient sums the unrounded fp32 dS.
+#include "attention_mma.cuh"
+
+namespace tbe {
+
+namespace {
+
+template <int DP>
+struct Shape {
+    static constexpr int NB = DP == 64 ? 1 : 2;  // warpgroups and score buffers
+    static constexpr int kThreads = NB * 128 + 128;
+    static constexpr int kPerSm = DP == 64 ? 2 : 1;
+    static constexpr int kStages = DP == 64 ? 3 : 3;
+    static constexpr int kBig = 128 * DP * 2;   // a 128-row tile
+    static constexpr int kSmall = 64 * DP * 2;  // a 64-row tile
+    static constexpr int a = 0, b = kBig, x = 2 * kBig, y = x + kStages * kSmall;
+    static constexpr int table = y + kStages * kSmall;      // bias by distance, 2 x 192 floats
+    static constexpr int stat = table + 2 * 192 * 4;        // dkv: -lse and delta, 2 x 2 x 64 floats
+    static constexpr int sums = stat + 2 * 2 * 64 * 4;      // dq: per warp, a sum per bucket
+    static constexpr int diag = sums + NB * 4 * kMaxBuckets * 4;  // dq: per warp, 96 diagonals
+    static constexpr int dq_bytes = diag + NB * 4 * 96 * 4 + 1024;
+    static constexpr int dkv_bytes = sums + 1024;
+    // TMEM columns: scores, score gradients, 16-bit dS (dq only), accumulators
+    static constexpr int cols = DP == 64 ? 256 : 512;
+};
+
+struct Bars {
+    uint64_t big_full, x_full[3], x_empty[3], y_full[3], y_empty[3], s_full[2], ds_full[2], t_full[2], t_empty[2],
+        v_done, k_done, last;
+};
+
+template <int NB>
+__device__ __forceinline__ void init_bars(Bars& b) {
+    mbar_init(&b.big_full, 2);
+    for (int i = 0; i < 3; ++i) {
+        mbar_init(&b.x_full[i], 1);
+        mbar_init(&b.x_empty[i], 1);
+        mbar_init(&b.y_full[i], 1);
+        mbar_init(&b.y_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+        mbar_init(&b.s_full[i], 1);
+        mbar_init(&b.ds_full[i], 4);
+        mbar_init(&b.t_full[i], 1);
+        mbar_init(&b.t_empty[i], 4);
+    }
+    mbar_init(&b.v_done, 1);
+    mbar_init(&b.k_done, 1);
+    mbar_init(&b.last, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    fence_proxy_async_smem();
+}
+
+// A loader warp: its 128-row tile, then `steps` 64-row tiles through the
+// stages; tile n is signalled once tile n + 1 is under way.  place(n) gives
+// tile n's first row and head.
+template <int DP, typename F>
+__device__ __forceinline__ bool run_loader(uint32_t big, const Rows& big_rows, int big_head, int big_first,
+                                           uint32_t ring, const Rows& rows, uint64_t* big_full, uint64_t* full,
+                                           uint64_t* empty, const AttnItem& it, int D, int steps, int lane, F place) {
+    using L = Shape<DP>;
+    load_tile_async<128, DP>(big, big_rows, it.start, big_head, big_first, it.len, D, lane);
+    cp_async_commit();
+    bool ok = true;
+    for (int n = 0; n <= steps; ++n) {
+        if (n < steps) {
+            const int st = n % L::kStages;
+            if (n >= L::kStages) ok = mbar_wait_tight(&empty[st], ((n / L::kStages) - 1) & 1);
+            if (!__all_sync(0xffffffffu, ok)) {
+                ok = false;
+                break;
+            }
+            const int2 at = place(n);
+            load_tile_async<64, DP>(ring + st * L::kSmall, rows, it.start, at.y, at.x, it.len, D, lane);
+        }
+        cp_async_commit();
+        cp_async_wait<1>();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(n == 0 ? big_full : &full[(n - 1) % L::kStages]);
+    }
+    cp_async_wait<0>();
+    return ok;
+}
+
+// The helper warp's table of one block: entry x is the bias (base 2) at
+// distance least + x, 191 of them; nothing where all share one bucket.
+// Returns whether they do, and that bucket's bias.
+template <int DT>
+__device__ __forceinline__ bool spread_bias(float* bt, const AttnShape& s, const void* bias, int head, int least,
+                                            int lane, float& same, int& bucket) {
+    bucket = attn_bucket(s, tmax(0, least));
+    const int b1 = attn_bucket(s, tmax(0, least + 190));
+    same = bias_base2(load_elem<DT>(bias, (int64_t)bucket * s.H + head));
+    if (bucket == b1) return true;
+    for (int x = lane; x < 191; x += 32) {
+        const int d = least + x;
+        bt[x] = d >= 0 ? bias_base2(load_elem<DT>(bias, (int64_t)attn_bucket(s, d) * s.H + head)) : 0.f;
+    }
+    return false;
+}
+
+// ------------------------------------------------------------------- dq
+
+template <int DT, int DP>
+__global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_dq_mma_kernel(const AttnBackward p) {
+    using L = Shape<DP>;
+    constexpr int NB = L::NB, kHelp = NB * 4;  // first helper warp: products; then loaders K, V; then bias
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    __shared__ Bars bars;
+    __shared__ uint32_t tmem_slot;
+    __shared__ float same_bias[2];
+    __shared__ int same_bucket[2];  // -1: the block's distances have several
+
+    const int64_t w = blockIdx.x / p.s.H;
+    const int head = (int)(blockIdx.x % p.s.H);
+    if (w >= *p.n_items) return;
+    const AttnItem it = p.items[w];
+    const int kvh = head / p.s.G, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int first = it.tile * 128, D = p.s.D, ksteps = (D + 15) / 16;
+    const int hi = tmin(first + 127, it.len - 1) / 64 + 1;
+    const int64_t from = (int64_t)first - p.s.window + 1;
+    const int lo = from > 0 ? (int)(from / 64) : 0;
+    const int sink_blocks = tmin((p.s.sinks + 63) / 64, lo);
+    const int steps = sink_blocks + hi - lo;
+    auto block_of = [&](int n) { return n < sink_blocks ? n : lo + n - sink_blocks; };
+
+    const uint32_t sbase = smem_u32(smem);
+    if (threadIdx.x == 0) init_bars<NB>(bars);
+    if (warp == kHelp) tmem_alloc(&tmem_slot, L::cols);
+    float* sums = reinterpret_cast<float*>(smem + L::sums);
+    for (int i = threadIdx.x; i < NB * 4 * p.s.buckets; i += L::kThreads)
+        sums[i / p.s.buckets * kMaxBuckets + i % p.s.buckets] = 0.f;
+    tcgen05_before_sync();
+    __syncthreads();
+    tcgen05_after_sync();
+    const uint32_t tmem = tmem_slot;
+    const uint32_t t_ds = tmem + NB * 128, t_acc = t_ds + NB * 32;  // S at buf*128, dP at buf*128 + 64
+    bool ok = true;
+
+    if (warp == kHelp) {
+        if (lane == 0) {
+            const uint32_t id_s = mma_idesc(DT == DT_BF16, 128, 64);
+            const uint32_t id_o = mma_idesc(DT == DT_BF16, 128, ksteps * 16) | kMnMajorB;
+            ok = mbar_wait_tight(&bars.big_full, 0);
+            auto scores = [&](int n) {
+                const int st = n % L::kStages;
+                const uint32_t t = tmem + (n % NB) * 128;
+                if (!mbar_wait_tight(&bars.x_full[st], (n / L::kStages) & 1)) return false;
+                tcgen05_after_sync();
+                for (int k = 0; k < ksteps; ++k) {
+                    const uint32_t oa = (k / 4) * (128 * 128) + (k % 4) * 32, ob = (k / 4) * (64 * 128) + (k % 4) * 32;
+                    mma_f16(t, smem_desc_sw128(sbase + L::a + oa, 1024),
+                            smem_desc_sw128(sbase + L::x + st * L::kSmall + ob, 1024), id_s, k > 0);
+                }
+                if (!mbar_wait_tight(&bars.y_full[st], (n / L::kStages) & 1)) return false;
+                tcgen05_after_sync();
+                for (int k = 0; k < ksteps; ++k) {
+                    const uint32_t oa = (k / 4) * (128 * 128) + (k % 4) * 32, ob = (k / 4) * (64 * 128) + (k % 4) * 32;
+                    mma_f16(t + 64, smem_desc_sw128(sbase + L::b + oa, 1024),
+                            smem_desc_sw128(sbase + L::y + st * L::kSmall + ob, 1024), id_s, k > 0);
+                }
+                if (n + L::kStages < steps) mma_commit(&bars.y_empty[st]);
+                mma_commit(&bars.s_full[n % NB]);
+                return true;
+            };
+            for (int n = 0; n < NB && n < steps && ok; ++n) ok = scores(n);
+            for (int n = 0; n < steps && ok; ++n) {
+                const int st = n % L::kStages;
+                ok = mbar_wait_tight(&bars.ds_full[n % NB], (n / NB) & 1);
+                if (!ok) break;
+                tcgen05_after_sync();
+                for (int k = 0; k < 4; ++k)
+                    mma_f16_ts(t_acc, t_ds + (n % NB) * 32 + k * 8,
+                               smem_desc_mn(sbase + L::x + st * L::kSmall + k * 2048, 64 * 128), id_o, n > 0 || k > 0);
+                if (n + L::kStages < steps) mma_commit(&bars.x_empty[st]);
+                if (n + 1 == steps) mma_commit(&bars.last);
+                // dS(n) is out, so S(n) and dP(n) are read; their commit also
+                // covers dQ's product, so dS(n + NB) may overwrite dS(n)
+                if (n + NB < steps) ok = scores(n + NB);
+            }
+        }
+        __syncwarp();
+    } else if (warp == kHelp + 1) {
+        ok = run_loader<DP>(sbase + L::a, p.q, head, first, sbase + L::x, p.k, &bars.big_full, bars.x_full,
+                            bars.x_empty, it, D, steps, lane, [&](int n) { return make_int2(block_of(n) * 64, kvh); });
+    } else if (warp == kHelp + 2) {
+        ok = run_loader<DP>(sbase + L::b, p.g, head, first, sbase + L::y, p.v, &bars.big_full, bars.y_full,
+                            bars.y_empty, it, D, steps, lane, [&](int n) { return make_int2(block_of(n) * 64, kvh); });
+    } else if (warp == kHelp + 3) {
+        if (p.bias) {
+            float* bt = reinterpret_cast<float*>(smem + L::table);
+            for (int n = 0; n < steps; ++n) {
+                const int buf = n & 1;
+                if (n >= 2) ok = mbar_wait_tight(&bars.t_empty[buf], ((n / 2) - 1) & 1);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    ok = false;
+                    break;
+                }
+                float same;
+                int bucket;
+                const bool one = spread_bias<DT>(bt + buf * 192, p.s, p.bias, head, first - block_of(n) * 64 - 63, lane,
+                                                 same, bucket);
+                if (lane == 0) {
+                    same_bias[buf] = same;
+                    same_bucket[buf] = one ? bucket : -1;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars.t_full[buf]);
+            }
+        }
+    } else {
+        const int wg = warp / 4, q4 = warp % 4, row = q4 * 32 + lane, i = first + row;
+        const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
+        const float c2 = p.s.scale * kLog2e;
+        const float* bt = reinterpret_cast<const float*>(smem + L::table);
+        float* mine = sums + warp * kMaxBuckets;
+        float* diag = reinterpret_cast<float*>(smem + L::diag) + warp * 96;
+        float less = -INFINITY, delta = 0.f;
+        if (i < it.len) {
+            const int64_t at = (int64_t)head * p.N + it.start + i;
+            const float x = p.lse[at];
+            less = x == -INFINITY ? -INFINITY : -x;  // a row that sees nothing: all its weights 2^-inf
+            delta = p.delta[at];
+        }
+        for (int n = wg; n < steps; n += NB) {
+            const int buf = n & 1, sb = n % NB;
+            const uint32_t t_s = tmem + sb * 128 + lanes;
+            ok = mbar_wait_tight(&bars.s_full[sb], (n / NB) & 1);
+            if (ok && p.bias) ok = mbar_wait_tight(&bars.t_full[buf], (n / 2) & 1);
+            if (!__all_sync(0xffffffffu, ok)) {
+                ok = false;
+                break;
+            }
+            tcgen05_after_sync();
+            const int key0 = block_of(n) * 64, base = first - key0;
+            const int bucket = p.bias ? same_bucket[buf] : 0;
+            const float add = less + (p.bias && bucket >= 0 ? same_bias[buf] : 0.f);
+            const bool all = key0 + 63 < first && (first + 127 - key0 < p.s.window || key0 + 63 < p.s.sinks);
+            float sum0 = 0.f, sum1 = 0.f, run = 0.f;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float x[32], y[32];
+                tmem_ld32_issue(t_s + 32 * h, x);
+                tmem_ld32_issue(t_s + 64 + 32 * h, y);
+                tmem_wait_ld(x, 32);
+                tmem_wait_ld(y, 32);
+                if (bucket < 0) {
+                    const float* b = bt + buf * 192 + row + 63 - 32 * h;
+#pragma unroll
+                    for (int c = 0; c < 32; c += 2) {
+                        float b0 = b[-c], b1 = b[-c - 1];
+                        add2(b0, b1, less, less);
+                        fma2(x[c], x[c + 1], c2, b0, b1);
+                    }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 32; c += 2) fma2(x[c], x[c + 1], c2, add, add);
+                }
+                if (!all) {
+                    const int up = i - key0 + 1 - 32 * h, down = i - p.s.window + 1 - key0 - 32 * h,
+                              sk = p.s.sinks - key0 - 32 * h;
+                    uint32_t seen = bits_below(up) & (~bits_below(down) | bits_below(sk));
+                    // the only key a query sees: no gradient (attn_lone)
+                    if (attn_lone(i, i, p.s.window, p.s.sinks) && up >= 1 && up <= 32) seen &= ~(1u << (up - 1));
+#pragma unroll
+                    for (int c = 0; c < 32; ++c)
+                        if (!(seen >> c & 1)) x[c] = -INFINITY;
+                }
+#pragma unroll
+                for (int c = 0; c < 32; c += 2) {
+                    x[c] = ex2(x[c]);
+                    x[c + 1] = ex2(x[c + 1]);
+                    add2(y[c], y[c + 1], -delta, -delta);
+                    mul2(x[c], x[c + 1], y[c], y[c + 1]);
+                }
+                uint32_t pk[16];
+#pragma unroll
+                for (int c = 0; c < 16; ++c) pk[c] = pack2<DT>(x[2 * c], x[2 * c + 1]);
+                tmem_st16(t_ds + sb * 32 + lanes + 16 * h, pk);
+                if (p.bias) {
+                    if (bucket >= 0) {
+#pragma unroll
+                        for (int c = 0; c < 32; c += 2) add2(sum0, sum1, x[c], x[c + 1]);
+                    } else {
+                        // a diagonal's sum moves one lane up a column: complete at lane 31
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) {
+                            const float t = __shfl_up_sync(0xffffffffu, run, 1);
+                            run = x[c] + (lane == 0 ? 0.f : t);
+                            if (lane == 31) diag[94 - 32 * h - c] = run;
+                        }
+                    }
+                }
+            }
+            tmem_wait_st();
+            tcgen05_before_sync();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&bars.ds_full[sb]);
+                if (p.bias) mbar_arrive(&bars.t_empty[buf]);
+            }
+            if (p.bias && bucket >= 0) {
+                float t = sum0 + sum1;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+                if (lane == 0) mine[bucket] += t;
+                __syncwarp();
+            } else if (p.bias) {
+                // diag[x], x in [0, 95): distance base + 32 q4 + x - 63; the
+                // last column's running sums are the lowest 32
+                if (lane < 31) diag[lane] = run;
+                __syncwarp();
+#pragma unroll
+                for (int r = 0; r < 3; ++r) {
+                    // sums of equal buckets, which are neighbours: a segmented
+                    // scan over 32 distances, added by each segment's last lane
+                    const int x = r * 32 + lane, d = base + 32 * q4 + x - 63;
+                    int b = x < 95 && d >= 0 ? attn_bucket(p.s, d) : -1;
+                    float t = b >= 0 ? diag[x] : 0.f;
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const float tu = __shfl_up_sync(0xffffffffu, t, o);
+                        const int bu = __shfl_up_sync(0xffffffffu, b, o);
+                        if (lane >= o && bu == b) t += tu;
+                    }
+                    const int next = __shfl_down_sync(0xffffffffu, b, 1);
+                    if (b >= 0 && (lane == 31 || next != b)) mine[b] += t;
+                    __syncwarp();
+                }
+            }
+        }
+        if (ok) ok = mbar_wait_tight(&bars.last, 0);
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok) {
+            tcgen05_after_sync();
+            // the warpgroups take the accumulator's 64-column slabs in turn
+            unsigned char* qt = smem + L::a;
+#pragma unroll
+            for (int c = wg * 64; c < wg * 64 + 64; c += 32) tmem_to_tile<DT>(qt, t_acc + lanes, c, row, p.s.scale);
+        }
+    }
+    if (!ok) atomicOr(p.s.error, ERR_TIMEOUT);
+    tcgen05_before_sync();
+    __syncthreads();
+    tcgen05_after_sync();
+    if (warp < 4) store_tile_rows<DP>(p.gq, smem + L::a, warp * 32, it.start, first, it.len, p.s.H, head, D, lane);
+    if (warp == kHelp) tmem_dealloc(tmem, L::cols);
+    for (int b = threadIdx.x; b < p.s.buckets; b += L::kThreads) {
+        float t = 0.f;
+        for (int k = 0; k < NB * 4; ++k) t += sums[k * kMaxBuckets + b];
+        p.bias_part[(w * p.s.H + head) * p.s.buckets + b] = t;
+    }
+}
+
+// ------------------------------------------------------------------ dkv
+
+template <int DT, int DP>
+__global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_dkv_mma_kernel(const AttnBackward p) {
+    using L = Shape<DP>;
+    constexpr int NB = L::NB, kHelp = NB * 4;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    __shared__ Bars bars;
+    __shared__ uint32_t tmem_slot;
+    __shared__ int several[2];  // the block's distances have several buckets
+
+    const int64_t w = blockIdx.x / p.s.Hk;
+    const int kvh = (int)(blockIdx.x % p.s.Hk);
+    if (w >= *p.n_items) return;
+    const AttnItem it = p.items[w];
+    const int kt = it.tiles - 1 - it.tile;  // the first tiles are seen most: they start first
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int first = kt * 128, D = p.s.D, ksteps = (D + 15) / 16;
+    // query blocks that see a key of the tile, for each head of the group
+    const int64_t end = first < p.s.sinks ? it.len - 1 : tmin<int64_t>(it.len - 1, (int64_t)first + 126 + p.s.window);
+    const int qb0 = first / 64, blocks = (int)(end / 64) + 1 - qb0, steps = blocks * p.s.G;
+    auto place = [&](int n) { return make_int2((qb0 + n % blocks) * 64, kvh * p.s.G + n / blocks); };
+
+    const uint32_t sbase = smem_u32(smem);
+    if (threadIdx.x == 0) init_bars<NB>(bars);
+    if (warp == kHelp) tmem_alloc(&tmem_slot, L::cols);
+    tcgen05_before_sync();
+    __syncthreads();
+    tcgen05_after_sync();
+    const uint32_t tmem = tmem_slot;
+    const uint32_t t_dk = tmem + NB * 128, t_dv = t_dk + DP;  // S^T at buf*128, dP^T at buf*128 + 64
+    bool ok = true;
+
+    if (warp == kHelp) {
+        if (lane == 0) {
+            const uint32_t id_s = mma_idesc(DT == DT_BF16, 128, 64);
+            const uint32_t id_o = mma_idesc(DT == DT_BF16, 128, ksteps * 16) | kMnMajorB;
+            ok = mbar_wait_tight(&bars.big_full, 0);
+            // S^T (which = 0: K Q^T) or dP^T (which = 1: V G^T) of block n
+            auto score = [&](int n, int which) {
+                const int st = n % L::kStages;
+                const uint32_t big = sbase + (which ? L::b : L::a);
+                const uint32_t small = sbase + (which ? L::y : L::x) + st * L::kSmall;
+                if (!mbar_wait_tight(which ? &bars.y_full[st] : &bars.x_full[st], (n / L::kStages) & 1)) return false;
+                tcgen05_after_sync();
+                for (int k = 0; k < ksteps; ++k) {
+                    const uint32_t oa = (k / 4) * (128 * 128) + (k % 4) * 32, ob = (k / 4) * (64 * 128) + (k % 4) * 32;
+                    mma_f16(tmem + (n % NB) * 128 + which * 64, smem_desc_sw128(big + oa, 1024),
+                            smem_desc_sw128(small + ob, 1024), id_s, k > 0);
+                }
+                if (which) mma_commit(&bars.s_full[n % NB]);
+                return true;
+            };
+            for (int n = 0; n < NB && n < steps && ok; ++n) ok = score(n, 0) && score(n, 1);
+            for (int n = 0; n < steps && ok; ++n) {
+                const int st = n % L::kStages;
+                const uint32_t t = tmem + (n % NB) * 128;
+                ok = mbar_wait_tight(&bars.ds_full[n % NB], (n / NB) & 1);
+                if (!ok) break;
+                tcgen05_after_sync();
+                for (int k = 0; k < 4; ++k)
+                    mma_f16_ts(t_dv, t + k * 8, smem_desc_mn(sbase + L::y + st * L::kSmall + k * 2048, 64 * 128), id_o,
+                               n > 0 || k > 0);
+                if (n + L::kStages < steps) mma_commit(&bars.y_empty[st]);
+                if (n + NB < steps) mma_commit(&bars.v_done);
+                for (int k = 0; k < 4; ++k)
+                    mma_f16_ts(t_dk, t + 64 + k * 8, smem_desc_mn(sbase + L::x + st * L::kSmall + k * 2048, 64 * 128),
+                               id_o, n > 0 || k > 0);
+                if (n + L::kStages < steps) mma_commit(&bars.x_empty[st]);
+                if (n + NB < steps) mma_commit(&bars.k_done);
+                if (n + 1 == steps) mma_commit(&bars.last);
+                // block n + NB's scores overwrite P^T and dS^T: each waits for
+                // its product, the first under the second's cover
+                if (n + NB < steps)
+                    ok = mbar_wait_tight(&bars.v_done, n & 1) && score(n + NB, 0) &&
+                         mbar_wait_tight(&bars.k_done, n & 1) && score(n + NB, 1);
+            }
+        }
+        __syncwarp();
+    } else if (warp == kHelp + 1) {
+        ok = run_loader<DP>(sbase + L::a, p.k, kvh, first, sbase + L::x, p.q, &bars.big_full, bars.x_full, bars.x_empty,
+                            it, D, steps, lane, place);
+    } else if (warp == kHelp + 2) {
+        ok = run_loader<DP>(sbase + L::b, p.v, kvh, first, sbase + L::y, p.g, &bars.big_full, bars.y_full, bars.y_empty,
+                            it, D, steps, lane, place);
+    } else if (warp == kHelp + 3) {
+        // per query of the block: -lse (plus the bias where the block has one
+        // bucket) and delta; the bias table else
+        float* bt = reinterpret_cast<float*>(smem + L::table);
+        float* stat = reinterpret_cast<float*>(smem + L::stat);
+        for (int n = 0; n < steps; ++n) {
+            const int buf = n & 1;
+            if (n >= 2) ok = mbar_wait_tight(&bars.t_empty[buf], ((n / 2) - 1) & 1);
+            if (!__all_sync(0xffffffffu, ok)) {
+                ok = false;
+                break;
+            }
+            const int2 at = place(n);
+            float same = 0.f;
+            bool one = true;
+            if (p.bias) {
+                int bucket;
+                one = spread_bias<DT>(bt + buf * 192, p.s, p.bias, at.y, at.x - first - 127, lane, same, bucket);
+            }
+#pragma unroll
+            for (int c = lane; c < 64; c += 32) {
+                const int i = at.x + c;
+                float less = -INFINITY, delta = 0.f;
+                if (i < it.len) {
+                    const int64_t k = (int64_t)at.y * p.N + it.start + i;
+                    const float x = p.lse[k];
+                    less = x == -INFINITY ? -INFINITY : (one ? same : 0.f) - x;
+                    delta = p.delta[k];
+                }
+                stat[buf * 128 + c] = less;
+                stat[buf * 128 + 64 + c] = -delta;
+            }
+            if (lane == 0) several[buf] = !one;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.t_full[buf]);
+        }
+    } else {
+        const int wg = warp / 4, q4 = warp % 4, row = q4 * 32 + lane, j = first + row;
+        const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
+        const float c2 = p.s.scale * kLog2e;
+        for (int n = wg; n < steps; n += NB) {
+            const int buf = n & 1, sb = n % NB;
+            const uint32_t t_s = tmem + sb * 128 + lanes;
+            ok = mbar_wait_tight(&bars.s_full[sb], (n / NB) & 1);
+            if (ok) ok = mbar_wait_tight(&bars.t_full[buf], (n / 2) & 1);
+            if (!__all_sync(0xffffffffu, ok)) {
+                ok = false;
+                break;
+            }
+            tcgen05_after_sync();
+            const int q0 = place(n).x;
+            const float* less = reinterpret_cast<const float*>(smem + L::stat) + buf * 128;
+            const bool table = several[buf];
+            const bool all = q0 > first + 127 && (q0 + 63 - first < p.s.window || first + 127 < p.s.sinks);
+            // whether the block holds a query whose only key is its own (attn_lone)
+            const bool lone = !all && (q0 == 0 || (p.s.window == 1 && p.s.sinks == 0));
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float x[32], y[32];
+                tmem_ld32_issue(t_s + 32 * h, x);
+                tmem_ld32_issue(t_s + 64 + 32 * h, y);
+                tmem_wait_ld(x, 32);
+                tmem_wait_ld(y, 32);
+                if (table) {
+                    const float* b = reinterpret_cast<const float*>(smem + L::table) + buf * 192 + 127 - row + 32 * h;
+#pragma unroll
+                    for (int c = 0; c < 32; c += 4) {
+                        const float4 t = *reinterpret_cast<const float4*>(less + 32 * h + c);
+                        float b0 = b[c], b1 = b[c + 1], b2 = b[c + 2], b3 = b[c + 3];
+                        add2(b0, b1, t.x, t.y);
+                        add2(b2, b3, t.z, t.w);
+                        fma2(x[c], x[c + 1], c2, b0, b1);
+                        fma2(x[c + 2], x[c + 3], c2, b2, b3);
+                    }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 32; c += 4) {
+                        const float4 t = *reinterpret_cast<const float4*>(less + 32 * h + c);
+                        fma2(x[c], x[c + 1], c2, t.x, t.y);
+                        fma2(x[c + 2], x[c + 3], c2, t.z, t.w);
+                    }
+                }
+                if (!all) {
+                    // query q0 + c sees key j: j <= q0 + c, and q0 + c < j + window or j a sink
+                    const int down = j - q0 - 32 * h, up = j < p.s.sinks ? INT_MAX : j + p.s.window - q0 - 32 * h;
+                    const uint32_t seen = ~bits_below(down) & bits_below(up);
+#pragma unroll
+                    for (int c = 0; c < 32; ++c)
+                        if (!(seen >> c & 1)) x[c] = -INFINITY;
+                }
+                uint32_t pk[16];
+#pragma unroll
+                for (int c = 0; c < 32; c += 4) {
+                    const float4 t = *reinterpret_cast<const float4*>(less + 64 + 32 * h + c);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[c + e] = ex2(x[c + e]);
+                    add2(y[c], y[c + 1], t.x, t.y);
+                    add2(y[c + 2], y[c + 3], t.z, t.w);
+                    mul2(y[c], y[c + 1], x[c], x[c + 1]);
+                    mul2(y[c + 2], y[c + 3], x[c + 2], x[c + 3]);
+                    pk[c / 2] = pack2<DT>(x[c], x[c + 1]);
+                    pk[c / 2 + 1] = pack2<DT>(x[c + 2], x[c + 3]);
+                }
+                if (lone) {
+                    const int own = j - q0 - 32 * h;  // the column of the key's own token
+#pragma unroll
+                    for (int c = 0; c < 32; ++c)
+                        if (c == own && attn_lone(j, j, p.s.window, p.s.sinks)) y[c] = 0.f;
+                }
+                uint32_t dk[16];
+#pragma unroll
+                for (int c = 0; c < 16; ++c) dk[c] = pack2<DT>(y[2 * c], y[2 * c + 1]);
+                // P^T into S^T's first columns, dS^T into dP^T's: the columns
+                // this thread has read already (h = 0 writes 16 of the 32 read)
+                tmem_st16(t_s + 16 * h, pk);
+                tmem_st16(t_s + 64 + 16 * h, dk);
+            }
+            tmem_wait_st();
+            tcgen05_before_sync();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&bars.ds_full[sb]);
+                mbar_arrive(&bars.t_empty[buf]);
+            }
+        }
+        if (ok) ok = mbar_wait_tight(&bars.last, 0);
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok) {
+            tcgen05_after_sync();
+            // dk into K's tile, dv into V's; two warpgroups take one each
+            if (wg == 0)
+#pragma unroll
+                for (int c = 0; c < DP; c += 32) tmem_to_tile<DT>(smem + L::a, t_dk + lanes, c, row, p.s.scale);
+            if (wg == NB - 1)
+#pragma unroll
+                for (int c = 0; c < DP; c += 32) tmem_to_tile<DT>(smem + L::b, t_dv + lanes, c, row, 1.f);
+        }
+    }
+    if (!ok) atomicOr(p.s.error, ERR_TIMEOUT);
+    tcgen05_before_sync();
+    __syncthreads();
+    tcgen05_after_sync();
+    if (warp < 4)
+        store_tile_rows<DP>(p.gk, smem + L::a, warp * 32, it.start, first, it.len, p.s.Hk, kvh, D, lane);
+    else if (warp < 8)
+        store_tile_rows<DP>(p.gv, smem + L::b, (warp - 4) * 32, it.start, first, it.len, p.s.Hk, kvh, D, lane);
+    if (warp == kHelp) tmem_dealloc(tmem, L::cols);
+}
+
+// delta_i = g_i . out_i of every (token, head): eight lanes a row, 16 bytes a
+// lane and step.  Memory-bound (each row of g and out is read once).
+template <int DT>
+__global__ void __launch_bounds__(256) attn_delta_kernel(const AttnBackward p) {
+    const int64_t r = (int64_t)blockIdx.x * 32 + threadIdx.x / 8;
+    const int chunk = threadIdx.x % 8;
+    const int64_t token = r / p.s.H;
+    const int head = (int)(r % p.s.H);
+    float t = 0.f;
+    if (token < p.N) {
+        const uint16_t* g = static_cast<const uint16_t*>(p.g.data) + token * p.g.token_stride + head * p.g.head_stride;
+        const uint16_t* o = static_cast<const uint16_t*>(p.out) + r * p.s.D;
+        for (int c = chunk * 8; c < p.s.D; c += 64) {
+            float x[8], y[8];
+            unpack16<DT>(__ldg(reinterpret_cast<const uint4*>(g + c)), x);
+            unpack16<DT>(__ldg(reinterpret_cast<const uint4*>(o + c)), y);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) t = fmaf(x[e], y[e], t);
+        }
+    }
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    if (chunk == 0 && token < p.N) p.delta[(int64_t)head * p.N + token] = t;
+}
+
+template <int DT, int DP>
+cudaError_t launch(const AttnBackward& p, int64_t max_items, cudaStream_t s) {
+    using L = Shape<DP>;
+    attn_delta_kernel<DT><<<(unsigned)((p.N * p.s.H + 31) / 32), 256, 0, s>>>(p);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    attn_dq_mma_kernel<DT, DP><<<(unsigned)(max_items * p.s.H), L::kThreads, L::dq_bytes, s>>>(p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    attn_dkv_mma_kernel<DT, DP><<<(unsigned)(max_items * p.s.Hk), L::kThreads, L::dkv_bytes, s>>>(p);
+    return cudaGetLastError();
+}
+
+template <int DT, int DP>
+cudaError_t configure() {
+    const cudaError_t e = cudaFuncSetAttribute(attn_dq_mma_kernel<DT, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               Shape<DP>::dq_bytes);
+    if (e != cudaSuccess) return e;
+    return cudaFuncSetAttribute(attn_dkv_mma_kernel<DT, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                Shape<DP>::dkv_bytes);
+}
+
+}  // namespace
+
+cudaError_t attn_backward_mma_configure() {
+    cudaError_t e = configure<DT_F16, 64>();
+    if (e == cudaSuccess) e = configure<DT_F16, 128>();
+    if (e == cudaSuccess) e = configure<DT_BF16, 64>();
+    if (e == cudaSuccess) e = configure<DT_BF16, 128>();
+    return e;
+}
+
+cudaError_t launch_attn_backward_mma(const AttnBackward& p, int64_t max_items, cudaStream_t s) {
+    if (p.s.dtype == DT_F16) return p.s.D <= 64 ? launch<DT_F16, 64>(p, max_items, s) : launch<DT_F16, 128>(p, max_items, s);
+    return p.s.D <= 64 ? launch<DT_BF16, 64>(p, max_items, s) : launch<DT_BF16, 128>(p, max_items, s);
+}
+
+}  // namespace tbe

@@ -1,0 +1,343 @@
+// Attention over ragged histories on the tensor cores (tcgen05), forward.
+//
+// One CTA takes 128 queries of one history and head and walks the visible
+// keys in blocks of 64:
+//   S = Q K^T           (128 x 64, both operands in shared memory, fp32 in TMEM)
+//   P = 2^(S c + b - m) (one query per thread, rounded to the 16-bit type, TMEM)
+//   O += P V            (P from TMEM, V as stored: its MN-major descriptor)
+// Roles: warps 0-3 softmax (lane = query), warp 4 issues the products, warps
+// 5 and 6 load K and V tiles (cp.async: any stride, zeros past the history's
+// end), warp 7 spreads the bias over the block's distances.  S has two
+// buffers, so the next block's scores are computed while this one's softmax
+// runs; P takes its S's place.  Two CTAs share an SM (256 TMEM columns each)
+// and fill each other's gaps.
+//
+// The running maximum m is only moved when a score exceeds it by 2^8
+// (kLazy): the weights then stay below 256, exact in fp32 sums and within
+// fp16's range, and the accumulator is rescaled rarely.
+//
+// The weights are rounded to the 16-bit type for the second product (the
+// tensor cores' operand type); their sum is kept unrounded in fp32.
+#include "attention_mma.cuh"
+
+namespace tbe {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr float kLazy = 8.f;
+
+template <int DP>
+struct Fwd {
+    static constexpr int kStages = DP == 64 ? 4 : 2;
+    static constexpr int kTile = 64 * DP * 2;  // bytes of a K or V tile
+    static constexpr int kQ = 128 * DP * 2;
+    static constexpr int q = 0, k = kQ, v = k + kStages * kTile, bias = v + kStages * kTile;
+    static constexpr int bytes = bias + 2 * 192 * 4 + 1024;  // 1024: the swizzle's alignment
+    static constexpr int cols = 256;
+};
+
+struct FwdBars {
+    uint64_t q_full, k_full[4], k_empty[4], v_full[4], v_empty[4], s_full[2], p_full[2], o_done, o_last, b_full[2], b_empty[2];
+};
+
+template <int DT, int DP>
+__global__ void __launch_bounds__(kThreads, 2) attn_fwd_mma_kernel(const AttnForward p) {
+    using L = Fwd<DP>;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    __shared__ FwdBars bars;
+    __shared__ uint32_t tmem_slot;
+    __shared__ float uniform_bias[2];
+    __shared__ int is_uniform[2];
+
+    const int64_t w = blockIdx.x / p.s.H;
+    const int head = (int)(blockIdx.x % p.s.H);
+    if (w >= *p.n_items) return;
+    const AttnItem it = p.items[w];
+    const int kvh = head / p.s.G, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int first = it.tile * 128, D = p.s.D;
+    const int ksteps = (D + 15) / 16;
+    // visible key blocks: [0, sink_blocks) and [lo, hi)
+    const int hi = tmin(first + 127, it.len - 1) / 64 + 1;
+    const int64_t from = (int64_t)first - p.s.window + 1;
+    const int lo = from > 0 ? (int)(from / 64) : 0;
+    const int sink_blocks = tmin((p.s.sinks + 63) / 64, lo);
+    const int steps = sink_blocks + hi - lo;
+    auto block_of = [&](int n) { return n < sink_blocks ? n : lo + n - sink_blocks; };
+
+    const uint32_t sbase = smem_u32(smem);
+    if (threadIdx.x == 0) {
+        mbar_init(&bars.q_full, 2);
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&bars.k_full[i], 1);
+            mbar_init(&bars.k_empty[i], 1);
+            mbar_init(&bars.v_full[i], 1);
+            mbar_init(&bars.v_empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars.s_full[i], 1);
+            mbar_init(&bars.p_full[i], 4);
+            mbar_init(&bars.b_full[i], 1);
+            mbar_init(&bars.b_empty[i], 4);
+        }
+        mbar_init(&bars.o_done, 1);
+        mbar_init(&bars.o_last, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        fence_proxy_async_smem();
+    }
+    if (warp == 4) tmem_alloc(&tmem_slot, L::cols);
+    tcgen05_before_sync();
+    __syncthreads();
+    tcgen05_after_sync();
+    const uint32_t tmem = tmem_slot;
+    const uint32_t t_o = tmem + 128;  // S0 and S1 at columns 0 and 64
+    bool ok = true;
+
+    if (warp == 5 || warp == 6) {
+        // ---- loaders: warp 5 K, warp 6 V, half of Q each
+        const bool is_k = warp == 5;
+        const Rows& src = is_k ? p.k : p.v;
+        uint64_t* full = is_k ? bars.k_full : bars.v_full;
+        uint64_t* empty = is_k ? bars.k_empty : bars.v_empty;
+        const uint32_t dst = sbase + (is_k ? L::k : L::v);
+        load_tile_async<128, DP, 64>(sbase + L::q, p.q, it.start, head, first, it.len, D, lane, is_k ? 0 : 64);
+        cp_async_commit();
+        // tile n is signalled once tile n + 1 is under way
+        for (int n = 0; n <= steps && ok; ++n) {
+            if (n < steps) {
+                const int st = n % L::kStages;
+                if (n >= L::kStages) ok = mbar_wait_tight(&empty[st], ((n / L::kStages) - 1) & 1);
+                if (!ok) break;
+                load_tile_async<64, DP>(dst + st * L::kTile, src, it.start, kvh, block_of(n) * 64, it.len, D, lane);
+            }
+            cp_async_commit();
+            if (n == 0) {
+                cp_async_wait<1>();
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars.q_full);
+            } else {
+                cp_async_wait<1>();
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&full[(n - 1) % L::kStages]);
+            }
+        }
+        cp_async_wait<0>();
+    } else if (warp == 7) {
+        // ---- bias by distance: entry x of the block's table is the bias at
+        // distance base + x - 63, x in [0, 191)
+        if (p.bias) {
+            float* bt = reinterpret_cast<float*>(smem + L::bias);
+            for (int n = 0; n < steps && ok; ++n) {
+                const int buf = n & 1;
+                if (n >= 2) ok = mbar_wait_tight(&bars.b_empty[buf], ((n / 2) - 1) & 1);
+                if (!ok) break;
+                const int base = first - block_of(n) * 64;
+                const int least = tmax(0, base - 63), most = base + 127;
+                const int b0 = attn_bucket(p.s, least), b1 = attn_bucket(p.s, tmax(most, 0));
+                if (lane == 0) {
+                    is_uniform[buf] = b0 == b1;
+                    uniform_bias[buf] = bias_base2(load_elem<DT>(p.bias, (int64_t)b0 * p.s.H + head));
+                }
+                if (b0 != b1)
+                    for (int x = lane; x < 191; x += 32) {
+                        const int d = base + x - 63;
+                        bt[buf * 192 + x] =
+                            d >= 0 ? bias_base2(load_elem<DT>(p.bias, (int64_t)attn_bucket(p.s, d) * p.s.H + head))
+                                   : 0.f;
+                    }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars.b_full[buf]);
+            }
+        }
+    } else if (warp == 4) {
+        // ---- products (one thread)
+        if (lane == 0) {
+            const int bf16 = DT == DT_BF16;
+            const uint32_t id_s = mma_idesc(bf16, 128, 64);
+            const uint32_t id_o = mma_idesc(bf16, 128, ksteps * 16) | kMnMajorB;
+            ok = mbar_wait_tight(&bars.q_full, 0);
+            auto scores = [&](int n) {
+                const int st = n % L::kStages;
+                if (!mbar_wait_tight(&bars.k_full[st], (n / L::kStages) & 1)) return false;
+                tcgen05_after_sync();
+                for (int k = 0; k < ksteps; ++k) {
+                    const uint32_t a = sbase + L::q + (k / 4) * (128 * 128) + (k % 4) * 32;
+                    const uint32_t b = sbase + L::k + st * L::kTile + (k / 4) * (64 * 128) + (k % 4) * 32;
+                    mma_f16(tmem + (n & 1) * 64, smem_desc_sw128(a, 1024), smem_desc_sw128(b, 1024), id_s, k > 0);
+                }
+                if (n + L::kStages < steps) mma_commit(&bars.k_empty[st]);
+                mma_commit(&bars.s_full[n & 1]);
+                return true;
+            };
+            if (ok) ok = scores(0);
+            if (ok && steps > 1) ok = scores(1);
+            for (int n = 0; n < steps && ok; ++n) {
+                const int st = n % L::kStages;
+                ok = mbar_wait_tight(&bars.v_full[st], (n / L::kStages) & 1) &&
+                     mbar_wait_tight(&bars.p_full[n & 1], (n / 2) & 1);
+                if (!ok) break;
+                tcgen05_after_sync();
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t b = sbase + L::v + st * L::kTile + k * 2048;
+                    mma_f16_ts(t_o, tmem + (n & 1) * 64 + k * 8, smem_desc_mn(b, 64 * 128), id_o, n > 0 || k > 0);
+                }
+                if (n + L::kStages < steps) mma_commit(&bars.v_empty[st]);
+                mma_commit(n + 1 < steps ? &bars.o_done : &bars.o_last);
+                if (n + 2 < steps) {
+                    // block n + 2's scores overwrite P(n): wait for its product
+                    ok = mbar_wait_tight(&bars.o_done, n & 1) && scores(n + 2);
+                }
+            }
+        }
+        __syncwarp();
+    } else {
+        // ---- softmax: thread = query
+        const int row = threadIdx.x, i = first + row;
+        const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+        const float c2 = p.s.scale * kLog2e;
+        const float* bt = reinterpret_cast<const float*>(smem + L::bias);
+        float m = -INFINITY, l0 = 0.f, l1 = 0.f;
+        for (int n = 0; n < steps; ++n) {
+            const int buf = n & 1;
+            const uint32_t t_s = tmem + buf * 64 + lanes;
+            ok = mbar_wait_tight(&bars.s_full[buf], (n / 2) & 1);
+            if (ok && p.bias) ok = mbar_wait_tight(&bars.b_full[buf], (n / 2) & 1);
+            // products up to n - 2 have completed (their P's place is S(n)'s,
+            // which is full); n - 1 is waited for where O is touched
+            if (!__all_sync(0xffffffffu, ok)) {
+                ok = false;
+                break;
+            }
+            tcgen05_after_sync();
+            float x[64];
+            tmem_ld32_issue(t_s, x);
+            tmem_ld32_issue(t_s + 32, x + 32);
+            tmem_wait_ld(x, 64);
+            const int key0 = block_of(n) * 64;
+            if (p.bias && !is_uniform[buf]) {
+                const float* b = bt + buf * 192 + row + 63;
+#pragma unroll
+                for (int c = 0; c < 64; c += 2) fma2(x[c], x[c + 1], c2, b[-c], b[-c - 1]);
+            } else {
+                const float b = p.bias ? uniform_bias[buf] : 0.f;
+#pragma unroll
+                for (int c = 0; c < 64; c += 2) fma2(x[c], x[c + 1], c2, b, b);
+            }
+            if (p.bias) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars.b_empty[buf]);
+            }
+            // a block needs masks unless all its pairs are visible
+            const bool all = key0 + 63 <= first && (first + 127 - key0 < p.s.window || key0 + 63 < p.s.sinks);
+            if (!all) {
+                const int up = i - key0 + 1, down = i - p.s.window + 1 - key0, sk = p.s.sinks - key0;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t seen = bits_below(up - 32 * h) & (~bits_below(down - 32 * h) | bits_below(sk - 32 * h));
+#pragma unroll
+                    for (int c = 0; c < 32; ++c)
+                        if (!(seen >> c & 1)) x[32 * h + c] = -INFINITY;
+                }
+            }
+            float t[8];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) t[c] = fmaxf(x[c], x[c + 8]);
+#pragma unroll
+            for (int c = 16; c < 64; c += 16)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) t[e] = fmaxf(t[e], fmaxf(x[c + e], x[c + 8 + e]));
+            const float top = fmaxf(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])), fmaxf(fmaxf(t[4], t[5]), fmaxf(t[6], t[7])));
+            if (__any_sync(0xffffffffu, top > m + kLazy || m == -INFINITY)) {
+                const float to = fmaxf(m, top);
+                const float keep = to == -INFINITY ? 1.f : ex2(m - to);
+                m = to;
+                l0 *= keep;
+                l1 *= keep;
+                if (n > 0) {
+                    ok = mbar_wait_tight(&bars.o_done, (n - 1) & 1);
+                    if (!__all_sync(0xffffffffu, ok)) {
+                        ok = false;
+                        break;
+                    }
+                    tcgen05_after_sync();
+                    for (int c = 0; c < DP; c += 32) {
+                        float o[32];
+                        tmem_ld32_issue(t_o + lanes + c, o);
+                        tmem_wait_ld(o, 32);
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) mul2(o[e], o[e + 1], keep, keep);
+                        tmem_st32(t_o + lanes + c, reinterpret_cast<const uint32_t*>(o));
+                    }
+                }
+            }
+            const float less = m == -INFINITY ? 0.f : -m;
+#pragma unroll
+            for (int c = 0; c < 64; c += 2) {
+                add2(x[c], x[c + 1], less, less);
+                x[c] = ex2(x[c]);
+                x[c + 1] = ex2(x[c + 1]);
+                add2(l0, l1, x[c], x[c + 1]);
+            }
+            uint32_t pk[32];
+#pragma unroll
+            for (int c = 0; c < 32; ++c) pk[c] = pack2<DT>(x[2 * c], x[2 * c + 1]);
+            tmem_st32(t_s, pk);
+            tmem_wait_st();
+            tcgen05_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.p_full[buf]);
+        }
+        // ---- out = O / l, through the warp's rows of Q's tile
+        // (a barrier of its own: o_done may be any of three phases along by now)
+        if (ok) ok = mbar_wait_tight(&bars.o_last, 0);
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok) {
+            tcgen05_after_sync();
+            const float l = l0 + l1;
+            const float inv = l == 0.f ? 0.f : 1.f / l;  // a row that sees nothing is zero
+            unsigned char* qt = smem + L::q;
+#pragma unroll
+            for (int c = 0; c < DP; c += 32) tmem_to_tile<DT>(qt, t_o + lanes, c, row, inv);
+            if (i < it.len) p.lse[(int64_t)head * p.N + it.start + i] = m + log2f(l);
+            __syncwarp();
+            store_tile_rows<DP>(p.out, qt, warp * 32, it.start, first, it.len, p.s.H, head, D, lane);
+        }
+    }
+    if (!ok) atomicOr(p.s.error, ERR_TIMEOUT);
+    tcgen05_before_sync();
+    __syncthreads();
+    tcgen05_after_sync();
+    if (warp == 4) tmem_dealloc(tmem, L::cols);
+}
+
+template <int DT, int DP>
+cudaError_t launch(const AttnForward& p, int64_t max_items, cudaStream_t s) {
+    attn_fwd_mma_kernel<DT, DP><<<(unsigned)(max_items * p.s.H), kThreads, Fwd<DP>::bytes, s>>>(p);
+    return cudaGetLastError();
+}
+
+template <int DT, int DP>
+cudaError_t configure() {
+    return cudaFuncSetAttribute(attn_fwd_mma_kernel<DT, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                Fwd<DP>::bytes);
+}
+
+}  // namespace
+
+cudaError_t attn_forward_mma_configure() {
+    cudaError_t e = configure<DT_F16, 64>();
+    if (e == cudaSuccess) e = configure<DT_F16, 128>();
+    if (e == cudaSuccess) e = configure<DT_BF16, 64>();
+    if (e == cudaSuccess) e = configure<DT_BF16, 128>();
+    return e;
+}
+
+cudaError_t launch_attn_forward_mma(const AttnForward& p, int64_t max_items, cudaStream_t s) {
+    if (p.s.dtype == DT_F16) return p.s.D <= 64 ? launch<DT_F16, 64>(p, max_items, s) : launch<DT_F16, 128>(p, max_items, s);
+    return p.s.D <= 64 ? launch<DT_BF16, 64>(p, max_items, s) : launch<DT_BF16, 128>(p, max_items, s);
+}
+
+}  // namespace tbe

@@ -481,3 +481,32 @@ def test_long_cache_beyond_32_bit_offsets():
     c.table = torch.arange(pages - c.table.shape[1], pages, dtype=torch.int32, device="cuda")[None].contiguous()
     c.append(0, 900)
     c.check()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (200, 6)])
+def test_many_tiles_on_every_sm(dim, window, sinks):
+    """Thousands of tiles of several key blocks each, launched again and
+    again: no wait may run out.  Against the fp32 path on the same values:
+    the result's and the weights' rounding, the latter by the sum of
+    magnitudes (the fp32 path on |v|)."""
+    g = np.random.default_rng(dim + window)
+    lengths = g.integers(1, 900, 120).tolist()
+    b = Batch(torch.bfloat16, 8, 4, dim, lengths, window, sinks, [0, 1, 2, 9, 100], seed=30)
+    first = b.run()
+    for _ in range(10):
+        again = b.run()
+    assert tbe.tbe_attention_get_error(b.handle) == tbe.TBE_OK
+    for x in first:
+        assert torch.equal(first[x], again[x]), x
+    h = tbe.tbe_attention_create(8, 4, dim, torch.float32, window, sinks, b.starts)
+    q, k, v, bias = (t.float() for t in (b.q, b.k, b.v, b.bias))
+    want, lse = tbe.tbe_attention_forward(h, q, k, v, b.offsets, bias)
+    size, _ = tbe.tbe_attention_forward(h, q, k, v.abs(), b.offsets, bias)
+    u = 2.0 ** -8
+    assert ((first["out"].float() - want).abs() <= u * want.abs() + (u + 2.0 ** -14) * size).all()
+    # gradients: by their size over the batch (the element-wise bounds are
+    # checked on small batches): roundings of relative size u add up at random
+    grads = tbe.tbe_attention_backward(h, q, k, v, b.offsets, want, lse, b.grad.float(), bias)
+    for x, y in zip(("grad_q", "grad_k", "grad_v", "grad_bias"), grads):
+        assert (first[x].float() - y).norm() <= 1.5 * u * y.norm(), x
