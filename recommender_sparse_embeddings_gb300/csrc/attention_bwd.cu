@@ -2,15 +2,23 @@
 //
 // Two kernels, each summing its gradients inside one CTA in a fixed order
 // (no atomics, no fp32 copies of the gradients in memory), at the price of
-// recomputing the logits twice (seven products instead of five):
+// computing the logits and their gradients twice (eight products, not five):
 //
 // dq (128 queries of one head; key blocks of 64):
-//   S = Q K^T, dP = G V^T, dS = P (dP - delta), dQ += dS K
-//   and the bias gradient: dS summed by bucket of the distance.
+//   S = Q K^T, dP = G V^T, dS = P (dP - delta), dQ += dS K, R += P K
 // dkv (128 keys of one key-value head; query blocks of 64, over the group's
 // heads), transposed so that P^T and dS^T are products' first operands and
 // stay in tensor memory:
 //   S^T = K Q^T, dP^T = V G^T, dV += P^T G, dK += dS^T Q
+//   and the bias gradient: dS summed by bucket of the distance.
+//
+// delta.  g . out with the rounded out (and the weights rounded on its way)
+// misses delta_i = sum_j p_ij dp_ij by about 2^-8 |g||out|, which is more than
+// the other roundings where few keys carry a row (measured on histories of a
+// few tokens: grad_q off by 0.0047 of its norm, 0.0017 being the result's own
+// rounding).  With that estimate e, sum_j p (dp - e) = delta - e: dq sums its
+// rows of dS in fp32, takes R times that sum off dQ (R needs little
+// precision: the sum is small), and leaves the exact delta to dkv.
 //
 // A thread owns one row of S (a query in dq, a key in dkv).  head_dim <= 64:
 // one warpgroup and one set of score buffers, two CTAs per SM that fill each
@@ -37,11 +45,12 @@ struct Shape {
     static constexpr int a = 0, b = kBig, x = 2 * kBig, y = x + kStages * kSmall;
     static constexpr int table = y + kStages * kSmall;      // bias by distance, 2 x 192 floats
     static constexpr int stat = table + 2 * 192 * 4;        // dkv: -lse and delta, 2 x 2 x 64 floats
-    static constexpr int sums = stat + 2 * 2 * 64 * 4;      // dq: per warp, a sum per bucket
-    static constexpr int diag = sums + NB * 4 * kMaxBuckets * 4;  // dq: per warp, 96 diagonals
-    static constexpr int dq_bytes = diag + NB * 4 * 96 * 4 + 1024;
-    static constexpr int dkv_bytes = sums + 1024;
-    // TMEM columns: scores, score gradients, 16-bit dS (dq only), accumulators
+    static constexpr int sums = stat + 2 * 2 * 64 * 4;      // dkv: per warp, a sum per bucket
+    static constexpr int diag = sums + NB * 4 * kMaxBuckets * 4;  // dkv: per warp, 96 diagonals
+    static constexpr int rows = stat;                             // dq: a row sum per thread
+    static constexpr int dq_bytes = sums + 1024;
+    static constexpr int dkv_bytes = diag + NB * 4 * 96 * 4 + 1024;
+    // TMEM columns: S (then P) and dP (then dS) per buffer, two accumulators
     static constexpr int cols = DP == 64 ? 256 : 512;
 };
 
@@ -132,7 +141,7 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
     __shared__ Bars bars;
     __shared__ uint32_t tmem_slot;
     __shared__ float same_bias[2];
-    __shared__ int same_bucket[2];  // -1: the block's distances have several
+    __shared__ int several[2];  // the block's distances have several buckets
 
     const int64_t w = blockIdx.x / p.s.H;
     const int head = (int)(blockIdx.x % p.s.H);
@@ -150,14 +159,11 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
     const uint32_t sbase = smem_u32(smem);
     if (threadIdx.x == 0) init_bars<NB>(bars);
     if (warp == kHelp) tmem_alloc(&tmem_slot, L::cols);
-    float* sums = reinterpret_cast<float*>(smem + L::sums);
-    for (int i = threadIdx.x; i < NB * 4 * p.s.buckets; i += L::kThreads)
-        sums[i / p.s.buckets * kMaxBuckets + i % p.s.buckets] = 0.f;
     tcgen05_before_sync();
     __syncthreads();
     tcgen05_after_sync();
     const uint32_t tmem = tmem_slot;
-    const uint32_t t_ds = tmem + NB * 128, t_acc = t_ds + NB * 32;  // S at buf*128, dP at buf*128 + 64
+    const uint32_t t_dq = tmem + NB * 128, t_r = t_dq + DP;  // S at buf*128, dP at buf*128 + 64
     bool ok = true;
 
     if (warp == kHelp) {
@@ -165,41 +171,44 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
             const uint32_t id_s = mma_idesc(DT == DT_BF16, 128, 64);
             const uint32_t id_o = mma_idesc(DT == DT_BF16, 128, ksteps * 16) | kMnMajorB;
             ok = mbar_wait_tight(&bars.big_full, 0);
-            auto scores = [&](int n) {
+            // S (which = 0: Q K^T) or dP (which = 1: G V^T) of block n
+            auto score = [&](int n, int which) {
                 const int st = n % L::kStages;
-                const uint32_t t = tmem + (n % NB) * 128;
-                if (!mbar_wait_tight(&bars.x_full[st], (n / L::kStages) & 1)) return false;
+                const uint32_t big = sbase + (which ? L::b : L::a);
+                const uint32_t small = sbase + (which ? L::y : L::x) + st * L::kSmall;
+                if (!mbar_wait_tight(which ? &bars.y_full[st] : &bars.x_full[st], (n / L::kStages) & 1)) return false;
                 tcgen05_after_sync();
                 for (int k = 0; k < ksteps; ++k) {
                     const uint32_t oa = (k / 4) * (128 * 128) + (k % 4) * 32, ob = (k / 4) * (64 * 128) + (k % 4) * 32;
-                    mma_f16(t, smem_desc_sw128(sbase + L::a + oa, 1024),
-                            smem_desc_sw128(sbase + L::x + st * L::kSmall + ob, 1024), id_s, k > 0);
+                    mma_f16(tmem + (n % NB) * 128 + which * 64, smem_desc_sw128(big + oa, 1024),
+                            smem_desc_sw128(small + ob, 1024), id_s, k > 0);
                 }
-                if (!mbar_wait_tight(&bars.y_full[st], (n / L::kStages) & 1)) return false;
-                tcgen05_after_sync();
-                for (int k = 0; k < ksteps; ++k) {
-                    const uint32_t oa = (k / 4) * (128 * 128) + (k % 4) * 32, ob = (k / 4) * (64 * 128) + (k % 4) * 32;
-                    mma_f16(t + 64, smem_desc_sw128(sbase + L::b + oa, 1024),
-                            smem_desc_sw128(sbase + L::y + st * L::kSmall + ob, 1024), id_s, k > 0);
-                }
-                if (n + L::kStages < steps) mma_commit(&bars.y_empty[st]);
-                mma_commit(&bars.s_full[n % NB]);
+                if (which && n + L::kStages < steps) mma_commit(&bars.y_empty[st]);
+                if (which) mma_commit(&bars.s_full[n % NB]);
                 return true;
             };
-            for (int n = 0; n < NB && n < steps && ok; ++n) ok = scores(n);
+            for (int n = 0; n < NB && n < steps && ok; ++n) ok = score(n, 0) && score(n, 1);
             for (int n = 0; n < steps && ok; ++n) {
                 const int st = n % L::kStages;
+                const uint32_t t = tmem + (n % NB) * 128;
                 ok = mbar_wait_tight(&bars.ds_full[n % NB], (n / NB) & 1);
                 if (!ok) break;
                 tcgen05_after_sync();
                 for (int k = 0; k < 4; ++k)
-                    mma_f16_ts(t_acc, t_ds + (n % NB) * 32 + k * 8,
-                               smem_desc_mn(sbase + L::x + st * L::kSmall + k * 2048, 64 * 128), id_o, n > 0 || k > 0);
+                    mma_f16_ts(t_r, t + k * 8, smem_desc_mn(sbase + L::x + st * L::kSmall + k * 2048, 64 * 128), id_o,
+                               n > 0 || k > 0);
+                if (n + NB < steps) mma_commit(&bars.v_done);
+                for (int k = 0; k < 4; ++k)
+                    mma_f16_ts(t_dq, t + 64 + k * 8, smem_desc_mn(sbase + L::x + st * L::kSmall + k * 2048, 64 * 128),
+                               id_o, n > 0 || k > 0);
                 if (n + L::kStages < steps) mma_commit(&bars.x_empty[st]);
+                if (n + NB < steps) mma_commit(&bars.k_done);
                 if (n + 1 == steps) mma_commit(&bars.last);
-                // dS(n) is out, so S(n) and dP(n) are read; their commit also
-                // covers dQ's product, so dS(n + NB) may overwrite dS(n)
-                if (n + NB < steps) ok = scores(n + NB);
+                // block n + NB's scores overwrite P and dS: each waits for its
+                // product, the first under the second's cover
+                if (n + NB < steps)
+                    ok = mbar_wait_tight(&bars.v_done, n & 1) && score(n + NB, 0) &&
+                         mbar_wait_tight(&bars.k_done, n & 1) && score(n + NB, 1);
             }
         }
         __syncwarp();
@@ -225,7 +234,7 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
                                                  same, bucket);
                 if (lane == 0) {
                     same_bias[buf] = same;
-                    same_bucket[buf] = one ? bucket : -1;
+                    several[buf] = !one;
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars.t_full[buf]);
@@ -236,8 +245,6 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
         const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
         const float c2 = p.s.scale * kLog2e;
         const float* bt = reinterpret_cast<const float*>(smem + L::table);
-        float* mine = sums + warp * kMaxBuckets;
-        float* diag = reinterpret_cast<float*>(smem + L::diag) + warp * 96;
         float less = -INFINITY, delta = 0.f;
         if (i < it.len) {
             const int64_t at = (int64_t)head * p.N + it.start + i;
@@ -245,6 +252,7 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
             less = x == -INFINITY ? -INFINITY : -x;  // a row that sees nothing: all its weights 2^-inf
             delta = p.delta[at];
         }
+        float sum0 = 0.f, sum1 = 0.f;  // of the row's dS
         for (int n = wg; n < steps; n += NB) {
             const int buf = n & 1, sb = n % NB;
             const uint32_t t_s = tmem + sb * 128 + lanes;
@@ -255,11 +263,12 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
                 break;
             }
             tcgen05_after_sync();
-            const int key0 = block_of(n) * 64, base = first - key0;
-            const int bucket = p.bias ? same_bucket[buf] : 0;
-            const float add = less + (p.bias && bucket >= 0 ? same_bias[buf] : 0.f);
+            const int key0 = block_of(n) * 64;
+            const bool table = p.bias && several[buf];
+            const float add = less + (p.bias ? same_bias[buf] : 0.f);
+            // whether the block holds a query whose only key is its own (attn_lone)
+            const bool lone = (first == 0 && key0 == 0) || (p.s.window == 1 && p.s.sinks == 0);
             const bool all = key0 + 63 < first && (first + 127 - key0 < p.s.window || key0 + 63 < p.s.sinks);
-            float sum0 = 0.f, sum1 = 0.f, run = 0.f;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 float x[32], y[32];
@@ -267,7 +276,7 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
                 tmem_ld32_issue(t_s + 64 + 32 * h, y);
                 tmem_wait_ld(x, 32);
                 tmem_wait_ld(y, 32);
-                if (bucket < 0) {
+                if (table) {
                     const float* b = bt + buf * 192 + row + 63 - 32 * h;
 #pragma unroll
                     for (int c = 0; c < 32; c += 2) {
@@ -282,38 +291,36 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
                 if (!all) {
                     const int up = i - key0 + 1 - 32 * h, down = i - p.s.window + 1 - key0 - 32 * h,
                               sk = p.s.sinks - key0 - 32 * h;
-                    uint32_t seen = bits_below(up) & (~bits_below(down) | bits_below(sk));
-                    // the only key a query sees: no gradient (attn_lone)
-                    if (attn_lone(i, i, p.s.window, p.s.sinks) && up >= 1 && up <= 32) seen &= ~(1u << (up - 1));
+                    const uint32_t seen = bits_below(up) & (~bits_below(down) | bits_below(sk));
 #pragma unroll
                     for (int c = 0; c < 32; ++c)
                         if (!(seen >> c & 1)) x[c] = -INFINITY;
                 }
+                uint32_t pk[16];
 #pragma unroll
                 for (int c = 0; c < 32; c += 2) {
                     x[c] = ex2(x[c]);
                     x[c + 1] = ex2(x[c + 1]);
                     add2(y[c], y[c + 1], -delta, -delta);
-                    mul2(x[c], x[c + 1], y[c], y[c + 1]);
+                    mul2(y[c], y[c + 1], x[c], x[c + 1]);
+                    pk[c / 2] = pack2<DT>(x[c], x[c + 1]);
                 }
-                uint32_t pk[16];
+                if (lone) {
+                    const int own = i - key0 - 32 * h;  // the column of the query's own token
 #pragma unroll
-                for (int c = 0; c < 16; ++c) pk[c] = pack2<DT>(x[2 * c], x[2 * c + 1]);
-                tmem_st16(t_ds + sb * 32 + lanes + 16 * h, pk);
-                if (p.bias) {
-                    if (bucket >= 0) {
-#pragma unroll
-                        for (int c = 0; c < 32; c += 2) add2(sum0, sum1, x[c], x[c + 1]);
-                    } else {
-                        // a diagonal's sum moves one lane up a column: complete at lane 31
-#pragma unroll
-                        for (int c = 0; c < 32; ++c) {
-                            const float t = __shfl_up_sync(0xffffffffu, run, 1);
-                            run = x[c] + (lane == 0 ? 0.f : t);
-                            if (lane == 31) diag[94 - 32 * h - c] = run;
-                        }
-                    }
+                    for (int c = 0; c < 32; ++c)
+                        if (c == own && attn_lone(i, i, p.s.window, p.s.sinks)) y[c] = 0.f;
                 }
+                uint32_t dk[16];
+#pragma unroll
+                for (int c = 0; c < 32; c += 2) {
+                    dk[c / 2] = pack2<DT>(y[c], y[c + 1]);
+                    add2(sum0, sum1, y[c], y[c + 1]);
+                }
+                // P into S's first columns, dS into dP's: the columns this
+                // thread has read already (h = 0 writes 16 of the 32 read)
+                tmem_st16(t_s + 16 * h, pk);
+                tmem_st16(t_s + 64 + 16 * h, dk);
             }
             tmem_wait_st();
             tcgen05_before_sync();
@@ -322,44 +329,25 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
                 mbar_arrive(&bars.ds_full[sb]);
                 if (p.bias) mbar_arrive(&bars.t_empty[buf]);
             }
-            if (p.bias && bucket >= 0) {
-                float t = sum0 + sum1;
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-                if (lane == 0) mine[bucket] += t;
-                __syncwarp();
-            } else if (p.bias) {
-                // diag[x], x in [0, 95): distance base + 32 q4 + x - 63; the
-                // last column's running sums are the lowest 32
-                if (lane < 31) diag[lane] = run;
-                __syncwarp();
-#pragma unroll
-                for (int r = 0; r < 3; ++r) {
-                    // sums of equal buckets, which are neighbours: a segmented
-                    // scan over 32 distances, added by each segment's last lane
-                    const int x = r * 32 + lane, d = base + 32 * q4 + x - 63;
-                    int b = x < 95 && d >= 0 ? attn_bucket(p.s, d) : -1;
-                    float t = b >= 0 ? diag[x] : 0.f;
-#pragma unroll
-                    for (int o = 1; o < 32; o <<= 1) {
-                        const float tu = __shfl_up_sync(0xffffffffu, t, o);
-                        const int bu = __shfl_up_sync(0xffffffffu, b, o);
-                        if (lane >= o && bu == b) t += tu;
-                    }
-                    const int next = __shfl_down_sync(0xffffffffu, b, 1);
-                    if (b >= 0 && (lane == 31 || next != b)) mine[b] += t;
-                    __syncwarp();
-                }
-            }
         }
         if (ok) ok = mbar_wait_tight(&bars.last, 0);
         ok = __all_sync(0xffffffffu, ok);
+        // delta - e of the row: both warpgroups' sums (every warp comes here)
+        float* rows = reinterpret_cast<float*>(smem + L::rows);
+        float over = sum0 + sum1;
+        if constexpr (NB == 2) {
+            rows[wg * 128 + row] = over;
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            over = rows[row] + rows[128 + row];
+        }
         if (ok) {
             tcgen05_after_sync();
-            // the warpgroups take the accumulator's 64-column slabs in turn
+            if (wg == 0 && i < it.len) p.delta[(int64_t)head * p.N + it.start + i] = delta + over;
+            // dq = scale (dQ - over R); the warpgroups take a 64-column slab each
             unsigned char* qt = smem + L::a;
 #pragma unroll
-            for (int c = wg * 64; c < wg * 64 + 64; c += 32) tmem_to_tile<DT>(qt, t_acc + lanes, c, row, p.s.scale);
+            for (int c = wg * 64; c < wg * 64 + 64; c += 32)
+                tmem_to_tile<DT>(qt, t_dq + lanes, c, row, p.s.scale, t_r + lanes, -over);
         }
     }
     if (!ok) atomicOr(p.s.error, ERR_TIMEOUT);
@@ -368,11 +356,6 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
     tcgen05_after_sync();
     if (warp < 4) store_tile_rows<DP>(p.gq, smem + L::a, warp * 32, it.start, first, it.len, p.s.H, head, D, lane);
     if (warp == kHelp) tmem_dealloc(tmem, L::cols);
-    for (int b = threadIdx.x; b < p.s.buckets; b += L::kThreads) {
-        float t = 0.f;
-        for (int k = 0; k < NB * 4; ++k) t += sums[k * kMaxBuckets + b];
-        p.bias_part[(w * p.s.H + head) * p.s.buckets + b] = t;
-    }
 }
 
 // ------------------------------------------------------------------ dkv
@@ -385,7 +368,7 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
     unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     __shared__ Bars bars;
     __shared__ uint32_t tmem_slot;
-    __shared__ int several[2];  // the block's distances have several buckets
+    __shared__ int same_bucket[2];  // -1: the block's distances have several
 
     const int64_t w = blockIdx.x / p.s.Hk;
     const int kvh = (int)(blockIdx.x % p.s.Hk);
@@ -402,6 +385,9 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
     const uint32_t sbase = smem_u32(smem);
     if (threadIdx.x == 0) init_bars<NB>(bars);
     if (warp == kHelp) tmem_alloc(&tmem_slot, L::cols);
+    float* sums = reinterpret_cast<float*>(smem + L::sums);
+    for (int i = threadIdx.x; i < NB * 4 * p.s.buckets; i += L::kThreads)
+        sums[i / p.s.buckets * kMaxBuckets + i % p.s.buckets] = 0.f;
     tcgen05_before_sync();
     __syncthreads();
     tcgen05_after_sync();
@@ -476,8 +462,8 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
             const int2 at = place(n);
             float same = 0.f;
             bool one = true;
+            int bucket = 0;
             if (p.bias) {
-                int bucket;
                 one = spread_bias<DT>(bt + buf * 192, p.s, p.bias, at.y, at.x - first - 127, lane, same, bucket);
             }
 #pragma unroll
@@ -493,7 +479,7 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
                 stat[buf * 128 + c] = less;
                 stat[buf * 128 + 64 + c] = -delta;
             }
-            if (lane == 0) several[buf] = !one;
+            if (lane == 0) same_bucket[buf] = one ? bucket : -1;
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars.t_full[buf]);
         }
@@ -501,7 +487,10 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
         const int wg = warp / 4, q4 = warp % 4, row = q4 * 32 + lane, j = first + row;
         const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
         const float c2 = p.s.scale * kLog2e;
-        for (int n = wg; n < steps; n += NB) {
+        float* mine = sums + warp * kMaxBuckets;
+        float* diag = reinterpret_cast<float*>(smem + L::diag) + warp * 96;
+        for (int g = 0; g < p.s.G; ++g) {
+        for (int n = g * blocks + (NB == 2 ? (g * blocks + wg) % 2 : 0); n < (g + 1) * blocks && ok; n += NB) {
             const int buf = n & 1, sb = n % NB;
             const uint32_t t_s = tmem + sb * 128 + lanes;
             ok = mbar_wait_tight(&bars.s_full[sb], (n / NB) & 1);
@@ -513,7 +502,9 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
             tcgen05_after_sync();
             const int q0 = place(n).x;
             const float* less = reinterpret_cast<const float*>(smem + L::stat) + buf * 128;
-            const bool table = several[buf];
+            const int bucket = same_bucket[buf];
+            const bool table = bucket < 0;
+            float sum0 = 0.f, sum1 = 0.f, run = 0.f;
             const bool all = q0 > first + 127 && (q0 + 63 - first < p.s.window || first + 127 < p.s.sinks);
             // whether the block holds a query whose only key is its own (attn_lone)
             const bool lone = !all && (q0 == 0 || (p.s.window == 1 && p.s.sinks == 0));
@@ -577,6 +568,20 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
                 // this thread has read already (h = 0 writes 16 of the 32 read)
                 tmem_st16(t_s + 16 * h, pk);
                 tmem_st16(t_s + 64 + 16 * h, dk);
+                if (table) {
+                    // the lane's column c has distance c - lane (plus the
+                    // block's): a diagonal's sum moves one lane up a column
+                    // and is complete at lane 31
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) {
+                        const float t = __shfl_up_sync(0xffffffffu, run, 1);
+                        run = y[c] + (lane == 0 ? 0.f : t);
+                        if (lane == 31) diag[32 * h + c] = run;
+                    }
+                } else if (p.bias) {
+#pragma unroll
+                    for (int c = 0; c < 32; c += 2) add2(sum0, sum1, y[c], y[c + 1]);
+                }
             }
             tmem_wait_st();
             tcgen05_before_sync();
@@ -585,6 +590,48 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
                 mbar_arrive(&bars.ds_full[sb]);
                 mbar_arrive(&bars.t_empty[buf]);
             }
+            if (table) {
+                // diag[x], x in [0, 95): distance q0 - first - 32 q4 + x - 31;
+                // the last column's running sums are the highest 32
+                if (lane < 31) diag[94 - lane] = run;
+                __syncwarp();
+#pragma unroll
+                for (int r = 0; r < 3; ++r) {
+                    // sums of equal buckets, which are neighbours: a segmented
+                    // scan over 32 distances, added by each segment's last lane
+                    const int at = r * 32 + lane, d = q0 - first - 32 * q4 + at - 31;
+                    const int b = at < 95 && d >= 0 ? attn_bucket(p.s, d) : -1;
+                    float t = b >= 0 ? diag[at] : 0.f;
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const float tu = __shfl_up_sync(0xffffffffu, t, o);
+                        const int bu = __shfl_up_sync(0xffffffffu, b, o);
+                        if (lane >= o && bu == b) t += tu;
+                    }
+                    const int next = __shfl_down_sync(0xffffffffu, b, 1);
+                    if (b >= 0 && (lane == 31 || next != b)) mine[b] += t;
+                    __syncwarp();
+                }
+            } else if (p.bias) {
+                float t = sum0 + sum1;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+                if (lane == 0) mine[bucket] += t;
+                __syncwarp();
+            }
+        }
+        if (p.bias) {  // the head's share: all warps come here, whatever their waits said
+            asm volatile("bar.sync 1, %0;" ::"n"(NB * 128) : "memory");
+            for (int b = threadIdx.x; b < p.s.buckets; b += NB * 128) {
+                float t = 0.f;
+                for (int k = 0; k < NB * 4; ++k) {
+                    t += sums[k * kMaxBuckets + b];
+                    sums[k * kMaxBuckets + b] = 0.f;
+                }
+                p.bias_part[(w * p.s.H + kvh * p.s.G + g) * p.s.buckets + b] = t;
+            }
+            asm volatile("bar.sync 1, %0;" ::"n"(NB * 128) : "memory");
+        }
         }
         if (ok) ok = mbar_wait_tight(&bars.last, 0);
         ok = __all_sync(0xffffffffu, ok);

@@ -191,12 +191,21 @@ __device__ __forceinline__ void store_tile_rows(void* out, const unsigned char* 
 }
 
 // 32 columns (from c) of the thread's accumulator row, times `mul`, rounded
-// into row `row` of a 128-row tile in shared memory.
+// into row `row` of a 128-row tile in shared memory.  A second accumulator,
+// if there is one, is added first, times `times`.
 template <int DT>
-__device__ __forceinline__ void tmem_to_tile(unsigned char* tile, uint32_t taddr, int c, int row, float mul) {
+__device__ __forceinline__ void tmem_to_tile(unsigned char* tile, uint32_t taddr, int c, int row, float mul,
+                                             uint32_t second = 0xffffffffu, float times = 0.f) {
     float o[32];
     tmem_ld32_issue(taddr + c, o);
     tmem_wait_ld(o, 32);
+    if (second != 0xffffffffu) {
+        float r[32];
+        tmem_ld32_issue(second + c, r);
+        tmem_wait_ld(r, 32);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = fmaf(times, r[e], o[e]);
+    }
 #pragma unroll
     for (int e = 0; e < 32; e += 8) {
         uint4 u;

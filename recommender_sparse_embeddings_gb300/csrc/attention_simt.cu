@@ -295,8 +295,23 @@ __global__ void __launch_bounds__(kThreads) attn_dq_simt_kernel(const AttnBackwa
     int sink_tiles, lo;
     key_tiles<T>(p.s, it.tile, sink_tiles, lo);
     const int steps = sink_tiles + it.tile + 1 - lo;
-    for (int st = 0; st < steps; ++st) {
-        const int kt = st < sink_tiles ? st : lo + st - sink_tiles;
+    // 16-bit out: g . out misses delta by out's rounding, so a first sweep
+    // adds up sum_j p (dp - g . out) in fp32, which is what it misses
+    constexpr bool kTwice = DT != DT_F32;
+    float over[R] = {};
+    for (int st = kTwice ? -steps : 0; st < steps; ++st) {
+        if (st == 0 && kTwice) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+#pragma unroll
+                for (int o2 = 8; o2 > 0; o2 >>= 1) over[r] += __shfl_xor_sync(0xffffffffu, over[r], o2, 16);
+                delta[r] += over[r];
+                const int row = first + ty * R + r;
+                if (tx == 0 && row < it.len) p.delta[(int64_t)head * p.N + it.start + row] = delta[r];
+            }
+        }
+        const int tile = st < 0 ? st + steps : st;
+        const int kt = tile < sink_tiles ? tile : lo + tile - sink_tiles;
         const int base = (it.tile - kt) * T;
         __syncthreads();
         load_tile<DT, T, DP>(ks, p.k, it.start, kvh, kt * T, it.len, p.s.D, p.vec);
@@ -320,9 +335,12 @@ __global__ void __launch_bounds__(kThreads) attn_dq_simt_kernel(const AttnBackwa
                 if (p.bias) x += bt[ty * R + r - jj + T - 1];
                 const bool seen = i < it.len && attn_visible(i - j, j, p.s.window, p.s.sinks) &&
                                   !attn_lone(i, j, p.s.window, p.s.sinks);
-                ps[(ty * R + r) * PLD + jj] = seen ? ex2(x - lse[r]) * (dp[r][c] - delta[r]) : 0.f;
+                const float ds = seen ? ex2(x - lse[r]) * (dp[r][c] - delta[r]) : 0.f;
+                if (st < 0) over[r] += ds;
+                ps[(ty * R + r) * PLD + jj] = ds;
             }
         }
+        if (st < 0) continue;
         __syncthreads();
         mul_tile<T, DP>(acc, ps, ks, tx, ty);
         if (p.bias) {
