@@ -366,7 +366,7 @@ typedef struct {
     int32_t head_dim; /* D */
     int32_t window;   /* newest tokens seen, the query's own included; 0: all */
     int32_t sinks;    /* first tokens that stay visible */
-    float scale;
+    float scale;                  /* > 0 */
     int32_t num_buckets;          /* 0: no bias */
     const int32_t* bucket_starts; /* host [num_buckets]: first distance of each
                                      bucket, rising, beginning with 0 */

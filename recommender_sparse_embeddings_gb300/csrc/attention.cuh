@@ -187,14 +187,16 @@ struct Elem<DT_BF16> {
     using type = __nv_bfloat16;
 };
 
+struct AttnMaps;
+
 // Launchers (each returns the launch's status).
 cudaError_t launch_attn_items(const void* offsets, int index64, int64_t N, int B, int tile, AttnItem* items,
                               int64_t capacity, int32_t* n_items, uint32_t* error, cudaStream_t s);
 cudaError_t launch_attn_forward_simt(const AttnForward& p, int64_t max_items, cudaStream_t s);
 cudaError_t launch_attn_backward_simt(const AttnBackward& p, int64_t max_items, cudaStream_t s);
-cudaError_t launch_attn_forward_mma(const AttnForward& p, int64_t max_items, cudaStream_t s);
+cudaError_t launch_attn_forward_mma(const AttnForward& p, const AttnMaps& maps, int64_t max_items, cudaStream_t s);
 cudaError_t attn_forward_mma_configure();
-cudaError_t launch_attn_backward_mma(const AttnBackward& p, int64_t max_items, cudaStream_t s);
+cudaError_t launch_attn_backward_mma(const AttnBackward& p, const AttnMaps& maps, int64_t max_items, cudaStream_t s);
 cudaError_t attn_backward_mma_configure();
 cudaError_t launch_attn_bias_reduce(const AttnBackward& p, void* grad_bias, cudaStream_t s);
 cudaError_t launch_attn_append(const AttnAppend& p, cudaStream_t s);

@@ -3,12 +3,13 @@
 // are in include/tbe.h.
 #include <algorithm>
 #include <new>
+#include <utility>
 #include <vector>
 
 #include <nvtx3/nvToolsExt.h>
 
 #include "../../include/tbe.h"
-#include "attention.cuh"
+#include "attention_mma.cuh"
 
 namespace tbe {
 int cuda_fail(cudaError_t e);
@@ -68,6 +69,41 @@ constexpr int kMmaTile = 128;
 bool takes_mma(const tbe_attention* h, bool vec) { return vec && h->s.dtype != TBE_F32 && h->s.D <= 128; }
 
 Rows as_rows(const tbe_rows& r) { return Rows{r.data, r.token_stride, r.head_stride}; }
+
+// The TMA map of a token operand, by the driver's encoder (found at run time;
+// it computes 128 bytes on the host).  Of the two strides the larger has to be
+// a multiple of the smaller, and neither 0: other layouts give false, and the
+// call then takes the kernels that load by plain loads.
+bool encode_rows(TileMap* map, const tbe_attention* h, const tbe_rows& r, int heads, int64_t N) {
+    using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static const Encode encode = [] {
+        void* fn = nullptr;
+        cudaDriverEntryPointQueryResult found{};
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            fn = nullptr;
+        return reinterpret_cast<Encode>(fn);
+    }();
+    if (!encode) return false;
+    const int64_t token = r.token_stride, head = heads == 1 ? token : r.head_stride;
+    map->heads_outer = head > token;
+    const int64_t inner = std::min(token, head), outer = std::max(token, head);
+    if (inner < h->s.D || outer % inner != 0 || outer >= (int64_t(1) << 38)) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)h->s.D, (cuuint64_t)heads, (cuuint64_t)N};
+    cuuint32_t box[3] = {64, 1, 64};
+    if (map->heads_outer) {
+        std::swap(dims[1], dims[2]);
+        std::swap(box[1], box[2]);
+    }
+    const cuuint64_t strides[2] = {(cuuint64_t)inner * 2, (cuuint64_t)outer * 2};
+    const cuuint32_t steps[3] = {1, 1, 1};
+    return encode(&map->map, h->s.dtype == TBE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                  const_cast<void*>(r.data), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 bool batch_within_limits(const tbe_attention* h, int64_t N, int64_t B) {
     if (N >= (int64_t(1) << 30) || B >= (int64_t(1) << 24)) return false;
@@ -146,7 +182,7 @@ int tbe_attention_create(const tbe_attention_config* c, tbe_attention** out) {
     if (!c) return TBE_ERR_INVALID_ARG;
     if (c->dtype != TBE_F32 && c->dtype != TBE_F16 && c->dtype != TBE_BF16) return TBE_ERR_INVALID_ARG;
     if (c->heads <= 0 || c->kv_heads <= 0 || c->heads % c->kv_heads != 0 || c->head_dim <= 0 || c->window < 0 ||
-        c->sinks < 0 || c->num_buckets < 0 || !(c->scale - c->scale == 0.f))
+        c->sinks < 0 || c->num_buckets < 0 || !(c->scale > 0.f && c->scale - c->scale == 0.f))
         return TBE_ERR_INVALID_ARG;
     if (c->num_buckets > 0) {
         if (!c->bucket_starts || c->bucket_starts[0] != 0) return TBE_ERR_INVALID_ARG;
@@ -248,13 +284,15 @@ int tbe_attention_forward(tbe_attention* h, const tbe_rows* q, const tbe_rows* k
     p.items = at<AttnItem>(workspace, L.items);
     p.n_items = at<int32_t>(workspace, L.n_items);
     p.vec = vec_rows(h, *q) && vec_rows(h, *k) && vec_rows(h, *v) && aligned16(out);
-    const bool mma = takes_mma(h, p.vec);
+    AttnMaps maps{};
+    const bool mma = N > 0 && takes_mma(h, p.vec) && encode_rows(&maps.q, h, *q, h->s.H, N) &&
+                     encode_rows(&maps.k, h, *k, h->s.Hk, N) && encode_rows(&maps.v, h, *v, h->s.Hk, N);
     const int tile = mma ? kMmaTile : attn_simt_tile(h->s.D);
     const int64_t most = N / tile + B;
     rc = status(launch_attn_items(offsets, index_dtype == TBE_I64, N, B, tile, at<AttnItem>(workspace, L.items), most,
                                   at<int32_t>(workspace, L.n_items), h->s.error, s));
     if (rc || N == 0) return rc;
-    return status(mma ? launch_attn_forward_mma(p, most, s) : launch_attn_forward_simt(p, most, s));
+    return status(mma ? launch_attn_forward_mma(p, maps, most, s) : launch_attn_forward_simt(p, most, s));
 }
 
 int tbe_attention_backward(tbe_attention* h, const tbe_rows* q, const tbe_rows* k, const tbe_rows* v, const void* bias,
@@ -290,13 +328,16 @@ int tbe_attention_backward(tbe_attention* h, const tbe_rows* q, const tbe_rows* 
     p.n_items = at<int32_t>(workspace, L.n_items);
     p.vec = vec_rows(h, *q) && vec_rows(h, *k) && vec_rows(h, *v) && vec_rows(h, *grad_out) && aligned16(out) &&
             aligned16(grad_q) && aligned16(grad_k) && aligned16(grad_v);
-    const bool mma = takes_mma(h, p.vec);
+    AttnMaps maps{};
+    const bool mma = N > 0 && takes_mma(h, p.vec) && encode_rows(&maps.q, h, *q, h->s.H, N) &&
+                     encode_rows(&maps.k, h, *k, h->s.Hk, N) && encode_rows(&maps.v, h, *v, h->s.Hk, N) &&
+                     encode_rows(&maps.g, h, *grad_out, h->s.H, N);
     const int tile = mma ? kMmaTile : attn_simt_tile(h->s.D);
     const int64_t most = N / tile + B;
     rc = status(launch_attn_items(offsets, index_dtype == TBE_I64, N, B, tile, at<AttnItem>(workspace, L.items), most,
                                   at<int32_t>(workspace, L.n_items), h->s.error, s));
     if (rc) return rc;
-    if (N > 0) rc = status(mma ? launch_attn_backward_mma(p, most, s) : launch_attn_backward_simt(p, most, s));
+    if (N > 0) rc = status(mma ? launch_attn_backward_mma(p, maps, most, s) : launch_attn_backward_simt(p, most, s));
     if (rc || !bias) return rc;
     return status(launch_attn_bias_reduce(p, grad_bias, s));
 }

@@ -55,7 +55,7 @@ struct Shape {
 };
 
 struct Bars {
-    uint64_t big_full, x_full[3], x_empty[3], y_full[3], y_empty[3], s_full[2], ds_full[2], t_full[2], t_empty[2],
+    uint64_t big_full, fix[2], x_full[3], x_empty[3], y_full[3], y_empty[3], s_full[2], ds_full[2], t_full[2], t_empty[2],
         v_done, k_done, last;
 };
 
@@ -73,6 +73,7 @@ __device__ __forceinline__ void init_bars(Bars& b) {
         mbar_init(&b.ds_full[i], 4);
         mbar_init(&b.t_full[i], 1);
         mbar_init(&b.t_empty[i], 4);
+        mbar_init(&b.fix[i], 1);
     }
     mbar_init(&b.v_done, 1);
     mbar_init(&b.k_done, 1);
@@ -81,36 +82,15 @@ __device__ __forceinline__ void init_bars(Bars& b) {
     fence_proxy_async_smem();
 }
 
-// A loader warp: its 128-row tile, then `steps` 64-row tiles through the
-// stages; tile n is signalled once tile n + 1 is under way.  place(n) gives
-// tile n's first row and head.
+// A loader warp: its 128-row tile, then the 64-row tiles of the ring.
 template <int DP, typename F>
-__device__ __forceinline__ bool run_loader(uint32_t big, const Rows& big_rows, int big_head, int big_first,
-                                           uint32_t ring, const Rows& rows, uint64_t* big_full, uint64_t* full,
-                                           uint64_t* empty, const AttnItem& it, int D, int steps, int lane, F place) {
-    using L = Shape<DP>;
-    load_tile_async<128, DP>(big, big_rows, it.start, big_head, big_first, it.len, D, lane);
-    cp_async_commit();
-    bool ok = true;
-    for (int n = 0; n <= steps; ++n) {
-        if (n < steps) {
-            const int st = n % L::kStages;
-            if (n >= L::kStages) ok = mbar_wait_tight(&empty[st], ((n / L::kStages) - 1) & 1);
-            if (!__all_sync(0xffffffffu, ok)) {
-                ok = false;
-                break;
-            }
-            const int2 at = place(n);
-            load_tile_async<64, DP>(ring + st * L::kSmall, rows, it.start, at.y, at.x, it.len, D, lane);
-        }
-        cp_async_commit();
-        cp_async_wait<1>();
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(n == 0 ? big_full : &full[(n - 1) % L::kStages]);
-    }
-    cp_async_wait<0>();
-    return ok;
+__device__ __forceinline__ bool run_loader(unsigned char* big, const TileMap& big_map, int big_head, int big_first,
+                                           unsigned char* ring, const TileMap& map, uint64_t* big_full,
+                                           uint64_t* full, uint64_t* empty, uint64_t* fix, const AttnItem& it,
+                                           int steps, int lane, F place) {
+    uint32_t phase = 0;
+    return load_tile<128, DP>(big, big_map, it, big_head, big_first, big_full, fix, phase, lane) &&
+           load_ring<DP, Shape<DP>::kStages>(ring, map, it, full, empty, fix, phase, steps, lane, place);
 }
 
 // The helper warp's table of one block: entry x is the bias (base 2) at
@@ -133,7 +113,8 @@ __device__ __forceinline__ bool spread_bias(float* bt, const AttnShape& s, const
 // ------------------------------------------------------------------- dq
 
 template <int DT, int DP>
-__global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_dq_mma_kernel(const AttnBackward p) {
+__global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_dq_mma_kernel(const AttnBackward p,
+                                                                                                   const __grid_constant__ AttnMaps maps) {
     using L = Shape<DP>;
     constexpr int NB = L::NB, kHelp = NB * 4;  // first helper warp: products; then loaders K, V; then bias
     extern __shared__ unsigned char smem_raw[];
@@ -213,11 +194,13 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
         }
         __syncwarp();
     } else if (warp == kHelp + 1) {
-        ok = run_loader<DP>(sbase + L::a, p.q, head, first, sbase + L::x, p.k, &bars.big_full, bars.x_full,
-                            bars.x_empty, it, D, steps, lane, [&](int n) { return make_int2(block_of(n) * 64, kvh); });
+        ok = run_loader<DP>(smem + L::a, maps.q, head, first, smem + L::x, maps.k, &bars.big_full, bars.x_full,
+                            bars.x_empty, &bars.fix[0], it, steps, lane,
+                            [&](int n) { return make_int2(block_of(n) * 64, kvh); });
     } else if (warp == kHelp + 2) {
-        ok = run_loader<DP>(sbase + L::b, p.g, head, first, sbase + L::y, p.v, &bars.big_full, bars.y_full,
-                            bars.y_empty, it, D, steps, lane, [&](int n) { return make_int2(block_of(n) * 64, kvh); });
+        ok = run_loader<DP>(smem + L::b, maps.g, head, first, smem + L::y, maps.v, &bars.big_full, bars.y_full,
+                            bars.y_empty, &bars.fix[1], it, steps, lane,
+                            [&](int n) { return make_int2(block_of(n) * 64, kvh); });
     } else if (warp == kHelp + 3) {
         if (p.bias) {
             float* bt = reinterpret_cast<float*>(smem + L::table);
@@ -361,7 +344,8 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
 // ------------------------------------------------------------------ dkv
 
 template <int DT, int DP>
-__global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_dkv_mma_kernel(const AttnBackward p) {
+__global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_dkv_mma_kernel(const AttnBackward p,
+                                                                                                    const __grid_constant__ AttnMaps maps) {
     using L = Shape<DP>;
     constexpr int NB = L::NB, kHelp = NB * 4;
     extern __shared__ unsigned char smem_raw[];
@@ -442,11 +426,11 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
         }
         __syncwarp();
     } else if (warp == kHelp + 1) {
-        ok = run_loader<DP>(sbase + L::a, p.k, kvh, first, sbase + L::x, p.q, &bars.big_full, bars.x_full, bars.x_empty,
-                            it, D, steps, lane, place);
+        ok = run_loader<DP>(smem + L::a, maps.k, kvh, first, smem + L::x, maps.q, &bars.big_full, bars.x_full,
+                            bars.x_empty, &bars.fix[0], it, steps, lane, place);
     } else if (warp == kHelp + 2) {
-        ok = run_loader<DP>(sbase + L::b, p.v, kvh, first, sbase + L::y, p.g, &bars.big_full, bars.y_full, bars.y_empty,
-                            it, D, steps, lane, place);
+        ok = run_loader<DP>(smem + L::b, maps.v, kvh, first, smem + L::y, maps.g, &bars.big_full, bars.y_full,
+                            bars.y_empty, &bars.fix[1], it, steps, lane, place);
     } else if (warp == kHelp + 3) {
         // per query of the block: -lse (plus the bias where the block has one
         // bucket) and delta; the bias table else
@@ -683,15 +667,15 @@ __global__ void __launch_bounds__(256) attn_delta_kernel(const AttnBackward p) {
 }
 
 template <int DT, int DP>
-cudaError_t launch(const AttnBackward& p, int64_t max_items, cudaStream_t s) {
+cudaError_t launch(const AttnBackward& p, const AttnMaps& maps, int64_t max_items, cudaStream_t s) {
     using L = Shape<DP>;
     attn_delta_kernel<DT><<<(unsigned)((p.N * p.s.H + 31) / 32), 256, 0, s>>>(p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    attn_dq_mma_kernel<DT, DP><<<(unsigned)(max_items * p.s.H), L::kThreads, L::dq_bytes, s>>>(p);
+    attn_dq_mma_kernel<DT, DP><<<(unsigned)(max_items * p.s.H), L::kThreads, L::dq_bytes, s>>>(p, maps);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    attn_dkv_mma_kernel<DT, DP><<<(unsigned)(max_items * p.s.Hk), L::kThreads, L::dkv_bytes, s>>>(p);
+    attn_dkv_mma_kernel<DT, DP><<<(unsigned)(max_items * p.s.Hk), L::kThreads, L::dkv_bytes, s>>>(p, maps);
     return cudaGetLastError();
 }
 
@@ -714,9 +698,9 @@ cudaError_t attn_backward_mma_configure() {
     return e;
 }
 
-cudaError_t launch_attn_backward_mma(const AttnBackward& p, int64_t max_items, cudaStream_t s) {
-    if (p.s.dtype == DT_F16) return p.s.D <= 64 ? launch<DT_F16, 64>(p, max_items, s) : launch<DT_F16, 128>(p, max_items, s);
-    return p.s.D <= 64 ? launch<DT_BF16, 64>(p, max_items, s) : launch<DT_BF16, 128>(p, max_items, s);
+cudaError_t launch_attn_backward_mma(const AttnBackward& p, const AttnMaps& maps, int64_t max_items, cudaStream_t s) {
+    if (p.s.dtype == DT_F16) return p.s.D <= 64 ? launch<DT_F16, 64>(p, maps, max_items, s) : launch<DT_F16, 128>(p, maps, max_items, s);
+    return p.s.D <= 64 ? launch<DT_BF16, 64>(p, maps, max_items, s) : launch<DT_BF16, 128>(p, maps, max_items, s);
 }
 
 }  // namespace tbe

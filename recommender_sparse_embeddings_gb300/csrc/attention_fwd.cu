@@ -5,9 +5,9 @@
 //   S = Q K^T           (128 x 64, both operands in shared memory, fp32 in TMEM)
 //   P = 2^(S c + b - m) (one query per thread, rounded to the 16-bit type, TMEM)
 //   O += P V            (P from TMEM, V as stored: its MN-major descriptor)
-// Roles: warps 0-3 softmax (lane = query), warp 4 issues the products, warps
-// 5 and 6 load K and V tiles (cp.async: any stride, zeros past the history's
-// end), warp 7 spreads the bias over the block's distances.  S has two
+// Roles: warps 0-3 softmax (thread = query), warp 4 issues the products,
+// warps 5 and 6 fetch the tiles (TMA), warp 7 spreads the bias over the
+// block's distances.  S has two
 // buffers, so the next block's scores are computed while this one's softmax
 // runs; P takes its S's place.  Two CTAs share an SM (256 TMEM columns each)
 // and fill each other's gaps.
@@ -38,11 +38,11 @@ struct Fwd {
 };
 
 struct FwdBars {
-    uint64_t q_full, k_full[4], k_empty[4], v_full[4], v_empty[4], s_full[2], p_full[2], o_done, o_last, b_full[2], b_empty[2];
+    uint64_t q_full, fix[2], k_full[4], k_empty[4], v_full[4], v_empty[4], s_full[2], p_full[2], o_done, o_last, b_full[2], b_empty[2];
 };
 
 template <int DT, int DP>
-__global__ void __launch_bounds__(kThreads, 2) attn_fwd_mma_kernel(const AttnForward p) {
+__global__ void __launch_bounds__(kThreads, 2) attn_fwd_mma_kernel(const AttnForward p, const __grid_constant__ AttnMaps maps) {
     using L = Fwd<DP>;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_fwd_mma_kernel(const AttnFor
 
     const uint32_t sbase = smem_u32(smem);
     if (threadIdx.x == 0) {
-        mbar_init(&bars.q_full, 2);
+        mbar_init(&bars.q_full, 1);
         for (int i = 0; i < 4; ++i) {
             mbar_init(&bars.k_full[i], 1);
             mbar_init(&bars.k_empty[i], 1);
@@ -82,6 +82,8 @@ __global__ void __launch_bounds__(kThreads, 2) attn_fwd_mma_kernel(const AttnFor
             mbar_init(&bars.b_empty[i], 4);
         }
         mbar_init(&bars.o_done, 1);
+        mbar_init(&bars.fix[0], 1);
+        mbar_init(&bars.fix[1], 1);
         mbar_init(&bars.o_last, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_proxy_async_smem();
@@ -93,38 +95,17 @@ __global__ void __launch_bounds__(kThreads, 2) attn_fwd_mma_kernel(const AttnFor
     const uint32_t tmem = tmem_slot;
     const uint32_t t_o = tmem + 128;  // S0 and S1 at columns 0 and 64
     bool ok = true;
-
     if (warp == 5 || warp == 6) {
-        // ---- loaders: warp 5 K, warp 6 V, half of Q each
-        const bool is_k = warp == 5;
-        const Rows& src = is_k ? p.k : p.v;
-        uint64_t* full = is_k ? bars.k_full : bars.v_full;
-        uint64_t* empty = is_k ? bars.k_empty : bars.v_empty;
-        const uint32_t dst = sbase + (is_k ? L::k : L::v);
-        load_tile_async<128, DP, 64>(sbase + L::q, p.q, it.start, head, first, it.len, D, lane, is_k ? 0 : 64);
-        cp_async_commit();
-        // tile n is signalled once tile n + 1 is under way
-        for (int n = 0; n <= steps && ok; ++n) {
-            if (n < steps) {
-                const int st = n % L::kStages;
-                if (n >= L::kStages) ok = mbar_wait_tight(&empty[st], ((n / L::kStages) - 1) & 1);
-                if (!ok) break;
-                load_tile_async<64, DP>(dst + st * L::kTile, src, it.start, kvh, block_of(n) * 64, it.len, D, lane);
-            }
-            cp_async_commit();
-            if (n == 0) {
-                cp_async_wait<1>();
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars.q_full);
-            } else {
-                cp_async_wait<1>();
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&full[(n - 1) % L::kStages]);
-            }
-        }
-        cp_async_wait<0>();
+        // ---- loaders: warp 5 Q and K, warp 6 V
+        uint32_t fix_phase = 0;
+        auto place = [&](int n) { return make_int2(block_of(n) * 64, kvh); };
+        if (warp == 5)
+            ok = load_tile<128, DP>(smem + L::q, maps.q, it, head, first, &bars.q_full, &bars.fix[0], fix_phase, lane) &&
+                 load_ring<DP, L::kStages>(smem + L::k, maps.k, it, bars.k_full, bars.k_empty, &bars.fix[0], fix_phase,
+                                           steps, lane, place);
+        else
+            ok = load_ring<DP, L::kStages>(smem + L::v, maps.v, it, bars.v_full, bars.v_empty, &bars.fix[1], fix_phase,
+                                           steps, lane, place);
     } else if (warp == 7) {
         // ---- bias by distance: entry x of the block's table is the bias at
         // distance base + x - 63, x in [0, 191)
@@ -137,11 +118,15 @@ __global__ void __launch_bounds__(kThreads, 2) attn_fwd_mma_kernel(const AttnFor
                 const int base = first - block_of(n) * 64;
                 const int least = tmax(0, base - 63), most = base + 127;
                 const int b0 = attn_bucket(p.s, least), b1 = attn_bucket(p.s, tmax(most, 0));
+                const float same = bias_base2(load_elem<DT>(p.bias, (int64_t)b0 * p.s.H + head));
+                // a bias that swallows the logits (a type's lowest value) does
+                // so in the table's addition only
+                const bool one = b0 == b1 && (same > -1e30f || same == -INFINITY);
                 if (lane == 0) {
-                    is_uniform[buf] = b0 == b1;
-                    uniform_bias[buf] = bias_base2(load_elem<DT>(p.bias, (int64_t)b0 * p.s.H + head));
+                    is_uniform[buf] = one;
+                    uniform_bias[buf] = same;
                 }
-                if (b0 != b1)
+                if (!one)
                     for (int x = lane; x < 191; x += 32) {
                         const int d = base + x - 63;
                         bt[buf * 192 + x] =
@@ -217,19 +202,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_fwd_mma_kernel(const AttnFor
             tmem_ld32_issue(t_s + 32, x + 32);
             tmem_wait_ld(x, 64);
             const int key0 = block_of(n) * 64;
-            if (p.bias && !is_uniform[buf]) {
-                const float* b = bt + buf * 192 + row + 63;
-#pragma unroll
-                for (int c = 0; c < 64; c += 2) fma2(x[c], x[c + 1], c2, b[-c], b[-c - 1]);
-            } else {
-                const float b = p.bias ? uniform_bias[buf] : 0.f;
-#pragma unroll
-                for (int c = 0; c < 64; c += 2) fma2(x[c], x[c + 1], c2, b, b);
-            }
-            if (p.bias) {
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars.b_empty[buf]);
-            }
+            const bool table = p.bias && !is_uniform[buf];
             // a block needs masks unless all its pairs are visible
             const bool all = key0 + 63 <= first && (first + 127 - key0 < p.s.window || key0 + 63 < p.s.sinks);
             if (!all) {
@@ -242,14 +215,31 @@ __global__ void __launch_bounds__(kThreads, 2) attn_fwd_mma_kernel(const AttnFor
                         if (!(seen >> c & 1)) x[32 * h + c] = -INFINITY;
                 }
             }
+            // logit = x * by + add: with a table it is formed here, else (one
+            // bias for the block, and c2 > 0) the maximum is taken of the raw
+            // products and one multiply-add before ex2 does it all
+            float by = c2, add = p.bias ? uniform_bias[buf] : 0.f;
+            if (table) {
+                const float* b = bt + buf * 192 + row + 63;
+#pragma unroll
+                for (int c = 0; c < 64; c += 2) fma2(x[c], x[c + 1], c2, b[-c], b[-c - 1]);
+                by = 1.f;
+                add = 0.f;
+            }
+            if (p.bias) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars.b_empty[buf]);
+            }
             float t[8];
 #pragma unroll
-            for (int c = 0; c < 8; ++c) t[c] = fmaxf(x[c], x[c + 8]);
+            for (int c = 0; c < 8; ++c) t[c] = max3(x[c], x[c + 8], x[c + 16]);
 #pragma unroll
-            for (int c = 16; c < 64; c += 16)
+            for (int c = 24; c < 56; c += 16)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) t[e] = fmaxf(t[e], fmaxf(x[c + e], x[c + 8 + e]));
-            const float top = fmaxf(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])), fmaxf(fmaxf(t[4], t[5]), fmaxf(t[6], t[7])));
+                for (int e = 0; e < 8; ++e) t[e] = max3(t[e], x[c + e], x[c + 8 + e]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) t[e] = fmaxf(t[e], x[56 + e]);
+            const float top = fmaf(fmaxf(max3(max3(t[0], t[1], t[2]), t[3], t[4]), max3(t[5], t[6], t[7])), by, add);
             if (__any_sync(0xffffffffu, top > m + kLazy || m == -INFINITY)) {
                 const float to = fmaxf(m, top);
                 const float keep = to == -INFINITY ? 1.f : ex2(m - to);
@@ -263,28 +253,29 @@ __global__ void __launch_bounds__(kThreads, 2) attn_fwd_mma_kernel(const AttnFor
                         break;
                     }
                     tcgen05_after_sync();
-                    for (int c = 0; c < DP; c += 32) {
-                        float o[32];
-                        tmem_ld32_issue(t_o + lanes + c, o);
-                        tmem_wait_ld(o, 32);
+                    for (int c = 0; c < DP; c += 16) {
+                        float o[16];
+                        tmem_ld16(t_o + lanes + c, o);
 #pragma unroll
-                        for (int e = 0; e < 32; e += 2) mul2(o[e], o[e + 1], keep, keep);
-                        tmem_st32(t_o + lanes + c, reinterpret_cast<const uint32_t*>(o));
+                        for (int e = 0; e < 16; e += 2) mul2(o[e], o[e + 1], keep, keep);
+                        tmem_st16(t_o + lanes + c, reinterpret_cast<const uint32_t*>(o));
                     }
                 }
             }
-            const float less = m == -INFINITY ? 0.f : -m;
+            const float less = m == -INFINITY ? 0.f : add - m;
 #pragma unroll
-            for (int c = 0; c < 64; c += 2) {
-                add2(x[c], x[c + 1], less, less);
-                x[c] = ex2(x[c]);
-                x[c + 1] = ex2(x[c + 1]);
-                add2(l0, l1, x[c], x[c + 1]);
+            for (int h = 0; h < 64; h += 32) {
+                uint32_t pk[16];
+#pragma unroll
+                for (int c = h; c < h + 32; c += 2) {
+                    fma2(x[c], x[c + 1], by, less, less);
+                    x[c] = ex2(x[c]);
+                    x[c + 1] = ex2(x[c + 1]);
+                    add2(l0, l1, x[c], x[c + 1]);
+                    pk[(c - h) / 2] = pack2<DT>(x[c], x[c + 1]);
+                }
+                tmem_st16(t_s + h / 2, pk);
             }
-            uint32_t pk[32];
-#pragma unroll
-            for (int c = 0; c < 32; ++c) pk[c] = pack2<DT>(x[2 * c], x[2 * c + 1]);
-            tmem_st32(t_s, pk);
             tmem_wait_st();
             tcgen05_before_sync();
             __syncwarp();
@@ -314,8 +305,8 @@ __global__ void __launch_bounds__(kThreads, 2) attn_fwd_mma_kernel(const AttnFor
 }
 
 template <int DT, int DP>
-cudaError_t launch(const AttnForward& p, int64_t max_items, cudaStream_t s) {
-    attn_fwd_mma_kernel<DT, DP><<<(unsigned)(max_items * p.s.H), kThreads, Fwd<DP>::bytes, s>>>(p);
+cudaError_t launch(const AttnForward& p, const AttnMaps& maps, int64_t max_items, cudaStream_t s) {
+    attn_fwd_mma_kernel<DT, DP><<<(unsigned)(max_items * p.s.H), kThreads, Fwd<DP>::bytes, s>>>(p, maps);
     return cudaGetLastError();
 }
 
@@ -335,9 +326,9 @@ cudaError_t attn_forward_mma_configure() {
     return e;
 }
 
-cudaError_t launch_attn_forward_mma(const AttnForward& p, int64_t max_items, cudaStream_t s) {
-    if (p.s.dtype == DT_F16) return p.s.D <= 64 ? launch<DT_F16, 64>(p, max_items, s) : launch<DT_F16, 128>(p, max_items, s);
-    return p.s.D <= 64 ? launch<DT_BF16, 64>(p, max_items, s) : launch<DT_BF16, 128>(p, max_items, s);
+cudaError_t launch_attn_forward_mma(const AttnForward& p, const AttnMaps& maps, int64_t max_items, cudaStream_t s) {
+    if (p.s.dtype == DT_F16) return p.s.D <= 64 ? launch<DT_F16, 64>(p, maps, max_items, s) : launch<DT_F16, 128>(p, maps, max_items, s);
+    return p.s.D <= 64 ? launch<DT_BF16, 64>(p, maps, max_items, s) : launch<DT_BF16, 128>(p, maps, max_items, s);
 }
 
 }  // namespace tbe

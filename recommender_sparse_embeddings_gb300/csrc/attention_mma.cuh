@@ -8,6 +8,8 @@
 // its descriptor alone, so nothing is transposed.
 #pragma once
 
+#include <cuda.h>
+
 #include "attention.cuh"
 #include "tcgen05.cuh"
 
@@ -141,37 +143,86 @@ __device__ __forceinline__ void fma2(float& a0, float& a1, float m, float b0, fl
         : "f"(m), "f"(b0), "f"(b1));
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool real) {
-    const int n = real ? 16 : 0;  // 0: sixteen zero bytes, nothing is read
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
 
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// A tensor's TMA map: dimensions (column, head, token), or (column, token,
+// head) where the heads are the outer ones; boxes of 64 columns x 64 tokens of
+// one head in the 128-byte swizzle.  Columns from D on and tokens from N on
+// read as zeros.
+struct alignas(64) TileMap {
+    CUtensorMap map;
+    int32_t heads_outer;
+};
 
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+struct AttnMaps {
+    TileMap q, k, v, g;
+};
+
+__device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
 }
 
-// Rows [from, from + COUNT) of a tile of ROWS rows whose row 0 is row `row0`
-// of a history (zeros from row `len` on and from column D on), by one warp.
-// 16-bit elements.
-template <int ROWS, int DP, int COUNT = ROWS>
-__device__ __forceinline__ void load_tile_async(uint32_t dst, const Rows& r, int64_t token0, int head, int row0,
-                                                int len, int D, int lane, int from = 0) {
-    const int chunk = lane % 8;
-    const uint16_t* base = static_cast<const uint16_t*>(r.data) + head * r.head_stride + chunk * 8;
-    const uint16_t* src = base + (token0 + row0) * r.token_stride;
+__device__ __forceinline__ void tma_load(uint32_t dst, const TileMap& map, int col, int head, int token,
+                                         uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];" ::"r"(dst),
+        "l"(&map.map), "r"(col), "r"(map.heads_outer ? token : head), "r"(map.heads_outer ? head : token),
+        "r"(smem_u32(bar))
+        : "memory");
+}
+
+// A tile of ROWS rows from row `row0` of a history, by one warp; `full`
+// completes when it has landed.  Where it reaches past the history's end (its
+// last tile only) the rows there belong to the next history: the tile lands
+// on `fix`, the warp clears them, and then arrives on `full` itself, so what
+// another history holds (a NaN too) never meets a product.
+template <int ROWS, int DP>
+__device__ __forceinline__ bool load_tile(unsigned char* dst, const TileMap& map, const AttnItem& it, int head,
+                                          int row0, uint64_t* full, uint64_t* fix, uint32_t& fix_phase, int lane) {
+    const bool part = it.len - row0 < ROWS;
+    if (lane == 0) {
+        uint64_t* bar = part ? fix : full;
+        mbar_expect_tx(bar, ROWS * DP * 2);
+        const uint32_t to = smem_u32(dst);
 #pragma unroll
-    for (int slab = 0; slab < DP / 64; ++slab) {
-        const int col = slab * 64 + chunk * 8;
-        const bool inside = col < D;
-        for (int row = from + lane / 8; row < from + COUNT; row += 4) {
-            const bool real = inside && row0 + row < len;
-            const uint16_t* p = real ? src + row * r.token_stride + slab * 64 : base;
-            cp_async16(dst + slab * (ROWS * 128) + row * 128 + ((chunk ^ (row & 7)) << 4), p, real);
-        }
+        for (int slab = 0; slab < DP / 64; ++slab)
+#pragma unroll
+            for (int r = 0; r < ROWS; r += 64)
+                tma_load(to + slab * (ROWS * 128) + r * 128, map, slab * 64, head, it.start + row0 + r, bar);
     }
+    if (!part) return true;
+    const bool ok = mbar_wait_tight(fix, fix_phase);
+    fix_phase ^= 1u;
+    if (!__all_sync(0xffffffffu, ok)) return false;
+    for (int slab = 0; slab < DP / 64; ++slab)
+        for (int c = (it.len - row0) * 8 + lane; c < ROWS * 8; c += 32)
+            *reinterpret_cast<uint4*>(dst + slab * (ROWS * 128) + c * 16) = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(full);
+    return true;
+}
+
+// A loader warp's ring: `steps` tiles of 64 rows through STAGES stages;
+// place(n) gives tile n's first row and head.
+template <int DP, int STAGES, typename F>
+__device__ __forceinline__ bool load_ring(unsigned char* ring, const TileMap& map, const AttnItem& it,
+                                          uint64_t* full, uint64_t* empty, uint64_t* fix, uint32_t& fix_phase,
+                                          int steps, int lane, F place) {
+    for (int n = 0; n < steps; ++n) {
+        const int st = n % STAGES;
+        bool ok = n < STAGES || mbar_wait_tight(&empty[st], ((n / STAGES) - 1) & 1);
+        const int2 at = place(n);
+        ok = __all_sync(0xffffffffu, ok) &&
+             load_tile<64, DP>(ring + st * (64 * DP * 2), map, it, at.y, at.x, &full[st], fix, fix_phase, lane);
+        if (!ok) return false;
+    }
+    return true;
 }
 
 // The warp's 32 rows (row0 ..) of a 128-row tile in shared memory to rows of
