@@ -93,6 +93,66 @@ __device__ __forceinline__ bool run_loader(unsigned char* big, const TileMap& bi
            load_ring<DP, Shape<DP>::kStages>(ring, map, it, full, empty, fix, phase, steps, lane, place);
 }
 
+// The product warp of both kernels.  Per block n: S = A X^T and dP = B Y^T
+// into its buffer; once P and dS stand there, first += P Z and second += dS X,
+// where Z is X (dq) or Y (dkv).
+template <int DT, int DP, bool ZisX>
+__device__ __forceinline__ bool run_products(Bars& bars, uint32_t sbase, uint32_t tmem, uint32_t t_first,
+                                             uint32_t t_second, int ksteps, int steps) {
+    using L = Shape<DP>;
+    constexpr int NB = L::NB;
+    const uint32_t id_s = mma_idesc(DT == DT_BF16, 128, 64);
+    const uint32_t id_o = mma_idesc(DT == DT_BF16, 128, ksteps * 16) | kMnMajorB;
+    const uint64_t da = smem_desc_sw128(sbase + L::a, 1024), db = smem_desc_sw128(sbase + L::b, 1024);
+    const uint64_t dx = smem_desc_sw128(sbase + L::x, 1024), dy = smem_desc_sw128(sbase + L::y, 1024);
+    const uint64_t mx = smem_desc_mn(sbase + L::x, 64 * 128), my = smem_desc_mn(sbase + L::y, 64 * 128);
+    auto wait = [&](uint64_t* bar, int phase) {
+        const bool in = mbar_wait_tight(bar, phase & 1);
+        const bool all = __all_sync(0xffffffffu, in);
+        tcgen05_after_sync();
+        return all;
+    };
+    // S (which = 0) or dP (which = 1) of block n
+    auto score = [&](int n, int which) {
+        const int st = n % L::kStages;
+        if (!wait(which ? &bars.y_full[st] : &bars.x_full[st], n / L::kStages)) return false;
+        if (elect_one()) {
+            issue_scores<DP>(tmem + (n % NB) * 128 + which * 64, which ? db : da,
+                             (which ? dy : dx) + st * (L::kSmall / 16), id_s, ksteps);
+            if (which) {
+                if (ZisX && n + L::kStages < steps) mma_commit(&bars.y_empty[st]);
+                mma_commit(&bars.s_full[n % NB]);
+            }
+        }
+        __syncwarp();
+        return true;
+    };
+    if (!wait(&bars.big_full, 0)) return false;
+    for (int n = 0; n < NB && n < steps; ++n)
+        if (!score(n, 0) || !score(n, 1)) return false;
+    for (int n = 0; n < steps; ++n) {
+        const int st = n % L::kStages;
+        const uint32_t t = tmem + (n % NB) * 128;
+        if (!wait(&bars.ds_full[n % NB], n / NB)) return false;
+        if (elect_one()) {
+            issue_product(t_first, t, (ZisX ? mx : my) + st * (L::kSmall / 16), id_o, n > 0);
+            if (!ZisX && n + L::kStages < steps) mma_commit(&bars.y_empty[st]);
+            if (n + NB < steps) mma_commit(&bars.v_done);
+            issue_product(t_second, t + 64, mx + st * (L::kSmall / 16), id_o, n > 0);
+            if (n + L::kStages < steps) mma_commit(&bars.x_empty[st]);
+            if (n + NB < steps) mma_commit(&bars.k_done);
+            if (n + 1 == steps) mma_commit(&bars.last);
+        }
+        __syncwarp();
+        // block n + NB's scores overwrite P and dS: each waits for its
+        // product, the first under the second's cover
+        if (n + NB < steps &&
+            !(wait(&bars.v_done, n) && score(n + NB, 0) && wait(&bars.k_done, n) && score(n + NB, 1)))
+            return false;
+    }
+    return true;
+}
+
 // The helper warp's table of one block: entry x is the bias (base 2) at
 // distance least + x, 191 of them; nothing where all share one bucket.
 // Returns whether they do, and that bucket's bias.
@@ -148,51 +208,8 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
     bool ok = true;
 
     if (warp == kHelp) {
-        if (lane == 0) {
-            const uint32_t id_s = mma_idesc(DT == DT_BF16, 128, 64);
-            const uint32_t id_o = mma_idesc(DT == DT_BF16, 128, ksteps * 16) | kMnMajorB;
-            ok = mbar_wait_tight(&bars.big_full, 0);
-            // S (which = 0: Q K^T) or dP (which = 1: G V^T) of block n
-            auto score = [&](int n, int which) {
-                const int st = n % L::kStages;
-                const uint32_t big = sbase + (which ? L::b : L::a);
-                const uint32_t small = sbase + (which ? L::y : L::x) + st * L::kSmall;
-                if (!mbar_wait_tight(which ? &bars.y_full[st] : &bars.x_full[st], (n / L::kStages) & 1)) return false;
-                tcgen05_after_sync();
-                for (int k = 0; k < ksteps; ++k) {
-                    const uint32_t oa = (k / 4) * (128 * 128) + (k % 4) * 32, ob = (k / 4) * (64 * 128) + (k % 4) * 32;
-                    mma_f16(tmem + (n % NB) * 128 + which * 64, smem_desc_sw128(big + oa, 1024),
-                            smem_desc_sw128(small + ob, 1024), id_s, k > 0);
-                }
-                if (which && n + L::kStages < steps) mma_commit(&bars.y_empty[st]);
-                if (which) mma_commit(&bars.s_full[n % NB]);
-                return true;
-            };
-            for (int n = 0; n < NB && n < steps && ok; ++n) ok = score(n, 0) && score(n, 1);
-            for (int n = 0; n < steps && ok; ++n) {
-                const int st = n % L::kStages;
-                const uint32_t t = tmem + (n % NB) * 128;
-                ok = mbar_wait_tight(&bars.ds_full[n % NB], (n / NB) & 1);
-                if (!ok) break;
-                tcgen05_after_sync();
-                for (int k = 0; k < 4; ++k)
-                    mma_f16_ts(t_r, t + k * 8, smem_desc_mn(sbase + L::x + st * L::kSmall + k * 2048, 64 * 128), id_o,
-                               n > 0 || k > 0);
-                if (n + NB < steps) mma_commit(&bars.v_done);
-                for (int k = 0; k < 4; ++k)
-                    mma_f16_ts(t_dq, t + 64 + k * 8, smem_desc_mn(sbase + L::x + st * L::kSmall + k * 2048, 64 * 128),
-                               id_o, n > 0 || k > 0);
-                if (n + L::kStages < steps) mma_commit(&bars.x_empty[st]);
-                if (n + NB < steps) mma_commit(&bars.k_done);
-                if (n + 1 == steps) mma_commit(&bars.last);
-                // block n + NB's scores overwrite P and dS: each waits for its
-                // product, the first under the second's cover
-                if (n + NB < steps)
-                    ok = mbar_wait_tight(&bars.v_done, n & 1) && score(n + NB, 0) &&
-                         mbar_wait_tight(&bars.k_done, n & 1) && score(n + NB, 1);
-            }
-        }
-        __syncwarp();
+        // R += P K, dQ += dS K
+        ok = run_products<DT, DP, true>(bars, sbase, tmem, t_r, t_dq, ksteps, steps);
     } else if (warp == kHelp + 1) {
         ok = run_loader<DP>(smem + L::a, maps.q, head, first, smem + L::x, maps.k, &bars.big_full, bars.x_full,
                             bars.x_empty, &bars.fix[0], it, steps, lane,
@@ -380,51 +397,8 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
     bool ok = true;
 
     if (warp == kHelp) {
-        if (lane == 0) {
-            const uint32_t id_s = mma_idesc(DT == DT_BF16, 128, 64);
-            const uint32_t id_o = mma_idesc(DT == DT_BF16, 128, ksteps * 16) | kMnMajorB;
-            ok = mbar_wait_tight(&bars.big_full, 0);
-            // S^T (which = 0: K Q^T) or dP^T (which = 1: V G^T) of block n
-            auto score = [&](int n, int which) {
-                const int st = n % L::kStages;
-                const uint32_t big = sbase + (which ? L::b : L::a);
-                const uint32_t small = sbase + (which ? L::y : L::x) + st * L::kSmall;
-                if (!mbar_wait_tight(which ? &bars.y_full[st] : &bars.x_full[st], (n / L::kStages) & 1)) return false;
-                tcgen05_after_sync();
-                for (int k = 0; k < ksteps; ++k) {
-                    const uint32_t oa = (k / 4) * (128 * 128) + (k % 4) * 32, ob = (k / 4) * (64 * 128) + (k % 4) * 32;
-                    mma_f16(tmem + (n % NB) * 128 + which * 64, smem_desc_sw128(big + oa, 1024),
-                            smem_desc_sw128(small + ob, 1024), id_s, k > 0);
-                }
-                if (which) mma_commit(&bars.s_full[n % NB]);
-                return true;
-            };
-            for (int n = 0; n < NB && n < steps && ok; ++n) ok = score(n, 0) && score(n, 1);
-            for (int n = 0; n < steps && ok; ++n) {
-                const int st = n % L::kStages;
-                const uint32_t t = tmem + (n % NB) * 128;
-                ok = mbar_wait_tight(&bars.ds_full[n % NB], (n / NB) & 1);
-                if (!ok) break;
-                tcgen05_after_sync();
-                for (int k = 0; k < 4; ++k)
-                    mma_f16_ts(t_dv, t + k * 8, smem_desc_mn(sbase + L::y + st * L::kSmall + k * 2048, 64 * 128), id_o,
-                               n > 0 || k > 0);
-                if (n + L::kStages < steps) mma_commit(&bars.y_empty[st]);
-                if (n + NB < steps) mma_commit(&bars.v_done);
-                for (int k = 0; k < 4; ++k)
-                    mma_f16_ts(t_dk, t + 64 + k * 8, smem_desc_mn(sbase + L::x + st * L::kSmall + k * 2048, 64 * 128),
-                               id_o, n > 0 || k > 0);
-                if (n + L::kStages < steps) mma_commit(&bars.x_empty[st]);
-                if (n + NB < steps) mma_commit(&bars.k_done);
-                if (n + 1 == steps) mma_commit(&bars.last);
-                // block n + NB's scores overwrite P^T and dS^T: each waits for
-                // its product, the first under the second's cover
-                if (n + NB < steps)
-                    ok = mbar_wait_tight(&bars.v_done, n & 1) && score(n + NB, 0) &&
-                         mbar_wait_tight(&bars.k_done, n & 1) && score(n + NB, 1);
-            }
-        }
-        __syncwarp();
+        // dV += P^T G, dK += dS^T Q
+        ok = run_products<DT, DP, false>(bars, sbase, tmem, t_dv, t_dk, ksteps, steps);
     } else if (warp == kHelp + 1) {
         ok = run_loader<DP>(smem + L::a, maps.k, kvh, first, smem + L::x, maps.q, &bars.big_full, bars.x_full,
                             bars.x_empty, &bars.fix[0], it, steps, lane, place);

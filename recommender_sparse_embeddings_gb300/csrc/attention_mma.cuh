@@ -39,6 +39,30 @@ __device__ __forceinline__ uint64_t smem_desc_mn(uint32_t addr, uint32_t slab) {
     return smem_desc(addr, slab, 1024u) | ((uint64_t)2u << 61);
 }
 
+// True in one lane of a converged warp.  The products are issued under this
+// election by a warp whose other lanes run along: the compiler then knows the
+// operands to be uniform (under a plain `lane == 0` each issue took about a
+// hundred cycles, and the products' issue bounded the kernels).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
+
+// D[tmem] = A B^T of K-major tiles, 16 columns a step: A of 128 rows, B of 64.
+template <int DP>
+__device__ __forceinline__ void issue_scores(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, int ksteps) {
+#pragma unroll
+    for (int k = 0; k < DP / 16; ++k)
+        if (k < ksteps)
+            mma_f16(d_tmem, a + (k / 4) * (128 * 128 / 16) + (k % 4) * 2, b + (k / 4) * (64 * 128 / 16) + (k % 4) * 2,
+                    idesc, k > 0);
+}
+
 // Bits of the instruction descriptor that make A or B MN-major.
 constexpr uint32_t kMnMajorA = 1u << 15;
 constexpr uint32_t kMnMajorB = 1u << 16;
@@ -53,6 +77,14 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uin
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
         "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
+}
+
+// D[tmem] (+)= A B of a 16-bit A in tensor memory (128 x 64) and a 64-row tile
+// read MN-major.
+__device__ __forceinline__ void issue_product(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
+                                              bool accumulate) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) mma_f16_ts(d_tmem, a_tmem + k * 8, b + k * (2048 / 16), idesc, accumulate || k > 0);
 }
 
 // 32 consecutive columns of the thread's lane (no wait).
@@ -143,6 +175,20 @@ __device__ __forceinline__ void fma2(float& a0, float& a1, float m, float b0, fl
         : "f"(m), "f"(b0), "f"(b1));
 }
 
+// Whether `p` holds in any thread of the CTA's first eight warps (barrier 1).
+__device__ __forceinline__ bool any_of_256(bool p) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred a, b;\n\t"
+        "setp.ne.u32 a, %1, 0;\n\t"
+        "barrier.cta.red.or.pred b, 1, 256, a;\n\t"
+        "selp.u32 %0, 1, 0, b;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)p)
+        : "memory");
+    return r != 0;
+}
+
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -185,7 +231,7 @@ template <int ROWS, int DP>
 __device__ __forceinline__ bool load_tile(unsigned char* dst, const TileMap& map, const AttnItem& it, int head,
                                           int row0, uint64_t* full, uint64_t* fix, uint32_t& fix_phase, int lane) {
     const bool part = it.len - row0 < ROWS;
-    if (lane == 0) {
+    if (elect_one()) {
         uint64_t* bar = part ? fix : full;
         mbar_expect_tx(bar, ROWS * DP * 2);
         const uint32_t to = smem_u32(dst);
@@ -225,13 +271,13 @@ __device__ __forceinline__ bool load_ring(unsigned char* ring, const TileMap& ma
     return true;
 }
 
-// The warp's 32 rows (row0 ..) of a 128-row tile in shared memory to rows of
-// a contiguous [N, heads, D] tensor; rows from `len` on are left out.
-template <int DP>
+// COUNT rows (from row0) of a 128-row tile in shared memory to rows of a
+// contiguous [N, heads, D] tensor, by one warp; rows from `len` on are left out.
+template <int DP, int COUNT = 32>
 __device__ __forceinline__ void store_tile_rows(void* out, const unsigned char* tile, int row0, int64_t token0,
                                                 int first, int len, int heads, int head, int D, int lane) {
     const int chunks = D / 8;
-    for (int x = lane; x < 32 * chunks; x += 32) {
+    for (int x = lane; x < COUNT * chunks; x += 32) {
         const int r = row0 + x / chunks, ch = x % chunks;
         if (first + r >= len) continue;
         const uint4 u =
