@@ -297,6 +297,255 @@ __global__ void __launch_bounds__(kWarps * 32) attn_decode_kernel(const AttnDeco
     }
 }
 
+// ---- 16-bit caches: the products on mma.sync (m16n8k16).  One new token is a
+// row of G heads against the cache, far from a tcgen05 tile, and the work is
+// bound by the cache's bytes: on the FMA units the dot products and their
+// shuffles took about 140 instructions a kilobyte of cache (405 us for 128
+// histories of 4000 rows of 4 x 128, twice the bytes' time); with a warp's
+// tensor instruction it is about 15.
+//
+// A warp takes 16 rows a step.  Lane (g, t) = (lane / 4, lane % 4).
+//   S [heads x rows] = Q K^T: a lane holds 16-byte chunks t, t + 4, .. of rows
+//     g and g + 8 as they lie in memory.  The product runs over all columns, so
+//     which k slot a column takes does not matter as long as Q's fragment says
+//     the same: a chunk is two instructions' operand as loaded.
+//   O^T [columns x heads] = V^T P^T: a lane holds chunk g (g + 8) of rows 2t,
+//     2t + 1, 2t + 8, 2t + 9; a byte permute pairs neighbouring rows, and S's
+//     accumulator is P^T's fragment as it stands.
+// The next step's keys are fetched before this step's softmax, its values after
+// this step's product: a warp keeps 8 KB in flight (head_dim 128).
+
+constexpr int kMmaHeads = 8;
+constexpr int kMmaWarps = 4;
+
+template <int DT>
+__device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1) {
+    if constexpr (DT == DT_BF16)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+template <int DT>
+__device__ __forceinline__ uint32_t round2(float lo, float hi) {
+    uint32_t r;
+    if constexpr (DT == DT_BF16)
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+template <int DT, int DP>
+__global__ void __launch_bounds__(kMmaWarps * 32) attn_decode_mma_kernel(const AttnDecode p) {
+    constexpr int KC = DP / 32, VC = DP / 64;  // 16-byte chunks a lane holds of a key row, of a value row
+    constexpr int STEP = kMmaWarps * 16;
+    extern __shared__ float dsm[];  // bias by bucket [8][buckets]; then the warps' sums [warps][8][DP]
+    __shared__ float stat[kMmaWarps][kMmaHeads][2];
+    const int hchunks = (p.s.G + kMmaHeads - 1) / kMmaHeads;
+    uint32_t bx = blockIdx.x;
+    const int split = (int)(bx % p.splits);
+    bx /= p.splits;
+    const int hc = (int)(bx % hchunks);
+    bx /= hchunks;
+    const int kvh = (int)(bx % p.s.Hk), b = (int)(bx / p.s.Hk);
+    const int g0 = hc * kMmaHeads, gn = tmin(kMmaHeads, p.s.G - g0), head0 = kvh * p.s.G + g0;
+    const int len = cache_length(p, b);
+    if (len < 0 && threadIdx.x == 0 && split == 0) atomicOr(p.s.error, ERR_OOB);
+    const Visible vis = visible_rows(p.s, tmax(len, 0));
+    if (split > 0 && split * p.chunk >= vis.count) return;
+    const int begin = split * p.chunk, end = tmin(vis.count, begin + p.chunk);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
+    const int D = p.s.D;
+    if (p.bias) {
+        for (int i = threadIdx.x; i < kMmaHeads * p.s.buckets; i += kMmaWarps * 32) {
+            const int h = i / p.s.buckets, k = i % p.s.buckets;
+            dsm[i] = h < gn ? bias_base2(load_elem<DT>(p.bias, (int64_t)k * p.s.H + head0 + h)) : 0.f;
+        }
+        __syncthreads();
+    }
+    const float* bias = dsm + g * p.s.buckets;
+    const float c2 = p.s.scale * kLog2e;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    uint4 q[KC];
+#pragma unroll
+    for (int c = 0; c < KC; ++c) {
+        const int col = (t + 4 * c) * 8;
+        q[c] = zero;
+        if (g < gn && col < D)
+            q[c] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q.data) +
+                                                        b * p.q.token_stride + (head0 + g) * p.q.head_stride + col));
+    }
+    const uint16_t* kbase = static_cast<const uint16_t*>(p.kp) + kvh * p.k_head;
+    const uint16_t* vbase = static_cast<const uint16_t*>(p.vp) + kvh * p.v_head;
+    const int32_t* table = p.table + (int64_t)b * p.width;
+
+    // lanes 0-15: where the keys of the step's 16 rows lie, lanes 16-31 the
+    // values (elements from the base); -1 for none
+    auto find = [&](int x0) {
+        const int xi = x0 + lane % 16;
+        if (xi >= end) return (int64_t)-1;
+        const int j = xi < vis.sinks ? xi : vis.lo + xi - vis.sinks;
+        const uint32_t pg = fast_div((uint32_t)j, p.page);
+        const int row = (int)((uint32_t)j - pg * p.page.n);
+        const int32_t page = __ldg(table + pg);
+        if (page < 0 || page >= p.num_pages) {
+            atomicOr(p.s.error, ERR_OOB);
+            return (int64_t)-1;
+        }
+        return lane < 16 ? page * p.k_page + row * p.k_token : page * p.v_page + row * p.v_token;
+    };
+    uint4 kr[2][KC], vr[4][VC];
+    auto load_keys = [&](int64_t where) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int64_t at = __shfl_sync(0xffffffffu, where, g + 8 * r);
+#pragma unroll
+            for (int c = 0; c < KC; ++c) {
+                const int col = (t + 4 * c) * 8;
+                kr[r][c] = at >= 0 && col < D ? __ldg(reinterpret_cast<const uint4*>(kbase + at + col)) : zero;
+            }
+        }
+    };
+    auto load_values = [&](int64_t where) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int64_t at = __shfl_sync(0xffffffffu, where, 16 + 2 * t + (r & 1) + 8 * (r >> 1));
+#pragma unroll
+            for (int c = 0; c < VC; ++c) {
+                const int col = (g + 8 * c) * 8;
+                vr[r][c] = at >= 0 && col < D ? __ldg(reinterpret_cast<const uint4*>(vbase + at + col)) : zero;
+            }
+        }
+    };
+
+    float m = -INFINITY, l = 0.f;  // of head g (l: this lane's rows)
+    float o[VC * 4][4];
+#pragma unroll
+    for (int i = 0; i < VC * 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+    int x0 = begin + warp * 16;
+    int64_t where = find(x0), next = find(x0 + STEP);
+    load_keys(where);
+    load_values(where);
+    for (; x0 < end; x0 += STEP) {
+        float s[2][4];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[r][e] = 0.f;
+#pragma unroll
+            for (int c = 0; c < KC; ++c) {
+                mma_16816<DT>(s[r], q[c].x, 0u, q[c].y, 0u, kr[r][c].x, kr[r][c].y);
+                mma_16816<DT>(s[r], q[c].z, 0u, q[c].w, 0u, kr[r][c].z, kr[r][c].w);
+            }
+        }
+        // rows 2t, 2t + 1, 2t + 8, 2t + 9 of the step, for head g; rows without
+        // a page count as not there
+        const uint32_t there = __ballot_sync(0xffffffffu, where >= 0);
+        float y[4] = {s[0][0], s[0][1], s[1][0], s[1][1]};
+        const int64_t now = next;
+        load_keys(now);
+        next = find(x0 + 2 * STEP);
+        float top = m;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int r = 2 * t + (e & 1) + 8 * (e >> 1);
+            const int xi = x0 + r, j = xi < vis.sinks ? xi : vis.lo + xi - vis.sinks;
+            y[e] *= c2;
+            if (p.bias) y[e] += bias[xi < end ? attn_bucket(p.s, len - 1 - j) : 0];
+            if (!(there >> r & 1)) y[e] = -INFINITY;
+            top = fmaxf(top, y[e]);
+        }
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const float safe = top == -INFINITY ? 0.f : top;
+        if (__any_sync(0xffffffffu, top > m)) {
+            const float keep = ex2(m - safe);
+            l *= keep;
+            const float k0 = __shfl_sync(0xffffffffu, keep, 8 * t), k1 = __shfl_sync(0xffffffffu, keep, 8 * t + 4);
+#pragma unroll
+            for (int i = 0; i < VC * 4; ++i) {
+                o[i][0] *= k0;
+                o[i][1] *= k1;
+                o[i][2] *= k0;
+                o[i][3] *= k1;
+            }
+            m = top;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            y[e] = ex2(y[e] - safe);
+            l += y[e];
+        }
+        const uint32_t p0 = round2<DT>(y[0], y[1]), p1 = round2<DT>(y[2], y[3]);
+#pragma unroll
+        for (int c = 0; c < VC; ++c) {
+            const uint32_t* r0 = &vr[0][c].x;
+            const uint32_t* r1 = &vr[1][c].x;
+            const uint32_t* r2 = &vr[2][c].x;
+            const uint32_t* r3 = &vr[3][c].x;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                mma_16816<DT>(o[c * 4 + i], __byte_perm(r0[i], r1[i], 0x5410), __byte_perm(r0[i], r1[i], 0x7632),
+                              __byte_perm(r2[i], r3[i], 0x5410), __byte_perm(r2[i], r3[i], 0x7632), p0, p1);
+        }
+        load_values(now);
+        where = now;
+    }
+    // join the lanes of a head, then the CTA's warps
+    l += __shfl_xor_sync(0xffffffffu, l, 1);
+    l += __shfl_xor_sync(0xffffffffu, l, 2);
+    if (t == 0) {
+        stat[warp][g][0] = m;
+        stat[warp][g][1] = l;
+    }
+    float* osm = dsm + (p.bias ? kMmaHeads * p.s.buckets : 0);
+#pragma unroll
+    for (int c = 0; c < VC; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                osm[(warp * kMmaHeads + 2 * t + (e & 1)) * DP + (g + 8 * c) * 8 + 2 * i + (e >> 1)] = o[c * 4 + i][e];
+    __syncthreads();
+    const bool whole = vis.count <= p.chunk;
+    for (int i = threadIdx.x; i < gn * D; i += kMmaWarps * 32) {
+        const int h = i / D, d = i % D;
+        float top = -INFINITY, sum = 0.f, v = 0.f;
+#pragma unroll
+        for (int w = 0; w < kMmaWarps; ++w) top = fmaxf(top, stat[w][h][0]);
+        const float safe = top == -INFINITY ? 0.f : top;
+#pragma unroll
+        for (int w = 0; w < kMmaWarps; ++w) {
+            const float keep = ex2(stat[w][h][0] - safe);
+            sum += stat[w][h][1] * keep;
+            v += osm[(w * kMmaHeads + h) * DP + d] * keep;
+        }
+        const int64_t row = (int64_t)b * p.s.H + head0 + h;
+        if (whole) {
+            store_elem<DT>(p.out, row * D + d, sum == 0.f ? 0.f : v / sum);  // an empty cache gives zeros
+        } else {
+            float* to = p.part + (row * p.splits + split) * (D + 2);
+            to[d] = v;
+            if (d == 0) {
+                to[D] = top;
+                to[D + 1] = sum;
+            }
+        }
+    }
+}
+
 // Joins the chunks of one history and head: the partial sums scaled to the
 // largest of their maxima, added in the chunks' order.
 template <int DT>
@@ -331,6 +580,15 @@ cudaError_t decode(const AttnDecode& p, cudaStream_t s) {
     return cudaGetLastError();
 }
 
+template <int DT, int DP>
+cudaError_t decode_mma(const AttnDecode& p, cudaStream_t s) {
+    const int64_t grid = (int64_t)p.splits * ((p.s.G + kMmaHeads - 1) / kMmaHeads) * p.s.Hk * p.B;
+    const size_t smem =
+        sizeof(float) * ((p.bias ? (size_t)kMmaHeads * p.s.buckets : 0) + (size_t)kMmaWarps * kMmaHeads * DP);
+    attn_decode_mma_kernel<DT, DP><<<(unsigned)grid, kMmaWarps * 32, smem, s>>>(p);
+    return cudaGetLastError();
+}
+
 template <int DT, int GT>
 cudaError_t decode_dim(const AttnDecode& p, cudaStream_t s) {
     constexpr int V = 16 / sizeof(typename Elem<DT>::type);
@@ -348,8 +606,13 @@ cudaError_t decode_dim(const AttnDecode& p, cudaStream_t s) {
 
 template <int DT>
 cudaError_t decode_type(const AttnDecode& p, cudaStream_t s) {
-    cudaError_t e;
-    switch (attn_decode_heads(p.s.G)) {
+    cudaError_t e = cudaErrorInvalidValue;
+    bool mma = false;
+    if constexpr (DT != DT_F32) {
+        mma = p.vec && p.s.D <= 128;
+        if (mma) e = p.s.D <= 64 ? decode_mma<DT, 64>(p, s) : decode_mma<DT, 128>(p, s);
+    }
+    if (!mma) switch (attn_decode_heads(p.s.G)) {
         case 1: e = decode_dim<DT, 1>(p, s); break;
         case 2: e = decode_dim<DT, 2>(p, s); break;
         case 4: e = decode_dim<DT, 4>(p, s); break;

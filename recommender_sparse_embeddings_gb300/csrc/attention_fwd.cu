@@ -5,10 +5,9 @@
 //   S = Q K^T           (128 x 64, both operands in shared memory, fp32 in TMEM)
 //   P = 2^(S c + b - m) (one query per thread, rounded to the 16-bit type, TMEM)
 //   O += P V            (P from TMEM, V as stored: its MN-major descriptor)
-// Roles: warps 0-7 softmax (thread = query; the second warpgroup takes the
-// block's last 32 keys: one warp a scheduler and CTA left the softmax bound by
-// its own latency), warp 8 issues the products, warps 9 and 10 fetch the tiles
-// (TMA), warp 11 spreads the bias over the block's distances.  S has two
+// Roles: warps 0-3 softmax (thread = query), warp 4 issues the products,
+// warps 5 and 6 fetch the tiles (TMA), warp 7 spreads the bias over the
+// block's distances.  S has two
 // buffers, so the next block's scores are computed while this one's softmax
 // runs; P takes its S's place.  Two CTAs share an SM (256 TMEM columns each)
 // and fill each other's gaps.
@@ -25,7 +24,7 @@ namespace tbe {
 
 namespace {
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 256;
 constexpr float kLazy = 8.f;
 
 template <int DP>
@@ -34,8 +33,7 @@ struct Fwd {
     static constexpr int kTile = 64 * DP * 2;  // bytes of a K or V tile
     static constexpr int kQ = 128 * DP * 2;
     static constexpr int q = 0, k = kQ, v = k + kStages * kTile, bias = v + kStages * kTile;
-    static constexpr int red = bias + 2 * 192 * 4;  // a float per row and warpgroup
-    static constexpr int bytes = red + 2 * 128 * 4 + 1024;  // 1024: the swizzle's alignment
+    static constexpr int bytes = bias + 2 * 192 * 4 + 1024;  // 1024: the swizzle's alignment
     static constexpr int cols = 256;
 };
 
@@ -79,9 +77,9 @@ __global__ void __launch_bounds__(kThreads, 2) attn_fwd_mma_kernel(const AttnFor
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars.s_full[i], 1);
-            mbar_init(&bars.p_full[i], 8);
+            mbar_init(&bars.p_full[i], 4);
             mbar_init(&bars.b_full[i], 1);
-            mbar_init(&bars.b_empty[i], 8);
+            mbar_init(&bars.b_empty[i], 4);
         }
         mbar_init(&bars.o_done, 1);
         mbar_init(&bars.fix[0], 1);
@@ -90,25 +88,25 @@ __global__ void __launch_bounds__(kThreads, 2) attn_fwd_mma_kernel(const AttnFor
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_proxy_async_smem();
     }
-    if (warp == 8) tmem_alloc(&tmem_slot, L::cols);
+    if (warp == 4) tmem_alloc(&tmem_slot, L::cols);
     tcgen05_before_sync();
     __syncthreads();
     tcgen05_after_sync();
     const uint32_t tmem = tmem_slot;
     const uint32_t t_o = tmem + 128;  // S0 and S1 at columns 0 and 64
     bool ok = true;
-    if (warp == 9 || warp == 10) {
-        // ---- loaders: warp 9 Q and K, warp 10 V
+    if (warp == 5 || warp == 6) {
+        // ---- loaders: warp 5 Q and K, warp 6 V
         uint32_t fix_phase = 0;
         auto place = [&](int n) { return make_int2(block_of(n) * 64, kvh); };
-        if (warp == 9)
+        if (warp == 5)
             ok = load_tile<128, DP>(smem + L::q, maps.q, it, head, first, &bars.q_full, &bars.fix[0], fix_phase, lane) &&
                  load_ring<DP, L::kStages>(smem + L::k, maps.k, it, bars.k_full, bars.k_empty, &bars.fix[0], fix_phase,
                                            steps, lane, place);
         else
             ok = load_ring<DP, L::kStages>(smem + L::v, maps.v, it, bars.v_full, bars.v_empty, &bars.fix[1], fix_phase,
                                            steps, lane, place);
-    } else if (warp == 11) {
+    } else if (warp == 7) {
         // ---- bias by distance: entry x of the block's table is the bias at
         // distance base + x - 63, x in [0, 191)
         if (p.bias) {
@@ -139,7 +137,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_fwd_mma_kernel(const AttnFor
                 if (lane == 0) mbar_arrive(&bars.b_full[buf]);
             }
         }
-    } else if (warp == 8) {
+    } else if (warp == 4) {
         // ---- products
         const uint32_t id_s = mma_idesc(DT == DT_BF16, 128, 64);
         const uint32_t id_o = mma_idesc(DT == DT_BF16, 128, ksteps * 16) | kMnMajorB;
@@ -181,66 +179,81 @@ __global__ void __launch_bounds__(kThreads, 2) attn_fwd_mma_kernel(const AttnFor
             }
         }
     } else {
-        // ---- softmax: thread = query, warpgroup = half of the block's keys.
-        // All eight warps run every step and barrier, whatever their waits said.
-        const int wg = warp / 4, q4 = warp % 4, row = q4 * 32 + lane, i = first + row;
-        const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
+        // ---- softmax: thread = query
+        const int row = threadIdx.x, i = first + row;
+        const uint32_t lanes = (uint32_t)(warp * 32) << 16;
         const float c2 = p.s.scale * kLog2e;
         const float* bt = reinterpret_cast<const float*>(smem + L::bias);
-        float* red = reinterpret_cast<float*>(smem + L::red);
         float m = -INFINITY, l0 = 0.f, l1 = 0.f;
         for (int n = 0; n < steps; ++n) {
             const int buf = n & 1;
             const uint32_t t_s = tmem + buf * 64 + lanes;
-            if (ok) ok = mbar_wait_tight(&bars.s_full[buf], (n / 2) & 1);
+            ok = mbar_wait_tight(&bars.s_full[buf], (n / 2) & 1);
             if (ok && p.bias) ok = mbar_wait_tight(&bars.b_full[buf], (n / 2) & 1);
-            __syncwarp();
             // products up to n - 2 have completed (their P's place is S(n)'s,
             // which is full); n - 1 is waited for where O is touched
+            if (!__all_sync(0xffffffffu, ok)) {
+                ok = false;
+                break;
+            }
             tcgen05_after_sync();
-            float x[32];
-            tmem_ld32_issue(t_s + 32 * wg, x);
-            tmem_wait_ld(x, 32);
+            float x[64];
+            tmem_ld32_issue(t_s, x);
+            tmem_ld32_issue(t_s + 32, x + 32);
+            tmem_wait_ld(x, 64);
             const int key0 = block_of(n) * 64;
             const bool table = p.bias && !is_uniform[buf];
             // a block needs masks unless all its pairs are visible
             const bool all = key0 + 63 <= first && (first + 127 - key0 < p.s.window || key0 + 63 < p.s.sinks);
             if (!all) {
-                const int key = key0 + 32 * wg;
-                const uint32_t seen =
-                    bits_below(i - key + 1) & (~bits_below(i - p.s.window + 1 - key) | bits_below(p.s.sinks - key));
+                const int up = i - key0 + 1, down = i - p.s.window + 1 - key0, sk = p.s.sinks - key0;
 #pragma unroll
-                for (int c = 0; c < 32; ++c)
-                    if (!(seen >> c & 1)) x[c] = -INFINITY;
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t seen = bits_below(up - 32 * h) & (~bits_below(down - 32 * h) | bits_below(sk - 32 * h));
+#pragma unroll
+                    for (int c = 0; c < 32; ++c)
+                        if (!(seen >> c & 1)) x[32 * h + c] = -INFINITY;
+                }
             }
             // logit = x * by + add: with a table it is formed here, else (one
             // bias for the block, and c2 > 0) the maximum is taken of the raw
             // products and one multiply-add before ex2 does it all
             float by = c2, add = p.bias ? uniform_bias[buf] : 0.f;
             if (table) {
-                const float* b = bt + buf * 192 + row + 63 - 32 * wg;
+                const float* b = bt + buf * 192 + row + 63;
 #pragma unroll
-                for (int c = 0; c < 32; c += 2) fma2(x[c], x[c + 1], c2, b[-c], b[-c - 1]);
+                for (int c = 0; c < 64; c += 2) fma2(x[c], x[c + 1], c2, b[-c], b[-c - 1]);
                 by = 1.f;
                 add = 0.f;
             }
+            if (p.bias) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars.b_empty[buf]);
+            }
             float t[8];
 #pragma unroll
-            for (int c = 0; c < 8; ++c) t[c] = fmaxf(max3(x[c], x[c + 8], x[c + 16]), x[c + 24]);
+            for (int c = 0; c < 8; ++c) t[c] = max3(x[c], x[c + 8], x[c + 16]);
+#pragma unroll
+            for (int c = 24; c < 56; c += 16)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) t[e] = max3(t[e], x[c + e], x[c + 8 + e]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) t[e] = fmaxf(t[e], x[56 + e]);
             const float top = fmaf(fmaxf(max3(max3(t[0], t[1], t[2]), t[3], t[4]), max3(t[5], t[6], t[7])), by, add);
-            if (any_of_256(top > m + kLazy)) {
-                red[wg * 128 + row] = top;
-                asm volatile("bar.sync 2, 256;" ::: "memory");
-                const float to = max3(m, red[row], red[128 + row]);
+            if (__any_sync(0xffffffffu, top > m + kLazy || m == -INFINITY)) {
+                const float to = fmaxf(m, top);
                 const float keep = to == -INFINITY ? 1.f : ex2(m - to);
                 m = to;
                 l0 *= keep;
                 l1 *= keep;
                 if (n > 0) {
-                    if (ok) ok = mbar_wait_tight(&bars.o_done, (n - 1) & 1);
-                    __syncwarp();
+                    ok = mbar_wait_tight(&bars.o_done, (n - 1) & 1);
+                    if (!__all_sync(0xffffffffu, ok)) {
+                        ok = false;
+                        break;
+                    }
                     tcgen05_after_sync();
-                    for (int c = wg * (DP / 2); c < (wg + 1) * (DP / 2); c += 16) {
+                    for (int c = 0; c < DP; c += 16) {
                         float o[16];
                         tmem_ld16(t_o + lanes + c, o);
 #pragma unroll
@@ -250,48 +263,45 @@ __global__ void __launch_bounds__(kThreads, 2) attn_fwd_mma_kernel(const AttnFor
                 }
             }
             const float less = m == -INFINITY ? 0.f : add - m;
-            uint32_t pk[16];
 #pragma unroll
-            for (int c = 0; c < 32; c += 2) {
-                fma2(x[c], x[c + 1], by, less, less);
-                x[c] = ex2(x[c]);
-                x[c + 1] = ex2(x[c + 1]);
-                add2(l0, l1, x[c], x[c + 1]);
-                pk[c / 2] = pack2<DT>(x[c], x[c + 1]);
+            for (int h = 0; h < 64; h += 32) {
+                uint32_t pk[16];
+#pragma unroll
+                for (int c = h; c < h + 32; c += 2) {
+                    fma2(x[c], x[c + 1], by, less, less);
+                    x[c] = ex2(x[c]);
+                    x[c + 1] = ex2(x[c + 1]);
+                    add2(l0, l1, x[c], x[c + 1]);
+                    pk[(c - h) / 2] = pack2<DT>(x[c], x[c + 1]);
+                }
+                tmem_st16(t_s + h / 2, pk);
             }
-            // (S(n)'s other half may still be read: the barrier above orders
-            // this store after both warpgroups' loads)
-            tmem_st16(t_s + 16 * wg, pk);
             tmem_wait_st();
             tcgen05_before_sync();
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&bars.p_full[buf]);
-                if (p.bias) mbar_arrive(&bars.b_empty[buf]);
-            }
+            if (lane == 0) mbar_arrive(&bars.p_full[buf]);
         }
-        // ---- out = O / l, through the rows of Q's tile; each warpgroup half
-        // of the columns.  (o_last: a barrier of its own, as o_done may be any
-        // of three phases along by now)
+        // ---- out = O / l, through the warp's rows of Q's tile
+        // (a barrier of its own: o_done may be any of three phases along by now)
         if (ok) ok = mbar_wait_tight(&bars.o_last, 0);
-        __syncwarp();
-        tcgen05_after_sync();
-        red[wg * 128 + row] = l0 + l1;
-        asm volatile("bar.sync 2, 256;" ::: "memory");
-        const float l = red[row] + red[128 + row];
-        const float inv = l == 0.f ? 0.f : 1.f / l;  // a row that sees nothing is zero
-        unsigned char* qt = smem + L::q;
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok) {
+            tcgen05_after_sync();
+            const float l = l0 + l1;
+            const float inv = l == 0.f ? 0.f : 1.f / l;  // a row that sees nothing is zero
+            unsigned char* qt = smem + L::q;
 #pragma unroll
-        for (int c = 0; c < DP / 2; c += 32) tmem_to_tile<DT>(qt, t_o + lanes, wg * (DP / 2) + c, row, inv);
-        if (wg == 0 && i < it.len) p.lse[(int64_t)head * p.N + it.start + i] = m + log2f(l);
-        asm volatile("bar.sync 2, 256;" ::: "memory");
-        store_tile_rows<DP, 16>(p.out, qt, warp * 16, it.start, first, it.len, p.s.H, head, D, lane);
+            for (int c = 0; c < DP; c += 32) tmem_to_tile<DT>(qt, t_o + lanes, c, row, inv);
+            if (i < it.len) p.lse[(int64_t)head * p.N + it.start + i] = m + log2f(l);
+            __syncwarp();
+            store_tile_rows<DP>(p.out, qt, warp * 32, it.start, first, it.len, p.s.H, head, D, lane);
+        }
     }
     if (!ok) atomicOr(p.s.error, ERR_TIMEOUT);
     tcgen05_before_sync();
     __syncthreads();
     tcgen05_after_sync();
-    if (warp == 8) tmem_dealloc(tmem, L::cols);
+    if (warp == 4) tmem_dealloc(tmem, L::cols);
 }
 
 template <int DT, int DP>

@@ -175,20 +175,6 @@ __device__ __forceinline__ void fma2(float& a0, float& a1, float m, float b0, fl
         : "f"(m), "f"(b0), "f"(b1));
 }
 
-// Whether `p` holds in any thread of the CTA's first eight warps (barrier 1).
-__device__ __forceinline__ bool any_of_256(bool p) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred a, b;\n\t"
-        "setp.ne.u32 a, %1, 0;\n\t"
-        "barrier.cta.red.or.pred b, 1, 256, a;\n\t"
-        "selp.u32 %0, 1, 0, b;\n\t}"
-        : "=r"(r)
-        : "r"((uint32_t)p)
-        : "memory");
-    return r != 0;
-}
-
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -199,7 +185,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // head) where the heads are the outer ones; boxes of 64 columns x 64 tokens of
 // one head in the 128-byte swizzle.  Columns from D on and tokens from N on
 // read as zeros.
-struct alignas(64) TileMap {
+struct TileMap {
     CUtensorMap map;
     int32_t heads_outer;
 };
@@ -271,13 +257,13 @@ __device__ __forceinline__ bool load_ring(unsigned char* ring, const TileMap& ma
     return true;
 }
 
-// COUNT rows (from row0) of a 128-row tile in shared memory to rows of a
-// contiguous [N, heads, D] tensor, by one warp; rows from `len` on are left out.
-template <int DP, int COUNT = 32>
+// The warp's 32 rows (row0 ..) of a 128-row tile in shared memory to rows of
+// a contiguous [N, heads, D] tensor; rows from `len` on are left out.
+template <int DP>
 __device__ __forceinline__ void store_tile_rows(void* out, const unsigned char* tile, int row0, int64_t token0,
                                                 int first, int len, int heads, int head, int D, int lane) {
     const int chunks = D / 8;
-    for (int x = lane; x < COUNT * chunks; x += 32) {
+    for (int x = lane; x < 32 * chunks; x += 32) {
         const int r = row0 + x / chunks, ch = x % chunks;
         if (first + r >= len) continue;
         const uint4 u =
