@@ -156,16 +156,19 @@ struct Split {
     int chunk, splits;
 };
 
-// Visible rows a decode CTA takes.  Whole histories where they are short or
-// there are many; else chunks of at least 256 rows (the join reads D + 2
-// floats per chunk and head, under 2 % of a chunk's rows), small enough that
-// the batch makes about 16 CTAs per SM, so that histories of uneven length
-// leave no SM idle.
+// Visible rows a decode CTA takes: small enough that the batch makes so many
+// CTAs per SM that histories of uneven length leave no SM idle, and at least
+// 256 (the join reads D + 2 floats per chunk and head, under 2 % of a chunk's
+// rows).  The tensor-instruction kernel runs three CTAs per SM and pays about
+// 3 us to start each: 16 (198 us for 128 bf16 histories of 4000 rows; 32: 205,
+// 64: 215).  The FMA kernel is lighter: 64 (106 us for 200 fp32 histories of
+// 600 rows; 32: 117, 16: 131).
 Split decode_split(const tbe_attention* h, int64_t B, int64_t max_length) {
     const int64_t most = std::max<int64_t>(1, visible_most(h, max_length));
     const int gt = attn_decode_heads(h->s.G);
     const int64_t rows = std::max<int64_t>(1, B * h->s.Hk * ((h->s.G + gt - 1) / gt));
-    int64_t chunk = most * rows / ((int64_t)h->num_sms * 16);
+    const int64_t per_sm = h->s.dtype == TBE_F32 || h->s.D > 128 ? 64 : 16;
+    int64_t chunk = most * rows / (h->num_sms * per_sm);
     chunk = std::max<int64_t>(256, (chunk + 63) / 64 * 64);
     const int64_t splits = (most + chunk - 1) / chunk;
     return Split{(int)std::min<int64_t>(chunk, INT_MAX / 2), (int)splits};

@@ -89,6 +89,8 @@ __device__ __forceinline__ int cache_length(const AttnDecode& p, int b) {
     return len < 0 || (int64_t)len > p.max_length ? -1 : len;
 }
 
+// The 16-byte vectors that a lane holds of a row; columns from D on keep what
+// the registers hold (zeros, from the start).
 template <int DT, int NV>
 __device__ __forceinline__ void load_vecs(uint4 (&u)[NV], const typename Elem<DT>::type* row, int col, int step, int D,
                                           int vec) {
@@ -97,7 +99,6 @@ __device__ __forceinline__ void load_vecs(uint4 (&u)[NV], const typename Elem<DT
 #pragma unroll
     for (int n = 0; n < NV; ++n) {
         const int c = col + n * step;
-        u[n] = make_uint4(0, 0, 0, 0);
         if (vec) {
             if (c < D) u[n] = __ldg(reinterpret_cast<const uint4*>(row + c));
         } else {
@@ -151,12 +152,11 @@ __global__ void __launch_bounds__(kWarps * 32) attn_decode_kernel(const AttnDeco
         m[g] = -INFINITY;
         l[g] = 0.f;
         uint4 u[NV];
+#pragma unroll
+        for (int n = 0; n < NV; ++n) u[n] = make_uint4(0, 0, 0, 0);
         if (g < gn) {
             const E* row = static_cast<const E*>(p.q.data) + b * p.q.token_stride + (head0 + g) * p.q.head_stride;
             load_vecs<DT, NV>(u, row, col, cstep, p.s.D, p.vec);
-        } else {
-#pragma unroll
-            for (int n = 0; n < NV; ++n) u[n] = make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
         for (int n = 0; n < NV; ++n) unpack16<DT>(u[n], &q[g][n * V]);
@@ -170,29 +170,57 @@ __global__ void __launch_bounds__(kWarps * 32) attn_decode_kernel(const AttnDeco
     const E* vbase = static_cast<const E*>(p.vp) + kvh * p.v_head;
     const int32_t* table = p.table + (int64_t)b * p.width;
 
-    for (int x0 = begin; x0 < end; x0 += STEP) {
-        uint4 kr[U][NV], vr[U][NV];
+    // Where the lane's rows of a step lie (elements from the bases) and how far
+    // they are from the new token; -1 for a row that is not there.  Such a row
+    // leaves its registers as they are: its logit is replaced, its weight is 0.
+    struct Place {
+        int64_t k[U], v[U];
         int dist[U];
+    };
+    auto find = [&](int x0) {
+        Place at;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int xi = x0 + (u * kWarps + warp) * RPW + sub;
             const int j = xi < vis.sinks ? xi : vis.lo + xi - vis.sinks;
-            dist[u] = -1;
-#pragma unroll
-            for (int n = 0; n < NV; ++n) kr[u][n] = vr[u][n] = make_uint4(0, 0, 0, 0);
+            at.dist[u] = -1;
+            at.k[u] = at.v[u] = 0;
             if (xi < end) {
                 const uint32_t pg = fast_div((uint32_t)j, p.page);
                 const int row = (int)((uint32_t)j - pg * p.page.n);
                 const int32_t page = __ldg(table + pg);
                 if (page >= 0 && page < p.num_pages) {
-                    dist[u] = len - 1 - j;
-                    load_vecs<DT, NV>(kr[u], kbase + page * p.k_page + row * p.k_token, col, cstep, p.s.D, p.vec);
-                    load_vecs<DT, NV>(vr[u], vbase + page * p.v_page + row * p.v_token, col, cstep, p.s.D, p.vec);
+                    at.dist[u] = len - 1 - j;
+                    at.k[u] = page * p.k_page + row * p.k_token;
+                    at.v[u] = page * p.v_page + row * p.v_token;
                 } else {
                     atomicOr(p.s.error, ERR_OOB);
                 }
             }
         }
+        return at;
+    };
+    uint4 kr[U][NV], vr[U][NV];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int n = 0; n < NV; ++n) kr[u][n] = vr[u][n] = make_uint4(0, 0, 0, 0);
+    auto load_keys = [&](const Place& at) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (at.dist[u] >= 0) load_vecs<DT, NV>(kr[u], kbase + at.k[u], col, cstep, p.s.D, p.vec);
+    };
+    auto load_values = [&](const Place& at) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (at.dist[u] >= 0) load_vecs<DT, NV>(vr[u], vbase + at.v[u], col, cstep, p.s.D, p.vec);
+    };
+    // the next step's keys are fetched before this step's softmax, its values
+    // after this step's product
+    Place here = find(begin), next = find(begin + STEP);
+    load_keys(here);
+    load_values(here);
+    for (int x0 = begin; x0 < end; x0 += STEP) {
         float s[U][GT];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -209,17 +237,18 @@ __global__ void __launch_bounds__(kWarps * 32) attn_decode_kernel(const AttnDeco
                 s[u][g] = t;
             }
             if (p.bias) {
-                const int bk = dist[u] >= 0 ? attn_bucket(p.s, dist[u]) : 0;
+                const int bk = here.dist[u] >= 0 ? attn_bucket(p.s, here.dist[u]) : 0;
 #pragma unroll
                 for (int g = 0; g < GT; ++g) s[u][g] += dsm[g * p.s.buckets + bk];
             }
         }
+        load_keys(next);
 #pragma unroll
         for (int g = 0; g < GT; ++g) {
             float top = m[g];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                if (dist[u] < 0) s[u][g] = -INFINITY;
+                if (here.dist[u] < 0) s[u][g] = -INFINITY;
                 top = fmaxf(top, s[u][g]);
             }
             const float safe = top == -INFINITY ? 0.f : top;
@@ -245,6 +274,9 @@ __global__ void __launch_bounds__(kWarps * 32) attn_decode_kernel(const AttnDeco
 #pragma unroll
                 for (int i = 0; i < W; ++i) o[g][i] = fmaf(s[u][g], f[i], o[g][i]);
         }
+        load_values(next);
+        here = next;
+        next = find(x0 + 2 * STEP);
     }
     // join the warp's groups, then the CTA's warps
     float* osm = dsm + (p.bias ? GT * p.s.buckets : 0);  // [kWarps][GT][LPR * W]
@@ -389,12 +421,14 @@ __global__ void __launch_bounds__(kMmaWarps * 32) attn_decode_mma_kernel(const A
     const uint16_t* vbase = static_cast<const uint16_t*>(p.vp) + kvh * p.v_head;
     const int32_t* table = p.table + (int64_t)b * p.width;
 
+    auto row_of = [&](int x) { return x < vis.sinks ? x : vis.lo + x - vis.sinks; };
+    const float last_bias = p.bias ? bias[p.s.buckets - 1] : 0.f;
     // lanes 0-15: where the keys of the step's 16 rows lie, lanes 16-31 the
     // values (elements from the base); -1 for none
     auto find = [&](int x0) {
         const int xi = x0 + lane % 16;
         if (xi >= end) return (int64_t)-1;
-        const int j = xi < vis.sinks ? xi : vis.lo + xi - vis.sinks;
+        const int j = row_of(xi);
         const uint32_t pg = fast_div((uint32_t)j, p.page);
         const int row = (int)((uint32_t)j - pg * p.page.n);
         const int32_t page = __ldg(table + pg);
@@ -404,27 +438,31 @@ __global__ void __launch_bounds__(kMmaWarps * 32) attn_decode_mma_kernel(const A
         }
         return lane < 16 ? page * p.k_page + row * p.k_token : page * p.v_page + row * p.v_token;
     };
+    // A row that is not there leaves its registers as they are: zeros or an
+    // earlier row of this history.  Its logit is replaced, its weight is 0.
     uint4 kr[2][KC], vr[4][VC];
+#pragma unroll
+    for (int c = 0; c < KC; ++c) kr[0][c] = kr[1][c] = zero;
+#pragma unroll
+    for (int c = 0; c < VC; ++c) vr[0][c] = vr[1][c] = vr[2][c] = vr[3][c] = zero;
     auto load_keys = [&](int64_t where) {
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             const int64_t at = __shfl_sync(0xffffffffu, where, g + 8 * r);
+            const uint4* row = reinterpret_cast<const uint4*>(kbase + at + t * 8);
 #pragma unroll
-            for (int c = 0; c < KC; ++c) {
-                const int col = (t + 4 * c) * 8;
-                kr[r][c] = at >= 0 && col < D ? __ldg(reinterpret_cast<const uint4*>(kbase + at + col)) : zero;
-            }
+            for (int c = 0; c < KC; ++c)
+                if (at >= 0 && (t + 4 * c) * 8 < D) kr[r][c] = __ldg(row + 4 * c);
         }
     };
     auto load_values = [&](int64_t where) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int64_t at = __shfl_sync(0xffffffffu, where, 16 + 2 * t + (r & 1) + 8 * (r >> 1));
+            const uint4* row = reinterpret_cast<const uint4*>(vbase + at + g * 8);
 #pragma unroll
-            for (int c = 0; c < VC; ++c) {
-                const int col = (g + 8 * c) * 8;
-                vr[r][c] = at >= 0 && col < D ? __ldg(reinterpret_cast<const uint4*>(vbase + at + col)) : zero;
-            }
+            for (int c = 0; c < VC; ++c)
+                if (at >= 0 && (g + 8 * c) * 8 < D) vr[r][c] = __ldg(row + 8 * c);
         }
     };
 
@@ -458,13 +496,20 @@ __global__ void __launch_bounds__(kMmaWarps * 32) attn_decode_mma_kernel(const A
         load_keys(now);
         next = find(x0 + 2 * STEP);
         float top = m;
+        // the step's last row is its nearest: from `far` on all share a bucket
+        const bool distant = x0 + 15 < end && len - 1 - row_of(x0 + 15) >= p.s.far;
+        float add[4] = {last_bias, last_bias, last_bias, last_bias};
+        if (p.bias && !distant) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int xi = x0 + 2 * t + (e & 1) + 8 * (e >> 1);
+                add[e] = bias[xi < end ? attn_bucket(p.s, len - 1 - row_of(xi)) : 0];
+            }
+        }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const int r = 2 * t + (e & 1) + 8 * (e >> 1);
-            const int xi = x0 + r, j = xi < vis.sinks ? xi : vis.lo + xi - vis.sinks;
-            y[e] *= c2;
-            if (p.bias) y[e] += bias[xi < end ? attn_bucket(p.s, len - 1 - j) : 0];
-            if (!(there >> r & 1)) y[e] = -INFINITY;
+            y[e] = fmaf(y[e], c2, add[e]);
+            if (!(there >> (2 * t + (e & 1) + 8 * (e >> 1)) & 1)) y[e] = -INFINITY;
             top = fmaxf(top, y[e]);
         }
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
