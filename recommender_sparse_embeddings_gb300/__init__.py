@@ -170,7 +170,8 @@ def _ptr(t: Optional[torch.Tensor]):
 
 def _stream(stream) -> ctypes.c_void_p:
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # the current stream's handle without building a Stream object (3 us)
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()))
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
@@ -430,7 +431,7 @@ def tbe_attention_destroy(h: AttentionHandle):
 
 
 def _rows(h: AttentionHandle, t: torch.Tensor, tokens: int, heads: int, name: str) -> _Rows:
-    if t.dim() != 3 or t.shape[0] != tokens or t.shape[1] != heads or t.shape[2] != h.head_dim:
+    if tuple(t.shape) != (tokens, heads, h.head_dim):
         raise ValueError(f"{name}: expected [{tokens}, {heads}, {h.head_dim}], got {list(t.shape)}")
     if t.dtype != h.dtype:
         raise ValueError(f"{name}: expected {h.dtype}, got {t.dtype}")

@@ -170,6 +170,7 @@ Split decode_split(const tbe_attention* h, int64_t B, int64_t max_length) {
     const int64_t per_sm = h->s.dtype == TBE_F32 || h->s.D > 128 ? 64 : 16;
     int64_t chunk = most * rows / (h->num_sms * per_sm);
     chunk = std::max<int64_t>(256, (chunk + 63) / 64 * 64);
+    if (most <= 512) chunk = std::max(chunk, most);  // not worth a second launch
     const int64_t splits = (most + chunk - 1) / chunk;
     return Split{(int)std::min<int64_t>(chunk, INT_MAX / 2), (int)splits};
 }

@@ -20,11 +20,12 @@
 // rows of dS in fp32, takes R times that sum off dQ (R needs little
 // precision: the sum is small), and leaves the exact delta to dkv.
 //
-// A thread owns one row of S (a query in dq, a key in dkv).  head_dim <= 64:
-// one warpgroup and one set of score buffers, two CTAs per SM that fill each
-// other's gaps (256 TMEM columns each).  Above: one CTA per SM (shared
-// memory), two warpgroups that take the blocks in turn, each with its own
-// score buffers, so one block's products run beside the other's arithmetic.
+// A thread owns one row of S (a query in dq, a key in dkv) and half of a
+// block's columns: a block takes two warpgroups.  head_dim <= 64: one set of
+// score buffers, two CTAs per SM that fill each other's gaps (256 TMEM columns
+// each).  Above: one CTA per SM (shared memory) with two sets of buffers and
+// four warpgroups, two for the even and two for the odd blocks, so one block's
+// products run beside the other's arithmetic.
 //
 // P and dS are rounded to the 16-bit type where they enter a product; the
 // bias gradient sums the unrounded fp32 dS.
@@ -36,8 +37,9 @@ namespace {
 
 template <int DP>
 struct Shape {
-    static constexpr int NB = DP == 64 ? 1 : 2;  // warpgroups and score buffers
-    static constexpr int kThreads = NB * 128 + 128;
+    static constexpr int NB = DP == 64 ? 1 : 2;  // score buffers
+    static constexpr int W = NB * 8;             // compute warps
+    static constexpr int kThreads = W * 32 + 128;
     static constexpr int kPerSm = DP == 64 ? 2 : 1;
     static constexpr int kStages = DP == 64 ? 3 : 3;
     static constexpr int kBig = 128 * DP * 2;   // a 128-row tile
@@ -46,10 +48,10 @@ struct Shape {
     static constexpr int table = y + kStages * kSmall;      // bias by distance, 2 x 192 floats
     static constexpr int stat = table + 2 * 192 * 4;        // dkv: -lse and delta, 2 x 2 x 64 floats
     static constexpr int sums = stat + 2 * 2 * 64 * 4;      // dkv: per warp, a sum per bucket
-    static constexpr int diag = sums + NB * 4 * kMaxBuckets * 4;  // dkv: per warp, 96 diagonals
-    static constexpr int rows = stat;                             // dq: a row sum per thread
-    static constexpr int dq_bytes = sums + 1024;
-    static constexpr int dkv_bytes = diag + NB * 4 * 96 * 4 + 1024;
+    static constexpr int diag = sums + W * kMaxBuckets * 4;       // dkv: per warp, 64 diagonals
+    static constexpr int rows = sums;                             // dq: a row sum per thread
+    static constexpr int dq_bytes = rows + W * 32 * 4 + 1024;
+    static constexpr int dkv_bytes = diag + W * 64 * 4 + 1024;
     // TMEM columns: S (then P) and dP (then dS) per buffer, two accumulators
     static constexpr int cols = DP == 64 ? 256 : 512;
 };
@@ -70,9 +72,9 @@ __device__ __forceinline__ void init_bars(Bars& b) {
     }
     for (int i = 0; i < 2; ++i) {
         mbar_init(&b.s_full[i], 1);
-        mbar_init(&b.ds_full[i], 4);
+        mbar_init(&b.ds_full[i], 8);
         mbar_init(&b.t_full[i], 1);
-        mbar_init(&b.t_empty[i], 4);
+        mbar_init(&b.t_empty[i], 8);
         mbar_init(&b.fix[i], 1);
     }
     mbar_init(&b.v_done, 1);
@@ -135,10 +137,10 @@ __device__ __forceinline__ bool run_products(Bars& bars, uint32_t sbase, uint32_
         const uint32_t t = tmem + (n % NB) * 128;
         if (!wait(&bars.ds_full[n % NB], n / NB)) return false;
         if (elect_one()) {
-            issue_product(t_first, t, (ZisX ? mx : my) + st * (L::kSmall / 16), id_o, n > 0);
+            issue_product<16>(t_first, t, (ZisX ? mx : my) + st * (L::kSmall / 16), id_o, n > 0);
             if (!ZisX && n + L::kStages < steps) mma_commit(&bars.y_empty[st]);
             if (n + NB < steps) mma_commit(&bars.v_done);
-            issue_product(t_second, t + 64, mx + st * (L::kSmall / 16), id_o, n > 0);
+            issue_product<16>(t_second, t + 64, mx + st * (L::kSmall / 16), id_o, n > 0);
             if (n + L::kStages < steps) mma_commit(&bars.x_empty[st]);
             if (n + NB < steps) mma_commit(&bars.k_done);
             if (n + 1 == steps) mma_commit(&bars.last);
@@ -176,7 +178,7 @@ template <int DT, int DP>
 __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_dq_mma_kernel(const AttnBackward p,
                                                                                                    const __grid_constant__ AttnMaps maps) {
     using L = Shape<DP>;
-    constexpr int NB = L::NB, kHelp = NB * 4;  // first helper warp: products; then loaders K, V; then bias
+    constexpr int NB = L::NB, kHelp = L::W;  // first helper warp: products; then loaders K, V; then bias
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     __shared__ Bars bars;
@@ -241,7 +243,7 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
             }
         }
     } else {
-        const int wg = warp / 4, q4 = warp % 4, row = q4 * 32 + lane, i = first + row;
+        const int wg = warp / 4, half = wg % 2, q4 = warp % 4, row = q4 * 32 + lane, i = first + row;
         const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
         const float c2 = p.s.scale * kLog2e;
         const float* bt = reinterpret_cast<const float*>(smem + L::table);
@@ -253,7 +255,7 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
             delta = p.delta[at];
         }
         float sum0 = 0.f, sum1 = 0.f;  // of the row's dS
-        for (int n = wg; n < steps; n += NB) {
+        for (int n = wg / 2; n < steps; n += NB) {
             const int buf = n & 1, sb = n % NB;
             const uint32_t t_s = tmem + sb * 128 + lanes;
             ok = mbar_wait_tight(&bars.s_full[sb], (n / NB) & 1);
@@ -269,59 +271,53 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
             // whether the block holds a query whose only key is its own (attn_lone)
             const bool lone = (first == 0 && key0 == 0) || (p.s.window == 1 && p.s.sinks == 0);
             const bool all = key0 + 63 < first && (first + 127 - key0 < p.s.window || key0 + 63 < p.s.sinks);
+            uint32_t pk[16], dk[16];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float x[32], y[32];
-                tmem_ld32_issue(t_s + 32 * h, x);
-                tmem_ld32_issue(t_s + 64 + 32 * h, y);
-                tmem_wait_ld(x, 32);
-                tmem_wait_ld(y, 32);
+            for (int h = 0; h < 32; h += 16) {
+                float x[16], y[16];
+                tmem_ld16_pair(t_s + 32 * half + h, t_s + 64 + 32 * half + h, x, y);
+                const int key = key0 + 32 * half + h;
                 if (table) {
-                    const float* b = bt + buf * 192 + row + 63 - 32 * h;
+                    const float* b = bt + buf * 192 + row + 63 - 32 * half - h;
 #pragma unroll
-                    for (int c = 0; c < 32; c += 2) {
+                    for (int c = 0; c < 16; c += 2) {
                         float b0 = b[-c], b1 = b[-c - 1];
                         add2(b0, b1, less, less);
                         fma2(x[c], x[c + 1], c2, b0, b1);
                     }
                 } else {
 #pragma unroll
-                    for (int c = 0; c < 32; c += 2) fma2(x[c], x[c + 1], c2, add, add);
+                    for (int c = 0; c < 16; c += 2) fma2(x[c], x[c + 1], c2, add, add);
                 }
                 if (!all) {
-                    const int up = i - key0 + 1 - 32 * h, down = i - p.s.window + 1 - key0 - 32 * h,
-                              sk = p.s.sinks - key0 - 32 * h;
-                    const uint32_t seen = bits_below(up) & (~bits_below(down) | bits_below(sk));
+                    const uint32_t seen =
+                        bits_below(i - key + 1) & (~bits_below(i - p.s.window + 1 - key) | bits_below(p.s.sinks - key));
 #pragma unroll
-                    for (int c = 0; c < 32; ++c)
+                    for (int c = 0; c < 16; ++c)
                         if (!(seen >> c & 1)) x[c] = -INFINITY;
                 }
-                uint32_t pk[16];
 #pragma unroll
-                for (int c = 0; c < 32; c += 2) {
+                for (int c = 0; c < 16; c += 2) {
                     x[c] = ex2(x[c]);
                     x[c + 1] = ex2(x[c + 1]);
                     add2(y[c], y[c + 1], -delta, -delta);
                     mul2(y[c], y[c + 1], x[c], x[c + 1]);
-                    pk[c / 2] = pack2<DT>(x[c], x[c + 1]);
+                    pk[(h + c) / 2] = pack2<DT>(x[c], x[c + 1]);
                 }
                 if (lone) {
-                    const int own = i - key0 - 32 * h;  // the column of the query's own token
 #pragma unroll
-                    for (int c = 0; c < 32; ++c)
-                        if (c == own && attn_lone(i, i, p.s.window, p.s.sinks)) y[c] = 0.f;
+                    for (int c = 0; c < 16; ++c)
+                        if (key + c == i && attn_lone(i, i, p.s.window, p.s.sinks)) y[c] = 0.f;
                 }
-                uint32_t dk[16];
 #pragma unroll
-                for (int c = 0; c < 32; c += 2) {
-                    dk[c / 2] = pack2<DT>(y[c], y[c + 1]);
+                for (int c = 0; c < 16; c += 2) {
+                    dk[(h + c) / 2] = pack2<DT>(y[c], y[c + 1]);
                     add2(sum0, sum1, y[c], y[c + 1]);
                 }
-                // P into S's first columns, dS into dP's: the columns this
-                // thread has read already (h = 0 writes 16 of the 32 read)
-                tmem_st16(t_s + 16 * h, pk);
-                tmem_st16(t_s + 64 + 16 * h, dk);
             }
+            // P and dS into the columns of S and dP that this thread has read
+            tmem_st16(t_s + 32 * half, pk);
+            tmem_st16(t_s + 64 + 32 * half, dk);
             tmem_wait_st();
             tcgen05_before_sync();
             __syncwarp();
@@ -332,22 +328,18 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
         }
         if (ok) ok = mbar_wait_tight(&bars.last, 0);
         ok = __all_sync(0xffffffffu, ok);
-        // delta - e of the row: both warpgroups' sums (every warp comes here)
+        // delta - e of the row: all warpgroups' sums (every warp comes here)
         float* rows = reinterpret_cast<float*>(smem + L::rows);
-        float over = sum0 + sum1;
-        if constexpr (NB == 2) {
-            rows[wg * 128 + row] = over;
-            asm volatile("bar.sync 1, 256;" ::: "memory");
-            over = rows[row] + rows[128 + row];
-        }
+        rows[wg * 128 + row] = sum0 + sum1;
+        asm volatile("bar.sync 1, %0;" ::"n"(L::W * 32) : "memory");
+        float over = 0.f;
+#pragma unroll
+        for (int k = 0; k < 2 * NB; ++k) over += rows[k * 128 + row];
         if (ok) {
             tcgen05_after_sync();
             if (wg == 0 && i < it.len) p.delta[(int64_t)head * p.N + it.start + i] = delta + over;
-            // dq = scale (dQ - over R); the warpgroups take a 64-column slab each
-            unsigned char* qt = smem + L::a;
-#pragma unroll
-            for (int c = wg * 64; c < wg * 64 + 64; c += 32)
-                tmem_to_tile<DT>(qt, t_dq + lanes, c, row, p.s.scale, t_r + lanes, -over);
+            // dq = scale (dQ - over R); the warpgroups take 32 columns each
+            tmem_to_tile<DT>(smem + L::a, t_dq + lanes, wg * 32, row, p.s.scale, t_r + lanes, -over);
         }
     }
     if (!ok) atomicOr(p.s.error, ERR_TIMEOUT);
@@ -364,7 +356,7 @@ template <int DT, int DP>
 __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_dkv_mma_kernel(const AttnBackward p,
                                                                                                     const __grid_constant__ AttnMaps maps) {
     using L = Shape<DP>;
-    constexpr int NB = L::NB, kHelp = NB * 4;
+    constexpr int NB = L::NB, kHelp = L::W;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     __shared__ Bars bars;
@@ -387,7 +379,7 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
     if (threadIdx.x == 0) init_bars<NB>(bars);
     if (warp == kHelp) tmem_alloc(&tmem_slot, L::cols);
     float* sums = reinterpret_cast<float*>(smem + L::sums);
-    for (int i = threadIdx.x; i < NB * 4 * p.s.buckets; i += L::kThreads)
+    for (int i = threadIdx.x; i < L::W * p.s.buckets; i += L::kThreads)
         sums[i / p.s.buckets * kMaxBuckets + i % p.s.buckets] = 0.f;
     tcgen05_before_sync();
     __syncthreads();
@@ -442,166 +434,163 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
             if (lane == 0) mbar_arrive(&bars.t_full[buf]);
         }
     } else {
-        const int wg = warp / 4, q4 = warp % 4, row = q4 * 32 + lane, j = first + row;
+        const int wg = warp / 4, half = wg % 2, q4 = warp % 4, row = q4 * 32 + lane, j = first + row;
         const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
         const float c2 = p.s.scale * kLog2e;
         float* mine = sums + warp * kMaxBuckets;
-        float* diag = reinterpret_cast<float*>(smem + L::diag) + warp * 96;
+        float* diag = reinterpret_cast<float*>(smem + L::diag) + warp * 64;
         for (int g = 0; g < p.s.G; ++g) {
-        for (int n = g * blocks + (NB == 2 ? (g * blocks + wg) % 2 : 0); n < (g + 1) * blocks && ok; n += NB) {
-            const int buf = n & 1, sb = n % NB;
-            const uint32_t t_s = tmem + sb * 128 + lanes;
-            ok = mbar_wait_tight(&bars.s_full[sb], (n / NB) & 1);
-            if (ok) ok = mbar_wait_tight(&bars.t_full[buf], (n / 2) & 1);
-            if (!__all_sync(0xffffffffu, ok)) {
-                ok = false;
-                break;
-            }
-            tcgen05_after_sync();
-            const int q0 = place(n).x;
-            const float* less = reinterpret_cast<const float*>(smem + L::stat) + buf * 128;
-            const int bucket = same_bucket[buf];
-            const bool table = bucket < 0;
-            float sum0 = 0.f, sum1 = 0.f, run = 0.f;
-            const bool all = q0 > first + 127 && (q0 + 63 - first < p.s.window || first + 127 < p.s.sinks);
-            // whether the block holds a query whose only key is its own (attn_lone)
-            const bool lone = !all && (q0 == 0 || (p.s.window == 1 && p.s.sinks == 0));
+            // the head's blocks, or every other one
+            for (int n = g * blocks + (NB == 2 ? (g * blocks + wg / 2) % 2 : 0); n < (g + 1) * blocks && ok; n += NB) {
+                const int buf = n & 1, sb = n % NB;
+                const uint32_t t_s = tmem + sb * 128 + lanes;
+                ok = mbar_wait_tight(&bars.s_full[sb], (n / NB) & 1);
+                if (ok) ok = mbar_wait_tight(&bars.t_full[buf], (n / 2) & 1);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    ok = false;
+                    break;
+                }
+                tcgen05_after_sync();
+                const int q0 = place(n).x;
+                const float* less = reinterpret_cast<const float*>(smem + L::stat) + buf * 128 + 32 * half;
+                const int bucket = same_bucket[buf];
+                const bool table = bucket < 0;
+                float sum0 = 0.f, sum1 = 0.f, run = 0.f;
+                const bool all = q0 > first + 127 && (q0 + 63 - first < p.s.window || first + 127 < p.s.sinks);
+                // whether the block holds a query whose only key is its own (attn_lone)
+                const bool lone = !all && (q0 == 0 || (p.s.window == 1 && p.s.sinks == 0));
+                uint32_t pk[16], dk[16];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float x[32], y[32];
-                tmem_ld32_issue(t_s + 32 * h, x);
-                tmem_ld32_issue(t_s + 64 + 32 * h, y);
-                tmem_wait_ld(x, 32);
-                tmem_wait_ld(y, 32);
-                if (table) {
-                    const float* b = reinterpret_cast<const float*>(smem + L::table) + buf * 192 + 127 - row + 32 * h;
+                for (int h = 0; h < 32; h += 16) {
+                    float x[16], y[16];
+                    tmem_ld16_pair(t_s + 32 * half + h, t_s + 64 + 32 * half + h, x, y);
+                    const int query = q0 + 32 * half + h;
+                    if (table) {
+                        const float* b =
+                            reinterpret_cast<const float*>(smem + L::table) + buf * 192 + 127 - row + 32 * half + h;
 #pragma unroll
-                    for (int c = 0; c < 32; c += 4) {
-                        const float4 t = *reinterpret_cast<const float4*>(less + 32 * h + c);
-                        float b0 = b[c], b1 = b[c + 1], b2 = b[c + 2], b3 = b[c + 3];
-                        add2(b0, b1, t.x, t.y);
-                        add2(b2, b3, t.z, t.w);
-                        fma2(x[c], x[c + 1], c2, b0, b1);
-                        fma2(x[c + 2], x[c + 3], c2, b2, b3);
+                        for (int c = 0; c < 16; c += 4) {
+                            const float4 t = *reinterpret_cast<const float4*>(less + h + c);
+                            float b0 = b[c], b1 = b[c + 1], b2 = b[c + 2], b3 = b[c + 3];
+                            add2(b0, b1, t.x, t.y);
+                            add2(b2, b3, t.z, t.w);
+                            fma2(x[c], x[c + 1], c2, b0, b1);
+                            fma2(x[c + 2], x[c + 3], c2, b2, b3);
+                        }
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 16; c += 4) {
+                            const float4 t = *reinterpret_cast<const float4*>(less + h + c);
+                            fma2(x[c], x[c + 1], c2, t.x, t.y);
+                            fma2(x[c + 2], x[c + 3], c2, t.z, t.w);
+                        }
                     }
-                } else {
+                    if (!all) {
+                        // query i sees key j: j <= i, and i < j + window or j a sink
+                        const uint32_t seen =
+                            ~bits_below(j - query) & bits_below(j < p.s.sinks ? INT_MAX : j + p.s.window - query);
 #pragma unroll
-                    for (int c = 0; c < 32; c += 4) {
-                        const float4 t = *reinterpret_cast<const float4*>(less + 32 * h + c);
-                        fma2(x[c], x[c + 1], c2, t.x, t.y);
-                        fma2(x[c + 2], x[c + 3], c2, t.z, t.w);
+                        for (int c = 0; c < 16; ++c)
+                            if (!(seen >> c & 1)) x[c] = -INFINITY;
+                    }
+#pragma unroll
+                    for (int c = 0; c < 16; c += 4) {
+                        const float4 t = *reinterpret_cast<const float4*>(less + 64 + h + c);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) x[c + e] = ex2(x[c + e]);
+                        add2(y[c], y[c + 1], t.x, t.y);
+                        add2(y[c + 2], y[c + 3], t.z, t.w);
+                        mul2(y[c], y[c + 1], x[c], x[c + 1]);
+                        mul2(y[c + 2], y[c + 3], x[c + 2], x[c + 3]);
+                        pk[(h + c) / 2] = pack2<DT>(x[c], x[c + 1]);
+                        pk[(h + c) / 2 + 1] = pack2<DT>(x[c + 2], x[c + 3]);
+                    }
+                    if (lone) {
+#pragma unroll
+                        for (int c = 0; c < 16; ++c)
+                            if (query + c == j && attn_lone(j, j, p.s.window, p.s.sinks)) y[c] = 0.f;
+                    }
+#pragma unroll
+                    for (int c = 0; c < 16; c += 2) dk[(h + c) / 2] = pack2<DT>(y[c], y[c + 1]);
+                    if (table) {
+                        // the lane's column c has distance c - lane (plus the
+                        // block's): a diagonal's sum moves one lane up a column
+                        // and is complete at lane 31
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) {
+                            const float t = __shfl_up_sync(0xffffffffu, run, 1);
+                            run = y[c] + (lane == 0 ? 0.f : t);
+                            if (lane == 31) diag[h + c] = run;
+                        }
+                    } else if (p.bias) {
+#pragma unroll
+                        for (int c = 0; c < 16; c += 2) add2(sum0, sum1, y[c], y[c + 1]);
                     }
                 }
-                if (!all) {
-                    // query q0 + c sees key j: j <= q0 + c, and q0 + c < j + window or j a sink
-                    const int down = j - q0 - 32 * h, up = j < p.s.sinks ? INT_MAX : j + p.s.window - q0 - 32 * h;
-                    const uint32_t seen = ~bits_below(down) & bits_below(up);
-#pragma unroll
-                    for (int c = 0; c < 32; ++c)
-                        if (!(seen >> c & 1)) x[c] = -INFINITY;
+                // P^T and dS^T into the columns of S^T and dP^T that this thread
+                // has read
+                tmem_st16(t_s + 32 * half, pk);
+                tmem_st16(t_s + 64 + 32 * half, dk);
+                tmem_wait_st();
+                tcgen05_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&bars.ds_full[sb]);
+                    mbar_arrive(&bars.t_empty[buf]);
                 }
-                uint32_t pk[16];
-#pragma unroll
-                for (int c = 0; c < 32; c += 4) {
-                    const float4 t = *reinterpret_cast<const float4*>(less + 64 + 32 * h + c);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) x[c + e] = ex2(x[c + e]);
-                    add2(y[c], y[c + 1], t.x, t.y);
-                    add2(y[c + 2], y[c + 3], t.z, t.w);
-                    mul2(y[c], y[c + 1], x[c], x[c + 1]);
-                    mul2(y[c + 2], y[c + 3], x[c + 2], x[c + 3]);
-                    pk[c / 2] = pack2<DT>(x[c], x[c + 1]);
-                    pk[c / 2 + 1] = pack2<DT>(x[c + 2], x[c + 3]);
-                }
-                if (lone) {
-                    const int own = j - q0 - 32 * h;  // the column of the key's own token
-#pragma unroll
-                    for (int c = 0; c < 32; ++c)
-                        if (c == own && attn_lone(j, j, p.s.window, p.s.sinks)) y[c] = 0.f;
-                }
-                uint32_t dk[16];
-#pragma unroll
-                for (int c = 0; c < 16; ++c) dk[c] = pack2<DT>(y[2 * c], y[2 * c + 1]);
-                // P^T into S^T's first columns, dS^T into dP^T's: the columns
-                // this thread has read already (h = 0 writes 16 of the 32 read)
-                tmem_st16(t_s + 16 * h, pk);
-                tmem_st16(t_s + 64 + 16 * h, dk);
                 if (table) {
-                    // the lane's column c has distance c - lane (plus the
-                    // block's): a diagonal's sum moves one lane up a column
-                    // and is complete at lane 31
+                    // diag[x], x in [0, 63): distance q0 + 32 half - first - 32 q4
+                    // + x - 31; the last column's running sums are the highest 32
+                    if (lane < 31) diag[62 - lane] = run;
+                    __syncwarp();
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) {
-                        const float t = __shfl_up_sync(0xffffffffu, run, 1);
-                        run = y[c] + (lane == 0 ? 0.f : t);
-                        if (lane == 31) diag[32 * h + c] = run;
+                    for (int r = 0; r < 2; ++r) {
+                        // sums of equal buckets, which are neighbours: a segmented
+                        // scan over 32 distances, added by each segment's last lane
+                        const int at = r * 32 + lane, d = q0 + 32 * half - first - 32 * q4 + at - 31;
+                        const int b = at < 63 && d >= 0 ? attn_bucket(p.s, d) : -1;
+                        float t = b >= 0 ? diag[at] : 0.f;
+#pragma unroll
+                        for (int o = 1; o < 32; o <<= 1) {
+                            const float tu = __shfl_up_sync(0xffffffffu, t, o);
+                            const int bu = __shfl_up_sync(0xffffffffu, b, o);
+                            if (lane >= o && bu == b) t += tu;
+                        }
+                        const int next = __shfl_down_sync(0xffffffffu, b, 1);
+                        if (b >= 0 && (lane == 31 || next != b)) mine[b] += t;
+                        __syncwarp();
                     }
                 } else if (p.bias) {
+                    float t = sum0 + sum1;
 #pragma unroll
-                    for (int c = 0; c < 32; c += 2) add2(sum0, sum1, y[c], y[c + 1]);
-                }
-            }
-            tmem_wait_st();
-            tcgen05_before_sync();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&bars.ds_full[sb]);
-                mbar_arrive(&bars.t_empty[buf]);
-            }
-            if (table) {
-                // diag[x], x in [0, 95): distance q0 - first - 32 q4 + x - 31;
-                // the last column's running sums are the highest 32
-                if (lane < 31) diag[94 - lane] = run;
-                __syncwarp();
-#pragma unroll
-                for (int r = 0; r < 3; ++r) {
-                    // sums of equal buckets, which are neighbours: a segmented
-                    // scan over 32 distances, added by each segment's last lane
-                    const int at = r * 32 + lane, d = q0 - first - 32 * q4 + at - 31;
-                    const int b = at < 95 && d >= 0 ? attn_bucket(p.s, d) : -1;
-                    float t = b >= 0 ? diag[at] : 0.f;
-#pragma unroll
-                    for (int o = 1; o < 32; o <<= 1) {
-                        const float tu = __shfl_up_sync(0xffffffffu, t, o);
-                        const int bu = __shfl_up_sync(0xffffffffu, b, o);
-                        if (lane >= o && bu == b) t += tu;
-                    }
-                    const int next = __shfl_down_sync(0xffffffffu, b, 1);
-                    if (b >= 0 && (lane == 31 || next != b)) mine[b] += t;
+                    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+                    if (lane == 0) mine[bucket] += t;
                     __syncwarp();
                 }
-            } else if (p.bias) {
-                float t = sum0 + sum1;
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-                if (lane == 0) mine[bucket] += t;
-                __syncwarp();
             }
-        }
-        if (p.bias) {  // the head's share: all warps come here, whatever their waits said
-            asm volatile("bar.sync 1, %0;" ::"n"(NB * 128) : "memory");
-            for (int b = threadIdx.x; b < p.s.buckets; b += NB * 128) {
-                float t = 0.f;
-                for (int k = 0; k < NB * 4; ++k) {
-                    t += sums[k * kMaxBuckets + b];
-                    sums[k * kMaxBuckets + b] = 0.f;
+            if (p.bias) {  // the head's share: all warps come here, whatever their waits said
+                asm volatile("bar.sync 1, %0;" ::"n"(L::W * 32) : "memory");
+                for (int b = threadIdx.x; b < p.s.buckets; b += L::W * 32) {
+                    float t = 0.f;
+                    for (int k = 0; k < L::W; ++k) {
+                        t += sums[k * kMaxBuckets + b];
+                        sums[k * kMaxBuckets + b] = 0.f;
+                    }
+                    p.bias_part[(w * p.s.H + kvh * p.s.G + g) * p.s.buckets + b] = t;
                 }
-                p.bias_part[(w * p.s.H + kvh * p.s.G + g) * p.s.buckets + b] = t;
+                asm volatile("bar.sync 1, %0;" ::"n"(L::W * 32) : "memory");
             }
-            asm volatile("bar.sync 1, %0;" ::"n"(NB * 128) : "memory");
-        }
         }
         if (ok) ok = mbar_wait_tight(&bars.last, 0);
         ok = __all_sync(0xffffffffu, ok);
         if (ok) {
             tcgen05_after_sync();
-            // dk into K's tile, dv into V's; two warpgroups take one each
-            if (wg == 0)
+            // dk into K's tile, dv into V's: 64 columns a warpgroup
+            const bool of_v = wg / NB == 1;
 #pragma unroll
-                for (int c = 0; c < DP; c += 32) tmem_to_tile<DT>(smem + L::a, t_dk + lanes, c, row, p.s.scale);
-            if (wg == NB - 1)
-#pragma unroll
-                for (int c = 0; c < DP; c += 32) tmem_to_tile<DT>(smem + L::b, t_dv + lanes, c, row, 1.f);
+            for (int c = 0; c < 64; c += 32)
+                tmem_to_tile<DT>(smem + (of_v ? L::b : L::a), (of_v ? t_dv : t_dk) + lanes, (wg % NB) * 64 + c, row,
+                                 of_v ? 1.f : p.s.scale);
         }
     }
     if (!ok) atomicOr(p.s.error, ERR_TIMEOUT);

@@ -79,12 +79,13 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uin
         : "memory");
 }
 
-// D[tmem] (+)= A B of a 16-bit A in tensor memory (128 x 64) and a 64-row tile
-// read MN-major.
+// D[tmem] (+)= A B of a 16-bit A in tensor memory (128 x 64, 32 columns, with
+// GAP columns left out after the first 16) and a 64-row tile read MN-major.
+template <int GAP = 0>
 __device__ __forceinline__ void issue_product(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
                                               bool accumulate) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) mma_f16_ts(d_tmem, a_tmem + k * 8, b + k * (2048 / 16), idesc, accumulate || k > 0);
+    for (int k = 0; k < 4; ++k) mma_f16_ts(d_tmem, a_tmem + k * 8 + (k / 2) * GAP, b + k * (2048 / 16), idesc, accumulate || k > 0);
 }
 
 // 32 consecutive columns of the thread's lane (no wait).
@@ -131,6 +132,26 @@ __device__ __forceinline__ void tmem_wait_ld(float* v, int n) {
 }
 
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// 16 columns at each of two places of the thread's lane.
+__device__ __forceinline__ void tmem_ld16_pair(uint32_t a, uint32_t b, float (&x)[16], float (&y)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7]), "=f"(x[8]),
+          "=f"(x[9]), "=f"(x[10]), "=f"(x[11]), "=f"(x[12]), "=f"(x[13]), "=f"(x[14]), "=f"(x[15])
+        : "r"(a)
+        : "memory");
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=f"(y[0]), "=f"(y[1]), "=f"(y[2]), "=f"(y[3]), "=f"(y[4]), "=f"(y[5]), "=f"(y[6]), "=f"(y[7]), "=f"(y[8]),
+          "=f"(y[9]), "=f"(y[10]), "=f"(y[11]), "=f"(y[12]), "=f"(y[13]), "=f"(y[14]), "=f"(y[15])
+        : "r"(b)
+        : "memory");
+    tmem_wait_ld(x, 16);
+    tmem_wait_ld(y, 16);
+}
 
 // Two floats rounded to the 16-bit type, the first in the low half.
 template <int DT>
