@@ -39,6 +39,26 @@ struct AttnItem {
     int32_t tiles;  // tiles of the history
 };
 
+// The first key tile of a long history with sinks is seen by every query
+// behind the window: its far queries, in chunks of blocks, are work items of
+// their own (FarItem), which leave fp32 sums of the sinks' rows to a join.
+struct FarItem {
+    int32_t start, len;
+    int32_t chunk, chunks;  // this chunk of the history's far query blocks
+    int32_t slot;           // of the history's first partial sums: the tile's own; chunk c has slot + 1 + c
+    int32_t pad[3];
+};
+
+struct FarWork {
+    FarItem* items;
+    int32_t* n_items;
+    int32_t* slot_of;  // per tile item: its history's first slot, -1 for none
+    float* part;       // [slots, Hk, 2, sinks, DP]: dk (unscaled) and dv of the sinks' rows
+    int32_t most;      // items at most (0: no history is split)
+    int32_t blocks;    // query blocks of 64 a chunk
+    int32_t near;      // query blocks of the tile's own item
+};
+
 // First words of the handle's device block; the bucket map follows.
 struct AttnBlock {
     uint32_t error;  // sticky ERR_* bits
@@ -82,7 +102,9 @@ struct AttnBackward {
     void* gk;          // [N, Hk, D]
     void* gv;          // [N, Hk, D]
     float* delta;      // workspace [H, N]: g_i . out_i
-    float* bias_part;  // workspace [items, H, buckets]
+    float* bias_part;  // workspace [items, then far items, H, buckets]
+    int64_t max_items;
+    FarWork far;
     int64_t N;
     const AttnItem* items;
     const int32_t* n_items;
@@ -191,7 +213,8 @@ struct AttnMaps;
 
 // Launchers (each returns the launch's status).
 cudaError_t launch_attn_items(const void* offsets, int index64, int64_t N, int B, int tile, AttnItem* items,
-                              int64_t capacity, int32_t* n_items, uint32_t* error, cudaStream_t s);
+                              int64_t capacity, int32_t* n_items, uint32_t* error, const FarWork& far,
+                              cudaStream_t s);
 cudaError_t launch_attn_forward_simt(const AttnForward& p, int64_t max_items, cudaStream_t s);
 cudaError_t launch_attn_backward_simt(const AttnBackward& p, int64_t max_items, cudaStream_t s);
 cudaError_t launch_attn_forward_mma(const AttnForward& p, const AttnMaps& maps, int64_t max_items, cudaStream_t s);

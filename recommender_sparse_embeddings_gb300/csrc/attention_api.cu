@@ -81,7 +81,7 @@ bool encode_rows(TileMap* map, const tbe_attention* h, const tbe_rows& r, int he
     static const Encode encode = [] {
         void* fn = nullptr;
         cudaDriverEntryPointQueryResult found{};
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &found) != cudaSuccess ||
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) != cudaSuccess ||
             found != cudaDriverEntryPointSuccess)
             fn = nullptr;
         return reinterpret_cast<Encode>(fn);
@@ -118,9 +118,23 @@ int check_batch(const tbe_attention* h, const void* offsets, int32_t index_dtype
 }
 
 struct Layout {
-    size_t n_items, items, delta, bias_part, total;
+    size_t n_items, items, delta, bias_part, far_items, slot_of, far_part, total;
     int64_t capacity;
+    FarWork far;  // sizes only
 };
+
+// How the first key tile's far queries are split (tensor-core backward): in
+// chunks about as long as another tile's work, and of at least 32 blocks, so
+// that N tokens make at most 2 N / (64 blocks) chunks and, with a slot for
+// each split history's tile, half as many slots more.
+FarWork far_split(const tbe_attention* h, int64_t N) {
+    FarWork f{};
+    if (h->s.sinks == 0 || h->s.window >= INT_MAX / 2 || h->s.dtype == TBE_F32 || h->s.D > 128) return f;
+    f.near = (int32_t)((126 + (int64_t)h->s.window) / 64 + 1);
+    f.blocks = std::max(32, h->s.window / 64 + 2);
+    f.most = (int32_t)(2 * N / (64 * (int64_t)f.blocks));
+    return f;
+}
 
 // Laid out for the smallest tile any path of the handle's head_dim takes.
 Layout make_layout(const tbe_attention* h, int64_t N, int64_t B, bool backward) {
@@ -132,11 +146,18 @@ Layout make_layout(const tbe_attention* h, int64_t N, int64_t B, bool backward) 
         o = align_up(o + bytes);
         return at;
     };
-    L.n_items = take(sizeof(int32_t));
+    L.n_items = take(2 * sizeof(int32_t));  // of the tiles, of the far items
     L.items = take(sizeof(AttnItem) * (size_t)L.capacity);
     if (backward) {
         L.delta = take(sizeof(float) * (size_t)N * h->s.H);
-        L.bias_part = take(sizeof(float) * (size_t)L.capacity * h->s.H * h->s.buckets);
+        L.far = far_split(h, N);
+        L.bias_part = take(sizeof(float) * (size_t)(L.capacity + L.far.most) * h->s.H * h->s.buckets);
+        if (L.far.most > 0) {
+            L.far_items = take(sizeof(FarItem) * (size_t)L.far.most);
+            L.slot_of = take(sizeof(int32_t) * (size_t)L.capacity);
+            const size_t slots = (size_t)L.far.most + L.far.most / 2 + 1;
+            L.far_part = take(sizeof(float) * slots * h->s.Hk * 2 * h->s.sinks * (h->s.D <= 64 ? 64 : 128));
+        }
     }
     L.total = o;
     return L;
@@ -294,7 +315,7 @@ int tbe_attention_forward(tbe_attention* h, const tbe_rows* q, const tbe_rows* k
     const int tile = mma ? kMmaTile : attn_simt_tile(h->s.D);
     const int64_t most = N / tile + B;
     rc = status(launch_attn_items(offsets, index_dtype == TBE_I64, N, B, tile, at<AttnItem>(workspace, L.items), most,
-                                  at<int32_t>(workspace, L.n_items), h->s.error, s));
+                                  at<int32_t>(workspace, L.n_items), h->s.error, FarWork{}, s));
     if (rc || N == 0) return rc;
     return status(mma ? launch_attn_forward_mma(p, maps, most, s) : launch_attn_forward_simt(p, most, s));
 }
@@ -338,8 +359,16 @@ int tbe_attention_backward(tbe_attention* h, const tbe_rows* q, const tbe_rows* 
                      encode_rows(&maps.g, h, *grad_out, h->s.H, N);
     const int tile = mma ? kMmaTile : attn_simt_tile(h->s.D);
     const int64_t most = N / tile + B;
+    p.max_items = most;
+    if (mma && L.far.most > 0) {
+        p.far = L.far;
+        p.far.items = at<FarItem>(workspace, L.far_items);
+        p.far.n_items = at<int32_t>(workspace, L.n_items) + 1;
+        p.far.slot_of = at<int32_t>(workspace, L.slot_of);
+        p.far.part = at<float>(workspace, L.far_part);
+    }
     rc = status(launch_attn_items(offsets, index_dtype == TBE_I64, N, B, tile, at<AttnItem>(workspace, L.items), most,
-                                  at<int32_t>(workspace, L.n_items), h->s.error, s));
+                                  at<int32_t>(workspace, L.n_items), h->s.error, p.far, s));
     if (rc) return rc;
     if (N > 0) rc = status(mma ? launch_attn_backward_mma(p, maps, most, s) : launch_attn_backward_simt(p, most, s));
     if (rc || !bias) return rc;

@@ -363,16 +363,38 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
     __shared__ uint32_t tmem_slot;
     __shared__ int same_bucket[2];  // -1: the block's distances have several
 
-    const int64_t w = blockIdx.x / p.s.Hk;
+    // far items (the longest) first, then the tiles
+    const int64_t turn = blockIdx.x / p.s.Hk;
     const int kvh = (int)(blockIdx.x % p.s.Hk);
-    if (w >= *p.n_items) return;
-    const AttnItem it = p.items[w];
-    const int kt = it.tiles - 1 - it.tile;  // the first tiles are seen most: they start first
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int first = kt * 128, D = p.s.D, ksteps = (D + 15) / 16;
-    // query blocks that see a key of the tile, for each head of the group
-    const int64_t end = first < p.s.sinks ? it.len - 1 : tmin<int64_t>(it.len - 1, (int64_t)first + 126 + p.s.window);
-    const int qb0 = first / 64, blocks = (int)(end / 64) + 1 - qb0, steps = blocks * p.s.G;
+    const int D = p.s.D, ksteps = (D + 15) / 16;
+    AttnItem it;
+    int64_t share;      // row of the bias gradient's shares
+    int slot = -1;      // of the partial sums of the sinks' rows
+    int first, qb0, blocks;
+    const bool far = turn < p.far.most;
+    if (far) {
+        if (turn >= *p.far.n_items) return;
+        const FarItem f = p.far.items[turn];
+        it = AttnItem{f.start, f.len, 0, 0};
+        share = p.max_items + turn;
+        slot = f.slot + 1 + f.chunk;
+        first = 0;
+        qb0 = p.far.near + f.chunk * p.far.blocks;
+        blocks = tmin(p.far.blocks, (it.len + 63) / 64 - qb0);
+    } else {
+        share = turn - p.far.most;
+        if (share >= *p.n_items) return;
+        it = p.items[share];
+        const int kt = it.tiles - 1 - it.tile;  // the first tiles are seen most: they start first
+        first = kt * 128;
+        if (kt == 0 && p.far.most > 0) slot = p.far.slot_of[share];
+        // query blocks that see a key of the tile
+        const int64_t end = first < p.s.sinks ? it.len - 1 : tmin<int64_t>(it.len - 1, (int64_t)first + 126 + p.s.window);
+        qb0 = first / 64;
+        blocks = slot >= 0 ? p.far.near : (int)(end / 64) + 1 - qb0;
+    }
+    const int steps = blocks * p.s.G;  // for each head of the group
     auto place = [&](int n) { return make_int2((qb0 + n % blocks) * 64, kvh * p.s.G + n / blocks); };
 
     const uint32_t sbase = smem_u32(smem);
@@ -576,7 +598,7 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
                         t += sums[k * kMaxBuckets + b];
                         sums[k * kMaxBuckets + b] = 0.f;
                     }
-                    p.bias_part[(w * p.s.H + kvh * p.s.G + g) * p.s.buckets + b] = t;
+                    p.bias_part[(share * p.s.H + kvh * p.s.G + g) * p.s.buckets + b] = t;
                 }
                 asm volatile("bar.sync 1, %0;" ::"n"(L::W * 32) : "memory");
             }
@@ -587,6 +609,18 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
             tcgen05_after_sync();
             // dk into K's tile, dv into V's: 64 columns a warpgroup
             const bool of_v = wg / NB == 1;
+            if (slot >= 0 && q4 * 32 < p.s.sinks) {
+                float* to = p.far.part + ((((int64_t)slot * p.s.Hk + kvh) * 2 + of_v) * p.s.sinks + row) * DP + (wg % NB) * 64;
+#pragma unroll
+                for (int c = 0; c < 64; c += 16) {
+                    float o[16];
+                    tmem_ld16((of_v ? t_dv : t_dk) + lanes + (wg % NB) * 64 + c, o);
+                    if (row < p.s.sinks)
+#pragma unroll
+                        for (int e = 0; e < 16; e += 4)
+                            *reinterpret_cast<float4*>(to + c + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                }
+            }
 #pragma unroll
             for (int c = 0; c < 64; c += 32)
                 tmem_to_tile<DT>(smem + (of_v ? L::b : L::a), (of_v ? t_dv : t_dk) + lanes, (wg % NB) * 64 + c, row,
@@ -597,11 +631,36 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
     tcgen05_before_sync();
     __syncthreads();
     tcgen05_after_sync();
-    if (warp < 4)
+    if (far) {
+        // the join writes the sinks' rows
+    } else if (warp < 4)
         store_tile_rows<DP>(p.gk, smem + L::a, warp * 32, it.start, first, it.len, p.s.Hk, kvh, D, lane);
     else if (warp < 8)
         store_tile_rows<DP>(p.gv, smem + L::b, (warp - 4) * 32, it.start, first, it.len, p.s.Hk, kvh, D, lane);
     if (warp == kHelp) tmem_dealloc(tmem, L::cols);
+}
+
+// The sinks' rows of a split history: the tile's own sums and its far chunks',
+// in their order, rounded once.
+template <int DT, int DP>
+__global__ void __launch_bounds__(256) attn_far_join_kernel(const AttnBackward p) {
+    const int turn = blockIdx.x / p.s.Hk, kvh = blockIdx.x % p.s.Hk;
+    if (turn >= *p.far.n_items) return;
+    const FarItem f = p.far.items[turn];
+    if (f.chunk != 0) return;
+    const int64_t stride = (int64_t)p.s.Hk * 2 * p.s.sinks * DP;
+    for (int i = threadIdx.x; i < 2 * p.s.sinks * DP; i += 256) {
+        const int col = i % DP, row = i / DP % p.s.sinks, of_v = i / DP / p.s.sinks;
+        if (col >= p.s.D) continue;
+        const float* from = p.far.part + f.slot * stride + (int64_t)kvh * 2 * p.s.sinks * DP + i;
+        float t = 0.f;
+        for (int c = 0; c <= f.chunks; ++c) t += from[c * stride];
+        const int64_t at = (((int64_t)f.start + row) * p.s.Hk + kvh) * p.s.D + col;
+        if (of_v)
+            store_elem<DT>(p.gv, at, t);
+        else
+            store_elem<DT>(p.gk, at, t * p.s.scale);
+    }
 }
 
 // delta_i = g_i . out_i of every (token, head): eight lanes a row, 16 bytes a
@@ -638,7 +697,11 @@ cudaError_t launch(const AttnBackward& p, const AttnMaps& maps, int64_t max_item
     attn_dq_mma_kernel<DT, DP><<<(unsigned)(max_items * p.s.H), L::kThreads, L::dq_bytes, s>>>(p, maps);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    attn_dkv_mma_kernel<DT, DP><<<(unsigned)(max_items * p.s.Hk), L::kThreads, L::dkv_bytes, s>>>(p, maps);
+    attn_dkv_mma_kernel<DT, DP>
+        <<<(unsigned)((p.far.most + max_items) * p.s.Hk), L::kThreads, L::dkv_bytes, s>>>(p, maps);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || p.far.most == 0) return e;
+    attn_far_join_kernel<DT, DP><<<(unsigned)(p.far.most * p.s.Hk), 256, 0, s>>>(p);
     return cudaGetLastError();
 }
 

@@ -460,16 +460,38 @@ __global__ void __launch_bounds__(kThreads) attn_dkv_simt_kernel(const AttnBackw
     store_rows<DT, T, DP>(p.gk, dk, mul, it.start, p.s.Hk, kvh, first, it.len, p.s.D, tx, ty);
 }
 
+// Exclusive sum over the CTA's 1024 threads, and the total.
+__device__ __forceinline__ int block_scan(int n, int32_t* warp_sum, int& all) {
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    int incl = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += t;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    int before = 0;
+    all = 0;
+    for (int k = 0; k < 32; ++k) {
+        if (k < warp) before += warp_sum[k];
+        all += warp_sum[k];
+    }
+    __syncthreads();
+    return before + incl - n;
+}
+
 // Work items of the batch, and the offsets' check: histories of n tiles of
 // `tile` tokens, each history's last tile first.  One CTA; 1024 histories a
 // pass.  A history whose offsets are not ordered within [0, N] gets no item.
 template <typename I>
 __global__ void __launch_bounds__(1024) attn_items_kernel(const I* __restrict__ off, int64_t N, int B, int tile,
                                                           AttnItem* __restrict__ items, int64_t capacity,
-                                                          int32_t* n_items, uint32_t* error) {
+                                                          int32_t* n_items, uint32_t* error, const FarWork far) {
     __shared__ int32_t warp_sum[32];
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const int lane = threadIdx.x % 32;
     int64_t base = 0;
+    int far_base = 0, slot_base = 0;
     for (int b0 = 0; b0 < B; b0 += 1024) {
         const int b = b0 + threadIdx.x;
         int64_t lo = 0, hi = 0;
@@ -480,40 +502,51 @@ __global__ void __launch_bounds__(1024) attn_items_kernel(const I* __restrict__ 
             if (bad || (b == 0 && lo != 0) || (b == B - 1 && hi != N)) atomicOr(error, ERR_OFFSETS);
             if (bad) hi = lo = 0;
         }
+        int all;
         const int n = (int)((hi - lo + tile - 1) / tile);
-        int incl = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int t = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += t;
+        const int64_t at = base + block_scan(n, warp_sum, all);
+        base += all;
+        int slot = -1;
+        if (far.most > 0) {
+            // chunks of the query blocks behind the first tile's window, where there are many
+            const int behind = (int)((hi - lo + 63) / 64) - far.near;
+            int chunks = behind > far.blocks ? (behind + far.blocks - 1) / far.blocks : 0;
+            int here = far_base + block_scan(chunks, warp_sum, all);
+            far_base += all;
+            const int first = slot_base + block_scan(chunks > 0 ? chunks + 1 : 0, warp_sum, all);
+            slot_base += all;
+            if (chunks > 0 && here + chunks <= far.most) {
+                slot = first;
+                for (int c = 0; c < chunks; ++c)
+                    far.items[here + c] = FarItem{(int)lo, (int)(hi - lo), c, chunks, first, {0, 0, 0}};
+            }
         }
-        if (lane == 31) warp_sum[warp] = incl;
-        __syncthreads();
-        int before = 0, all = 0;
-        for (int k = 0; k < 32; ++k) {
-            if (k < warp) before += warp_sum[k];
-            all += warp_sum[k];
-        }
-        __syncthreads();
-        const int64_t at = base + before + incl - n;
         for (int k = 0; k < 32; ++k) {  // the warp writes its histories' items one history after another
             const int nk = __shfl_sync(0xffffffffu, n, k);
             const int64_t ak = __shfl_sync(0xffffffffu, at, k);
             const int sk = (int)__shfl_sync(0xffffffffu, lo, k);
             const int lk = (int)(__shfl_sync(0xffffffffu, hi, k)) - sk;
+            const int pk = __shfl_sync(0xffffffffu, slot, k);
             for (int t = lane; t < nk; t += 32)
-                if (ak + t < capacity) items[ak + t] = AttnItem{sk, lk, nk - 1 - t, nk};
+                if (ak + t < capacity) {
+                    items[ak + t] = AttnItem{sk, lk, nk - 1 - t, nk};
+                    if (far.most > 0) far.slot_of[ak + t] = pk;
+                }
         }
-        base += all;
     }
-    if (threadIdx.x == 0) *n_items = (int32_t)tmin<int64_t>(base, capacity);
+    if (threadIdx.x == 0) {
+        *n_items = (int32_t)tmin<int64_t>(base, capacity);
+        if (far.most > 0) *far.n_items = tmin(far_base, far.most);
+    }
 }
 
 // grad_bias[bucket, head] = the items' shares added up in a fixed order: a
 // warp per (bucket, head), its lanes over the items, then a tree.
 template <int DT>
 __global__ void __launch_bounds__(256) attn_bias_reduce_kernel(const float* __restrict__ part,
-                                                               const int32_t* __restrict__ n_items, int H,
+                                                               const int32_t* __restrict__ n_items,
+                                                               int64_t max_items,
+                                                               const int32_t* __restrict__ n_far, int H,
                                                                int buckets, void* grad_bias) {
     const int pair = blockIdx.x * 8 + threadIdx.x / 32, lane = threadIdx.x % 32;
     if (pair >= H * buckets) return;
@@ -521,6 +554,8 @@ __global__ void __launch_bounds__(256) attn_bias_reduce_kernel(const float* __re
     const int n = *n_items;
     float t = 0.f;
     for (int w = lane; w < n; w += 32) t += part[((int64_t)w * H + head) * buckets + b];
+    const int nf = n_far ? *n_far : 0;
+    for (int w = lane; w < nf; w += 32) t += part[((max_items + w) * H + head) * buckets + b];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
     if (lane == 0) store_elem<DT>(grad_bias, (int64_t)b * H + head, t);
@@ -609,24 +644,29 @@ cudaError_t launch_attn_backward_simt(const AttnBackward& p, int64_t max_items, 
 }
 
 cudaError_t launch_attn_items(const void* offsets, int index64, int64_t N, int B, int tile, AttnItem* items,
-                              int64_t capacity, int32_t* n_items, uint32_t* error, cudaStream_t s) {
+                              int64_t capacity, int32_t* n_items, uint32_t* error, const FarWork& far,
+                              cudaStream_t s) {
     if (index64)
         attn_items_kernel<int64_t><<<1, 1024, 0, s>>>(static_cast<const int64_t*>(offsets), N, B, tile, items, capacity,
-                                                      n_items, error);
+                                                      n_items, error, far);
     else
         attn_items_kernel<int32_t><<<1, 1024, 0, s>>>(static_cast<const int32_t*>(offsets), N, B, tile, items, capacity,
-                                                      n_items, error);
+                                                      n_items, error, far);
     return cudaGetLastError();
 }
 
 cudaError_t launch_attn_bias_reduce(const AttnBackward& p, void* grad_bias, cudaStream_t s) {
     const int grid = (p.s.H * p.s.buckets + 7) / 8;
+    const int32_t* far = p.far.most > 0 ? p.far.n_items : nullptr;
     if (p.s.dtype == DT_F32)
-        attn_bias_reduce_kernel<DT_F32><<<grid, 256, 0, s>>>(p.bias_part, p.n_items, p.s.H, p.s.buckets, grad_bias);
+        attn_bias_reduce_kernel<DT_F32><<<grid, 256, 0, s>>>(p.bias_part, p.n_items, p.max_items, far, p.s.H, p.s.buckets,
+                                                               grad_bias);
     else if (p.s.dtype == DT_F16)
-        attn_bias_reduce_kernel<DT_F16><<<grid, 256, 0, s>>>(p.bias_part, p.n_items, p.s.H, p.s.buckets, grad_bias);
+        attn_bias_reduce_kernel<DT_F16><<<grid, 256, 0, s>>>(p.bias_part, p.n_items, p.max_items, far, p.s.H, p.s.buckets,
+                                                               grad_bias);
     else
-        attn_bias_reduce_kernel<DT_BF16><<<grid, 256, 0, s>>>(p.bias_part, p.n_items, p.s.H, p.s.buckets, grad_bias);
+        attn_bias_reduce_kernel<DT_BF16><<<grid, 256, 0, s>>>(p.bias_part, p.n_items, p.max_items, far, p.s.H, p.s.buckets,
+                                                               grad_bias);
     return cudaGetLastError();
 }
 

@@ -78,6 +78,14 @@ def test_long_history_with_window_and_sinks(dtype):
     Batch(dtype, 2, 1, 64, [1900, 40], 150, 9, tbe.tbe_relative_buckets(32, 150), seed=3).check()
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("dim,sinks", [(64, 5), (64, 128), (128, 40)])
+def test_sinks_seen_by_many_queries(dtype, dim, sinks):
+    """Histories long enough that the first tile's far queries are work items
+    of their own, joined; others in the batch are not split."""
+    Batch(dtype, 2, 1, dim, [2500, 50, 0, 5000, 300], 70, sinks, [0, 1, 9, 60, 2000], seed=31).check()
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("dim", [64, 128])
 def test_long_full_history(dtype, dim):
