@@ -430,60 +430,65 @@ def tbe_attention_destroy(h: AttentionHandle):
     h.close()
 
 
+# The calls below are made once per request by a serving loop: their checks
+# use few Python objects (addresses as ints, torch.Size compared as it is).
+
+def _refuse(name: str, t: torch.Tensor, shape, dtype) -> None:
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected {list(shape)}, got {list(t.shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    raise ValueError(f"{name}: the last dimension must be contiguous")
+
+
 def _rows(h: AttentionHandle, t: torch.Tensor, tokens: int, heads: int, name: str) -> _Rows:
-    if tuple(t.shape) != (tokens, heads, h.head_dim):
-        raise ValueError(f"{name}: expected [{tokens}, {heads}, {h.head_dim}], got {list(t.shape)}")
-    if t.dtype != h.dtype:
-        raise ValueError(f"{name}: expected {h.dtype}, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError("expected a CUDA tensor")
-    st = t.stride()
-    if st[2] != 1 and h.head_dim > 1:
-        raise ValueError(f"{name}: the last dimension must be contiguous")
-    return _Rows(t.data_ptr(), st[0], st[1])
+    d = h.head_dim
+    if t.shape != (tokens, heads, d) or t.dtype is not h.dtype or not t.is_cuda:
+        _refuse(name, t, (tokens, heads, d), h.dtype)
+    s0, s1, s2 = t.stride()
+    if s2 != 1 and d > 1:
+        _refuse(name, t, t.shape, t.dtype)
+    return _Rows(t.data_ptr(), s0, s1)
 
 
-def _pages(h: AttentionHandle, t: torch.Tensor, name: str) -> _Pages:
-    if t.dim() != 4 or t.shape[2] != h.kv_heads or t.shape[3] != h.head_dim:
-        raise ValueError(f"{name}: expected [pages, page size, {h.kv_heads}, {h.head_dim}], got {list(t.shape)}")
-    if t.dtype != h.dtype:
-        raise ValueError(f"{name}: expected {h.dtype}, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError("expected a CUDA tensor")
-    st = t.stride()
-    if st[3] != 1 and h.head_dim > 1:
-        raise ValueError(f"{name}: the last dimension must be contiguous")
-    return _Pages(t.data_ptr(), st[0], st[1], st[2])
+def _pages(h: AttentionHandle, t: torch.Tensor, shape, name: str) -> _Pages:
+    if t.shape != shape or t.dtype is not h.dtype or not t.is_cuda:
+        _refuse(name, t, shape, h.dtype)
+    s0, s1, s2, s3 = t.stride()
+    if s3 != 1 and h.head_dim > 1:
+        _refuse(name, t, t.shape, t.dtype)
+    return _Pages(t.data_ptr(), s0, s1, s2)
+
+
+def _packed(t: torch.Tensor, shape, dtype, name: str) -> int:
+    """Address of a contiguous CUDA tensor of this shape and type."""
+    if t.shape != shape or t.dtype is not dtype or not t.is_cuda:
+        _refuse(name, t, shape, dtype)
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor")
+    return t.data_ptr()
+
+
+def _space(t: torch.Tensor) -> int:
+    if not t.is_cuda or not t.is_contiguous() or t.dtype is not torch.uint8:
+        raise ValueError("workspace: expected a contiguous CUDA tensor of bytes")
+    return t.data_ptr()
 
 
 def _bias(h: AttentionHandle, bias: Optional[torch.Tensor]):
     if (bias is None) != (h.buckets == 0):
         raise ValueError("bias must be given exactly where the handle has buckets")
-    if bias is None:
-        return None
-    if tuple(bias.shape) != (h.buckets, h.heads) or bias.dtype != h.dtype:
-        raise ValueError(f"bias: expected {h.dtype} [{h.buckets}, {h.heads}]")
-    return _ptr(bias)
+    return None if bias is None else _packed(bias, (h.buckets, h.heads), h.dtype, "bias")
 
 
-def _offsets(offsets: torch.Tensor) -> int:
-    if offsets.dim() != 1 or offsets.numel() < 1 or offsets.dtype not in (torch.int32, torch.int64):
+def _offsets(offsets: torch.Tensor):
+    """(address, index type, histories) of B+1 offsets."""
+    if offsets.dim() != 1 or offsets.shape[0] < 1 or offsets.dtype not in (torch.int32, torch.int64):
         raise ValueError("offsets must be a 1-D int32 or int64 tensor of B+1 entries")
-    return TBE_I64 if offsets.dtype == torch.int64 else TBE_I32
-
-
-def _result(t: Optional[torch.Tensor], shape, dtype, device, name: str) -> torch.Tensor:
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
-        raise ValueError(f"{name}: expected {dtype} {list(shape)}")
-    return t
-
-
-def _int32(t: torch.Tensor, shape, name: str):
-    if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: expected int32 {list(shape)}")
-    return _ptr(t)
+    at = _packed(offsets, offsets.shape, offsets.dtype, "offsets")
+    return at, TBE_I64 if offsets.dtype is torch.int64 else TBE_I32, offsets.shape[0] - 1
 
 
 def tbe_attention_workspace_bytes(h: AttentionHandle, num_tokens: int, batch_size: int,
@@ -506,15 +511,19 @@ def tbe_attention_forward(h: AttentionHandle, q: torch.Tensor, k: torch.Tensor, 
                           workspace: Optional[torch.Tensor] = None, stream=None):
     """q [N, H, D], k and v [N, Hk, D] of the batch's histories (strided rows
     are fine), offsets [B+1]; returns (out [N, H, D], lse [H, N])."""
-    n, b = int(q.shape[0]), offsets.numel() - 1
-    rq, rk, rv = _rows(h, q, n, h.heads, "q"), _rows(h, k, n, h.kv_heads, "k"), _rows(h, v, n, h.kv_heads, "v")
-    it, pb = _offsets(offsets), _bias(h, bias)
-    out = _result(out, (n, h.heads, h.head_dim), h.dtype, q.device, "out")
-    lse = _result(lse, (h.heads, n), torch.float32, q.device, "lse")
+    n, heads = q.shape[0], h.heads
+    rq, rk, rv = _rows(h, q, n, heads, "q"), _rows(h, k, n, h.kv_heads, "k"), _rows(h, v, n, h.kv_heads, "v")
+    po, it, b = _offsets(offsets)
+    shape = (n, heads, h.head_dim)
+    if out is None:
+        out = torch.empty(shape, dtype=h.dtype, device=q.device)
+    if lse is None:
+        lse = torch.empty((heads, n), dtype=torch.float32, device=q.device)
     if workspace is None:
         workspace = make_attention_workspace(h, n, b, False, q.device)
-    rc = load_library().tbe_attention_forward(h.ptr, rq, rk, rv, pb, _ptr(offsets), it, n, b, _ptr(out), _ptr(lse),
-                                              _ptr(workspace), workspace.numel(), _stream(stream))
+    rc = load_library().tbe_attention_forward(
+        h.ptr, rq, rk, rv, _bias(h, bias), po, it, n, b, _packed(out, shape, h.dtype, "out"),
+        _packed(lse, (heads, n), torch.float32, "lse"), _space(workspace), workspace.numel(), _stream(stream))
     _check(rc, "tbe_attention_forward")
     return out, lse
 
@@ -527,36 +536,42 @@ def tbe_attention_backward(h: AttentionHandle, q: torch.Tensor, k: torch.Tensor,
                            stream=None):
     """Gradients (grad_q, grad_k, grad_v, grad_bias) from a forward call's out
     and lse and the upstream gradient; grad_bias is None without buckets."""
-    n, b, d = int(q.shape[0]), offsets.numel() - 1, h.head_dim
-    rq, rk, rv = _rows(h, q, n, h.heads, "q"), _rows(h, k, n, h.kv_heads, "k"), _rows(h, v, n, h.kv_heads, "v")
-    rg = _rows(h, grad_out, n, h.heads, "grad_out")
-    it, pb = _offsets(offsets), _bias(h, bias)
-    _result(out, (n, h.heads, d), h.dtype, q.device, "out")
-    _result(lse, (h.heads, n), torch.float32, q.device, "lse")
-    grad_q = _result(grad_q, (n, h.heads, d), h.dtype, q.device, "grad_q")
-    grad_k = _result(grad_k, (n, h.kv_heads, d), h.dtype, q.device, "grad_k")
-    grad_v = _result(grad_v, (n, h.kv_heads, d), h.dtype, q.device, "grad_v")
+    n, heads, kv, d, dt = q.shape[0], h.heads, h.kv_heads, h.head_dim, h.dtype
+    rq, rk, rv = _rows(h, q, n, heads, "q"), _rows(h, k, n, kv, "k"), _rows(h, v, n, kv, "v")
+    rg = _rows(h, grad_out, n, heads, "grad_out")
+    po, it, b = _offsets(offsets)
+    if grad_q is None:
+        grad_q = torch.empty((n, heads, d), dtype=dt, device=q.device)
+    if grad_k is None:
+        grad_k = torch.empty((n, kv, d), dtype=dt, device=q.device)
+    if grad_v is None:
+        grad_v = torch.empty((n, kv, d), dtype=dt, device=q.device)
+    pb = None
     if h.buckets:
-        grad_bias = _result(grad_bias, (h.buckets, h.heads), h.dtype, q.device, "grad_bias")
+        if grad_bias is None:
+            grad_bias = torch.empty((h.buckets, heads), dtype=dt, device=q.device)
+        pb = _packed(grad_bias, (h.buckets, heads), dt, "grad_bias")
     elif grad_bias is not None:
         raise ValueError("grad_bias without buckets")
     if workspace is None:
         workspace = make_attention_workspace(h, n, b, True, q.device)
     rc = load_library().tbe_attention_backward(
-        h.ptr, rq, rk, rv, pb, _ptr(offsets), it, n, b, _ptr(out), _ptr(lse), rg, _ptr(grad_q), _ptr(grad_k),
-        _ptr(grad_v), _ptr(grad_bias), _ptr(workspace), workspace.numel(), _stream(stream))
+        h.ptr, rq, rk, rv, _bias(h, bias), po, it, n, b, _packed(out, (n, heads, d), dt, "out"),
+        _packed(lse, (heads, n), torch.float32, "lse"), rg, _packed(grad_q, (n, heads, d), dt, "grad_q"),
+        _packed(grad_k, (n, kv, d), dt, "grad_k"), _packed(grad_v, (n, kv, d), dt, "grad_v"), pb, _space(workspace),
+        workspace.numel(), _stream(stream))
     _check(rc, "tbe_attention_backward")
     return grad_q, grad_k, grad_v, grad_bias
 
 
 def _cache(h: AttentionHandle, k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: torch.Tensor, b: int):
-    if k_pages.shape != v_pages.shape:
-        raise ValueError("k_pages and v_pages must have one shape")
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [B, width]")
-    width = int(block_table.shape[1])
-    return (_pages(h, k_pages, "k_pages"), _pages(h, v_pages, "v_pages"), int(k_pages.shape[0]),
-            int(k_pages.shape[1]), _int32(block_table, (b, width), "block_table"), width)
+    if k_pages.dim() != 4 or block_table.dim() != 2:
+        raise ValueError("pages must be [pages, page size, Hk, D], block_table [B, width]")
+    pages, size = k_pages.shape[0], k_pages.shape[1]
+    width = block_table.shape[1]
+    shape = (pages, size, h.kv_heads, h.head_dim)
+    return (_pages(h, k_pages, shape, "k_pages"), _pages(h, v_pages, shape, "v_pages"), pages, size,
+            _packed(block_table, (b, width), torch.int32, "block_table"), width)
 
 
 def tbe_attention_append(h: AttentionHandle, k: torch.Tensor, v: torch.Tensor, offsets: torch.Tensor,
@@ -565,12 +580,13 @@ def tbe_attention_append(h: AttentionHandle, k: torch.Tensor, v: torch.Tensor, o
     """Writes new tokens' keys and values ([N, Hk, D], ragged by offsets) into
     the paged cache ([pages, page size, Hk, D]) behind the ``before`` tokens
     each history holds already; block_table [B, width] names its pages."""
-    n, b = int(k.shape[0]), offsets.numel() - 1
+    n = k.shape[0]
     rk, rv = _rows(h, k, n, h.kv_heads, "k"), _rows(h, v, n, h.kv_heads, "v")
-    it = _offsets(offsets)
+    po, it, b = _offsets(offsets)
     kp, vp, pages, size, table, width = _cache(h, k_pages, v_pages, block_table, b)
-    rc = load_library().tbe_attention_append(h.ptr, rk, rv, _ptr(offsets), it, n, b, _int32(before, (b,), "before"),
-                                             kp, vp, pages, size, table, width, _stream(stream))
+    rc = load_library().tbe_attention_append(
+        h.ptr, rk, rv, po, it, n, b, _packed(before, (b,), torch.int32, "before"), kp, vp, pages, size, table, width,
+        _stream(stream))
     _check(rc, "tbe_attention_append")
 
 
@@ -593,16 +609,17 @@ def tbe_attention_decode(h: AttentionHandle, q: torch.Tensor, k_pages: torch.Ten
     """Attention of each history's newest token (q [B, H, D]) over its paged
     cache of ``lengths`` tokens (the newest included); max_length, an upper
     bound of them, defaults to the block table's room."""
-    b = int(q.shape[0])
-    rq, pb = _rows(h, q, b, h.heads, "q"), _bias(h, bias)
+    b, shape = q.shape[0], q.shape
+    rq = _rows(h, q, b, h.heads, "q")
     kp, vp, pages, size, table, width = _cache(h, k_pages, v_pages, block_table, b)
     most = width * size if max_length is None else int(max_length)
-    out = _result(out, (b, h.heads, h.head_dim), h.dtype, q.device, "out")
+    if out is None:
+        out = torch.empty(shape, dtype=h.dtype, device=q.device)
     if workspace is None:
         workspace = make_attention_decode_workspace(h, b, most, q.device)
-    rc = load_library().tbe_attention_decode(h.ptr, rq, kp, vp, pages, size, table, width,
-                                             _int32(lengths, (b,), "lengths"), b, most, pb, _ptr(out),
-                                             _ptr(workspace), workspace.numel(), _stream(stream))
+    rc = load_library().tbe_attention_decode(
+        h.ptr, rq, kp, vp, pages, size, table, width, _packed(lengths, (b,), torch.int32, "lengths"), b, most,
+        _bias(h, bias), _packed(out, shape, h.dtype, "out"), _space(workspace), workspace.numel(), _stream(stream))
     _check(rc, "tbe_attention_decode")
     return out
 
