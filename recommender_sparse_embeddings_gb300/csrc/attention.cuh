@@ -80,6 +80,77 @@ struct AttnShape {
     uint32_t* error;            // device
 };
 
+// Where a kernel finds its work items: in the list that the items kernel left,
+// or, for a batch of few histories, in the offsets themselves (each warp adds
+// up the histories' tiles; a launch of its own costs more than that).
+constexpr int kScanHistories = 128;
+
+struct ItemSource {
+    const AttnItem* items;
+    const int32_t* n_items;
+    const void* offsets;  // null: the list
+    int64_t N;
+    int32_t index64, B, tile;
+    uint32_t* error;
+};
+
+// Item w of the batch; false if there is none.  All lanes of a warp call it
+// together.
+__device__ __forceinline__ bool find_item(const ItemSource& s, int64_t w, AttnItem& it) {
+    if (!s.offsets) {
+        if (w >= *s.n_items) return false;
+        it = s.items[w];
+        return true;
+    }
+    const int lane = threadIdx.x % 32;
+    int64_t base = 0;
+    for (int b0 = 0; b0 < s.B; b0 += 32) {
+        const int b = b0 + lane;
+        int64_t lo = 0, hi = 0;
+        if (b < s.B) {
+            lo = s.index64 ? static_cast<const int64_t*>(s.offsets)[b] : static_cast<const int32_t*>(s.offsets)[b];
+            hi = s.index64 ? static_cast<const int64_t*>(s.offsets)[b + 1]
+                           : static_cast<const int32_t*>(s.offsets)[b + 1];
+            const bool bad = lo < 0 || hi < lo || hi > s.N;
+            if (bad || (b == 0 && lo != 0) || (b == s.B - 1 && hi != s.N)) atomicOr(s.error, ERR_OFFSETS);
+            if (bad) hi = lo = 0;
+        }
+        const int n = (int)((hi - lo + s.tile - 1) / s.tile);
+        int incl = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int t = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += t;
+        }
+        const uint32_t hit = __ballot_sync(0xffffffffu, w < base + incl);
+        if (hit) {
+            const int k = __ffs(hit) - 1;
+            const int nk = __shfl_sync(0xffffffffu, n, k), ik = __shfl_sync(0xffffffffu, incl, k);
+            const int lk = (int)__shfl_sync(0xffffffffu, lo, k), hk = (int)__shfl_sync(0xffffffffu, hi, k);
+            it = AttnItem{lk, hk - lk, (int)(base + ik - 1 - w), nk};  // the history's last tile first
+            return true;
+        }
+        base += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    return false;
+}
+
+// Items of the batch, by the same rules.
+__device__ __forceinline__ int count_items(const ItemSource& s) {
+    if (!s.offsets) return *s.n_items;
+    const int lane = threadIdx.x % 32;
+    int n = 0;
+    for (int b = lane; b < s.B; b += 32) {
+        const int64_t lo = s.index64 ? static_cast<const int64_t*>(s.offsets)[b] : static_cast<const int32_t*>(s.offsets)[b];
+        const int64_t hi = s.index64 ? static_cast<const int64_t*>(s.offsets)[b + 1]
+                                     : static_cast<const int32_t*>(s.offsets)[b + 1];
+        if (lo >= 0 && hi >= lo && hi <= s.N) n += (int)((hi - lo + s.tile - 1) / s.tile);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+    return n;
+}
+
 struct AttnForward {
     AttnShape s;
     Rows q, k, v;
@@ -87,8 +158,7 @@ struct AttnForward {
     void* out;         // [N, H, D]
     float* lse;        // [H, N]
     int64_t N;
-    const AttnItem* items;
-    const int32_t* n_items;
+    ItemSource src;
     int32_t vec;  // rows are 16-byte aligned and D * element size is a multiple of 16
 };
 
@@ -106,8 +176,7 @@ struct AttnBackward {
     int64_t max_items;
     FarWork far;
     int64_t N;
-    const AttnItem* items;
-    const int32_t* n_items;
+    ItemSource src;
     int32_t vec;
 };
 

@@ -168,6 +168,24 @@ T* at(void* base, size_t offset) {
     return reinterpret_cast<T*>(static_cast<char*>(base) + offset);
 }
 
+// The batch's work items: their source for the kernels, listed by a launch
+// where there are many histories or some are split (or no kernel follows that
+// would check the offsets).
+int make_items(ItemSource* src, const tbe_attention* h, const Layout& L, const void* offsets, int32_t index_dtype,
+               int64_t N, int32_t B, int tile, int64_t most, const FarWork& far, void* workspace, cudaStream_t s) {
+    src->items = at<AttnItem>(workspace, L.items);
+    src->n_items = at<int32_t>(workspace, L.n_items);
+    src->offsets = B <= kScanHistories && far.most == 0 && N > 0 ? offsets : nullptr;
+    src->index64 = index_dtype == TBE_I64;
+    src->N = N;
+    src->B = B;
+    src->tile = tile;
+    src->error = h->s.error;
+    if (src->offsets) return TBE_OK;
+    return status(launch_attn_items(offsets, src->index64, N, B, tile, at<AttnItem>(workspace, L.items), most,
+                                    at<int32_t>(workspace, L.n_items), h->s.error, far, s));
+}
+
 // Rows of a cache that a query sees at most.
 int64_t visible_most(const tbe_attention* h, int64_t max_length) {
     return std::min<int64_t>(max_length, (int64_t)h->s.window + h->s.sinks);
@@ -306,16 +324,13 @@ int tbe_attention_forward(tbe_attention* h, const tbe_rows* q, const tbe_rows* k
     p.out = out;
     p.lse = lse;
     p.N = N;
-    p.items = at<AttnItem>(workspace, L.items);
-    p.n_items = at<int32_t>(workspace, L.n_items);
     p.vec = vec_rows(h, *q) && vec_rows(h, *k) && vec_rows(h, *v) && aligned16(out);
     AttnMaps maps{};
     const bool mma = N > 0 && takes_mma(h, p.vec) && encode_rows(&maps.q, h, *q, h->s.H, N) &&
                      encode_rows(&maps.k, h, *k, h->s.Hk, N) && encode_rows(&maps.v, h, *v, h->s.Hk, N);
     const int tile = mma ? kMmaTile : attn_simt_tile(h->s.D);
     const int64_t most = N / tile + B;
-    rc = status(launch_attn_items(offsets, index_dtype == TBE_I64, N, B, tile, at<AttnItem>(workspace, L.items), most,
-                                  at<int32_t>(workspace, L.n_items), h->s.error, FarWork{}, s));
+    rc = make_items(&p.src, h, L, offsets, index_dtype, N, B, tile, most, FarWork{}, workspace, s);
     if (rc || N == 0) return rc;
     return status(mma ? launch_attn_forward_mma(p, maps, most, s) : launch_attn_forward_simt(p, most, s));
 }
@@ -349,8 +364,6 @@ int tbe_attention_backward(tbe_attention* h, const tbe_rows* q, const tbe_rows* 
     p.delta = at<float>(workspace, L.delta);
     p.bias_part = at<float>(workspace, L.bias_part);
     p.N = N;
-    p.items = at<AttnItem>(workspace, L.items);
-    p.n_items = at<int32_t>(workspace, L.n_items);
     p.vec = vec_rows(h, *q) && vec_rows(h, *k) && vec_rows(h, *v) && vec_rows(h, *grad_out) && aligned16(out) &&
             aligned16(grad_q) && aligned16(grad_k) && aligned16(grad_v);
     AttnMaps maps{};
@@ -367,8 +380,7 @@ int tbe_attention_backward(tbe_attention* h, const tbe_rows* q, const tbe_rows* 
         p.far.slot_of = at<int32_t>(workspace, L.slot_of);
         p.far.part = at<float>(workspace, L.far_part);
     }
-    rc = status(launch_attn_items(offsets, index_dtype == TBE_I64, N, B, tile, at<AttnItem>(workspace, L.items), most,
-                                  at<int32_t>(workspace, L.n_items), h->s.error, p.far, s));
+    rc = make_items(&p.src, h, L, offsets, index_dtype, N, B, tile, most, p.far, workspace, s);
     if (rc) return rc;
     if (N > 0) rc = status(mma ? launch_attn_backward_mma(p, maps, most, s) : launch_attn_backward_simt(p, most, s));
     if (rc || !bias) return rc;

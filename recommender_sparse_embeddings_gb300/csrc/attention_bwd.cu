@@ -188,8 +188,8 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
 
     const int64_t w = blockIdx.x / p.s.H;
     const int head = (int)(blockIdx.x % p.s.H);
-    if (w >= *p.n_items) return;
-    const AttnItem it = p.items[w];
+    AttnItem it;
+    if (!find_item(p.src, w, it)) return;
     const int kvh = head / p.s.G, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int first = it.tile * 128, D = p.s.D, ksteps = (D + 15) / 16;
     const int hi = tmin(first + 127, it.len - 1) / 64 + 1;
@@ -252,7 +252,32 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
             const int64_t at = (int64_t)head * p.N + it.start + i;
             const float x = p.lse[at];
             less = x == -INFINITY ? -INFINITY : -x;  // a row that sees nothing: all its weights 2^-inf
-            delta = p.delta[at];
+            if constexpr (L::kPerSm == 1) {
+                delta = p.delta[at];
+            } else {
+                // the estimate of delta, g . out: half of the columns each warpgroup
+                const int64_t token = (int64_t)it.start + i;
+                const uint16_t* g =
+                    static_cast<const uint16_t*>(p.g.data) + token * p.g.token_stride + head * p.g.head_stride;
+                const uint16_t* o = static_cast<const uint16_t*>(p.out) + (token * p.s.H + head) * D;
+#pragma unroll
+                for (int c = 0; c < 32; c += 8) {
+                    const int col = wg * 32 + c;
+                    if (col >= D) break;
+                    float u[8], v[8];
+                    unpack16<DT>(__ldg(reinterpret_cast<const uint4*>(g + col)), u);
+                    unpack16<DT>(__ldg(reinterpret_cast<const uint4*>(o + col)), v);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) delta = fmaf(u[e], v[e], delta);
+                }
+            }
+        }
+        float* rows = reinterpret_cast<float*>(smem + L::rows);
+        if constexpr (L::kPerSm > 1) {
+            rows[wg * 128 + row] = delta;
+            asm volatile("bar.sync 1, %0;" ::"n"(L::W * 32) : "memory");
+            delta = rows[row] + rows[128 + row];
+            asm volatile("bar.sync 1, %0;" ::"n"(L::W * 32) : "memory");  // read before they are written again
         }
         float sum0 = 0.f, sum1 = 0.f;  // of the row's dS
         for (int n = wg / 2; n < steps; n += NB) {
@@ -329,7 +354,6 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
         if (ok) ok = mbar_wait_tight(&bars.last, 0);
         ok = __all_sync(0xffffffffu, ok);
         // delta - e of the row: all warpgroups' sums (every warp comes here)
-        float* rows = reinterpret_cast<float*>(smem + L::rows);
         rows[wg * 128 + row] = sum0 + sum1;
         asm volatile("bar.sync 1, %0;" ::"n"(L::W * 32) : "memory");
         float over = 0.f;
@@ -384,8 +408,7 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
         blocks = tmin(p.far.blocks, (it.len + 63) / 64 - qb0);
     } else {
         share = turn - p.far.most;
-        if (share >= *p.n_items) return;
-        it = p.items[share];
+        if (!find_item(p.src, share, it)) return;
         const int kt = it.tiles - 1 - it.tile;  // the first tiles are seen most: they start first
         first = kt * 128;
         if (kt == 0 && p.far.most > 0) slot = p.far.slot_of[share];
@@ -664,7 +687,11 @@ __global__ void __launch_bounds__(256) attn_far_join_kernel(const AttnBackward p
 }
 
 // delta_i = g_i . out_i of every (token, head): eight lanes a row, 16 bytes a
-// lane and step.  Memory-bound (each row of g and out is read once).
+// lane and step.  Memory-bound (each row of g and out is read once).  For
+// head_dim > 64 only: there dq runs one CTA per SM and shows every microsecond
+// of its start (long window f16 backward 1082 us with this kernel, 1133 with
+// dq's own loads); with two, dq's own loads save the launch and the pass
+// (train full bf16 337 -> 324).
 template <int DT>
 __global__ void __launch_bounds__(256) attn_delta_kernel(const AttnBackward p) {
     const int64_t r = (int64_t)blockIdx.x * 32 + threadIdx.x / 8;
@@ -691,9 +718,12 @@ __global__ void __launch_bounds__(256) attn_delta_kernel(const AttnBackward p) {
 template <int DT, int DP>
 cudaError_t launch(const AttnBackward& p, const AttnMaps& maps, int64_t max_items, cudaStream_t s) {
     using L = Shape<DP>;
-    attn_delta_kernel<DT><<<(unsigned)((p.N * p.s.H + 31) / 32), 256, 0, s>>>(p);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
+    cudaError_t e = cudaSuccess;
+    if constexpr (L::kPerSm == 1) {
+        attn_delta_kernel<DT><<<(unsigned)((p.N * p.s.H + 31) / 32), 256, 0, s>>>(p);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
     attn_dq_mma_kernel<DT, DP><<<(unsigned)(max_items * p.s.H), L::kThreads, L::dq_bytes, s>>>(p, maps);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;

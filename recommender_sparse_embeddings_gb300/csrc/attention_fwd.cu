@@ -53,8 +53,8 @@ __global__ void __launch_bounds__(kThreads, 2) attn_fwd_mma_kernel(const AttnFor
 
     const int64_t w = blockIdx.x / p.s.H;
     const int head = (int)(blockIdx.x % p.s.H);
-    if (w >= *p.n_items) return;
-    const AttnItem it = p.items[w];
+    AttnItem it;
+    if (!find_item(p.src, w, it)) return;
     const int kvh = head / p.s.G, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int first = it.tile * 128, D = p.s.D;
     const int ksteps = (D + 15) / 16;

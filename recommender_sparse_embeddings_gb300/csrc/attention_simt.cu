@@ -165,8 +165,8 @@ __global__ void __launch_bounds__(kThreads) attn_fwd_simt_kernel(const AttnForwa
     float* bt = ps + Tile<T, DP>::pbytes / 4;
     const int64_t w = blockIdx.x / p.s.H;
     const int head = (int)(blockIdx.x % p.s.H);
-    if (w >= *p.n_items) return;
-    const AttnItem it = p.items[w];
+    AttnItem it;
+    if (!find_item(p.src, w, it)) return;
     const int tx = threadIdx.x % 16, ty = threadIdx.x / 16, kvh = head / p.s.G;
     const int first = it.tile * T;
     const float c2 = p.s.scale * kLog2e;
@@ -261,8 +261,8 @@ __global__ void __launch_bounds__(kThreads) attn_dq_simt_kernel(const AttnBackwa
     float* diag = bt + 2 * T;
     const int64_t w = blockIdx.x / p.s.H;
     const int head = (int)(blockIdx.x % p.s.H);
-    if (w >= *p.n_items) return;
-    const AttnItem it = p.items[w];
+    AttnItem it;
+    if (!find_item(p.src, w, it)) return;
     const int tx = threadIdx.x % 16, ty = threadIdx.x / 16, kvh = head / p.s.G;
     const int first = it.tile * T;
     const float c2 = p.s.scale * kLog2e;
@@ -382,8 +382,8 @@ __global__ void __launch_bounds__(kThreads) attn_dkv_simt_kernel(const AttnBackw
     float* de = ls + T;
     const int64_t w = blockIdx.x / p.s.Hk;
     const int kvh = (int)(blockIdx.x % p.s.Hk);
-    if (w >= *p.n_items) return;
-    const AttnItem it = p.items[w];
+    AttnItem it;
+    if (!find_item(p.src, w, it)) return;
     const int kt = it.tiles - 1 - it.tile;  // the first tiles are seen most: they start first
     const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
     const int first = kt * T;
@@ -544,14 +544,13 @@ __global__ void __launch_bounds__(1024) attn_items_kernel(const I* __restrict__ 
 // warp per (bucket, head), its lanes over the items, then a tree.
 template <int DT>
 __global__ void __launch_bounds__(256) attn_bias_reduce_kernel(const float* __restrict__ part,
-                                                               const int32_t* __restrict__ n_items,
-                                                               int64_t max_items,
+                                                               const ItemSource src, int64_t max_items,
                                                                const int32_t* __restrict__ n_far, int H,
                                                                int buckets, void* grad_bias) {
     const int pair = blockIdx.x * 8 + threadIdx.x / 32, lane = threadIdx.x % 32;
     if (pair >= H * buckets) return;
     const int head = pair / buckets, b = pair % buckets;
-    const int n = *n_items;
+    const int n = count_items(src);
     float t = 0.f;
     for (int w = lane; w < n; w += 32) t += part[((int64_t)w * H + head) * buckets + b];
     const int nf = n_far ? *n_far : 0;
@@ -659,13 +658,13 @@ cudaError_t launch_attn_bias_reduce(const AttnBackward& p, void* grad_bias, cuda
     const int grid = (p.s.H * p.s.buckets + 7) / 8;
     const int32_t* far = p.far.most > 0 ? p.far.n_items : nullptr;
     if (p.s.dtype == DT_F32)
-        attn_bias_reduce_kernel<DT_F32><<<grid, 256, 0, s>>>(p.bias_part, p.n_items, p.max_items, far, p.s.H, p.s.buckets,
+        attn_bias_reduce_kernel<DT_F32><<<grid, 256, 0, s>>>(p.bias_part, p.src, p.max_items, far, p.s.H, p.s.buckets,
                                                                grad_bias);
     else if (p.s.dtype == DT_F16)
-        attn_bias_reduce_kernel<DT_F16><<<grid, 256, 0, s>>>(p.bias_part, p.n_items, p.max_items, far, p.s.H, p.s.buckets,
+        attn_bias_reduce_kernel<DT_F16><<<grid, 256, 0, s>>>(p.bias_part, p.src, p.max_items, far, p.s.H, p.s.buckets,
                                                                grad_bias);
     else
-        attn_bias_reduce_kernel<DT_BF16><<<grid, 256, 0, s>>>(p.bias_part, p.n_items, p.max_items, far, p.s.H, p.s.buckets,
+        attn_bias_reduce_kernel<DT_BF16><<<grid, 256, 0, s>>>(p.bias_part, p.src, p.max_items, far, p.s.H, p.s.buckets,
                                                                grad_bias);
     return cudaGetLastError();
 }
