@@ -45,8 +45,8 @@ struct Shape {
     static constexpr int kBig = 128 * DP * 2;   // a 128-row tile
     static constexpr int kSmall = 64 * DP * 2;  // a 64-row tile
     static constexpr int a = 0, b = kBig, x = 2 * kBig, y = x + kStages * kSmall;
-    static constexpr int table = y + kStages * kSmall;      // bias by distance, 2 x 192 floats
-    static constexpr int stat = table + 2 * 192 * 4;        // dkv: -lse and delta, 2 x 2 x 64 floats
+    static constexpr int table = y + kStages * kSmall;      // bias by distance: all, or 2 x 192 floats
+    static constexpr int stat = table + kWholeEntries * 4;  // dkv: -lse and delta, 2 x 2 x 64 floats
     static constexpr int sums = stat + 2 * 2 * 64 * 4;      // dkv: per warp, a sum per bucket
     static constexpr int diag = sums + W * kMaxBuckets * 4;       // dkv: per warp, 64 diagonals
     static constexpr int rows = sums;                             // dq: a row sum per thread
@@ -208,6 +208,8 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
     const uint32_t tmem = tmem_slot;
     const uint32_t t_dq = tmem + NB * 128, t_r = t_dq + DP;  // S at buf*128, dP at buf*128 + 64
     bool ok = true;
+    float last_bias;
+    const bool whole = keep_whole<DT>(p.s, p.bias, head, last_bias);
 
     if (warp == kHelp) {
         // R += P K, dQ += dS K
@@ -221,7 +223,7 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
                             bars.y_empty, &bars.fix[1], it, steps, lane,
                             [&](int n) { return make_int2(block_of(n) * 64, kvh); });
     } else if (warp == kHelp + 3) {
-        if (p.bias) {
+        if (p.bias && !whole) {
             float* bt = reinterpret_cast<float*>(smem + L::table);
             for (int n = 0; n < steps; ++n) {
                 const int buf = n & 1;
@@ -246,7 +248,9 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
         const int wg = warp / 4, half = wg % 2, q4 = warp % 4, row = q4 * 32 + lane, i = first + row;
         const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
         const float c2 = p.s.scale * kLog2e;
-        const float* bt = reinterpret_cast<const float*>(smem + L::table);
+        float* bt = reinterpret_cast<float*>(smem + L::table);
+        const bool wait_bias = p.bias && !whole;
+        if (p.bias && whole) fill_bias<DT>(bt, p.s, p.bias, head, first + 127, threadIdx.x, L::W * 32);
         float less = -INFINITY, delta = 0.f;
         if (i < it.len) {
             const int64_t at = (int64_t)head * p.N + it.start + i;
@@ -277,22 +281,22 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
             rows[wg * 128 + row] = delta;
             asm volatile("bar.sync 1, %0;" ::"n"(L::W * 32) : "memory");
             delta = rows[row] + rows[128 + row];
-            asm volatile("bar.sync 1, %0;" ::"n"(L::W * 32) : "memory");  // read before they are written again
         }
+        asm volatile("bar.sync 1, %0;" ::"n"(L::W * 32) : "memory");  // the table stands; rows is free again
         float sum0 = 0.f, sum1 = 0.f;  // of the row's dS
         for (int n = wg / 2; n < steps; n += NB) {
             const int buf = n & 1, sb = n % NB;
             const uint32_t t_s = tmem + sb * 128 + lanes;
             ok = mbar_wait_tight(&bars.s_full[sb], (n / NB) & 1);
-            if (ok && p.bias) ok = mbar_wait_tight(&bars.t_full[buf], (n / 2) & 1);
+            if (ok && wait_bias) ok = mbar_wait_tight(&bars.t_full[buf], (n / 2) & 1);
             if (!__all_sync(0xffffffffu, ok)) {
                 ok = false;
                 break;
             }
             tcgen05_after_sync();
             const int key0 = block_of(n) * 64;
-            const bool table = p.bias && several[buf];
-            const float add = less + (p.bias ? same_bias[buf] : 0.f);
+            const bool table = p.bias && (whole ? first - key0 - 63 < p.s.far : several[buf] != 0);
+            const float add = less + (wait_bias ? same_bias[buf] : last_bias);
             // whether the block holds a query whose only key is its own (attn_lone)
             const bool lone = (first == 0 && key0 == 0) || (p.s.window == 1 && p.s.sinks == 0);
             const bool all = key0 + 63 < first && (first + 127 - key0 < p.s.window || key0 + 63 < p.s.sinks);
@@ -303,7 +307,7 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
                 tmem_ld16_pair(t_s + 32 * half + h, t_s + 64 + 32 * half + h, x, y);
                 const int key = key0 + 32 * half + h;
                 if (table) {
-                    const float* b = bt + buf * 192 + row + 63 - 32 * half - h;
+                    const float* b = bt + (whole ? i - key + 127 : buf * 192 + row + 63 - 32 * half - h);
 #pragma unroll
                     for (int c = 0; c < 16; c += 2) {
                         float b0 = b[-c], b1 = b[-c - 1];
@@ -348,7 +352,7 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(&bars.ds_full[sb]);
-                if (p.bias) mbar_arrive(&bars.t_empty[buf]);
+                if (wait_bias) mbar_arrive(&bars.t_empty[buf]);
             }
         }
         if (ok) ok = mbar_wait_tight(&bars.last, 0);
@@ -459,7 +463,13 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
             bool one = true;
             int bucket = 0;
             if (p.bias) {
-                one = spread_bias<DT>(bt + buf * 192, p.s, p.bias, at.y, at.x - first - 127, lane, same, bucket);
+                const int least = at.x - first - 127;
+                if (keep_whole<DT>(p.s, p.bias, at.y, same)) {
+                    one = least >= p.s.far;
+                    bucket = p.s.buckets - 1;
+                } else {
+                    one = spread_bias<DT>(bt + buf * 192, p.s, p.bias, at.y, least, lane, same, bucket);
+                }
             }
 #pragma unroll
             for (int c = lane; c < 64; c += 32) {
@@ -485,6 +495,13 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
         float* mine = sums + warp * kMaxBuckets;
         float* diag = reinterpret_cast<float*>(smem + L::diag) + warp * 64;
         for (int g = 0; g < p.s.G; ++g) {
+            float* bt = reinterpret_cast<float*>(smem + L::table);
+            float last_bias;
+            const bool whole = keep_whole<DT>(p.s, p.bias, kvh * p.s.G + g, last_bias);
+            if (p.bias && whole) {
+                fill_bias<DT>(bt, p.s, p.bias, kvh * p.s.G + g, (qb0 + blocks) * 64 - 1 - first, threadIdx.x, L::W * 32);
+                asm volatile("bar.sync 1, %0;" ::"n"(L::W * 32) : "memory");
+            }
             // the head's blocks, or every other one
             for (int n = g * blocks + (NB == 2 ? (g * blocks + wg / 2) % 2 : 0); n < (g + 1) * blocks && ok; n += NB) {
                 const int buf = n & 1, sb = n % NB;
@@ -511,8 +528,7 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
                     tmem_ld16_pair(t_s + 32 * half + h, t_s + 64 + 32 * half + h, x, y);
                     const int query = q0 + 32 * half + h;
                     if (table) {
-                        const float* b =
-                            reinterpret_cast<const float*>(smem + L::table) + buf * 192 + 127 - row + 32 * half + h;
+                        const float* b = bt + (whole ? query - j + 127 : buf * 192 + 127 - row + 32 * half + h);
 #pragma unroll
                         for (int c = 0; c < 16; c += 4) {
                             const float4 t = *reinterpret_cast<const float4*>(less + h + c);

@@ -7,7 +7,7 @@
 //   O += P V            (P from TMEM, V as stored: its MN-major descriptor)
 // Roles: warps 0-3 softmax (thread = query), warp 4 issues the products,
 // warps 5 and 6 fetch the tiles (TMA), warp 7 spreads the bias over the
-// block's distances.  S has two
+// block's distances where the table of all distances is too large to keep.  S has two
 // buffers, so the next block's scores are computed while this one's softmax
 // runs; P takes its S's place.  Two CTAs share an SM (256 TMEM columns each)
 // and fill each other's gaps.
@@ -33,7 +33,7 @@ struct Fwd {
     static constexpr int kTile = 64 * DP * 2;  // bytes of a K or V tile
     static constexpr int kQ = 128 * DP * 2;
     static constexpr int q = 0, k = kQ, v = k + kStages * kTile, bias = v + kStages * kTile;
-    static constexpr int bytes = bias + 2 * 192 * 4 + 1024;  // 1024: the swizzle's alignment
+    static constexpr int bytes = bias + kWholeEntries * 4 + 1024;  // 1024: the swizzle's alignment
     static constexpr int cols = 256;
 };
 
@@ -95,6 +95,8 @@ __global__ void __launch_bounds__(kThreads, 2) attn_fwd_mma_kernel(const AttnFor
     const uint32_t tmem = tmem_slot;
     const uint32_t t_o = tmem + 128;  // S0 and S1 at columns 0 and 64
     bool ok = true;
+    float last_bias;
+    const bool whole = keep_whole<DT>(p.s, p.bias, head, last_bias);
     if (warp == 5 || warp == 6) {
         // ---- loaders: warp 5 Q and K, warp 6 V
         uint32_t fix_phase = 0;
@@ -109,7 +111,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_fwd_mma_kernel(const AttnFor
     } else if (warp == 7) {
         // ---- bias by distance: entry x of the block's table is the bias at
         // distance base + x - 63, x in [0, 191)
-        if (p.bias) {
+        if (p.bias && !whole) {
             float* bt = reinterpret_cast<float*>(smem + L::bias);
             for (int n = 0; n < steps && ok; ++n) {
                 const int buf = n & 1;
@@ -184,12 +186,17 @@ __global__ void __launch_bounds__(kThreads, 2) attn_fwd_mma_kernel(const AttnFor
         const uint32_t lanes = (uint32_t)(warp * 32) << 16;
         const float c2 = p.s.scale * kLog2e;
         const float* bt = reinterpret_cast<const float*>(smem + L::bias);
+        if (p.bias && whole) {
+            fill_bias<DT>(reinterpret_cast<float*>(smem + L::bias), p.s, p.bias, head, first + 127, row, 128);
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+        }
+        const bool wait_bias = p.bias && !whole;
         float m = -INFINITY, l0 = 0.f, l1 = 0.f;
         for (int n = 0; n < steps; ++n) {
             const int buf = n & 1;
             const uint32_t t_s = tmem + buf * 64 + lanes;
             ok = mbar_wait_tight(&bars.s_full[buf], (n / 2) & 1);
-            if (ok && p.bias) ok = mbar_wait_tight(&bars.b_full[buf], (n / 2) & 1);
+            if (ok && wait_bias) ok = mbar_wait_tight(&bars.b_full[buf], (n / 2) & 1);
             // products up to n - 2 have completed (their P's place is S(n)'s,
             // which is full); n - 1 is waited for where O is touched
             if (!__all_sync(0xffffffffu, ok)) {
@@ -202,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_fwd_mma_kernel(const AttnFor
             tmem_ld32_issue(t_s + 32, x + 32);
             tmem_wait_ld(x, 64);
             const int key0 = block_of(n) * 64;
-            const bool table = p.bias && !is_uniform[buf];
+            const bool table = p.bias && (whole ? first - key0 - 63 < p.s.far : !is_uniform[buf]);
             // a block needs masks unless all its pairs are visible
             const bool all = key0 + 63 <= first && (first + 127 - key0 < p.s.window || key0 + 63 < p.s.sinks);
             if (!all) {
@@ -218,15 +225,15 @@ __global__ void __launch_bounds__(kThreads, 2) attn_fwd_mma_kernel(const AttnFor
             // logit = x * by + add: with a table it is formed here, else (one
             // bias for the block, and c2 > 0) the maximum is taken of the raw
             // products and one multiply-add before ex2 does it all
-            float by = c2, add = p.bias ? uniform_bias[buf] : 0.f;
+            float by = c2, add = wait_bias ? uniform_bias[buf] : last_bias;
             if (table) {
-                const float* b = bt + buf * 192 + row + 63;
+                const float* b = bt + (whole ? i - key0 + 127 : buf * 192 + row + 63);
 #pragma unroll
                 for (int c = 0; c < 64; c += 2) fma2(x[c], x[c + 1], c2, b[-c], b[-c - 1]);
                 by = 1.f;
                 add = 0.f;
             }
-            if (p.bias) {
+            if (wait_bias) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars.b_empty[buf]);
             }

@@ -15,12 +15,21 @@
 
 namespace tbe {
 
-// Bounded wait without a sleep between the tries: each try may suspend the
-// thread up to the hint (about 2 us), so 2^20 tries end within seconds.
+// Bounded wait: a plain test first (a phase that has completed is the usual
+// case), then tries that may each suspend the thread up to the hint (about 2
+// us), so 2^20 of them end within seconds.
 __device__ __forceinline__ bool mbar_wait_tight(uint64_t* bar, uint32_t parity) {
     const uint32_t a = smem_u32(bar);
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(a), "r"(parity)
+        : "memory");
+    if (ok) return true;
     for (int i = 0; i < kSpinLimit; ++i) {
-        uint32_t ok;
         asm volatile(
             "{\n\t.reg .pred p;\n\t"
             "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
@@ -31,6 +40,36 @@ __device__ __forceinline__ bool mbar_wait_tight(uint64_t* bar, uint32_t parity) 
         if (ok) return true;
     }
     return false;
+}
+
+// The bias of every distance in shared memory, in base 2: entry x belongs to
+// distance x - 127, for distances up to `far` and a block's width beyond, or
+// up to `most` where the CTA sees no larger ones.  Kept where `far` is at most
+// kWholeFar (9 KB); filling it once per CTA (and head) is hidden behind the
+// first tiles' fetch, where a table per block by one warp held up every block
+// that had several buckets (long window f16: 280 us forward, the softmax
+// waiting 1500 to 2300 of its 3900 cycles a block).
+constexpr int kWholeFar = 2047;
+constexpr int kWholeEntries = kWholeFar + 191 + 127 + 3;
+
+template <int DT>
+__device__ __forceinline__ void fill_bias(float* table, const AttnShape& s, const void* bias, int head, int most,
+                                          int thread, int threads) {
+    const int n = tmin(s.far + 190, most) + 128;
+#pragma unroll 4
+    for (int x = thread; x < n; x += threads) {
+        const int d = x - 127;
+        table[x] = d >= 0 ? bias_base2(load_elem<DT>(bias, (int64_t)attn_bucket(s, d) * s.H + head)) : 0.f;
+    }
+}
+
+// The last bucket's bias, and whether the table is kept: a bias that swallows
+// the logits (a type's lowest value) does so in a table's addition only, and
+// the blocks beyond `far` have none.
+template <int DT>
+__device__ __forceinline__ bool keep_whole(const AttnShape& s, const void* bias, int head, float& last) {
+    last = bias ? bias_base2(load_elem<DT>(bias, (int64_t)(s.buckets - 1) * s.H + head)) : 0.f;
+    return s.far <= kWholeFar && (last > -1e30f || last == -INFINITY);
 }
 
 // Descriptor of an MN-major operand in the tile layout: 8-row groups (along

@@ -59,6 +59,8 @@ class Batch:
     (64, 70, tuple(range(0, 200, 3))),
     (128, 128, [0, 64, 128]),
     (200, 1, None),
+    (0, 0, [0, 1, 2, 5, 40, 150, 5000]),
+    (90, 7, [0, 64, 2048]),
 ])
 def test_masks_and_bias(dtype, window, sinks, starts):
     Batch(dtype, 2, 1, 64, LENGTHS, window, sinks, list(starts) if starts else None).check()
