@@ -58,7 +58,7 @@ struct Shape {
 
 struct Bars {
     uint64_t big_full, fix[2], x_full[3], x_empty[3], y_full[3], y_empty[3], s_full[2], ds_full[2], t_full[2], t_empty[2],
-        v_done, k_done, last;
+        p_done, ds_done, last;
 };
 
 template <int NB>
@@ -77,8 +77,8 @@ __device__ __forceinline__ void init_bars(Bars& b) {
         mbar_init(&b.t_empty[i], 8);
         mbar_init(&b.fix[i], 1);
     }
-    mbar_init(&b.v_done, 1);
-    mbar_init(&b.k_done, 1);
+    mbar_init(&b.p_done, 1);
+    mbar_init(&b.ds_done, 1);
     mbar_init(&b.last, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_proxy_async_smem();
@@ -97,7 +97,9 @@ __device__ __forceinline__ bool run_loader(unsigned char* big, const TileMap& bi
 
 // The product warp of both kernels.  Per block n: S = A X^T and dP = B Y^T
 // into its buffer; once P and dS stand there, first += P Z and second += dS X,
-// where Z is X (dq) or Y (dkv).
+// where Z is X (dq) or Y (dkv).  Block n + NB's scores overwrite P and dS, so
+// each waits for its product; the next tiles' wait and the first product's
+// are hidden behind the second product, the second's behind S.
 template <int DT, int DP, bool ZisX>
 __device__ __forceinline__ bool run_products(Bars& bars, uint32_t sbase, uint32_t tmem, uint32_t t_first,
                                              uint32_t t_second, int ksteps, int steps) {
@@ -114,43 +116,50 @@ __device__ __forceinline__ bool run_products(Bars& bars, uint32_t sbase, uint32_
         tcgen05_after_sync();
         return all;
     };
-    // S (which = 0) or dP (which = 1) of block n
-    auto score = [&](int n, int which) {
+    auto tiles_in = [&](int n) {
+        return wait(&bars.x_full[n % L::kStages], n / L::kStages) && wait(&bars.y_full[n % L::kStages], n / L::kStages);
+    };
+    auto issue_dp = [&](int n) {
         const int st = n % L::kStages;
-        if (!wait(which ? &bars.y_full[st] : &bars.x_full[st], n / L::kStages)) return false;
-        if (elect_one()) {
-            issue_scores<DP>(tmem + (n % NB) * 128 + which * 64, which ? db : da,
-                             (which ? dy : dx) + st * (L::kSmall / 16), id_s, ksteps);
-            if (which) {
-                if (ZisX && n + L::kStages < steps) mma_commit(&bars.y_empty[st]);
-                mma_commit(&bars.s_full[n % NB]);
-            }
-        }
-        __syncwarp();
-        return true;
+        issue_scores<DP>(tmem + (n % NB) * 128 + 64, db, dy + st * (L::kSmall / 16), id_s, ksteps);
+        if (ZisX && n + L::kStages < steps) mma_commit(&bars.y_empty[st]);
+        mma_commit(&bars.s_full[n % NB]);
+    };
+    auto issue_s = [&](int n) {
+        issue_scores<DP>(tmem + (n % NB) * 128, da, dx + n % L::kStages * (L::kSmall / 16), id_s, ksteps);
     };
     if (!wait(&bars.big_full, 0)) return false;
-    for (int n = 0; n < NB && n < steps; ++n)
-        if (!score(n, 0) || !score(n, 1)) return false;
+    for (int n = 0; n < NB && n < steps; ++n) {
+        if (!tiles_in(n)) return false;
+        if (elect_one()) {
+            issue_s(n);
+            issue_dp(n);
+        }
+        __syncwarp();
+    }
     for (int n = 0; n < steps; ++n) {
         const int st = n % L::kStages;
         const uint32_t t = tmem + (n % NB) * 128;
+        const bool more = n + NB < steps;
         if (!wait(&bars.ds_full[n % NB], n / NB)) return false;
         if (elect_one()) {
             issue_product<16>(t_first, t, (ZisX ? mx : my) + st * (L::kSmall / 16), id_o, n > 0);
             if (!ZisX && n + L::kStages < steps) mma_commit(&bars.y_empty[st]);
-            if (n + NB < steps) mma_commit(&bars.v_done);
+            if (more) mma_commit(&bars.p_done);
             issue_product<16>(t_second, t + 64, mx + st * (L::kSmall / 16), id_o, n > 0);
             if (n + L::kStages < steps) mma_commit(&bars.x_empty[st]);
-            if (n + NB < steps) mma_commit(&bars.k_done);
+            if (more) mma_commit(&bars.ds_done);
             if (n + 1 == steps) mma_commit(&bars.last);
         }
         __syncwarp();
-        // block n + NB's scores overwrite P and dS: each waits for its
-        // product, the first under the second's cover
-        if (n + NB < steps &&
-            !(wait(&bars.v_done, n) && score(n + NB, 0) && wait(&bars.k_done, n) && score(n + NB, 1)))
-            return false;
+        if (more) {
+            if (!tiles_in(n + NB) || !wait(&bars.p_done, n)) return false;
+            if (elect_one()) issue_s(n + NB);
+            __syncwarp();
+            if (!wait(&bars.ds_done, n)) return false;
+            if (elect_one()) issue_dp(n + NB);
+            __syncwarp();
+        }
     }
     return true;
 }
