@@ -527,6 +527,21 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
                 const int bucket = same_bucket[buf];
                 const bool table = bucket < 0;
                 float sum0 = 0.f, sum1 = 0.f, run = 0.f;
+                // the warp's 32 x 32 pairs have 63 distances from `least` on: of
+                // one bucket, of two (cut at column `cut` of the lane's row), or
+                // of more.  Telling them apart pays where one CTA has the SM
+                // (long window f16 backward 974 -> 932 us, its wide buckets
+                // mostly one or two a warp); with two CTAs the longer code
+                // costs more (train full bf16 320 -> 338), so there a block of
+                // several buckets takes the general way.
+                constexpr bool kTell = L::kPerSm == 1;
+                const int least = q0 + 32 * half - first - 32 * q4 - 31;
+                int low = bucket, high = table ? bucket + 2 : bucket, cut = 0;
+                if (kTell && table) {
+                    low = attn_bucket(p.s, tmax(0, least));
+                    high = attn_bucket(p.s, tmax(0, least + 62));
+                    if (high > low) cut = __ldg(p.s.starts + high) - (least + 31 - lane);
+                }
                 const bool all = q0 > first + 127 && (q0 + 63 - first < p.s.window || first + 127 < p.s.sinks);
                 // whether the block holds a query whose only key is its own (attn_lone)
                 const bool lone = !all && (q0 == 0 || (p.s.window == 1 && p.s.sinks == 0));
@@ -582,19 +597,26 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
                     }
 #pragma unroll
                     for (int c = 0; c < 16; c += 2) dk[(h + c) / 2] = pack2<DT>(y[c], y[c + 1]);
-                    if (table) {
-                        // the lane's column c has distance c - lane (plus the
-                        // block's): a diagonal's sum moves one lane up a column
-                        // and is complete at lane 31
+                    if (p.bias && high == low) {
+#pragma unroll
+                        for (int c = 0; c < 16; c += 2) add2(sum0, sum1, y[c], y[c + 1]);
+                    } else if (kTell && p.bias && high - low == 1) {
+#pragma unroll
+                        for (int c = 0; c < 16; ++c)
+                            if (h + c >= cut)
+                                run += y[c];
+                            else
+                                sum0 += y[c];
+                    } else if (p.bias) {
+                        // column c has distance least + 31 - lane + c: a
+                        // diagonal's sum moves one lane up a column and is
+                        // complete at lane 31
 #pragma unroll
                         for (int c = 0; c < 16; ++c) {
                             const float t = __shfl_up_sync(0xffffffffu, run, 1);
                             run = y[c] + (lane == 0 ? 0.f : t);
                             if (lane == 31) diag[h + c] = run;
                         }
-                    } else if (p.bias) {
-#pragma unroll
-                        for (int c = 0; c < 16; c += 2) add2(sum0, sum1, y[c], y[c + 1]);
                     }
                 }
                 // P^T and dS^T into the columns of S^T and dP^T that this thread
@@ -608,16 +630,28 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
                     mbar_arrive(&bars.ds_full[sb]);
                     mbar_arrive(&bars.t_empty[buf]);
                 }
-                if (table) {
-                    // diag[x], x in [0, 63): distance q0 + 32 half - first - 32 q4
-                    // + x - 31; the last column's running sums are the highest 32
+                if (p.bias && (high == low || (kTell && high - low == 1))) {
+                    float t = sum0 + sum1;  // the lower bucket's
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) {
+                        t += __shfl_xor_sync(0xffffffffu, t, o);
+                        if (kTell && high > low) run += __shfl_xor_sync(0xffffffffu, run, o);
+                    }
+                    if (lane == 0) {
+                        mine[low] += t;
+                        if (kTell && high > low) mine[high] += run;
+                    }
+                    __syncwarp();
+                } else if (p.bias) {
+                    // diag[x], x in [0, 63): distance least + x; the last
+                    // column's running sums are the highest 32
                     if (lane < 31) diag[62 - lane] = run;
                     __syncwarp();
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
                         // sums of equal buckets, which are neighbours: a segmented
                         // scan over 32 distances, added by each segment's last lane
-                        const int at = r * 32 + lane, d = q0 + 32 * half - first - 32 * q4 + at - 31;
+                        const int at = r * 32 + lane, d = least + at;
                         const int b = at < 63 && d >= 0 ? attn_bucket(p.s, d) : -1;
                         float t = b >= 0 ? diag[at] : 0.f;
 #pragma unroll
@@ -630,12 +664,6 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
                         if (b >= 0 && (lane == 31 || next != b)) mine[b] += t;
                         __syncwarp();
                     }
-                } else if (p.bias) {
-                    float t = sum0 + sum1;
-#pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-                    if (lane == 0) mine[bucket] += t;
-                    __syncwarp();
                 }
             }
             if (p.bias) {  // the head's share: all warps come here, whatever their waits said
