@@ -294,7 +294,7 @@ cudaError_t launch_attn_bias_reduce(const AttnBackward& p, void* grad_bias, cuda
 cudaError_t launch_attn_append(const AttnAppend& p, cudaStream_t s);
 cudaError_t launch_attn_decode(const AttnDecode& p, cudaStream_t s);
 cudaError_t attn_simt_configure(int optin_smem);
-int attn_simt_tile(int D);
+int attn_simt_tile(int dtype, int D, int H, int64_t N, int64_t B, int num_sms);
 // query heads one decode CTA takes at once
 int attn_decode_heads(int G);
 

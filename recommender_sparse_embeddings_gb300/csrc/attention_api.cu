@@ -136,10 +136,11 @@ FarWork far_split(const tbe_attention* h, int64_t N) {
     return f;
 }
 
-// Laid out for the smallest tile any path of the handle's head_dim takes.
+// Laid out for the smallest tile that any call of the handle takes, so that a
+// workspace serves every smaller batch too.
 Layout make_layout(const tbe_attention* h, int64_t N, int64_t B, bool backward) {
     Layout L{};
-    L.capacity = N / attn_simt_tile(h->s.D) + B;
+    L.capacity = N / (h->s.dtype == TBE_F32 || h->s.D > 128 ? 32 : 64) + B;
     size_t o = 0;
     auto take = [&](size_t bytes) {
         const size_t at = o;
@@ -328,7 +329,7 @@ int tbe_attention_forward(tbe_attention* h, const tbe_rows* q, const tbe_rows* k
     AttnMaps maps{};
     const bool mma = N > 0 && takes_mma(h, p.vec) && encode_rows(&maps.q, h, *q, h->s.H, N) &&
                      encode_rows(&maps.k, h, *k, h->s.Hk, N) && encode_rows(&maps.v, h, *v, h->s.Hk, N);
-    const int tile = mma ? kMmaTile : attn_simt_tile(h->s.D);
+    const int tile = mma ? kMmaTile : attn_simt_tile(h->s.dtype, h->s.D, h->s.H, N, B, h->num_sms);
     const int64_t most = N / tile + B;
     rc = make_items(&p.src, h, L, offsets, index_dtype, N, B, tile, most, FarWork{}, workspace, s);
     if (rc || N == 0) return rc;
@@ -370,7 +371,7 @@ int tbe_attention_backward(tbe_attention* h, const tbe_rows* q, const tbe_rows* 
     const bool mma = N > 0 && takes_mma(h, p.vec) && encode_rows(&maps.q, h, *q, h->s.H, N) &&
                      encode_rows(&maps.k, h, *k, h->s.Hk, N) && encode_rows(&maps.v, h, *v, h->s.Hk, N) &&
                      encode_rows(&maps.g, h, *grad_out, h->s.H, N);
-    const int tile = mma ? kMmaTile : attn_simt_tile(h->s.D);
+    const int tile = mma ? kMmaTile : attn_simt_tile(h->s.dtype, h->s.D, h->s.H, N, B, h->num_sms);
     const int64_t most = N / tile + B;
     p.max_items = most;
     if (mma && L.far.most > 0) {

@@ -600,7 +600,15 @@ cudaError_t backward(const AttnBackward& p, int64_t n, cudaStream_t s) {
 
 }  // namespace
 
-int attn_simt_tile(int D) { return D <= 128 ? 64 : 32; }
+// Tokens a tile.  64 up to head_dim 128, 32 above (the tiles must fit shared
+// memory).  fp32 batches that would leave SMs without a CTA take 32 as well:
+// more and shorter CTAs (40 fp32 histories of 93 tokens, 2 heads: forward and
+// backward 185 us with 64, 152 with 32; 64 histories of 190, 4 heads, which
+// fill the SMs: forward 101 us with 64, 108 with 32).
+int attn_simt_tile(int dtype, int D, int H, int64_t N, int64_t B, int num_sms) {
+    if (D > 128) return 32;
+    return dtype == DT_F32 && (N / 64 + B) * H < 2 * (int64_t)num_sms ? 32 : 64;
+}
 
 cudaError_t attn_simt_configure(int optin) {
     cudaError_t e = cudaSuccess;
@@ -609,6 +617,10 @@ cudaError_t attn_simt_configure(int optin) {
         if (e == cudaSuccess) e = configure<DT, 64, 64>(optin);
         if (e == cudaSuccess) e = configure<DT, 64, 128>(optin);
         if (e == cudaSuccess) e = configure<DT, 32, 256>(optin);
+        if constexpr (DT == DT_F32) {
+            if (e == cudaSuccess) e = configure<DT, 32, 64>(optin);
+            if (e == cudaSuccess) e = configure<DT, 32, 128>(optin);
+        }
     };
     all(std::integral_constant<int, DT_F32>{});
     all(std::integral_constant<int, DT_F16>{});
@@ -618,8 +630,10 @@ cudaError_t attn_simt_configure(int optin) {
 
 #define ATTN_BY_TYPE_AND_DIM(CALL)                                          \
     do {                                                                    \
-        const int D = p.s.D;                                                \
+        const int D = p.s.D, tile = p.src.tile;                             \
         if (p.s.dtype == DT_F32) {                                          \
+            if (D <= 64 && tile == 32) return CALL<DT_F32, 32, 64>(p, max_items, s);   \
+            if (D <= 128 && tile == 32) return CALL<DT_F32, 32, 128>(p, max_items, s); \
             if (D <= 64) return CALL<DT_F32, 64, 64>(p, max_items, s);      \
             if (D <= 128) return CALL<DT_F32, 64, 128>(p, max_items, s);    \
             return CALL<DT_F32, 32, 256>(p, max_items, s);                  \

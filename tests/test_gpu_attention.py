@@ -217,6 +217,16 @@ def test_deterministic_and_reused_workspace(dtype):
             assert torch.equal(x, y)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("dim", [64, 128, 200])
+def test_a_workspace_serves_smaller_batches(dtype, dim):
+    big = tbe.tbe_attention_create(1, 1, dim, dtype, 70, 3, [0, 2])
+    for backward in (False, True):
+        room = tbe.tbe_attention_workspace_bytes(big, 40000, 300, backward)
+        for n, b in ((40000, 1), (39999, 300), (20000, 300), (19000, 10), (9000, 100), (1, 1), (0, 0)):
+            assert 0 < tbe.tbe_attention_workspace_bytes(big, n, b, backward) <= room, (n, b)
+
+
 def test_another_stream():
     b = Batch(torch.bfloat16, 2, 2, 64, [300, 100], 50, 2, [0, 4], seed=13)
     want = b.run()
