@@ -521,7 +521,16 @@ __global__ void __launch_bounds__(1024) attn_items_kernel(const I* __restrict__ 
                     far.items[here + c] = FarItem{(int)lo, (int)(hi - lo), c, chunks, first, {0, 0, 0}};
             }
         }
-        for (int k = 0; k < 32; ++k) {  // the warp writes its histories' items one history after another
+        // short histories' items by their own lanes, a long one's by the warp
+        constexpr int kOwn = 8;
+        const int own = n <= kOwn ? n : 0;
+        for (int t = 0; t < own; ++t)
+            if (at + t < capacity) {
+                items[at + t] = AttnItem{(int)lo, (int)(hi - lo), n - 1 - t, n};
+                if (far.most > 0) far.slot_of[at + t] = slot;
+            }
+        for (uint32_t left = __ballot_sync(0xffffffffu, n > kOwn); left; left &= left - 1) {
+            const int k = __ffs(left) - 1;
             const int nk = __shfl_sync(0xffffffffu, n, k);
             const int64_t ak = __shfl_sync(0xffffffffu, at, k);
             const int sk = (int)__shfl_sync(0xffffffffu, lo, k);
