@@ -159,6 +159,8 @@ struct AttnForward {
     float* lse;        // [H, N]
     int64_t N;
     ItemSource src;
+    int64_t max_items;  // room of the list
+    int32_t ctas;  // > 0: so many CTAs take the items in turn; 0: a CTA per item
     int32_t vec;  // rows are 16-byte aligned and D * element size is a multiple of 16
 };
 
@@ -286,7 +288,7 @@ cudaError_t launch_attn_items(const void* offsets, int index64, int64_t N, int B
                               cudaStream_t s);
 cudaError_t launch_attn_forward_simt(const AttnForward& p, int64_t max_items, cudaStream_t s);
 cudaError_t launch_attn_backward_simt(const AttnBackward& p, int64_t max_items, cudaStream_t s);
-cudaError_t launch_attn_forward_mma(const AttnForward& p, const AttnMaps& maps, int64_t max_items, cudaStream_t s);
+cudaError_t launch_attn_forward_mma(const AttnForward& p, const AttnMaps& maps, cudaStream_t s);
 cudaError_t attn_forward_mma_configure();
 cudaError_t launch_attn_backward_mma(const AttnBackward& p, const AttnMaps& maps, int64_t max_items, cudaStream_t s);
 cudaError_t attn_backward_mma_configure();

@@ -333,7 +333,10 @@ int tbe_attention_forward(tbe_attention* h, const tbe_rows* q, const tbe_rows* k
     const int64_t most = N / tile + B;
     rc = make_items(&p.src, h, L, offsets, index_dtype, N, B, tile, most, FarWork{}, workspace, s);
     if (rc || N == 0) return rc;
-    return status(mma ? launch_attn_forward_mma(p, maps, most, s) : launch_attn_forward_simt(p, most, s));
+    // where the items are listed there are many, often of few blocks each
+    p.max_items = most;
+    p.ctas = p.src.offsets ? 0 : 2 * h->num_sms;
+    return status(mma ? launch_attn_forward_mma(p, maps, s) : launch_attn_forward_simt(p, most, s));
 }
 
 int tbe_attention_backward(tbe_attention* h, const tbe_rows* q, const tbe_rows* k, const tbe_rows* v, const void* bias,

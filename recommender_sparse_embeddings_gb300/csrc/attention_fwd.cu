@@ -16,6 +16,12 @@
 // (kLazy): the weights then stay below 256, exact in fp32 sums and within
 // fp16's range, and the accumulator is rescaled rarely.
 //
+// A batch of many histories has many tiles of few blocks: there two CTAs per SM
+// take the (tile, head) items in turn, so that the next one's tiles are fetched
+// and its first scores computed under the last one's softmax (512 ragged bf16
+// histories 83 -> 73 us).  Few histories get a CTA per item, which the hardware
+// hands out as others end (8 histories of 2048: 73 us, in turn 77).
+//
 // The weights are rounded to the 16-bit type for the second product (the
 // tensor cores' operand type); their sum is kept unrounded in fp32.
 #include "attention_mma.cuh"
@@ -29,20 +35,45 @@ constexpr float kLazy = 8.f;
 
 template <int DP>
 struct Fwd {
-    static constexpr int kStages = DP == 64 ? 4 : 2;
+    static constexpr int kStages = DP == 64 ? 3 : 2;
+    static constexpr int kQs = DP == 64 ? 2 : 1;   // query tiles
     static constexpr int kTile = 64 * DP * 2;  // bytes of a K or V tile
     static constexpr int kQ = 128 * DP * 2;
-    static constexpr int q = 0, k = kQ, v = k + kStages * kTile, bias = v + kStages * kTile;
+    static constexpr int q = 0, k = kQs * kQ, v = k + kStages * kTile, bias = v + kStages * kTile;
     static constexpr int bytes = bias + kWholeEntries * 4 + 1024;  // 1024: the swizzle's alignment
     static constexpr int cols = 256;
 };
 
 struct FwdBars {
-    uint64_t q_full, fix[2], k_full[4], k_empty[4], v_full[4], v_empty[4], s_full[2], p_full[2], o_done, o_last, b_full[2], b_empty[2];
+    uint64_t q_full[2], q_empty[2], fix[2], k_full[3], k_empty[3], v_full[3], v_empty[3], s_full[2], p_full[2], o_done,
+        o_last, o_free, b_full[2], b_empty[2];
 };
 
-template <int DT, int DP>
-__global__ void __launch_bounds__(kThreads, 2) attn_fwd_mma_kernel(const AttnForward p, const __grid_constant__ AttnMaps maps) {
+// One (query tile, head) and the key blocks it sees: [0, sinks) and
+// [lo, lo + steps - sinks).
+struct Turn {
+    AttnItem it;
+    int head, kvh, first, lo, sinks, steps;
+    __device__ __forceinline__ int block(int n) const { return n < sinks ? n : lo + n - sinks; }
+};
+
+__device__ __forceinline__ bool take(const AttnForward& p, int64_t w, Turn& t) {
+    if (!find_item(p.src, w / p.s.H, t.it)) return false;
+    t.head = (int)(w % p.s.H);
+    t.kvh = t.head / p.s.G;
+    t.first = t.it.tile * 128;
+    const int hi = tmin(t.first + 127, t.it.len - 1) / 64 + 1;
+    const int64_t from = (int64_t)t.first - p.s.window + 1;
+    t.lo = from > 0 ? (int)(from / 64) : 0;
+    t.sinks = tmin((p.s.sinks + 63) / 64, t.lo);
+    t.steps = t.sinks + hi - t.lo;
+    return true;
+}
+
+// TURNS: the grid is two CTAs per SM, which take the items in turn.
+template <int DT, int DP, bool TURNS>
+__global__ void __launch_bounds__(kThreads, 2)
+    attn_fwd_mma_kernel(const AttnForward p, const __grid_constant__ AttnMaps maps) {
     using L = Fwd<DP>;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -51,40 +82,39 @@ __global__ void __launch_bounds__(kThreads, 2) attn_fwd_mma_kernel(const AttnFor
     __shared__ float uniform_bias[2];
     __shared__ int is_uniform[2];
 
-    const int64_t w = blockIdx.x / p.s.H;
-    const int head = (int)(blockIdx.x % p.s.H);
-    AttnItem it;
-    if (!find_item(p.src, w, it)) return;
-    const int kvh = head / p.s.G, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int first = it.tile * 128, D = p.s.D;
-    const int ksteps = (D + 15) / 16;
-    // visible key blocks: [0, sink_blocks) and [lo, hi)
-    const int hi = tmin(first + 127, it.len - 1) / 64 + 1;
-    const int64_t from = (int64_t)first - p.s.window + 1;
-    const int lo = from > 0 ? (int)(from / 64) : 0;
-    const int sink_blocks = tmin((p.s.sinks + 63) / 64, lo);
-    const int steps = sink_blocks + hi - lo;
-    auto block_of = [&](int n) { return n < sink_blocks ? n : lo + n - sink_blocks; };
+    int64_t w = blockIdx.x;
+    Turn t;
+    if (!take(p, w, t)) return;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int D = p.s.D, ksteps = (D + 15) / 16;
+    // every role walks the CTA's turns by itself, with its own counts of blocks
+    // and turns: a loader is ahead of the products, the products of the softmax
+    auto more = [&]() {
+        if constexpr (!TURNS) return false;
+        w += gridDim.x;
+        return take(p, w, t);
+    };
 
     const uint32_t sbase = smem_u32(smem);
     if (threadIdx.x == 0) {
-        mbar_init(&bars.q_full, 1);
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 3; ++i) {
             mbar_init(&bars.k_full[i], 1);
             mbar_init(&bars.k_empty[i], 1);
             mbar_init(&bars.v_full[i], 1);
             mbar_init(&bars.v_empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars.q_full[i], 1);
+            mbar_init(&bars.q_empty[i], 4);
+            mbar_init(&bars.fix[i], 1);
             mbar_init(&bars.s_full[i], 1);
             mbar_init(&bars.p_full[i], 4);
             mbar_init(&bars.b_full[i], 1);
             mbar_init(&bars.b_empty[i], 4);
         }
         mbar_init(&bars.o_done, 1);
-        mbar_init(&bars.fix[0], 1);
-        mbar_init(&bars.fix[1], 1);
         mbar_init(&bars.o_last, 1);
+        mbar_init(&bars.o_free, 4);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_proxy_async_smem();
     }
@@ -95,49 +125,64 @@ __global__ void __launch_bounds__(kThreads, 2) attn_fwd_mma_kernel(const AttnFor
     const uint32_t tmem = tmem_slot;
     const uint32_t t_o = tmem + 128;  // S0 and S1 at columns 0 and 64
     bool ok = true;
-    float last_bias;
-    const bool whole = keep_whole<DT>(p.s, p.bias, head, last_bias);
     if (warp == 5 || warp == 6) {
         // ---- loaders: warp 5 Q and K, warp 6 V
         uint32_t fix_phase = 0;
-        auto place = [&](int n) { return make_int2(block_of(n) * 64, kvh); };
-        if (warp == 5)
-            ok = load_tile<128, DP>(smem + L::q, maps.q, it, head, first, &bars.q_full, &bars.fix[0], fix_phase, lane) &&
-                 load_ring<DP, L::kStages>(smem + L::k, maps.k, it, bars.k_full, bars.k_empty, &bars.fix[0], fix_phase,
-                                           steps, lane, place);
-        else
-            ok = load_ring<DP, L::kStages>(smem + L::v, maps.v, it, bars.v_full, bars.v_empty, &bars.fix[1], fix_phase,
-                                           steps, lane, place);
-    } else if (warp == 7) {
-        // ---- bias by distance: entry x of the block's table is the bias at
-        // distance base + x - 63, x in [0, 191)
-        if (p.bias && !whole) {
-            float* bt = reinterpret_cast<float*>(smem + L::bias);
-            for (int n = 0; n < steps && ok; ++n) {
-                const int buf = n & 1;
-                if (n >= 2) ok = mbar_wait_tight(&bars.b_empty[buf], ((n / 2) - 1) & 1);
-                if (!ok) break;
-                const int base = first - block_of(n) * 64;
-                const int least = tmax(0, base - 63), most = base + 127;
-                const int b0 = attn_bucket(p.s, least), b1 = attn_bucket(p.s, tmax(most, 0));
-                const float same = bias_base2(load_elem<DT>(p.bias, (int64_t)b0 * p.s.H + head));
-                // a bias that swallows the logits (a type's lowest value) does
-                // so in the table's addition only
-                const bool one = b0 == b1 && (same > -1e30f || same == -INFINITY);
-                if (lane == 0) {
-                    is_uniform[buf] = one;
-                    uniform_bias[buf] = same;
-                }
-                if (!one)
-                    for (int x = lane; x < 191; x += 32) {
-                        const int d = base + x - 63;
-                        bt[buf * 192 + x] =
-                            d >= 0 ? bias_base2(load_elem<DT>(p.bias, (int64_t)attn_bucket(p.s, d) * p.s.H + head))
-                                   : 0.f;
-                    }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars.b_full[buf]);
+        int done = 0, turn = 0;
+        do {
+            auto place = [&](int n) { return make_int2(t.block(n) * 64, t.kvh); };
+            if (warp == 5) {
+                const int qb = turn % L::kQs;
+                ok = turn < L::kQs || mbar_wait_tight(&bars.q_empty[qb], (turn / L::kQs - 1) & 1);
+                ok = __all_sync(0xffffffffu, ok) &&
+                     load_tile<128, DP>(smem + L::q + qb * L::kQ, maps.q, t.it, t.head, t.first, &bars.q_full[qb],
+                                        &bars.fix[0], fix_phase, lane) &&
+                     load_ring<DP, L::kStages>(smem + L::k, maps.k, t.it, bars.k_full, bars.k_empty, &bars.fix[0],
+                                               fix_phase, t.steps, lane, place, done);
+            } else {
+                ok = load_ring<DP, L::kStages>(smem + L::v, maps.v, t.it, bars.v_full, bars.v_empty, &bars.fix[1],
+                                               fix_phase, t.steps, lane, place, done);
             }
+            done += t.steps;
+            ++turn;
+        } while (ok && more());
+    } else if (warp == 7) {
+        // ---- bias by distance, where the table of all distances is not kept:
+        // entry x of the block's table is the bias at distance base + x - 63,
+        // x in [0, 191)
+        if (p.bias) {
+            float* bt = reinterpret_cast<float*>(smem + L::bias);
+            int done = 0;
+            do {
+                float last;
+                if (keep_whole<DT>(p.s, p.bias, t.head, last)) continue;
+                for (int n = 0; n < t.steps && ok; ++n, ++done) {
+                    const int buf = done & 1;
+                    if (done >= 2) ok = mbar_wait_tight(&bars.b_empty[buf], (done / 2 - 1) & 1);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    const int base = t.first - t.block(n) * 64;
+                    const int least = tmax(0, base - 63), most = base + 127;
+                    const int b0 = attn_bucket(p.s, least), b1 = attn_bucket(p.s, tmax(most, 0));
+                    const float same = bias_base2(load_elem<DT>(p.bias, (int64_t)b0 * p.s.H + t.head));
+                    // a bias that swallows the logits (a type's lowest value)
+                    // does so in the table's addition only
+                    const bool one = b0 == b1 && (same > -1e30f || same == -INFINITY);
+                    if (lane == 0) {
+                        is_uniform[buf] = one;
+                        uniform_bias[buf] = same;
+                    }
+                    if (!one)
+                        for (int x = lane; x < 191; x += 32) {
+                            const int d = base + x - 63;
+                            bt[buf * 192 + x] =
+                                d >= 0 ? bias_base2(load_elem<DT>(p.bias, (int64_t)attn_bucket(p.s, d) * p.s.H + t.head))
+                                       : 0.f;
+                        }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars.b_full[buf]);
+                }
+            } while (ok && more());
         }
     } else if (warp == 4) {
         // ---- products
@@ -145,164 +190,196 @@ __global__ void __launch_bounds__(kThreads, 2) attn_fwd_mma_kernel(const AttnFor
         const uint32_t id_o = mma_idesc(DT == DT_BF16, 128, ksteps * 16) | kMnMajorB;
         const uint64_t dq = smem_desc_sw128(sbase + L::q, 1024), dk = smem_desc_sw128(sbase + L::k, 1024);
         const uint64_t dv = smem_desc_mn(sbase + L::v, 64 * 128);
-        ok = mbar_wait_tight(&bars.q_full, 0);
-        auto scores = [&](int n) {
-            const int st = n % L::kStages;
-            const bool in = mbar_wait_tight(&bars.k_full[st], (n / L::kStages) & 1);
-            if (!__all_sync(0xffffffffu, in)) return false;
+        auto wait = [&](uint64_t* bar, int phase) {
+            const bool in = mbar_wait_tight(bar, phase & 1);
+            const bool all = __all_sync(0xffffffffu, in);
             tcgen05_after_sync();
-            if (elect_one()) {
-                issue_scores<DP>(tmem + (n & 1) * 64, dq, dk + st * (L::kTile / 16), id_s, ksteps);
-                if (n + L::kStages < steps) mma_commit(&bars.k_empty[st]);
-                mma_commit(&bars.s_full[n & 1]);
-            }
-            __syncwarp();
-            return true;
+            return all;
         };
-        ok = __all_sync(0xffffffffu, ok) && scores(0);
-        if (ok && steps > 1) ok = scores(1);
-        for (int n = 0; n < steps && ok; ++n) {
-            const int st = n % L::kStages;
-            ok = mbar_wait_tight(&bars.v_full[st], (n / L::kStages) & 1) &&
-                 mbar_wait_tight(&bars.p_full[n & 1], (n / 2) & 1);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            tcgen05_after_sync();
-            if (elect_one()) {
-                issue_product(t_o, tmem + (n & 1) * 64, dv + st * (L::kTile / 16), id_o, n > 0);
-                if (n + L::kStages < steps) mma_commit(&bars.v_empty[st]);
-                mma_commit(n + 1 < steps ? &bars.o_done : &bars.o_last);
-            }
-            __syncwarp();
-            if (n + 2 < steps) {
+        int g = 0, turn = 0, last = 0;  // blocks before this turn, turns, o_done's phases before this turn
+        do {
+            const int steps = t.steps, qb = turn % L::kQs;
+            auto scores = [&](int n) {
+                const int st = (g + n) % L::kStages;
+                if (!wait(&bars.k_full[st], (g + n) / L::kStages)) return false;
+                if (elect_one()) {
+                    issue_scores<DP>(tmem + ((g + n) & 1) * 64, dq + qb * (L::kQ / 16), dk + st * (L::kTile / 16), id_s,
+                                     ksteps);
+                    mma_commit(&bars.k_empty[st]);
+                    mma_commit(&bars.s_full[(g + n) & 1]);
+                }
+                __syncwarp();
+                return true;
+            };
+            // the first block's scores take the place of the last turn's last
+            // but one weights, the second's of its last; and this turn's O the
+            // last's, once the softmax has read it
+            ok = wait(&bars.q_full[qb], turn / L::kQs) && scores(0) && (turn == 0 || wait(&bars.o_last, turn - 1)) &&
+                 (steps == 1 || scores(1)) && (turn == 0 || wait(&bars.o_free, turn - 1));
+            for (int n = 0; n < steps && ok; ++n) {
+                const int st = (g + n) % L::kStages;
+                ok = wait(&bars.v_full[st], (g + n) / L::kStages) && wait(&bars.p_full[(g + n) & 1], (g + n) / 2);
+                if (!ok) break;
+                if (elect_one()) {
+                    issue_product(t_o, tmem + ((g + n) & 1) * 64, dv + st * (L::kTile / 16), id_o, n > 0);
+                    mma_commit(&bars.v_empty[st]);
+                    mma_commit(n + 1 < steps ? &bars.o_done : &bars.o_last);
+                }
+                __syncwarp();
                 // block n + 2's scores overwrite P(n): wait for its product
-                ok = mbar_wait_tight(&bars.o_done, n & 1);
-                ok = __all_sync(0xffffffffu, ok) && scores(n + 2);
+                if (n + 2 <= steps) ok = wait(&bars.o_done, last + n) && (n + 2 == steps || scores(n + 2));
             }
-        }
+            g += steps;
+            last += steps - 1;
+            ++turn;
+        } while (ok && more());
+        // nothing of this CTA arrives on a barrier after its end
+        if (ok)
+            ok = wait(&bars.k_empty[(g - 1) % L::kStages], (g - 1) / L::kStages) &&
+                 wait(&bars.v_empty[(g - 1) % L::kStages], (g - 1) / L::kStages);
     } else {
         // ---- softmax: thread = query
-        const int row = threadIdx.x, i = first + row;
+        const int row = threadIdx.x;
         const uint32_t lanes = (uint32_t)(warp * 32) << 16;
         const float c2 = p.s.scale * kLog2e;
-        const float* bt = reinterpret_cast<const float*>(smem + L::bias);
-        if (p.bias && whole) {
-            fill_bias<DT>(reinterpret_cast<float*>(smem + L::bias), p.s, p.bias, head, first + 127, row, 128);
-            asm volatile("bar.sync 1, 128;" ::: "memory");
-        }
-        const bool wait_bias = p.bias && !whole;
-        float m = -INFINITY, l0 = 0.f, l1 = 0.f;
-        for (int n = 0; n < steps; ++n) {
-            const int buf = n & 1;
-            const uint32_t t_s = tmem + buf * 64 + lanes;
-            ok = mbar_wait_tight(&bars.s_full[buf], (n / 2) & 1);
-            if (ok && wait_bias) ok = mbar_wait_tight(&bars.b_full[buf], (n / 2) & 1);
-            // products up to n - 2 have completed (their P's place is S(n)'s,
-            // which is full); n - 1 is waited for where O is touched
-            if (!__all_sync(0xffffffffu, ok)) {
-                ok = false;
-                break;
-            }
-            tcgen05_after_sync();
-            float x[64];
-            tmem_ld32_issue(t_s, x);
-            tmem_ld32_issue(t_s + 32, x + 32);
-            tmem_wait_ld(x, 64);
-            const int key0 = block_of(n) * 64;
-            const bool table = p.bias && (whole ? first - key0 - 63 < p.s.far : !is_uniform[buf]);
-            // a block needs masks unless all its pairs are visible
-            const bool all = key0 + 63 <= first && (first + 127 - key0 < p.s.window || key0 + 63 < p.s.sinks);
-            if (!all) {
-                const int up = i - key0 + 1, down = i - p.s.window + 1 - key0, sk = p.s.sinks - key0;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t seen = bits_below(up - 32 * h) & (~bits_below(down - 32 * h) | bits_below(sk - 32 * h));
-#pragma unroll
-                    for (int c = 0; c < 32; ++c)
-                        if (!(seen >> c & 1)) x[32 * h + c] = -INFINITY;
+        float* bt = reinterpret_cast<float*>(smem + L::bias);
+        int g = 0, turn = 0, last = 0, tables = 0, held = -1;  // held: the head whose bias the kept table has
+        float last_bias = 0.f;
+        bool whole = true;
+        do {
+            const int steps = t.steps, first = t.first, i = first + row;
+            if (p.bias && t.head != held) {
+                whole = keep_whole<DT>(p.s, p.bias, t.head, last_bias);
+                if (whole) {
+                    asm volatile("bar.sync 1, 128;" ::: "memory");  // the last table is read
+                    fill_bias<DT>(bt, p.s, p.bias, t.head, TURNS ? INT_MAX / 2 : first + 127, row, 128);
+                    asm volatile("bar.sync 1, 128;" ::: "memory");
                 }
+                held = t.head;
             }
-            // logit = x * by + add: with a table it is formed here, else (one
-            // bias for the block, and c2 > 0) the maximum is taken of the raw
-            // products and one multiply-add before ex2 does it all
-            float by = c2, add = wait_bias ? uniform_bias[buf] : last_bias;
-            if (table) {
-                const float* b = bt + (whole ? i - key0 + 127 : buf * 192 + row + 63);
+            const bool wait_bias = p.bias && !whole;
+            float m = -INFINITY, l0 = 0.f, l1 = 0.f;
+            for (int n = 0; n < steps; ++n) {
+                const int buf = (g + n) & 1, tb = (tables + n) & 1;
+                const uint32_t t_s = tmem + buf * 64 + lanes;
+                ok = mbar_wait_tight(&bars.s_full[buf], ((g + n) / 2) & 1);
+                if (ok && wait_bias) ok = mbar_wait_tight(&bars.b_full[tb], ((tables + n) / 2) & 1);
+                // products up to n - 2 have completed (their P's place is S(n)'s,
+                // which is full); n - 1 is waited for where O is touched
+                if (!__all_sync(0xffffffffu, ok)) {
+                    ok = false;
+                    break;
+                }
+                tcgen05_after_sync();
+                float x[64];
+                tmem_ld32_issue(t_s, x);
+                tmem_ld32_issue(t_s + 32, x + 32);
+                tmem_wait_ld(x, 64);
+                const int key0 = t.block(n) * 64;
+                const bool table = p.bias && (whole ? first - key0 - 63 < p.s.far : !is_uniform[tb]);
+                // a block needs masks unless all its pairs are visible
+                const bool all = key0 + 63 <= first && (first + 127 - key0 < p.s.window || key0 + 63 < p.s.sinks);
+                if (!all) {
+                    const int up = i - key0 + 1, down = i - p.s.window + 1 - key0, sk = p.s.sinks - key0;
 #pragma unroll
-                for (int c = 0; c < 64; c += 2) fma2(x[c], x[c + 1], c2, b[-c], b[-c - 1]);
-                by = 1.f;
-                add = 0.f;
-            }
-            if (wait_bias) {
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t seen = bits_below(up - 32 * h) & (~bits_below(down - 32 * h) | bits_below(sk - 32 * h));
+#pragma unroll
+                        for (int c = 0; c < 32; ++c)
+                            if (!(seen >> c & 1)) x[32 * h + c] = -INFINITY;
+                    }
+                }
+                // logit = x * by + add: with a table it is formed here, else (one
+                // bias for the block, and c2 > 0) the maximum is taken of the raw
+                // products and one multiply-add before ex2 does it all
+                float by = c2, add = wait_bias ? uniform_bias[tb] : last_bias;
+                if (table) {
+                    const float* b = bt + (whole ? i - key0 + 127 : tb * 192 + row + 63);
+#pragma unroll
+                    for (int c = 0; c < 64; c += 2) fma2(x[c], x[c + 1], c2, b[-c], b[-c - 1]);
+                    by = 1.f;
+                    add = 0.f;
+                }
+                if (wait_bias) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars.b_empty[tb]);
+                }
+                float u[8];
+#pragma unroll
+                for (int c = 0; c < 8; ++c) u[c] = max3(x[c], x[c + 8], x[c + 16]);
+#pragma unroll
+                for (int c = 24; c < 56; c += 16)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) u[e] = max3(u[e], x[c + e], x[c + 8 + e]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) u[e] = fmaxf(u[e], x[56 + e]);
+                const float top = fmaf(fmaxf(max3(max3(u[0], u[1], u[2]), u[3], u[4]), max3(u[5], u[6], u[7])), by, add);
+                if (__any_sync(0xffffffffu, top > m + kLazy || m == -INFINITY)) {
+                    const float to = fmaxf(m, top);
+                    const float keep = to == -INFINITY ? 1.f : ex2(m - to);
+                    m = to;
+                    l0 *= keep;
+                    l1 *= keep;
+                    if (n > 0) {
+                        ok = mbar_wait_tight(&bars.o_done, (last + n - 1) & 1);
+                        if (!__all_sync(0xffffffffu, ok)) {
+                            ok = false;
+                            break;
+                        }
+                        tcgen05_after_sync();
+                        for (int c = 0; c < DP; c += 16) {
+                            float o[16];
+                            tmem_ld16(t_o + lanes + c, o);
+#pragma unroll
+                            for (int e = 0; e < 16; e += 2) mul2(o[e], o[e + 1], keep, keep);
+                            tmem_st16(t_o + lanes + c, reinterpret_cast<const uint32_t*>(o));
+                        }
+                    }
+                }
+                const float less = m == -INFINITY ? 0.f : add - m;
+#pragma unroll
+                for (int h = 0; h < 64; h += 32) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int c = h; c < h + 32; c += 2) {
+                        fma2(x[c], x[c + 1], by, less, less);
+                        x[c] = ex2(x[c]);
+                        x[c + 1] = ex2(x[c + 1]);
+                        add2(l0, l1, x[c], x[c + 1]);
+                        pk[(c - h) / 2] = pack2<DT>(x[c], x[c + 1]);
+                    }
+                    tmem_st16(t_s + h / 2, pk);
+                }
+                tmem_wait_st();
+                tcgen05_before_sync();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bars.b_empty[buf]);
+                if (lane == 0) mbar_arrive(&bars.p_full[buf]);
             }
-            float t[8];
+            // ---- out = O / l, through the warp's rows of Q's tile
+            // (a barrier of its own: o_done may be any of three phases along by now)
+            if (ok) ok = mbar_wait_tight(&bars.o_last, turn & 1);
+            ok = __all_sync(0xffffffffu, ok);
+            if (ok) {
+                tcgen05_after_sync();
+                const float l = l0 + l1;
+                const float inv = l == 0.f ? 0.f : 1.f / l;  // a row that sees nothing is zero
+                unsigned char* qt = smem + L::q + turn % L::kQs * L::kQ;
 #pragma unroll
-            for (int c = 0; c < 8; ++c) t[c] = max3(x[c], x[c + 8], x[c + 16]);
-#pragma unroll
-            for (int c = 24; c < 56; c += 16)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) t[e] = max3(t[e], x[c + e], x[c + 8 + e]);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) t[e] = fmaxf(t[e], x[56 + e]);
-            const float top = fmaf(fmaxf(max3(max3(t[0], t[1], t[2]), t[3], t[4]), max3(t[5], t[6], t[7])), by, add);
-            if (__any_sync(0xffffffffu, top > m + kLazy || m == -INFINITY)) {
-                const float to = fmaxf(m, top);
-                const float keep = to == -INFINITY ? 1.f : ex2(m - to);
-                m = to;
-                l0 *= keep;
-                l1 *= keep;
-                if (n > 0) {
-                    ok = mbar_wait_tight(&bars.o_done, (n - 1) & 1);
-                    if (!__all_sync(0xffffffffu, ok)) {
-                        ok = false;
-                        break;
-                    }
-                    tcgen05_after_sync();
-                    for (int c = 0; c < DP; c += 16) {
-                        float o[16];
-                        tmem_ld16(t_o + lanes + c, o);
-#pragma unroll
-                        for (int e = 0; e < 16; e += 2) mul2(o[e], o[e + 1], keep, keep);
-                        tmem_st16(t_o + lanes + c, reinterpret_cast<const uint32_t*>(o));
-                    }
-                }
+                for (int c = 0; c < DP; c += 32) tmem_to_tile<DT>(qt, t_o + lanes, c, row, inv);
+                tcgen05_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars.o_free);
+                if (i < t.it.len) p.lse[(int64_t)t.head * p.N + t.it.start + i] = m + log2f(l);
+                store_tile_rows<DP>(p.out, qt, warp * 32, t.it.start, first, t.it.len, p.s.H, t.head, D, lane);
+                fence_proxy_async_smem();  // before the next queries land here
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars.q_empty[turn % L::kQs]);
             }
-            const float less = m == -INFINITY ? 0.f : add - m;
-#pragma unroll
-            for (int h = 0; h < 64; h += 32) {
-                uint32_t pk[16];
-#pragma unroll
-                for (int c = h; c < h + 32; c += 2) {
-                    fma2(x[c], x[c + 1], by, less, less);
-                    x[c] = ex2(x[c]);
-                    x[c + 1] = ex2(x[c + 1]);
-                    add2(l0, l1, x[c], x[c + 1]);
-                    pk[(c - h) / 2] = pack2<DT>(x[c], x[c + 1]);
-                }
-                tmem_st16(t_s + h / 2, pk);
-            }
-            tmem_wait_st();
-            tcgen05_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars.p_full[buf]);
-        }
-        // ---- out = O / l, through the warp's rows of Q's tile
-        // (a barrier of its own: o_done may be any of three phases along by now)
-        if (ok) ok = mbar_wait_tight(&bars.o_last, 0);
-        ok = __all_sync(0xffffffffu, ok);
-        if (ok) {
-            tcgen05_after_sync();
-            const float l = l0 + l1;
-            const float inv = l == 0.f ? 0.f : 1.f / l;  // a row that sees nothing is zero
-            unsigned char* qt = smem + L::q;
-#pragma unroll
-            for (int c = 0; c < DP; c += 32) tmem_to_tile<DT>(qt, t_o + lanes, c, row, inv);
-            if (i < it.len) p.lse[(int64_t)head * p.N + it.start + i] = m + log2f(l);
-            __syncwarp();
-            store_tile_rows<DP>(p.out, qt, warp * 32, it.start, first, it.len, p.s.H, head, D, lane);
-        }
+            g += steps;
+            last += steps - 1;
+            if (wait_bias) tables += steps;
+            ++turn;
+        } while (ok && more());
     }
     if (!ok) atomicOr(p.s.error, ERR_TIMEOUT);
     tcgen05_before_sync();
@@ -312,14 +389,21 @@ __global__ void __launch_bounds__(kThreads, 2) attn_fwd_mma_kernel(const AttnFor
 }
 
 template <int DT, int DP>
-cudaError_t launch(const AttnForward& p, const AttnMaps& maps, int64_t max_items, cudaStream_t s) {
-    attn_fwd_mma_kernel<DT, DP><<<(unsigned)(max_items * p.s.H), kThreads, Fwd<DP>::bytes, s>>>(p, maps);
+cudaError_t launch(const AttnForward& p, const AttnMaps& maps, cudaStream_t s) {
+    const int64_t turns = p.max_items * p.s.H;
+    if (p.ctas > 0 && p.ctas < turns)
+        attn_fwd_mma_kernel<DT, DP, true><<<(unsigned)p.ctas, kThreads, Fwd<DP>::bytes, s>>>(p, maps);
+    else
+        attn_fwd_mma_kernel<DT, DP, false><<<(unsigned)turns, kThreads, Fwd<DP>::bytes, s>>>(p, maps);
     return cudaGetLastError();
 }
 
 template <int DT, int DP>
 cudaError_t configure() {
-    return cudaFuncSetAttribute(attn_fwd_mma_kernel<DT, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const cudaError_t e = cudaFuncSetAttribute(attn_fwd_mma_kernel<DT, DP, true>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, Fwd<DP>::bytes);
+    if (e != cudaSuccess) return e;
+    return cudaFuncSetAttribute(attn_fwd_mma_kernel<DT, DP, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 Fwd<DP>::bytes);
 }
 
@@ -333,9 +417,9 @@ cudaError_t attn_forward_mma_configure() {
     return e;
 }
 
-cudaError_t launch_attn_forward_mma(const AttnForward& p, const AttnMaps& maps, int64_t max_items, cudaStream_t s) {
-    if (p.s.dtype == DT_F16) return p.s.D <= 64 ? launch<DT_F16, 64>(p, maps, max_items, s) : launch<DT_F16, 128>(p, maps, max_items, s);
-    return p.s.D <= 64 ? launch<DT_BF16, 64>(p, maps, max_items, s) : launch<DT_BF16, 128>(p, maps, max_items, s);
+cudaError_t launch_attn_forward_mma(const AttnForward& p, const AttnMaps& maps, cudaStream_t s) {
+    if (p.s.dtype == DT_F16) return p.s.D <= 64 ? launch<DT_F16, 64>(p, maps, s) : launch<DT_F16, 128>(p, maps, s);
+    return p.s.D <= 64 ? launch<DT_BF16, 64>(p, maps, s) : launch<DT_BF16, 128>(p, maps, s);
 }
 
 }  // namespace tbe

@@ -300,15 +300,15 @@ __device__ __forceinline__ bool load_tile(unsigned char* dst, const TileMap& map
     return true;
 }
 
-// A loader warp's ring: `steps` tiles of 64 rows through STAGES stages;
-// place(n) gives tile n's first row and head.
+// A loader warp's ring: `steps` tiles of 64 rows through STAGES stages, the
+// ring's tiles `base` on; place(n) gives tile n's first row and head.
 template <int DP, int STAGES, typename F>
 __device__ __forceinline__ bool load_ring(unsigned char* ring, const TileMap& map, const AttnItem& it,
                                           uint64_t* full, uint64_t* empty, uint64_t* fix, uint32_t& fix_phase,
-                                          int steps, int lane, F place) {
+                                          int steps, int lane, F place, int base = 0) {
     for (int n = 0; n < steps; ++n) {
-        const int st = n % STAGES;
-        bool ok = n < STAGES || mbar_wait_tight(&empty[st], ((n / STAGES) - 1) & 1);
+        const int st = (base + n) % STAGES;
+        bool ok = base + n < STAGES || mbar_wait_tight(&empty[st], (((base + n) / STAGES) - 1) & 1);
         const int2 at = place(n);
         ok = __all_sync(0xffffffffu, ok) &&
              load_tile<64, DP>(ring + st * (64 * DP * 2), map, it, at.y, at.x, &full[st], fix, fix_phase, lane);

@@ -99,6 +99,18 @@ def test_many_short_histories():
     Batch(torch.bfloat16, 2, 2, 32, g.integers(0, 9, 1500).tolist(), 4, 1, [0, 1, 2], seed=5).check()
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("window,sinks,starts", [(0, 0, [0, 1, 30]), (100, 3, [0, 2, 50, 4000]), (60, 0, None)])
+def test_many_histories_taken_in_turn(dtype, dim, window, sinks, starts):
+    """Two hundred histories of one to five key blocks, some empty, whose
+    heads do not divide the number of CTAs: a CTA takes tiles of other heads,
+    lengths and histories one after another."""
+    g = np.random.default_rng(dim + window)
+    lengths = np.where(g.random(200) < 0.1, 0, g.integers(1, 330, 200))
+    Batch(dtype, 6, 3, dim, lengths.tolist(), window, sinks, starts, seed=32).check()
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_one_token(dtype):
     b = Batch(dtype, 2, 2, 64, [1], 0, 0, [0])
