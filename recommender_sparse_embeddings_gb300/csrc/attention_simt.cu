@@ -27,7 +27,14 @@ struct Tile {
     static constexpr size_t pbytes = sizeof(float) * T * PLD;
 };
 
-// Rows [first, first + T) of a history (zeros from `len` on, and beyond
+// Rows of a tile that a history of `len` tokens has, rounded up to 16 (the
+// step of a thread's columns); loads, products and sums leave out the rest.
+template <int T>
+__device__ __forceinline__ int rows_of(int len, int first) {
+    return tmin(T, (len - first + 15) / 16 * 16);
+}
+
+// Rows [first, first + rows_of) of a history (zeros from `len` on, and beyond
 // column D) into a shared tile as fp32.
 template <int DT, int T, int DP>
 __device__ __forceinline__ void load_tile(float* dst, const Rows& r, int64_t token0, int head, int first, int len,
@@ -36,8 +43,9 @@ __device__ __forceinline__ void load_tile(float* dst, const Rows& r, int64_t tok
     constexpr int V = 16 / sizeof(E);
     constexpr int LD = Tile<T, DP>::LD;
     const E* base = static_cast<const E*>(r.data) + head * r.head_stride;
+    const int rows = rows_of<T>(len, first);
     if (vec) {
-        for (int c = threadIdx.x; c < T * (DP / V); c += kThreads) {
+        for (int c = threadIdx.x; c < rows * (DP / V); c += kThreads) {
             const int row = c / (DP / V), col = c % (DP / V) * V;
             float f[V];
 #pragma unroll
@@ -51,7 +59,7 @@ __device__ __forceinline__ void load_tile(float* dst, const Rows& r, int64_t tok
                 *reinterpret_cast<float4*>(dst + row * LD + col + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
         }
     } else {
-        for (int c = threadIdx.x; c < T * DP; c += kThreads) {
+        for (int c = threadIdx.x; c < rows * DP; c += kThreads) {
             const int row = c / DP, col = c % DP;
             float f = 0.f;
             if (first + row < len && col < D) f = load_elem<DT>(base, (token0 + first + row) * r.token_stride + col);
@@ -60,9 +68,10 @@ __device__ __forceinline__ void load_tile(float* dst, const Rows& r, int64_t tok
     }
 }
 
-// acc[r][c] += sum_d a[ty*R + r][d] * b[tx + 16 c][d]
-template <int T, int DP>
-__device__ __forceinline__ void dot_tile(float (&acc)[T / 16][T / 16], const float* a, const float* b, int tx, int ty) {
+// acc[r][c] += sum_d a[ty*R + r][d] * b[tx + 16 c][d], for columns below `cols`
+template <int T, int DP, bool FULL>
+__device__ __forceinline__ void dot_columns(float (&acc)[T / 16][T / 16], const float* a, const float* b, int tx, int ty,
+                                         int cols) {
     constexpr int R = T / 16, LD = Tile<T, DP>::LD;
 #pragma unroll 4
     for (int d = 0; d < DP; d += 4) {
@@ -70,26 +79,38 @@ __device__ __forceinline__ void dot_tile(float (&acc)[T / 16][T / 16], const flo
 #pragma unroll
         for (int r = 0; r < R; ++r) x[r] = *reinterpret_cast<const float4*>(a + (ty * R + r) * LD + d);
 #pragma unroll
-        for (int c = 0; c < R; ++c) y[c] = *reinterpret_cast<const float4*>(b + (tx + 16 * c) * LD + d);
+        for (int c = 0; c < R; ++c)
+            if (FULL || 16 * c < cols) y[c] = *reinterpret_cast<const float4*>(b + (tx + 16 * c) * LD + d);
 #pragma unroll
-        for (int r = 0; r < R; ++r)
+        for (int c = 0; c < R; ++c)
+            if (FULL || 16 * c < cols)
 #pragma unroll
-            for (int c = 0; c < R; ++c) {
-                acc[r][c] = fmaf(x[r].x, y[c].x, acc[r][c]);
-                acc[r][c] = fmaf(x[r].y, y[c].y, acc[r][c]);
-                acc[r][c] = fmaf(x[r].z, y[c].z, acc[r][c]);
-                acc[r][c] = fmaf(x[r].w, y[c].w, acc[r][c]);
-            }
+                for (int r = 0; r < R; ++r) {
+                    acc[r][c] = fmaf(x[r].x, y[c].x, acc[r][c]);
+                    acc[r][c] = fmaf(x[r].y, y[c].y, acc[r][c]);
+                    acc[r][c] = fmaf(x[r].z, y[c].z, acc[r][c]);
+                    acc[r][c] = fmaf(x[r].w, y[c].w, acc[r][c]);
+                }
     }
 }
 
-// acc[r][u] (columns 64 u + 4 tx ..) += sum_j p[ty*R + r][j] * b[j][column]
+// (a whole tile without the columns' tests, which cost its inner loop 30 %)
 template <int T, int DP>
-__device__ __forceinline__ void mul_tile(float4 (&acc)[T / 16][DP / 64], const float* p, const float* b, int tx,
-                                         int ty) {
+__device__ __forceinline__ void dot_tile(float (&acc)[T / 16][T / 16], const float* a, const float* b, int tx, int ty,
+                                         int cols) {
+    if (cols == T)
+        dot_columns<T, DP, true>(acc, a, b, tx, ty, T);
+    else
+        dot_columns<T, DP, false>(acc, a, b, tx, ty, cols);
+}
+
+// acc[r][u] (columns 64 u + 4 tx ..) += sum_{j < rows} p[ty*R + r][j] * b[j][column]
+template <int T, int DP, bool FULL>
+__device__ __forceinline__ void mul_rows(float4 (&acc)[T / 16][DP / 64], const float* p, const float* b, int tx,
+                                         int ty, int rows) {
     constexpr int R = T / 16, LD = Tile<T, DP>::LD, PLD = Tile<T, DP>::PLD, U = DP / 64;
 #pragma unroll 2
-    for (int j = 0; j < T; j += 4) {
+    for (int j = 0; j < (FULL ? T : rows); j += 4) {
         float w[R][4];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -113,6 +134,15 @@ __device__ __forceinline__ void mul_tile(float4 (&acc)[T / 16][DP / 64], const f
                 }
             }
     }
+}
+
+template <int T, int DP>
+__device__ __forceinline__ void mul_tile(float4 (&acc)[T / 16][DP / 64], const float* p, const float* b, int tx, int ty,
+                                         int rows) {
+    if (rows == T)
+        mul_rows<T, DP, true>(acc, p, b, tx, ty, T);
+    else
+        mul_rows<T, DP, false>(acc, p, b, tx, ty, rows);
 }
 
 template <int DT, int T, int DP>
@@ -183,6 +213,7 @@ __global__ void __launch_bounds__(kThreads) attn_fwd_simt_kernel(const AttnForwa
     int sink_tiles, lo;
     key_tiles<T>(p.s, it.tile, sink_tiles, lo);
     const int steps = sink_tiles + it.tile + 1 - lo;
+    const bool active = first + ty / 2 * 2 * R < it.len;  // the warp has a row that exists
     for (int st = 0; st < steps; ++st) {
         const int kt = st < sink_tiles ? st : lo + st - sink_tiles;
         __syncthreads();
@@ -190,12 +221,14 @@ __global__ void __launch_bounds__(kThreads) attn_fwd_simt_kernel(const AttnForwa
         load_tile<DT, T, DP>(vs, p.v, it.start, kvh, kt * T, it.len, p.s.D, p.vec);
         if (p.bias) load_bias<DT, T>(bt, p.s, p.bias, head, (it.tile - kt) * T);
         __syncthreads();
+        if (!active) continue;
+        const int cols = rows_of<T>(it.len, kt * T);
         float s[R][R];
 #pragma unroll
         for (int r = 0; r < R; ++r)
 #pragma unroll
             for (int c = 0; c < R; ++c) s[r][c] = 0.f;
-        dot_tile<T, DP>(s, qs, ks, tx, ty);
+        dot_tile<T, DP>(s, qs, ks, tx, ty, cols);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const int i = first + ty * R + r;
@@ -232,7 +265,7 @@ __global__ void __launch_bounds__(kThreads) attn_fwd_simt_kernel(const AttnForwa
             }
         }
         __syncwarp();  // a warp reads only the rows of ps that it wrote
-        mul_tile<T, DP>(o, ps, vs, tx, ty);
+        mul_tile<T, DP>(o, ps, vs, tx, ty, cols);
     }
     float inv[R];
 #pragma unroll
@@ -297,6 +330,7 @@ __global__ void __launch_bounds__(kThreads) attn_dq_simt_kernel(const AttnBackwa
     const int steps = sink_tiles + it.tile + 1 - lo;
     // 16-bit out: g . out misses delta by out's rounding, so a first sweep
     // adds up sum_j p (dp - g . out) in fp32, which is what it misses
+    const bool active = first + ty / 2 * 2 * R < it.len;  // the warp has a row that exists
     constexpr bool kTwice = DT != DT_F32;
     float over[R] = {};
     for (int st = kTwice ? -steps : 0; st < steps; ++st) {
@@ -323,8 +357,11 @@ __global__ void __launch_bounds__(kThreads) attn_dq_simt_kernel(const AttnBackwa
         for (int r = 0; r < R; ++r)
 #pragma unroll
             for (int c = 0; c < R; ++c) s[r][c] = dp[r][c] = 0.f;
-        dot_tile<T, DP>(s, qs, ks, tx, ty);
-        dot_tile<T, DP>(dp, gs, vs, tx, ty);
+        const int cols = rows_of<T>(it.len, kt * T);
+        if (active) {
+            dot_tile<T, DP>(s, qs, ks, tx, ty, cols);
+            dot_tile<T, DP>(dp, gs, vs, tx, ty, cols);
+        }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const int i = first + ty * R + r;
@@ -342,7 +379,7 @@ __global__ void __launch_bounds__(kThreads) attn_dq_simt_kernel(const AttnBackwa
         }
         if (st < 0) continue;
         __syncthreads();
-        mul_tile<T, DP>(acc, ps, ks, tx, ty);
+        if (active) mul_tile<T, DP>(acc, ps, ks, tx, ty, cols);
         if (p.bias) {
             for (int x = threadIdx.x; x < 2 * T - 1; x += kThreads) {
                 const int off = x - (T - 1);  // row - column
@@ -398,6 +435,7 @@ __global__ void __launch_bounds__(kThreads) attn_dkv_simt_kernel(const AttnBackw
     // last query that sees a key of the tile: window - 1 tokens after its last key, or the last of all for sinks
     const int64_t last = first < p.s.sinks ? it.len - 1 : tmin<int64_t>(it.len - 1, (int64_t)first + T - 1 + p.s.window - 1);
     const int qt_end = (int)(last / T) + 1;
+    const bool active = first + ty / 2 * 2 * R < it.len;  // the warp has a row that exists
     for (int g = 0; g < p.s.G; ++g) {
         const int head = kvh * p.s.G + g;
         for (int qt = kt; qt < qt_end; ++qt) {
@@ -417,13 +455,15 @@ __global__ void __launch_bounds__(kThreads) attn_dkv_simt_kernel(const AttnBackw
                 de[threadIdx.x] = y;
             }
             __syncthreads();
+            if (!active) continue;
+            const int cols = rows_of<T>(it.len, qt * T);
             float s[R][R], dp[R][R];
 #pragma unroll
             for (int r = 0; r < R; ++r)
 #pragma unroll
                 for (int c = 0; c < R; ++c) s[r][c] = dp[r][c] = 0.f;
-            dot_tile<T, DP>(s, ks, qs, tx, ty);
-            dot_tile<T, DP>(dp, vs, gs, tx, ty);
+            dot_tile<T, DP>(s, ks, qs, tx, ty, cols);
+            dot_tile<T, DP>(dp, vs, gs, tx, ty, cols);
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 const int j = first + ty * R + r;
@@ -440,14 +480,14 @@ __global__ void __launch_bounds__(kThreads) attn_dkv_simt_kernel(const AttnBackw
                 }
             }
             __syncwarp();  // a warp reads only the rows of ps that it wrote
-            mul_tile<T, DP>(dv, ps, gs, tx, ty);
+            mul_tile<T, DP>(dv, ps, gs, tx, ty, cols);
             __syncwarp();
 #pragma unroll
             for (int r = 0; r < R; ++r)
 #pragma unroll
                 for (int c = 0; c < R; ++c) ps[(ty * R + r) * PLD + tx + 16 * c] = s[r][c];
             __syncwarp();
-            mul_tile<T, DP>(dk, ps, qs, tx, ty);
+            mul_tile<T, DP>(dk, ps, qs, tx, ty, cols);
         }
     }
     float one[R], mul[R];
@@ -616,7 +656,7 @@ cudaError_t backward(const AttnBackward& p, int64_t n, cudaStream_t s) {
 // fill the SMs: forward 101 us with 64, 108 with 32).
 int attn_simt_tile(int dtype, int D, int H, int64_t N, int64_t B, int num_sms) {
     if (D > 128) return 32;
-    return dtype == DT_F32 && (N / 64 + B) * H < 2 * (int64_t)num_sms ? 32 : 64;
+    return dtype == DT_F32 && ((N / 64 + B) * H < 2 * (int64_t)num_sms || N < 32 * B) ? 32 : 64;
 }
 
 cudaError_t attn_simt_configure(int optin) {
