@@ -345,7 +345,7 @@ int tbe_per_sample_weight_grad(tbe_handle* h, const void* indices, const void* o
  * fp32; results are rounded once to dtype.  With 16-bit types the softmax
  * weights and the logits' gradients are rounded to dtype where they enter a
  * tensor-core product (their sums stay fp32), as the operands of every
- * 16-bit matrix product are.  fp16 gradients below fp16's range are lost, as
+ * 16-bit matrix product are.  fp16 gradients outside fp16's range are lost, as
  * always in fp16: scale the loss.
  *
  * A row with no visible key (every visible bias entry -inf, or an empty
@@ -374,8 +374,9 @@ typedef struct {
 
 /* Rows of a token operand: the D elements of (token, head) are consecutive
  * and start at data + token*token_stride + head*head_stride (strides in
- * elements, >= 0).  The fastest path wants 16-byte aligned rows and
- * D*sizeof(dtype) a multiple of 16. */
+ * elements, >= 0; 0 repeats a row).  The fastest path wants 16-byte aligned
+ * rows, D*sizeof(dtype) a multiple of 16 and, for 16-bit types on the tensor
+ * cores, D <= 128 and the larger stride a multiple of the smaller, neither 0. */
 typedef struct {
     const void* data; /* device */
     int64_t token_stride;
