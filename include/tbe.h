@@ -349,7 +349,9 @@ int tbe_per_sample_weight_grad(tbe_handle* h, const void* indices, const void* o
  * always in fp16: scale the loss.
  *
  * A row with no visible key (every visible bias entry -inf, or an empty
- * cache) gives 0 and has zero gradients.  Keys and values of a history's
+ * cache) gives 0 and has zero gradients.  A row whose visible keys all carry a
+ * bias of bf16's or fp32's lowest finite value weighs them equally and has zero
+ * gradients too (fp32 cannot hold logits beside it).  Keys and values of a history's
  * own tokens are expected to be finite; what lies outside a history or
  * behind a cache's length is never used, whatever its bits are.
  *

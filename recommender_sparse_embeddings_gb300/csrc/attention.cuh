@@ -254,6 +254,11 @@ __device__ __forceinline__ bool attn_visible(int d, int j, int window, int sinks
     return d >= 0 && (d < window || j < sinks);
 }
 
+// A saved statistic of a row that has no weights to pass gradients through: it
+// sees nothing (-inf), or all it sees carries a bias of its type's lowest
+// value, beside which fp32 cannot hold the logits or the sum.
+__device__ __forceinline__ bool attn_no_weights(float lse) { return lse < -1e30f; }
+
 // Whether key j is the only one that query i can see.  Its weight is 1
 // whatever the logit, so the logit's gradient is exactly 0, which dp - delta,
 // two sums of the same products in different orders, would miss by rounding.

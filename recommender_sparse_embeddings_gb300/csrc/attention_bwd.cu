@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
         if (i < it.len) {
             const int64_t at = (int64_t)head * p.N + it.start + i;
             const float x = p.lse[at];
-            less = x == -INFINITY ? -INFINITY : -x;  // a row that sees nothing: all its weights 2^-inf
+            less = attn_no_weights(x) ? -INFINITY : -x;  // then all its weights are 2^-inf
             if constexpr (L::kPerSm == 1) {
                 delta = p.delta[at];
             } else {
@@ -487,7 +487,7 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
                 if (i < it.len) {
                     const int64_t k = (int64_t)at.y * p.N + it.start + i;
                     const float x = p.lse[k];
-                    less = x == -INFINITY ? -INFINITY : (one ? same : 0.f) - x;
+                    less = attn_no_weights(x) ? -INFINITY : (one ? same : 0.f) - x;
                     delta = p.delta[k];
                 }
                 stat[buf * 128 + c] = less;

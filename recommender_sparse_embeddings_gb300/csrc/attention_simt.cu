@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(kThreads) attn_dq_simt_kernel(const AttnBackwa
         if (first + row < it.len) {
             const int64_t at = (int64_t)head * p.N + it.start + first + row;
             const float x = p.lse[at];
-            lse[r] = x == -INFINITY ? INFINITY : x;  // a row that sees nothing: all its weights 2^-inf
+            lse[r] = attn_no_weights(x) ? INFINITY : x;  // then all its weights are 2^-inf
             if (tx == 0) p.delta[at] = t;
         }
 #pragma unroll
@@ -449,7 +449,7 @@ __global__ void __launch_bounds__(kThreads) attn_dkv_simt_kernel(const AttnBackw
                 if (i < it.len) {
                     x = p.lse[(int64_t)head * p.N + it.start + i];
                     y = p.delta[(int64_t)head * p.N + it.start + i];
-                    if (x == -INFINITY) x = INFINITY;
+                    if (attn_no_weights(x)) x = INFINITY;
                 }
                 ls[threadIdx.x] = x;
                 de[threadIdx.x] = y;

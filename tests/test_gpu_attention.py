@@ -205,6 +205,21 @@ def test_lowest_bias(dtype):
     ref.close(out[5:], want["out"][5:], bound["out"][5:], "out")
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("dim", [64, 63])
+def test_lowest_bias_has_finite_gradients(dtype, dim):
+    """Rows that see nothing but keys of the lowest bias pass no gradient; the
+    others' gradients are those of a bias of -inf there."""
+    b = Batch(dtype, 1, 1, dim, [12, 300], 0, 0, [0, 5], seed=33, scale=4.0)
+    b.bias[0] = torch.finfo(dtype).min
+    got = b.run()
+    b.bias[0] = -float("inf")
+    want = b.run()
+    for x in ("grad_q", "grad_k", "grad_v"):
+        assert torch.equal(got[x], want[x]), x
+    assert torch.equal(got["grad_bias"][1], want["grad_bias"][1]) and not got["grad_bias"][0].any()
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_large_logits(dtype):
     """Logits of several hundred, rising along the history: the running
