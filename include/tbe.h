@@ -435,7 +435,7 @@ int tbe_attention_backward(tbe_attention* h, const tbe_rows* q, const tbe_rows* 
  * block_table: device int32 [B, table_width]; page block_table[b, j /
  * page_size] holds token j.  A position or page out of range is skipped and
  * reported as TBE_ERR_INDEX_OOB by tbe_attention_get_error.  Needs
- * table_width * page_size < 2^31. */
+ * table_width * page_size < 2^30. */
 int tbe_attention_append(tbe_attention* h, const tbe_rows* k, const tbe_rows* v, const void* offsets,
                          int32_t index_dtype, int64_t num_tokens, int32_t batch_size, const int32_t* before,
                          const tbe_pages* k_pages, const tbe_pages* v_pages, int32_t num_pages,

@@ -136,15 +136,15 @@ __device__ __forceinline__ bool find_item(const ItemSource& s, int64_t w, AttnIt
 }
 
 // Items of the batch, by the same rules.
-__device__ __forceinline__ int count_items(const ItemSource& s) {
+__device__ __forceinline__ int64_t count_items(const ItemSource& s) {
     if (!s.offsets) return *s.n_items;
     const int lane = threadIdx.x % 32;
-    int n = 0;
+    int64_t n = 0;  // (overlapping offsets: up to half the histories of N tokens each)
     for (int b = lane; b < s.B; b += 32) {
         const int64_t lo = s.index64 ? static_cast<const int64_t*>(s.offsets)[b] : static_cast<const int32_t*>(s.offsets)[b];
         const int64_t hi = s.index64 ? static_cast<const int64_t*>(s.offsets)[b + 1]
                                      : static_cast<const int32_t*>(s.offsets)[b + 1];
-        if (lo >= 0 && hi >= lo && hi <= s.N) n += (int)((hi - lo + s.tile - 1) / s.tile);
+        if (lo >= 0 && hi >= lo && hi <= s.N) n += (hi - lo + s.tile - 1) / s.tile;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);

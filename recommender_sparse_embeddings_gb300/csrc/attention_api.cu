@@ -401,7 +401,7 @@ int tbe_attention_append(tbe_attention* h, const tbe_rows* k, const tbe_rows* v,
     if (!rows_ok(k, N) || !rows_ok(v, N) || !pages_ok(k_pages) || !pages_ok(v_pages)) return TBE_ERR_INVALID_ARG;
     if (num_pages < 0 || page_size <= 0 || table_width < 0 || (B > 0 && (!before || (table_width > 0 && !block_table))))
         return TBE_ERR_INVALID_ARG;
-    if ((int64_t)table_width * page_size >= (int64_t(1) << 31)) return TBE_ERR_UNSUPPORTED;
+    if ((int64_t)table_width * page_size >= (int64_t(1) << 30)) return TBE_ERR_UNSUPPORTED;
     if (N == 0) return TBE_OK;
     AttnAppend p{};
     p.Hk = h->s.Hk;
@@ -432,7 +432,7 @@ int tbe_attention_append(tbe_attention* h, const tbe_rows* k, const tbe_rows* v,
 }
 
 size_t tbe_attention_decode_workspace_bytes(const tbe_attention* h, int32_t B, int64_t max_length) {
-    if (!h || B < 0 || max_length < 0 || max_length >= (int64_t(1) << 31)) return 0;
+    if (!h || B < 0 || max_length < 0 || max_length >= (int64_t(1) << 30)) return 0;
     const Split sp = decode_split(h, B, max_length);
     return align_up(sizeof(float) * (size_t)B * h->s.H * sp.splits * (h->s.D + 2)) + 256;
 }
@@ -447,7 +447,7 @@ int tbe_attention_decode(tbe_attention* h, const tbe_rows* q, const tbe_pages* k
     if (!rows_ok(q, B) || !pages_ok(k_pages) || !pages_ok(v_pages)) return TBE_ERR_INVALID_ARG;
     if ((bias != nullptr) != (h->s.buckets > 0) || !workspace) return TBE_ERR_INVALID_ARG;
     if (B > 0 && (!lengths || !out || (table_width > 0 && !block_table))) return TBE_ERR_INVALID_ARG;
-    if ((int64_t)table_width * page_size >= (int64_t(1) << 31) || B >= (1 << 24)) return TBE_ERR_UNSUPPORTED;
+    if ((int64_t)table_width * page_size >= (int64_t(1) << 30) || B >= (1 << 24)) return TBE_ERR_UNSUPPORTED;
     const int64_t room = (int64_t)table_width * page_size;
     const int64_t most = max_length == 0 ? room : std::min(max_length, room);
     const Split sp = decode_split(h, B, most);

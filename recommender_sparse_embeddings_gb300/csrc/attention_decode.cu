@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(kWarps * 32) attn_decode_kernel(const AttnDeco
     if (len < 0 && threadIdx.x == 0 && split == 0) atomicOr(p.s.error, ERR_OOB);
     const Visible vis = visible_rows(p.s, tmax(len, 0));
     if (split > 0 && split * p.chunk >= vis.count) return;
-    const int begin = split * p.chunk, end = tmin(vis.count, begin + p.chunk);
+    const int begin = split * p.chunk, end = vis.count - begin <= p.chunk ? vis.count : begin + p.chunk;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, sub = lane / LPR;
     const int col = lane % LPR * V;
     constexpr int cstep = LPR * V;
@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(kMmaWarps * 32) attn_decode_mma_kernel(const A
     if (len < 0 && threadIdx.x == 0 && split == 0) atomicOr(p.s.error, ERR_OOB);
     const Visible vis = visible_rows(p.s, tmax(len, 0));
     if (split > 0 && split * p.chunk >= vis.count) return;
-    const int begin = split * p.chunk, end = tmin(vis.count, begin + p.chunk);
+    const int begin = split * p.chunk, end = vis.count - begin <= p.chunk ? vis.count : begin + p.chunk;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
     const int D = p.s.D;
     if (p.bias) {

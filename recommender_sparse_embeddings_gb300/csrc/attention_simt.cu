@@ -500,18 +500,19 @@ __global__ void __launch_bounds__(kThreads) attn_dkv_simt_kernel(const AttnBackw
     store_rows<DT, T, DP>(p.gk, dk, mul, it.start, p.s.Hk, kvh, first, it.len, p.s.D, tx, ty);
 }
 
-// Exclusive sum over the CTA's 1024 threads, and the total.
-__device__ __forceinline__ int block_scan(int n, int32_t* warp_sum, int& all) {
+// Exclusive sum over the CTA's 1024 threads, and the total (64 bits: offsets
+// that overlap can name far more tiles than N tokens have).
+__device__ __forceinline__ int64_t block_scan(int64_t n, int64_t* warp_sum, int64_t& all) {
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    int incl = n;
+    int64_t incl = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int t = __shfl_up_sync(0xffffffffu, incl, o);
+        const int64_t t = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += t;
     }
     if (lane == 31) warp_sum[warp] = incl;
     __syncthreads();
-    int before = 0;
+    int64_t before = 0;
     all = 0;
     for (int k = 0; k < 32; ++k) {
         if (k < warp) before += warp_sum[k];
@@ -528,10 +529,11 @@ template <typename I>
 __global__ void __launch_bounds__(1024) attn_items_kernel(const I* __restrict__ off, int64_t N, int B, int tile,
                                                           AttnItem* __restrict__ items, int64_t capacity,
                                                           int32_t* n_items, uint32_t* error, const FarWork far) {
-    __shared__ int32_t warp_sum[32];
+    __shared__ int64_t warp_sum[32];
+    __shared__ int32_t far_count;  // far items written: the first ones, all of them where the offsets are in order
+    if (threadIdx.x == 0) far_count = 0;
     const int lane = threadIdx.x % 32;
-    int64_t base = 0;
-    int far_base = 0, slot_base = 0;
+    int64_t base = 0, far_base = 0, slot_base = 0;
     for (int b0 = 0; b0 < B; b0 += 1024) {
         const int b = b0 + threadIdx.x;
         int64_t lo = 0, hi = 0;
@@ -542,7 +544,7 @@ __global__ void __launch_bounds__(1024) attn_items_kernel(const I* __restrict__ 
             if (bad || (b == 0 && lo != 0) || (b == B - 1 && hi != N)) atomicOr(error, ERR_OFFSETS);
             if (bad) hi = lo = 0;
         }
-        int all;
+        int64_t all;
         const int n = (int)((hi - lo + tile - 1) / tile);
         const int64_t at = base + block_scan(n, warp_sum, all);
         base += all;
@@ -550,15 +552,16 @@ __global__ void __launch_bounds__(1024) attn_items_kernel(const I* __restrict__ 
         if (far.most > 0) {
             // chunks of the query blocks behind the first tile's window, where there are many
             const int behind = (int)((hi - lo + 63) / 64) - far.near;
-            int chunks = behind > far.blocks ? (behind + far.blocks - 1) / far.blocks : 0;
-            int here = far_base + block_scan(chunks, warp_sum, all);
+            const int chunks = behind > far.blocks ? (behind + far.blocks - 1) / far.blocks : 0;
+            const int64_t here = far_base + block_scan(chunks, warp_sum, all);
             far_base += all;
-            const int first = slot_base + block_scan(chunks > 0 ? chunks + 1 : 0, warp_sum, all);
+            const int64_t first = slot_base + block_scan(chunks > 0 ? chunks + 1 : 0, warp_sum, all);
             slot_base += all;
             if (chunks > 0 && here + chunks <= far.most) {
-                slot = first;
+                slot = (int)first;
+                atomicMax(&far_count, (int32_t)here + chunks);
                 for (int c = 0; c < chunks; ++c)
-                    far.items[here + c] = FarItem{(int)lo, (int)(hi - lo), c, chunks, first, {0, 0, 0}};
+                    far.items[here + c] = FarItem{(int)lo, (int)(hi - lo), c, chunks, slot, {0, 0, 0}};
             }
         }
         // short histories' items by their own lanes, a long one's by the warp
@@ -583,9 +586,10 @@ __global__ void __launch_bounds__(1024) attn_items_kernel(const I* __restrict__ 
                 }
         }
     }
+    __syncthreads();
     if (threadIdx.x == 0) {
         *n_items = (int32_t)tmin<int64_t>(base, capacity);
-        if (far.most > 0) *far.n_items = tmin(far_base, far.most);
+        if (far.most > 0) *far.n_items = far_count;
     }
 }
 
@@ -599,7 +603,8 @@ __global__ void __launch_bounds__(256) attn_bias_reduce_kernel(const float* __re
     const int pair = blockIdx.x * 8 + threadIdx.x / 32, lane = threadIdx.x % 32;
     if (pair >= H * buckets) return;
     const int head = pair / buckets, b = pair % buckets;
-    const int n = count_items(src);
+    // (offsets that overlap can name more tiles than there is room for)
+    const int n = (int)tmin<int64_t>(count_items(src), max_items);
     float t = 0.f;
     for (int w = lane; w < n; w += 32) t += part[((int64_t)w * H + head) * buckets + b];
     const int nf = n_far ? *n_far : 0;

@@ -290,6 +290,22 @@ def test_malformed_offsets_are_reported(index):
         assert tbe.tbe_attention_get_error(b.handle) == tbe.TBE_OK
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("tokens,histories,window,sinks", [(300, 101, 0, 0), (300, 301, 0, 0), (6000, 9, 64, 4)])
+def test_overlapping_offsets_stay_in_bounds(dtype, tokens, histories, window, sinks):
+    """Offsets that run back and forth name many times the tiles that N tokens
+    have (and many times the sinks' far queries): reported, and nothing beyond
+    the workspace is touched."""
+    b = Batch(dtype, 2, 1, 64, [tokens], window, sinks, [0, 3], seed=34)
+    b.offsets = torch.tensor([0, tokens] * (histories // 2 + 1), device="cuda")[:histories + 1]
+    n = tbe.tbe_attention_workspace_bytes(b.handle, tokens, histories, True)
+    room = torch.full((n + 65536,), 77, dtype=torch.uint8, device="cuda")
+    out, lse = tbe.tbe_attention_forward(b.handle, b.q, b.k, b.v, b.offsets, b.bias, workspace=room[:n])
+    tbe.tbe_attention_backward(b.handle, b.q, b.k, b.v, b.offsets, out, lse, b.grad, b.bias, workspace=room[:n])
+    assert tbe.tbe_attention_get_error(b.handle) == tbe.TBE_ERR_BAD_OFFSETS
+    assert (room[n:] == 77).all()
+
+
 def test_gradients_match_differences():
     """Directional derivatives of the fp32 forward by central differences.
     With step h the truncation is about h^2 / 6 of a third derivative (of the
