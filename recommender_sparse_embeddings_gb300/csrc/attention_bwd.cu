@@ -217,8 +217,7 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
     const uint32_t tmem = tmem_slot;
     const uint32_t t_dq = tmem + NB * 128, t_r = t_dq + DP;  // S at buf*128, dP at buf*128 + 64
     bool ok = true;
-    float last_bias;
-    const bool whole = keep_whole<DT>(p.s, p.bias, head, last_bias);
+    const bool whole = keep_whole(p.s);
 
     if (warp == kHelp) {
         // R += P K, dQ += dS K
@@ -259,6 +258,7 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
         const float c2 = p.s.scale * kLog2e;
         float* bt = reinterpret_cast<float*>(smem + L::table);
         const bool wait_bias = p.bias && !whole;
+        const float last_bias = last_bias_of<DT>(p.s, p.bias, head);
         if (p.bias && whole) fill_bias<DT>(bt, p.s, p.bias, head, first + 127, threadIdx.x, L::W * 32);
         float less = -INFINITY, delta = 0.f;
         if (i < it.len) {
@@ -473,7 +473,8 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
             int bucket = 0;
             if (p.bias) {
                 const int least = at.x - first - 127;
-                if (keep_whole<DT>(p.s, p.bias, at.y, same)) {
+                if (keep_whole(p.s)) {
+                    same = last_bias_of<DT>(p.s, p.bias, at.y);
                     one = least >= p.s.far;
                     bucket = p.s.buckets - 1;
                 } else {
@@ -505,8 +506,7 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
         float* diag = reinterpret_cast<float*>(smem + L::diag) + warp * 64;
         for (int g = 0; g < p.s.G; ++g) {
             float* bt = reinterpret_cast<float*>(smem + L::table);
-            float last_bias;
-            const bool whole = keep_whole<DT>(p.s, p.bias, kvh * p.s.G + g, last_bias);
+            const bool whole = keep_whole(p.s);
             if (p.bias && whole) {
                 fill_bias<DT>(bt, p.s, p.bias, kvh * p.s.G + g, (qb0 + blocks) * 64 - 1 - first, threadIdx.x, L::W * 32);
                 asm volatile("bar.sync 1, %0;" ::"n"(L::W * 32) : "memory");

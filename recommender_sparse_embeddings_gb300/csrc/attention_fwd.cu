@@ -150,12 +150,10 @@ __global__ void __launch_bounds__(kThreads, 2)
         // ---- bias by distance, where the table of all distances is not kept:
         // entry x of the block's table is the bias at distance base + x - 63,
         // x in [0, 191)
-        if (p.bias) {
+        if (p.bias && !keep_whole(p.s)) {
             float* bt = reinterpret_cast<float*>(smem + L::bias);
             int done = 0;
             do {
-                float last;
-                if (keep_whole<DT>(p.s, p.bias, t.head, last)) continue;
                 for (int n = 0; n < t.steps && ok; ++n, ++done) {
                     const int buf = done & 1;
                     if (done >= 2) ok = mbar_wait_tight(&bars.b_empty[buf], (done / 2 - 1) & 1);
@@ -164,15 +162,11 @@ __global__ void __launch_bounds__(kThreads, 2)
                     const int base = t.first - t.block(n) * 64;
                     const int least = tmax(0, base - 63), most = base + 127;
                     const int b0 = attn_bucket(p.s, least), b1 = attn_bucket(p.s, tmax(most, 0));
-                    const float same = bias_base2(load_elem<DT>(p.bias, (int64_t)b0 * p.s.H + t.head));
-                    // a bias that swallows the logits (a type's lowest value)
-                    // does so in the table's addition only
-                    const bool one = b0 == b1 && (same > -1e30f || same == -INFINITY);
                     if (lane == 0) {
-                        is_uniform[buf] = one;
-                        uniform_bias[buf] = same;
+                        is_uniform[buf] = b0 == b1;
+                        uniform_bias[buf] = bias_base2(load_elem<DT>(p.bias, (int64_t)b0 * p.s.H + t.head));
                     }
-                    if (!one)
+                    if (b0 != b1)
                         for (int x = lane; x < 191; x += 32) {
                             const int d = base + x - 63;
                             bt[buf * 192 + x] =
@@ -243,13 +237,13 @@ __global__ void __launch_bounds__(kThreads, 2)
         const uint32_t lanes = (uint32_t)(warp * 32) << 16;
         const float c2 = p.s.scale * kLog2e;
         float* bt = reinterpret_cast<float*>(smem + L::bias);
-        int g = 0, turn = 0, last = 0, tables = 0, held = -1;  // held: the head whose bias the kept table has
+        int g = 0, turn = 0, last = 0, held = -1;  // held: the head whose bias the kept table has
         float last_bias = 0.f;
-        bool whole = true;
+        const bool whole = keep_whole(p.s), wait_bias = p.bias && !whole;
         do {
             const int steps = t.steps, first = t.first, i = first + row;
             if (p.bias && t.head != held) {
-                whole = keep_whole<DT>(p.s, p.bias, t.head, last_bias);
+                last_bias = last_bias_of<DT>(p.s, p.bias, t.head);
                 if (whole) {
                     asm volatile("bar.sync 1, 128;" ::: "memory");  // the last table is read
                     fill_bias<DT>(bt, p.s, p.bias, t.head, TURNS ? INT_MAX / 2 : first + 127, row, 128);
@@ -257,13 +251,12 @@ __global__ void __launch_bounds__(kThreads, 2)
                 }
                 held = t.head;
             }
-            const bool wait_bias = p.bias && !whole;
             float m = -INFINITY, l0 = 0.f, l1 = 0.f;
             for (int n = 0; n < steps; ++n) {
-                const int buf = (g + n) & 1, tb = (tables + n) & 1;
+                const int buf = (g + n) & 1;
                 const uint32_t t_s = tmem + buf * 64 + lanes;
                 ok = mbar_wait_tight(&bars.s_full[buf], ((g + n) / 2) & 1);
-                if (ok && wait_bias) ok = mbar_wait_tight(&bars.b_full[tb], ((tables + n) / 2) & 1);
+                if (ok && wait_bias) ok = mbar_wait_tight(&bars.b_full[buf], ((g + n) / 2) & 1);
                 // products up to n - 2 have completed (their P's place is S(n)'s,
                 // which is full); n - 1 is waited for where O is touched
                 if (!__all_sync(0xffffffffu, ok)) {
@@ -276,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 tmem_ld32_issue(t_s + 32, x + 32);
                 tmem_wait_ld(x, 64);
                 const int key0 = t.block(n) * 64;
-                const bool table = p.bias && (whole ? first - key0 - 63 < p.s.far : !is_uniform[tb]);
+                const bool table = p.bias && (whole ? first - key0 - 63 < p.s.far : !is_uniform[buf]);
                 // a block needs masks unless all its pairs are visible
                 const bool all = key0 + 63 <= first && (first + 127 - key0 < p.s.window || key0 + 63 < p.s.sinks);
                 if (!all) {
@@ -292,17 +285,24 @@ __global__ void __launch_bounds__(kThreads, 2)
                 // logit = x * by + add: with a table it is formed here, else (one
                 // bias for the block, and c2 > 0) the maximum is taken of the raw
                 // products and one multiply-add before ex2 does it all
-                float by = c2, add = wait_bias ? uniform_bias[tb] : last_bias;
+                float by = c2, add = wait_bias ? uniform_bias[buf] : last_bias;
                 if (table) {
-                    const float* b = bt + (whole ? i - key0 + 127 : tb * 192 + row + 63);
+                    const float* b = bt + (whole ? i - key0 + 127 : buf * 192 + row + 63);
 #pragma unroll
                     for (int c = 0; c < 64; c += 2) fma2(x[c], x[c + 1], c2, b[-c], b[-c - 1]);
+                    by = 1.f;
+                    add = 0.f;
+                } else if (add < -1e30f && add > -INFINITY) {
+                    // a bias that swallows the logits (a type's lowest value):
+                    // one rounding of the two, as in a table's addition
+#pragma unroll
+                    for (int c = 0; c < 64; c += 2) fma2(x[c], x[c + 1], c2, add, add);
                     by = 1.f;
                     add = 0.f;
                 }
                 if (wait_bias) {
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&bars.b_empty[tb]);
+                    if (lane == 0) mbar_arrive(&bars.b_empty[buf]);
                 }
                 float u[8];
 #pragma unroll
@@ -377,7 +377,6 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
             g += steps;
             last += steps - 1;
-            if (wait_bias) tables += steps;
             ++turn;
         } while (ok && more());
     }

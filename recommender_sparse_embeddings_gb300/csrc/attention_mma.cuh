@@ -63,13 +63,15 @@ __device__ __forceinline__ void fill_bias(float* table, const AttnShape& s, cons
     }
 }
 
-// The last bucket's bias, and whether the table is kept: a bias that swallows
-// the logits (a type's lowest value) does so in a table's addition only, and
-// the blocks beyond `far` have none.
+// Whether the table of all distances is kept: by the handle's buckets alone, so
+// that all heads agree. It shares its memory with the tables per block, which
+// the helper warp writes two blocks, heads and turns ahead of the arithmetic.
+__device__ __forceinline__ bool keep_whole(const AttnShape& s) { return s.far <= kWholeFar; }
+
+// The last bucket's bias of a head, in base 2.
 template <int DT>
-__device__ __forceinline__ bool keep_whole(const AttnShape& s, const void* bias, int head, float& last) {
-    last = bias ? bias_base2(load_elem<DT>(bias, (int64_t)(s.buckets - 1) * s.H + head)) : 0.f;
-    return s.far <= kWholeFar && (last > -1e30f || last == -INFINITY);
+__device__ __forceinline__ float last_bias_of(const AttnShape& s, const void* bias, int head) {
+    return bias ? bias_base2(load_elem<DT>(bias, (int64_t)(s.buckets - 1) * s.H + head)) : 0.f;
 }
 
 // Descriptor of an MN-major operand in the tile layout: 8-row groups (along
