@@ -175,6 +175,22 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
+def _new(shape, dtype, device, stream, returned: bool = True) -> torch.Tensor:
+    """Memory that a call allocates for its launches on ``stream``.  It belongs
+    to that stream, so the allocator hands it on only behind them, and (what
+    the call returns) waits for the current stream's use of it too."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        at = _stream(stream).value
+        stream = torch.cuda.ExternalStream(at, device=device) if at else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if returned:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def _index_dtype(indices: torch.Tensor, offsets: torch.Tensor) -> int:
     if indices.dtype != offsets.dtype or indices.dtype not in (torch.int32, torch.int64):
         raise ValueError("indices and offsets must share dtype int32 or int64")
@@ -256,7 +272,7 @@ def tbe_forward(h: Handle, indices: torch.Tensor, offsets: torch.Tensor, batch_s
                 stream=None) -> torch.Tensor:
     lib = load_library()
     if out is None:
-        out = torch.empty((batch_size, h.total_dim), dtype=torch.float32, device=offsets.device)
+        out = _new((batch_size, h.total_dim), torch.float32, offsets.device, stream)
     rc = lib.tbe_forward(h.ptr, _ptr(indices), _ptr(offsets), _index_dtype(indices, offsets),
                          indices.numel(), batch_size, _ptr(per_sample_weights), _ptr(out),
                          _stream(stream))
@@ -270,7 +286,7 @@ def tbe_per_sample_weight_grad(h: Handle, indices: torch.Tensor, offsets: torch.
     """dL/dw_i for every lookup; call before the backward pass updates the rows."""
     lib = load_library()
     if grad_weights is None:
-        grad_weights = torch.empty(indices.numel(), dtype=torch.float32, device=offsets.device)
+        grad_weights = _new((indices.numel(),), torch.float32, offsets.device, stream)
     rc = lib.tbe_per_sample_weight_grad(h.ptr, _ptr(indices), _ptr(offsets), _index_dtype(indices, offsets),
                                         indices.numel(), batch_size, _ptr(grad_out), _ptr(grad_weights),
                                         _stream(stream))
@@ -290,9 +306,10 @@ def tbe_backward_workspace_layout(h: Handle, num_indices: int, batch_size: int) 
     return out
 
 
-def make_workspace(h: Handle, num_indices: int, batch_size: int, device=None) -> torch.Tensor:
+def make_workspace(h: Handle, num_indices: int, batch_size: int, device=None, stream=None) -> torch.Tensor:
+    """Workspace of a backward pass on ``stream`` (the current one by default)."""
     n = tbe_backward_workspace_bytes(h, num_indices, batch_size)
-    return torch.empty(n, dtype=torch.uint8, device=device or h.tables[0].device)
+    return _new((n,), torch.uint8, device or h.tables[0].device, stream, False)
 
 
 def tbe_backward_prepare(h: Handle, indices, offsets, batch_size: int, workspace: torch.Tensor,
@@ -307,7 +324,7 @@ def tbe_forward_prepare(h: Handle, indices, offsets, batch_size: int, workspace:
                         per_sample_weights=None, out: Optional[torch.Tensor] = None, stream=None):
     """Forward pass and backward preparation of one batch, run side by side."""
     if out is None:
-        out = torch.empty((batch_size, h.total_dim), dtype=torch.float32, device=offsets.device)
+        out = _new((batch_size, h.total_dim), torch.float32, offsets.device, stream)
     rc = load_library().tbe_forward_prepare(
         h.ptr, _ptr(indices), _ptr(offsets), _index_dtype(indices, offsets), indices.numel(),
         batch_size, _ptr(per_sample_weights), _ptr(out), _ptr(workspace), workspace.numel(),
@@ -497,12 +514,13 @@ def tbe_attention_workspace_bytes(h: AttentionHandle, num_tokens: int, batch_siz
 
 
 def make_attention_workspace(h: AttentionHandle, num_tokens: int, batch_size: int, backward: bool = False,
-                             device=None) -> torch.Tensor:
-    """Workspace of forward calls (``backward``: of both) up to this size."""
+                             device=None, stream=None) -> torch.Tensor:
+    """Workspace of forward calls (``backward``: of both) up to this size, on
+    ``stream`` (the current one by default)."""
     n = tbe_attention_workspace_bytes(h, num_tokens, batch_size, backward)
     if n == 0:
         raise TBEError(TBE_ERR_UNSUPPORTED, "tbe_attention_workspace_bytes")
-    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+    return _new((n,), torch.uint8, device or "cuda", stream, False)
 
 
 def tbe_attention_forward(h: AttentionHandle, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -516,11 +534,11 @@ def tbe_attention_forward(h: AttentionHandle, q: torch.Tensor, k: torch.Tensor, 
     po, it, b = _offsets(offsets)
     shape = (n, heads, h.head_dim)
     if out is None:
-        out = torch.empty(shape, dtype=h.dtype, device=q.device)
+        out = _new(shape, h.dtype, q.device, stream)
     if lse is None:
-        lse = torch.empty((heads, n), dtype=torch.float32, device=q.device)
+        lse = _new((heads, n), torch.float32, q.device, stream)
     if workspace is None:
-        workspace = make_attention_workspace(h, n, b, False, q.device)
+        workspace = make_attention_workspace(h, n, b, False, q.device, stream)
     rc = load_library().tbe_attention_forward(
         h.ptr, rq, rk, rv, _bias(h, bias), po, it, n, b, _packed(out, shape, h.dtype, "out"),
         _packed(lse, (heads, n), torch.float32, "lse"), _space(workspace), workspace.numel(), _stream(stream))
@@ -541,20 +559,20 @@ def tbe_attention_backward(h: AttentionHandle, q: torch.Tensor, k: torch.Tensor,
     rg = _rows(h, grad_out, n, heads, "grad_out")
     po, it, b = _offsets(offsets)
     if grad_q is None:
-        grad_q = torch.empty((n, heads, d), dtype=dt, device=q.device)
+        grad_q = _new((n, heads, d), dt, q.device, stream)
     if grad_k is None:
-        grad_k = torch.empty((n, kv, d), dtype=dt, device=q.device)
+        grad_k = _new((n, kv, d), dt, q.device, stream)
     if grad_v is None:
-        grad_v = torch.empty((n, kv, d), dtype=dt, device=q.device)
+        grad_v = _new((n, kv, d), dt, q.device, stream)
     pb = None
     if h.buckets:
         if grad_bias is None:
-            grad_bias = torch.empty((h.buckets, heads), dtype=dt, device=q.device)
+            grad_bias = _new((h.buckets, heads), dt, q.device, stream)
         pb = _packed(grad_bias, (h.buckets, heads), dt, "grad_bias")
     elif grad_bias is not None:
         raise ValueError("grad_bias without buckets")
     if workspace is None:
-        workspace = make_attention_workspace(h, n, b, True, q.device)
+        workspace = make_attention_workspace(h, n, b, True, q.device, stream)
     rc = load_library().tbe_attention_backward(
         h.ptr, rq, rk, rv, _bias(h, bias), po, it, n, b, _packed(out, (n, heads, d), dt, "out"),
         _packed(lse, (heads, n), torch.float32, "lse"), rg, _packed(grad_q, (n, heads, d), dt, "grad_q"),
@@ -595,11 +613,11 @@ def tbe_attention_decode_workspace_bytes(h: AttentionHandle, batch_size: int, ma
 
 
 def make_attention_decode_workspace(h: AttentionHandle, batch_size: int, max_length: int,
-                                    device=None) -> torch.Tensor:
+                                    device=None, stream=None) -> torch.Tensor:
     n = tbe_attention_decode_workspace_bytes(h, batch_size, max_length)
     if n == 0:
         raise TBEError(TBE_ERR_UNSUPPORTED, "tbe_attention_decode_workspace_bytes")
-    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+    return _new((n,), torch.uint8, device or "cuda", stream, False)
 
 
 def tbe_attention_decode(h: AttentionHandle, q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
@@ -614,9 +632,9 @@ def tbe_attention_decode(h: AttentionHandle, q: torch.Tensor, k_pages: torch.Ten
     kp, vp, pages, size, table, width = _cache(h, k_pages, v_pages, block_table, b)
     most = width * size if max_length is None else int(max_length)
     if out is None:
-        out = torch.empty(shape, dtype=h.dtype, device=q.device)
+        out = _new(shape, h.dtype, q.device, stream)
     if workspace is None:
-        workspace = make_attention_decode_workspace(h, b, most, q.device)
+        workspace = make_attention_decode_workspace(h, b, most, q.device, stream)
     rc = load_library().tbe_attention_decode(
         h.ptr, rq, kp, vp, pages, size, table, width, _packed(lengths, (b,), torch.int32, "lengths"), b, most,
         _bias(h, bias), _packed(out, shape, h.dtype, "out"), _space(workspace), workspace.numel(), _stream(stream))

@@ -33,3 +33,58 @@ def test_lowest_bias_in_some_heads(dim, starts, heads, kv_heads, histories):
         for x in want:
             assert torch.equal(got[x], want[x]), x
     assert tbe.tbe_attention_get_error(b.handle) == tbe.TBE_OK
+
+
+@pytest.mark.parametrize("as_handle", [False, True])
+def test_a_stream_that_is_not_the_current_one(as_handle):
+    """The calls' own memory belongs to the stream they launch on: what is
+    allocated and filled on the current stream meanwhile is other memory."""
+    b = Batch(torch.bfloat16, 2, 1, 64, [300, 100, 700], 50, 2, [0, 4], seed=41)
+    want = b.run()
+    c = Cache(torch.bfloat16, 4, 2, 64, [3000, 20], 16, seed=42)
+    c.append(0, 10 ** 6)
+    one = c.check()
+    n, count = b.q.shape[0], len(b.off) - 1
+    sizes = [tbe.tbe_attention_workspace_bytes(b.handle, n, count, x) for x in (False, True)]
+    sizes.append(tbe.tbe_attention_decode_workspace_bytes(c.handle, 2, c.table.shape[1] * 16))
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    stream = s.cuda_stream if as_handle else s
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)  # the launches wait behind some 10 ms
+    got = b.run(stream=stream)
+    last = tbe.tbe_attention_decode(c.handle, c.q, c.k_pages, c.v_pages, c.table, c.n, c.bias, stream=stream)
+    fill = [torch.full((size,), 255, dtype=torch.uint8, device="cuda") for size in sizes for _ in range(8)]
+    torch.cuda.current_stream().wait_stream(s)
+    for x in want:
+        assert torch.equal(got[x], want[x]), x
+    assert torch.equal(last, one)
+    assert all((f == 255).all() for f in fill)
+    assert tbe.tbe_attention_get_error(b.handle) == tbe.TBE_OK
+
+
+@pytest.mark.parametrize("as_handle", [False, True])
+def test_table_calls_on_a_stream_that_is_not_the_current_one(as_handle):
+    g = torch.Generator().manual_seed(43)
+    table = torch.randn((1000, 64), generator=g).cuda()
+    h = tbe.tbe_create([table], "sum")
+    ids = torch.randint(0, 1000, (5000,), generator=g).cuda()
+    off = torch.arange(0, 5001, 5).cuda()
+    up = torch.randn((1000, 64), generator=g).cuda()
+    want = tbe.tbe_forward(h, ids, off, 1000)
+    grad = tbe.tbe_per_sample_weight_grad(h, ids, off, 1000, up)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    stream = s.cuda_stream if as_handle else s
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)
+    got = tbe.tbe_forward(h, ids, off, 1000, stream=stream)
+    weights = tbe.tbe_per_sample_weight_grad(h, ids, off, 1000, up, stream=stream)
+    space = tbe.make_workspace(h, 5000, 1000, stream=stream)
+    both = tbe.tbe_forward_prepare(h, ids, off, 1000, space, stream=stream)
+    size = space.numel()
+    del space
+    fill = [torch.full((size,), 255, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    torch.cuda.current_stream().wait_stream(s)
+    assert torch.equal(got, want) and torch.equal(both, want) and torch.equal(weights, grad)
+    assert all((f == 255).all() for f in fill) and tbe.tbe_get_error(h) == tbe.TBE_OK
