@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 held = t.head;
             }
             float m = -INFINITY, l0 = 0.f, l1 = 0.f;
-            for (int n = 0; n < steps; ++n) {
+            for (int n = 0; n < steps && ok; ++n) {
                 const int buf = (g + n) & 1;
                 const uint32_t t_s = tmem + buf * 64 + lanes;
                 ok = mbar_wait_tight(&bars.s_full[buf], ((g + n) / 2) & 1);
@@ -378,7 +378,9 @@ __global__ void __launch_bounds__(kThreads, 2)
             g += steps;
             last += steps - 1;
             ++turn;
-        } while (ok && more());
+            // (a warp whose wait ran out waits for nothing any more, but meets the
+            // others at the table's barriers to the last turn)
+        } while (more());
     }
     if (!ok) atomicOr(p.s.error, ERR_TIMEOUT);
     tcgen05_before_sync();
