@@ -404,7 +404,8 @@ void tbe_attention_destroy(tbe_attention* h);
 
 /* Bytes of workspace of a forward call (backward = 0) or a backward call
  * (backward = 1, enough for the forward too) of N tokens in B histories; 0
- * for arguments outside the limits. */
+ * for arguments outside the limits.  The attention calls' workspaces start on
+ * a 16-byte boundary (INVALID_ARG else). */
 size_t tbe_attention_workspace_bytes(const tbe_attention* h, int64_t num_tokens, int32_t batch_size,
                                      int32_t backward);
 

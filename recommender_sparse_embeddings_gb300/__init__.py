@@ -491,7 +491,10 @@ def _packed(t: torch.Tensor, shape, dtype, name: str) -> int:
 def _space(t: torch.Tensor) -> int:
     if not t.is_cuda or not t.is_contiguous() or t.dtype is not torch.uint8:
         raise ValueError("workspace: expected a contiguous CUDA tensor of bytes")
-    return t.data_ptr()
+    at = t.data_ptr()
+    if at % 16:
+        raise ValueError("workspace: expected memory on a 16-byte boundary")
+    return at
 
 
 def _bias(h: AttentionHandle, bias: Optional[torch.Tensor]):

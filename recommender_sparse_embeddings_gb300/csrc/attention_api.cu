@@ -311,7 +311,7 @@ int tbe_attention_forward(tbe_attention* h, const tbe_rows* q, const tbe_rows* k
     int rc = check_batch(h, offsets, index_dtype, N, B);
     if (rc) return rc;
     if (!rows_ok(q, N) || !rows_ok(k, N) || !rows_ok(v, N)) return TBE_ERR_INVALID_ARG;
-    if ((bias != nullptr) != (h->s.buckets > 0) || (N > 0 && (!out || !lse)) || !workspace)
+    if ((bias != nullptr) != (h->s.buckets > 0) || (N > 0 && (!out || !lse)) || !workspace || !aligned16(workspace))
         return TBE_ERR_INVALID_ARG;
     const Layout L = make_layout(h, N, B, false);
     if (workspace_bytes < L.total) return TBE_ERR_WORKSPACE_TOO_SMALL;
@@ -347,7 +347,8 @@ int tbe_attention_backward(tbe_attention* h, const tbe_rows* q, const tbe_rows* 
     int rc = check_batch(h, offsets, index_dtype, N, B);
     if (rc) return rc;
     if (!rows_ok(q, N) || !rows_ok(k, N) || !rows_ok(v, N) || !rows_ok(grad_out, N)) return TBE_ERR_INVALID_ARG;
-    if ((bias != nullptr) != (h->s.buckets > 0) || (grad_bias != nullptr) != (h->s.buckets > 0) || !workspace)
+    if ((bias != nullptr) != (h->s.buckets > 0) || (grad_bias != nullptr) != (h->s.buckets > 0) || !workspace ||
+        !aligned16(workspace))
         return TBE_ERR_INVALID_ARG;
     if (N > 0 && (!out || !lse || !grad_q || !grad_k || !grad_v)) return TBE_ERR_INVALID_ARG;
     const Layout L = make_layout(h, N, B, true);
@@ -445,7 +446,7 @@ int tbe_attention_decode(tbe_attention* h, const tbe_rows* q, const tbe_pages* k
     if (!h || !on_device(h)) return TBE_ERR_INVALID_ARG;
     if (B < 0 || max_length < 0 || num_pages < 0 || page_size <= 0 || table_width < 0) return TBE_ERR_INVALID_ARG;
     if (!rows_ok(q, B) || !pages_ok(k_pages) || !pages_ok(v_pages)) return TBE_ERR_INVALID_ARG;
-    if ((bias != nullptr) != (h->s.buckets > 0) || !workspace) return TBE_ERR_INVALID_ARG;
+    if ((bias != nullptr) != (h->s.buckets > 0) || !workspace || !aligned16(workspace)) return TBE_ERR_INVALID_ARG;
     if (B > 0 && (!lengths || !out || (table_width > 0 && !block_table))) return TBE_ERR_INVALID_ARG;
     if ((int64_t)table_width * page_size >= (int64_t(1) << 30) || B >= (1 << 24)) return TBE_ERR_UNSUPPORTED;
     const int64_t room = (int64_t)table_width * page_size;

@@ -88,3 +88,55 @@ def test_table_calls_on_a_stream_that_is_not_the_current_one(as_handle):
     torch.cuda.current_stream().wait_stream(s)
     assert torch.equal(got, want) and torch.equal(both, want) and torch.equal(weights, grad)
     assert all((f == 255).all() for f in fill) and tbe.tbe_get_error(h) == tbe.TBE_OK
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_workspaces_start_on_16_byte_boundaries(dtype):
+    """Others are refused, by the binding and by the library; slices on a
+    boundary are as good as the whole."""
+    b = Batch(dtype, 2, 1, 64, [300, 20], 50, 2, [0, 4], seed=44)
+    want = b.run()
+    c = Cache(dtype, 4, 2, 64, [3000, 20], 16, seed=45)
+    c.append(0, 10 ** 6)
+    one = c.check()
+    space = torch.empty(1 << 22, dtype=torch.uint8, device="cuda")
+
+    def calls(ws):
+        out, lse = tbe.tbe_attention_forward(b.handle, b.q, b.k, b.v, b.offsets, b.bias, workspace=ws)
+        yield torch.equal(out, want["out"])
+        gq = tbe.tbe_attention_backward(b.handle, b.q, b.k, b.v, b.offsets, want["out"], want["lse"], b.grad, b.bias,
+                                        workspace=ws)[0]
+        yield torch.equal(gq, want["grad_q"])
+        yield torch.equal(c.check(workspace=ws), one)
+
+    assert all(calls(space[16:])) and all(calls(space[4096 + 48:]))
+    for at in (1, 4, 8, 20):
+        with pytest.raises(ValueError):
+            next(calls(space[at:]))
+        with pytest.raises(ValueError):
+            tbe.tbe_attention_backward(b.handle, b.q, b.k, b.v, b.offsets, want["out"], want["lse"], b.grad, b.bias,
+                                       workspace=space[at:])
+        with pytest.raises(ValueError):
+            c.check(workspace=space[at:])
+
+
+def test_the_library_refuses_misaligned_workspaces():
+    b = Batch(torch.bfloat16, 2, 2, 64, [10], seed=46)
+    lib, h = tbe.load_library(), b.handle.ptr
+    space = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    rows = [tbe._rows(b.handle, t, 10, 2, "x") for t in (b.q, b.k, b.v, b.grad)]
+    out = [torch.empty_like(b.q) for _ in range(4)]
+    lse = torch.empty((2, 10), device="cuda")
+    off = b.offsets.data_ptr()
+    for at in (1, 4, 8):
+        ws = space.data_ptr() + at
+        assert lib.tbe_attention_forward(h, *rows[:3], None, off, 1, 10, 1, out[0].data_ptr(), lse.data_ptr(), ws,
+                                         1 << 19, None) == tbe.TBE_ERR_INVALID_ARG
+        assert lib.tbe_attention_backward(h, *rows[:3], None, off, 1, 10, 1, out[0].data_ptr(), lse.data_ptr(),
+                                          rows[3], *[t.data_ptr() for t in out[1:]], None, ws, 1 << 19,
+                                          None) == tbe.TBE_ERR_INVALID_ARG
+        pages = [tbe._pages(b.handle, t[None], (1, 10, 2, 64), "x") for t in (b.k, b.v)]
+        table = torch.zeros((1, 1), dtype=torch.int32, device="cuda")
+        one = torch.ones(1, dtype=torch.int32, device="cuda")
+        assert lib.tbe_attention_decode(h, rows[0], *pages, 1, 10, table.data_ptr(), 1, one.data_ptr(), 1, 10, None,
+                                        out[0].data_ptr(), ws, 1 << 19, None) == tbe.TBE_ERR_INVALID_ARG
