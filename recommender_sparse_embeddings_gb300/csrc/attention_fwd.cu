@@ -336,7 +336,9 @@ __global__ void __launch_bounds__(kThreads, 2)
                         }
                     }
                 }
-                const float less = m == -INFINITY ? 0.f : add - m;
+                // (nothing seen yet: all of the row's logits so far are -inf, the
+                // raw products may be finite where one bias hides the block)
+                const float less = m == -INFINITY ? -INFINITY : add - m;
 #pragma unroll
                 for (int h = 0; h < 64; h += 32) {
                     uint32_t pk[16];

@@ -140,3 +140,27 @@ def test_the_library_refuses_misaligned_workspaces():
         one = torch.ones(1, dtype=torch.int32, device="cuda")
         assert lib.tbe_attention_decode(h, rows[0], *pages, 1, 10, table.data_ptr(), 1, one.data_ptr(), 1, 10, None,
                                         out[0].data_ptr(), ws, 1 << 19, None) == tbe.TBE_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("dim", [64, 128])
+def test_a_head_whose_every_bucket_is_hidden(dtype, dim):
+    """Over several tiles, beside a head that sees its keys: zeros, a statistic
+    of -inf and no gradients."""
+    b = Batch(dtype, 2, 2, dim, [300, 20], 0, 0, [0, 7], seed=50)
+    b.bias[:, 0] = -float("inf")
+    got = b.check()
+    assert not got["out"][:, 0].any() and not got["grad_q"][:, 0].any() and not got["grad_v"][:, 0].any()
+    assert (got["lse"][0] == -float("inf")).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_hidden_distant_keys_of_large_logits(dtype):
+    """Keys far back are hidden by a bias of -inf; their logits (up to about
+    1200) would not fit fp32's exponentials."""
+    b = Batch(dtype, 1, 1, 64, [400], 0, 0, [0, 70], seed=51, scale=1.0)
+    b.q = (b.q.float().abs() + 2).to(dtype)
+    b.k = (b.k.float() * 0.1).to(dtype)
+    b.k[:150] = 6
+    b.bias[1] = -float("inf")
+    b.check()
