@@ -270,18 +270,6 @@ __global__ void __launch_bounds__(kThreads, 2)
                 tmem_wait_ld(x, 64);
                 const int key0 = t.block(n) * 64;
                 const bool table = p.bias && (whole ? first - key0 - 63 < p.s.far : !is_uniform[buf]);
-                // a block needs masks unless all its pairs are visible
-                const bool all = key0 + 63 <= first && (first + 127 - key0 < p.s.window || key0 + 63 < p.s.sinks);
-                if (!all) {
-                    const int up = i - key0 + 1, down = i - p.s.window + 1 - key0, sk = p.s.sinks - key0;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint32_t seen = bits_below(up - 32 * h) & (~bits_below(down - 32 * h) | bits_below(sk - 32 * h));
-#pragma unroll
-                        for (int c = 0; c < 32; ++c)
-                            if (!(seen >> c & 1)) x[32 * h + c] = -INFINITY;
-                    }
-                }
                 // logit = x * by + add: with a table it is formed here, else (one
                 // bias for the block, and c2 > 0) the maximum is taken of the raw
                 // products and one multiply-add before ex2 does it all
@@ -303,6 +291,19 @@ __global__ void __launch_bounds__(kThreads, 2)
                 if (wait_bias) {
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bars.b_empty[buf]);
+                }
+                // a block needs masks unless all its pairs are visible (set after
+                // the bias, whose entries for unseen distances may hold anything)
+                const bool all = key0 + 63 <= first && (first + 127 - key0 < p.s.window || key0 + 63 < p.s.sinks);
+                if (!all) {
+                    const int up = i - key0 + 1, down = i - p.s.window + 1 - key0, sk = p.s.sinks - key0;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t seen = bits_below(up - 32 * h) & (~bits_below(down - 32 * h) | bits_below(sk - 32 * h));
+#pragma unroll
+                        for (int c = 0; c < 32; ++c)
+                            if (!(seen >> c & 1)) x[32 * h + c] = -INFINITY;
+                    }
                 }
                 float u[8];
 #pragma unroll

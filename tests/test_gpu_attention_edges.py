@@ -164,3 +164,22 @@ def test_hidden_distant_keys_of_large_logits(dtype):
     b.k[:150] = 6
     b.bias[1] = -float("inf")
     b.check()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("last", [False, True])
+def test_bias_of_distances_nobody_sees(dtype, bad, last):
+    """Buckets that begin behind the window reach no result, whatever they
+    hold; their gradient is zero."""
+    b = Batch(dtype, 2, 1, 64, [300, 65], 50, 0, [0, 20, 60, 200], seed=52)
+    b.bias[2:] = 0
+    clean = b.run()
+    b.bias[2] = bad
+    if last:
+        b.bias[3] = bad
+    got = b.run()
+    assert tbe.tbe_attention_get_error(b.handle) == tbe.TBE_OK
+    for x in clean:
+        assert torch.equal(got[x], clean[x]), x
+    assert not got["grad_bias"][2:].any()
