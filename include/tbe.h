@@ -350,10 +350,14 @@ int tbe_per_sample_weight_grad(tbe_handle* h, const void* indices, const void* o
  *
  * A row with no visible key (every visible bias entry -inf, or an empty
  * cache) gives 0 and has zero gradients.  A row whose visible keys all carry a
- * bias of bf16's or fp32's lowest finite value weighs them equally and has zero
- * gradients too (fp32 cannot hold logits beside it).  Keys and values of a history's
- * own tokens are expected to be finite; what lies outside a history or
- * behind a cache's length is never used, whatever its bits are.
+ * bias of bf16's or fp32's lowest finite value (below -2.35e38) weighs them
+ * equally and has zero gradients too (fp32 cannot hold logits beside it).  Any
+ * other bias that a row's keys share, however large, leaves the row's weights
+ * and gradients as they are without it (beside a bias from 2^31 on the logits'
+ * own part has to stay within 2^6).  Keys and values of a history's own tokens
+ * are expected to be finite; what lies outside a history or behind a cache's
+ * length is never used, whatever its bits are, and neither is the bias of a
+ * distance that no token sees.
  *
  * Results are deterministic: every sum has a fixed order.
  *

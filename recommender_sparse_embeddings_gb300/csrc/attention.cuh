@@ -7,6 +7,14 @@
 // in base 2: logits are multiplied by log2(e) so that the softmax's
 // exponential is one ex2, and the saved statistic is
 //     lse_i = log2 sum_j 2^(logit_ij * log2 e).
+//
+// Biases of large magnitude.  A bias of -1e9 on all keys that a row sees must
+// not change its weights, but fp32 holds no logit beside it (steps of 128 in
+// base 2), nor log2 of the sum in lse.  So the forward takes the largest bias
+// that the row sees off each one first (attn_bias_top; only for heads with an
+// entry from kCoarse on), and the backward adds up a row's recomputed weights
+// 2^(logit - lse) where |lse| is kCoarse or more and divides by their sum
+// (its log2 is the row's `excess`).
 #pragma once
 
 #include <float.h>
@@ -174,6 +182,7 @@ struct AttnBackward {
     void* gk;          // [N, Hk, D]
     void* gv;          // [N, Hk, D]
     float* delta;      // workspace [H, N]: g_i . out_i
+    float* excess;     // workspace [H, N], where |lse| >= kCoarse: log2 of the sum of 2^(logit - lse)
     float* bias_part;  // workspace [items, then far items, H, buckets]
     int64_t max_items;
     FarWork far;
@@ -242,13 +251,49 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // A bias entry in base 2.  The product of a type's lowest finite value with
-// log2(e) leaves fp32's range; it is held at fp32's lowest instead, so a row
-// whose visible keys all carry it keeps equal weights (an entry of -inf
-// stays -inf and hides its keys).
+// log2(e) leaves fp32's range; it is held at fp32's lowest instead (its
+// largest at fp32's largest), so a row whose visible keys all carry it keeps
+// equal weights (an entry of -inf stays -inf and hides its keys).
 __device__ __forceinline__ float bias_base2(float b) {
     const float x = b * kLog2e;
-    return (x < -FLT_MAX && b >= -FLT_MAX) ? -FLT_MAX : x;
+    return fabsf(b) <= FLT_MAX ? fminf(fmaxf(x, -FLT_MAX), FLT_MAX) : x;
 }
+
+__device__ __forceinline__ int attn_bucket(const AttnShape& s, int d) {
+    return d >= s.far ? s.buckets - 1 : (int)__ldg(s.bucket_of + d);
+}
+
+// From this magnitude on (base 2) a bias or a row's statistic is kept apart
+// from the logits: below it their sum in fp32 is off by 2^-19 at most, 3e-6 of
+// a weight.
+constexpr float kCoarse = 64.f;
+
+// Neither an infinity nor a type's lowest value counts: they hide their keys
+// exactly.
+__device__ __forceinline__ bool attn_coarse(float x) { return fabsf(x) >= kCoarse && fabsf(x) <= FLT_MAX && x > -FLT_MAX; }
+
+// The largest bias (base 2) of the keys that query i sees, over every `step`-th
+// bucket from `at` on of those that its distances have: 0 .. min(i, window - 1),
+// and behind the window the sinks' i - sinks + 1 .. i.  bias_of(b): bucket b's.
+template <typename F>
+__device__ __forceinline__ float attn_bias_top(const AttnShape& s, int i, int at, int step, F bias_of) {
+    float top = -INFINITY;
+    const int near = attn_bucket(s, tmin(i, s.window - 1));
+#pragma unroll 1
+    for (int b = at; b <= near; b += step) top = fmaxf(top, bias_of(b));
+    if (i >= s.window && s.sinks > 0) {
+        const int last = attn_bucket(s, i);
+#pragma unroll 1
+        for (int b = attn_bucket(s, tmax(s.window, i - s.sinks + 1)) + at; b <= last; b += step)
+            top = fmaxf(top, bias_of(b));
+    }
+    return top;
+}
+
+// What is taken off the row's biases, given their largest: nothing where the
+// row sees no key, or only keys of the lowest value (its logits are then
+// swallowed and its weights equal).
+__device__ __forceinline__ float attn_bias_off(float top) { return fabsf(top) <= FLT_MAX && top > -FLT_MAX ? top : 0.f; }
 
 __device__ __forceinline__ bool attn_visible(int d, int j, int window, int sinks) {
     return d >= 0 && (d < window || j < sinks);
@@ -256,18 +301,14 @@ __device__ __forceinline__ bool attn_visible(int d, int j, int window, int sinks
 
 // A saved statistic of a row that has no weights to pass gradients through: it
 // sees nothing (-inf), or all it sees carries a bias of its type's lowest
-// value, beside which fp32 cannot hold the logits or the sum.
-__device__ __forceinline__ bool attn_no_weights(float lse) { return lse < -1e30f; }
+// value, which swallowed the logits.
+__device__ __forceinline__ bool attn_no_weights(float lse) { return lse <= -FLT_MAX; }
 
 // Whether key j is the only one that query i can see.  Its weight is 1
 // whatever the logit, so the logit's gradient is exactly 0, which dp - delta,
 // two sums of the same products in different orders, would miss by rounding.
 __device__ __forceinline__ bool attn_lone(int i, int j, int window, int sinks) {
     return i == j && (i == 0 || (window == 1 && sinks == 0));
-}
-
-__device__ __forceinline__ int attn_bucket(const AttnShape& s, int d) {
-    return d >= s.far ? s.buckets - 1 : (int)__ldg(s.bucket_of + d);
 }
 
 template <int DT>

@@ -18,7 +18,9 @@
 // few tokens: grad_q off by 0.0047 of its norm, 0.0017 being the result's own
 // rounding).  With that estimate e, sum_j p (dp - e) = delta - e: dq sums its
 // rows of dS in fp32, takes R times that sum off dQ (R needs little
-// precision: the sum is small), and leaves the exact delta to dkv.
+// precision: the sum is small), and leaves the exact delta to dkv.  Where
+// |lse| is large (kCoarse) it adds up the weights too, divides by their sum and
+// leaves the sum's log2 to dkv (`excess`).
 //
 // A thread owns one row of S (a query in dq, a key in dkv) and half of a
 // block's columns: a block takes two warpgroups.  head_dim <= 64: one set of
@@ -29,6 +31,8 @@
 //
 // P and dS are rounded to the 16-bit type where they enter a product; the
 // bias gradient sums the unrounded fp32 dS.
+#include <type_traits>
+
 #include "attention_mma.cuh"
 
 namespace tbe {
@@ -46,11 +50,11 @@ struct Shape {
     static constexpr int kSmall = 64 * DP * 2;  // a 64-row tile
     static constexpr int a = 0, b = kBig, x = 2 * kBig, y = x + kStages * kSmall;
     static constexpr int table = y + kStages * kSmall;      // bias by distance: all, or 2 x 192 floats
-    static constexpr int stat = table + kWholeEntries * 4;  // dkv: -lse and delta, 2 x 2 x 64 floats
-    static constexpr int sums = stat + 2 * 2 * 64 * 4;      // dkv: per warp, a sum per bucket
+    static constexpr int stat = table + kWholeEntries * 4;  // dkv: -lse, -delta and -excess, 2 x 3 x 64 floats
+    static constexpr int sums = stat + 2 * 3 * 64 * 4;      // dkv: per warp, a sum per bucket
     static constexpr int diag = sums + W * kMaxBuckets * 4;       // dkv: per warp, 64 diagonals
-    static constexpr int rows = sums;                             // dq: a row sum per thread
-    static constexpr int dq_bytes = rows + W * 32 * 4 + 1024;
+    static constexpr int rows = sums;                             // dq: two row sums per thread
+    static constexpr int dq_bytes = rows + 2 * W * 32 * 4 + 1024;
     static constexpr int dkv_bytes = diag + W * 64 * 4 + 1024;
     // TMEM columns: S (then P) and dP (then dS) per buffer, two accumulators
     static constexpr int cols = DP == 64 ? 256 : 512;
@@ -293,90 +297,115 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
         }
         asm volatile("bar.sync 1, %0;" ::"n"(L::W * 32) : "memory");  // the table stands; rows is free again
         float sum0 = 0.f, sum1 = 0.f;  // of the row's dS
-        for (int n = wg / 2; n < steps; n += NB) {
-            const int buf = n & 1, sb = n % NB;
-            const uint32_t t_s = tmem + sb * 128 + lanes;
-            ok = mbar_wait_tight(&bars.s_full[sb], (n / NB) & 1);
-            if (ok && wait_bias) ok = mbar_wait_tight(&bars.t_full[buf], (n / 2) & 1);
-            if (!__all_sync(0xffffffffu, ok)) {
-                ok = false;
-                break;
-            }
-            tcgen05_after_sync();
-            const int key0 = block_of(n) * 64;
-            const bool table = p.bias && (whole ? first - key0 - 63 < p.s.far : several[buf] != 0);
-            const float add = less + (wait_bias ? same_bias[buf] : last_bias);
-            // whether the block holds a query whose only key is its own (attn_lone)
-            const bool lone = (first == 0 && key0 == 0) || (p.s.window == 1 && p.s.sinks == 0);
-            const bool all = key0 + 63 < first && (first + 127 - key0 < p.s.window || key0 + 63 < p.s.sinks);
-            uint32_t pk[16], dk[16];
+        // the blocks' loop, for warps with a row whose weights have to be added
+        // up and for the others (a test in the loop costs the latter 5 %)
+        const bool large = fabsf(less) >= kCoarse && less > -INFINITY;
+        float z0 = 0.f, z1 = 0.f;
+        auto walk = [&](auto adds_up) {
+            for (int n = wg / 2; n < steps; n += NB) {
+                const int buf = n & 1, sb = n % NB;
+                const uint32_t t_s = tmem + sb * 128 + lanes;
+                ok = mbar_wait_tight(&bars.s_full[sb], (n / NB) & 1);
+                if (ok && wait_bias) ok = mbar_wait_tight(&bars.t_full[buf], (n / 2) & 1);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    ok = false;
+                    break;
+                }
+                tcgen05_after_sync();
+                const int key0 = block_of(n) * 64;
+                const bool table = p.bias && (whole ? first - key0 - 63 < p.s.far : several[buf] != 0);
+                const float add = less + (wait_bias ? same_bias[buf] : last_bias);
+                // whether the block holds a query whose only key is its own (attn_lone)
+                const bool lone = (first == 0 && key0 == 0) || (p.s.window == 1 && p.s.sinks == 0);
+                const bool all = key0 + 63 < first && (first + 127 - key0 < p.s.window || key0 + 63 < p.s.sinks);
+                uint32_t pk[16], dk[16];
 #pragma unroll
-            for (int h = 0; h < 32; h += 16) {
-                float x[16], y[16];
-                tmem_ld16_pair(t_s + 32 * half + h, t_s + 64 + 32 * half + h, x, y);
-                const int key = key0 + 32 * half + h;
-                if (table) {
-                    const float* b = bt + (whole ? i - key + 127 : buf * 192 + row + 63 - 32 * half - h);
+                for (int h = 0; h < 32; h += 16) {
+                    float x[16], y[16];
+                    tmem_ld16_pair(t_s + 32 * half + h, t_s + 64 + 32 * half + h, x, y);
+                    const int key = key0 + 32 * half + h;
+                    if (table) {
+                        const float* b = bt + (whole ? i - key + 127 : buf * 192 + row + 63 - 32 * half - h);
+#pragma unroll
+                        for (int c = 0; c < 16; c += 2) {
+                            float b0 = b[-c], b1 = b[-c - 1];
+                            add2(b0, b1, less, less);
+                            fma2(x[c], x[c + 1], c2, b0, b1);
+                        }
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 16; c += 2) fma2(x[c], x[c + 1], c2, add, add);
+                    }
+                    if (!all) {
+                        const uint32_t seen =
+                            bits_below(i - key + 1) &
+                            (~bits_below(i - p.s.window + 1 - key) | bits_below(p.s.sinks - key));
+#pragma unroll
+                        for (int c = 0; c < 16; ++c)
+                            if (!(seen >> c & 1)) x[c] = -INFINITY;
+                    }
 #pragma unroll
                     for (int c = 0; c < 16; c += 2) {
-                        float b0 = b[-c], b1 = b[-c - 1];
-                        add2(b0, b1, less, less);
-                        fma2(x[c], x[c + 1], c2, b0, b1);
+                        x[c] = ex2(x[c]);
+                        x[c + 1] = ex2(x[c + 1]);
+                        add2(y[c], y[c + 1], -delta, -delta);
+                        mul2(y[c], y[c + 1], x[c], x[c + 1]);
+                        pk[(h + c) / 2] = pack2<DT>(x[c], x[c + 1]);
                     }
-                } else {
+                    if constexpr (decltype(adds_up)::value) {
 #pragma unroll
-                    for (int c = 0; c < 16; c += 2) fma2(x[c], x[c + 1], c2, add, add);
+                        for (int c = 0; c < 16; c += 2) add2(z0, z1, x[c], x[c + 1]);
+                    }
+                    if (lone) {
+#pragma unroll
+                        for (int c = 0; c < 16; ++c)
+                            if (key + c == i && attn_lone(i, i, p.s.window, p.s.sinks)) y[c] = 0.f;
+                    }
+#pragma unroll
+                    for (int c = 0; c < 16; c += 2) {
+                        dk[(h + c) / 2] = pack2<DT>(y[c], y[c + 1]);
+                        add2(sum0, sum1, y[c], y[c + 1]);
+                    }
                 }
-                if (!all) {
-                    const uint32_t seen =
-                        bits_below(i - key + 1) & (~bits_below(i - p.s.window + 1 - key) | bits_below(p.s.sinks - key));
-#pragma unroll
-                    for (int c = 0; c < 16; ++c)
-                        if (!(seen >> c & 1)) x[c] = -INFINITY;
-                }
-#pragma unroll
-                for (int c = 0; c < 16; c += 2) {
-                    x[c] = ex2(x[c]);
-                    x[c + 1] = ex2(x[c + 1]);
-                    add2(y[c], y[c + 1], -delta, -delta);
-                    mul2(y[c], y[c + 1], x[c], x[c + 1]);
-                    pk[(h + c) / 2] = pack2<DT>(x[c], x[c + 1]);
-                }
-                if (lone) {
-#pragma unroll
-                    for (int c = 0; c < 16; ++c)
-                        if (key + c == i && attn_lone(i, i, p.s.window, p.s.sinks)) y[c] = 0.f;
-                }
-#pragma unroll
-                for (int c = 0; c < 16; c += 2) {
-                    dk[(h + c) / 2] = pack2<DT>(y[c], y[c + 1]);
-                    add2(sum0, sum1, y[c], y[c + 1]);
+                // P and dS into the columns of S and dP that this thread has read
+                tmem_st16(t_s + 32 * half, pk);
+                tmem_st16(t_s + 64 + 32 * half, dk);
+                tmem_wait_st();
+                tcgen05_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&bars.ds_full[sb]);
+                    if (wait_bias) mbar_arrive(&bars.t_empty[buf]);
                 }
             }
-            // P and dS into the columns of S and dP that this thread has read
-            tmem_st16(t_s + 32 * half, pk);
-            tmem_st16(t_s + 64 + 32 * half, dk);
-            tmem_wait_st();
-            tcgen05_before_sync();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&bars.ds_full[sb]);
-                if (wait_bias) mbar_arrive(&bars.t_empty[buf]);
-            }
-        }
+        };
+        if (__any_sync(0xffffffffu, large))
+            walk(std::true_type{});
+        else
+            walk(std::false_type{});
         if (ok) ok = mbar_wait_tight(&bars.last, 0);
         ok = __all_sync(0xffffffffu, ok);
         // delta - e of the row: all warpgroups' sums (every warp comes here)
         rows[wg * 128 + row] = sum0 + sum1;
+        rows[(2 * NB + wg) * 128 + row] = z0 + z1;
         asm volatile("bar.sync 1, %0;" ::"n"(L::W * 32) : "memory");
-        float over = 0.f;
+        float over = 0.f, z = 0.f;
 #pragma unroll
-        for (int k = 0; k < 2 * NB; ++k) over += rows[k * 128 + row];
+        for (int k = 0; k < 2 * NB; ++k) {
+            over += rows[k * 128 + row];
+            z += rows[(2 * NB + k) * 128 + row];
+        }
+        const float inv = large ? 1.f / z : 1.f;
+        over *= inv;
         if (ok) {
             tcgen05_after_sync();
-            if (wg == 0 && i < it.len) p.delta[(int64_t)head * p.N + it.start + i] = delta + over;
-            // dq = scale (dQ - over R); the warpgroups take 32 columns each
-            tmem_to_tile<DT>(smem + L::a, t_dq + lanes, wg * 32, row, p.s.scale, t_r + lanes, -over);
+            if (wg == 0 && i < it.len) {
+                const int64_t at = (int64_t)head * p.N + it.start + i;
+                p.delta[at] = delta + over;
+                if (large) p.excess[at] = log2f(z);
+            }
+            // dq = scale (dQ - over R) / z; the warpgroups take 32 columns each
+            tmem_to_tile<DT>(smem + L::a, t_dq + lanes, wg * 32, row, p.s.scale * inv, t_r + lanes, -over);
         }
     }
     if (!ok) atomicOr(p.s.error, ERR_TIMEOUT);
@@ -398,7 +427,8 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
     unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     __shared__ Bars bars;
     __shared__ uint32_t tmem_slot;
-    __shared__ int same_bucket[2];  // -1: the block's distances have several
+    // -1: the block's distances have several; -2: and a query's excess is not in its -lse
+    __shared__ int same_bucket[2];
 
     // far items (the longest) first, then the tiles
     const int64_t turn = blockIdx.x / p.s.Hk;
@@ -456,8 +486,8 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
         ok = run_loader<DP>(smem + L::b, maps.v, kvh, first, smem + L::y, maps.g, &bars.big_full, bars.y_full,
                             bars.y_empty, &bars.fix[1], it, steps, lane, place);
     } else if (warp == kHelp + 3) {
-        // per query of the block: -lse (plus the bias where the block has one
-        // bucket) and delta; the bias table else
+        // per query of the block: -lse (plus the bias less the excess where the
+        // block has one bucket), delta and excess; the bias table else
         float* bt = reinterpret_cast<float*>(smem + L::table);
         float* stat = reinterpret_cast<float*>(smem + L::stat);
         for (int n = 0; n < steps; ++n) {
@@ -481,20 +511,28 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
                     one = spread_bias<DT>(bt + buf * 192, p.s, p.bias, at.y, least, lane, same, bucket);
                 }
             }
+            float x[2], delta[2], excess[2] = {0.f, 0.f};
+            const int64_t k = (int64_t)at.y * p.N + it.start + at.x + lane;
 #pragma unroll
-            for (int c = lane; c < 64; c += 32) {
-                const int i = at.x + c;
-                float less = -INFINITY, delta = 0.f;
-                if (i < it.len) {
-                    const int64_t k = (int64_t)at.y * p.N + it.start + i;
-                    const float x = p.lse[k];
-                    less = attn_no_weights(x) ? -INFINITY : (one ? same : 0.f) - x;
-                    delta = p.delta[k];
-                }
-                stat[buf * 128 + c] = less;
-                stat[buf * 128 + 64 + c] = -delta;
+            for (int c = 0; c < 2; ++c) {
+                const bool there = at.x + lane + 32 * c < it.len;
+                x[c] = there ? p.lse[k + 32 * c] : -INFINITY;
+                delta[c] = there ? p.delta[k + 32 * c] : 0.f;
             }
-            if (lane == 0) same_bucket[buf] = one ? bucket : -1;
+            const bool apart = __any_sync(0xffffffffu, attn_coarse(x[0]) || attn_coarse(x[1]));
+            if (apart) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    if (attn_coarse(x[c])) excess[c] = p.excess[k + 32 * c];
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const float less = attn_no_weights(x[c]) ? -INFINITY : one ? (same - x[c]) - excess[c] : -x[c];
+                stat[buf * 192 + lane + 32 * c] = less;
+                stat[buf * 192 + 64 + lane + 32 * c] = -delta[c];
+                if (apart) stat[buf * 192 + 128 + lane + 32 * c] = -excess[c];
+            }
+            if (lane == 0) same_bucket[buf] = one ? bucket : apart ? -2 : -1;
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars.t_full[buf]);
         }
@@ -523,7 +561,7 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
                 }
                 tcgen05_after_sync();
                 const int q0 = place(n).x;
-                const float* less = reinterpret_cast<const float*>(smem + L::stat) + buf * 128 + 32 * half;
+                const float* less = reinterpret_cast<const float*>(smem + L::stat) + buf * 192 + 32 * half;
                 const int bucket = same_bucket[buf];
                 const bool table = bucket < 0;
                 float sum0 = 0.f, sum1 = 0.f, run = 0.f;
@@ -551,8 +589,15 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
                     float x[16], y[16];
                     tmem_ld16_pair(t_s + 32 * half + h, t_s + 64 + 32 * half + h, x, y);
                     const int query = q0 + 32 * half + h;
-                    if (table) {
-                        const float* b = bt + (whole ? query - j + 127 : buf * 192 + 127 - row + 32 * half + h);
+                    const float* b = bt + (whole ? query - j + 127 : buf * 192 + 127 - row + 32 * half + h);
+                    if (bucket == -2) {
+#pragma unroll
+                        for (int c = 0; c < 16; c += 2) {
+                            const float b0 = (b[c] + less[h + c]) + less[128 + h + c];
+                            const float b1 = (b[c + 1] + less[h + c + 1]) + less[128 + h + c + 1];
+                            fma2(x[c], x[c + 1], c2, b0, b1);
+                        }
+                    } else if (table) {
 #pragma unroll
                         for (int c = 0; c < 16; c += 4) {
                             const float4 t = *reinterpret_cast<const float4*>(less + h + c);

@@ -89,6 +89,38 @@ __device__ __forceinline__ int cache_length(const AttnDecode& p, int b) {
     return len < 0 || (int64_t)len > p.max_length ? -1 : len;
 }
 
+// The buckets' biases of the CTA's heads, table[head][bucket] in base 2, a warp
+// per head.  Where a head has one of large magnitude the largest that its new
+// token sees is taken off them: fp32 holds no logit beside it.  (All CTAs of a
+// history take off the same, so their shares still join.)
+template <int DT, int HEADS, int WARPS>
+__device__ __forceinline__ void load_biases(float* table, const AttnShape& s, const void* bias, int head0, int heads,
+                                            int len) {
+    const int lane = threadIdx.x % 32;
+#pragma unroll 1
+    for (int h = threadIdx.x / 32; h < HEADS; h += WARPS) {
+        auto bias_of = [&](int b) {
+            return h < heads ? bias_base2(load_elem<DT>(bias, (int64_t)b * s.H + head0 + h)) : 0.f;
+        };
+        bool large = false;
+#pragma unroll 1
+        for (int b = lane; b < s.buckets; b += 32) {
+            const float x = bias_of(b);
+            table[h * s.buckets + b] = x;
+            large |= attn_coarse(x);
+        }
+        if (__any_sync(0xffffffffu, large) && len > 0) {
+            float top = attn_bias_top(s, len - 1, lane, 32, bias_of);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const float off = attn_bias_off(top);
+#pragma unroll 1
+            for (int b = lane; b < s.buckets; b += 32) table[h * s.buckets + b] = bias_of(b) - off;
+        }
+    }
+    __syncthreads();
+}
+
 // The 16-byte vectors that a lane holds of a row; columns from D on keep what
 // the registers hold (zeros, from the start).
 template <int DT, int NV>
@@ -139,13 +171,7 @@ __global__ void __launch_bounds__(kWarps * 32) attn_decode_kernel(const AttnDeco
     constexpr int cstep = LPR * V;
     const float c2 = p.s.scale * kLog2e;
 
-    if (p.bias) {
-        for (int i = threadIdx.x; i < GT * p.s.buckets; i += kWarps * 32) {
-            const int g = i / p.s.buckets, k = i % p.s.buckets;
-            dsm[i] = g < gn ? bias_base2(load_elem<DT>(p.bias, (int64_t)k * p.s.H + head0 + g)) : 0.f;
-        }
-        __syncthreads();
-    }
+    if (p.bias) load_biases<DT, GT, kWarps>(dsm, p.s, p.bias, head0, gn, len);
     float q[GT][W], o[GT][W], m[GT], l[GT];
 #pragma unroll
     for (int g = 0; g < GT; ++g) {
@@ -378,7 +404,8 @@ __device__ __forceinline__ uint32_t round2(float lo, float hi) {
 }
 
 template <int DT, int DP>
-__global__ void __launch_bounds__(kMmaWarps * 32) attn_decode_mma_kernel(const AttnDecode p) {
+__global__ void __launch_bounds__(kMmaWarps * 32) __maxnreg__(DP == 64 ? 96 : 168)
+    attn_decode_mma_kernel(const AttnDecode p) {
     constexpr int KC = DP / 32, VC = DP / 64;  // 16-byte chunks a lane holds of a key row, of a value row
     constexpr int STEP = kMmaWarps * 16;
     extern __shared__ float dsm[];  // bias by bucket [8][buckets]; then the warps' sums [warps][8][DP]
@@ -398,13 +425,7 @@ __global__ void __launch_bounds__(kMmaWarps * 32) attn_decode_mma_kernel(const A
     const int begin = split * p.chunk, end = vis.count - begin <= p.chunk ? vis.count : begin + p.chunk;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
     const int D = p.s.D;
-    if (p.bias) {
-        for (int i = threadIdx.x; i < kMmaHeads * p.s.buckets; i += kMmaWarps * 32) {
-            const int h = i / p.s.buckets, k = i % p.s.buckets;
-            dsm[i] = h < gn ? bias_base2(load_elem<DT>(p.bias, (int64_t)k * p.s.H + head0 + h)) : 0.f;
-        }
-        __syncthreads();
-    }
+    if (p.bias) load_biases<DT, kMmaHeads, kMmaWarps>(dsm, p.s, p.bias, head0, gn, len);
     const float* bias = dsm + g * p.s.buckets;
     const float c2 = p.s.scale * kLog2e;
     const uint4 zero = make_uint4(0, 0, 0, 0);

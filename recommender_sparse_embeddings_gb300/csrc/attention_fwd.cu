@@ -24,6 +24,8 @@
 //
 // The weights are rounded to the 16-bit type for the second product (the
 // tensor cores' operand type); their sum is kept unrounded in fp32.
+#include <type_traits>
+
 #include "attention_mma.cuh"
 
 namespace tbe {
@@ -48,6 +50,20 @@ struct FwdBars {
     uint64_t q_full[2], q_empty[2], fix[2], k_full[3], k_empty[3], v_full[3], v_empty[3], s_full[2], p_full[2], o_done,
         o_last, o_free, b_full[2], b_empty[2];
 };
+
+// Whether any thread of the four softmax warps says so; they all wait for it.
+__device__ __forceinline__ bool softmax_warps_any(bool x) {
+    uint32_t any;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, 1, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(any)
+        : "r"((uint32_t)x)
+        : "memory");
+    return any != 0;
+}
 
 // One (query tile, head) and the key blocks it sees: [0, sinks) and
 // [lo, lo + steps - sinks).
@@ -240,124 +256,153 @@ __global__ void __launch_bounds__(kThreads, 2)
         int g = 0, turn = 0, last = 0, held = -1;  // held: the head whose bias the kept table has
         float last_bias = 0.f;
         const bool whole = keep_whole(p.s), wait_bias = p.bias && !whole;
+        bool coarse = false;  // the head has a bias of large magnitude
         do {
             const int steps = t.steps, first = t.first, i = first + row;
             if (p.bias && t.head != held) {
                 last_bias = last_bias_of<DT>(p.s, p.bias, t.head);
+                bool large = false;
                 if (whole) {
                     asm volatile("bar.sync 1, 128;" ::: "memory");  // the last table is read
-                    fill_bias<DT>(bt, p.s, p.bias, t.head, TURNS ? INT_MAX / 2 : first + 127, row, 128);
-                    asm volatile("bar.sync 1, 128;" ::: "memory");
+                    large = fill_bias<DT>(bt, p.s, p.bias, t.head, TURNS ? INT_MAX / 2 : first + 127, row, 128);
+                } else {
+                    for (int b = row; b < p.s.buckets; b += 128)
+                        large |= attn_coarse(bias_base2(load_elem<DT>(p.bias, (int64_t)b * p.s.H + t.head)));
                 }
+                coarse = softmax_warps_any(large);  // (and the table stands)
                 held = t.head;
             }
+            float off = 0.f;  // taken off the row's biases
+            if (coarse)
+                off = attn_bias_off(attn_bias_top(p.s, i, 0, 1, [&](int b) {
+                    return bias_base2(load_elem<DT>(p.bias, (int64_t)b * p.s.H + t.head));
+                }));
             float m = -INFINITY, l0 = 0.f, l1 = 0.f;
-            for (int n = 0; n < steps && ok; ++n) {
-                const int buf = (g + n) & 1;
-                const uint32_t t_s = tmem + buf * 64 + lanes;
-                ok = mbar_wait_tight(&bars.s_full[buf], ((g + n) / 2) & 1);
-                if (ok && wait_bias) ok = mbar_wait_tight(&bars.b_full[buf], ((g + n) / 2) & 1);
-                // products up to n - 2 have completed (their P's place is S(n)'s,
-                // which is full); n - 1 is waited for where O is touched
-                if (!__all_sync(0xffffffffu, ok)) {
-                    ok = false;
-                    break;
-                }
-                tcgen05_after_sync();
-                float x[64];
-                tmem_ld32_issue(t_s, x);
-                tmem_ld32_issue(t_s + 32, x + 32);
-                tmem_wait_ld(x, 64);
-                const int key0 = t.block(n) * 64;
-                const bool table = p.bias && (whole ? first - key0 - 63 < p.s.far : !is_uniform[buf]);
-                // logit = x * by + add: with a table it is formed here, else (one
-                // bias for the block, and c2 > 0) the maximum is taken of the raw
-                // products and one multiply-add before ex2 does it all
-                float by = c2, add = wait_bias ? uniform_bias[buf] : last_bias;
-                if (table) {
-                    const float* b = bt + (whole ? i - key0 + 127 : buf * 192 + row + 63);
+            // the blocks' loop, with biases less `off` and without (a register
+            // and a test more in the latter cost 4 %)
+            auto walk = [&](auto shifts) {
+                constexpr bool kShifts = decltype(shifts)::value;
+                for (int n = 0; n < steps && ok; ++n) {
+                    const int buf = (g + n) & 1;
+                    const uint32_t t_s = tmem + buf * 64 + lanes;
+                    ok = mbar_wait_tight(&bars.s_full[buf], ((g + n) / 2) & 1);
+                    if (ok && wait_bias) ok = mbar_wait_tight(&bars.b_full[buf], ((g + n) / 2) & 1);
+                    // products up to n - 2 have completed (their P's place is S(n)'s,
+                    // which is full); n - 1 is waited for where O is touched
+                    if (!__all_sync(0xffffffffu, ok)) {
+                        ok = false;
+                        break;
+                    }
+                    tcgen05_after_sync();
+                    float x[64];
+                    tmem_ld32_issue(t_s, x);
+                    tmem_ld32_issue(t_s + 32, x + 32);
+                    tmem_wait_ld(x, 64);
+                    const int key0 = t.block(n) * 64;
+                    const bool table = p.bias && (whole ? first - key0 - 63 < p.s.far : !is_uniform[buf]);
+                    // logit = x * by + add: with a table it is formed here, else (one
+                    // bias for the block, and c2 > 0) the maximum is taken of the raw
+                    // products and one multiply-add before ex2 does it all
+                    float by = c2, add = wait_bias ? uniform_bias[buf] : last_bias;
+                    if (table) {
+                        const float* b = bt + (whole ? i - key0 + 127 : buf * 192 + row + 63);
+                        if constexpr (kShifts) {
 #pragma unroll
-                    for (int c = 0; c < 64; c += 2) fma2(x[c], x[c + 1], c2, b[-c], b[-c - 1]);
-                    by = 1.f;
-                    add = 0.f;
-                } else if (add < -1e30f && add > -INFINITY) {
-                    // a bias that swallows the logits (a type's lowest value):
-                    // one rounding of the two, as in a table's addition
+                            for (int c = 0; c < 64; c += 2) fma2(x[c], x[c + 1], c2, b[-c] - off, b[-c - 1] - off);
+                        } else {
 #pragma unroll
-                    for (int c = 0; c < 64; c += 2) fma2(x[c], x[c + 1], c2, add, add);
-                    by = 1.f;
-                    add = 0.f;
-                }
-                if (wait_bias) {
+                            for (int c = 0; c < 64; c += 2) fma2(x[c], x[c + 1], c2, b[-c], b[-c - 1]);
+                        }
+                        by = 1.f;
+                        add = 0.f;
+                    } else if (add == -FLT_MAX) {
+                        // a bias that swallows the logits (a type's lowest value):
+                        // one rounding of the two, as in a table's addition
+#pragma unroll
+                        for (int c = 0; c < 64; c += 2)
+                            fma2(x[c], x[c + 1], c2, kShifts ? add - off : add, kShifts ? add - off : add);
+                        by = 1.f;
+                        add = 0.f;
+                    } else if constexpr (kShifts) {
+                        add -= off;
+                    }
+                    if (wait_bias) {
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bars.b_empty[buf]);
+                    }
+                    // a block needs masks unless all its pairs are visible (set after
+                    // the bias, whose entries for unseen distances may hold anything)
+                    const bool all = key0 + 63 <= first && (first + 127 - key0 < p.s.window || key0 + 63 < p.s.sinks);
+                    if (!all) {
+                        const int up = i - key0 + 1, down = i - p.s.window + 1 - key0, sk = p.s.sinks - key0;
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t seen =
+                                bits_below(up - 32 * h) & (~bits_below(down - 32 * h) | bits_below(sk - 32 * h));
+#pragma unroll
+                            for (int c = 0; c < 32; ++c)
+                                if (!(seen >> c & 1)) x[32 * h + c] = -INFINITY;
+                        }
+                    }
+                    float u[8];
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) u[c] = max3(x[c], x[c + 8], x[c + 16]);
+#pragma unroll
+                    for (int c = 24; c < 56; c += 16)
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) u[e] = max3(u[e], x[c + e], x[c + 8 + e]);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) u[e] = fmaxf(u[e], x[56 + e]);
+                    const float most = fmaxf(max3(max3(u[0], u[1], u[2]), u[3], u[4]), max3(u[5], u[6], u[7]));
+                    const float top = fmaf(most, by, add);
+                    if (__any_sync(0xffffffffu, top > m + kLazy || m == -INFINITY)) {
+                        const float to = fmaxf(m, top);
+                        const float keep = to == -INFINITY ? 1.f : ex2(m - to);
+                        m = to;
+                        l0 *= keep;
+                        l1 *= keep;
+                        if (n > 0) {
+                            ok = mbar_wait_tight(&bars.o_done, (last + n - 1) & 1);
+                            if (!__all_sync(0xffffffffu, ok)) {
+                                ok = false;
+                                break;
+                            }
+                            tcgen05_after_sync();
+                            for (int c = 0; c < DP; c += 16) {
+                                float o[16];
+                                tmem_ld16(t_o + lanes + c, o);
+#pragma unroll
+                                for (int e = 0; e < 16; e += 2) mul2(o[e], o[e + 1], keep, keep);
+                                tmem_st16(t_o + lanes + c, reinterpret_cast<const uint32_t*>(o));
+                            }
+                        }
+                    }
+                    // (nothing seen yet: all of the row's logits so far are -inf, the
+                    // raw products may be finite where one bias hides the block)
+                    const float less = m == -INFINITY ? -INFINITY : add - m;
+#pragma unroll
+                    for (int h = 0; h < 64; h += 32) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int c = h; c < h + 32; c += 2) {
+                            fma2(x[c], x[c + 1], by, less, less);
+                            x[c] = ex2(x[c]);
+                            x[c + 1] = ex2(x[c + 1]);
+                            add2(l0, l1, x[c], x[c + 1]);
+                            pk[(c - h) / 2] = pack2<DT>(x[c], x[c + 1]);
+                        }
+                        tmem_st16(t_s + h / 2, pk);
+                    }
+                    tmem_wait_st();
+                    tcgen05_before_sync();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&bars.b_empty[buf]);
+                    if (lane == 0) mbar_arrive(&bars.p_full[buf]);
                 }
-                // a block needs masks unless all its pairs are visible (set after
-                // the bias, whose entries for unseen distances may hold anything)
-                const bool all = key0 + 63 <= first && (first + 127 - key0 < p.s.window || key0 + 63 < p.s.sinks);
-                if (!all) {
-                    const int up = i - key0 + 1, down = i - p.s.window + 1 - key0, sk = p.s.sinks - key0;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint32_t seen = bits_below(up - 32 * h) & (~bits_below(down - 32 * h) | bits_below(sk - 32 * h));
-#pragma unroll
-                        for (int c = 0; c < 32; ++c)
-                            if (!(seen >> c & 1)) x[32 * h + c] = -INFINITY;
-                    }
-                }
-                float u[8];
-#pragma unroll
-                for (int c = 0; c < 8; ++c) u[c] = max3(x[c], x[c + 8], x[c + 16]);
-#pragma unroll
-                for (int c = 24; c < 56; c += 16)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) u[e] = max3(u[e], x[c + e], x[c + 8 + e]);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) u[e] = fmaxf(u[e], x[56 + e]);
-                const float top = fmaf(fmaxf(max3(max3(u[0], u[1], u[2]), u[3], u[4]), max3(u[5], u[6], u[7])), by, add);
-                if (__any_sync(0xffffffffu, top > m + kLazy || m == -INFINITY)) {
-                    const float to = fmaxf(m, top);
-                    const float keep = to == -INFINITY ? 1.f : ex2(m - to);
-                    m = to;
-                    l0 *= keep;
-                    l1 *= keep;
-                    if (n > 0) {
-                        ok = mbar_wait_tight(&bars.o_done, (last + n - 1) & 1);
-                        if (!__all_sync(0xffffffffu, ok)) {
-                            ok = false;
-                            break;
-                        }
-                        tcgen05_after_sync();
-                        for (int c = 0; c < DP; c += 16) {
-                            float o[16];
-                            tmem_ld16(t_o + lanes + c, o);
-#pragma unroll
-                            for (int e = 0; e < 16; e += 2) mul2(o[e], o[e + 1], keep, keep);
-                            tmem_st16(t_o + lanes + c, reinterpret_cast<const uint32_t*>(o));
-                        }
-                    }
-                }
-                // (nothing seen yet: all of the row's logits so far are -inf, the
-                // raw products may be finite where one bias hides the block)
-                const float less = m == -INFINITY ? -INFINITY : add - m;
-#pragma unroll
-                for (int h = 0; h < 64; h += 32) {
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int c = h; c < h + 32; c += 2) {
-                        fma2(x[c], x[c + 1], by, less, less);
-                        x[c] = ex2(x[c]);
-                        x[c + 1] = ex2(x[c + 1]);
-                        add2(l0, l1, x[c], x[c + 1]);
-                        pk[(c - h) / 2] = pack2<DT>(x[c], x[c + 1]);
-                    }
-                    tmem_st16(t_s + h / 2, pk);
-                }
-                tmem_wait_st();
-                tcgen05_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars.p_full[buf]);
-            }
+            };
+            if (__any_sync(0xffffffffu, off != 0.f))
+                walk(std::true_type{});
+            else
+                walk(std::false_type{});
             // ---- out = O / l, through the warp's rows of Q's tile
             // (a barrier of its own: o_done may be any of three phases along by now)
             if (ok) ok = mbar_wait_tight(&bars.o_last, turn & 1);
@@ -372,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 tcgen05_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars.o_free);
-                if (i < t.it.len) p.lse[(int64_t)t.head * p.N + t.it.start + i] = m + log2f(l);
+                if (i < t.it.len) p.lse[(int64_t)t.head * p.N + t.it.start + i] = off + (m + log2f(l));
                 store_tile_rows<DP>(p.out, qt, warp * 32, t.it.start, first, t.it.len, p.s.H, t.head, D, lane);
                 fence_proxy_async_smem();  // before the next queries land here
                 __syncwarp();

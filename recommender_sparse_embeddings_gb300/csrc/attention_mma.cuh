@@ -52,15 +52,25 @@ __device__ __forceinline__ bool mbar_wait_tight(uint64_t* bar, uint32_t parity) 
 constexpr int kWholeFar = 2047;
 constexpr int kWholeEntries = kWholeFar + 191 + 127 + 3;
 
+// Returns whether the thread saw an entry of large magnitude.
 template <int DT>
-__device__ __forceinline__ void fill_bias(float* table, const AttnShape& s, const void* bias, int head, int most,
+__device__ __forceinline__ bool fill_bias(float* table, const AttnShape& s, const void* bias, int head, int most,
                                           int thread, int threads) {
     const int n = tmin(s.far + 190, most) + 128;
+    float size = 0.f;
 #pragma unroll 4
     for (int x = thread; x < n; x += threads) {
         const int d = x - 127;
-        table[x] = d >= 0 ? bias_base2(load_elem<DT>(bias, (int64_t)attn_bucket(s, d) * s.H + head)) : 0.f;
+        const float b = d >= 0 ? bias_base2(load_elem<DT>(bias, (int64_t)attn_bucket(s, d) * s.H + head)) : 0.f;
+        table[x] = b;
+        size = fmaxf(size, fabsf(b));
     }
+    bool large = size >= kCoarse;
+    if (large) {  // not if they are infinities and lowest values
+        large = false;
+        for (int x = thread; x < n; x += threads) large |= attn_coarse(table[x]);
+    }
+    return large;
 }
 
 // Whether the table of all distances is kept: by the handle's buckets alone, so

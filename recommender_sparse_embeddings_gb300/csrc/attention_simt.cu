@@ -184,6 +184,13 @@ __device__ __forceinline__ void load_bias(float* bt, const AttnShape& s, const v
     }
 }
 
+// Whether the head has a bias of large magnitude; the whole CTA calls it.
+template <int DT>
+__device__ __forceinline__ bool any_coarse(const AttnShape& s, const void* bias, int head) {
+    return __syncthreads_or(threadIdx.x < s.buckets &&
+                            attn_coarse(bias_base2(load_elem<DT>(bias, (int64_t)threadIdx.x * s.H + head))));
+}
+
 template <int DT, int T, int DP>
 __global__ void __launch_bounds__(kThreads) attn_fwd_simt_kernel(const AttnForward p) {
     constexpr int R = T / 16, U = DP / 64, PLD = Tile<T, DP>::PLD;
@@ -200,13 +207,23 @@ __global__ void __launch_bounds__(kThreads) attn_fwd_simt_kernel(const AttnForwa
     const int tx = threadIdx.x % 16, ty = threadIdx.x / 16, kvh = head / p.s.G;
     const int first = it.tile * T;
     const float c2 = p.s.scale * kLog2e;
+    const bool coarse = p.bias && any_coarse<DT>(p.s, p.bias, head);
     load_tile<DT, T, DP>(qs, p.q, it.start, head, first, it.len, p.s.D, p.vec);
     float4 o[R][U];
-    float m[R], l[R];
+    float m[R], l[R], off[R];  // off: taken off the row's biases
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         m[r] = -INFINITY;
         l[r] = 0.f;
+        off[r] = 0.f;
+        if (coarse) {
+            float top = attn_bias_top(p.s, first + ty * R + r, tx, 16, [&](int b) {
+                return bias_base2(load_elem<DT>(p.bias, (int64_t)b * p.s.H + head));
+            });
+#pragma unroll
+            for (int o2 = 8; o2 > 0; o2 >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o2, 16));
+            off[r] = attn_bias_off(top);
+        }
 #pragma unroll
         for (int u = 0; u < U; ++u) o[r][u] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
@@ -237,7 +254,7 @@ __global__ void __launch_bounds__(kThreads) attn_fwd_simt_kernel(const AttnForwa
             for (int c = 0; c < R; ++c) {
                 const int jj = tx + 16 * c, j = kt * T + jj;
                 float x = s[r][c] * c2;
-                if (p.bias) x += bt[ty * R + r - jj + T - 1];
+                if (p.bias) x += bt[ty * R + r - jj + T - 1] - off[r];
                 s[r][c] = attn_visible(i - j, j, p.s.window, p.s.sinks) ? x : -INFINITY;
                 top = fmaxf(top, s[r][c]);
             }
@@ -272,7 +289,7 @@ __global__ void __launch_bounds__(kThreads) attn_fwd_simt_kernel(const AttnForwa
     for (int r = 0; r < R; ++r) {
         inv[r] = l[r] == 0.f ? 0.f : 1.f / l[r];  // a row that sees nothing is zero
         const int row = first + ty * R + r;
-        if (tx == 0 && row < it.len) p.lse[(int64_t)head * p.N + it.start + row] = m[r] + log2f(l[r]);
+        if (tx == 0 && row < it.len) p.lse[(int64_t)head * p.N + it.start + row] = off[r] + (m[r] + log2f(l[r]));
     }
     store_rows<DT, T, DP>(p.out, o, inv, it.start, p.s.H, head, first, it.len, p.s.D, tx, ty);
 }
@@ -305,7 +322,8 @@ __global__ void __launch_bounds__(kThreads) attn_dq_simt_kernel(const AttnBackwa
     load_tile<DT, T, DP>(ks, orows, it.start, head, first, it.len, p.s.D, p.vec);
     __syncthreads();
     float4 acc[R][U];
-    float lse[R], delta[R];
+    float lse[R], delta[R], excess[R];
+    bool large = false;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         const int row = ty * R + r;
@@ -314,11 +332,13 @@ __global__ void __launch_bounds__(kThreads) attn_dq_simt_kernel(const AttnBackwa
 #pragma unroll
         for (int o2 = 8; o2 > 0; o2 >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o2, 16);
         delta[r] = t;
+        excess[r] = 0.f;
         lse[r] = INFINITY;
         if (first + row < it.len) {
             const int64_t at = (int64_t)head * p.N + it.start + first + row;
             const float x = p.lse[at];
             lse[r] = attn_no_weights(x) ? INFINITY : x;  // then all its weights are 2^-inf
+            large |= attn_coarse(x);
             if (tx == 0) p.delta[at] = t;
         }
 #pragma unroll
@@ -329,19 +349,33 @@ __global__ void __launch_bounds__(kThreads) attn_dq_simt_kernel(const AttnBackwa
     key_tiles<T>(p.s, it.tile, sink_tiles, lo);
     const int steps = sink_tiles + it.tile + 1 - lo;
     // 16-bit out: g . out misses delta by out's rounding, so a first sweep
-    // adds up sum_j p (dp - g . out) in fp32, which is what it misses
+    // adds up sum_j p (dp - g . out) in fp32, which is what it misses.  The
+    // same sweep adds up the weights of rows whose |lse| is large.
     const bool active = first + ty / 2 * 2 * R < it.len;  // the warp has a row that exists
     constexpr bool kTwice = DT != DT_F32;
-    float over[R] = {};
-    for (int st = kTwice ? -steps : 0; st < steps; ++st) {
-        if (st == 0 && kTwice) {
+    const bool twice = __syncthreads_or(large) || kTwice;
+    float over[R] = {}, z[R] = {};
+    for (int st = twice ? -steps : 0; st < steps; ++st) {
+        if (st == 0 && twice) {
 #pragma unroll
             for (int r = 0; r < R; ++r) {
 #pragma unroll
-                for (int o2 = 8; o2 > 0; o2 >>= 1) over[r] += __shfl_xor_sync(0xffffffffu, over[r], o2, 16);
-                delta[r] += over[r];
+                for (int o2 = 8; o2 > 0; o2 >>= 1) {
+                    over[r] += __shfl_xor_sync(0xffffffffu, over[r], o2, 16);
+                    z[r] += __shfl_xor_sync(0xffffffffu, z[r], o2, 16);
+                }
+                const bool of_row = attn_coarse(lse[r]);
+                if (of_row) {
+                    over[r] /= z[r];
+                    excess[r] = log2f(z[r]);
+                }
+                if (kTwice || of_row) delta[r] += over[r];
                 const int row = first + ty * R + r;
-                if (tx == 0 && row < it.len) p.delta[(int64_t)head * p.N + it.start + row] = delta[r];
+                if (tx == 0 && row < it.len) {
+                    const int64_t at = (int64_t)head * p.N + it.start + row;
+                    p.delta[at] = delta[r];
+                    if (of_row) p.excess[at] = excess[r];
+                }
             }
         }
         const int tile = st < 0 ? st + steps : st;
@@ -368,12 +402,15 @@ __global__ void __launch_bounds__(kThreads) attn_dq_simt_kernel(const AttnBackwa
 #pragma unroll
             for (int c = 0; c < R; ++c) {
                 const int jj = tx + 16 * c, j = kt * T + jj;
-                float x = s[r][c] * c2;
-                if (p.bias) x += bt[ty * R + r - jj + T - 1];
-                const bool seen = i < it.len && attn_visible(i - j, j, p.s.window, p.s.sinks) &&
-                                  !attn_lone(i, j, p.s.window, p.s.sinks);
-                const float ds = seen ? ex2(x - lse[r]) * (dp[r][c] - delta[r]) : 0.f;
-                if (st < 0) over[r] += ds;
+                const float b = p.bias ? bt[ty * R + r - jj + T - 1] : 0.f;
+                const float x = s[r][c] * c2 + ((b - lse[r]) - excess[r]);
+                const bool seen = i < it.len && attn_visible(i - j, j, p.s.window, p.s.sinks);
+                const float e = seen ? ex2(x) : 0.f;
+                const float ds = seen && !attn_lone(i, j, p.s.window, p.s.sinks) ? e * (dp[r][c] - delta[r]) : 0.f;
+                if (st < 0) {
+                    over[r] += ds;
+                    z[r] += e;
+                }
                 ps[(ty * R + r) * PLD + jj] = ds;
             }
         }
@@ -417,6 +454,7 @@ __global__ void __launch_bounds__(kThreads) attn_dkv_simt_kernel(const AttnBackw
     float* bt = ps + Tile<T, DP>::pbytes / 4;
     float* ls = bt + 2 * T;
     float* de = ls + T;
+    float* ex = de + T;
     const int64_t w = blockIdx.x / p.s.Hk;
     const int kvh = (int)(blockIdx.x % p.s.Hk);
     AttnItem it;
@@ -445,14 +483,17 @@ __global__ void __launch_bounds__(kThreads) attn_dkv_simt_kernel(const AttnBackw
             if (p.bias) load_bias<DT, T>(bt, p.s, p.bias, head, (qt - kt) * T);
             if (threadIdx.x < T) {
                 const int i = qt * T + threadIdx.x;
-                float x = INFINITY, y = 0.f;
+                float x = INFINITY, y = 0.f, z = 0.f;
                 if (i < it.len) {
-                    x = p.lse[(int64_t)head * p.N + it.start + i];
-                    y = p.delta[(int64_t)head * p.N + it.start + i];
+                    const int64_t at = (int64_t)head * p.N + it.start + i;
+                    x = p.lse[at];
+                    y = p.delta[at];
+                    if (attn_coarse(x)) z = p.excess[at];
                     if (attn_no_weights(x)) x = INFINITY;
                 }
                 ls[threadIdx.x] = x;
                 de[threadIdx.x] = y;
+                ex[threadIdx.x] = z;
             }
             __syncthreads();
             if (!active) continue;
@@ -470,10 +511,10 @@ __global__ void __launch_bounds__(kThreads) attn_dkv_simt_kernel(const AttnBackw
 #pragma unroll
                 for (int c = 0; c < R; ++c) {
                     const int ii = tx + 16 * c, i = qt * T + ii;
-                    float x = s[r][c] * c2;
-                    if (p.bias) x += bt[ii - (ty * R + r) + T - 1];
+                    const float b = p.bias ? bt[ii - (ty * R + r) + T - 1] : 0.f;
+                    const float x = s[r][c] * c2 + ((b - ls[ii]) - ex[ii]);
                     const bool seen = i < it.len && attn_visible(i - j, j, p.s.window, p.s.sinks);
-                    const float e = seen ? ex2(x - ls[ii]) : 0.f;
+                    const float e = seen ? ex2(x) : 0.f;
                     ps[(ty * R + r) * PLD + ii] = e;
                     const bool live = seen && !attn_lone(i, j, p.s.window, p.s.sinks);
                     s[r][c] = live ? e * (dp[r][c] - de[ii]) : 0.f;
@@ -620,7 +661,7 @@ constexpr size_t fwd_smem() {
 }
 template <int T, int DP>
 constexpr size_t bwd_smem() {
-    return 4 * Tile<T, DP>::bytes + Tile<T, DP>::pbytes + sizeof(float) * 4 * T;
+    return 4 * Tile<T, DP>::bytes + Tile<T, DP>::pbytes + sizeof(float) * 5 * T;
 }
 
 template <typename K>

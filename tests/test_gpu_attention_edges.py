@@ -183,3 +183,118 @@ def test_bias_of_distances_nobody_sees(dtype, bad, last):
     for x in clean:
         assert torch.equal(got[x], clean[x]), x
     assert not got["grad_bias"][2:].any()
+
+
+def _offsets_of(dtype):
+    return [-6.0e4, 6.0e4] if dtype == torch.float16 else [-1.0e6, -1.0e9, -1.0e30, 1.0e9]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("dim", [64, 128, 40, 63])
+@pytest.mark.parametrize("which", range(4))
+@pytest.mark.parametrize("shape", ["all", "near", "window"])
+def test_bias_of_large_magnitude(dtype, dim, which, shape):
+    """A softmax does not change when all the logits of a row move by the same
+    amount: a large bias on every key that a row sees leaves the results of no
+    bias, and the bounds are those of logits without it.
+
+    all: every bucket.  near: the first bucket alone, so that the rows of short
+    distances see nothing else; to the others its keys are hidden (a large
+    negative value) or the only ones (a positive one).  window: the buckets
+    that a window and its sinks reach, the rest at zero."""
+    values = _offsets_of(dtype)
+    if which >= len(values):
+        pytest.skip("fp16 holds two of the values")
+    value = values[which]
+    window, sinks = (40, 3) if shape == "window" else (0, 0)
+    b = Batch(dtype, 2, 1, dim, [200, 1, 70, 29, 150], window, sinks, [0, 30, 60, 190], seed=53 + which)
+    zero = np.zeros((4, 2))
+    if shape == "all":
+        b.bias[:] = value
+    elif shape == "near":
+        b.bias[0] = value
+        hide = np.where(np.arange(4)[:, None] == 0, 0.0, -np.inf) + zero
+    else:
+        # distances up to 39 are seen within the window, any by the sinks
+        b.bias[:3] = value
+        b.bias[3] = 0
+    q, k, v, grad = (ref.f64(x) for x in (b.q, b.k, b.v, b.grad))
+    got = b.run()
+    assert tbe.tbe_attention_get_error(b.handle) == tbe.TBE_OK
+
+    def want(bias, rows=None):
+        g = grad if rows is None else grad * rows[:, None, None]
+        return ref.attention(q, k, v, b.off, window, sinks, b.scale, b.starts, bias, g, dtype)
+
+    if shape == "all":
+        res, bound = want(zero)
+    else:
+        first = np.concatenate([np.arange(n) for n in np.diff(b.off)])
+        if shape == "near":
+            rows = first < 30  # rows that see the first bucket alone
+            one = want(hide if value > 0 else zero, rows)
+            rest = ref.f64(b.bias)
+            rest[0] = -np.inf
+            two = want(hide if value > 0 else rest, ~rows)
+        else:
+            rows = first < 190  # rows that see buckets of the value alone
+            one = want(zero, rows)
+            far = np.where(np.arange(4)[:, None] == 3, -np.inf if value > 0 else 0.0, 0.0 if value > 0 else -np.inf)
+            two = want(far + zero, ~rows)
+        res, bound = ({}, {})
+        for x in one[0]:
+            if x == "lse":
+                continue
+            if x == "out":
+                pick = rows[:, None, None]
+                res[x], bound[x] = np.where(pick, one[0][x], two[0][x]), np.where(pick, one[1][x], two[1][x])
+            else:
+                res[x], bound[x] = one[0][x] + two[0][x], one[1][x] + two[1][x]
+    for x in res:
+        if x != "lse":
+            ref.close(got[x], res[x], bound[x], x)
+    # the statistic holds the offset, in fp32's steps
+    if shape == "all":
+        lse = res["lse"] + float(b.bias[0, 0]) * np.log2(np.e)
+        assert (np.abs(ref.f64(got["lse"]) - lse) <= bound["lse"] + 4 * ref.F * np.abs(lse)).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("dim", [64, 63, 128])
+@pytest.mark.parametrize("which", range(4))
+def test_decode_with_a_bias_of_large_magnitude(dtype, dim, which):
+    values = _offsets_of(dtype)
+    if which >= len(values):
+        pytest.skip("fp16 holds two of the values")
+    c = Cache(dtype, 4, 2, dim, [3000, 1, 700, 40], 16, 0, 0, [0, 30, 500], seed=54)
+    c.append(0, 10 ** 6)
+    keep = c.bias
+    c.bias = torch.full_like(keep, values[which])
+    got = tbe.tbe_attention_decode(c.handle, c.q, c.k_pages, c.v_pages, c.table, c.n, c.bias)
+    c.bias = torch.zeros_like(keep)
+    want, bound = ref.decode(ref.f64(c.q), [ref.f64(x) for x in c.keys], [ref.f64(x) for x in c.values], 0, 0,
+                             c.scale, c.starts, ref.f64(c.bias), dtype)
+    ref.close(got, want, bound, "out")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("far", [40, 4000])
+@pytest.mark.parametrize("histories", [5, 200])
+def test_bias_of_large_magnitude_in_some_heads(dtype, dim, far, histories):
+    """Beside heads of an ordinary bias, with the table of all distances and
+    with tables per block, and where tiles are taken in turn."""
+    g = np.random.default_rng(far + histories)
+    lengths = g.integers(1, 170, histories)
+    lengths[0] = 300
+    b = Batch(dtype, 4, 2, dim, lengths.tolist(), 0, 0, [0, 3, far], seed=58)
+    b.bias[:, ::2] = -6.0e4 if dtype == torch.float16 else -1.0e9
+    bias = ref.f64(b.bias)
+    bias[:, ::2] = 0
+    got = b.run()
+    assert tbe.tbe_attention_get_error(b.handle) == tbe.TBE_OK
+    want, bound = ref.attention(ref.f64(b.q), ref.f64(b.k), ref.f64(b.v), b.off, 0, 0, b.scale, b.starts, bias,
+                                ref.f64(b.grad), dtype)
+    for x in want:
+        if x != "lse":
+            ref.close(got[x], want[x], bound[x], x)
