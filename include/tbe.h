@@ -453,7 +453,11 @@ int tbe_attention_append(tbe_attention* h, const tbe_rows* k, const tbe_rows* v,
  * and joined; max_length (an upper bound of the lengths; 0: table_width *
  * page_size) only sizes the chunks and the workspace: a length above
  * table_width * page_size or below 0 gives zeros, and one above max_length is
- * refused in the same way (TBE_ERR_INDEX_OOB by tbe_attention_get_error). */
+ * refused in the same way (TBE_ERR_INDEX_OOB by tbe_attention_get_error).
+ * The workspace's bytes are enough for every call of at most batch_size
+ * histories and max_length tokens (here 0 stands for no tokens: give
+ * table_width * page_size where the call is given 0); 0 for arguments outside
+ * the limits. */
 size_t tbe_attention_decode_workspace_bytes(const tbe_attention* h, int32_t batch_size, int64_t max_length);
 int tbe_attention_decode(tbe_attention* h, const tbe_rows* q, const tbe_pages* k_pages,
                          const tbe_pages* v_pages, int32_t num_pages, int32_t page_size,

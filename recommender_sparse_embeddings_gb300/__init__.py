@@ -617,6 +617,8 @@ def tbe_attention_decode_workspace_bytes(h: AttentionHandle, batch_size: int, ma
 
 def make_attention_decode_workspace(h: AttentionHandle, batch_size: int, max_length: int,
                                     device=None, stream=None) -> torch.Tensor:
+    """Workspace of decode calls of up to this many histories and tokens each,
+    on ``stream`` (the current one by default)."""
     n = tbe_attention_decode_workspace_bytes(h, batch_size, max_length)
     if n == 0:
         raise TBEError(TBE_ERR_UNSUPPORTED, "tbe_attention_decode_workspace_bytes")
@@ -629,11 +631,11 @@ def tbe_attention_decode(h: AttentionHandle, q: torch.Tensor, k_pages: torch.Ten
                          workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Attention of each history's newest token (q [B, H, D]) over its paged
     cache of ``lengths`` tokens (the newest included); max_length, an upper
-    bound of them, defaults to the block table's room."""
+    bound of them, is the block table's room if it is not given or 0."""
     b, shape = q.shape[0], q.shape
     rq = _rows(h, q, b, h.heads, "q")
     kp, vp, pages, size, table, width = _cache(h, k_pages, v_pages, block_table, b)
-    most = width * size if max_length is None else int(max_length)
+    most = int(max_length or 0) or width * size
     if out is None:
         out = _new(shape, h.dtype, q.device, stream)
     if workspace is None:

@@ -197,6 +197,15 @@ struct Split {
     int chunk, splits;
 };
 
+// CTAs that a decode call aims at, and those that one chunk makes.
+int64_t decode_target(const tbe_attention* h) {
+    return (int64_t)h->num_sms * (h->s.dtype == TBE_F32 || h->s.D > 128 ? 64 : 16);
+}
+int64_t decode_groups(const tbe_attention* h) {
+    const int gt = attn_decode_heads(h->s.G);
+    return (int64_t)h->s.Hk * ((h->s.G + gt - 1) / gt);
+}
+
 // Visible rows a decode CTA takes: small enough that the batch makes so many
 // CTAs per SM that histories of uneven length leave no SM idle, and at least
 // 256 (the join reads D + 2 floats per chunk and head, under 2 % of a chunk's
@@ -206,14 +215,24 @@ struct Split {
 // 600 rows; 32: 117, 16: 131).
 Split decode_split(const tbe_attention* h, int64_t B, int64_t max_length) {
     const int64_t most = std::max<int64_t>(1, visible_most(h, max_length));
-    const int gt = attn_decode_heads(h->s.G);
-    const int64_t rows = std::max<int64_t>(1, B * h->s.Hk * ((h->s.G + gt - 1) / gt));
-    const int64_t per_sm = h->s.dtype == TBE_F32 || h->s.D > 128 ? 64 : 16;
-    int64_t chunk = most * rows / (h->num_sms * per_sm);
+    const int64_t rows = std::max<int64_t>(1, B * decode_groups(h)), target = decode_target(h);
+    int64_t chunk = (most * rows + target - 1) / target;
     chunk = std::max<int64_t>(256, (chunk + 63) / 64 * 64);
     if (most <= 512) chunk = std::max(chunk, most);  // not worth a second launch
     const int64_t splits = (most + chunk - 1) / chunk;
     return Split{(int)std::min<int64_t>(chunk, INT_MAX / 2), (int)splits};
+}
+
+// (history, chunk) pairs at most of any call of up to B histories and
+// max_length tokens, so that a workspace serves smaller batches too.  Fewer
+// histories make shorter chunks: b histories of m visible rows make at most
+// b (1 + m / chunk) pairs, and a chunk holds at least 256 rows and at least
+// m b groups / target.
+int64_t decode_pairs(const tbe_attention* h, int64_t B, int64_t max_length) {
+    const int64_t most = visible_most(h, max_length);
+    if (most <= 512) return B;
+    const int64_t target = decode_target(h), groups = decode_groups(h);
+    return B + std::min(B * ((most + 255) / 256), (target + groups - 1) / groups);
 }
 
 }  // namespace
@@ -435,9 +454,8 @@ int tbe_attention_append(tbe_attention* h, const tbe_rows* k, const tbe_rows* v,
 }
 
 size_t tbe_attention_decode_workspace_bytes(const tbe_attention* h, int32_t B, int64_t max_length) {
-    if (!h || B < 0 || max_length < 0 || max_length >= (int64_t(1) << 30)) return 0;
-    const Split sp = decode_split(h, B, max_length);
-    return align_up(sizeof(float) * (size_t)B * h->s.H * sp.splits * (h->s.D + 2)) + 256;
+    if (!h || B < 0 || B >= (1 << 24) || max_length < 0 || max_length >= (int64_t(1) << 30)) return 0;
+    return align_up(sizeof(float) * (size_t)decode_pairs(h, B, max_length) * h->s.H * (h->s.D + 2)) + 256;
 }
 
 int tbe_attention_decode(tbe_attention* h, const tbe_rows* q, const tbe_pages* k_pages, const tbe_pages* v_pages,

@@ -298,3 +298,29 @@ def test_bias_of_large_magnitude_in_some_heads(dtype, dim, far, histories):
     for x in want:
         if x != "lse":
             ref.close(got[x], want[x], bound[x], x)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("heads,kv_heads,dim,window", [(16, 4, 128, 0), (2, 2, 64, 0), (8, 1, 64, 3000), (12, 1, 200, 0)])
+def test_a_decode_workspace_serves_smaller_batches(dtype, heads, kv_heads, dim, window):
+    h = tbe.tbe_attention_create(heads, kv_heads, dim, dtype, window, 4 if window else 0)
+    for b, n in ((200, 8192), (128, 8192), (37, 65000), (1, 20000), (5, 600)):
+        room = tbe.tbe_attention_decode_workspace_bytes(h, b, n)
+        table = torch.zeros((b, n), dtype=torch.int32, device="cuda")  # pages of one token, all of them page 0
+        page = torch.zeros((1, 1, kv_heads, dim), dtype=dtype, device="cuda")
+        q = torch.zeros((b, heads, dim), dtype=dtype, device="cuda")
+        space = torch.empty(room, dtype=torch.uint8, device="cuda")
+        for few in sorted(x for x in {1, 2, b // 3, b // 2, 3 * b // 4, b - 1, b} if 0 < x <= b):
+            for most in sorted({0, 1, 255, 257, 513, n // 7, n // 3, n // 2, 2 * n // 3, n - 1, n} - {n + 1}):
+                if most > n:
+                    continue
+                assert 0 < tbe.tbe_attention_decode_workspace_bytes(h, few, most) <= room, (few, most)
+                empty = torch.zeros(few, dtype=torch.int32, device="cuda")
+                tbe.tbe_attention_decode(h, q[:few], page, page, table[:few], empty, max_length=most, workspace=space)
+    assert tbe.tbe_attention_get_error(h) == tbe.TBE_OK
+
+
+def test_decode_with_a_most_of_zero_takes_the_table_s_room():
+    c = Cache(torch.bfloat16, 4, 2, 64, [3000, 20], 16, seed=55)
+    c.append(0, 10 ** 6)
+    assert torch.equal(c.check(max_length=0), c.check())
