@@ -345,8 +345,10 @@ int tbe_per_sample_weight_grad(tbe_handle* h, const void* indices, const void* o
  * fp32; results are rounded once to dtype.  With 16-bit types the softmax
  * weights and the logits' gradients are rounded to dtype where they enter a
  * tensor-core product (their sums stay fp32), as the operands of every
- * 16-bit matrix product are.  fp16 gradients outside fp16's range are lost, as
- * always in fp16: scale the loss.
+ * 16-bit matrix product are.  fp16 results outside fp16's range are lost, as
+ * always in fp16: scale the loss.  (On the way the logits' gradients are held
+ * relative to the largest upstream gradient, so they do not narrow that range
+ * while the sums of a value row's magnitudes stay below 2^14.)
  *
  * A row with no visible key (every visible bias entry -inf, or an empty
  * cache) gives 0 and has zero gradients.  A row whose visible keys all carry a

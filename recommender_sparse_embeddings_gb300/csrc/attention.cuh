@@ -182,6 +182,7 @@ struct AttnBackward {
     void* gk;          // [N, Hk, D]
     void* gv;          // [N, Hk, D]
     float* delta;      // workspace [H, N]: g_i . out_i
+    float* size;       // workspace [H, N], fp16 on the tensor cores: the largest |element| of g_i
     float* excess;     // workspace [H, N], where |lse| >= kCoarse: log2 of the sum of 2^(logit - lse)
     float* bias_part;  // workspace [items, then far items, H, buckets]
     int64_t max_items;
@@ -303,6 +304,15 @@ __device__ __forceinline__ bool attn_visible(int d, int j, int window, int sinks
 // sees nothing (-inf), or all it sees carries a bias of its type's lowest
 // value, which swallowed the logits.
 __device__ __forceinline__ bool attn_no_weights(float lse) { return lse <= -FLT_MAX; }
+
+// The power of two that brings x into [1, 2); 1 for 0, infinities and NaN.
+__device__ __forceinline__ float attn_unit(float x) {
+    const uint32_t e = __float_as_uint(x) & 0x7f800000u;
+    return e == 0u || e >= 0x7f000000u ? 1.f : __uint_as_float(0x7f000000u - e);
+}
+
+// Its inverse.
+__device__ __forceinline__ float attn_unit_back(float s) { return __uint_as_float(0x7f000000u - __float_as_uint(s)); }
 
 // Whether key j is the only one that query i can see.  Its weight is 1
 // whatever the logit, so the logit's gradient is exactly 0, which dp - delta,

@@ -118,7 +118,7 @@ int check_batch(const tbe_attention* h, const void* offsets, int32_t index_dtype
 }
 
 struct Layout {
-    size_t n_items, items, delta, excess, bias_part, far_items, slot_of, far_part, total;
+    size_t n_items, items, delta, excess, size, bias_part, far_items, slot_of, far_part, total;
     int64_t capacity;
     FarWork far;  // sizes only
 };
@@ -152,6 +152,7 @@ Layout make_layout(const tbe_attention* h, int64_t N, int64_t B, bool backward) 
     if (backward) {
         L.delta = take(sizeof(float) * (size_t)N * h->s.H);
         L.excess = take(sizeof(float) * (size_t)N * h->s.H);
+        if (h->s.dtype == TBE_F16 && h->s.D <= 128) L.size = take(sizeof(float) * (size_t)N * h->s.H);
         L.far = far_split(h, N);
         L.bias_part = take(sizeof(float) * (size_t)(L.capacity + L.far.most) * h->s.H * h->s.buckets);
         if (L.far.most > 0) {
@@ -388,6 +389,7 @@ int tbe_attention_backward(tbe_attention* h, const tbe_rows* q, const tbe_rows* 
     p.gv = grad_v;
     p.delta = at<float>(workspace, L.delta);
     p.excess = at<float>(workspace, L.excess);
+    p.size = at<float>(workspace, L.size);
     p.bias_part = at<float>(workspace, L.bias_part);
     p.N = N;
     p.vec = vec_rows(h, *q) && vec_rows(h, *k) && vec_rows(h, *v) && vec_rows(h, *grad_out) && aligned16(out) &&

@@ -30,7 +30,11 @@
 // products run beside the other's arithmetic.
 //
 // P and dS are rounded to the 16-bit type where they enter a product; the
-// bias gradient sums the unrounded fp32 dS.
+// bias gradient sums the unrounded fp32 dS.  fp16's range is narrow (6e-8 to
+// 65504), and dS moves with the upstream gradient: there dS is multiplied by the
+// power of two that brings the largest |g| into [1, 2), of the row in dq and of
+// the CTA's queries in dkv (a product's sum runs over them), and the results
+// divided by it, both exactly.
 #include <type_traits>
 
 #include "attention_mma.cuh"
@@ -192,6 +196,7 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
                                                                                                    const __grid_constant__ AttnMaps maps) {
     using L = Shape<DP>;
     constexpr int NB = L::NB, kHelp = L::W;  // first helper warp: products; then loaders K, V; then bias
+    constexpr bool kUnits = DT == DT_F16;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     __shared__ Bars bars;
@@ -264,13 +269,14 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
         const bool wait_bias = p.bias && !whole;
         const float last_bias = last_bias_of<DT>(p.s, p.bias, head);
         if (p.bias && whole) fill_bias<DT>(bt, p.s, p.bias, head, first + 127, threadIdx.x, L::W * 32);
-        float less = -INFINITY, delta = 0.f;
+        float less = -INFINITY, delta = 0.f, size = 0.f;  // size: the largest |g|
         if (i < it.len) {
             const int64_t at = (int64_t)head * p.N + it.start + i;
             const float x = p.lse[at];
             less = attn_no_weights(x) ? -INFINITY : -x;  // then all its weights are 2^-inf
             if constexpr (L::kPerSm == 1) {
                 delta = p.delta[at];
+                if constexpr (kUnits) size = p.size[at];
             } else {
                 // the estimate of delta, g . out: half of the columns each warpgroup
                 const int64_t token = (int64_t)it.start + i;
@@ -285,16 +291,24 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
                     unpack16<DT>(__ldg(reinterpret_cast<const uint4*>(g + col)), u);
                     unpack16<DT>(__ldg(reinterpret_cast<const uint4*>(o + col)), v);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) delta = fmaf(u[e], v[e], delta);
+                    for (int e = 0; e < 8; ++e) {
+                        delta = fmaf(u[e], v[e], delta);
+                        if constexpr (kUnits) size = fmaxf(size, fabsf(u[e]));
+                    }
                 }
             }
         }
         float* rows = reinterpret_cast<float*>(smem + L::rows);
         if constexpr (L::kPerSm > 1) {
             rows[wg * 128 + row] = delta;
+            rows[(2 + wg) * 128 + row] = size;
             asm volatile("bar.sync 1, %0;" ::"n"(L::W * 32) : "memory");
             delta = rows[row] + rows[128 + row];
+            size = fmaxf(rows[256 + row], rows[384 + row]);
+            if constexpr (kUnits)
+                if (wg == 0 && i < it.len) p.size[(int64_t)head * p.N + it.start + i] = size;
         }
+        const float unit = kUnits ? attn_unit(size) : 1.f;
         asm volatile("bar.sync 1, %0;" ::"n"(L::W * 32) : "memory");  // the table stands; rows is free again
         float sum0 = 0.f, sum1 = 0.f;  // of the row's dS
         // the blocks' loop, for warps with a row whose weights have to be added
@@ -348,7 +362,10 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
                     for (int c = 0; c < 16; c += 2) {
                         x[c] = ex2(x[c]);
                         x[c + 1] = ex2(x[c + 1]);
-                        add2(y[c], y[c + 1], -delta, -delta);
+                        if constexpr (kUnits)
+                            fma2(y[c], y[c + 1], unit, -unit * delta, -unit * delta);
+                        else
+                            add2(y[c], y[c + 1], -delta, -delta);
                         mul2(y[c], y[c + 1], x[c], x[c + 1]);
                         pk[(h + c) / 2] = pack2<DT>(x[c], x[c + 1]);
                     }
@@ -401,11 +418,12 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
             tcgen05_after_sync();
             if (wg == 0 && i < it.len) {
                 const int64_t at = (int64_t)head * p.N + it.start + i;
-                p.delta[at] = delta + over;
+                p.delta[at] = delta + over * attn_unit_back(unit);
                 if (large) p.excess[at] = log2f(z);
             }
             // dq = scale (dQ - over R) / z; the warpgroups take 32 columns each
-            tmem_to_tile<DT>(smem + L::a, t_dq + lanes, wg * 32, row, p.s.scale * inv, t_r + lanes, -over);
+            tmem_to_tile<DT>(smem + L::a, t_dq + lanes, wg * 32, row, p.s.scale * inv * attn_unit_back(unit),
+                             t_r + lanes, -over);
         }
     }
     if (!ok) atomicOr(p.s.error, ERR_TIMEOUT);
@@ -423,12 +441,14 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
                                                                                                     const __grid_constant__ AttnMaps maps) {
     using L = Shape<DP>;
     constexpr int NB = L::NB, kHelp = L::W;
+    constexpr bool kUnits = DT == DT_F16;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     __shared__ Bars bars;
     __shared__ uint32_t tmem_slot;
     // -1: the block's distances have several; -2: and a query's excess is not in its -lse
     __shared__ int same_bucket[2];
+    __shared__ uint32_t warp_size[L::kThreads / 32];  // fp16: the largest |g| that a warp saw
 
     // far items (the longest) first, then the tiles
     const int64_t turn = blockIdx.x / p.s.Hk;
@@ -469,9 +489,27 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
     float* sums = reinterpret_cast<float*>(smem + L::sums);
     for (int i = threadIdx.x; i < L::W * p.s.buckets; i += L::kThreads)
         sums[i / p.s.buckets * kMaxBuckets + i % p.s.buckets] = 0.f;
+    if constexpr (kUnits) {  // the largest |g| of the CTA's queries and heads
+        float size = 0.f;
+        const int from = qb0 * 64, rows = tmin(it.len - from, blocks * 64);
+        for (int g = 0; g < p.s.G; ++g) {
+            const float* of = p.size + (int64_t)(kvh * p.s.G + g) * p.N + it.start + from;
+#pragma unroll 4
+            for (int r = threadIdx.x; r < rows; r += L::kThreads) size = fmaxf(size, of[r]);
+        }
+        const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(size));
+        if (lane == 0) warp_size[warp] = most;
+    }
     tcgen05_before_sync();
     __syncthreads();
     tcgen05_after_sync();
+    float unit = 1.f;
+    if constexpr (kUnits) {
+        uint32_t most = 0;
+#pragma unroll
+        for (int k = 0; k < L::kThreads / 32; ++k) most = tmax(most, warp_size[k]);
+        unit = attn_unit(__uint_as_float(most));
+    }
     const uint32_t tmem = tmem_slot;
     const uint32_t t_dk = tmem + NB * 128, t_dv = t_dk + DP;  // S^T at buf*128, dP^T at buf*128 + 64
     bool ok = true;
@@ -529,7 +567,7 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
             for (int c = 0; c < 2; ++c) {
                 const float less = attn_no_weights(x[c]) ? -INFINITY : one ? (same - x[c]) - excess[c] : -x[c];
                 stat[buf * 192 + lane + 32 * c] = less;
-                stat[buf * 192 + 64 + lane + 32 * c] = -delta[c];
+                stat[buf * 192 + 64 + lane + 32 * c] = -unit * delta[c];
                 if (apart) stat[buf * 192 + 128 + lane + 32 * c] = -excess[c];
             }
             if (lane == 0) same_bucket[buf] = one ? bucket : apart ? -2 : -1;
@@ -628,8 +666,13 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
                         const float4 t = *reinterpret_cast<const float4*>(less + 64 + h + c);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) x[c + e] = ex2(x[c + e]);
-                        add2(y[c], y[c + 1], t.x, t.y);
-                        add2(y[c + 2], y[c + 3], t.z, t.w);
+                        if constexpr (kUnits) {
+                            fma2(y[c], y[c + 1], unit, t.x, t.y);
+                            fma2(y[c + 2], y[c + 3], unit, t.z, t.w);
+                        } else {
+                            add2(y[c], y[c + 1], t.x, t.y);
+                            add2(y[c + 2], y[c + 3], t.z, t.w);
+                        }
                         mul2(y[c], y[c + 1], x[c], x[c + 1]);
                         mul2(y[c + 2], y[c + 3], x[c + 2], x[c + 3]);
                         pk[(h + c) / 2] = pack2<DT>(x[c], x[c + 1]);
@@ -719,7 +762,7 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
                         t += sums[k * kMaxBuckets + b];
                         sums[k * kMaxBuckets + b] = 0.f;
                     }
-                    p.bias_part[(share * p.s.H + kvh * p.s.G + g) * p.s.buckets + b] = t;
+                    p.bias_part[(share * p.s.H + kvh * p.s.G + g) * p.s.buckets + b] = t * attn_unit_back(unit);
                 }
                 asm volatile("bar.sync 1, %0;" ::"n"(L::W * 32) : "memory");
             }
@@ -730,6 +773,7 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
             tcgen05_after_sync();
             // dk into K's tile, dv into V's: 64 columns a warpgroup
             const bool of_v = wg / NB == 1;
+            const float back = of_v ? 1.f : attn_unit_back(unit);
             if (slot >= 0 && q4 * 32 < p.s.sinks) {
                 float* to = p.far.part + ((((int64_t)slot * p.s.Hk + kvh) * 2 + of_v) * p.s.sinks + row) * DP + (wg % NB) * 64;
 #pragma unroll
@@ -739,13 +783,14 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
                     if (row < p.s.sinks)
 #pragma unroll
                         for (int e = 0; e < 16; e += 4)
-                            *reinterpret_cast<float4*>(to + c + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                            *reinterpret_cast<float4*>(to + c + e) =
+                                make_float4(o[e] * back, o[e + 1] * back, o[e + 2] * back, o[e + 3] * back);
                 }
             }
 #pragma unroll
             for (int c = 0; c < 64; c += 32)
                 tmem_to_tile<DT>(smem + (of_v ? L::b : L::a), (of_v ? t_dv : t_dk) + lanes, (wg % NB) * 64 + c, row,
-                                 of_v ? 1.f : p.s.scale);
+                                 of_v ? 1.f : p.s.scale * back);
         }
     }
     if (!ok) atomicOr(p.s.error, ERR_TIMEOUT);
@@ -784,7 +829,7 @@ __global__ void __launch_bounds__(256) attn_far_join_kernel(const AttnBackward p
     }
 }
 
-// delta_i = g_i . out_i of every (token, head): eight lanes a row, 16 bytes a
+// delta_i = g_i . out_i of every (token, head), and in fp16 the largest |g|: eight lanes a row, 16 bytes a
 // lane and step.  Memory-bound (each row of g and out is read once).  For
 // head_dim > 64 only: there dq runs one CTA per SM and shows every microsecond
 // of its start (long window f16 backward 1082 us with this kernel, 1133 with
@@ -796,7 +841,7 @@ __global__ void __launch_bounds__(256) attn_delta_kernel(const AttnBackward p) {
     const int chunk = threadIdx.x % 8;
     const int64_t token = r / p.s.H;
     const int head = (int)(r % p.s.H);
-    float t = 0.f;
+    float t = 0.f, size = 0.f;
     if (token < p.N) {
         const uint16_t* g = static_cast<const uint16_t*>(p.g.data) + token * p.g.token_stride + head * p.g.head_stride;
         const uint16_t* o = static_cast<const uint16_t*>(p.out) + r * p.s.D;
@@ -805,12 +850,21 @@ __global__ void __launch_bounds__(256) attn_delta_kernel(const AttnBackward p) {
             unpack16<DT>(__ldg(reinterpret_cast<const uint4*>(g + c)), x);
             unpack16<DT>(__ldg(reinterpret_cast<const uint4*>(o + c)), y);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) t = fmaf(x[e], y[e], t);
+            for (int e = 0; e < 8; ++e) {
+                t = fmaf(x[e], y[e], t);
+                size = fmaxf(size, fabsf(x[e]));
+            }
         }
     }
 #pragma unroll
-    for (int o = 4; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-    if (chunk == 0 && token < p.N) p.delta[(int64_t)head * p.N + token] = t;
+    for (int o = 4; o > 0; o >>= 1) {
+        t += __shfl_xor_sync(0xffffffffu, t, o);
+        if constexpr (DT == DT_F16) size = fmaxf(size, __shfl_xor_sync(0xffffffffu, size, o));
+    }
+    if (chunk == 0 && token < p.N) {
+        p.delta[(int64_t)head * p.N + token] = t;
+        if constexpr (DT == DT_F16) p.size[(int64_t)head * p.N + token] = size;
+    }
 }
 
 template <int DT, int DP>

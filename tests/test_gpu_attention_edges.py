@@ -324,3 +324,29 @@ def test_decode_with_a_most_of_zero_takes_the_table_s_room():
     c = Cache(torch.bfloat16, 4, 2, 64, [3000, 20], 16, seed=55)
     c.append(0, 10 ** 6)
     assert torch.equal(c.check(max_length=0), c.check())
+
+
+@pytest.mark.parametrize("dim,lengths,window,sinks", [(64, [300, 1, 77], 0, 0), (128, [300, 1, 77], 0, 0),
+                                                      (64, [2500, 40], 70, 5), (128, [2500, 40], 70, 5),
+                                                      (40, [300, 1, 77], 50, 2)])
+def test_fp16_gradients_scale_with_the_upstream_gradient(dim, lengths, window, sinks):
+    """Gradients are linear in the upstream gradient: times a power of two,
+    they are times that power, bit by bit where fp16 holds them as normal
+    numbers.  The logits' gradients on the way may not fit fp16."""
+    b = Batch(torch.float16, 4, 2, dim, lengths, window, sinks, [0, 1, 9, 60], seed=56)
+    b.v = b.v * 4
+    b.grad = torch.where(b.grad.float().abs() < 2.0 ** -6, 2.0 ** -6, b.grad.float()).half()
+    base = b.check()
+    unit = b.grad.clone()
+    for power in (-7, 12):
+        b.grad = (unit.float() * 2.0 ** power).half()
+        assert torch.equal(b.grad.float() * 2.0 ** -power, unit.float())
+        got = b.run()
+        for x in ("grad_q", "grad_k", "grad_v", "grad_bias"):
+            want = (base[x].double() * 2.0 ** power)
+            fits = (base[x].double().abs() < 65504 * 2.0 ** -max(power, 0)) & (base[x].double().abs() < 60000)
+            # rounded once more where the smaller result is subnormal (steps of 2^-24), else the same bits
+            step = 2.0 ** -24 if power < 0 else 2.0 ** (power - 24)
+            assert ((got[x].double() - want).abs() <= step)[fits].all(), (x, power)
+            # the bias gradient sums whole diagonals: few of its entries fit times 2^12
+            assert x == "grad_bias" or fits.float().mean() > 0.5
