@@ -392,7 +392,8 @@ typedef struct {
 } tbe_rows;
 
 /* A paged cache: the row of (page, token of the page, key-value head) starts
- * at data + page*page_stride + token*token_stride + head*head_stride. */
+ * at data + page*page_stride + token*token_stride + head*head_stride (data may
+ * be NULL where there are no pages). */
 typedef struct {
     void* data; /* device */
     int64_t page_stride;

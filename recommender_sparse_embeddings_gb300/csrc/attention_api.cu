@@ -59,8 +59,8 @@ bool rows_ok(const tbe_rows* r, int64_t n) {
     return r && (n == 0 || r->data) && r->token_stride >= 0 && r->head_stride >= 0;
 }
 
-bool pages_ok(const tbe_pages* r) {
-    return r && r->data && r->page_stride >= 0 && r->token_stride >= 0 && r->head_stride >= 0;
+bool pages_ok(const tbe_pages* r, int32_t num_pages) {
+    return r && (num_pages == 0 || r->data) && r->page_stride >= 0 && r->token_stride >= 0 && r->head_stride >= 0;
 }
 
 // The tensor-core kernels take 16-bit rows of up to 128 columns that are
@@ -422,7 +422,8 @@ int tbe_attention_append(tbe_attention* h, const tbe_rows* k, const tbe_rows* v,
     CallRange range("tbe_attention_append");
     const int rc = check_batch(h, offsets, index_dtype, N, B);
     if (rc) return rc;
-    if (!rows_ok(k, N) || !rows_ok(v, N) || !pages_ok(k_pages) || !pages_ok(v_pages)) return TBE_ERR_INVALID_ARG;
+    if (!rows_ok(k, N) || !rows_ok(v, N)) return TBE_ERR_INVALID_ARG;
+    if (!pages_ok(k_pages, num_pages) || !pages_ok(v_pages, num_pages)) return TBE_ERR_INVALID_ARG;
     if (num_pages < 0 || page_size <= 0 || table_width < 0 || (B > 0 && (!before || (table_width > 0 && !block_table))))
         return TBE_ERR_INVALID_ARG;
     if ((int64_t)table_width * page_size >= (int64_t(1) << 30)) return TBE_ERR_UNSUPPORTED;
@@ -467,7 +468,7 @@ int tbe_attention_decode(tbe_attention* h, const tbe_rows* q, const tbe_pages* k
     CallRange range("tbe_attention_decode");
     if (!h || !on_device(h)) return TBE_ERR_INVALID_ARG;
     if (B < 0 || max_length < 0 || num_pages < 0 || page_size <= 0 || table_width < 0) return TBE_ERR_INVALID_ARG;
-    if (!rows_ok(q, B) || !pages_ok(k_pages) || !pages_ok(v_pages)) return TBE_ERR_INVALID_ARG;
+    if (!rows_ok(q, B) || !pages_ok(k_pages, num_pages) || !pages_ok(v_pages, num_pages)) return TBE_ERR_INVALID_ARG;
     if ((bias != nullptr) != (h->s.buckets > 0) || !workspace || !aligned16(workspace)) return TBE_ERR_INVALID_ARG;
     if (B > 0 && (!lengths || !out || (table_width > 0 && !block_table))) return TBE_ERR_INVALID_ARG;
     if ((int64_t)table_width * page_size >= (int64_t(1) << 30) || B >= (1 << 24)) return TBE_ERR_UNSUPPORTED;

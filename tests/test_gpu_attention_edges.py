@@ -350,3 +350,21 @@ def test_fp16_gradients_scale_with_the_upstream_gradient(dim, lengths, window, s
             assert ((got[x].double() - want).abs() <= step)[fits].all(), (x, power)
             # the bias gradient sums whole diagonals: few of its entries fit times 2^12
             assert x == "grad_bias" or fits.float().mean() > 0.5
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_caches_without_pages(dtype):
+    """Users without events: no page is there, every result is zero."""
+    h = tbe.tbe_attention_create(4, 2, 64, dtype)
+    none = torch.empty((0, 16, 2, 64), dtype=dtype, device="cuda")
+    q = torch.ones((3, 4, 64), dtype=dtype, device="cuda")
+    n = torch.zeros(3, dtype=torch.int32, device="cuda")
+    for width in (0, 2):
+        table = torch.zeros((3, width), dtype=torch.int32, device="cuda")
+        out = tbe.tbe_attention_decode(h, q, none, none, table, n)
+        assert not out.any()
+        kv = torch.empty((0, 2, 64), dtype=dtype, device="cuda")
+        tbe.tbe_attention_append(h, kv, kv, torch.zeros(4, dtype=torch.int64, device="cuda"), n, none, none, table)
+    assert tbe.tbe_attention_get_error(h) == tbe.TBE_OK
+    out = tbe.tbe_attention_decode(h, q[:0], none, none, torch.zeros((0, 2), dtype=torch.int32, device="cuda"), n[:0])
+    assert out.shape == (0, 4, 64)
