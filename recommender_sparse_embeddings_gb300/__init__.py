@@ -433,9 +433,13 @@ def tbe_attention_create(heads: int, kv_heads: int, head_dim: int, dtype: torch.
     defaults to head_dim ** -0.5."""
     if dtype not in _DTYPES:
         raise ValueError("dtype must be fp32, fp16 or bf16")
+    firsts = [] if bucket_starts is None else [int(x) for x in bucket_starts]
+    for x in (heads, kv_heads, head_dim, window, sinks, *firsts):
+        if not -2 ** 31 <= x < 2 ** 31:  # a C int32 field would keep its low bits
+            raise ValueError(f"{x} is outside int32")
     lib = load_library()
-    n = 0 if bucket_starts is None else len(bucket_starts)
-    starts = (ctypes.c_int32 * max(n, 1))(*(bucket_starts or ()))
+    n = len(firsts)
+    starts = (ctypes.c_int32 * max(n, 1))(*firsts)
     cfg = _AttentionConfig(_DTYPES[dtype], heads, kv_heads, head_dim, window, sinks,
                            head_dim ** -0.5 if scale is None else scale, n, starts)
     out = ctypes.c_void_p()
