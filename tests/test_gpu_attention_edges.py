@@ -368,3 +368,40 @@ def test_caches_without_pages(dtype):
     assert tbe.tbe_attention_get_error(h) == tbe.TBE_OK
     out = tbe.tbe_attention_decode(h, q[:0], none, none, torch.zeros((0, 2), dtype=torch.int32, device="cuda"), n[:0])
     assert out.shape == (0, 4, 64)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_delta_is_exact(dtype, dim):
+    """Short histories, where out's rounding would show in the logits' gradients
+    most.  A rounding is off by 0.42 u of a value in the 2-norm (u: the unit
+    roundoff).  grad_q carries two, of ds and of the result: 0.6 u, of which 0.7
+    is allowed; g . out with the rounded out (and the weights rounded on its way)
+    for delta would exceed it, as the same arithmetic in 64 bits shows."""
+    g = np.random.default_rng(57)
+    b = Batch(dtype, 4, 4, dim, g.integers(2, 9, 400).tolist(), seed=57)
+    got = b.check()
+    q, k, v, up = (ref.f64(x) for x in (b.q, b.k, b.v, b.grad))
+    want = ref.attention(q, k, v, b.off, 0, 0, b.scale, None, None, up, dtype)[0]["grad_q"]
+
+    def rounded(x):
+        return ref.f64(torch.from_numpy(x).to(dtype))
+
+    exact, estimate = np.zeros_like(q), np.zeros_like(q)
+    for lo, hi in zip(b.off[:-1], b.off[1:]):
+        s = np.einsum("ihd,jhd->hij", q[lo:hi], k[lo:hi]) * b.scale
+        s = np.where(np.tril(np.ones(s.shape[1:], bool)), s, -np.inf)
+        p = np.exp(s - s.max(-1, keepdims=True))
+        total = p.sum(-1, keepdims=True)
+        out = np.einsum("hij,jhd->ihd", p / total, v[lo:hi])
+        coarse = rounded(np.einsum("hij,jhd->ihd", rounded(p) / total, v[lo:hi]))
+        dp = np.einsum("ihd,jhd->hij", up[lo:hi], v[lo:hi])
+        for res, o in ((exact, out), (estimate, coarse)):
+            ds = rounded(p / total * (dp - (o * up[lo:hi]).sum(-1).T[:, :, None]))
+            res[lo:hi] = rounded(b.scale * np.einsum("hij,jhd->ihd", ds, k[lo:hi]))
+
+    def off(x):
+        return np.linalg.norm(x - want) / np.linalg.norm(want) / ref.UNIT[dtype]
+
+    assert off(exact) <= 0.7 < off(estimate), (off(exact), off(estimate))
+    assert off(ref.f64(got["grad_q"])) <= 0.7, off(ref.f64(got["grad_q"]))
