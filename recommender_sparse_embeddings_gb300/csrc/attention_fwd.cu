@@ -16,11 +16,12 @@
 // (kLazy): the weights then stay below 256, exact in fp32 sums and within
 // fp16's range, and the accumulator is rescaled rarely.
 //
-// A batch of many histories has many tiles of few blocks: there two CTAs per SM
-// take the (tile, head) items in turn, so that the next one's tiles are fetched
-// and its first scores computed under the last one's softmax (512 ragged bf16
-// histories 83 -> 73 us).  Few histories get a CTA per item, which the hardware
-// hands out as others end (8 histories of 2048: 73 us, in turn 77).
+// A batch of many histories whose tokens see few keys has many tiles of few
+// blocks: there two CTAs per SM take the (tile, head) items in turn, so that the
+// next one's tiles are fetched and its first scores computed under the last
+// one's softmax (512 ragged bf16 histories 83 -> 73 us).  Else each item gets a
+// CTA, which the hardware hands out as others end (the call's rule has both
+// sides' times).
 //
 // The weights are rounded to the 16-bit type for the second product (the
 // tensor cores' operand type); their sum is kept unrounded in fp32.

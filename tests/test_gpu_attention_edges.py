@@ -405,3 +405,13 @@ def test_delta_is_exact(dtype, dim):
 
     assert off(exact) <= 0.7 < off(estimate), (off(exact), off(estimate))
     assert off(ref.f64(got["grad_q"])) <= 0.7, off(ref.f64(got["grad_q"]))
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_many_histories_whose_tokens_see_many_keys(dim):
+    """Listed tiles, a CTA each: above the length up to which they are taken in
+    turn, one history far longer and one far shorter."""
+    g = np.random.default_rng(dim)
+    lengths = g.integers(250, 330, 135)
+    lengths[7], lengths[90] = 700, 1
+    Batch(torch.bfloat16, 2, 1, dim, lengths.tolist(), 0, 0, [0, 2, 60], seed=59).check()
