@@ -49,7 +49,7 @@ struct Shape {
     static constexpr int W = NB * 8;             // compute warps
     static constexpr int kThreads = W * 32 + 128;
     static constexpr int kPerSm = DP == 64 ? 2 : 1;
-    static constexpr int kStages = DP == 64 ? 3 : 3;
+    static constexpr int kStages = 3;
     static constexpr int kBig = 128 * DP * 2;   // a 128-row tile
     static constexpr int kSmall = 64 * DP * 2;  // a 64-row tile
     static constexpr int a = 0, b = kBig, x = 2 * kBig, y = x + kStages * kSmall;
@@ -396,10 +396,11 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, Shape<DP>::kPerSm) attn_d
                 }
             }
         };
-        if (__any_sync(0xffffffffu, large))
-            walk(std::true_type{});
-        else
+        // (the usual one first: train full bf16 399 -> 394.5 us)
+        if (!__any_sync(0xffffffffu, large))
             walk(std::false_type{});
+        else
+            walk(std::true_type{});
         if (ok) ok = mbar_wait_tight(&bars.last, 0);
         ok = __all_sync(0xffffffffu, ok);
         // delta - e of the row: all warpgroups' sums (every warp comes here)
