@@ -265,8 +265,8 @@ __device__ __forceinline__ int attn_bucket(const AttnShape& s, int d) {
 }
 
 // From this magnitude on (base 2) a bias or a row's statistic is kept apart
-// from the logits: below it their sum in fp32 is off by 2^-19 at most, 3e-6 of
-// a weight.
+// from the logits: below it the sum with a logit of its size is off by 2^-18 at
+// most, 3e-6 of a weight.
 constexpr float kCoarse = 64.f;
 
 // Neither an infinity nor a type's lowest value counts: they hide their keys

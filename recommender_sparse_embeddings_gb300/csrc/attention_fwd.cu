@@ -19,9 +19,9 @@
 // A batch of many histories whose tokens see few keys has many tiles of few
 // blocks: there two CTAs per SM take the (tile, head) items in turn, so that the
 // next one's tiles are fetched and its first scores computed under the last
-// one's softmax (512 ragged bf16 histories 83 -> 73 us).  Else each item gets a
-// CTA, which the hardware hands out as others end (the call's rule has both
-// sides' times).
+// one's softmax (12 % on 512 ragged bf16 histories, 78 us now).  Else each item
+// gets a CTA, which the hardware hands out as others end (the call's rule has
+// both sides' times).
 //
 // The weights are rounded to the 16-bit type for the second product (the
 // tensor cores' operand type); their sum is kept unrounded in fp32.
