@@ -348,7 +348,7 @@ int tbe_per_sample_weight_grad(tbe_handle* h, const void* indices, const void* o
  * 16-bit matrix product are.  fp16 results outside fp16's range are lost, as
  * always in fp16: scale the loss.  (On the way the logits' gradients are held
  * relative to the largest upstream gradient, so they do not narrow that range
- * while the sums of a value row's magnitudes stay below 2^14.)
+ * while the sums of a value row's magnitudes stay below 2^11.)
  *
  * A row with no visible key (every visible bias entry -inf, or an empty
  * cache) gives 0 and has zero gradients.  A row whose visible keys all carry a

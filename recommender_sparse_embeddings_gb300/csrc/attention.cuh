@@ -305,10 +305,13 @@ __device__ __forceinline__ bool attn_visible(int d, int j, int window, int sinks
 // value, which swallowed the logits.
 __device__ __forceinline__ bool attn_no_weights(float lse) { return lse <= -FLT_MAX; }
 
-// The power of two that brings x into [1, 2); 1 for 0, infinities and NaN.
+// The power of two that brings x, the largest |element| of upstream gradients
+// in fp16, into [4, 8): at an ordinary scale about 1, so that small logits'
+// gradients keep the bits they have there, and 2^13 below fp16's largest, for
+// the sum over a value row.  1 for 0, infinities and NaN.
 __device__ __forceinline__ float attn_unit(float x) {
     const uint32_t e = __float_as_uint(x) & 0x7f800000u;
-    return e == 0u || e >= 0x7f000000u ? 1.f : __uint_as_float(0x7f000000u - e);
+    return e < 0x01000000u || e >= 0x7f000000u ? 1.f : __uint_as_float(0x7f000000u + 0x01000000u - e);
 }
 
 // Its inverse.

@@ -32,7 +32,7 @@
 // P and dS are rounded to the 16-bit type where they enter a product; the
 // bias gradient sums the unrounded fp32 dS.  fp16's range is narrow (6e-8 to
 // 65504), and dS moves with the upstream gradient: there dS is multiplied by the
-// power of two that brings the largest |g| into [1, 2), of the row in dq and of
+// power of two that brings the largest |g| into [4, 8), of the row in dq and of
 // the CTA's queries in dkv (a product's sum runs over them), and the results
 // divided by it, both exactly.
 #include <type_traits>
