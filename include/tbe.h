@@ -471,6 +471,137 @@ int tbe_attention_decode(tbe_attention* h, const tbe_rows* q, const tbe_pages* k
 /* As tbe_get_error, for an attention handle. */
 int tbe_attention_get_error(tbe_attention* h, void* stream);
 
+/* ---------------------------------------------------------- layer normalisation */
+
+/* Rows between an encoder's blocks: the residual sum and its layer norm.  Row i
+ * of D elements, all of one dtype (fp32, fp16 or bf16):
+ *   t = x + residual, rounded to dtype (the stream as it is kept; t = x
+ *       without a residual)
+ *   mean = sum_j t_j / D,  var = sum_j (t_j - mean)^2 / D,
+ *   rstd = 1 / sqrt(var + eps)
+ *   out_j = (t_j - mean) * rstd * weight_j + bias_j
+ * and with the upstream gradients g (of out) and u (of t, where the stream goes
+ * on beside the norm; may be absent), xhat = (t - mean) * rstd, a = g * weight:
+ *   grad_x = rstd * (a - mean_j(a) - xhat * mean_j(a * xhat)) + u
+ *   grad_weight = sum over rows of g * xhat,   grad_bias = sum over rows of g
+ * (grad_x is the residual's gradient too).  Sums and statistics are fp32, the
+ * variance is that of the differences from the mean; results are rounded once
+ * to dtype.  Without weight (bias) it counts as 1 (0).
+ *
+ * Rows start at data + row * stride (stride in elements, >= 0; 0 repeats a
+ * row) and their D elements are consecutive.  The fastest path wants 16-byte
+ * aligned rows and D * sizeof(dtype) a multiple of 16.  Results are
+ * deterministic.  Limits: D in [1, 16384], rows < 2^31.
+ *
+ * A handle holds no device memory and no state of a call: it may be used on
+ * several streams at once, on the device of its creation. */
+typedef struct {
+    int32_t dtype; /* tbe_dtype */
+    int32_t dim;   /* D */
+    float eps;     /* >= 0 */
+    int32_t has_weight, has_bias; /* 0 or 1 */
+} tbe_layer_norm_config;
+
+typedef struct tbe_layer_norm tbe_layer_norm;
+
+/* Errors: INVALID_ARG, UNSUPPORTED (limits), NO_MEMORY, CUDA. */
+int tbe_layer_norm_create(const tbe_layer_norm_config* config, tbe_layer_norm** out);
+void tbe_layer_norm_destroy(tbe_layer_norm* h);
+
+/* out: device dtype [rows, D], contiguous.  total: device dtype [rows, D],
+ * contiguous, receives t; NULL exactly where residual is.  stats: device fp32
+ * [2, rows], every row's mean and rstd, kept for the backward call.  weight and
+ * bias: device dtype [D], NULL exactly where the handle has none.  out or total
+ * may be x or residual itself (contiguous, the same rows) but not each other. */
+int tbe_layer_norm_forward(tbe_layer_norm* h, const void* x, int64_t x_stride, const void* residual,
+                           int64_t residual_stride, const void* weight, const void* bias, int64_t num_rows,
+                           void* out, void* total, float* stats, void* stream);
+
+/* Bytes of the backward call's workspace, enough for every call of at most
+ * num_rows rows; 0 for arguments outside the limits.  It starts on a 16-byte
+ * boundary (INVALID_ARG else). */
+size_t tbe_layer_norm_workspace_bytes(const tbe_layer_norm* h, int64_t num_rows);
+
+/* Gradients from the kept stream (t; x where there was no residual), the
+ * forward call's stats, the upstream gradient grad_out and grad_total (u; NULL:
+ * none).  grad_x: device dtype [rows, D], contiguous, may be grad_out or
+ * grad_total itself.  grad_weight and grad_bias: device dtype [D], written, not
+ * added to (zeros where there are no rows); NULL exactly where the handle has
+ * no weight (bias). */
+int tbe_layer_norm_backward(tbe_layer_norm* h, const void* total, int64_t total_stride, const float* stats,
+                            const void* grad_out, int64_t grad_out_stride, const void* grad_total,
+                            int64_t grad_total_stride, const void* weight, int64_t num_rows, void* grad_x,
+                            void* grad_weight, void* grad_bias, void* workspace, size_t workspace_bytes,
+                            void* stream);
+
+/* ------------------------------------------- softmax loss over a table of items */
+
+/* The loss of the item that came next: every row of states x [N, D] is scored
+ * against every row of the items' table w [V, D] (a table of tbe_create, or
+ * weights of its own), and the loss is the softmax cross entropy of the target:
+ *   s_iv = scale * x_i . w_v
+ *   lse_i = log sum_v exp(s_iv)
+ *   loss_i = lse_i - s_i,target(i)
+ * and with the upstream gradient g_i of loss_i
+ *   d_iv = g_i * (exp(s_iv - lse_i) - (v == target(i)))
+ *   grad_x_i = scale * sum_v d_iv w_v,   grad_table_v = scale * sum_i d_iv x_i
+ * A row with a negative target is left out: its loss and its gradients are 0
+ * whatever its elements' and its g's bits are (its lse is still given).  A
+ * target >= V leaves the row out too and raises TBE_ERR_INDEX_OOB.
+ *
+ * The logits are never kept as a whole: the forward call carries a running
+ * maximum and sum, the backward call computes them again in pieces of the
+ * table.  dtype (fp32, fp16 or bf16) is that of x, the table and the gradients;
+ * loss, lse and g are fp32.  Logits, statistics and sums are fp32.  With 16-bit
+ * types d is rounded to dtype where it enters the gradients' products; fp16's
+ * range holds it relative to the largest finite |g| (g itself may be of any
+ * size, the gradients have to fit fp16).  fp32 operands enter the products as
+ * three bf16 terms that sum to them exactly; the six products of those terms
+ * that matter to fp32 are summed.  x and the table are expected to be finite
+ * in rows that are not left out.
+ *
+ * Results are deterministic.  Rows start at data + row * stride (elements,
+ * >= D for the table, >= 0 for x).  The fastest path wants 16-bit rows that are
+ * 16-byte aligned; others are copied into the workspace first.  Limits: D in
+ * [1, 4096], N < 2^30, V in [1, 2^31 - 1024] where there are rows.  A handle
+ * follows the rules of tbe_handle: one device, one stream at a time. */
+typedef struct {
+    int32_t dtype; /* tbe_dtype */
+    int32_t dim;   /* D */
+    float scale;   /* > 0: the inverse temperature */
+} tbe_softmax_loss_config;
+
+typedef struct tbe_softmax_loss tbe_softmax_loss;
+
+/* Creates a handle (a device block of 16 bytes).  Errors: INVALID_ARG,
+ * UNSUPPORTED (limits), NO_MEMORY, CUDA. */
+int tbe_softmax_loss_create(const tbe_softmax_loss_config* config, tbe_softmax_loss** out);
+void tbe_softmax_loss_destroy(tbe_softmax_loss* h);
+
+/* Bytes of workspace of a forward call (backward = 0) or a backward call
+ * (backward = 1, enough for the forward too) of at most N rows and V items; 0
+ * for arguments outside the limits.  It starts on a 16-byte boundary
+ * (INVALID_ARG else). */
+size_t tbe_softmax_loss_workspace_bytes(const tbe_softmax_loss* h, int64_t num_rows, int64_t num_items,
+                                        int32_t backward);
+
+/* targets: device int32 or int64 [N].  loss, lse: device fp32 [N]. */
+int tbe_softmax_loss_forward(tbe_softmax_loss* h, const void* x, int64_t x_stride, const void* table,
+                             int64_t table_stride, const void* targets, int32_t index_dtype, int64_t num_rows,
+                             int64_t num_items, float* loss, float* lse, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
+/* lse: the forward call's.  grad_loss: device fp32 [N].  grad_x: device dtype
+ * [N, D], grad_table: device dtype [V, D], both contiguous and written, not
+ * added to; either may be NULL (not wanted). */
+int tbe_softmax_loss_backward(tbe_softmax_loss* h, const void* x, int64_t x_stride, const void* table,
+                              int64_t table_stride, const void* targets, int32_t index_dtype, int64_t num_rows,
+                              int64_t num_items, const float* lse, const float* grad_loss, void* grad_x,
+                              void* grad_table, void* workspace, size_t workspace_bytes, void* stream);
+
+/* As tbe_get_error, for a loss handle. */
+int tbe_softmax_loss_get_error(tbe_softmax_loss* h, void* stream);
+
 /* ------------------------------------------------------------- diagnostics */
 
 /* Synchronises `stream`, returns the first device-detected error since the

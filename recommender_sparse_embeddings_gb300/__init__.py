@@ -85,6 +85,15 @@ class _Pages(ctypes.Structure):
                 ("head_stride", ctypes.c_int64)]
 
 
+class _LayerNormConfig(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("dim", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("has_weight", ctypes.c_int32), ("has_bias", ctypes.c_int32)]
+
+
+class _SoftmaxLossConfig(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("dim", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
 _lib = None
 
 
@@ -129,6 +138,20 @@ def load_library():
         "tbe_attention_decode": ([P, R, G, G, i32, i32, P, i32, P, i32, i64, P, P, P, ctypes.c_size_t, P],
                                  ctypes.c_int),
         "tbe_attention_get_error": ([P, P], ctypes.c_int),
+        "tbe_layer_norm_create": ([ctypes.POINTER(_LayerNormConfig), ctypes.POINTER(P)], ctypes.c_int),
+        "tbe_layer_norm_destroy": ([P], None),
+        "tbe_layer_norm_forward": ([P, P, i64, P, i64, P, P, i64, P, P, P, P], ctypes.c_int),
+        "tbe_layer_norm_workspace_bytes": ([P, i64], ctypes.c_size_t),
+        "tbe_layer_norm_backward": ([P, P, i64, P, P, i64, P, i64, P, i64, P, P, P, P, ctypes.c_size_t, P],
+                                    ctypes.c_int),
+        "tbe_softmax_loss_create": ([ctypes.POINTER(_SoftmaxLossConfig), ctypes.POINTER(P)], ctypes.c_int),
+        "tbe_softmax_loss_destroy": ([P], None),
+        "tbe_softmax_loss_workspace_bytes": ([P, i64, i64, i32], ctypes.c_size_t),
+        "tbe_softmax_loss_forward": ([P, P, i64, P, i64, P, i32, i64, i64, P, P, P, ctypes.c_size_t, P],
+                                     ctypes.c_int),
+        "tbe_softmax_loss_backward": ([P, P, i64, P, i64, P, i32, i64, i64, P, P, P, P, P, ctypes.c_size_t, P],
+                                      ctypes.c_int),
+        "tbe_softmax_loss_get_error": ([P, P], ctypes.c_int),
         "tbe_get_error": ([P, P], ctypes.c_int),
         "tbe_strerror": ([ctypes.c_int], ctypes.c_char_p),
         "tbe_last_cuda_error": ([], ctypes.c_int),
@@ -655,7 +678,282 @@ def tbe_attention_get_error(h: AttentionHandle, stream=None) -> int:
     return int(load_library().tbe_attention_get_error(h.ptr, _stream(stream)))
 
 
+# ------------------------------------------------------ layer normalisation
+
+
+class LayerNormHandle:
+    """A created layer norm handle; ``close()`` (or garbage collection) calls
+    tbe_layer_norm_destroy."""
+
+    def __init__(self, ptr: ctypes.c_void_p, dim: int, dtype: torch.dtype, weight: bool, bias: bool):
+        self._ptr = ptr
+        self.dim, self.dtype, self.weight, self.bias = dim, dtype, weight, bias
+        self.device = torch.cuda.current_device()
+
+    @property
+    def ptr(self):
+        if self._ptr is None:
+            raise RuntimeError("handle already destroyed")
+        return self._ptr
+
+    def close(self):
+        if self._ptr is not None and _lib is not None:
+            _lib.tbe_layer_norm_destroy(self._ptr)
+        self._ptr = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def tbe_layer_norm_create(dim: int, dtype: torch.dtype, eps: float = 1e-5, weight: bool = True,
+                          bias: bool = True) -> LayerNormHandle:
+    """Layer norm of rows of ``dim`` elements; ``weight`` and ``bias`` say
+    whether it has them."""
+    if dtype not in _DTYPES:
+        raise ValueError("dtype must be fp32, fp16 or bf16")
+    if not -2 ** 31 <= dim < 2 ** 31:  # a C int32 field would keep its low bits
+        raise ValueError(f"{dim} is outside int32")
+    cfg = _LayerNormConfig(_DTYPES[dtype], dim, eps, int(bool(weight)), int(bool(bias)))
+    out = ctypes.c_void_p()
+    _check(load_library().tbe_layer_norm_create(ctypes.byref(cfg), ctypes.byref(out)), "tbe_layer_norm_create")
+    return LayerNormHandle(out, dim, dtype, bool(weight), bool(bias))
+
+
+def tbe_layer_norm_destroy(h: LayerNormHandle):
+    h.close()
+
+
+def _on_device(h, *tensors: Optional[torch.Tensor]) -> None:
+    """Refuses tensors of another device than the handle's: the launches go to
+    that one."""
+    for t in tensors:
+        if t is not None and t.get_device() != h.device:
+            raise ValueError(f"expected tensors on cuda:{h.device}, got {t.device}")
+
+
+def _matrix(t: torch.Tensor, rows: int, dim: int, dtype, name: str):
+    """(address, row stride) of a [rows, dim] CUDA tensor with packed elements."""
+    if t.shape != (rows, dim) or t.dtype is not dtype or not t.is_cuda:
+        _refuse(name, t, (rows, dim), dtype)
+    s0, s1 = t.stride()
+    if s1 != 1 and dim > 1:
+        _refuse(name, t, t.shape, t.dtype)
+    return t.data_ptr(), s0
+
+
+def _param(t: Optional[torch.Tensor], has: bool, dim: int, dtype, name: str):
+    if (t is not None) != has:
+        raise ValueError(f"{name} must be given exactly where the handle has one")
+    return None if t is None else _packed(t, (dim,), dtype, name)
+
+
+def tbe_layer_norm_forward(h: LayerNormHandle, x: torch.Tensor, weight: Optional[torch.Tensor] = None,
+                           bias: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
+                           out: Optional[torch.Tensor] = None, total: Optional[torch.Tensor] = None,
+                           stats: Optional[torch.Tensor] = None, stream=None):
+    """x [N, D] and residual [N, D] (strided rows are fine); returns (out,
+    total, stats): the normalised rows, the kept stream x + residual (x itself
+    without a residual) and fp32 [2, N] of the rows' mean and 1 / deviation."""
+    if x.dim() != 2:
+        raise ValueError("x must be [N, D]")
+    n, d, dt = x.shape[0], h.dim, h.dtype
+    px, sx = _matrix(x, n, d, dt, "x")
+    pr, sr, pt = None, 0, None
+    if out is None:
+        out = _new((n, d), dt, x.device, stream)
+    if stats is None:
+        stats = _new((2, n), torch.float32, x.device, stream)
+    if residual is not None:
+        pr, sr = _matrix(residual, n, d, dt, "residual")
+        if total is None:
+            total = _new((n, d), dt, x.device, stream)
+        pt = _packed(total, (n, d), dt, "total")
+    elif total is not None:
+        raise ValueError("total without residual")
+    _on_device(h, x, residual, weight, bias, out, total, stats)
+    rc = load_library().tbe_layer_norm_forward(
+        h.ptr, px, sx, pr, sr, _param(weight, h.weight, d, dt, "weight"), _param(bias, h.bias, d, dt, "bias"), n,
+        _packed(out, (n, d), dt, "out"), pt, _packed(stats, (2, n), torch.float32, "stats"), _stream(stream))
+    _check(rc, "tbe_layer_norm_forward")
+    return out, x if residual is None else total, stats
+
+
+def tbe_layer_norm_workspace_bytes(h: LayerNormHandle, num_rows: int) -> int:
+    return int(load_library().tbe_layer_norm_workspace_bytes(h.ptr, num_rows))
+
+
+def make_layer_norm_workspace(h: LayerNormHandle, num_rows: int, device=None, stream=None) -> torch.Tensor:
+    """Workspace of backward calls of up to this many rows, on ``stream`` (the
+    current one by default)."""
+    n = tbe_layer_norm_workspace_bytes(h, num_rows)
+    if n == 0:
+        raise TBEError(TBE_ERR_UNSUPPORTED, "tbe_layer_norm_workspace_bytes")
+    return _new((n,), torch.uint8, device or "cuda", stream, False)
+
+
+def tbe_layer_norm_backward(h: LayerNormHandle, total: torch.Tensor, stats: torch.Tensor, grad_out: torch.Tensor,
+                            weight: Optional[torch.Tensor] = None, grad_total: Optional[torch.Tensor] = None,
+                            grad_x: Optional[torch.Tensor] = None, grad_weight: Optional[torch.Tensor] = None,
+                            grad_bias: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                            stream=None):
+    """Gradients (grad_x, grad_weight, grad_bias) from a forward call's total
+    and stats and the upstream gradients of its out and (optionally) its total;
+    grad_x is the residual's gradient too.  What the handle has no parameter
+    for is None."""
+    if total.dim() != 2:
+        raise ValueError("total must be [N, D]")
+    n, d, dt = total.shape[0], h.dim, h.dtype
+    pt, st = _matrix(total, n, d, dt, "total")
+    pg, sg = _matrix(grad_out, n, d, dt, "grad_out")
+    pu, su = (None, 0) if grad_total is None else _matrix(grad_total, n, d, dt, "grad_total")
+    if grad_x is None:
+        grad_x = _new((n, d), dt, total.device, stream)
+    if grad_weight is None and h.weight:
+        grad_weight = _new((d,), dt, total.device, stream)
+    if grad_bias is None and h.bias:
+        grad_bias = _new((d,), dt, total.device, stream)
+    if workspace is None:
+        workspace = make_layer_norm_workspace(h, n, total.device, stream)
+    _on_device(h, total, stats, grad_out, grad_total, weight, grad_x, grad_weight, grad_bias, workspace)
+    rc = load_library().tbe_layer_norm_backward(
+        h.ptr, pt, st, _packed(stats, (2, n), torch.float32, "stats"), pg, sg, pu, su,
+        _param(weight, h.weight, d, dt, "weight"), n, _packed(grad_x, (n, d), dt, "grad_x"),
+        _param(grad_weight, h.weight, d, dt, "grad_weight"), _param(grad_bias, h.bias, d, dt, "grad_bias"),
+        _space(workspace), workspace.numel(), _stream(stream))
+    _check(rc, "tbe_layer_norm_backward")
+    return grad_x, grad_weight, grad_bias
+
+
+# ---------------------------------------- softmax loss over a table of items
+
+
+class SoftmaxLossHandle:
+    """A created loss handle; ``close()`` (or garbage collection) calls
+    tbe_softmax_loss_destroy."""
+
+    def __init__(self, ptr: ctypes.c_void_p, dim: int, dtype: torch.dtype):
+        self._ptr = ptr
+        self.dim, self.dtype = dim, dtype
+        self.device = torch.cuda.current_device()
+
+    @property
+    def ptr(self):
+        if self._ptr is None:
+            raise RuntimeError("handle already destroyed")
+        return self._ptr
+
+    def close(self):
+        if self._ptr is not None and _lib is not None:
+            _lib.tbe_softmax_loss_destroy(self._ptr)
+        self._ptr = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def tbe_softmax_loss_create(dim: int, dtype: torch.dtype, scale: float = 1.0) -> SoftmaxLossHandle:
+    """Softmax cross entropy of rows of ``dim`` elements over a table of items;
+    logits are ``scale`` times the products (an inverse temperature)."""
+    if dtype not in _DTYPES:
+        raise ValueError("dtype must be fp32, fp16 or bf16")
+    if not -2 ** 31 <= dim < 2 ** 31:  # a C int32 field would keep its low bits
+        raise ValueError(f"{dim} is outside int32")
+    cfg = _SoftmaxLossConfig(_DTYPES[dtype], dim, scale)
+    out = ctypes.c_void_p()
+    _check(load_library().tbe_softmax_loss_create(ctypes.byref(cfg), ctypes.byref(out)), "tbe_softmax_loss_create")
+    return SoftmaxLossHandle(out, dim, dtype)
+
+
+def tbe_softmax_loss_destroy(h: SoftmaxLossHandle):
+    h.close()
+
+
+def tbe_softmax_loss_workspace_bytes(h: SoftmaxLossHandle, num_rows: int, num_items: int,
+                                     backward: bool = False) -> int:
+    return int(load_library().tbe_softmax_loss_workspace_bytes(h.ptr, num_rows, num_items, int(backward)))
+
+
+def make_softmax_loss_workspace(h: SoftmaxLossHandle, num_rows: int, num_items: int, backward: bool = False,
+                                device=None, stream=None) -> torch.Tensor:
+    """Workspace of forward calls (``backward``: of both) of up to this many
+    rows and items, on ``stream`` (the current one by default)."""
+    n = tbe_softmax_loss_workspace_bytes(h, num_rows, num_items, backward)
+    if n == 0:
+        raise TBEError(TBE_ERR_UNSUPPORTED, "tbe_softmax_loss_workspace_bytes")
+    return _new((n,), torch.uint8, device or "cuda", stream, False)
+
+
+def _loss_operands(h: SoftmaxLossHandle, x: torch.Tensor, table: torch.Tensor, targets: torch.Tensor):
+    """(x, its stride, table, its stride, targets, their type, rows, items)."""
+    if x.dim() != 2 or table.dim() != 2:
+        raise ValueError("x must be [N, D], table [V, D]")
+    if targets.dtype not in (torch.int32, torch.int64):
+        raise ValueError("targets must be int32 or int64")
+    n, v = x.shape[0], table.shape[0]
+    return (*_matrix(x, n, h.dim, h.dtype, "x"), *_matrix(table, v, h.dim, h.dtype, "table"),
+            _packed(targets, (n,), targets.dtype, "targets"), TBE_I64 if targets.dtype is torch.int64 else TBE_I32,
+            n, v)
+
+
+def tbe_softmax_loss_forward(h: SoftmaxLossHandle, x: torch.Tensor, table: torch.Tensor, targets: torch.Tensor,
+                             loss: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                             workspace: Optional[torch.Tensor] = None, stream=None):
+    """x [N, D] states and table [V, D] (strided rows are fine), targets [N]
+    (the item of each row; negative: the row is left out); returns (loss, lse),
+    both fp32 [N]."""
+    ops = _loss_operands(h, x, table, targets)
+    n, v = ops[-2:]
+    if loss is None:
+        loss = _new((n,), torch.float32, x.device, stream)
+    if lse is None:
+        lse = _new((n,), torch.float32, x.device, stream)
+    if workspace is None:
+        workspace = make_softmax_loss_workspace(h, n, v, False, x.device, stream)
+    _on_device(h, x, table, targets, loss, lse, workspace)
+    rc = load_library().tbe_softmax_loss_forward(
+        h.ptr, *ops, _packed(loss, (n,), torch.float32, "loss"), _packed(lse, (n,), torch.float32, "lse"),
+        _space(workspace), workspace.numel(), _stream(stream))
+    _check(rc, "tbe_softmax_loss_forward")
+    return loss, lse
+
+
+def tbe_softmax_loss_backward(h: SoftmaxLossHandle, x: torch.Tensor, table: torch.Tensor, targets: torch.Tensor,
+                              lse: torch.Tensor, grad_loss: torch.Tensor, grad_x: Optional[torch.Tensor] = None,
+                              grad_table: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                              want=(True, True), stream=None):
+    """Gradients (grad_x [N, D], grad_table [V, D]) from a forward call's lse and
+    the upstream gradient of its losses (fp32 [N]); ``want`` says which of them
+    are computed (the other is None)."""
+    ops = _loss_operands(h, x, table, targets)
+    n, v = ops[-2:]
+    if grad_x is None and want[0]:
+        grad_x = _new((n, h.dim), h.dtype, x.device, stream)
+    if grad_table is None and want[1]:
+        grad_table = _new((v, h.dim), h.dtype, x.device, stream)
+    if workspace is None:
+        workspace = make_softmax_loss_workspace(h, n, v, True, x.device, stream)
+    _on_device(h, x, table, targets, lse, grad_loss, grad_x, grad_table, workspace)
+    rc = load_library().tbe_softmax_loss_backward(
+        h.ptr, *ops, _packed(lse, (n,), torch.float32, "lse"), _packed(grad_loss, (n,), torch.float32, "grad_loss"),
+        None if grad_x is None else _packed(grad_x, (n, h.dim), h.dtype, "grad_x"),
+        None if grad_table is None else _packed(grad_table, (v, h.dim), h.dtype, "grad_table"),
+        _space(workspace), workspace.numel(), _stream(stream))
+    _check(rc, "tbe_softmax_loss_backward")
+    return grad_x, grad_table
+
+
+def tbe_softmax_loss_get_error(h: SoftmaxLossHandle, stream=None) -> int:
+    return int(load_library().tbe_softmax_loss_get_error(h.ptr, _stream(stream)))
+
+
 __all__ = [n for n in dir() if n.startswith("tbe_") or n.startswith("TBE_")] + [
     "Handle", "TBEError", "WorkspaceLayout", "load_library", "declared_functions",
     "make_workspace", "library_path", "AttentionHandle", "make_attention_workspace",
-    "make_attention_decode_workspace"]
+    "make_attention_decode_workspace", "LayerNormHandle", "make_layer_norm_workspace", "SoftmaxLossHandle",
+    "make_softmax_loss_workspace"]
