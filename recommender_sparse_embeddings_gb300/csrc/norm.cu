@@ -23,7 +23,9 @@ struct tbe_layer_norm {
 namespace {
 
 constexpr int kMaxNormDim = 16384;
-constexpr int kThreads = 256;
+// CTAs of the backward kernel per SM at most: bounds its partial sums (the
+// wide rows' CTAs are large, fewer fit).
+constexpr int most_ctas(int D) { return D <= 2048 ? 8 : D <= 4096 ? 4 : 2; }
 
 struct CallRange {
     explicit CallRange(const char* name) { nvtxRangePushA(name); }
@@ -47,94 +49,343 @@ struct NormBackward {
     const float* stats;
     int D;
     void *gx, *gw, *gb;
-    float* part;  // [CTAs][2][D]
+    float* part;  // [CTAs][2][D]: sums of g xhat and of g over a CTA's rows
 };
 
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-    for (int o = 16; o > 0; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
+// Both kernels stream rows that stay in registers from the load to the store:
+// T threads hold a row, thread t the accesses t, t + T, ... (K of them) of E
+// consecutive elements (16 bytes, or one element where rows are not aligned).
+// A group of T <= 32 lanes sums by shuffles alone and a CTA holds several; a
+// wider row is a CTA's.  Groups take rows in turn (the grid fills the GPU
+// once), so weights stay in registers and the next row is fetched before this
+// one's sums.
+template <int DT, int E>
+struct Access {
+    using Raw = uint4;
+};
+template <>
+struct Access<DT_F32, 1> {
+    using Raw = float;
+};
+template <>
+struct Access<DT_F16, 1> {
+    using Raw = unsigned short;
+};
+template <>
+struct Access<DT_BF16, 1> {
+    using Raw = unsigned short;
+};
+
+template <int DT, int E>
+using Raw = typename Access<DT, E>::Raw;
+
+template <int DT, int E>
+__device__ __forceinline__ void to_floats(const Raw<DT, E>& r, float* f) {
+    if constexpr (E > 1)
+        unpack16<DT>(r, f);
+    else if constexpr (DT == DT_F32)
+        f[0] = r;
+    else
+        f[0] = DT == DT_F16 ? h_bits_to_float(r) : bf16_bits_to_float(r);
 }
 
-__device__ __forceinline__ float cta_sum(float v) {
-    __shared__ float part[kThreads / 32];
-    v = warp_sum(v);
-    __syncthreads();
-    if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = v;
-    __syncthreads();
-    float t = 0.f;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) t += part[w];
-    return t;
-}
-
-// One CTA a row, three passes over it.
 template <int DT>
-__global__ void __launch_bounds__(kThreads) norm_forward_kernel(const NormForward p) {
-    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
-        const int64_t at = row * p.D;
-        const void* t = p.residual ? p.total : p.x;
-        const int64_t t0 = p.residual ? at : row * p.x_stride;
-        if (p.residual)
-            for (int j = threadIdx.x; j < p.D; j += kThreads)
-                store_elem<DT>(p.total, at + j,
-                               load_elem<DT>(p.x, row * p.x_stride + j) +
-                                   load_elem<DT>(p.residual, row * p.residual_stride + j));
-        auto value = [&](int j) {  // (written above: no read-only load)
-            if constexpr (DT == DT_F32) return static_cast<const float*>(t)[t0 + j];
-            if constexpr (DT == DT_F16) return __half2float(static_cast<const __half*>(t)[t0 + j]);
-            return __bfloat162float(static_cast<const __nv_bfloat16*>(t)[t0 + j]);
-        };
-        float s = 0.f;
-        for (int j = threadIdx.x; j < p.D; j += kThreads) s += value(j);
-        const float mean = cta_sum(s) / p.D;
-        s = 0.f;
-        for (int j = threadIdx.x; j < p.D; j += kThreads) s += (value(j) - mean) * (value(j) - mean);
-        const float rstd = 1.f / sqrtf(cta_sum(s) / p.D + p.eps);
-        for (int j = threadIdx.x; j < p.D; j += kThreads)
-            store_elem<DT>(p.out, at + j, (value(j) - mean) * rstd * (p.weight ? load_elem<DT>(p.weight, j) : 1.f) +
-                                              (p.bias ? load_elem<DT>(p.bias, j) : 0.f));
-        if (threadIdx.x == 0) {
+__device__ __forceinline__ uint32_t pair_bits(float a, float b) {
+    uint32_t r;
+    if constexpr (DT == DT_F16)
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    else
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    return r;
+}
+
+template <int DT, int E>
+__device__ __forceinline__ Raw<DT, E> from_floats(const float* f) {
+    if constexpr (DT == DT_F32) {
+        if constexpr (E == 1)
+            return f[0];
+        else
+            return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                              __float_as_uint(f[3]));
+    } else if constexpr (E == 1) {
+        return (unsigned short)pair_bits<DT>(f[0], 0.f);
+    } else {
+        return make_uint4(pair_bits<DT>(f[0], f[1]), pair_bits<DT>(f[2], f[3]), pair_bits<DT>(f[4], f[5]),
+                          pair_bits<DT>(f[6], f[7]));
+    }
+}
+
+// The thread's K accesses of one row of D elements, zeros behind its end.
+template <int DT, int E, int K, int T>
+struct RowPart {
+    Raw<DT, E> r[K];
+
+    __device__ __forceinline__ void load(const void* base, int64_t at, int D, int t) {
+        const Raw<DT, E>* p =
+            reinterpret_cast<const Raw<DT, E>*>(static_cast<const char*>(base) + at * elem_bytes(DT));
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            r[k] = Raw<DT, E>{};
+            if ((k * T + t) * E < D) r[k] = __ldg(p + k * T + t);
+        }
+    }
+    __device__ __forceinline__ void store(void* base, int64_t at, int D, int t) const {
+        Raw<DT, E>* p = reinterpret_cast<Raw<DT, E>*>(static_cast<char*>(base) + at * elem_bytes(DT));
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if ((k * T + t) * E < D) p[k * T + t] = r[k];
+    }
+    __device__ __forceinline__ void get(float* f) const {
+#pragma unroll
+        for (int k = 0; k < K; ++k) to_floats<DT, E>(r[k], f + k * E);
+    }
+    __device__ __forceinline__ void set(const float* f) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) r[k] = from_floats<DT, E>(f + k * E);
+    }
+};
+
+// Sums of N values over the T threads of a row, in all of them.  Wider groups
+// than a warp join through shared memory; `turn` alternates between its two
+// halves, so one barrier a sum is enough.
+template <int T, int N>
+__device__ __forceinline__ void row_sums(float (&v)[N], int& turn) {
+#pragma unroll
+    for (int o = (T < 32 ? T : 32) / 2; o > 0; o /= 2)
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+    if constexpr (T > 32) {
+        __shared__ float part[2][N][T / 32];
+        if (threadIdx.x % 32 == 0)
+#pragma unroll
+            for (int i = 0; i < N; ++i) part[turn][i][threadIdx.x / 32] = v[i];
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            float s = part[turn][i][threadIdx.x % (T / 32)];
+#pragma unroll
+            for (int o = T / 64; o > 0; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
+            v[i] = s;
+        }
+        turn ^= 1;
+    }
+}
+
+constexpr int cta_threads(int T) { return T > 32 ? T : 256; }
+
+template <int DT, int E, int K, int T>
+__global__ void __launch_bounds__(cta_threads(T)) norm_forward_kernel(const NormForward p) {
+    using Part = RowPart<DT, E, K, T>;
+    constexpr int kGroups = cta_threads(T) / T, M = E * K;
+    const int t = threadIdx.x % T;
+    const int64_t step = (int64_t)gridDim.x * kGroups;
+    const float width = p.D;
+    Part w{}, b{};
+    if (p.weight) w.load(p.weight, 0, p.D, t);
+    if (p.bias) b.load(p.bias, 0, p.D, t);
+    int64_t row = (int64_t)blockIdx.x * kGroups + threadIdx.x / T;
+    Part x{}, r{};
+    auto fetch = [&](int64_t i) {
+        if (i >= p.rows) return;
+        x.load(p.x, i * p.x_stride, p.D, t);
+        if (p.residual) r.load(p.residual, i * p.residual_stride, p.D, t);
+    };
+    fetch(row);
+    int turn = 0;
+    // (the groups of a warp run alike: its first row decides)
+    for (; row - threadIdx.x % 32 / T < p.rows; row += step) {
+        float f[M], s[1] = {0.f};
+        x.get(f);
+        Part keep{};
+        if (p.residual) {
+            float q[M];
+            r.get(q);
+#pragma unroll
+            for (int i = 0; i < M; ++i) f[i] += q[i];
+            keep.set(f);
+            keep.get(f);
+        }
+        fetch(row + step);
+#pragma unroll
+        for (int i = 0; i < M; ++i) s[0] += f[i];
+        row_sums<T>(s, turn);
+        const float mean = s[0] / width;  // (exact where all elements are the same)
+        s[0] = 0.f;
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if ((k * T + t) * E < p.D)
+#pragma unroll
+                for (int i = k * E; i < k * E + E; ++i) {
+                    f[i] -= mean;
+                    s[0] = fmaf(f[i], f[i], s[0]);
+                }
+        row_sums<T>(s, turn);
+        const float rstd = rsqrtf(s[0] / width + p.eps);
+        if (row >= p.rows) continue;
+        if (p.residual) keep.store(p.total, row * p.D, p.D, t);
+        float q[M];
+#pragma unroll
+        for (int i = 0; i < M; ++i) f[i] *= rstd;
+        if (p.weight) {
+            w.get(q);
+#pragma unroll
+            for (int i = 0; i < M; ++i) f[i] *= q[i];
+        }
+        if (p.bias) {
+            b.get(q);
+#pragma unroll
+            for (int i = 0; i < M; ++i) f[i] += q[i];
+        }
+        keep.set(f);
+        keep.store(p.out, row * p.D, p.D, t);
+        if (t == 0) {
             p.stats[row] = mean;
             p.stats[p.rows + row] = rstd;
         }
     }
 }
 
-template <int DT>
-__global__ void __launch_bounds__(kThreads) norm_backward_kernel(const NormBackward p) {
-    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
-        const float mean = p.stats[row], rstd = p.stats[p.rows + row];
-        float s = 0.f, sx = 0.f;
-        for (int j = threadIdx.x; j < p.D; j += kThreads) {
-            const float a = load_elem<DT>(p.g, row * p.g_stride + j) * (p.weight ? load_elem<DT>(p.weight, j) : 1.f);
-            s += a;
-            sx += a * (load_elem<DT>(p.total, row * p.total_stride + j) - mean) * rstd;
+// Wide rows of 1024 threads keep the weights' sums in shared memory (64
+// registers a thread hold the row alone).
+template <int E, int K, int T>
+constexpr bool sums_in_smem() {
+    return T == 1024;
+}
+
+template <int DT, int E, int K, int T>
+__global__ void __launch_bounds__(cta_threads(T)) norm_backward_kernel(const NormBackward p) {
+    using Part = RowPart<DT, E, K, T>;
+    constexpr int kThreads = cta_threads(T), kGroups = kThreads / T, M = E * K;
+    constexpr bool kSmem = sums_in_smem<E, K, T>();
+    extern __shared__ float room[];  // kSmem: [2 M][threads]; several groups: [M][threads]
+    const int t = threadIdx.x % T;
+    const int64_t step = (int64_t)gridDim.x * kGroups;
+    const float width = p.D;
+    const bool params = p.gw || p.gb;
+    Part w{};
+    if (p.weight) w.load(p.weight, 0, p.D, t);
+    int64_t row = (int64_t)blockIdx.x * kGroups + threadIdx.x / T;
+    Part x{}, g{}, u{};
+    float mean = 0.f, rstd = 0.f;
+    auto fetch = [&](int64_t i) {
+        if (i >= p.rows) {  // a group without a row adds nothing to the sums
+            x = g = Part{};
+            mean = rstd = 0.f;
+            return;
         }
-        s = cta_sum(s) / p.D;
-        sx = cta_sum(sx) / p.D;
-        for (int j = threadIdx.x; j < p.D; j += kThreads) {
-            const float a = load_elem<DT>(p.g, row * p.g_stride + j) * (p.weight ? load_elem<DT>(p.weight, j) : 1.f);
-            const float hat = (load_elem<DT>(p.total, row * p.total_stride + j) - mean) * rstd;
-            store_elem<DT>(p.gx, row * p.D + j,
-                           rstd * (a - s - hat * sx) + (p.u ? load_elem<DT>(p.u, row * p.u_stride + j) : 0.f));
+        x.load(p.total, i * p.total_stride, p.D, t);
+        g.load(p.g, i * p.g_stride, p.D, t);
+        if (p.u) u.load(p.u, i * p.u_stride, p.D, t);
+        mean = __ldg(p.stats + i);
+        rstd = __ldg(p.stats + p.rows + i);
+    };
+    float sw[kSmem ? 1 : M], sb[kSmem ? 1 : M];
+    if constexpr (kSmem) {
+#pragma unroll
+        for (int i = 0; i < 2 * M; ++i) room[i * kThreads + threadIdx.x] = 0.f;
+    } else {
+#pragma unroll
+        for (int i = 0; i < M; ++i) sw[i] = sb[i] = 0.f;
+    }
+    fetch(row);
+    int turn = 0;
+    for (; row - threadIdx.x % 32 / T < p.rows; row += step) {
+        float h[M], a[M], q[M], s[2] = {0.f, 0.f};
+        x.get(h);
+        g.get(a);
+        const float m = mean, is = rstd;
+        Part on = u;
+        fetch(row + step);
+        // (accesses behind the row's end hold g = 0, and their xhat meets nothing else)
+#pragma unroll
+        for (int i = 0; i < M; ++i) {
+            h[i] = (h[i] - m) * is;
+            if constexpr (kSmem) {
+                if (params) {
+                    room[i * kThreads + threadIdx.x] = fmaf(a[i], h[i], room[i * kThreads + threadIdx.x]);
+                    room[(M + i) * kThreads + threadIdx.x] += a[i];
+                }
+            } else {
+                sw[i] = fmaf(a[i], h[i], sw[i]);
+                sb[i] += a[i];
+            }
+        }
+        if (p.weight) {
+            w.get(q);
+#pragma unroll
+            for (int i = 0; i < M; ++i) a[i] *= q[i];
+        }
+#pragma unroll
+        for (int i = 0; i < M; ++i) {
+            s[0] += a[i];
+            s[1] = fmaf(a[i], h[i], s[1]);
+        }
+        row_sums<T>(s, turn);
+        s[0] /= width;
+        s[1] /= width;
+        if (row >= p.rows) continue;
+        if (p.u) {
+            on.get(q);
+#pragma unroll
+            for (int i = 0; i < M; ++i) a[i] = fmaf(is, (a[i] - s[0]) - h[i] * s[1], q[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < M; ++i) a[i] = is * ((a[i] - s[0]) - h[i] * s[1]);
+        }
+        on.set(a);
+        on.store(p.gx, row * p.D, p.D, t);
+    }
+    if (!params) return;
+    // the CTA's sums of both kinds, its groups in order
+    float* part = p.part + (int64_t)blockIdx.x * 2 * p.D;
+#pragma unroll
+    for (int kind = 0; kind < 2; ++kind) {
+        if constexpr (kGroups > 1) {
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < M; ++i) room[i * kThreads + threadIdx.x] = kind ? sb[i] : sw[i];
+            __syncthreads();
+        }
+        // element k * T * E + t * E + e of the row: sum i = k * E + e of thread t
+        for (int y = threadIdx.x; y < M * T; y += kThreads) {
+            const int i = y / T, lane = y % T, j = (i / E) * T * E + lane * E + i % E;
+            if (j >= p.D) continue;
+            float v = 0.f;
+            if constexpr (kGroups > 1) {
+#pragma unroll
+                for (int o = 0; o < kGroups; ++o) v += room[i * kThreads + o * T + lane];
+            } else if constexpr (kSmem) {
+                v = room[(kind * M + i) * kThreads + lane];
+            } else {
+#pragma unroll
+                for (int z = 0; z < M; ++z)
+                    if (z == i) v = kind ? sb[z] : sw[z];
+            }
+            part[(int64_t)kind * p.D + j] = v;
         }
     }
 }
 
-// One thread a column.
+// The CTAs' partial sums joined: 32 columns a CTA, 32 of its threads share a
+// column's partials and add up their sums in order.
 template <int DT>
-__global__ void __launch_bounds__(kThreads) norm_weight_kernel(const NormBackward p) {
-    const int j = blockIdx.x * kThreads + threadIdx.x;
-    if (j >= p.D) return;
-    float w = 0.f, b = 0.f;
-    for (int64_t row = 0; row < p.rows; ++row) {
-        const float g = load_elem<DT>(p.g, row * p.g_stride + j);
-        w += g * (load_elem<DT>(p.total, row * p.total_stride + j) - p.stats[row]) * p.stats[p.rows + row];
-        b += g;
-    }
-    if (p.gw) store_elem<DT>(p.gw, j, w);
-    if (p.gb) store_elem<DT>(p.gb, j, b);
+__global__ void __launch_bounds__(1024) norm_join_kernel(const NormBackward p, int parts) {
+    chain_wait();
+    __shared__ float s[32][33];
+    const int j = blockIdx.x * 32 + threadIdx.x % 32, lane = threadIdx.x / 32;
+    float v = 0.f;
+    if (j < 2 * p.D)
+#pragma unroll 4
+        for (int i = lane; i < parts; i += 32) v += p.part[(int64_t)i * 2 * p.D + j];
+    s[lane][threadIdx.x % 32] = v;
+    __syncthreads();
+    v = s[threadIdx.x % 32][lane];
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
+    const int column = blockIdx.x * 32 + lane;
+    if (threadIdx.x % 32 != 0 || column >= 2 * p.D) return;
+    void* to = column < p.D ? p.gw : p.gb;
+    if (to) store_elem<DT>(to, column < p.D ? column : column - p.D, v);
 }
 
 bool on_device(const tbe_layer_norm* h) {
@@ -144,18 +395,95 @@ bool on_device(const tbe_layer_norm* h) {
 
 bool aligned16(const void* p) { return (uintptr_t)p % 16 == 0; }
 
-template <int DT>
-cudaError_t launch_forward(const NormForward& p, const tbe_layer_norm* h, cudaStream_t s) {
-    norm_forward_kernel<DT><<<(unsigned)std::min<int64_t>(p.rows, h->num_sms * 8), kThreads, 0, s>>>(p);
+bool vec_rows(const tbe_layer_norm* h, const void* p, int64_t stride) {
+    const int e = elem_bytes(h->c.dtype);
+    return aligned16(p) && stride * e % 16 == 0 && h->c.dim * e % 16 == 0;
+}
+
+// CTAs that fill the GPU once, no more than the rows need.
+unsigned fill(const tbe_layer_norm* h, int per_sm, int groups, int64_t rows) {
+    return (unsigned)std::min<int64_t>((rows + groups - 1) / groups, (int64_t)per_sm * h->num_sms);
+}
+
+template <typename F>
+int resident(F kernel, int threads, size_t smem) {
+    int ctas = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&ctas, kernel, threads, smem) != cudaSuccess) return 1;
+    return std::max(ctas, 1);
+}
+
+template <int DT, int E, int K, int T>
+cudaError_t forward(const NormForward& p, const tbe_layer_norm* h, cudaStream_t s) {
+    constexpr int threads = cta_threads(T);
+    auto* kernel = norm_forward_kernel<DT, E, K, T>;
+    static const int per_sm = resident(kernel, threads, 0);
+    kernel<<<fill(h, per_sm, threads / T, p.rows), threads, 0, s>>>(p);
     return cudaGetLastError();
 }
 
+template <int DT, int E, int K, int T>
+cudaError_t backward(const NormBackward& p, const tbe_layer_norm* h, cudaStream_t s) {
+    constexpr int threads = cta_threads(T), M = E * K;
+    constexpr size_t smem = sizeof(float) * threads * (sums_in_smem<E, K, T>() ? 2 * M : threads > T ? M : 0);
+    auto* kernel = norm_backward_kernel<DT, E, K, T>;
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    static const int per_sm = resident(kernel, threads, smem);
+    const unsigned grid = fill(h, std::min(per_sm, most_ctas(p.D)), threads / T, p.rows);
+    if (grid > 0) kernel<<<grid, threads, smem, s>>>(p);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || !(p.gw || p.gb)) return e;
+    return launch_chained(norm_join_kernel<DT>, dim3((2 * p.D + 31) / 32), dim3(1024), s, p, (int)grid);
+}
+
+// The fewest threads a row whose registers hold it: 32 elements a thread in
+// the forward pass, 16 in the backward pass (whose sums take two registers an
+// element besides).
 template <int DT>
-cudaError_t launch_backward(const NormBackward& p, const tbe_layer_norm* h, cudaStream_t s) {
-    if (p.gw || p.gb) norm_weight_kernel<DT><<<(p.D + kThreads - 1) / kThreads, kThreads, 0, s>>>(p);
-    if (p.rows > 0)
-        norm_backward_kernel<DT><<<(unsigned)std::min<int64_t>(p.rows, h->num_sms * 8), kThreads, 0, s>>>(p);
-    return cudaGetLastError();
+cudaError_t launch_forward(const NormForward& p, bool vec, const tbe_layer_norm* h, cudaStream_t s) {
+    constexpr int E = DT == DT_F32 ? 4 : 8;
+    if (!vec) {
+        if (p.D <= 128) return forward<DT, 1, 4, 32>(p, h, s);
+        if (p.D <= 512) return forward<DT, 1, 16, 32>(p, h, s);
+        if (p.D <= 2048) return forward<DT, 1, 16, 128>(p, h, s);
+        if (p.D <= 8192) return forward<DT, 1, 16, 512>(p, h, s);
+        return forward<DT, 1, 16, 1024>(p, h, s);
+    }
+    if (p.D <= 8 * E) return forward<DT, E, 1, 8>(p, h, s);
+    if (p.D <= 16 * E) return forward<DT, E, 1, 16>(p, h, s);
+    if (p.D <= 32 * E) return forward<DT, E, 1, 32>(p, h, s);
+    if (p.D <= 64 * E) return forward<DT, E, 2, 32>(p, h, s);
+    if (p.D <= 128 * E) return forward<DT, E, 4, 32>(p, h, s);
+    if (p.D <= 256 * E) return forward<DT, E, 2, 128>(p, h, s);
+    if (p.D <= 512 * E) return forward<DT, E, 4, 128>(p, h, s);
+    if (p.D <= 1024 * E) return forward<DT, E, 4, 256>(p, h, s);
+    if (p.D <= 2048 * E) return forward<DT, E, 4, 512>(p, h, s);
+    if constexpr (DT == DT_F32) return forward<DT, E, 4, 1024>(p, h, s);
+    return cudaErrorInvalidValue;
+}
+
+template <int DT>
+cudaError_t launch_backward(const NormBackward& p, bool vec, const tbe_layer_norm* h, cudaStream_t s) {
+    constexpr int E = DT == DT_F32 ? 4 : 8, K2 = 16 / E;
+    if (!vec) {
+        if (p.D <= 128) return backward<DT, 1, 4, 32>(p, h, s);
+        if (p.D <= 512) return backward<DT, 1, 16, 32>(p, h, s);
+        if (p.D <= 2048) return backward<DT, 1, 16, 128>(p, h, s);
+        if (p.D <= 8192) return backward<DT, 1, 16, 512>(p, h, s);
+        return backward<DT, 1, 16, 1024>(p, h, s);
+    }
+    if (p.D <= 8 * E) return backward<DT, E, 1, 8>(p, h, s);
+    if (p.D <= 16 * E) return backward<DT, E, 1, 16>(p, h, s);
+    if (p.D <= 32 * E) return backward<DT, E, 1, 32>(p, h, s);
+    if (p.D <= 64 * E) return backward<DT, E, 2, 32>(p, h, s);
+    if (p.D <= 512) return backward<DT, E, K2, 32>(p, h, s);
+    if (p.D <= 128 * E) return backward<DT, E, 1, 128>(p, h, s);
+    if (p.D <= 2048) return backward<DT, E, K2, 128>(p, h, s);
+    if (p.D <= 4096) return backward<DT, E, K2, 256>(p, h, s);
+    if (p.D <= 8192) return backward<DT, E, K2, 512>(p, h, s);
+    return backward<DT, E, K2, 1024>(p, h, s);
 }
 
 }  // namespace
@@ -188,7 +516,8 @@ void tbe_layer_norm_destroy(tbe_layer_norm* h) { delete h; }
 
 size_t tbe_layer_norm_workspace_bytes(const tbe_layer_norm* h, int64_t rows) {
     if (!h || rows < 0 || rows >= (int64_t(1) << 31)) return 0;
-    return 256;
+    const int64_t ctas = std::min<int64_t>(rows, (int64_t)most_ctas(h->c.dim) * h->num_sms);
+    return 256 + sizeof(float) * 2 * (size_t)ctas * h->c.dim;
 }
 
 int tbe_layer_norm_forward(tbe_layer_norm* h, const void* x, int64_t x_stride, const void* residual,
@@ -203,9 +532,12 @@ int tbe_layer_norm_forward(tbe_layer_norm* h, const void* x, int64_t x_stride, c
     if (!x || !out || !stats || (residual != nullptr) != (total != nullptr)) return TBE_ERR_INVALID_ARG;
     const NormForward p{x, residual, weight, bias, x_stride, residual_stride, rows, h->c.dim, h->c.eps, out, total, stats};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = h->c.dtype == TBE_F32   ? launch_forward<DT_F32>(p, h, s)
-                          : h->c.dtype == TBE_F16 ? launch_forward<DT_F16>(p, h, s)
-                                                  : launch_forward<DT_BF16>(p, h, s);
+    const bool vec = vec_rows(h, x, x_stride) && vec_rows(h, out, 0) && (!weight || aligned16(weight)) &&
+                     (!bias || aligned16(bias)) &&
+                     (!residual || (vec_rows(h, residual, residual_stride) && vec_rows(h, total, 0)));
+    const cudaError_t e = h->c.dtype == TBE_F32   ? launch_forward<DT_F32>(p, vec, h, s)
+                          : h->c.dtype == TBE_F16 ? launch_forward<DT_F16>(p, vec, h, s)
+                                                  : launch_forward<DT_BF16>(p, vec, h, s);
     return e == cudaSuccess ? TBE_OK : cuda_fail(e);
 }
 
@@ -227,9 +559,12 @@ int tbe_layer_norm_backward(tbe_layer_norm* h, const void* total, int64_t total_
     const NormBackward p{total, grad_out, grad_total, weight, total_stride, grad_out_stride, grad_total_stride, rows,
                          stats, h->c.dim, grad_x, grad_weight, grad_bias, static_cast<float*>(workspace)};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = h->c.dtype == TBE_F32   ? launch_backward<DT_F32>(p, h, s)
-                          : h->c.dtype == TBE_F16 ? launch_backward<DT_F16>(p, h, s)
-                                                  : launch_backward<DT_BF16>(p, h, s);
+    const bool vec = vec_rows(h, total, total_stride) && vec_rows(h, grad_out, grad_out_stride) &&
+                     (!grad_total || vec_rows(h, grad_total, grad_total_stride)) && vec_rows(h, grad_x, 0) &&
+                     (!weight || aligned16(weight));
+    const cudaError_t e = h->c.dtype == TBE_F32   ? launch_backward<DT_F32>(p, vec, h, s)
+                          : h->c.dtype == TBE_F16 ? launch_backward<DT_F16>(p, vec, h, s)
+                                                  : launch_backward<DT_BF16>(p, vec, h, s);
     return e == cudaSuccess ? TBE_OK : cuda_fail(e);
 }
 
