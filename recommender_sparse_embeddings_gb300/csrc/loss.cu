@@ -6,7 +6,7 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include "../../include/tbe.h"
-#include "tbe_internal.cuh"
+#include "loss_mma.cuh"
 
 namespace tbe {
 int cuda_fail(cudaError_t e);
@@ -24,7 +24,6 @@ struct tbe_softmax_loss {
 namespace {
 
 constexpr int kMaxLossDim = 4096;
-constexpr int kChunk = 4096;  // items of a piece of the backward pass
 
 struct CallRange {
     explicit CallRange(const char* name) { nvtxRangePushA(name); }
@@ -33,154 +32,114 @@ struct CallRange {
     CallRange& operator=(const CallRange&) = delete;
 };
 
-struct Loss {
-    const void *x, *table, *targets;
-    int64_t x_stride, table_stride, N, V;
-    int index64, D;
+// Rows of a 16-bit operand: P planes of [rows][pitch].
+struct Copy {
+    const void* from;
+    int64_t stride, rows;
+    int32_t D, pitch;
+    uint16_t* to;
+    bool vec;
+};
+
+template <int DT>
+__device__ __forceinline__ void copy_row(const Copy& c, int64_t row, bool zero, int lane) {
+    const int64_t in = row * c.stride, out = row * c.pitch, plane = c.rows * c.pitch;
+    if constexpr (DT == DT_F32) {
+        for (int j = lane; j < c.D; j += 32) {
+            float x = zero ? 0.f : load_elem<DT>(c.from, in + j);
+#pragma unroll
+            for (int p = 0; p < 3; ++p) {
+                const __nv_bfloat16 y = __float2bfloat16_rn(x);
+                x -= __bfloat162float(y);
+                c.to[p * plane + out + j] = __bfloat16_as_ushort(y);
+            }
+        }
+    } else if (c.vec) {
+        for (int j = lane; j < c.D / 8; j += 32)
+            reinterpret_cast<uint4*>(c.to + out)[j] =
+                zero ? make_uint4(0, 0, 0, 0)
+                     : __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(c.from) + in) + j);
+    } else {
+        for (int j = lane; j < c.D; j += 32)
+            c.to[out + j] = zero ? (uint16_t)0 : __ldg(static_cast<const uint16_t*>(c.from) + in + j);
+    }
+}
+
+// One warp a row.
+template <int DT>
+__global__ void __launch_bounds__(256) loss_copy_kernel(const Copy c) {
+    chain_wait();
+    for (int64_t row = ((int64_t)blockIdx.x * 256 + threadIdx.x) / 32; row < c.rows; row += (int64_t)gridDim.x * 8)
+        copy_row<DT>(c, row, false, threadIdx.x % 32);
+}
+
+struct RowsIn {
+    Copy x;
+    const void* targets;
+    int32_t index64;
+    int64_t V, padded;  // padded: rows of `rows`, to whole tiles
+    const float *lse, *g;
     float scale;
-    float *loss, *lse;  // forward: written; backward: lse is read
-    const float* g;
-    void *gx, *gw;
-    float *d, *sum;  // [N][kChunk], [N][D]
-    int64_t v0, v1;  // the piece
+    RowStat* rows;
+    float* gmax;  // [CTAs]
     uint32_t* error;
 };
 
-// The row's item; -1 for a row that is left out.
-__device__ __forceinline__ int64_t target_of(const Loss& p, int64_t i) {
-    const int64_t t = p.index64 ? static_cast<const int64_t*>(p.targets)[i] : static_cast<const int32_t*>(p.targets)[i];
-    if (t >= p.V) {
-        atomicOr(p.error, ERR_OOB);
-        return -1;
-    }
-    return t < 0 ? -1 : t;
-}
-
-// acc[a][b] = sum_k A(m0 + 4 ty + a, k) B(k, n0 + 4 tx + b) of a 64 x 64 tile.
-template <typename FA, typename FB>
-__device__ __forceinline__ void tile_product(float (&acc)[4][4], int64_t K, FA A, FB B) {
-    __shared__ float sa[16][65], sb[16][65];
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-#pragma unroll
-    for (int a = 0; a < 4; ++a)
-#pragma unroll
-        for (int b = 0; b < 4; ++b) acc[a][b] = 0.f;
-    for (int64_t k0 = 0; k0 < K; k0 += 16) {
-        __syncthreads();
-        for (int x = threadIdx.x; x < 1024; x += 256) {
-            sa[x % 16][x / 16] = k0 + x % 16 < K ? A(x / 16, k0 + x % 16) : 0.f;
-            sb[x % 16][x / 16] = k0 + x % 16 < K ? B(k0 + x % 16, x / 16) : 0.f;
+// The backward pass's rows: x copied with zeros in the rows left out, what
+// each row brings, and per CTA the largest finite |coef|.
+template <int DT>
+__global__ void __launch_bounds__(256) loss_rows_kernel(const RowsIn p) {
+    chain_wait();
+    __shared__ float most[8];
+    const int lane = threadIdx.x % 32;
+    float m = 0.f;
+    for (int64_t row = ((int64_t)blockIdx.x * 256 + threadIdx.x) / 32; row < p.padded; row += (int64_t)gridDim.x * 8) {
+        RowStat r{0.f, 0.f, -1, 0};
+        if (row < p.x.rows) {
+            const int64_t t =
+                p.index64 ? static_cast<const int64_t*>(p.targets)[row] : static_cast<const int32_t*>(p.targets)[row];
+            if (t >= p.V && lane == 0) atomicOr(p.error, ERR_OOB);
+            if (t >= 0 && t < p.V) r = RowStat{-p.lse[row] * kLog2e, p.g[row] * p.scale, (int32_t)t, 0};
+            copy_row<DT>(p.x, row, r.target < 0, lane);
         }
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < 16; ++k)
-#pragma unroll
-            for (int a = 0; a < 4; ++a)
-#pragma unroll
-                for (int b = 0; b < 4; ++b) acc[a][b] = fmaf(sa[k][4 * ty + a], sb[k][4 * tx + b], acc[a][b]);
+        const float a = fabsf(r.coef);
+        if (a <= FLT_MAX) m = fmaxf(m, a);
+        if (lane == 0) p.rows[row] = r;
+    }
+    if (lane == 0) most[threadIdx.x / 32] = m;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < 8; ++w) m = fmaxf(m, most[w]);
+        p.gmax[blockIdx.x] = m;
     }
 }
 
-template <int DT>
-__device__ __forceinline__ void tile_scores(const Loss& p, float (&s)[4][4], int64_t m0, int64_t n0) {
-    tile_product(
-        s, p.D,
-        [&](int m, int64_t k) { return m0 + m < p.N ? load_elem<DT>(p.x, (m0 + m) * p.x_stride + k) : 0.f; },
-        [&](int64_t k, int n) { return n0 + n < p.V ? load_elem<DT>(p.table, (n0 + n) * p.table_stride + k) : 0.f; });
-}
-
-template <int DT>
-__global__ void __launch_bounds__(256) loss_forward_kernel(const Loss p) {
-    const int64_t m0 = (int64_t)blockIdx.x * 64;
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    float m[4];
-    double l[4];  // (fp32 would lose 2^-24 of the sum per item)
-    for (int a = 0; a < 4; ++a) m[a] = -INFINITY, l[a] = 0.;
-    for (int64_t n0 = 0; n0 < p.V; n0 += 64) {
-        float s[4][4];
-        tile_scores<DT>(p, s, m0, n0);
-        for (int a = 0; a < 4; ++a)
-            for (int b = 0; b < 4; ++b)
-                if (n0 + 4 * tx + b < p.V) {
-                    const float y = s[a][b] * p.scale, to = fmaxf(m[a], y);
-                    l[a] = l[a] * expf(m[a] - to) + expf(y - to);
-                    m[a] = to;
-                }
+// The slices' sums of a row joined, by one warp.
+__global__ void __launch_bounds__(256)
+    loss_join_kernel(const float2* part, int parts, const float* picked, const void* targets, int index64, int64_t N,
+                     int64_t V, float* loss, float* lse) {
+    chain_wait();
+    const int64_t row = ((int64_t)blockIdx.x * 256 + threadIdx.x) / 32;
+    const int lane = threadIdx.x % 32;
+    if (row >= N) return;
+    float m = -INFINITY;
+    for (int i = lane; i < parts; i += 32) m = fmaxf(m, part[row * parts + i].x);
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float l = 0.f;
+    for (int i = lane; i < parts; i += 32) {
+        const float2 y = part[row * parts + i];
+        // (a half of a tile that no item reaches: -inf and 0)
+        if (!(y.y == 0.f)) l = fmaf(y.y, ex2(y.x - m), l);
     }
-    for (int a = 0; a < 4; ++a) {
-        for (int o = 8; o > 0; o /= 2) {
-            const float mo = __shfl_xor_sync(0xffffffffu, m[a], o), to = fmaxf(m[a], mo);
-            const double lo = __shfl_xor_sync(0xffffffffu, l[a], o);
-            l[a] = (l[a] == 0. ? 0. : l[a] * expf(m[a] - to)) + (lo == 0. ? 0. : lo * expf(mo - to));
-            m[a] = to;
-        }
-        const int64_t i = m0 + 4 * ty + a;
-        if (tx == 0 && i < p.N) {
-            p.lse[i] = m[a] + logf((float)l[a]);
-            const int64_t t = target_of(p, i);
-            float y = 0.f;
-            if (t >= 0)
-                for (int k = 0; k < p.D; ++k)
-                    y = fmaf(load_elem<DT>(p.x, i * p.x_stride + k), load_elem<DT>(p.table, t * p.table_stride + k), y);
-            p.loss[i] = t < 0 ? 0.f : (m[a] - y * p.scale) + logf((float)l[a]);
-        }
-    }
-}
-
-template <int DT>
-__global__ void __launch_bounds__(256) loss_d_kernel(const Loss p) {
-    const int64_t m0 = (int64_t)blockIdx.x * 64, n0 = p.v0 + (int64_t)blockIdx.y * 64;
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    float s[4][4];
-    tile_scores<DT>(p, s, m0, n0);
-    for (int a = 0; a < 4; ++a) {
-        const int64_t i = m0 + 4 * ty + a;
-        if (i >= p.N) continue;
-        const int64_t t = target_of(p, i);
-        for (int b = 0; b < 4; ++b) {
-            const int64_t v = n0 + 4 * tx + b;
-            if (v < p.v1)
-                p.d[i * kChunk + v - p.v0] =
-                    t < 0 ? 0.f : p.g[i] * p.scale * (expf(s[a][b] * p.scale - p.lse[i]) - (v == t ? 1.f : 0.f));
-        }
-    }
-}
-
-template <int DT>
-__global__ void __launch_bounds__(256) loss_gx_kernel(const Loss p) {
-    const int64_t m0 = (int64_t)blockIdx.x * 64, n0 = (int64_t)blockIdx.y * 64;
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    float s[4][4];
-    tile_product(
-        s, p.v1 - p.v0, [&](int m, int64_t k) { return m0 + m < p.N ? p.d[(m0 + m) * kChunk + k] : 0.f; },
-        [&](int64_t k, int n) {
-            return n0 + n < p.D ? load_elem<DT>(p.table, (p.v0 + k) * p.table_stride + n0 + n) : 0.f;
-        });
-    for (int a = 0; a < 4; ++a)
-        for (int b = 0; b < 4; ++b) {
-            const int64_t i = m0 + 4 * ty + a, j = n0 + 4 * tx + b;
-            if (i >= p.N || j >= p.D) continue;
-            const float y = (p.v0 > 0 ? p.sum[i * p.D + j] : 0.f) + s[a][b];
-            p.sum[i * p.D + j] = y;
-            if (p.v1 == p.V) store_elem<DT>(p.gx, i * p.D + j, y);
-        }
-}
-
-template <int DT>
-__global__ void __launch_bounds__(256) loss_gw_kernel(const Loss p) {
-    const int64_t m0 = (int64_t)blockIdx.x * 64, n0 = (int64_t)blockIdx.y * 64;
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    float s[4][4];
-    tile_product(
-        s, p.N, [&](int m, int64_t k) { return p.v0 + m0 + m < p.v1 ? p.d[k * kChunk + m0 + m] : 0.f; },
-        [&](int64_t k, int n) {
-            return n0 + n < p.D && target_of(p, k) >= 0 ? load_elem<DT>(p.x, k * p.x_stride + n0 + n) : 0.f;
-        });
-    for (int a = 0; a < 4; ++a)
-        for (int b = 0; b < 4; ++b) {
-            const int64_t v = p.v0 + m0 + 4 * ty + a, j = n0 + 4 * tx + b;
-            if (v < p.v1 && j < p.D) store_elem<DT>(p.gw, v * p.D + j, s[a][b]);
-        }
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if (lane != 0) return;
+    const int64_t t = index64 ? static_cast<const int64_t*>(targets)[row] : static_cast<const int32_t*>(targets)[row];
+    constexpr float kLn2 = 0.6931471805599453f;
+    const float log_l = logf(l);
+    lse[row] = fmaf(m, kLn2, log_l);
+    loss[row] = t >= 0 && t < V ? fmaf(m - picked[row], kLn2, log_l) : 0.f;
 }
 
 size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
@@ -203,17 +162,278 @@ int check(const tbe_softmax_loss* h, const void* x, int64_t x_stride, const void
     return within_limits(N, V) ? TBE_OK : TBE_ERR_UNSUPPORTED;
 }
 
-template <int DT>
-cudaError_t launch_backward(Loss p, cudaStream_t s) {
-    const unsigned mt = (unsigned)((p.N + 63) / 64), dt = (unsigned)((p.D + 63) / 64);
-    for (p.v0 = 0; p.v0 < p.V; p.v0 = p.v1) {
-        p.v1 = std::min<int64_t>(p.V, p.v0 + kChunk);
-        const unsigned vt = (unsigned)((p.v1 - p.v0 + 63) / 64);
-        loss_d_kernel<DT><<<dim3(mt, vt), 256, 0, s>>>(p);
-        if (p.gx) loss_gx_kernel<DT><<<dim3(mt, dt), 256, 0, s>>>(p);
-        if (p.gw) loss_gw_kernel<DT><<<dim3(vt, dt), 256, 0, s>>>(p);
+// ---- workspaces and plans
+
+template <typename T>
+T* at(void* base, size_t offset) {
+    return reinterpret_cast<T*>(static_cast<char*>(base) + offset);
+}
+
+int64_t up_to(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
+
+// Elements of a piece of d: two pieces of this size, the rows and the piece of
+// the table stay in L2 (129 MB).
+constexpr int64_t kPieceBytes = 48 << 20;
+// Work items that the sums' parts make at most.
+constexpr int kMostParts = 304;
+constexpr int kRowCtas = 512;
+
+struct Plan {
+    int planes, pitch, cols4, col_tiles;
+    int64_t row_tiles;
+    int64_t piece;  // items
+    int64_t span;   // items of a copied part of the table, whole pieces
+    size_t rows, gmax, x, w, d, x_part, w_part, total;  // offsets
+    size_t w_bytes, d_bytes, w_part_bytes;              // of one of two
+};
+
+// Sized so that a workspace serves every smaller call: each size grows with N
+// and V although the piece shrinks with N.
+Plan make_plan(const tbe_softmax_loss* h, int64_t N, int64_t V, bool backward, bool copied) {
+    Plan L{};
+    const int D = h->c.dim;
+    L.planes = h->c.dtype == TBE_F32 ? 3 : 1;
+    L.pitch = (int)up_to(D, 8);
+    L.cols4 = (int)up_to(D, 32) / 4;
+    L.col_tiles = (D + 255) / 256;
+    L.row_tiles = (N + 127) / 128;
+    const int64_t padded = up_to(V, 256), room = kPieceBytes / (2 * L.planes);  // elements
+    L.piece = std::max<int64_t>(256, std::min(padded, room / std::max<int64_t>(N, 1) / 256 * 256));
+    const int64_t item_bytes = 2 * (int64_t)L.planes * L.pitch;
+    size_t o = 0;
+    auto take = [&](size_t bytes) {
+        const size_t here = o;
+        o = align_up(o + bytes);
+        return here;
+    };
+    L.x = take((size_t)N * item_bytes);
+    if (copied) {
+        // 16-bit tables of aligned rows are read where they are; a copy is rare
+        const int64_t budget = h->c.dtype != TBE_F32 && D % 8 == 0 ? 16 << 20 : 64 << 20;
+        const int64_t items = std::max<int64_t>(256, budget / item_bytes / 256 * 256);
+        L.piece = std::min(L.piece, items);
+        L.span = backward ? items / L.piece * L.piece : items;
+        L.w_bytes = align_up((size_t)(std::min(padded, items) * item_bytes));
+        L.w = take(2 * L.w_bytes);
     }
-    return cudaGetLastError();
+    if (backward) {
+        L.rows = take(sizeof(RowStat) * 128 * L.row_tiles);
+        L.gmax = take(sizeof(float) * kRowCtas);
+        L.d_bytes = align_up((size_t)std::min(std::max(room, 256 * N), N * padded) * 2 * L.planes);
+        L.d = take(2 * L.d_bytes);
+        const size_t tile = (size_t)L.cols4 * 128 * sizeof(float4);
+        L.x_part = take(std::max<int64_t>(L.row_tiles, kMostParts / L.col_tiles + 1) * tile);
+        L.w_part_bytes = (kMostParts / L.col_tiles + 1) * tile;
+        L.w_part = take(2 * L.w_part_bytes);
+    } else {
+        L.rows = take(sizeof(float) * N);                                   // picked
+        L.d = take(sizeof(float2) * 2 * (N + 128 * (int64_t)kMostParts));  // part
+    }
+    L.total = o + 256;
+    return L;
+}
+
+// A map of 16-bit rows: (column, row, plane), boxes of 64 columns x `box` rows
+// in the 128-byte swizzle; zeros outside.  The encoder is the driver's, found at
+// run time (it computes 128 bytes on the host).
+bool encode(CUtensorMap* map, int dtype, const void* base, int64_t D, int64_t rows, int planes, int64_t pitch, int box) {
+    using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static const Encode fn = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult found{};
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<Encode>(f);
+    }();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)rows, (cuuint64_t)planes};
+    const cuuint64_t strides[2] = {(cuuint64_t)pitch * 2, (cuuint64_t)pitch * 2 * (planes > 1 ? rows : 1)};
+    const cuuint32_t boxes[3] = {64, (cuuint32_t)box, 1}, steps[3] = {1, 1, 1};
+    return fn(map, dtype == TBE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+              const_cast<void*>(base), dims, strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Whether TMA reads these rows where they are.
+bool direct(const tbe_softmax_loss* h, const void* p, int64_t stride, int64_t rows) {
+    return h->c.dtype != TBE_F32 && aligned16(p) &&
+           (rows == 1 ? h->c.dim % 8 == 0 : stride % 8 == 0 && stride >= h->c.dim) && stride < (int64_t(1) << 38);
+}
+
+Copy make_copy(const tbe_softmax_loss* h, const void* from, int64_t stride, int64_t rows, int pitch, void* to) {
+    return Copy{from, stride, rows, h->c.dim, pitch, static_cast<uint16_t*>(to),
+                aligned16(from) && stride % 8 == 0 && h->c.dim % 8 == 0};
+}
+
+cudaError_t launch_copy(const tbe_softmax_loss* h, const Copy& c, cudaStream_t s) {
+    const unsigned grid = (unsigned)std::min<int64_t>((c.rows + 7) / 8, (int64_t)h->num_sms * 16);
+    return h->c.dtype == TBE_F32 ? launch_chained(loss_copy_kernel<DT_F32>, dim3(grid), dim3(256), s, c)
+                                 : launch_chained(loss_copy_kernel<DT_F16>, dim3(grid), dim3(256), s, c);
+}
+
+// The table's maps over the pieces of a call: the table itself, or spans of it
+// copied in turn into one of two places.
+struct Table {
+    const tbe_softmax_loss* h;
+    const void* data;
+    int64_t stride, V, span;
+    int planes, pitch;
+    bool is_direct;
+    char* room;
+    size_t room_bytes;
+    int64_t now = -1;
+
+    int64_t first(int64_t item) const { return is_direct ? 0 : item / span * span; }
+
+    bool map(CUtensorMap* m, int64_t item) const {
+        if (is_direct)
+            return encode(m, h->c.dtype, data, h->c.dim, V, 1, V == 1 ? pitch : stride, 64);
+        const int64_t k = item / span, rows = std::min(span, V - k * span);
+        return encode(m, h->c.dtype, room + (k & 1) * room_bytes, h->c.dim, rows, planes, pitch, 64);
+    }
+    // Copies the item's span unless that was done.
+    cudaError_t fetch(int64_t item, cudaStream_t s) {
+        if (is_direct || item / span == now) return cudaSuccess;
+        now = item / span;
+        const int64_t from = now * span;
+        return launch_copy(h,
+                           make_copy(h, static_cast<const char*>(data) + from * stride * elem_bytes(h->c.dtype), stride,
+                                     std::min(span, V - from), pitch, room + (now & 1) * room_bytes),
+                           s);
+    }
+};
+
+// Slices of the table a row tile's items are cut into: those that end soonest
+// with every CTA taking items in turn.
+int choose_slices(int64_t row_tiles, int64_t item_tiles, int ctas) {
+    int best = 1;
+    int64_t least = INT64_MAX;
+    const int64_t most = std::min<int64_t>(item_tiles, kMostParts / row_tiles + 1);
+    for (int64_t s = 1; s <= most; ++s) {
+        const int64_t turns = (row_tiles * s + ctas - 1) / ctas, time = turns * ((item_tiles + s - 1) / s);
+        if (time < least) {
+            least = time;
+            best = (int)s;
+        }
+    }
+    return best;
+}
+
+int forward(const tbe_softmax_loss* h, const Plan& L, LossForward p, const void* x, int64_t x_stride, const void* table,
+            int64_t table_stride, float* loss, float* lse, char* base, cudaStream_t s) {
+    LossMaps maps{};
+    const bool as_is = direct(h, x, x_stride, p.N);
+    cudaError_t e = cudaSuccess;
+    if (!as_is) e = launch_copy(h, make_copy(h, x, x_stride, p.N, L.pitch, base + L.x), s);
+    if (e != cudaSuccess) return cuda_fail(e);
+    if (!encode(&maps.x, h->c.dtype, as_is ? x : base + L.x, p.D, p.N, L.planes,
+                as_is && p.N > 1 ? x_stride : L.pitch, 64))
+        return TBE_ERR_CUDA;
+    Table w{h, table, table_stride, p.V, L.span, L.planes, L.pitch, direct(h, table, table_stride, p.V), base + L.w,
+            L.w_bytes};
+    const int64_t whole = w.is_direct ? p.V : std::min(p.V, L.span);
+    p.row_tiles = (int)L.row_tiles;
+    p.slices = choose_slices(L.row_tiles, (whole + 255) / 256, h->num_sms);
+    p.part = at<float2>(base, L.d);
+    p.picked = at<float>(base, L.rows);
+    for (p.v0 = 0; p.v0 < p.V; p.v0 = p.v1) {
+        p.v1 = std::min(p.V, p.v0 + whole);
+        p.w0 = w.first(p.v0);
+        p.first = p.v0 == 0;
+        p.item_tiles = (int)((p.v1 - p.v0 + 255) / 256);
+        e = w.fetch(p.v0, s);
+        if (e != cudaSuccess) return cuda_fail(e);
+        if (!w.map(&maps.w, p.v0)) return TBE_ERR_CUDA;
+        const int64_t items = (int64_t)p.row_tiles * p.slices;
+        e = launch_loss_forward(p, maps, h->c.dtype, (int)std::min<int64_t>(items, h->num_sms), s);
+        if (e != cudaSuccess) return cuda_fail(e);
+    }
+    return status(launch_chained(loss_join_kernel, dim3((unsigned)((p.N + 7) / 8)), dim3(256), s,
+                                 (const float2*)p.part, 2 * p.slices, (const float*)p.picked, p.targets, p.index64, p.N,
+                                 p.V, loss, lse));
+}
+
+int backward(const tbe_softmax_loss* h, const Plan& L, LossStep p, RowsIn rows, const void* table, int64_t table_stride,
+             char* base, cudaStream_t s) {
+    LossMaps maps{};
+    const int dt = h->c.dtype;
+    rows.rows = at<RowStat>(base, L.rows);
+    rows.gmax = at<float>(base, L.gmax);
+    rows.padded = L.row_tiles * 128;
+    rows.x.to = at<uint16_t>(base, L.x);
+    const unsigned row_ctas = (unsigned)std::min<int64_t>(rows.padded / 8, kRowCtas);
+    cudaError_t e = dt == TBE_F32   ? launch_chained(loss_rows_kernel<DT_F32>, dim3(row_ctas), dim3(256), s, rows)
+                    : dt == TBE_F16 ? launch_chained(loss_rows_kernel<DT_F16>, dim3(row_ctas), dim3(256), s, rows)
+                                    : launch_chained(loss_rows_kernel<DT_BF16>, dim3(row_ctas), dim3(256), s, rows);
+    if (e != cudaSuccess) return cuda_fail(e);
+    p.rows = rows.rows;
+    p.gmax = rows.gmax;
+    p.n_gmax = (int)row_ctas;
+    p.row_tiles = (int)L.row_tiles;
+    p.col_tiles = L.col_tiles;
+    p.cols4 = L.cols4;
+    p.x_part = at<float4>(base, L.x_part);
+    if (!encode(&maps.x, dt, rows.x.to, p.D, p.N, L.planes, L.pitch, 64)) return TBE_ERR_CUDA;
+    Table w{h, table, table_stride, p.V, L.span, L.planes, L.pitch, direct(h, table, table_stride, p.V), base + L.w,
+            L.w_bytes};
+
+    // How the products' sums are cut: into items of about a quarter of a CTA's
+    // share of a launch, so that none is waited for at its end.
+    const int64_t piece = std::min(L.piece, p.V), item_tiles = (piece + 127) / 128;
+    const int64_t row_blocks = (p.N + 63) / 64, piece_blocks = (piece + 63) / 64;
+    const int64_t products = (p.gx ? L.row_tiles * L.col_tiles * piece_blocks : 0) +
+                             (p.gw ? item_tiles * L.col_tiles * row_blocks : 0);
+    const int64_t share = std::max<int64_t>(4, products / (h->num_sms * 2));
+    auto slabs = [&](int64_t blocks, int64_t tiles) {
+        const int64_t most = std::max<int64_t>(1, kMostParts / std::max<int64_t>(tiles, 1));
+        return (int)std::min({most, blocks, (blocks + share - 1) / share});
+    };
+    p.x_slabs = slabs(piece_blocks, L.row_tiles * L.col_tiles);
+    p.w_slabs = slabs(row_blocks, item_tiles * L.col_tiles);
+    const int64_t pieces = (p.V + L.piece - 1) / L.piece;
+    for (int64_t j = 0; j <= pieces + 1; ++j) {
+        LossStep q = p;
+        q.n_d = q.n_gx = q.n_gw = q.n_fin_w = q.n_fin_x = 0;
+        if (j < pieces) {
+            q.d0 = j * L.piece;
+            const int64_t items = std::min(L.piece, p.V - q.d0);
+            q.n_d = (int)((items + 255) / 256 * L.row_tiles);
+            q.dw0 = w.first(q.d0);
+            e = w.fetch(q.d0, s);
+            if (e != cudaSuccess) return cuda_fail(e);
+            if (!w.map(&maps.w, q.d0) ||
+                !encode(&maps.d_out, dt, base + L.d + (j & 1) * L.d_bytes, L.piece, p.N, L.planes, L.piece, 32))
+                return TBE_ERR_CUDA;
+        }
+        if (j >= 1 && j <= pieces) {
+            q.p0 = (j - 1) * L.piece;
+            q.p_items = (int)std::min(L.piece, p.V - q.p0);
+            q.pw0 = w.first(q.p0);
+            q.first = j == 1;
+            q.n_gx = p.gx ? (int)(L.row_tiles * L.col_tiles * p.x_slabs) : 0;
+            q.n_gw = p.gw ? (int)((q.p_items + 127) / 128 * L.col_tiles * p.w_slabs) : 0;
+            q.w_part = at<float4>(base, L.w_part + ((j - 1) & 1) * L.w_part_bytes);
+            if (!w.map(&maps.pw, q.p0) ||
+                !encode(&maps.d_in, dt, base + L.d + ((j - 1) & 1) * L.d_bytes, L.piece, p.N, L.planes, L.piece, 64))
+                return TBE_ERR_CUDA;
+        }
+        if (j >= 2 && p.gw && p.w_slabs > 1) {
+            q.f0 = (j - 2) * L.piece;
+            q.f_items = (int)std::min(L.piece, p.V - q.f0);
+            q.f_part = at<float4>(base, L.w_part + ((j - 2) & 1) * L.w_part_bytes);
+            q.n_fin_w = (q.f_items + 127) / 128;
+        }
+        if (j == pieces + 1 && p.gx) q.n_fin_x = (int)L.row_tiles;
+        const int64_t n = (int64_t)q.n_d + q.n_gx + q.n_gw + q.n_fin_w + q.n_fin_x;
+        if (n == 0) continue;
+        e = launch_loss_step(q, maps, dt, (int)std::min<int64_t>(n, h->num_sms), s);
+        if (e != cudaSuccess) return cuda_fail(e);
+    }
+    return TBE_OK;
 }
 
 }  // namespace
@@ -233,6 +453,7 @@ int tbe_softmax_loss_create(const tbe_softmax_loss_config* c, tbe_softmax_loss**
     h->c = *c;
     cudaError_t e = cudaGetDevice(&h->device);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, h->device);
+    if (e == cudaSuccess) e = loss_mma_configure();
     if (e == cudaSuccess) e = cudaMalloc(&h->error, 16);
     if (e == cudaSuccess) e = cudaMemset(h->error, 0, 16);
     if (e != cudaSuccess) {
@@ -252,7 +473,9 @@ void tbe_softmax_loss_destroy(tbe_softmax_loss* h) {
 
 size_t tbe_softmax_loss_workspace_bytes(const tbe_softmax_loss* h, int64_t N, int64_t V, int32_t backward) {
     if (!h || N < 0 || V < 0 || !within_limits(N, V)) return 0;
-    return 256 + (backward ? align_up(sizeof(float) * N * kChunk) + align_up(sizeof(float) * N * h->c.dim) : 0);
+    const size_t one = std::max(make_plan(h, N, V, false, false).total, make_plan(h, N, V, false, true).total);
+    if (!backward) return one;
+    return std::max({one, make_plan(h, N, V, true, false).total, make_plan(h, N, V, true, true).total});
 }
 
 int tbe_softmax_loss_forward(tbe_softmax_loss* h, const void* x, int64_t x_stride, const void* table,
@@ -264,19 +487,12 @@ int tbe_softmax_loss_forward(tbe_softmax_loss* h, const void* x, int64_t x_strid
     if (!workspace || !aligned16(workspace) || (N > 0 && (!loss || !lse))) return TBE_ERR_INVALID_ARG;
     if (workspace_bytes < tbe_softmax_loss_workspace_bytes(h, N, V, 0)) return TBE_ERR_WORKSPACE_TOO_SMALL;
     if (N == 0) return TBE_OK;
-    Loss p{};
-    p.x = x, p.table = table, p.targets = targets, p.x_stride = x_stride, p.table_stride = table_stride;
-    p.N = N, p.V = V, p.index64 = index_dtype == TBE_I64, p.D = h->c.dim, p.scale = h->c.scale;
-    p.loss = loss, p.lse = lse, p.error = h->error;
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const unsigned grid = (unsigned)((N + 63) / 64);
-    if (h->c.dtype == TBE_F32)
-        loss_forward_kernel<DT_F32><<<grid, 256, 0, s>>>(p);
-    else if (h->c.dtype == TBE_F16)
-        loss_forward_kernel<DT_F16><<<grid, 256, 0, s>>>(p);
-    else
-        loss_forward_kernel<DT_BF16><<<grid, 256, 0, s>>>(p);
-    return status(cudaGetLastError());
+    LossForward p{};
+    p.N = N, p.V = V, p.D = h->c.dim, p.c2 = h->c.scale * kLog2e;
+    p.targets = targets, p.index64 = index_dtype == TBE_I64, p.error = h->error;
+    char* base = reinterpret_cast<char*>(align_up(reinterpret_cast<uintptr_t>(workspace)));
+    return forward(h, make_plan(h, N, V, false, !direct(h, table, table_stride, V)), p, x, x_stride, table, table_stride, loss, lse, base,
+                   static_cast<cudaStream_t>(stream));
 }
 
 int tbe_softmax_loss_backward(tbe_softmax_loss* h, const void* x, int64_t x_stride, const void* table,
@@ -293,16 +509,17 @@ int tbe_softmax_loss_backward(tbe_softmax_loss* h, const void* x, int64_t x_stri
         if (!grad_table || V == 0) return TBE_OK;
         return status(cudaMemsetAsync(grad_table, 0, (size_t)V * h->c.dim * elem_bytes(h->c.dtype), s));
     }
-    Loss p{};
-    p.x = x, p.table = table, p.targets = targets, p.x_stride = x_stride, p.table_stride = table_stride;
-    p.N = N, p.V = V, p.index64 = index_dtype == TBE_I64, p.D = h->c.dim, p.scale = h->c.scale;
-    p.lse = const_cast<float*>(lse), p.g = grad_loss, p.gx = grad_x, p.gw = grad_table, p.error = h->error;
-    char* at = reinterpret_cast<char*>(align_up(reinterpret_cast<uintptr_t>(workspace)));
-    p.d = reinterpret_cast<float*>(at);
-    p.sum = reinterpret_cast<float*>(at + align_up(sizeof(float) * N * kChunk));
-    return status(h->c.dtype == TBE_F32   ? launch_backward<DT_F32>(p, s)
-                  : h->c.dtype == TBE_F16 ? launch_backward<DT_F16>(p, s)
-                                          : launch_backward<DT_BF16>(p, s));
+    if (!grad_x && !grad_table) return TBE_OK;
+    const Plan L = make_plan(h, N, V, true, !direct(h, table, table_stride, V));
+    RowsIn rows{};
+    rows.x = make_copy(h, x, x_stride, N, L.pitch, nullptr);
+    rows.targets = targets, rows.index64 = index_dtype == TBE_I64, rows.V = V;
+    rows.lse = lse, rows.g = grad_loss, rows.scale = h->c.scale, rows.error = h->error;
+    LossStep p{};
+    p.N = N, p.V = V, p.D = h->c.dim, p.c2 = h->c.scale * kLog2e;
+    p.gx = grad_x, p.gw = grad_table, p.error = h->error;
+    char* base = reinterpret_cast<char*>(align_up(reinterpret_cast<uintptr_t>(workspace)));
+    return backward(h, L, p, rows, table, table_stride, base, s);
 }
 
 int tbe_softmax_loss_get_error(tbe_softmax_loss* h, void* stream) {

@@ -1,0 +1,602 @@
+// The softmax loss's tensor-core kernel; see loss_mma.cuh.
+#include "loss_mma.cuh"
+
+namespace tbe {
+
+namespace {
+
+struct LossBars {
+    uint64_t full[kLossStages], empty[kLossStages], acc_full[2], acc_empty[2];
+};
+
+// Plane pairs of an fp32 product, small ones first.
+template <int P>
+constexpr int kTerms = P == 3 ? 6 : 1;
+__device__ __forceinline__ int plane_a(int term) { return (0x001012 >> (4 * term)) & 15; }
+__device__ __forceinline__ int plane_b(int term) { return (0x010210 >> (4 * term)) & 15; }
+
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap& map, int col, int64_t row, int plane,
+                                         uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];" ::"r"(dst),
+        "l"(&map), "r"(col), "r"((int)row), "r"(plane), "r"(smem_u32(bar))
+        : "memory");
+}
+
+__device__ __forceinline__ void store_box(const CUtensorMap& map, uint32_t src, int col, int row, int plane) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(&map),
+                 "r"(col), "r"(row), "r"(plane), "r"(src)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
+__device__ __forceinline__ void store_read_wait() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void store_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// A tile of products: `steps` of 64 along the sum, `wide` columns.
+struct Product {
+    int kind;
+    int row0;         // rows of A's tile: X rows, d rows, items of the piece
+    int64_t col0;     // of B's tile: first item (scores) or first column (gx, gw)
+    int k0, kblocks;  // along the sum, blocks of 64
+    int wide;
+    int slab;
+};
+
+__device__ __forceinline__ int columns_of(int64_t left) { return (int)tmin<int64_t>(256, (left + 15) / 16 * 16); }
+
+__device__ __forceinline__ Product score_tile(int64_t V, int D, int row0, int64_t item) {
+    return Product{ITEM_D, row0, item, 0, (D + 63) / 64, columns_of(V - item), 0};
+}
+
+// Work item i of a backward launch: the long ones first.
+__device__ __forceinline__ Product step_item(const LossStep& p, int i) {
+    Product t{};
+    if (i < p.n_gw) {
+        const int tiles = (p.p_items + 127) / 128, blocks = (int)((p.N + 63) / 64);
+        const int tile = i % tiles, rest = i / tiles, ct = rest % p.col_tiles;
+        t.kind = ITEM_GW;
+        t.slab = rest / p.col_tiles;
+        t.row0 = tile * 128;
+        t.col0 = ct * 256;
+        t.k0 = (int)((int64_t)blocks * t.slab / p.w_slabs);
+        t.kblocks = (int)((int64_t)blocks * (t.slab + 1) / p.w_slabs) - t.k0;
+        t.wide = columns_of(p.D - t.col0);
+        return t;
+    }
+    i -= p.n_gw;
+    if (i < p.n_gx) {
+        const int blocks = (p.p_items + 63) / 64;
+        const int tile = i % p.row_tiles, rest = i / p.row_tiles, ct = rest % p.col_tiles;
+        t.kind = ITEM_GX;
+        t.slab = rest / p.col_tiles;
+        t.row0 = tile * 128;
+        t.col0 = ct * 256;
+        t.k0 = (int)((int64_t)blocks * t.slab / p.x_slabs);
+        t.kblocks = (int)((int64_t)blocks * (t.slab + 1) / p.x_slabs) - t.k0;
+        t.wide = columns_of(p.D - t.col0);
+        return t;
+    }
+    i -= p.n_gx;
+    if (i < p.n_d) return score_tile(p.V, p.D, i % p.row_tiles * 128, p.d0 + (int64_t)(i / p.row_tiles) * 256);
+    i -= p.n_d;
+    t.kind = i < p.n_fin_w ? ITEM_FIN_W : ITEM_FIN_X;
+    t.row0 = (i < p.n_fin_w ? i : i - p.n_fin_w) * 128;
+    return t;
+}
+
+// The power of two that fp16's d is multiplied by: it brings the largest finite
+// |coef| into [2^14, 2^15).
+__device__ __forceinline__ float range_scale(const float* gmax, int n, int lane) {
+    float m = 0.f;
+    for (int i = lane; i < n; i += 32) m = fmaxf(m, __ldg(gmax + i));
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (!(m > 0.f)) return 1.f;
+    const int e = tmax((int)(__float_as_uint(m) >> 23), 27);  // 27: the scale stays below 2^115
+    return __uint_as_float((uint32_t)(127 + 14 + 127 - e) << 23);
+}
+
+// Warp roles' shared counters: steps through the ring and accumulators used.
+template <int P, typename Next>
+__device__ bool produce(unsigned char* smem, LossBars& bars, const LossMaps& maps, int64_t w0, int64_t p_row, Next next) {
+    int n = 0;
+    bool ok = true;
+    Product t;
+    while (ok && next(t)) {
+        if (t.kind >= ITEM_FIN_W) continue;
+        const int steps = t.kblocks * kTerms<P>, slabs = (t.wide + 63) / 64;
+        for (int s = 0; s < steps && ok; ++s, ++n) {
+            const int st = n % kLossStages;
+            if (n >= kLossStages) ok = mbar_wait_tight(&bars.empty[st], (n / kLossStages - 1) & 1);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            if (elect_one()) {
+                uint64_t* bar = &bars.full[st];
+                const uint32_t a = smem_u32(smem) + st * kStageBytes, b = a + 2 * kBox;
+                const int term = P == 3 ? s / t.kblocks : 0, k = (t.k0 + (P == 3 ? s % t.kblocks : s)) * 64;
+                const int pa = P == 3 ? plane_a(term) : 0, pb = P == 3 ? plane_b(term) : 0;
+                mbar_expect_tx(bar, (2 + slabs) * kBox);
+                if (t.kind == ITEM_D) {
+                    load_box(a, maps.x, k, t.row0, pa, bar);
+                    load_box(a + kBox, maps.x, k, t.row0 + 64, pa, bar);
+                    for (int j = 0; j < slabs; ++j) load_box(b + j * kBox, maps.w, k, t.col0 - w0 + j * 64, pb, bar);
+                } else if (t.kind == ITEM_GX) {
+                    load_box(a, maps.d_in, k, t.row0, pa, bar);
+                    load_box(a + kBox, maps.d_in, k, t.row0 + 64, pa, bar);
+                    for (int j = 0; j < slabs; ++j)
+                        load_box(b + j * kBox, maps.pw, (int)t.col0 + j * 64, p_row + k, pb, bar);
+                } else {
+                    load_box(a, maps.d_in, t.row0, k, pa, bar);
+                    load_box(a + kBox, maps.d_in, t.row0 + 64, k, pa, bar);
+                    for (int j = 0; j < slabs; ++j) load_box(b + j * kBox, maps.x, (int)t.col0 + j * 64, k, pb, bar);
+                }
+            }
+            __syncwarp();
+        }
+    }
+    // where a wait ran out: this CTA's copies in flight land before it ends
+    if (!ok)
+        for (int i = tmax(0, n - kLossStages); i < n; ++i)
+            mbar_wait_tight(&bars.full[i % kLossStages], (i / kLossStages) & 1);
+    return ok;
+}
+
+template <int DT, int P, typename Next>
+__device__ bool multiply(unsigned char* smem, LossBars& bars, uint32_t tmem, Next next) {
+    int n = 0, tile = 0;
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, int parity) {
+        const bool in = mbar_wait_tight(bar, parity & 1);
+        const bool all = __all_sync(0xffffffffu, in);
+        tcgen05_after_sync();
+        return all;
+    };
+    const uint32_t base = smem_u32(smem);
+    Product t;
+    while (ok && next(t)) {
+        if (t.kind >= ITEM_FIN_W) continue;
+        const int buf = tile & 1;
+        if (tile >= 2) ok = wait(&bars.acc_empty[buf], tile / 2 - 1);
+        const bool a_mn = t.kind == ITEM_GW, b_mn = t.kind != ITEM_D;
+        const uint32_t idesc =
+            mma_idesc(DT == DT_BF16, 128, t.wide) | (a_mn ? 1u << 15 : 0u) | (b_mn ? kMnMajorB : 0u);
+        const uint64_t da = a_mn ? smem_desc_mn(base, kBox) : smem_desc_sw128(base, 1024);
+        const uint64_t db = b_mn ? smem_desc_mn(base + 2 * kBox, kBox) : smem_desc_sw128(base + 2 * kBox, 1024);
+        const int ka = a_mn ? 2048 / 16 : 2, kb = b_mn ? 2048 / 16 : 2;
+        const int steps = t.kblocks * kTerms<P>;
+        for (int s = 0; s < steps && ok; ++s, ++n) {
+            const int st = n % kLossStages;
+            ok = wait(&bars.full[st], n / kLossStages);
+            if (!ok) break;
+            if (elect_one()) {
+                const uint64_t at = (uint64_t)(st * (kStageBytes / 16));
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    mma_f16(tmem + buf * 256, da + at + k * ka, db + at + k * kb, idesc, s > 0 || k > 0);
+                mma_commit(&bars.empty[st]);
+                if (s + 1 == steps) mma_commit(&bars.acc_full[buf]);
+            }
+            __syncwarp();
+        }
+        ++tile;
+    }
+    // nothing of this CTA arrives on a barrier after its end
+    if (ok && n > 0) ok = wait(&bars.empty[(n - 1) % kLossStages], (n - 1) / kLossStages);
+    return ok;
+}
+
+// 32 columns of one row in staging: the warp's tile of 32 rows x 128 bytes in
+// the 128-byte swizzle.
+__device__ __forceinline__ void stage_row(unsigned char* staging, int lane, int half, const uint32_t* pk) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+        *reinterpret_cast<uint4*>(staging + lane * 128 + (((half * 4 + c) ^ (lane & 7)) << 4)) =
+            make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+}
+
+// d of the warp's 32 rows and one of its two slabs of 64 items.
+template <int DT, int P>
+__device__ __forceinline__ void d_slab(float* x, const RowStat& r, float coef, float c2, int64_t item0, int64_t V,
+                                       unsigned char* staging, const CUtensorMap& map, int col, int row, int64_t rows,
+                                       int lane) {
+#pragma unroll
+    for (int c = 0; c < 64; c += 2) {
+        fma2(x[c], x[c + 1], c2, r.minus_lse2, r.minus_lse2);
+        x[c] = ex2(x[c]);
+        x[c + 1] = ex2(x[c + 1]);
+    }
+    const int at = (int)tmin<int64_t>(tmax<int64_t>(r.target - item0, -1), 64);  // (target -1: before any item)
+    if (__any_sync(0xffffffffu, at >= 0 && at < 64)) {
+#pragma unroll
+        for (int c = 0; c < 64; ++c)
+            if (c == at) x[c] -= 1.f;
+    }
+    const int64_t left = V - item0;
+    if (left < 64) {
+#pragma unroll
+        for (int c = 0; c < 64; ++c)
+            if (c >= left) x[c] = 0.f;
+    }
+#pragma unroll
+    for (int c = 0; c < 64; c += 2) mul2(x[c], x[c + 1], coef, coef);
+#pragma unroll
+    for (int plane = 0; plane < P; ++plane) {
+        if (lane == 0) store_read_wait();
+        __syncwarp();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+                pk[c] = pack2<DT>(x[32 * h + 2 * c], x[32 * h + 2 * c + 1]);
+                if constexpr (P == 3) {
+                    x[32 * h + 2 * c] -= bf16_bits_to_float(pk[c] & 0xffffu);
+                    x[32 * h + 2 * c + 1] -= __uint_as_float(pk[c] & 0xffff0000u);
+                }
+            }
+            stage_row(staging, lane, h, pk);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0 && row < rows) store_box(map, smem_u32(staging), col, row, plane);
+    }
+}
+
+// The accumulator's 32-column chunks of this warpgroup (every other one) into
+// a slab of partial sums: [columns / 4][128 rows] of float4, so that a warp's
+// 32 rows are 512 consecutive bytes.
+__device__ __forceinline__ void add_slab(float4* to, uint32_t acc, int wide, int group, bool first) {
+    for (int c = group * 32; c < wide; c += 64) {
+        float x[32];
+        tmem_ld32_issue(acc + c, x);
+        float4 old[8];
+        if (!first) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) old[q] = to[(c / 4 + q) * 128];
+        }
+        tmem_wait_ld(x, 32);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            float4 v = make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
+            if (!first) v.x += old[q].x, v.y += old[q].y, v.z += old[q].z, v.w += old[q].w;
+            to[(c / 4 + q) * 128] = v;
+        }
+    }
+}
+
+// The same chunks, times `times`, as columns of the thread's row of a result
+// that starts at element `at` and has `left` columns.
+template <int OUT>
+__device__ __forceinline__ void store_rows(void* out, int64_t at, uint32_t acc, int wide, int group, bool valid,
+                                           int left, bool vec, float times) {
+    vec = vec && (uintptr_t)out % 16 == 0;
+    for (int c = group * 32; c < wide; c += 64) {
+        float x[32];
+        tmem_ld32_issue(acc + c, x);
+        tmem_wait_ld(x, 32);
+        if (!valid) continue;
+#pragma unroll
+        for (int e = 0; e < 32; ++e) x[e] *= times;
+        if (vec) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) {
+                if (c + e >= left) break;
+                if constexpr (OUT == DT_F32) {
+                    float4* to = reinterpret_cast<float4*>(static_cast<float*>(out) + at + c + e);
+                    to[0] = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+                    to[1] = make_float4(x[e + 4], x[e + 5], x[e + 6], x[e + 7]);
+                } else {
+                    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at + c + e) =
+                        make_uint4(pack2<OUT>(x[e], x[e + 1]), pack2<OUT>(x[e + 2], x[e + 3]),
+                                   pack2<OUT>(x[e + 4], x[e + 5]), pack2<OUT>(x[e + 6], x[e + 7]));
+                }
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+                if (c + e < left) store_elem<OUT>(out, at + c + e, x[e]);
+        }
+    }
+}
+
+// 128 rows of a result: the slabs' sum in order, times `times`, rounded.
+template <int OUT>
+__device__ __forceinline__ void finish(const float4* part, int64_t slab_stride, int slabs, void* out, int64_t row0,
+                                       int rows, int D, float times, int thread, int threads) {
+    const int groups = (D + 3) / 4;
+    const bool vec = D % 4 == 0 && (uintptr_t)out % 16 == 0;
+    for (int x = thread; x < groups * 128; x += threads) {
+        const int r = x % 128, g = x / 128;
+        if (r >= rows) continue;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int s = 0; s < slabs; ++s) {
+            const float4 y = part[s * slab_stride + g * 128 + r];
+            v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
+        }
+        v.x *= times, v.y *= times, v.z *= times, v.w *= times;
+        const int64_t at = (row0 + r) * D + g * 4;
+        if (vec) {
+            if constexpr (OUT == DT_F32)
+                *reinterpret_cast<float4*>(static_cast<float*>(out) + at) = v;
+            else
+                *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + at) =
+                    make_uint2(pack2<OUT>(v.x, v.y), pack2<OUT>(v.z, v.w));
+        } else {
+            const float y[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (g * 4 + e < D) store_elem<OUT>(out, at + e, y[e]);
+        }
+    }
+}
+
+__device__ __forceinline__ uint32_t begin(LossBars& bars, uint32_t* slot) {
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kLossStages; ++i) {
+            mbar_init(&bars.full[i], 1);
+            mbar_init(&bars.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars.acc_full[i], 1);
+            mbar_init(&bars.acc_empty[i], 8);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        fence_proxy_async_smem();
+    }
+    if (threadIdx.x / 32 == 9) tmem_alloc(slot, 512);
+    tcgen05_before_sync();
+    __syncthreads();
+    tcgen05_after_sync();
+    return *slot;
+}
+
+__device__ __forceinline__ void end(uint32_t tmem, bool ok, uint32_t* error) {
+    if (!ok) atomicOr(error, ERR_TIMEOUT);
+    tcgen05_before_sync();
+    __syncthreads();
+    tcgen05_after_sync();
+    if (threadIdx.x / 32 == 9) tmem_dealloc(tmem, 512);
+}
+
+// Backward pass: one launch's work items.
+template <int DT, int P>
+__global__ void __launch_bounds__(kLossThreads, 1)
+    loss_step_kernel(const LossStep p, const __grid_constant__ LossMaps maps) {
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    __shared__ LossBars bars;
+    __shared__ uint32_t slot;
+    const uint32_t tmem = begin(bars, &slot);
+    chain_wait();
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int n_items = p.n_gw + p.n_gx + p.n_d + p.n_fin_w + p.n_fin_x;
+    int item = blockIdx.x;
+    auto next = [&](Product& t) {
+        do {
+            if (item >= n_items) return false;
+            t = step_item(p, item);
+            item += gridDim.x;
+        } while (t.kind <= ITEM_GX && t.kblocks == 0);  // (the last piece has fewer blocks than slabs)
+        return true;
+    };
+    bool ok = true;
+    if (warp == 8) {
+        ok = produce<P>(smem, bars, maps, p.dw0, p.p0 - p.pw0, next);
+    } else if (warp == 9) {
+        ok = multiply<DT, P>(smem, bars, tmem, next);
+    } else {
+        constexpr int OUT = P == 3 ? DT_F32 : DT;
+        unsigned char* staging = smem + kLossStages * kStageBytes + warp * kStagingBytes;
+        const int quarter = warp % 4, group = warp / 4;
+        const float up = DT == DT_F16 ? range_scale(p.gmax, p.n_gmax, lane) : 1.f, down = 1.f / up;
+        int tile = 0;
+        Product t;
+        while (next(t)) {
+            if (t.kind == ITEM_FIN_W) {
+                finish<OUT>(p.f_part + (int64_t)(t.row0 / 128) * p.cols4 * 128,
+                            (int64_t)((p.f_items + 127) / 128) * p.cols4 * 128, p.w_slabs, p.gw, p.f0 + t.row0,
+                            tmin(128, p.f_items - t.row0), p.D, down, threadIdx.x, 256);
+                continue;
+            }
+            if (t.kind == ITEM_FIN_X) {
+                finish<OUT>(p.x_part + (int64_t)(t.row0 / 128) * p.cols4 * 128, (int64_t)p.row_tiles * p.cols4 * 128,
+                            p.x_slabs, p.gx, t.row0, (int)tmin<int64_t>(128, p.N - t.row0), p.D, down, threadIdx.x,
+                            256);
+                continue;
+            }
+            const int buf = tile & 1;
+            RowStat r{};
+            if (t.kind == ITEM_D) r = p.rows[t.row0 + quarter * 32 + lane];
+            if (ok) ok = mbar_wait_tight(&bars.acc_full[buf], (tile / 2) & 1);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tcgen05_after_sync();
+            const uint32_t acc = tmem + buf * 256 + ((uint32_t)(quarter * 32) << 16);
+            if (t.kind == ITEM_D) {
+                const float coef = r.coef * up;
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    const int c = group * 128 + s * 64;
+                    if (t.col0 + c >= p.V) break;
+                    float x[64];
+                    tmem_ld32_issue(acc + c, x);
+                    tmem_ld32_issue(acc + c + 32, x + 32);
+                    tmem_wait_ld(x, 64);
+                    d_slab<DT, P>(x, r, coef, p.c2, t.col0 + c, p.V, staging, maps.d_out, (int)(t.col0 - p.d0) + c,
+                                  t.row0 + quarter * 32, p.N, lane);
+                }
+            } else if (t.kind == ITEM_GW && p.w_slabs == 1) {
+                const int r = t.row0 + quarter * 32 + lane;
+                store_rows<OUT>(p.gw, (p.p0 + r) * p.D + t.col0, acc, t.wide, group, r < p.p_items,
+                                (int)(p.D - t.col0), p.D % 8 == 0, down);
+            } else {
+                const int tiles = t.kind == ITEM_GX ? p.row_tiles : (p.p_items + 127) / 128;
+                float4* to = (t.kind == ITEM_GX ? p.x_part : p.w_part) +
+                             ((int64_t)t.slab * tiles + t.row0 / 128) * p.cols4 * 128 + t.col0 / 4 * 128 +
+                             quarter * 32 + lane;
+                add_slab(to, acc, t.wide, group, t.kind == ITEM_GW || p.first);
+            }
+            tcgen05_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.acc_empty[buf]);
+            ++tile;
+        }
+        if (lane == 0) store_wait();
+    }
+    end(tmem, ok, p.error);
+}
+
+// Forward pass: a CTA's item is a tile of 128 rows and a slice of the table,
+// whose maximum and sum its threads (a row and half of a tile's columns each)
+// carry in registers.
+template <int DT, int P>
+__global__ void __launch_bounds__(kLossThreads, 1)
+    loss_forward_kernel(const LossForward p, const __grid_constant__ LossMaps maps) {
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    __shared__ LossBars bars;
+    __shared__ uint32_t slot;
+    const uint32_t tmem = begin(bars, &slot);
+    chain_wait();
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int n_items = p.row_tiles * p.slices;
+    int item = blockIdx.x, at = -1, end_at = 0;
+    auto next = [&](Product& t) {
+        if (at < 0) {
+            if (item >= n_items) return false;
+            const int slice = item / p.row_tiles;
+            at = (int)((int64_t)p.item_tiles * slice / p.slices);
+            end_at = (int)((int64_t)p.item_tiles * (slice + 1) / p.slices);
+        }
+        t = score_tile(p.v1, p.D, item % p.row_tiles * 128, p.v0 + (int64_t)at * 256);
+        t.slab = item / p.row_tiles;
+        t.k0 = 0;
+        if (++at == end_at) {
+            at = -1;
+            item += gridDim.x;
+        }
+        return true;
+    };
+    bool ok = true;
+    if (warp == 8) {
+        ok = produce<P>(smem, bars, maps, p.w0, 0, next);
+    } else if (warp == 9) {
+        ok = multiply<DT, P>(smem, bars, tmem, next);
+    } else {
+        const int quarter = warp % 4, group = warp / 4;
+        int tile = 0;
+        float m = -INFINITY, l = 0.f, picked = 0.f;
+        int64_t target = -1;
+        bool begins = true, found = false;
+        Product t;
+        while (next(t)) {
+            const int buf = tile & 1;
+            const int64_t row = t.row0 + quarter * 32 + lane;
+            if (begins) {
+                m = -INFINITY;
+                l = 0.f;
+                found = false;
+                target = -1;
+                if (row < p.N) {
+                    if (!p.first) {
+                        const float2 y = p.part[row * 2 * p.slices + t.slab * 2 + group];
+                        m = y.x;
+                        l = y.y;
+                    }
+                    target = p.index64 ? static_cast<const int64_t*>(p.targets)[row]
+                                       : static_cast<const int32_t*>(p.targets)[row];
+                    if (target >= p.V) {
+                        atomicOr(p.error, ERR_OOB);
+                        target = -1;
+                    }
+                }
+            }
+            begins = at < 0;  // the next tile begins an item
+            if (ok) ok = mbar_wait_tight(&bars.acc_full[buf], (tile / 2) & 1);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tcgen05_after_sync();
+            const uint32_t acc = tmem + buf * 256 + group * 128 + ((uint32_t)(quarter * 32) << 16);
+            const int64_t item0 = t.col0 + group * 128;
+            const int left = (int)tmin<int64_t>(128, p.v1 - item0);  // items of this half
+            const int mine = (int)tmin<int64_t>(tmax<int64_t>(target - item0, -1), 128);
+#pragma unroll 1
+            for (int c = 0; c < left; c += 32) {
+                float x[32];
+                tmem_ld32_issue(acc + c, x);
+                tmem_wait_ld(x, 32);
+                if (left - c < 32) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (e >= left - c) x[e] = -INFINITY;
+                }
+                if (__any_sync(0xffffffffu, mine >= c && mine < c + 32)) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)  // (in C++ it becomes an indexed copy in local memory)
+                        asm("{\n\t.reg .pred q;\n\tsetp.eq.s32 q, %1, 0;\n\t@q mov.f32 %0, %2;\n\t}"
+                            : "+f"(picked)
+                            : "r"(mine - c - e), "f"(x[e]));
+                    found |= mine >= c && mine < c + 32;
+                }
+                float u[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) u[e] = fmaxf(max3(x[e], x[e + 8], x[e + 16]), x[e + 24]);
+                const float top = fmaxf(max3(max3(u[0], u[1], u[2]), u[3], u[4]), max3(u[5], u[6], u[7])) * p.c2;
+                const float to = fmaxf(m, top);
+                l *= ex2(m - to);  // (m = -inf: 0)
+                m = to;
+                float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+                    fma2(x[e], x[e + 1], p.c2, -to, -to);
+                    add2(s0, s1, ex2(x[e]), ex2(x[e + 1]));
+                }
+                l += s0 + s1;
+            }
+            tcgen05_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.acc_empty[buf]);
+            ++tile;
+            if (begins && row < p.N) {
+                p.part[row * 2 * p.slices + t.slab * 2 + group] = make_float2(m, l);
+                if (found) p.picked[row] = picked * p.c2;
+            }
+        }
+    }
+    end(tmem, ok, p.error);
+}
+
+template <int DT, int P>
+cudaError_t configure() {
+    cudaError_t e = cudaFuncSetAttribute(loss_step_kernel<DT, P>, cudaFuncAttributeMaxDynamicSharedMemorySize, kLossSmem);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(loss_forward_kernel<DT, P>, cudaFuncAttributeMaxDynamicSharedMemorySize, kLossSmem);
+    return e;
+}
+
+}  // namespace
+
+cudaError_t loss_mma_configure() {
+    cudaError_t e = configure<DT_F16, 1>();
+    if (e == cudaSuccess) e = configure<DT_BF16, 1>();
+    if (e == cudaSuccess) e = configure<DT_BF16, 3>();
+    return e;
+}
+
+cudaError_t launch_loss_forward(const LossForward& p, const LossMaps& maps, int dtype, int grid, cudaStream_t s) {
+    auto* kernel = dtype == DT_F32   ? loss_forward_kernel<DT_BF16, 3>
+                   : dtype == DT_F16 ? loss_forward_kernel<DT_F16, 1>
+                                     : loss_forward_kernel<DT_BF16, 1>;
+    return launch_chained_smem(kernel, dim3(grid), dim3(kLossThreads), kLossSmem, s, p, maps);
+}
+
+cudaError_t launch_loss_step(const LossStep& p, const LossMaps& maps, int dtype, int grid, cudaStream_t s) {
+    auto* kernel = dtype == DT_F32   ? loss_step_kernel<DT_BF16, 3>
+                   : dtype == DT_F16 ? loss_step_kernel<DT_F16, 1>
+                                     : loss_step_kernel<DT_BF16, 1>;
+    return launch_chained_smem(kernel, dim3(grid), dim3(kLossThreads), kLossSmem, s, p, maps);
+}
+
+}  // namespace tbe

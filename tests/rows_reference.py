@@ -17,7 +17,8 @@ Loss: the tensor units may cut instead of round, 2 f a step.
   s     2 (D + 8) f scale |x|.|w| =: es
   lse   sum_v p es + (V + 8) f + 2^-21 + 4 f |lse| =: el  (ex2: 2^-22)
   d     |g| scale (p (es + el + 2^-21) + 8 f (p + [target])) + u |d| =: ed, fp16: and
-        its smallest step where the largest |g| stands at 2^14 or more
+        its smallest step where the largest |g| stands at 2^14 or more; and 2^-126 (|g| scale + 3):
+        ex2 gives 0 below 2^-126, and so may each of the (up to three) bf16 parts of d
   grad_x    sum_v ed |w| + 2 (V + 8) f sum_v |d| |w| + u |grad_x|, grad_table alike
 """
 
@@ -99,6 +100,7 @@ def loss(x, w, targets, scale, g=None, dtype=torch.float32):
     size = (np.abs(g) * scale)[:, None]
     dd = (g * scale)[:, None] * (p - hot)
     ed = size * (p * (es + el[:, None] + 2.0 ** -21) + 8 * F * (p + hot)) + max(u, 4 * F) * np.abs(dd)
+    ed = ed + 2.0 ** -126 * (size + 3.0) * keep[:, None]
     if dtype == torch.float16:  # a step of 2^-24 beside a largest value of 2^14 or more
         ed = ed + np.abs(g).max(initial=0.0) * scale * 2.0 ** -38 * keep[:, None]
     ax, aw = np.abs(x), np.abs(w)
