@@ -77,40 +77,71 @@ struct RowsIn {
     Copy x;
     const void* targets;
     int32_t index64;
-    int64_t V, padded;  // padded: rows of `rows`, to whole tiles
+    int64_t V, tiles;
     const float *lse, *g;
     float scale;
-    RowStat* rows;
-    float* gmax;  // [CTAs]
+    float* rows;   // [tiles][kRowValues]
+    float* range;  // the power of two that fp16's d is multiplied by, else 1
+    float* gmax;   // fp16: kMaxCtas partial maxima
     uint32_t* error;
 };
 
-// The backward pass's rows: x copied with zeros in the rows left out, what
-// each row brings, and per CTA the largest finite |coef|.
-template <int DT>
-__global__ void __launch_bounds__(256) loss_rows_kernel(const RowsIn p) {
+__device__ __forceinline__ int64_t row_target(const RowsIn& p, int64_t row) {
+    const int64_t t =
+        p.index64 ? static_cast<const int64_t*>(p.targets)[row] : static_cast<const int32_t*>(p.targets)[row];
+    if (t >= p.V) atomicOr(p.error, ERR_OOB);
+    return t >= 0 && t < p.V ? t : -1;
+}
+
+// fp16: the largest finite |g scale| of the rows, in parts.
+constexpr int kMaxCtas = 64;
+__global__ void __launch_bounds__(256) loss_max_kernel(const RowsIn p) {
     chain_wait();
     __shared__ float most[8];
-    const int lane = threadIdx.x % 32;
     float m = 0.f;
-    for (int64_t row = ((int64_t)blockIdx.x * 256 + threadIdx.x) / 32; row < p.padded; row += (int64_t)gridDim.x * 8) {
-        RowStat r{0.f, 0.f, -1, 0};
-        if (row < p.x.rows) {
-            const int64_t t =
-                p.index64 ? static_cast<const int64_t*>(p.targets)[row] : static_cast<const int32_t*>(p.targets)[row];
-            if (t >= p.V && lane == 0) atomicOr(p.error, ERR_OOB);
-            if (t >= 0 && t < p.V) r = RowStat{-p.lse[row] * kLog2e, p.g[row] * p.scale, (int32_t)t, 0};
-            copy_row<DT>(p.x, row, r.target < 0, lane);
-        }
-        const float a = fabsf(r.coef);
-        if (a <= FLT_MAX) m = fmaxf(m, a);
-        if (lane == 0) p.rows[row] = r;
+    for (int64_t row = (int64_t)blockIdx.x * 256 + threadIdx.x; row < p.x.rows; row += (int64_t)gridDim.x * 256) {
+        const float a = fabsf(p.g[row] * p.scale);
+        if (a <= FLT_MAX && row_target(p, row) >= 0) m = fmaxf(m, a);
     }
-    if (lane == 0) most[threadIdx.x / 32] = m;
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (threadIdx.x % 32 == 0) most[threadIdx.x / 32] = m;
     __syncthreads();
     if (threadIdx.x == 0) {
         for (int w = 1; w < 8; ++w) m = fmaxf(m, most[w]);
         p.gmax[blockIdx.x] = m;
+    }
+}
+
+// The backward pass's rows, one warp each: x copied with zeros in the rows left
+// out, and what each row brings.  fp16's range is narrow (6e-8 to 65504) and d
+// moves with g and with the weights, 1 / V each: it is held times the power of
+// two that brings the largest |g scale| into [2^14, 2^15), so that weights down
+// to 2^-28 keep all their bits; the results are divided by it, exactly.
+template <int DT>
+__global__ void __launch_bounds__(256) loss_rows_kernel(const RowsIn p) {
+    chain_wait();
+    const int lane = threadIdx.x % 32;
+    float up = 1.f;
+    if constexpr (DT == DT_F16) {
+        float m = fmaxf(p.gmax[lane], p.gmax[lane + 32]);
+#pragma unroll
+        for (int o = 16; o > 0; o /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        // (27: the power stays below 2^115)
+        const int e = tmax((int)(__float_as_uint(m) >> 23), 27);
+        if (m > 0.f) up = __uint_as_float((uint32_t)(127 + 14 + 127 - e) << 23);
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.range = up;
+    for (int64_t row = ((int64_t)blockIdx.x * 256 + threadIdx.x) / 32; row < p.tiles * 128;
+         row += (int64_t)gridDim.x * 8) {
+        float* to = p.rows + row / 128 * kRowValues + row % 128;
+        const int64_t t = row < p.x.rows ? row_target(p, row) : -1;
+        if (row < p.x.rows) copy_row<DT>(p.x, row, t < 0, lane);
+        if (lane == 0) {
+            to[0] = t < 0 ? 0.f : -p.lse[row] * kLog2e;
+            to[128] = t < 0 ? 0.f : p.g[row] * p.scale * up;
+            to[256] = __int_as_float((int)t);
+        }
     }
 }
 
@@ -175,22 +206,27 @@ int64_t up_to(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 // the table stay in L2 (129 MB).
 constexpr int64_t kPieceBytes = 48 << 20;
 // Work items that the sums' parts make at most.
-constexpr int kMostParts = 304;
-constexpr int kRowCtas = 512;
+constexpr int kMostParts = 608;
+constexpr int kRowCtas = 1024;
 
 struct Plan {
     int planes, pitch, cols4, col_tiles;
     int64_t row_tiles;
     int64_t piece;  // items
     int64_t span;   // items of a copied part of the table, whole pieces
-    size_t rows, gmax, x, w, d, x_part, w_part, total;  // offsets
+    size_t rows, range, x, w, d, x_part, w_part, total;  // offsets
     size_t w_bytes, d_bytes, w_part_bytes;              // of one of two
 };
+
+// Whether the fused kernels take the call (their accumulators are 256 columns
+// wide); others go through pieces of d in memory.
+bool takes_fused(const tbe_softmax_loss* h) { return h->c.dtype != TBE_F32 && h->c.dim <= 256; }
 
 // Sized so that a workspace serves every smaller call: each size grows with N
 // and V although the piece shrinks with N.
 Plan make_plan(const tbe_softmax_loss* h, int64_t N, int64_t V, bool backward, bool copied) {
     Plan L{};
+    const bool fused = backward && takes_fused(h);
     const int D = h->c.dim;
     L.planes = h->c.dtype == TBE_F32 ? 3 : 1;
     L.pitch = (int)up_to(D, 8);
@@ -212,19 +248,22 @@ Plan make_plan(const tbe_softmax_loss* h, int64_t N, int64_t V, bool backward, b
         const int64_t budget = h->c.dtype != TBE_F32 && D % 8 == 0 ? 16 << 20 : 64 << 20;
         const int64_t items = std::max<int64_t>(256, budget / item_bytes / 256 * 256);
         L.piece = std::min(L.piece, items);
-        L.span = backward ? items / L.piece * L.piece : items;
+        L.span = backward && !fused ? items / L.piece * L.piece : items;
         L.w_bytes = align_up((size_t)(std::min(padded, items) * item_bytes));
         L.w = take(2 * L.w_bytes);
     }
     if (backward) {
-        L.rows = take(sizeof(RowStat) * 128 * L.row_tiles);
-        L.gmax = take(sizeof(float) * kRowCtas);
-        L.d_bytes = align_up((size_t)std::min(std::max(room, 256 * N), N * padded) * 2 * L.planes);
-        L.d = take(2 * L.d_bytes);
+        L.rows = take(sizeof(float) * kRowValues * L.row_tiles);
+        L.range = take(sizeof(float) * (1 + kMaxCtas));
         const size_t tile = (size_t)L.cols4 * 128 * sizeof(float4);
+        // (one sum over all items needs no slabs, and several make kMostParts tiles at most)
         L.x_part = take(std::max<int64_t>(L.row_tiles, kMostParts / L.col_tiles + 1) * tile);
         L.w_part_bytes = (kMostParts / L.col_tiles + 1) * tile;
-        L.w_part = take(2 * L.w_part_bytes);
+        L.w_part = take((fused ? 1 : 2) * L.w_part_bytes);
+        if (!fused) {
+            L.d_bytes = align_up((size_t)std::min(std::max(room, 256 * N), N * padded) * 2 * L.planes);
+            L.d = take(2 * L.d_bytes);
+        }
     } else {
         L.rows = take(sizeof(float) * N);                                   // picked
         L.d = take(sizeof(float2) * 2 * (N + 128 * (int64_t)kMostParts));  // part
@@ -312,7 +351,7 @@ struct Table {
 int choose_slices(int64_t row_tiles, int64_t item_tiles, int ctas) {
     int best = 1;
     int64_t least = INT64_MAX;
-    const int64_t most = std::min<int64_t>(item_tiles, kMostParts / row_tiles + 1);
+    const int64_t most = std::min<int64_t>(item_tiles, std::max<int64_t>(1, kMostParts / row_tiles));
     for (int64_t s = 1; s <= most; ++s) {
         const int64_t turns = (row_tiles * s + ctas - 1) / ctas, time = turns * ((item_tiles + s - 1) / s);
         if (time < least) {
@@ -357,27 +396,84 @@ int forward(const tbe_softmax_loss* h, const Plan& L, LossForward p, const void*
                                  p.V, loss, lse));
 }
 
-int backward(const tbe_softmax_loss* h, const Plan& L, LossStep p, RowsIn rows, const void* table, int64_t table_stride,
+cudaError_t launch_rows(const tbe_softmax_loss* h, const Plan& L, RowsIn rows, char* base, cudaStream_t s) {
+    rows.rows = at<float>(base, L.rows);
+    rows.range = at<float>(base, L.range);
+    rows.gmax = rows.range + 1;
+    rows.tiles = L.row_tiles;
+    rows.x.to = at<uint16_t>(base, L.x);
+    const dim3 grid((unsigned)std::min<int64_t>(rows.tiles * 16, kRowCtas));
+    if (h->c.dtype == TBE_F32) return launch_chained(loss_rows_kernel<DT_F32>, grid, dim3(256), s, rows);
+    if (h->c.dtype == TBE_BF16) return launch_chained(loss_rows_kernel<DT_BF16>, grid, dim3(256), s, rows);
+    const cudaError_t e = launch_chained(loss_max_kernel, dim3(kMaxCtas), dim3(256), s, rows);
+    return e != cudaSuccess ? e : launch_chained(loss_rows_kernel<DT_F16>, grid, dim3(256), s, rows);
+}
+
+int backward_fused(const tbe_softmax_loss* h, const Plan& L, LossFused p, const RowsIn& rows, const void* table,
+                   int64_t table_stride, void* gx, void* gw, char* base, cudaStream_t s) {
+    const int dt = h->c.dtype;
+    LossFusedMaps maps{};
+    cudaError_t e = launch_rows(h, L, rows, base, s);
+    if (e != cudaSuccess) return cuda_fail(e);
+    p.rows = at<float>(base, L.rows);
+    p.range = at<float>(base, L.range);
+    p.cols4 = L.cols4;
+    if (!encode(&maps.x, dt, base + L.x, p.D, p.N, 1, L.pitch, 64)) return TBE_ERR_CUDA;
+    Table w{h, table, table_stride, p.V, L.span, 1, L.pitch, direct(h, table, table_stride, p.V), base + L.w, L.w_bytes};
+    const int64_t whole = w.is_direct ? p.V : std::min(p.V, L.span);
+    const int x_slices = choose_slices(L.row_tiles, (whole + 127) / 128, h->num_sms);
+    for (p.v0 = 0; p.v0 < p.V; p.v0 = p.v1) {
+        p.v1 = std::min(p.V, p.v0 + whole);
+        p.w0 = w.first(p.v0);
+        e = w.fetch(p.v0, s);
+        if (e != cudaSuccess) return cuda_fail(e);
+        if (!w.map(&maps.w, p.v0)) return TBE_ERR_CUDA;
+        const int64_t item_tiles = (p.v1 - p.v0 + 127) / 128;
+        if (gx) {
+            LossFused q = p;
+            q.tiles = (int)L.row_tiles;
+            q.others = (int)item_tiles;
+            q.slices = x_slices;
+            q.first = p.v0 == 0;
+            q.last = p.v1 == p.V;
+            q.part = at<float4>(base, L.x_part);
+            q.out = gx;
+            e = launch_loss_fused(q, maps, dt, false, q.tiles * q.slices, s);
+            if (e == cudaSuccess && q.last && !(q.slices == 1 && q.first))
+                e = launch_loss_finish(LossFinish{q.part, p.range, gx, p.N, q.tiles, q.slices, p.D, L.cols4}, dt, s);
+            if (e != cudaSuccess) return cuda_fail(e);
+        }
+        if (gw) {
+            LossFused q = p;
+            q.tiles = (int)item_tiles;
+            q.others = (int)L.row_tiles;
+            q.slices = choose_slices(item_tiles, L.row_tiles, h->num_sms);
+            q.first = q.last = 1;
+            q.part = at<float4>(base, L.w_part);
+            q.out = static_cast<char*>(gw) + p.v0 * p.D * 2;
+            e = launch_loss_fused(q, maps, dt, true, q.tiles * q.slices, s);
+            if (e == cudaSuccess && q.slices > 1)
+                e = launch_loss_finish(LossFinish{q.part, p.range, q.out, p.v1 - p.v0, q.tiles, q.slices, p.D, L.cols4},
+                                       dt, s);
+            if (e != cudaSuccess) return cuda_fail(e);
+        }
+    }
+    return TBE_OK;
+}
+
+int backward(const tbe_softmax_loss* h, const Plan& L, LossStep p, const RowsIn& rows, const void* table, int64_t table_stride,
              char* base, cudaStream_t s) {
     LossMaps maps{};
     const int dt = h->c.dtype;
-    rows.rows = at<RowStat>(base, L.rows);
-    rows.gmax = at<float>(base, L.gmax);
-    rows.padded = L.row_tiles * 128;
-    rows.x.to = at<uint16_t>(base, L.x);
-    const unsigned row_ctas = (unsigned)std::min<int64_t>(rows.padded / 8, kRowCtas);
-    cudaError_t e = dt == TBE_F32   ? launch_chained(loss_rows_kernel<DT_F32>, dim3(row_ctas), dim3(256), s, rows)
-                    : dt == TBE_F16 ? launch_chained(loss_rows_kernel<DT_F16>, dim3(row_ctas), dim3(256), s, rows)
-                                    : launch_chained(loss_rows_kernel<DT_BF16>, dim3(row_ctas), dim3(256), s, rows);
+    cudaError_t e = launch_rows(h, L, rows, base, s);
     if (e != cudaSuccess) return cuda_fail(e);
-    p.rows = rows.rows;
-    p.gmax = rows.gmax;
-    p.n_gmax = (int)row_ctas;
+    p.rows = at<float>(base, L.rows);
+    p.range = at<float>(base, L.range);
     p.row_tiles = (int)L.row_tiles;
     p.col_tiles = L.col_tiles;
     p.cols4 = L.cols4;
     p.x_part = at<float4>(base, L.x_part);
-    if (!encode(&maps.x, dt, rows.x.to, p.D, p.N, L.planes, L.pitch, 64)) return TBE_ERR_CUDA;
+    if (!encode(&maps.x, dt, base + L.x, p.D, p.N, L.planes, L.pitch, 64)) return TBE_ERR_CUDA;
     Table w{h, table, table_stride, p.V, L.span, L.planes, L.pitch, direct(h, table, table_stride, p.V), base + L.w,
             L.w_bytes};
 
@@ -425,9 +521,9 @@ int backward(const tbe_softmax_loss* h, const Plan& L, LossStep p, RowsIn rows, 
             q.f0 = (j - 2) * L.piece;
             q.f_items = (int)std::min(L.piece, p.V - q.f0);
             q.f_part = at<float4>(base, L.w_part + ((j - 2) & 1) * L.w_part_bytes);
-            q.n_fin_w = (q.f_items + 127) / 128;
+            q.n_fin_w = (q.f_items + 127) / 128 * ((p.D + 31) / 32);
         }
-        if (j == pieces + 1 && p.gx) q.n_fin_x = (int)L.row_tiles;
+        if (j == pieces + 1 && p.gx) q.n_fin_x = (int)L.row_tiles * ((p.D + 31) / 32);
         const int64_t n = (int64_t)q.n_d + q.n_gx + q.n_gw + q.n_fin_w + q.n_fin_x;
         if (n == 0) continue;
         e = launch_loss_step(q, maps, dt, (int)std::min<int64_t>(n, h->num_sms), s);
@@ -454,6 +550,7 @@ int tbe_softmax_loss_create(const tbe_softmax_loss_config* c, tbe_softmax_loss**
     cudaError_t e = cudaGetDevice(&h->device);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, h->device);
     if (e == cudaSuccess) e = loss_mma_configure();
+    if (e == cudaSuccess) e = loss_fused_configure();
     if (e == cudaSuccess) e = cudaMalloc(&h->error, 16);
     if (e == cudaSuccess) e = cudaMemset(h->error, 0, 16);
     if (e != cudaSuccess) {
@@ -515,10 +612,15 @@ int tbe_softmax_loss_backward(tbe_softmax_loss* h, const void* x, int64_t x_stri
     rows.x = make_copy(h, x, x_stride, N, L.pitch, nullptr);
     rows.targets = targets, rows.index64 = index_dtype == TBE_I64, rows.V = V;
     rows.lse = lse, rows.g = grad_loss, rows.scale = h->c.scale, rows.error = h->error;
+    char* base = reinterpret_cast<char*>(align_up(reinterpret_cast<uintptr_t>(workspace)));
+    if (takes_fused(h)) {
+        LossFused p{};
+        p.N = N, p.V = V, p.D = h->c.dim, p.c2 = h->c.scale * kLog2e, p.error = h->error;
+        return backward_fused(h, L, p, rows, table, table_stride, grad_x, grad_table, base, s);
+    }
     LossStep p{};
     p.N = N, p.V = V, p.D = h->c.dim, p.c2 = h->c.scale * kLog2e;
     p.gx = grad_x, p.gw = grad_table, p.error = h->error;
-    char* base = reinterpret_cast<char*>(align_up(reinterpret_cast<uintptr_t>(workspace)));
     return backward(h, L, p, rows, table, table_stride, base, s);
 }
 

@@ -1,0 +1,362 @@
+// The softmax loss's gradients for 16-bit operands of up to 256 columns: the
+// logits' gradients d never leave the SM.
+//
+// A CTA holds 128 rows (grad_x) or 128 items (grad_table) in shared memory and
+// walks the tiles of 128 of the others:
+//   grad_x:      S = X W^T,  d = coef (2^(S c - lse) - [target]),  dX += d W
+//   grad_table:  S = W X^T,  d likewise, transposed,               dW += d X
+// S (fp32) and d (16-bit, the second product's first operand) live in tensor
+// memory; the walked tile serves both products, K-major in the first and
+// MN-major in the second, so it is fetched once.  That is four products of
+// 2 N V D for both gradients where d in memory takes three, but no logit's
+// gradient is written or read (6 bytes each, against 4 D operations).
+//
+// Warp 8 fetches, warp 9 issues the products, warps 0 to 7 compute d: a thread
+// has one line of S and half of its columns.  S is double buffered.  Up to 128
+// columns d has columns of its own beside it, so the next S does not wait for
+// the last product; above, d takes its S's place.
+#include "loss_mma.cuh"
+
+namespace tbe {
+
+namespace {
+
+constexpr int kFusedThreads = 320;
+
+template <int DP>
+struct Fused {
+    static constexpr int kTile = 128 * DP * 2;
+    static constexpr int kStages = DP == 64 ? 6 : DP == 128 ? 4 : DP == 192 ? 3 : 2;
+    static constexpr int kStats = kRowValues * 4;  // bytes of a tile's rows' values
+    static constexpr int ring = kTile, stats = ring + kStages * kTile;
+    static constexpr int bytes = stats + kStages * kStats + 1024;
+    static constexpr bool kApart = DP <= 128;  // d beside S
+    // tensor memory: S at 0 and 128, d in its place or at 256 and 320, the sums behind
+    static constexpr int sums = kApart ? 384 : 256;
+    static constexpr int d_at(int buf) { return kApart ? 256 + buf * 64 : buf * 128; }
+    static constexpr int kGap = kApart ? 0 : 32;  // columns between d's halves
+};
+
+struct FusedBars {
+    uint64_t held, full[6], empty[6], s_full[2], d_full[2], done[2];
+};
+
+// 64 columns of the thread's line.
+template <bool ITEMS>
+__device__ __forceinline__ void gradients(float* x, float c2, float minus_lse2, float coef, int at, int left,
+                                          const float* stats, int line) {
+    if constexpr (!ITEMS) {
+#pragma unroll
+        for (int c = 0; c < 64; c += 2) {
+            fma2(x[c], x[c + 1], c2, minus_lse2, minus_lse2);
+            x[c] = ex2(x[c]);
+            x[c + 1] = ex2(x[c + 1]);
+        }
+        if (__any_sync(0xffffffffu, at >= 0 && at < 64)) {
+#pragma unroll
+            for (int c = 0; c < 64; ++c)
+                if (c == at) x[c] -= 1.f;
+        }
+        if (left < 64) {
+#pragma unroll
+            for (int c = 0; c < 64; ++c)
+                if (c >= left) x[c] = 0.f;
+        }
+#pragma unroll
+        for (int c = 0; c < 64; c += 2) mul2(x[c], x[c + 1], coef, coef);
+    } else {
+        // columns are rows of x: their values lie in shared memory
+#pragma unroll
+        for (int c = 0; c < 64; c += 4) {
+            const float4 l = *reinterpret_cast<const float4*>(stats + c);
+            fma2(x[c], x[c + 1], c2, l.x, l.y);
+            fma2(x[c + 2], x[c + 3], c2, l.z, l.w);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[c + e] = ex2(x[c + e]);
+        }
+        const int lane = threadIdx.x % 32;
+        const int first = line - lane;  // the warp's items
+        const int t0 = __float_as_int(stats[256 + lane]) - first, t1 = __float_as_int(stats[288 + lane]) - first;
+        const uint32_t lo = __ballot_sync(0xffffffffu, t0 >= 0 && t0 < 32);
+        const uint32_t hi = __ballot_sync(0xffffffffu, t1 >= 0 && t1 < 32);
+        if (lo | hi) {
+#pragma unroll
+            for (int c = 0; c < 64; ++c)
+                if ((c < 32 ? lo : hi) >> (c % 32) & 1)
+                    if (__float_as_int(stats[256 + c]) == line) x[c] -= 1.f;
+        }
+#pragma unroll
+        for (int c = 0; c < 64; c += 4) {
+            const float4 g = *reinterpret_cast<const float4*>(stats + 128 + c);
+            mul2(x[c], x[c + 1], g.x, g.y);
+            mul2(x[c + 2], x[c + 3], g.z, g.w);
+        }
+    }
+}
+
+template <int DT, int DP, bool ITEMS>
+__global__ void __launch_bounds__(kFusedThreads, 1)
+    loss_fused_kernel(const LossFused p, const __grid_constant__ LossFusedMaps maps) {
+    using L = Fused<DP>;
+    constexpr int kStages = L::kStages;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    __shared__ FusedBars bars;
+    __shared__ uint32_t slot;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    if (threadIdx.x == 0) {
+        mbar_init(&bars.held, 1);
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&bars.full[i], 1);
+            mbar_init(&bars.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars.s_full[i], 1);
+            mbar_init(&bars.d_full[i], 8);
+            mbar_init(&bars.done[i], 1);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        fence_proxy_async_smem();
+    }
+    if (warp == 9) tmem_alloc(&slot, 512);
+    tcgen05_before_sync();
+    __syncthreads();
+    tcgen05_after_sync();
+    const uint32_t tmem = slot;
+    chain_wait();
+
+    // the CTA's tile and the tiles [from, to) that it walks
+    const int tile = blockIdx.x % p.tiles, slice = blockIdx.x / p.tiles;
+    const int from = (int)((int64_t)p.others * slice / p.slices);
+    const int n = (int)((int64_t)p.others * (slice + 1) / p.slices) - from;
+    bool ok = true;
+    if (n == 0) {  // (a last span of fewer tiles than slices)
+    } else if (warp == 8) {
+        // ---- loader
+        const uint32_t base = smem_u32(smem);
+        const int64_t item0 = p.v0 - p.w0;
+        auto load = [&](uint32_t dst, const CUtensorMap& map, int64_t row, uint64_t* bar) {
+#pragma unroll
+            for (int c = 0; c < DP / 64; ++c)
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+                    load_box(dst + c * (2 * kBox) + r * kBox, map, c * 64, row + r * 64, 0, bar);
+        };
+        if (elect_one()) {
+            mbar_expect_tx(&bars.held, L::kTile);
+            load(base, ITEMS ? maps.w : maps.x, (ITEMS ? item0 : 0) + (int64_t)tile * 128, &bars.held);
+        }
+        __syncwarp();
+        int i = 0;
+        for (; i < n; ++i) {
+            const int st = i % kStages;
+            if (i >= kStages) ok = mbar_wait_tight(&bars.empty[st], (i / kStages - 1) & 1);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            if (elect_one()) {
+                const int64_t other = from + i;
+                mbar_expect_tx(&bars.full[st], L::kTile + (ITEMS ? L::kStats : 0));
+                load(base + L::ring + st * L::kTile, ITEMS ? maps.x : maps.w, (ITEMS ? 0 : item0) + other * 128,
+                     &bars.full[st]);
+                if constexpr (ITEMS)
+                    asm volatile(
+                        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                            base + L::stats + st * L::kStats),
+                        "l"(p.rows + other * kRowValues), "r"(L::kStats), "r"(smem_u32(&bars.full[st]))
+                        : "memory");
+            }
+            __syncwarp();
+        }
+        if (!ok) {  // this CTA's copies in flight land before it ends
+            mbar_wait_tight(&bars.held, 0);
+            for (int j = tmax(0, i - kStages); j < i; ++j) mbar_wait_tight(&bars.full[j % kStages], (j / kStages) & 1);
+        }
+    } else if (warp == 9) {
+        // ---- products
+        const int ksteps = (p.D + 15) / 16;
+        const uint32_t id_s = mma_idesc(DT == DT_BF16, 128, 128);
+        const uint32_t id_o = mma_idesc(DT == DT_BF16, 128, ksteps * 16) | kMnMajorB;
+        const uint64_t held = smem_desc_sw128(smem_u32(smem), 1024);
+        const uint64_t walk = smem_desc_sw128(smem_u32(smem) + L::ring, 1024);
+        const uint64_t walk_mn = smem_desc_mn(smem_u32(smem) + L::ring, 2 * kBox);
+        auto wait = [&](uint64_t* bar, int phase) {
+            const bool in = mbar_wait_tight(bar, phase & 1);
+            const bool all = __all_sync(0xffffffffu, in);
+            tcgen05_after_sync();
+            return all;
+        };
+        auto scores = [&](int i) {
+            const int st = i % kStages;
+            if (!wait(&bars.full[st], i / kStages)) return false;
+            if (elect_one()) {
+                const uint64_t b = walk + (uint64_t)(st * (L::kTile / 16));
+#pragma unroll
+                for (int k = 0; k < DP / 16; ++k)
+                    if (k < ksteps)
+                        mma_f16(tmem + (i & 1) * 128, held + (k / 4) * (2 * kBox / 16) + (k % 4) * 2,
+                                b + (k / 4) * (2 * kBox / 16) + (k % 4) * 2, id_s, k > 0);
+                mma_commit(&bars.s_full[i & 1]);
+            }
+            __syncwarp();
+            return true;
+        };
+        ok = wait(&bars.held, 0) && scores(0);
+        for (int i = 0; i < n && ok; ++i) {
+            const int st = i % kStages, buf = i & 1;
+            if (i + 1 < n) {
+                // the next scores' place: read once the last d is there, and free
+                // of that d (where it lies there) once its product is done
+                if (i >= 1 && !L::kApart) ok = wait(&bars.done[buf ^ 1], (i - 1) / 2);
+                ok = ok && scores(i + 1);
+            }
+            ok = ok && wait(&bars.d_full[buf], i / 2);
+            if (!ok) break;
+            if (elect_one()) {
+                const uint64_t b = walk_mn + (uint64_t)(st * (L::kTile / 16));
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    mma_f16_ts(tmem + L::sums, tmem + L::d_at(buf) + k * 8 + (k / 4) * L::kGap, b + k * (2048 / 16), id_o,
+                               i > 0 || k > 0);
+                mma_commit(&bars.empty[st]);
+                mma_commit(&bars.done[buf]);
+            }
+            __syncwarp();
+        }
+        // nothing of this CTA arrives on a barrier after its end
+        if (ok) ok = wait(&bars.empty[(n - 1) % kStages], (n - 1) / kStages);
+    } else {
+        // ---- d, then the sums
+        const int quarter = warp % 4, group = warp / 4, line = quarter * 32 + lane;
+        const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+        float minus_lse2 = 0.f, coef = 0.f;
+        int target = -1;
+        if constexpr (!ITEMS) {
+            const float* r = p.rows + (int64_t)tile * kRowValues + line;
+            minus_lse2 = __ldg(r);
+            coef = __ldg(r + 128);
+            target = __float_as_int(__ldg(r + 256));
+        }
+        for (int i = 0; i < n; ++i) {
+            const int buf = i & 1;
+            ok = mbar_wait_tight(&bars.s_full[buf], (i / 2) & 1);
+            if (ITEMS && ok) ok = mbar_wait_tight(&bars.full[i % kStages], (i / kStages) & 1);  // the rows' values
+            if (!__all_sync(0xffffffffu, ok)) {
+                ok = false;
+                break;
+            }
+            tcgen05_after_sync();
+            float x[64];
+            tmem_ld32_issue(tmem + buf * 128 + group * 64 + lanes, x);
+            tmem_ld32_issue(tmem + buf * 128 + group * 64 + 32 + lanes, x + 32);
+            tmem_wait_ld(x, 64);
+            if constexpr (ITEMS) {
+                const float* stats = reinterpret_cast<const float*>(smem + L::stats + i % kStages * L::kStats) + group * 64;
+                gradients<true>(x, p.c2, 0.f, 0.f, 0, 64, stats, (int)(p.v0 + (int64_t)tile * 128) + line);
+            } else {
+                const int64_t item0 = p.v0 + (int64_t)(from + i) * 128 + group * 64;
+                const int at = (int)tmin<int64_t>(tmax<int64_t>(target - item0, -1), 64);
+                const int left = (int)tmin<int64_t>(tmax<int64_t>(p.v1 - item0, 0), 64);
+                gradients<false>(x, p.c2, minus_lse2, coef, at, left, nullptr, 0);
+            }
+            if (L::kApart && i >= 2) {  // d's columns are free of the product before last
+                ok = mbar_wait_tight(&bars.done[buf], (i / 2 - 1) & 1);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    ok = false;
+                    break;
+                }
+                tcgen05_after_sync();
+            }
+#pragma unroll
+            for (int h = 0; h < 64; h += 32) {
+                uint32_t pk[16];
+#pragma unroll
+                for (int c = 0; c < 16; ++c) pk[c] = pack2<DT>(x[h + 2 * c], x[h + 2 * c + 1]);
+                tmem_st16(tmem + L::d_at(buf) + group * (32 + L::kGap) + h / 2 + lanes, pk);
+            }
+            tmem_wait_st();
+            tcgen05_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.d_full[buf]);
+        }
+        if (ok) ok = mbar_wait_tight(&bars.done[(n - 1) & 1], ((n - 1) / 2) & 1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok) {
+            tcgen05_after_sync();
+            const uint32_t acc = tmem + L::sums + lanes;
+            const int wide = (p.D + 15) / 16 * 16;
+            const int64_t row = (int64_t)tile * 128 + line;
+            if (p.slices == 1 && p.first && p.last)
+                store_rows<DT>(p.out, row * p.D, acc, wide, group, row < (ITEMS ? p.v1 - p.v0 : p.N), p.D, p.D % 8 == 0,
+                               1.f / __ldg(p.range));
+            else
+                add_slab(p.part + ((int64_t)slice * p.tiles + tile) * p.cols4 * 128 + line, acc, wide, group, p.first);
+        }
+    }
+    if (!ok) atomicOr(p.error, ERR_TIMEOUT);
+    tcgen05_before_sync();
+    __syncthreads();
+    tcgen05_after_sync();
+    if (warp == 9) tmem_dealloc(tmem, 512);
+}
+
+template <int OUT>
+__global__ void __launch_bounds__(256) loss_finish_kernel(const LossFinish p) {
+    chain_wait();
+    const int blocks = (p.D + 31) / 32, tile = blockIdx.x / blocks;
+    finish<OUT>(p.part + (int64_t)tile * p.cols4 * 128, (int64_t)p.tiles * p.cols4 * 128, p.slabs, p.out,
+                (int64_t)tile * 128, (int)tmin<int64_t>(128, p.rows - (int64_t)tile * 128), p.D,
+                (int)(blockIdx.x % blocks) * 32, 1.f / __ldg(p.range), threadIdx.x);
+}
+
+template <int DT, int DP>
+cudaError_t configure() {
+    cudaError_t e = cudaFuncSetAttribute(loss_fused_kernel<DT, DP, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         Fused<DP>::bytes);
+    if (e != cudaSuccess) return e;
+    return cudaFuncSetAttribute(loss_fused_kernel<DT, DP, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                Fused<DP>::bytes);
+}
+
+template <int DT, int DP>
+cudaError_t launch(const LossFused& p, const LossFusedMaps& maps, bool items, int grid, cudaStream_t s) {
+    return launch_chained_smem(items ? loss_fused_kernel<DT, DP, true> : loss_fused_kernel<DT, DP, false>, dim3(grid),
+                               dim3(kFusedThreads), Fused<DP>::bytes, s, p, maps);
+}
+
+template <int DT>
+cudaError_t launch_width(const LossFused& p, const LossFusedMaps& maps, bool items, int grid, cudaStream_t s) {
+    if (p.D <= 64) return launch<DT, 64>(p, maps, items, grid, s);
+    if (p.D <= 128) return launch<DT, 128>(p, maps, items, grid, s);
+    if (p.D <= 192) return launch<DT, 192>(p, maps, items, grid, s);
+    return launch<DT, 256>(p, maps, items, grid, s);
+}
+
+}  // namespace
+
+cudaError_t loss_fused_configure() {
+    cudaError_t e = cudaSuccess;
+    if (e == cudaSuccess) e = configure<DT_F16, 64>();
+    if (e == cudaSuccess) e = configure<DT_F16, 128>();
+    if (e == cudaSuccess) e = configure<DT_F16, 192>();
+    if (e == cudaSuccess) e = configure<DT_F16, 256>();
+    if (e == cudaSuccess) e = configure<DT_BF16, 64>();
+    if (e == cudaSuccess) e = configure<DT_BF16, 128>();
+    if (e == cudaSuccess) e = configure<DT_BF16, 192>();
+    if (e == cudaSuccess) e = configure<DT_BF16, 256>();
+    return e;
+}
+
+cudaError_t launch_loss_fused(const LossFused& p, const LossFusedMaps& maps, int dtype, bool items, int grid,
+                              cudaStream_t s) {
+    return dtype == DT_F16 ? launch_width<DT_F16>(p, maps, items, grid, s)
+                           : launch_width<DT_BF16>(p, maps, items, grid, s);
+}
+
+cudaError_t launch_loss_finish(const LossFinish& p, int dtype, cudaStream_t s) {
+    const dim3 grid((unsigned)p.tiles * ((p.D + 31) / 32));
+    return dtype == DT_F32   ? launch_chained(loss_finish_kernel<DT_F32>, grid, dim3(256), s, p)
+           : dtype == DT_F16 ? launch_chained(loss_finish_kernel<DT_F16>, grid, dim3(256), s, p)
+                             : launch_chained(loss_finish_kernel<DT_BF16>, grid, dim3(256), s, p);
+}
+
+}  // namespace tbe

@@ -15,15 +15,6 @@ constexpr int kTerms = P == 3 ? 6 : 1;
 __device__ __forceinline__ int plane_a(int term) { return (0x001012 >> (4 * term)) & 15; }
 __device__ __forceinline__ int plane_b(int term) { return (0x010210 >> (4 * term)) & 15; }
 
-__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap& map, int col, int64_t row, int plane,
-                                         uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
-        "[%5];" ::"r"(dst),
-        "l"(&map), "r"(col), "r"((int)row), "r"(plane), "r"(smem_u32(bar))
-        : "memory");
-}
-
 __device__ __forceinline__ void store_box(const CUtensorMap& map, uint32_t src, int col, int row, int plane) {
     asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(&map),
                  "r"(col), "r"(row), "r"(plane), "r"(src)
@@ -82,20 +73,11 @@ __device__ __forceinline__ Product step_item(const LossStep& p, int i) {
     if (i < p.n_d) return score_tile(p.V, p.D, i % p.row_tiles * 128, p.d0 + (int64_t)(i / p.row_tiles) * 256);
     i -= p.n_d;
     t.kind = i < p.n_fin_w ? ITEM_FIN_W : ITEM_FIN_X;
-    t.row0 = (i < p.n_fin_w ? i : i - p.n_fin_w) * 128;
+    if (i >= p.n_fin_w) i -= p.n_fin_w;
+    const int blocks = (p.D + 31) / 32;
+    t.row0 = i / blocks * 128;
+    t.col0 = i % blocks * 32;
     return t;
-}
-
-// The power of two that fp16's d is multiplied by: it brings the largest finite
-// |coef| into [2^14, 2^15).
-__device__ __forceinline__ float range_scale(const float* gmax, int n, int lane) {
-    float m = 0.f;
-    for (int i = lane; i < n; i += 32) m = fmaxf(m, __ldg(gmax + i));
-#pragma unroll
-    for (int o = 16; o > 0; o /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (!(m > 0.f)) return 1.f;
-    const int e = tmax((int)(__float_as_uint(m) >> 23), 27);  // 27: the scale stays below 2^115
-    return __uint_as_float((uint32_t)(127 + 14 + 127 - e) << 23);
 }
 
 // Warp roles' shared counters: steps through the ring and accumulators used.
@@ -198,16 +180,16 @@ __device__ __forceinline__ void stage_row(unsigned char* staging, int lane, int 
 
 // d of the warp's 32 rows and one of its two slabs of 64 items.
 template <int DT, int P>
-__device__ __forceinline__ void d_slab(float* x, const RowStat& r, float coef, float c2, int64_t item0, int64_t V,
+__device__ __forceinline__ void d_slab(float* x, float minus_lse2, float coef, int target, float c2, int64_t item0, int64_t V,
                                        unsigned char* staging, const CUtensorMap& map, int col, int row, int64_t rows,
                                        int lane) {
 #pragma unroll
     for (int c = 0; c < 64; c += 2) {
-        fma2(x[c], x[c + 1], c2, r.minus_lse2, r.minus_lse2);
+        fma2(x[c], x[c + 1], c2, minus_lse2, minus_lse2);
         x[c] = ex2(x[c]);
         x[c + 1] = ex2(x[c + 1]);
     }
-    const int at = (int)tmin<int64_t>(tmax<int64_t>(r.target - item0, -1), 64);  // (target -1: before any item)
+    const int at = (int)tmin<int64_t>(tmax<int64_t>(target - item0, -1), 64);  // (target -1: before any item)
     if (__any_sync(0xffffffffu, at >= 0 && at < 64)) {
 #pragma unroll
         for (int c = 0; c < 64; ++c)
@@ -241,94 +223,6 @@ __device__ __forceinline__ void d_slab(float* x, const RowStat& r, float coef, f
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0 && row < rows) store_box(map, smem_u32(staging), col, row, plane);
-    }
-}
-
-// The accumulator's 32-column chunks of this warpgroup (every other one) into
-// a slab of partial sums: [columns / 4][128 rows] of float4, so that a warp's
-// 32 rows are 512 consecutive bytes.
-__device__ __forceinline__ void add_slab(float4* to, uint32_t acc, int wide, int group, bool first) {
-    for (int c = group * 32; c < wide; c += 64) {
-        float x[32];
-        tmem_ld32_issue(acc + c, x);
-        float4 old[8];
-        if (!first) {
-#pragma unroll
-            for (int q = 0; q < 8; ++q) old[q] = to[(c / 4 + q) * 128];
-        }
-        tmem_wait_ld(x, 32);
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-            float4 v = make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
-            if (!first) v.x += old[q].x, v.y += old[q].y, v.z += old[q].z, v.w += old[q].w;
-            to[(c / 4 + q) * 128] = v;
-        }
-    }
-}
-
-// The same chunks, times `times`, as columns of the thread's row of a result
-// that starts at element `at` and has `left` columns.
-template <int OUT>
-__device__ __forceinline__ void store_rows(void* out, int64_t at, uint32_t acc, int wide, int group, bool valid,
-                                           int left, bool vec, float times) {
-    vec = vec && (uintptr_t)out % 16 == 0;
-    for (int c = group * 32; c < wide; c += 64) {
-        float x[32];
-        tmem_ld32_issue(acc + c, x);
-        tmem_wait_ld(x, 32);
-        if (!valid) continue;
-#pragma unroll
-        for (int e = 0; e < 32; ++e) x[e] *= times;
-        if (vec) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-                if (c + e >= left) break;
-                if constexpr (OUT == DT_F32) {
-                    float4* to = reinterpret_cast<float4*>(static_cast<float*>(out) + at + c + e);
-                    to[0] = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
-                    to[1] = make_float4(x[e + 4], x[e + 5], x[e + 6], x[e + 7]);
-                } else {
-                    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at + c + e) =
-                        make_uint4(pack2<OUT>(x[e], x[e + 1]), pack2<OUT>(x[e + 2], x[e + 3]),
-                                   pack2<OUT>(x[e + 4], x[e + 5]), pack2<OUT>(x[e + 6], x[e + 7]));
-                }
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-                if (c + e < left) store_elem<OUT>(out, at + c + e, x[e]);
-        }
-    }
-}
-
-// 128 rows of a result: the slabs' sum in order, times `times`, rounded.
-template <int OUT>
-__device__ __forceinline__ void finish(const float4* part, int64_t slab_stride, int slabs, void* out, int64_t row0,
-                                       int rows, int D, float times, int thread, int threads) {
-    const int groups = (D + 3) / 4;
-    const bool vec = D % 4 == 0 && (uintptr_t)out % 16 == 0;
-    for (int x = thread; x < groups * 128; x += threads) {
-        const int r = x % 128, g = x / 128;
-        if (r >= rows) continue;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int s = 0; s < slabs; ++s) {
-            const float4 y = part[s * slab_stride + g * 128 + r];
-            v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
-        }
-        v.x *= times, v.y *= times, v.z *= times, v.w *= times;
-        const int64_t at = (row0 + r) * D + g * 4;
-        if (vec) {
-            if constexpr (OUT == DT_F32)
-                *reinterpret_cast<float4*>(static_cast<float*>(out) + at) = v;
-            else
-                *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + at) =
-                    make_uint2(pack2<OUT>(v.x, v.y), pack2<OUT>(v.z, v.w));
-        } else {
-            const float y[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (g * 4 + e < D) store_elem<OUT>(out, at + e, y[e]);
-        }
     }
 }
 
@@ -390,32 +284,34 @@ __global__ void __launch_bounds__(kLossThreads, 1)
         constexpr int OUT = P == 3 ? DT_F32 : DT;
         unsigned char* staging = smem + kLossStages * kStageBytes + warp * kStagingBytes;
         const int quarter = warp % 4, group = warp / 4;
-        const float up = DT == DT_F16 ? range_scale(p.gmax, p.n_gmax, lane) : 1.f, down = 1.f / up;
+        const float down = 1.f / __ldg(p.range);
         int tile = 0;
         Product t;
         while (next(t)) {
-            if (t.kind == ITEM_FIN_W) {
-                finish<OUT>(p.f_part + (int64_t)(t.row0 / 128) * p.cols4 * 128,
-                            (int64_t)((p.f_items + 127) / 128) * p.cols4 * 128, p.w_slabs, p.gw, p.f0 + t.row0,
-                            tmin(128, p.f_items - t.row0), p.D, down, threadIdx.x, 256);
-                continue;
-            }
-            if (t.kind == ITEM_FIN_X) {
-                finish<OUT>(p.x_part + (int64_t)(t.row0 / 128) * p.cols4 * 128, (int64_t)p.row_tiles * p.cols4 * 128,
-                            p.x_slabs, p.gx, t.row0, (int)tmin<int64_t>(128, p.N - t.row0), p.D, down, threadIdx.x,
-                            256);
+            if (t.kind >= ITEM_FIN_W) {
+                const bool w = t.kind == ITEM_FIN_W;
+                const int tiles = w ? (p.f_items + 127) / 128 : p.row_tiles;
+                finish<OUT>((w ? p.f_part : p.x_part) + (int64_t)(t.row0 / 128) * p.cols4 * 128,
+                            (int64_t)tiles * p.cols4 * 128, w ? p.w_slabs : p.x_slabs, w ? p.gw : p.gx,
+                            (w ? p.f0 : 0) + t.row0, (int)tmin<int64_t>(128, (w ? p.f_items : p.N) - t.row0), p.D,
+                            (int)t.col0, down, threadIdx.x);
                 continue;
             }
             const int buf = tile & 1;
-            RowStat r{};
-            if (t.kind == ITEM_D) r = p.rows[t.row0 + quarter * 32 + lane];
+            float minus_lse2 = 0.f, coef = 0.f;
+            int target = -1;
+            if (t.kind == ITEM_D) {
+                const float* r = p.rows + (int64_t)(t.row0 / 128) * kRowValues + quarter * 32 + lane;
+                minus_lse2 = __ldg(r);
+                coef = __ldg(r + 128);
+                target = __float_as_int(__ldg(r + 256));
+            }
             if (ok) ok = mbar_wait_tight(&bars.acc_full[buf], (tile / 2) & 1);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tcgen05_after_sync();
             const uint32_t acc = tmem + buf * 256 + ((uint32_t)(quarter * 32) << 16);
             if (t.kind == ITEM_D) {
-                const float coef = r.coef * up;
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
                     const int c = group * 128 + s * 64;
@@ -424,7 +320,7 @@ __global__ void __launch_bounds__(kLossThreads, 1)
                     tmem_ld32_issue(acc + c, x);
                     tmem_ld32_issue(acc + c + 32, x + 32);
                     tmem_wait_ld(x, 64);
-                    d_slab<DT, P>(x, r, coef, p.c2, t.col0 + c, p.V, staging, maps.d_out, (int)(t.col0 - p.d0) + c,
+                    d_slab<DT, P>(x, minus_lse2, coef, target, p.c2, t.col0 + c, p.V, staging, maps.d_out, (int)(t.col0 - p.d0) + c,
                                   t.row0 + quarter * 32, p.N, lane);
                 }
             } else if (t.kind == ITEM_GW && p.w_slabs == 1) {
@@ -464,11 +360,15 @@ __global__ void __launch_bounds__(kLossThreads, 1)
     const int n_items = p.row_tiles * p.slices;
     int item = blockIdx.x, at = -1, end_at = 0;
     auto next = [&](Product& t) {
-        if (at < 0) {
+        while (at < 0) {
             if (item >= n_items) return false;
             const int slice = item / p.row_tiles;
             at = (int)((int64_t)p.item_tiles * slice / p.slices);
             end_at = (int)((int64_t)p.item_tiles * (slice + 1) / p.slices);
+            if (at == end_at) {  // (a last span of fewer tiles than slices)
+                at = -1;
+                item += gridDim.x;
+            }
         }
         t = score_tile(p.v1, p.D, item % p.row_tiles * 128, p.v0 + (int64_t)at * 256);
         t.slab = item / p.row_tiles;

@@ -25,6 +25,115 @@
 
 namespace tbe {
 
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap& map, int col, int64_t row, int plane,
+                                         uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];" ::"r"(dst),
+        "l"(&map), "r"(col), "r"((int)row), "r"(plane), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// Eight consecutive elements on a 16-byte boundary.
+template <int OUT>
+__device__ __forceinline__ void store8(void* out, int64_t at, const float* x) {
+    if constexpr (OUT == DT_F32) {
+        float4* to = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
+        to[0] = make_float4(x[0], x[1], x[2], x[3]);
+        to[1] = make_float4(x[4], x[5], x[6], x[7]);
+    } else {
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at) =
+            make_uint4(pack2<OUT>(x[0], x[1]), pack2<OUT>(x[2], x[3]), pack2<OUT>(x[4], x[5]), pack2<OUT>(x[6], x[7]));
+    }
+}
+
+// The accumulator's 32-column chunks of this warpgroup (every other one) into
+// a slab of partial sums: [columns / 4][128 rows] of float4, so that a warp's
+// 32 rows are 512 consecutive bytes.
+__device__ __forceinline__ void add_slab(float4* to, uint32_t acc, int wide, int group, bool first) {
+    for (int c = group * 32; c < wide; c += 64) {
+        float x[32];
+        tmem_ld32_issue(acc + c, x);
+        float4 old[8];
+        if (!first) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) old[q] = to[(c / 4 + q) * 128];
+        }
+        tmem_wait_ld(x, 32);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            float4 v = make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
+            if (!first) v.x += old[q].x, v.y += old[q].y, v.z += old[q].z, v.w += old[q].w;
+            to[(c / 4 + q) * 128] = v;
+        }
+    }
+}
+
+// The same chunks, times `times`, as columns of the thread's row of a result
+// that starts at element `at` and has `left` columns.
+template <int OUT>
+__device__ __forceinline__ void store_rows(void* out, int64_t at, uint32_t acc, int wide, int group, bool valid,
+                                           int left, bool vec, float times) {
+    vec = vec && (uintptr_t)out % 16 == 0;
+    for (int c = group * 32; c < wide; c += 64) {
+        float x[32];
+        tmem_ld32_issue(acc + c, x);
+        tmem_wait_ld(x, 32);
+        if (!valid) continue;
+#pragma unroll
+        for (int e = 0; e < 32; ++e) x[e] *= times;
+        if (vec) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) {
+                if (c + e >= left) break;
+                store8<OUT>(out, at + c + e, x + e);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+                if (c + e < left) store_elem<OUT>(out, at + c + e, x[e]);
+        }
+    }
+}
+
+// 128 rows x 32 columns of a result: the slabs' sum in order, times `times`,
+// rounded; 256 threads.
+template <int OUT>
+__device__ __forceinline__ void finish(const float4* part, int64_t slab_stride, int slabs, void* out, int64_t row0,
+                                       int rows, int D, int col0, float times, int thread) {
+    const int r = thread % 128;
+    float4 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float4* from = part + (col0 / 4 + thread / 128 * 4) * 128 + r;
+#pragma unroll 4
+    for (int s = 0; s < slabs; ++s)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float4 y = from[s * slab_stride + i * 128];
+            v[i].x += y.x, v[i].y += y.y, v[i].z += y.z, v[i].w += y.w;
+        }
+    if (r >= rows) return;
+    const int col = col0 + thread / 128 * 16;
+    const int64_t at = (row0 + r) * D + col;
+    const bool vec = D % 8 == 0 && (uintptr_t)out % 16 == 0;
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+        float x[8] = {v[i].x,     v[i].y,     v[i].z,     v[i].w,
+                      v[i + 1].x, v[i + 1].y, v[i + 1].z, v[i + 1].w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] *= times;
+        if (vec) {
+            if (col + i * 4 >= D) break;
+            store8<OUT>(out, at + i * 4, x);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (col + i * 4 + e < D) store_elem<OUT>(out, at + i * 4 + e, x[e]);
+        }
+    }
+}
+
 constexpr int kLossThreads = 320;
 constexpr int kLossStages = 4;
 constexpr int kBox = 64 * 64 * 2;  // bytes of a TMA box: 64 columns x 64 rows
@@ -34,13 +143,10 @@ constexpr int kLossSmem = kLossStages * kStageBytes + 8 * kStagingBytes + 1024;
 
 enum : int32_t { ITEM_GW = 0, ITEM_GX = 1, ITEM_D = 2, ITEM_FIN_W = 3, ITEM_FIN_X = 4 };
 
-// What a row brings into the backward pass.
-struct RowStat {
-    float minus_lse2;  // -lse log2(e); 0 in rows left out
-    float coef;        // g * scale; 0 in rows left out
-    int32_t target;    // -1 in rows left out
-    int32_t pad;
-};
+// What the rows bring into the backward pass: per tile of 128 rows 128 values
+// each of -lse log2(e), of g * scale (times a power of two with fp16) and of the
+// target as an int32; 0, 0 and -1 in rows that are left out or behind the last.
+constexpr int kRowValues = 3 * 128;
 
 struct LossForward {
     int64_t N, v0, v1;  // rows; the items of this launch
@@ -62,9 +168,8 @@ struct LossStep {
     int64_t N, V;
     int32_t D, row_tiles, col_tiles;  // col_tiles: of 256 columns
     float c2;
-    const RowStat* rows;
-    const float* gmax;  // fp16: partial maxima of |coef|
-    int32_t n_gmax;
+    const float* rows;   // [row_tiles][kRowValues]
+    const float* range;  // the power of two in the rows' second values
     // d of the items from d0 on
     int32_t n_d;
     int64_t d0, dw0;  // dw0, pw0: the items at the first row of the maps w and pw
@@ -91,7 +196,39 @@ struct LossMaps {
     CUtensorMap x, w, pw, d_in, d_out;
 };
 
+// One gradient of 16-bit operands of up to 256 columns, d never leaving the
+// SM: tiles of 128 rows (grad_x) or items (grad_table) by slices of the others.
+struct LossFused {
+    int64_t N, V, v0, v1;  // the call's items and this launch's
+    int64_t w0;            // the item at the table map's first row
+    int32_t D, tiles, others, slices;  // others: tiles along the sum
+    int32_t first, last;   // grad_x over spans of the table: its sums begin, end here
+    float c2;
+    const float *rows, *range;
+    float4* part;  // [slices][tiles][cols4][128]; one slice goes to `out` at once
+    void* out;
+    int32_t cols4;
+    uint32_t* error;
+};
+
+struct LossFusedMaps {
+    CUtensorMap x, w;
+};
+
+// A result's sums of slabs: [slabs][tiles][cols4][128] float4.
+struct LossFinish {
+    const float4* part;
+    const float* range;
+    void* out;
+    int64_t rows;
+    int32_t tiles, slabs, D, cols4;
+};
+
 cudaError_t loss_mma_configure();
+cudaError_t loss_fused_configure();
+cudaError_t launch_loss_fused(const LossFused& p, const LossFusedMaps& maps, int dtype, bool items, int grid,
+                              cudaStream_t s);
+cudaError_t launch_loss_finish(const LossFinish& p, int dtype, cudaStream_t s);
 cudaError_t launch_loss_forward(const LossForward& p, const LossMaps& maps, int dtype, int grid, cudaStream_t s);
 cudaError_t launch_loss_step(const LossStep& p, const LossMaps& maps, int dtype, int grid, cudaStream_t s);
 
