@@ -266,7 +266,7 @@ Plan make_plan(const tbe_softmax_loss* h, int64_t N, int64_t V, bool backward, b
         }
     } else {
         L.rows = take(sizeof(float) * N);                                   // picked
-        L.d = take(sizeof(float2) * 2 * (N + 128 * (int64_t)kMostParts));  // part
+        L.d = take(sizeof(float2) * 4 * (N + 128 * (int64_t)kMostParts));  // part
     }
     L.total = o + 256;
     return L;
@@ -392,7 +392,7 @@ int forward(const tbe_softmax_loss* h, const Plan& L, LossForward p, const void*
         if (e != cudaSuccess) return cuda_fail(e);
     }
     return status(launch_chained(loss_join_kernel, dim3((unsigned)((p.N + 7) / 8)), dim3(256), s,
-                                 (const float2*)p.part, 2 * p.slices, (const float*)p.picked, p.targets, p.index64, p.N,
+                                 (const float2*)p.part, 4 * p.slices, (const float*)p.picked, p.targets, p.index64, p.N,
                                  p.V, loss, lse));
 }
 

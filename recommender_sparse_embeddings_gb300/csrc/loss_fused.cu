@@ -11,8 +11,9 @@
 // 2 N V D for both gradients where d in memory takes three, but no logit's
 // gradient is written or read (6 bytes each, against 4 D operations).
 //
-// Warp 8 fetches, warp 9 issues the products, warps 0 to 7 compute d: a thread
-// has one line of S and half of its columns.  S is double buffered.  Up to 128
+// Warp 16 fetches, warp 17 issues the products, warps 0 to 15 compute d, eight
+// those of the even tiles and eight those of the odd ones: a thread has one line
+// of S and half of its columns.  S is double buffered.  Up to 128
 // columns d has columns of its own beside it, so the next S does not wait for
 // the last product; above, d takes its S's place.
 #include "loss_mma.cuh"
@@ -21,7 +22,7 @@ namespace tbe {
 
 namespace {
 
-constexpr int kFusedThreads = 320;
+constexpr int kFusedThreads = 576;
 
 template <int DP>
 struct Fused {
@@ -38,36 +39,36 @@ struct Fused {
 };
 
 struct FusedBars {
-    uint64_t held, full[6], empty[6], s_full[2], d_full[2], done[2];
+    uint64_t held, full[6], empty[6], s_full[2], d_full[2], done[2], last;
 };
 
-// 64 columns of the thread's line.
+// 32 columns of the thread's line: x = S in, d out.
 template <bool ITEMS>
-__device__ __forceinline__ void gradients(float* x, float c2, float minus_lse2, float coef, int at, int left,
+__device__ __forceinline__ void gradients(float (&x)[32], float c2, float minus_lse2, float coef, int at, int left,
                                           const float* stats, int line) {
     if constexpr (!ITEMS) {
 #pragma unroll
-        for (int c = 0; c < 64; c += 2) {
+        for (int c = 0; c < 32; c += 2) {
             fma2(x[c], x[c + 1], c2, minus_lse2, minus_lse2);
             x[c] = ex2(x[c]);
             x[c + 1] = ex2(x[c + 1]);
         }
-        if (__any_sync(0xffffffffu, at >= 0 && at < 64)) {
+        if (__any_sync(0xffffffffu, at >= 0 && at < 32)) {
 #pragma unroll
-            for (int c = 0; c < 64; ++c)
+            for (int c = 0; c < 32; ++c)
                 if (c == at) x[c] -= 1.f;
         }
-        if (left < 64) {
+        if (left < 32) {
 #pragma unroll
-            for (int c = 0; c < 64; ++c)
+            for (int c = 0; c < 32; ++c)
                 if (c >= left) x[c] = 0.f;
         }
 #pragma unroll
-        for (int c = 0; c < 64; c += 2) mul2(x[c], x[c + 1], coef, coef);
+        for (int c = 0; c < 32; c += 2) mul2(x[c], x[c + 1], coef, coef);
     } else {
         // columns are rows of x: their values lie in shared memory
 #pragma unroll
-        for (int c = 0; c < 64; c += 4) {
+        for (int c = 0; c < 32; c += 4) {
             const float4 l = *reinterpret_cast<const float4*>(stats + c);
             fma2(x[c], x[c + 1], c2, l.x, l.y);
             fma2(x[c + 2], x[c + 3], c2, l.z, l.w);
@@ -75,18 +76,16 @@ __device__ __forceinline__ void gradients(float* x, float c2, float minus_lse2, 
             for (int e = 0; e < 4; ++e) x[c + e] = ex2(x[c + e]);
         }
         const int lane = threadIdx.x % 32;
-        const int first = line - lane;  // the warp's items
-        const int t0 = __float_as_int(stats[256 + lane]) - first, t1 = __float_as_int(stats[288 + lane]) - first;
-        const uint32_t lo = __ballot_sync(0xffffffffu, t0 >= 0 && t0 < 32);
-        const uint32_t hi = __ballot_sync(0xffffffffu, t1 >= 0 && t1 < 32);
-        if (lo | hi) {
+        const int t = __float_as_int(stats[256 + lane]) - (line - lane);  // among the warp's items?
+        const uint32_t hit = __ballot_sync(0xffffffffu, t >= 0 && t < 32);
+        if (hit) {
 #pragma unroll
-            for (int c = 0; c < 64; ++c)
-                if ((c < 32 ? lo : hi) >> (c % 32) & 1)
+            for (int c = 0; c < 32; ++c)
+                if (hit >> c & 1)
                     if (__float_as_int(stats[256 + c]) == line) x[c] -= 1.f;
         }
 #pragma unroll
-        for (int c = 0; c < 64; c += 4) {
+        for (int c = 0; c < 32; c += 4) {
             const float4 g = *reinterpret_cast<const float4*>(stats + 128 + c);
             mul2(x[c], x[c + 1], g.x, g.y);
             mul2(x[c + 2], x[c + 3], g.z, g.w);
@@ -106,6 +105,7 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     if (threadIdx.x == 0) {
         mbar_init(&bars.held, 1);
+        mbar_init(&bars.last, 1);
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&bars.full[i], 1);
             mbar_init(&bars.empty[i], 1);
@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_proxy_async_smem();
     }
-    if (warp == 9) tmem_alloc(&slot, 512);
+    if (warp == 17) tmem_alloc(&slot, 512);
     tcgen05_before_sync();
     __syncthreads();
     tcgen05_after_sync();
@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
     const int n = (int)((int64_t)p.others * (slice + 1) / p.slices) - from;
     bool ok = true;
     if (n == 0) {  // (a last span of fewer tiles than slices)
-    } else if (warp == 8) {
+    } else if (warp == 16) {
         // ---- loader
         const uint32_t base = smem_u32(smem);
         const int64_t item0 = p.v0 - p.w0;
@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
             mbar_wait_tight(&bars.held, 0);
             for (int j = tmax(0, i - kStages); j < i; ++j) mbar_wait_tight(&bars.full[j % kStages], (j / kStages) & 1);
         }
-    } else if (warp == 9) {
+    } else if (warp == 17) {
         // ---- products
         const int ksteps = (p.D + 15) / 16;
         const uint32_t id_s = mma_idesc(DT == DT_BF16, 128, 128);
@@ -219,6 +219,7 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
                                i > 0 || k > 0);
                 mma_commit(&bars.empty[st]);
                 mma_commit(&bars.done[buf]);
+                if (i + 1 == n) mma_commit(&bars.last);
             }
             __syncwarp();
         }
@@ -226,7 +227,7 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
         if (ok) ok = wait(&bars.empty[(n - 1) % kStages], (n - 1) / kStages);
     } else {
         // ---- d, then the sums
-        const int quarter = warp % 4, group = warp / 4, line = quarter * 32 + lane;
+        const int quarter = warp % 4, group = warp / 4 % 2, buf = warp / 8, line = quarter * 32 + lane;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
         float minus_lse2 = 0.f, coef = 0.f;
         int target = -1;
@@ -236,8 +237,7 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
             coef = __ldg(r + 128);
             target = __float_as_int(__ldg(r + 256));
         }
-        for (int i = 0; i < n; ++i) {
-            const int buf = i & 1;
+        for (int i = buf; i < n; i += 2) {
             ok = mbar_wait_tight(&bars.s_full[buf], (i / 2) & 1);
             if (ITEMS && ok) ok = mbar_wait_tight(&bars.full[i % kStages], (i / kStages) & 1);  // the rows' values
             if (!__all_sync(0xffffffffu, ok)) {
@@ -245,19 +245,6 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
                 break;
             }
             tcgen05_after_sync();
-            float x[64];
-            tmem_ld32_issue(tmem + buf * 128 + group * 64 + lanes, x);
-            tmem_ld32_issue(tmem + buf * 128 + group * 64 + 32 + lanes, x + 32);
-            tmem_wait_ld(x, 64);
-            if constexpr (ITEMS) {
-                const float* stats = reinterpret_cast<const float*>(smem + L::stats + i % kStages * L::kStats) + group * 64;
-                gradients<true>(x, p.c2, 0.f, 0.f, 0, 64, stats, (int)(p.v0 + (int64_t)tile * 128) + line);
-            } else {
-                const int64_t item0 = p.v0 + (int64_t)(from + i) * 128 + group * 64;
-                const int at = (int)tmin<int64_t>(tmax<int64_t>(target - item0, -1), 64);
-                const int left = (int)tmin<int64_t>(tmax<int64_t>(p.v1 - item0, 0), 64);
-                gradients<false>(x, p.c2, minus_lse2, coef, at, left, nullptr, 0);
-            }
             if (L::kApart && i >= 2) {  // d's columns are free of the product before last
                 ok = mbar_wait_tight(&bars.done[buf], (i / 2 - 1) & 1);
                 if (!__all_sync(0xffffffffu, ok)) {
@@ -266,11 +253,22 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
                 }
                 tcgen05_after_sync();
             }
+            const float* stats =
+                reinterpret_cast<const float*>(smem + L::stats + i % kStages * L::kStats) + group * 64;
+            const int64_t item0 = p.v0 + (int64_t)(from + i) * 128 + group * 64;
+            const int at = (int)tmin<int64_t>(tmax<int64_t>(target - item0, -1), 64);
+            const int left = (int)tmin<int64_t>(tmax<int64_t>(p.v1 - item0, 0), 64);
 #pragma unroll
             for (int h = 0; h < 64; h += 32) {
+                float x[32];
+                tmem_ld32_issue(tmem + buf * 128 + group * 64 + h + lanes, x);
+                tmem_wait_ld(x, 32);
+                gradients<ITEMS>(x, p.c2, minus_lse2, coef, at - h, left - h, stats + h,
+                                 (int)(p.v0 + (int64_t)tile * 128) + line);
                 uint32_t pk[16];
 #pragma unroll
-                for (int c = 0; c < 16; ++c) pk[c] = pack2<DT>(x[h + 2 * c], x[h + 2 * c + 1]);
+                for (int c = 0; c < 16; ++c) pk[c] = pack2<DT>(x[2 * c], x[2 * c + 1]);
+                // (where d takes its S's place, these columns of it are read)
                 tmem_st16(tmem + L::d_at(buf) + group * (32 + L::kGap) + h / 2 + lanes, pk);
             }
             tmem_wait_st();
@@ -278,7 +276,8 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars.d_full[buf]);
         }
-        if (ok) ok = mbar_wait_tight(&bars.done[(n - 1) & 1], ((n - 1) / 2) & 1);
+        // (a barrier of its own: `done` of the other buffer may be two phases back)
+        if (ok) ok = mbar_wait_tight(&bars.last, 0);
         ok = __all_sync(0xffffffffu, ok);
         if (ok) {
             tcgen05_after_sync();
@@ -286,17 +285,17 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
             const int wide = (p.D + 15) / 16 * 16;
             const int64_t row = (int64_t)tile * 128 + line;
             if (p.slices == 1 && p.first && p.last)
-                store_rows<DT>(p.out, row * p.D, acc, wide, group, row < (ITEMS ? p.v1 - p.v0 : p.N), p.D, p.D % 8 == 0,
+                store_rows<DT, 4>(p.out, row * p.D, acc, wide, warp / 4, row < (ITEMS ? p.v1 - p.v0 : p.N), p.D, p.D % 8 == 0,
                                1.f / __ldg(p.range));
             else
-                add_slab(p.part + ((int64_t)slice * p.tiles + tile) * p.cols4 * 128 + line, acc, wide, group, p.first);
+                add_slab<4>(p.part + ((int64_t)slice * p.tiles + tile) * p.cols4 * 128 + line, acc, wide, warp / 4, p.first);
         }
     }
     if (!ok) atomicOr(p.error, ERR_TIMEOUT);
     tcgen05_before_sync();
     __syncthreads();
     tcgen05_after_sync();
-    if (warp == 9) tmem_dealloc(tmem, 512);
+    if (warp == 17) tmem_dealloc(tmem, 512);
 }
 
 template <int OUT>

@@ -5,6 +5,9 @@ namespace tbe {
 
 namespace {
 
+constexpr int kForwardThreads = 576;
+constexpr float kLazyMax = 8.f;
+
 struct LossBars {
     uint64_t full[kLossStages], empty[kLossStages], acc_full[2], acc_empty[2];
 };
@@ -226,6 +229,7 @@ __device__ __forceinline__ void d_slab(float* x, float minus_lse2, float coef, i
     }
 }
 
+template <int WARP>  // the one that allocates
 __device__ __forceinline__ uint32_t begin(LossBars& bars, uint32_t* slot) {
     if (threadIdx.x == 0) {
         for (int i = 0; i < kLossStages; ++i) {
@@ -239,19 +243,20 @@ __device__ __forceinline__ uint32_t begin(LossBars& bars, uint32_t* slot) {
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_proxy_async_smem();
     }
-    if (threadIdx.x / 32 == 9) tmem_alloc(slot, 512);
+    if (threadIdx.x / 32 == WARP) tmem_alloc(slot, 512);
     tcgen05_before_sync();
     __syncthreads();
     tcgen05_after_sync();
     return *slot;
 }
 
+template <int WARP>
 __device__ __forceinline__ void end(uint32_t tmem, bool ok, uint32_t* error) {
     if (!ok) atomicOr(error, ERR_TIMEOUT);
     tcgen05_before_sync();
     __syncthreads();
     tcgen05_after_sync();
-    if (threadIdx.x / 32 == 9) tmem_dealloc(tmem, 512);
+    if (threadIdx.x / 32 == WARP) tmem_dealloc(tmem, 512);
 }
 
 // Backward pass: one launch's work items.
@@ -262,7 +267,7 @@ __global__ void __launch_bounds__(kLossThreads, 1)
     unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     __shared__ LossBars bars;
     __shared__ uint32_t slot;
-    const uint32_t tmem = begin(bars, &slot);
+    const uint32_t tmem = begin<9>(bars, &slot);
     chain_wait();
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int n_items = p.n_gw + p.n_gx + p.n_d + p.n_fin_w + p.n_fin_x;
@@ -325,14 +330,14 @@ __global__ void __launch_bounds__(kLossThreads, 1)
                 }
             } else if (t.kind == ITEM_GW && p.w_slabs == 1) {
                 const int r = t.row0 + quarter * 32 + lane;
-                store_rows<OUT>(p.gw, (p.p0 + r) * p.D + t.col0, acc, t.wide, group, r < p.p_items,
+                store_rows<OUT, 2>(p.gw, (p.p0 + r) * p.D + t.col0, acc, t.wide, group, r < p.p_items,
                                 (int)(p.D - t.col0), p.D % 8 == 0, down);
             } else {
                 const int tiles = t.kind == ITEM_GX ? p.row_tiles : (p.p_items + 127) / 128;
                 float4* to = (t.kind == ITEM_GX ? p.x_part : p.w_part) +
                              ((int64_t)t.slab * tiles + t.row0 / 128) * p.cols4 * 128 + t.col0 / 4 * 128 +
                              quarter * 32 + lane;
-                add_slab(to, acc, t.wide, group, t.kind == ITEM_GW || p.first);
+                add_slab<2>(to, acc, t.wide, group, t.kind == ITEM_GW || p.first);
             }
             tcgen05_before_sync();
             __syncwarp();
@@ -341,20 +346,22 @@ __global__ void __launch_bounds__(kLossThreads, 1)
         }
         if (lane == 0) store_wait();
     }
-    end(tmem, ok, p.error);
+    end<9>(tmem, ok, p.error);
 }
 
 // Forward pass: a CTA's item is a tile of 128 rows and a slice of the table,
-// whose maximum and sum its threads (a row and half of a tile's columns each)
-// carry in registers.
+// whose maximum and sum its threads (a row and half of every other tile's
+// columns each) carry in registers: eight warps take the even tiles' scores,
+// eight the odd ones'.  The running maximum moves only when a logit exceeds it
+// by 2^8 (terms below 2^8 lose nothing in an fp32 sum).
 template <int DT, int P>
-__global__ void __launch_bounds__(kLossThreads, 1)
+__global__ void __launch_bounds__(kForwardThreads, 1)
     loss_forward_kernel(const LossForward p, const __grid_constant__ LossMaps maps) {
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     __shared__ LossBars bars;
     __shared__ uint32_t slot;
-    const uint32_t tmem = begin(bars, &slot);
+    const uint32_t tmem = begin<17>(bars, &slot);
     chain_wait();
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int n_items = p.row_tiles * p.slices;
@@ -380,19 +387,18 @@ __global__ void __launch_bounds__(kLossThreads, 1)
         return true;
     };
     bool ok = true;
-    if (warp == 8) {
+    if (warp == 16) {
         ok = produce<P>(smem, bars, maps, p.w0, 0, next);
-    } else if (warp == 9) {
+    } else if (warp == 17) {
         ok = multiply<DT, P>(smem, bars, tmem, next);
     } else {
-        const int quarter = warp % 4, group = warp / 4;
+        const int quarter = warp % 4, group = warp / 4 % 2, buf = warp / 8;
         int tile = 0;
         float m = -INFINITY, l = 0.f, picked = 0.f;
         int64_t target = -1;
         bool begins = true, found = false;
         Product t;
         while (next(t)) {
-            const int buf = tile & 1;
             const int64_t row = t.row0 + quarter * 32 + lane;
             if (begins) {
                 m = -INFINITY;
@@ -401,7 +407,7 @@ __global__ void __launch_bounds__(kLossThreads, 1)
                 target = -1;
                 if (row < p.N) {
                     if (!p.first) {
-                        const float2 y = p.part[row * 2 * p.slices + t.slab * 2 + group];
+                        const float2 y = p.part[(row * p.slices + t.slab) * 4 + warp / 4];
                         m = y.x;
                         l = y.y;
                     }
@@ -414,58 +420,62 @@ __global__ void __launch_bounds__(kLossThreads, 1)
                 }
             }
             begins = at < 0;  // the next tile begins an item
-            if (ok) ok = mbar_wait_tight(&bars.acc_full[buf], (tile / 2) & 1);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            tcgen05_after_sync();
-            const uint32_t acc = tmem + buf * 256 + group * 128 + ((uint32_t)(quarter * 32) << 16);
-            const int64_t item0 = t.col0 + group * 128;
-            const int left = (int)tmin<int64_t>(128, p.v1 - item0);  // items of this half
-            const int mine = (int)tmin<int64_t>(tmax<int64_t>(target - item0, -1), 128);
+            if ((tile & 1) == buf) {
+                ok = mbar_wait_tight(&bars.acc_full[buf], (tile / 2) & 1);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tcgen05_after_sync();
+                const uint32_t acc = tmem + buf * 256 + group * 128 + ((uint32_t)(quarter * 32) << 16);
+                const int64_t item0 = t.col0 + group * 128;
+                const int left = (int)tmin<int64_t>(128, p.v1 - item0);  // items of this half
+                const int mine = (int)tmin<int64_t>(tmax<int64_t>(target - item0, -1), 128);
 #pragma unroll 1
-            for (int c = 0; c < left; c += 32) {
-                float x[32];
-                tmem_ld32_issue(acc + c, x);
-                tmem_wait_ld(x, 32);
-                if (left - c < 32) {
+                for (int c = 0; c < left; c += 32) {
+                    float x[32];
+                    tmem_ld32_issue(acc + c, x);
+                    tmem_wait_ld(x, 32);
+                    if (left - c < 32) {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (e >= left - c) x[e] = -INFINITY;
+                        for (int e = 0; e < 32; ++e)
+                            if (e >= left - c) x[e] = -INFINITY;
+                    }
+                    if (__any_sync(0xffffffffu, mine >= c && mine < c + 32)) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)  // (in C++ it becomes an indexed copy in local memory)
+                            asm("{\n\t.reg .pred q;\n\tsetp.eq.s32 q, %1, 0;\n\t@q mov.f32 %0, %2;\n\t}"
+                                : "+f"(picked)
+                                : "r"(mine - c - e), "f"(x[e]));
+                        found |= mine >= c && mine < c + 32;
+                    }
+                    float u[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) u[e] = fmaxf(max3(x[e], x[e + 8], x[e + 16]), x[e + 24]);
+                    const float top = fmaxf(max3(max3(u[0], u[1], u[2]), u[3], u[4]), max3(u[5], u[6], u[7])) * p.c2;
+                    if (__any_sync(0xffffffffu, top > m + kLazyMax)) {
+                        const float to = fmaxf(m, top);
+                        l *= ex2(m - to);  // (m = -inf: 0)
+                        m = to;
+                    }
+                    float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        fma2(x[e], x[e + 1], p.c2, -m, -m);
+                        add2(s0, s1, ex2(x[e]), ex2(x[e + 1]));
+                    }
+                    l += s0 + s1;
                 }
-                if (__any_sync(0xffffffffu, mine >= c && mine < c + 32)) {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)  // (in C++ it becomes an indexed copy in local memory)
-                        asm("{\n\t.reg .pred q;\n\tsetp.eq.s32 q, %1, 0;\n\t@q mov.f32 %0, %2;\n\t}"
-                            : "+f"(picked)
-                            : "r"(mine - c - e), "f"(x[e]));
-                    found |= mine >= c && mine < c + 32;
-                }
-                float u[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) u[e] = fmaxf(max3(x[e], x[e + 8], x[e + 16]), x[e + 24]);
-                const float top = fmaxf(max3(max3(u[0], u[1], u[2]), u[3], u[4]), max3(u[5], u[6], u[7])) * p.c2;
-                const float to = fmaxf(m, top);
-                l *= ex2(m - to);  // (m = -inf: 0)
-                m = to;
-                float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                    fma2(x[e], x[e + 1], p.c2, -to, -to);
-                    add2(s0, s1, ex2(x[e]), ex2(x[e + 1]));
-                }
-                l += s0 + s1;
+                tcgen05_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars.acc_empty[buf]);
             }
-            tcgen05_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars.acc_empty[buf]);
             ++tile;
             if (begins && row < p.N) {
-                p.part[row * 2 * p.slices + t.slab * 2 + group] = make_float2(m, l);
+                p.part[(row * p.slices + t.slab) * 4 + warp / 4] = make_float2(m, l);
                 if (found) p.picked[row] = picked * p.c2;
             }
         }
     }
-    end(tmem, ok, p.error);
+    end<17>(tmem, ok, p.error);
 }
 
 template <int DT, int P>
@@ -489,7 +499,7 @@ cudaError_t launch_loss_forward(const LossForward& p, const LossMaps& maps, int 
     auto* kernel = dtype == DT_F32   ? loss_forward_kernel<DT_BF16, 3>
                    : dtype == DT_F16 ? loss_forward_kernel<DT_F16, 1>
                                      : loss_forward_kernel<DT_BF16, 1>;
-    return launch_chained_smem(kernel, dim3(grid), dim3(kLossThreads), kLossSmem, s, p, maps);
+    return launch_chained_smem(kernel, dim3(grid), dim3(kForwardThreads), kLossSmem, s, p, maps);
 }
 
 cudaError_t launch_loss_step(const LossStep& p, const LossMaps& maps, int dtype, int grid, cudaStream_t s) {

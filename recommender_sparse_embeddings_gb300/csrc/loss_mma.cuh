@@ -47,11 +47,12 @@ __device__ __forceinline__ void store8(void* out, int64_t at, const float* x) {
     }
 }
 
-// The accumulator's 32-column chunks of this warpgroup (every other one) into
+// The accumulator's 32-column chunks of this warpgroup (one of GROUPS) into
 // a slab of partial sums: [columns / 4][128 rows] of float4, so that a warp's
 // 32 rows are 512 consecutive bytes.
+template <int GROUPS>
 __device__ __forceinline__ void add_slab(float4* to, uint32_t acc, int wide, int group, bool first) {
-    for (int c = group * 32; c < wide; c += 64) {
+    for (int c = group * 32; c < wide; c += 32 * GROUPS) {
         float x[32];
         tmem_ld32_issue(acc + c, x);
         float4 old[8];
@@ -71,11 +72,11 @@ __device__ __forceinline__ void add_slab(float4* to, uint32_t acc, int wide, int
 
 // The same chunks, times `times`, as columns of the thread's row of a result
 // that starts at element `at` and has `left` columns.
-template <int OUT>
+template <int OUT, int GROUPS>
 __device__ __forceinline__ void store_rows(void* out, int64_t at, uint32_t acc, int wide, int group, bool valid,
                                            int left, bool vec, float times) {
     vec = vec && (uintptr_t)out % 16 == 0;
-    for (int c = group * 32; c < wide; c += 64) {
+    for (int c = group * 32; c < wide; c += 32 * GROUPS) {
         float x[32];
         tmem_ld32_issue(acc + c, x);
         tmem_wait_ld(x, 32);
@@ -157,7 +158,7 @@ struct LossForward {
     const void* targets;
     int32_t index64;
     int64_t V;
-    float2* part;   // [N][2 slices]: maximum and sum (base 2) of a half of a slice's columns
+    float2* part;   // [N][slices][4]: maximum and sum (base 2) of halves of a slice's even and odd tiles
     float* picked;  // [N]: the target's logit (base 2)
     uint32_t* error;
 };

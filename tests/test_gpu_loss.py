@@ -299,8 +299,8 @@ def test_refusals():
         forward()
 
 
-@pytest.mark.parametrize("dtype,n,v,d", [(torch.float32, 70, 30000, 512), (torch.bfloat16, 130, 60000, 136),
-                                         (torch.float16, 40, 9000, 1023)])
+@pytest.mark.parametrize("dtype,n,v,d", [(torch.float32, 70, 30000, 512), (torch.bfloat16, 130, 150000, 136),
+                                         (torch.float16, 20, 40000, 520)])
 def test_tables_copied_in_parts(dtype, n, v, d):
     """fp32 and rows off 16-byte boundaries are copied a part of the table at a time; the last part is a short one."""
     c = Case(dtype, n, v, d, seed=3, table_pad=1)
