@@ -421,7 +421,8 @@ int backward_fused(const tbe_softmax_loss* h, const Plan& L, LossFused p, const 
     if (!encode(&maps.x, dt, base + L.x, p.D, p.N, 1, L.pitch, 64)) return TBE_ERR_CUDA;
     Table w{h, table, table_stride, p.V, L.span, 1, L.pitch, direct(h, table, table_stride, p.V), base + L.w, L.w_bytes};
     const int64_t whole = w.is_direct ? p.V : std::min(p.V, L.span);
-    const int x_slices = choose_slices(L.row_tiles, (whole + 127) / 128, h->num_sms);
+    const int walked = loss_fused_walk(p.D);  // lines of a tile along the sum
+    const int x_slices = choose_slices(L.row_tiles, (whole + walked - 1) / walked, h->num_sms);
     for (p.v0 = 0; p.v0 < p.V; p.v0 = p.v1) {
         p.v1 = std::min(p.V, p.v0 + whole);
         p.w0 = w.first(p.v0);
@@ -432,7 +433,7 @@ int backward_fused(const tbe_softmax_loss* h, const Plan& L, LossFused p, const 
         if (gx) {
             LossFused q = p;
             q.tiles = (int)L.row_tiles;
-            q.others = (int)item_tiles;
+            q.others = (int)((p.v1 - p.v0 + walked - 1) / walked);
             q.slices = x_slices;
             q.first = p.v0 == 0;
             q.last = p.v1 == p.V;
@@ -446,8 +447,8 @@ int backward_fused(const tbe_softmax_loss* h, const Plan& L, LossFused p, const 
         if (gw) {
             LossFused q = p;
             q.tiles = (int)item_tiles;
-            q.others = (int)L.row_tiles;
-            q.slices = choose_slices(item_tiles, L.row_tiles, h->num_sms);
+            q.others = (int)((p.N + walked - 1) / walked);
+            q.slices = choose_slices(item_tiles, q.others, h->num_sms);
             q.first = q.last = 1;
             q.part = at<float4>(base, L.w_part);
             q.out = static_cast<char*>(gw) + p.v0 * p.D * 2;

@@ -2,7 +2,9 @@
 // logits' gradients d never leave the SM.
 //
 // A CTA holds 128 rows (grad_x) or 128 items (grad_table) in shared memory and
-// walks the tiles of 128 of the others:
+// walks tiles of the others, 128 at a time or, above 128 columns, 64 (shared
+// memory holds four of those, but two of 128: the products then waited for
+// each tile's fetch, 4150 cycles per 128 of them at 256 columns):
 //   grad_x:      S = X W^T,  d = coef (2^(S c - lse) - [target]),  dX += d W
 //   grad_table:  S = W X^T,  d likewise, transposed,               dW += d X
 // S (fp32) and d (16-bit, the second product's first operand) live in tensor
@@ -13,9 +15,8 @@
 //
 // Warp 16 fetches, warp 17 issues the products, warps 0 to 15 compute d, eight
 // those of the even tiles and eight those of the odd ones: a thread has one line
-// of S and half of its columns.  S is double buffered.  Up to 128
-// columns d has columns of its own beside it, so the next S does not wait for
-// the last product; above, d takes its S's place.
+// of S and half of its columns.  S and d are double buffered beside each other:
+// the scores after next are computed as soon as these are read.
 #include "loss_mma.cuh"
 
 namespace tbe {
@@ -26,24 +27,22 @@ constexpr int kFusedThreads = 576;
 
 template <int DP>
 struct Fused {
-    static constexpr int kTile = 128 * DP * 2;
-    static constexpr int kStages = DP == 64 ? 6 : DP == 128 ? 4 : DP == 192 ? 3 : 2;
-    static constexpr int kStats = kRowValues * 4;  // bytes of a tile's rows' values
-    static constexpr int ring = kTile, stats = ring + kStages * kTile;
+    static constexpr int BN = loss_fused_walk(DP);  // lines of a walked tile
+    static constexpr int kHeld = 128 * DP * 2, kTile = BN * DP * 2;
+    static constexpr int kStages = DP == 64 ? 6 : DP == 128 ? 5 : DP == 192 ? 5 : 4;
+    static constexpr int kStats = 3 * BN * 4;  // bytes of a tile's rows' values
+    static constexpr int ring = kHeld, stats = ring + kStages * kTile;
     static constexpr int bytes = stats + kStages * kStats + 1024;
-    static constexpr bool kApart = DP <= 128;  // d beside S
-    // tensor memory: S at 0 and 128, d in its place or at 256 and 320, the sums behind
-    static constexpr int sums = kApart ? 384 : 256;
-    static constexpr int d_at(int buf) { return kApart ? 256 + buf * 64 : buf * 128; }
-    static constexpr int kGap = kApart ? 0 : 32;  // columns between d's halves
+    // tensor memory: two S, two d (16-bit), the sums
+    static constexpr int d = 2 * BN, sums = BN == 128 ? 384 : 256;
 };
 
 struct FusedBars {
-    uint64_t held, full[6], empty[6], s_full[2], d_full[2], done[2], last;
+    uint64_t held, full[6], empty[6], s_full[2], s_read[2], d_full[2], done[2], last;
 };
 
 // 32 columns of the thread's line: x = S in, d out.
-template <bool ITEMS>
+template <bool ITEMS, int BN>
 __device__ __forceinline__ void gradients(float (&x)[32], float c2, float minus_lse2, float coef, int at, int left,
                                           const float* stats, int line) {
     if constexpr (!ITEMS) {
@@ -76,17 +75,17 @@ __device__ __forceinline__ void gradients(float (&x)[32], float c2, float minus_
             for (int e = 0; e < 4; ++e) x[c + e] = ex2(x[c + e]);
         }
         const int lane = threadIdx.x % 32;
-        const int t = __float_as_int(stats[256 + lane]) - (line - lane);  // among the warp's items?
+        const int t = __float_as_int(stats[2 * BN + lane]) - (line - lane);  // among the warp's items?
         const uint32_t hit = __ballot_sync(0xffffffffu, t >= 0 && t < 32);
         if (hit) {
 #pragma unroll
             for (int c = 0; c < 32; ++c)
                 if (hit >> c & 1)
-                    if (__float_as_int(stats[256 + c]) == line) x[c] -= 1.f;
+                    if (__float_as_int(stats[2 * BN + c]) == line) x[c] -= 1.f;
         }
 #pragma unroll
         for (int c = 0; c < 32; c += 4) {
-            const float4 g = *reinterpret_cast<const float4*>(stats + 128 + c);
+            const float4 g = *reinterpret_cast<const float4*>(stats + BN + c);
             mul2(x[c], x[c + 1], g.x, g.y);
             mul2(x[c + 2], x[c + 3], g.z, g.w);
         }
@@ -97,7 +96,7 @@ template <int DT, int DP, bool ITEMS>
 __global__ void __launch_bounds__(kFusedThreads, 1)
     loss_fused_kernel(const LossFused p, const __grid_constant__ LossFusedMaps maps) {
     using L = Fused<DP>;
-    constexpr int kStages = L::kStages;
+    constexpr int kStages = L::kStages, BN = L::BN;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     __shared__ FusedBars bars;
@@ -112,6 +111,7 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars.s_full[i], 1);
+            mbar_init(&bars.s_read[i], 8);
             mbar_init(&bars.d_full[i], 8);
             mbar_init(&bars.done[i], 1);
         }
@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
     const uint32_t tmem = slot;
     chain_wait();
 
-    // the CTA's tile and the tiles [from, to) that it walks
+    // the CTA's tile and the n tiles from `from` on that it walks
     const int tile = blockIdx.x % p.tiles, slice = blockIdx.x / p.tiles;
     const int from = (int)((int64_t)p.others * slice / p.slices);
     const int n = (int)((int64_t)p.others * (slice + 1) / p.slices) - from;
@@ -135,16 +135,16 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
         // ---- loader
         const uint32_t base = smem_u32(smem);
         const int64_t item0 = p.v0 - p.w0;
-        auto load = [&](uint32_t dst, const CUtensorMap& map, int64_t row, uint64_t* bar) {
+        auto load = [&](uint32_t dst, const CUtensorMap& map, int64_t row, int boxes, uint64_t* bar) {
 #pragma unroll
             for (int c = 0; c < DP / 64; ++c)
 #pragma unroll
-                for (int r = 0; r < 2; ++r)
-                    load_box(dst + c * (2 * kBox) + r * kBox, map, c * 64, row + r * 64, 0, bar);
+                for (int r = 0; r < boxes; ++r)
+                    load_box(dst + (c * boxes + r) * kBox, map, c * 64, row + r * 64, 0, bar);
         };
         if (elect_one()) {
-            mbar_expect_tx(&bars.held, L::kTile);
-            load(base, ITEMS ? maps.w : maps.x, (ITEMS ? item0 : 0) + (int64_t)tile * 128, &bars.held);
+            mbar_expect_tx(&bars.held, L::kHeld);
+            load(base, ITEMS ? maps.w : maps.x, (ITEMS ? item0 : 0) + (int64_t)tile * 128, 2, &bars.held);
         }
         __syncwarp();
         int i = 0;
@@ -154,16 +154,20 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             if (elect_one()) {
-                const int64_t other = from + i;
-                mbar_expect_tx(&bars.full[st], L::kTile + (ITEMS ? L::kStats : 0));
-                load(base + L::ring + st * L::kTile, ITEMS ? maps.x : maps.w, (ITEMS ? 0 : item0) + other * 128,
-                     &bars.full[st]);
-                if constexpr (ITEMS)
-                    asm volatile(
-                        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                            base + L::stats + st * L::kStats),
-                        "l"(p.rows + other * kRowValues), "r"(L::kStats), "r"(smem_u32(&bars.full[st]))
-                        : "memory");
+                const int64_t other = (int64_t)(from + i) * BN;
+                uint64_t* bar = &bars.full[st];
+                mbar_expect_tx(bar, L::kTile + (ITEMS ? L::kStats : 0));
+                load(base + L::ring + st * L::kTile, ITEMS ? maps.x : maps.w, (ITEMS ? 0 : item0) + other, BN / 64, bar);
+                if constexpr (ITEMS) {
+                    const float* r = p.rows + other / 128 * kRowValues + other % 128;
+#pragma unroll
+                    for (int k = 0; k < 3; ++k)
+                        asm volatile(
+                            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+                                "r"(base + L::stats + st * L::kStats + k * BN * 4),
+                            "l"(r + k * 128), "r"(BN * 4), "r"(smem_u32(bar))
+                            : "memory");
+                }
             }
             __syncwarp();
         }
@@ -174,11 +178,11 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
     } else if (warp == 17) {
         // ---- products
         const int ksteps = (p.D + 15) / 16;
-        const uint32_t id_s = mma_idesc(DT == DT_BF16, 128, 128);
+        const uint32_t id_s = mma_idesc(DT == DT_BF16, 128, BN);
         const uint32_t id_o = mma_idesc(DT == DT_BF16, 128, ksteps * 16) | kMnMajorB;
         const uint64_t held = smem_desc_sw128(smem_u32(smem), 1024);
         const uint64_t walk = smem_desc_sw128(smem_u32(smem) + L::ring, 1024);
-        const uint64_t walk_mn = smem_desc_mn(smem_u32(smem) + L::ring, 2 * kBox);
+        const uint64_t walk_mn = smem_desc_mn(smem_u32(smem) + L::ring, BN * 128);
         auto wait = [&](uint64_t* bar, int phase) {
             const bool in = mbar_wait_tight(bar, phase & 1);
             const bool all = __all_sync(0xffffffffu, in);
@@ -193,29 +197,24 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
 #pragma unroll
                 for (int k = 0; k < DP / 16; ++k)
                     if (k < ksteps)
-                        mma_f16(tmem + (i & 1) * 128, held + (k / 4) * (2 * kBox / 16) + (k % 4) * 2,
-                                b + (k / 4) * (2 * kBox / 16) + (k % 4) * 2, id_s, k > 0);
+                        mma_f16(tmem + (i & 1) * BN, held + (k / 4) * (2 * kBox / 16) + (k % 4) * 2,
+                                b + (k / 4) * (BN * 128 / 16) + (k % 4) * 2, id_s, k > 0);
                 mma_commit(&bars.s_full[i & 1]);
             }
             __syncwarp();
             return true;
         };
-        ok = wait(&bars.held, 0) && scores(0);
+        ok = wait(&bars.held, 0) && scores(0) && (n == 1 || scores(1));
         for (int i = 0; i < n && ok; ++i) {
             const int st = i % kStages, buf = i & 1;
-            if (i + 1 < n) {
-                // the next scores' place: read once the last d is there, and free
-                // of that d (where it lies there) once its product is done
-                if (i >= 1 && !L::kApart) ok = wait(&bars.done[buf ^ 1], (i - 1) / 2);
-                ok = ok && scores(i + 1);
-            }
+            if (i + 2 < n) ok = wait(&bars.s_read[buf], i / 2) && scores(i + 2);
             ok = ok && wait(&bars.d_full[buf], i / 2);
             if (!ok) break;
             if (elect_one()) {
                 const uint64_t b = walk_mn + (uint64_t)(st * (L::kTile / 16));
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    mma_f16_ts(tmem + L::sums, tmem + L::d_at(buf) + k * 8 + (k / 4) * L::kGap, b + k * (2048 / 16), id_o,
+                for (int k = 0; k < BN / 16; ++k)
+                    mma_f16_ts(tmem + L::sums, tmem + L::d + buf * (BN / 2) + k * 8, b + k * (2048 / 16), id_o,
                                i > 0 || k > 0);
                 mma_commit(&bars.empty[st]);
                 mma_commit(&bars.done[buf]);
@@ -245,32 +244,33 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
                 break;
             }
             tcgen05_after_sync();
-            if (L::kApart && i >= 2) {  // d's columns are free of the product before last
-                ok = mbar_wait_tight(&bars.done[buf], (i / 2 - 1) & 1);
-                if (!__all_sync(0xffffffffu, ok)) {
-                    ok = false;
-                    break;
-                }
-                tcgen05_after_sync();
-            }
-            const float* stats =
-                reinterpret_cast<const float*>(smem + L::stats + i % kStages * L::kStats) + group * 64;
-            const int64_t item0 = p.v0 + (int64_t)(from + i) * 128 + group * 64;
+            const float* stats = reinterpret_cast<const float*>(smem + L::stats + i % kStages * L::kStats) + group * (BN / 2);
+            const int64_t item0 = p.v0 + (int64_t)(from + i) * BN + group * (BN / 2);
             const int at = (int)tmin<int64_t>(tmax<int64_t>(target - item0, -1), 64);
             const int left = (int)tmin<int64_t>(tmax<int64_t>(p.v1 - item0, 0), 64);
 #pragma unroll
-            for (int h = 0; h < 64; h += 32) {
+            for (int h = 0; h < BN / 2; h += 32) {
                 float x[32];
-                tmem_ld32_issue(tmem + buf * 128 + group * 64 + h + lanes, x);
+                tmem_ld32_issue(tmem + buf * BN + group * (BN / 2) + h + lanes, x);
                 tmem_wait_ld(x, 32);
-                gradients<ITEMS>(x, p.c2, minus_lse2, coef, at - h, left - h, stats + h,
-                                 (int)(p.v0 + (int64_t)tile * 128) + line);
+                if (h + 32 == BN / 2) {
+                    tcgen05_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars.s_read[buf]);
+                }
+                gradients<ITEMS, BN>(x, p.c2, minus_lse2, coef, at - h, left - h, stats + h,
+                                     (int)(p.v0 + (int64_t)tile * 128) + line);
                 uint32_t pk[16];
 #pragma unroll
                 for (int c = 0; c < 16; ++c) pk[c] = pack2<DT>(x[2 * c], x[2 * c + 1]);
-                // (where d takes its S's place, these columns of it are read)
-                tmem_st16(tmem + L::d_at(buf) + group * (32 + L::kGap) + h / 2 + lanes, pk);
+                if (h == 0 && i >= 2) {  // d's columns are free of the product before last
+                    ok = mbar_wait_tight(&bars.done[buf], (i / 2 - 1) & 1);
+                    ok = __all_sync(0xffffffffu, ok);
+                    tcgen05_after_sync();
+                }
+                tmem_st16(tmem + L::d + buf * (BN / 2) + group * (BN / 4) + h / 2 + lanes, pk);
             }
+            if (!ok) break;
             tmem_wait_st();
             tcgen05_before_sync();
             __syncwarp();

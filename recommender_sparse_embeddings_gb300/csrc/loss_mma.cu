@@ -365,25 +365,20 @@ __global__ void __launch_bounds__(kForwardThreads, 1)
     chain_wait();
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int n_items = p.row_tiles * p.slices;
-    int item = blockIdx.x, at = -1, end_at = 0;
+    int item = blockIdx.x, tiles = 0;  // tiles: left of the item
+    // (called with the same t: all but an item's first tile only move it on)
     auto next = [&](Product& t) {
-        while (at < 0) {
+        while (tiles == 0) {
             if (item >= n_items) return false;
             const int slice = item / p.row_tiles;
-            at = (int)((int64_t)p.item_tiles * slice / p.slices);
-            end_at = (int)((int64_t)p.item_tiles * (slice + 1) / p.slices);
-            if (at == end_at) {  // (a last span of fewer tiles than slices)
-                at = -1;
-                item += gridDim.x;
-            }
-        }
-        t = score_tile(p.v1, p.D, item % p.row_tiles * 128, p.v0 + (int64_t)at * 256);
-        t.slab = item / p.row_tiles;
-        t.k0 = 0;
-        if (++at == end_at) {
-            at = -1;
+            const int at = (int)((int64_t)p.item_tiles * slice / p.slices);
+            tiles = (int)((int64_t)p.item_tiles * (slice + 1) / p.slices) - at;  // (none: a short last span's)
+            t = score_tile(p.v1, p.D, item % p.row_tiles * 128, p.v0 + (int64_t)(at - 1) * 256);
+            t.slab = slice;
             item += gridDim.x;
         }
+        t.col0 += 256;
+        t.wide = --tiles == 0 ? columns_of(p.v1 - t.col0) : 256;
         return true;
     };
     bool ok = true;
@@ -419,7 +414,7 @@ __global__ void __launch_bounds__(kForwardThreads, 1)
                     }
                 }
             }
-            begins = at < 0;  // the next tile begins an item
+            begins = tiles == 0;  // the next tile begins an item
             if ((tile & 1) == buf) {
                 ok = mbar_wait_tight(&bars.acc_full[buf], (tile / 2) & 1);
                 ok = __all_sync(0xffffffffu, ok);

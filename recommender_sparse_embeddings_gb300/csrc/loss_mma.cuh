@@ -227,6 +227,7 @@ struct LossFinish {
 
 cudaError_t loss_mma_configure();
 cudaError_t loss_fused_configure();
+constexpr int loss_fused_walk(int D) { return D <= 128 ? 128 : 64; }
 cudaError_t launch_loss_fused(const LossFused& p, const LossFusedMaps& maps, int dtype, bool items, int grid,
                               cudaStream_t s);
 cudaError_t launch_loss_finish(const LossFinish& p, int dtype, cudaStream_t s);
