@@ -13,7 +13,9 @@
 // 2 N V D for both gradients where d in memory takes three, but no logit's
 // gradient is written or read (6 bytes each, against 4 D operations).
 //
-// Warp 16 fetches, warp 17 issues the products, warps 0 to 15 compute d, eight
+// Warp 16 fetches, warp 17 issues the scores' products and warp 18 the sums'
+// (one warp's waits for the two left the tensor unit idle: it holds about four
+// instructions, a wait takes 100 cycles or more), warps 0 to 15 compute d, eight
 // those of the even tiles and eight those of the odd ones: a thread has one line
 // of S and half of its columns.  S and d are double buffered beside each other:
 // the scores after next are computed as soon as these are read.
@@ -23,7 +25,7 @@ namespace tbe {
 
 namespace {
 
-constexpr int kFusedThreads = 576;
+constexpr int kFusedThreads = 608;
 
 template <int DP>
 struct Fused {
@@ -175,55 +177,58 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
             mbar_wait_tight(&bars.held, 0);
             for (int j = tmax(0, i - kStages); j < i; ++j) mbar_wait_tight(&bars.full[j % kStages], (j / kStages) & 1);
         }
-    } else if (warp == 17) {
+    } else if (warp == 17 || warp == 18) {
         // ---- products
         const int ksteps = (p.D + 15) / 16;
-        const uint32_t id_s = mma_idesc(DT == DT_BF16, 128, BN);
-        const uint32_t id_o = mma_idesc(DT == DT_BF16, 128, ksteps * 16) | kMnMajorB;
-        const uint64_t held = smem_desc_sw128(smem_u32(smem), 1024);
-        const uint64_t walk = smem_desc_sw128(smem_u32(smem) + L::ring, 1024);
-        const uint64_t walk_mn = smem_desc_mn(smem_u32(smem) + L::ring, BN * 128);
         auto wait = [&](uint64_t* bar, int phase) {
             const bool in = mbar_wait_tight(bar, phase & 1);
             const bool all = __all_sync(0xffffffffu, in);
             tcgen05_after_sync();
             return all;
         };
-        auto scores = [&](int i) {
-            const int st = i % kStages;
-            if (!wait(&bars.full[st], i / kStages)) return false;
-            if (elect_one()) {
-                const uint64_t b = walk + (uint64_t)(st * (L::kTile / 16));
+        if (warp == 17) {
+            const uint32_t idesc = mma_idesc(DT == DT_BF16, 128, BN);
+            const uint64_t held = smem_desc_sw128(smem_u32(smem), 1024);
+            const uint64_t walk = smem_desc_sw128(smem_u32(smem) + L::ring, 1024);
+            ok = wait(&bars.held, 0);
+            for (int i = 0; i < n && ok; ++i) {
+                const int st = i % kStages, buf = i & 1;
+                ok = (i < 2 || wait(&bars.s_read[buf], i / 2 - 1)) && wait(&bars.full[st], i / kStages);
+                if (!ok) break;
+                if (elect_one()) {
+                    const uint64_t b = walk + (uint64_t)(st * (L::kTile / 16));
 #pragma unroll
-                for (int k = 0; k < DP / 16; ++k)
-                    if (k < ksteps)
-                        mma_f16(tmem + (i & 1) * BN, held + (k / 4) * (2 * kBox / 16) + (k % 4) * 2,
-                                b + (k / 4) * (BN * 128 / 16) + (k % 4) * 2, id_s, k > 0);
-                mma_commit(&bars.s_full[i & 1]);
+                    for (int k = 0; k < DP / 16; ++k)
+                        if (k < ksteps)
+                            mma_f16(tmem + buf * BN, held + (k / 4) * (2 * kBox / 16) + (k % 4) * 2,
+                                    b + (k / 4) * (BN * 128 / 16) + (k % 4) * 2, idesc, k > 0);
+                    mma_commit(&bars.s_full[buf]);
+                }
+                __syncwarp();
             }
-            __syncwarp();
-            return true;
-        };
-        ok = wait(&bars.held, 0) && scores(0) && (n == 1 || scores(1));
-        for (int i = 0; i < n && ok; ++i) {
-            const int st = i % kStages, buf = i & 1;
-            if (i + 2 < n) ok = wait(&bars.s_read[buf], i / 2) && scores(i + 2);
-            ok = ok && wait(&bars.d_full[buf], i / 2);
-            if (!ok) break;
-            if (elect_one()) {
-                const uint64_t b = walk_mn + (uint64_t)(st * (L::kTile / 16));
+        } else {
+            const uint32_t idesc = mma_idesc(DT == DT_BF16, 128, ksteps * 16) | kMnMajorB;
+            const uint64_t walk = smem_desc_mn(smem_u32(smem) + L::ring, BN * 128);
+            for (int i = 0; i < n && ok; ++i) {
+                const int st = i % kStages, buf = i & 1;
+                ok = wait(&bars.d_full[buf], i / 2);
+                if (!ok) break;
+                if (elect_one()) {
+                    const uint64_t b = walk + (uint64_t)(st * (L::kTile / 16));
 #pragma unroll
-                for (int k = 0; k < BN / 16; ++k)
-                    mma_f16_ts(tmem + L::sums, tmem + L::d + buf * (BN / 2) + k * 8, b + k * (2048 / 16), id_o,
-                               i > 0 || k > 0);
-                mma_commit(&bars.empty[st]);
-                mma_commit(&bars.done[buf]);
-                if (i + 1 == n) mma_commit(&bars.last);
+                    for (int k = 0; k < BN / 16; ++k)
+                        mma_f16_ts(tmem + L::sums, tmem + L::d + buf * (BN / 2) + k * 8, b + k * (2048 / 16), idesc,
+                                   i > 0 || k > 0);
+                    // (the tile's scores are done with it: d was computed from them)
+                    mma_commit(&bars.empty[st]);
+                    mma_commit(&bars.done[buf]);
+                    if (i + 1 == n) mma_commit(&bars.last);
+                }
+                __syncwarp();
             }
-            __syncwarp();
+            // nothing of this CTA arrives on a barrier after its end
+            if (ok) ok = wait(&bars.empty[(n - 1) % kStages], (n - 1) / kStages);
         }
-        // nothing of this CTA arrives on a barrier after its end
-        if (ok) ok = wait(&bars.empty[(n - 1) % kStages], (n - 1) / kStages);
     } else {
         // ---- d, then the sums
         const int quarter = warp % 4, group = warp / 4 % 2, buf = warp / 8, line = quarter * 32 + lane;

@@ -424,22 +424,15 @@ __global__ void __launch_bounds__(kForwardThreads, 1)
                 const int64_t item0 = t.col0 + group * 128;
                 const int left = (int)tmin<int64_t>(128, p.v1 - item0);  // items of this half
                 const int mine = (int)tmin<int64_t>(tmax<int64_t>(target - item0, -1), 128);
-#pragma unroll 1
-                for (int c = 0; c < left; c += 32) {
-                    float x[32];
-                    tmem_ld32_issue(acc + c, x);
-                    tmem_wait_ld(x, 32);
-                    if (left - c < 32) {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (e >= left - c) x[e] = -INFINITY;
-                    }
-                    if (__any_sync(0xffffffffu, mine >= c && mine < c + 32)) {
+                const bool picks = __any_sync(0xffffffffu, mine >= 0 && mine < 128);
+                // 32 columns from c on
+                auto take = [&](float (&x)[32], int c) {
+                    if (picks && __any_sync(0xffffffffu, mine >= c && mine < c + 32)) {
 #pragma unroll
                         for (int e = 0; e < 32; ++e)  // (in C++ it becomes an indexed copy in local memory)
-                            asm("{\n\t.reg .pred q;\n\tsetp.eq.s32 q, %1, 0;\n\t@q mov.f32 %0, %2;\n\t}"
-                                : "+f"(picked)
-                                : "r"(mine - c - e), "f"(x[e]));
+                            asm volatile("{\n\t.reg .pred q;\n\tsetp.eq.s32 q, %1, 0;\n\t@q mov.f32 %0, %2;\n\t}"
+                                         : "+f"(picked)
+                                         : "r"(mine - c - e), "f"(x[e]));
                         found |= mine >= c && mine < c + 32;
                     }
                     float u[8];
@@ -458,6 +451,50 @@ __global__ void __launch_bounds__(kForwardThreads, 1)
                         add2(s0, s1, ex2(x[e]), ex2(x[e + 1]));
                     }
                     l += s0 + s1;
+                };
+                if (left == 128) {
+#if VARIANT == 2
+                    float x[32], y[32];
+                    tmem_ld32_issue(acc, x);
+                    tmem_wait_ld(x, 32);
+                    tmem_ld32_issue(acc + 32, y);
+                    take(x, 0);
+                    tmem_wait_ld(y, 32);
+                    tmem_ld32_issue(acc + 64, x);
+                    take(y, 32);
+                    tmem_wait_ld(x, 32);
+                    tmem_ld32_issue(acc + 96, y);
+                    take(x, 64);
+                    tmem_wait_ld(y, 32);
+                    take(y, 96);
+#elif VARIANT == 3
+#pragma unroll
+                    for (int c = 0; c < 128; c += 32) {
+                        float x[32];
+                        tmem_ld32_issue(acc + c, x);
+                        tmem_wait_ld(x, 32);
+                        take(x, c);
+                    }
+#else
+#pragma unroll 1
+                    for (int c = 0; c < 128; c += 32) {
+                        float x[32];
+                        tmem_ld32_issue(acc + c, x);
+                        tmem_wait_ld(x, 32);
+                        take(x, c);
+                    }
+#endif
+                } else {
+#pragma unroll 1
+                    for (int c = 0; c < left; c += 32) {
+                        float x[32];
+                        tmem_ld32_issue(acc + c, x);
+                        tmem_wait_ld(x, 32);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (e >= left - c) x[e] = -INFINITY;
+                        take(x, c);
+                    }
                 }
                 tcgen05_before_sync();
                 __syncwarp();
