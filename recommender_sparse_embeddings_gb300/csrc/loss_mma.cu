@@ -229,7 +229,7 @@ __device__ __forceinline__ void d_slab(float* x, float minus_lse2, float coef, i
     }
 }
 
-template <int WARP>  // the one that allocates
+template <int WARP, int READERS>  // the warp that allocates; warps that read an accumulator
 __device__ __forceinline__ uint32_t begin(LossBars& bars, uint32_t* slot) {
     if (threadIdx.x == 0) {
         for (int i = 0; i < kLossStages; ++i) {
@@ -238,7 +238,7 @@ __device__ __forceinline__ uint32_t begin(LossBars& bars, uint32_t* slot) {
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars.acc_full[i], 1);
-            mbar_init(&bars.acc_empty[i], 8);
+            mbar_init(&bars.acc_empty[i], READERS);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_proxy_async_smem();
@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(kLossThreads, 1)
     unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     __shared__ LossBars bars;
     __shared__ uint32_t slot;
-    const uint32_t tmem = begin<9>(bars, &slot);
+    const uint32_t tmem = begin<9, 8>(bars, &slot);
     chain_wait();
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int n_items = p.n_gw + p.n_gx + p.n_d + p.n_fin_w + p.n_fin_x;
@@ -350,9 +350,8 @@ __global__ void __launch_bounds__(kLossThreads, 1)
 }
 
 // Forward pass: a CTA's item is a tile of 128 rows and a slice of the table,
-// whose maximum and sum its threads (a row and half of every other tile's
-// columns each) carry in registers: eight warps take the even tiles' scores,
-// eight the odd ones'.  The running maximum moves only when a logit exceeds it
+// whose maximum and sum its threads (a row and a quarter of a tile's columns
+// each) carry in registers.  The running maximum moves only when a logit exceeds it
 // by 2^8 (terms below 2^8 lose nothing in an fp32 sum).
 template <int DT, int P>
 __global__ void __launch_bounds__(kForwardThreads, 1)
@@ -361,7 +360,7 @@ __global__ void __launch_bounds__(kForwardThreads, 1)
     unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     __shared__ LossBars bars;
     __shared__ uint32_t slot;
-    const uint32_t tmem = begin<17>(bars, &slot);
+    const uint32_t tmem = begin<17, 16>(bars, &slot);
     chain_wait();
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int n_items = p.row_tiles * p.slices;
@@ -387,7 +386,7 @@ __global__ void __launch_bounds__(kForwardThreads, 1)
     } else if (warp == 17) {
         ok = multiply<DT, P>(smem, bars, tmem, next);
     } else {
-        const int quarter = warp % 4, group = warp / 4 % 2, buf = warp / 8;
+        const int quarter = warp % 4, group = warp / 4;
         int tile = 0;
         float m = -INFINITY, l = 0.f, picked = 0.f;
         int64_t target = -1;
@@ -402,7 +401,7 @@ __global__ void __launch_bounds__(kForwardThreads, 1)
                 target = -1;
                 if (row < p.N) {
                     if (!p.first) {
-                        const float2 y = p.part[(row * p.slices + t.slab) * 4 + warp / 4];
+                        const float2 y = p.part[(row * p.slices + t.slab) * 4 + group];
                         m = y.x;
                         l = y.y;
                     }
@@ -415,94 +414,72 @@ __global__ void __launch_bounds__(kForwardThreads, 1)
                 }
             }
             begins = tiles == 0;  // the next tile begins an item
-            if ((tile & 1) == buf) {
-                ok = mbar_wait_tight(&bars.acc_full[buf], (tile / 2) & 1);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                tcgen05_after_sync();
-                const uint32_t acc = tmem + buf * 256 + group * 128 + ((uint32_t)(quarter * 32) << 16);
-                const int64_t item0 = t.col0 + group * 128;
-                const int left = (int)tmin<int64_t>(128, p.v1 - item0);  // items of this half
-                const int mine = (int)tmin<int64_t>(tmax<int64_t>(target - item0, -1), 128);
-                const bool picks = __any_sync(0xffffffffu, mine >= 0 && mine < 128);
-                // 32 columns from c on
-                auto take = [&](float (&x)[32], int c) {
-                    if (picks && __any_sync(0xffffffffu, mine >= c && mine < c + 32)) {
+            const int buf = tile & 1;
+            ok = mbar_wait_tight(&bars.acc_full[buf], (tile / 2) & 1);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tcgen05_after_sync();
+            const uint32_t acc = tmem + buf * 256 + group * 64 + ((uint32_t)(quarter * 32) << 16);
+            const int item0 = (int)t.col0 + group * 64;
+            const int left = (int)p.v1 - item0, mine = (int)target - item0;  // (V < 2^31)
+            const bool picks = __any_sync(0xffffffffu, mine >= 0 && mine < 64);
+            // 32 columns from c on
+            auto take = [&](float (&x)[32], int c) {
+                if (picks && __any_sync(0xffffffffu, mine >= c && mine < c + 32)) {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)  // (in C++ it becomes an indexed copy in local memory)
-                            asm volatile("{\n\t.reg .pred q;\n\tsetp.eq.s32 q, %1, 0;\n\t@q mov.f32 %0, %2;\n\t}"
-                                         : "+f"(picked)
-                                         : "r"(mine - c - e), "f"(x[e]));
-                        found |= mine >= c && mine < c + 32;
-                    }
-                    float u[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) u[e] = fmaxf(max3(x[e], x[e + 8], x[e + 16]), x[e + 24]);
-                    const float top = fmaxf(max3(max3(u[0], u[1], u[2]), u[3], u[4]), max3(u[5], u[6], u[7])) * p.c2;
-                    if (__any_sync(0xffffffffu, top > m + kLazyMax)) {
-                        const float to = fmaxf(m, top);
-                        l *= ex2(m - to);  // (m = -inf: 0)
-                        m = to;
-                    }
-                    float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        fma2(x[e], x[e + 1], p.c2, -m, -m);
-                        add2(s0, s1, ex2(x[e]), ex2(x[e + 1]));
-                    }
-                    l += s0 + s1;
-                };
-                if (left == 128) {
-#if VARIANT == 2
-                    float x[32], y[32];
-                    tmem_ld32_issue(acc, x);
-                    tmem_wait_ld(x, 32);
-                    tmem_ld32_issue(acc + 32, y);
-                    take(x, 0);
-                    tmem_wait_ld(y, 32);
-                    tmem_ld32_issue(acc + 64, x);
-                    take(y, 32);
-                    tmem_wait_ld(x, 32);
-                    tmem_ld32_issue(acc + 96, y);
-                    take(x, 64);
-                    tmem_wait_ld(y, 32);
-                    take(y, 96);
-#elif VARIANT == 3
-#pragma unroll
-                    for (int c = 0; c < 128; c += 32) {
-                        float x[32];
-                        tmem_ld32_issue(acc + c, x);
-                        tmem_wait_ld(x, 32);
-                        take(x, c);
-                    }
-#else
-#pragma unroll 1
-                    for (int c = 0; c < 128; c += 32) {
-                        float x[32];
-                        tmem_ld32_issue(acc + c, x);
-                        tmem_wait_ld(x, 32);
-                        take(x, c);
-                    }
-#endif
-                } else {
-#pragma unroll 1
-                    for (int c = 0; c < left; c += 32) {
-                        float x[32];
-                        tmem_ld32_issue(acc + c, x);
-                        tmem_wait_ld(x, 32);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (e >= left - c) x[e] = -INFINITY;
-                        take(x, c);
-                    }
+                    for (int e = 0; e < 32; ++e)  // (in C++ it becomes an indexed copy in local memory)
+                        asm volatile("{\n\t.reg .pred q;\n\tsetp.eq.s32 q, %1, 0;\n\t@q mov.f32 %0, %2;\n\t}"
+                                     : "+f"(picked)
+                                     : "r"(mine - c - e), "f"(x[e]));
+                    found |= mine >= c && mine < c + 32;
                 }
+                float u[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) u[e] = fmaxf(max3(x[e], x[e + 8], x[e + 16]), x[e + 24]);
+                const float top = fmaxf(max3(max3(u[0], u[1], u[2]), u[3], u[4]), max3(u[5], u[6], u[7])) * p.c2;
+                if (__any_sync(0xffffffffu, top > m + kLazyMax)) {
+                    const float to = fmaxf(m, top);
+                    l *= ex2(m - to);  // (m = -inf: 0)
+                    m = to;
+                }
+                float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+                    fma2(x[e], x[e + 1], p.c2, -m, -m);
+                    add2(s0, s1, ex2(x[e]), ex2(x[e + 1]));
+                }
+                l += s0 + s1;
+            };
+            auto release = [&]() {
                 tcgen05_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars.acc_empty[buf]);
+            };
+            if (left >= 64) {
+                float x[32], y[32];
+                tmem_ld32_issue(acc, x);
+                tmem_wait_ld(x, 32);
+                tmem_ld32_issue(acc + 32, y);
+                take(x, 0);
+                tmem_wait_ld(y, 32);
+                release();
+                take(y, 32);
+            } else {
+#pragma unroll 1
+                for (int c = 0; c < left; c += 32) {
+                    float x[32];
+                    tmem_ld32_issue(acc + c, x);
+                    tmem_wait_ld(x, 32);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (e >= left - c) x[e] = -INFINITY;
+                    take(x, c);
+                }
+                release();
             }
             ++tile;
             if (begins && row < p.N) {
-                p.part[(row * p.slices + t.slab) * 4 + warp / 4] = make_float2(m, l);
+                p.part[(row * p.slices + t.slab) * 4 + group] = make_float2(m, l);
                 if (found) p.picked[row] = picked * p.c2;
             }
         }

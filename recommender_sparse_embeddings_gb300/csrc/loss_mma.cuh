@@ -158,7 +158,7 @@ struct LossForward {
     const void* targets;
     int32_t index64;
     int64_t V;
-    float2* part;   // [N][slices][4]: maximum and sum (base 2) of halves of a slice's even and odd tiles
+    float2* part;   // [N][slices][4]: maximum and sum (base 2) of a quarter of a slice's columns
     float* picked;  // [N]: the target's logit (base 2)
     uint32_t* error;
 };
