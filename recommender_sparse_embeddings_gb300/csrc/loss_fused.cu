@@ -241,18 +241,22 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
             coef = __ldg(r + 128);
             target = __float_as_int(__ldg(r + 256));
         }
-        for (int i = buf; i < n; i += 2) {
+        // the first tile's first item of the thread's half (V < 2^31)
+        const int item0 = (int)(p.v0 + (int64_t)(from + buf) * BN) + group * (BN / 2);
+        int left = (int)p.v1 - item0, at = target - item0, st = buf;
+        if (target < 0) at = -1;
+        const int mine = (int)(p.v0 + (int64_t)tile * 128) + line;
+#pragma unroll 1
+        for (int i = buf; i < n; i += 2, left -= 2 * BN, at -= 2 * BN) {
             ok = mbar_wait_tight(&bars.s_full[buf], (i / 2) & 1);
-            if (ITEMS && ok) ok = mbar_wait_tight(&bars.full[i % kStages], (i / kStages) & 1);  // the rows' values
+            if (ITEMS && ok) ok = mbar_wait_tight(&bars.full[st], (i / kStages) & 1);  // the rows' values
             if (!__all_sync(0xffffffffu, ok)) {
                 ok = false;
                 break;
             }
             tcgen05_after_sync();
-            const float* stats = reinterpret_cast<const float*>(smem + L::stats + i % kStages * L::kStats) + group * (BN / 2);
-            const int64_t item0 = p.v0 + (int64_t)(from + i) * BN + group * (BN / 2);
-            const int at = (int)tmin<int64_t>(tmax<int64_t>(target - item0, -1), 64);
-            const int left = (int)tmin<int64_t>(tmax<int64_t>(p.v1 - item0, 0), 64);
+            const float* stats = reinterpret_cast<const float*>(smem + L::stats + st * L::kStats) + group * (BN / 2);
+            st = st + 2 < kStages ? st + 2 : st + 2 - kStages;
 #pragma unroll
             for (int h = 0; h < BN / 2; h += 32) {
                 float x[32];
@@ -263,8 +267,7 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bars.s_read[buf]);
                 }
-                gradients<ITEMS, BN>(x, p.c2, minus_lse2, coef, at - h, left - h, stats + h,
-                                     (int)(p.v0 + (int64_t)tile * 128) + line);
+                gradients<ITEMS, BN>(x, p.c2, minus_lse2, coef, at - h, left - h, stats + h, mine);
                 uint32_t pk[16];
 #pragma unroll
                 for (int c = 0; c < 16; ++c) pk[c] = pack2<DT>(x[2 * c], x[2 * c + 1]);

@@ -386,99 +386,98 @@ __global__ void __launch_bounds__(kForwardThreads, 1)
     } else if (warp == 17) {
         ok = multiply<DT, P>(smem, bars, tmem, next);
     } else {
+        // (an item's tiles in a loop of its own: `next` for each of them took as
+        // long as their arithmetic)
         const int quarter = warp % 4, group = warp / 4;
         int tile = 0;
-        float m = -INFINITY, l = 0.f, picked = 0.f;
-        int64_t target = -1;
-        bool begins = true, found = false;
         Product t;
-        while (next(t)) {
+        while (ok && next(t)) {
+            const int count = tiles + 1;
+            tiles = 0;
             const int64_t row = t.row0 + quarter * 32 + lane;
-            if (begins) {
-                m = -INFINITY;
-                l = 0.f;
-                found = false;
-                target = -1;
-                if (row < p.N) {
-                    if (!p.first) {
-                        const float2 y = p.part[(row * p.slices + t.slab) * 4 + group];
-                        m = y.x;
-                        l = y.y;
-                    }
-                    target = p.index64 ? static_cast<const int64_t*>(p.targets)[row]
-                                       : static_cast<const int32_t*>(p.targets)[row];
-                    if (target >= p.V) {
-                        atomicOr(p.error, ERR_OOB);
-                        target = -1;
-                    }
+            float m = -INFINITY, l = 0.f, picked = 0.f;
+            int left = (int)(p.v1 - t.col0) - group * 64;  // items from the quarter on
+            int mine = -1;                                 // the target's place among them (V < 2^31)
+            bool found = false;
+            if (row < p.N) {
+                if (!p.first) {
+                    const float2 y = p.part[(row * p.slices + t.slab) * 4 + group];
+                    m = y.x;
+                    l = y.y;
                 }
+                const int64_t target = p.index64 ? static_cast<const int64_t*>(p.targets)[row]
+                                                 : static_cast<const int32_t*>(p.targets)[row];
+                if (target >= p.V)
+                    atomicOr(p.error, ERR_OOB);
+                else if (target >= 0)
+                    mine = (int)(target - t.col0) - group * 64;
             }
-            begins = tiles == 0;  // the next tile begins an item
-            const int buf = tile & 1;
-            ok = mbar_wait_tight(&bars.acc_full[buf], (tile / 2) & 1);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            tcgen05_after_sync();
-            const uint32_t acc = tmem + buf * 256 + group * 64 + ((uint32_t)(quarter * 32) << 16);
-            const int item0 = (int)t.col0 + group * 64;
-            const int left = (int)p.v1 - item0, mine = (int)target - item0;  // (V < 2^31)
-            const bool picks = __any_sync(0xffffffffu, mine >= 0 && mine < 64);
-            // 32 columns from c on
-            auto take = [&](float (&x)[32], int c) {
-                if (picks && __any_sync(0xffffffffu, mine >= c && mine < c + 32)) {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)  // (in C++ it becomes an indexed copy in local memory)
-                        asm volatile("{\n\t.reg .pred q;\n\tsetp.eq.s32 q, %1, 0;\n\t@q mov.f32 %0, %2;\n\t}"
-                                     : "+f"(picked)
-                                     : "r"(mine - c - e), "f"(x[e]));
-                    found |= mine >= c && mine < c + 32;
-                }
-                float u[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) u[e] = fmaxf(max3(x[e], x[e + 8], x[e + 16]), x[e + 24]);
-                const float top = fmaxf(max3(max3(u[0], u[1], u[2]), u[3], u[4]), max3(u[5], u[6], u[7])) * p.c2;
-                if (__any_sync(0xffffffffu, top > m + kLazyMax)) {
-                    const float to = fmaxf(m, top);
-                    l *= ex2(m - to);  // (m = -inf: 0)
-                    m = to;
-                }
-                float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                    fma2(x[e], x[e + 1], p.c2, -m, -m);
-                    add2(s0, s1, ex2(x[e]), ex2(x[e + 1]));
-                }
-                l += s0 + s1;
-            };
-            auto release = [&]() {
-                tcgen05_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars.acc_empty[buf]);
-            };
-            if (left >= 64) {
-                float x[32], y[32];
-                tmem_ld32_issue(acc, x);
-                tmem_wait_ld(x, 32);
-                tmem_ld32_issue(acc + 32, y);
-                take(x, 0);
-                tmem_wait_ld(y, 32);
-                release();
-                take(y, 32);
-            } else {
+            const uint32_t acc0 = tmem + group * 64 + ((uint32_t)(quarter * 32) << 16);
 #pragma unroll 1
-                for (int c = 0; c < left; c += 32) {
-                    float x[32];
-                    tmem_ld32_issue(acc + c, x);
-                    tmem_wait_ld(x, 32);
+            for (int j = 0; j < count; ++j, ++tile, left -= 256, mine -= 256) {
+                const int buf = tile & 1;
+                ok = mbar_wait_tight(&bars.acc_full[buf], (tile / 2) & 1);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tcgen05_after_sync();
+                const uint32_t acc = acc0 + buf * 256;
+                const bool picks = __any_sync(0xffffffffu, mine >= 0 && mine < 64);
+                // 32 columns from c on
+                auto take = [&](float (&x)[32], int c) {
+                    if (picks && __any_sync(0xffffffffu, mine >= c && mine < c + 32)) {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (e >= left - c) x[e] = -INFINITY;
-                    take(x, c);
+                        for (int e = 0; e < 32; ++e)  // (in C++ it becomes an indexed copy in local memory)
+                            asm volatile("{\n\t.reg .pred q;\n\tsetp.eq.s32 q, %1, 0;\n\t@q mov.f32 %0, %2;\n\t}"
+                                         : "+f"(picked)
+                                         : "r"(mine - c - e), "f"(x[e]));
+                        found |= mine >= c && mine < c + 32;
+                    }
+                    float u[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) u[e] = fmaxf(max3(x[e], x[e + 8], x[e + 16]), x[e + 24]);
+                    const float top = fmaxf(max3(max3(u[0], u[1], u[2]), u[3], u[4]), max3(u[5], u[6], u[7])) * p.c2;
+                    if (__any_sync(0xffffffffu, top > m + kLazyMax)) {
+                        const float to = fmaxf(m, top);
+                        l *= ex2(m - to);  // (m = -inf: 0)
+                        m = to;
+                    }
+                    float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        fma2(x[e], x[e + 1], p.c2, -m, -m);
+                        add2(s0, s1, ex2(x[e]), ex2(x[e + 1]));
+                    }
+                    l += s0 + s1;
+                };
+                auto release = [&]() {
+                    tcgen05_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars.acc_empty[buf]);
+                };
+                if (left >= 64) {
+                    float x[32], y[32];
+                    tmem_ld32_issue(acc, x);
+                    tmem_wait_ld(x, 32);
+                    tmem_ld32_issue(acc + 32, y);
+                    take(x, 0);
+                    tmem_wait_ld(y, 32);
+                    release();
+                    take(y, 32);
+                } else {
+#pragma unroll 1
+                    for (int c = 0; c < left; c += 32) {
+                        float x[32];
+                        tmem_ld32_issue(acc + c, x);
+                        tmem_wait_ld(x, 32);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (e >= left - c) x[e] = -INFINITY;
+                        take(x, c);
+                    }
+                    release();
                 }
-                release();
             }
-            ++tile;
-            if (begins && row < p.N) {
+            if (ok && row < p.N) {
                 p.part[(row * p.slices + t.slab) * 4 + group] = make_float2(m, l);
                 if (found) p.picked[row] = picked * p.c2;
             }
