@@ -409,6 +409,41 @@ cudaError_t launch_rows(const tbe_softmax_loss* h, const Plan& L, RowsIn rows, c
     return e != cudaSuccess ? e : launch_chained(loss_rows_kernel<DT_F16>, grid, dim3(256), s, rows);
 }
 
+// Slices of the fused launch's sums, x's and w's: those of the least estimated
+// time, in units of one walked tile (0.35 to 0.7 us).  A CTA's start and end take
+// about 4 of them, a slab's way through memory one per 64 columns; more CTAs than
+// SMs share the work evenly but for about half of one at the end.
+void choose_sides(LossSide* x, LossSide* w, int D, int ctas) {
+    static constexpr int kTry[] = {1, 2, 3, 4, 5, 6, 7, 8, 10, 12, 16, 24, 32, 48, 76, 152, 304, 608};
+    double least = 1e300;
+    LossSide a = *x, b = *w;
+    auto cost = [&](const LossSide& s) {
+        return (s.others + s.slices - 1) / s.slices + 4 + (s.slices > 1 ? (D + 63) / 64 : 0);
+    };
+    auto allowed = [](const LossSide& s, int slices) {
+        return slices == 1 || (slices <= s.others && (int64_t)slices * s.tiles <= kMostParts);
+    };
+    for (int i : kTry) {
+        if (x->tiles == 0 ? i > 1 : !allowed(*x, i)) continue;
+        a.slices = i;
+        const int ca = x->tiles ? cost(a) : 0;
+        for (int j : kTry) {
+            if (w->tiles == 0 ? j > 1 : !allowed(*w, j)) continue;
+            b.slices = j;
+            const int cb = w->tiles ? cost(b) : 0;
+            const int64_t na = (int64_t)x->tiles * i, nb = (int64_t)w->tiles * j, n = na + nb;
+            double time = std::max(ca, cb);
+            if (n > ctas)
+                time = std::max(time, ((double)na * ca + (double)nb * cb) / ctas + 0.5 * (nb ? cb : ca));
+            if (time < least) {
+                least = time;
+                x->slices = i;
+                w->slices = j;
+            }
+        }
+    }
+}
+
 int backward_fused(const tbe_softmax_loss* h, const Plan& L, LossFused p, const RowsIn& rows, const void* table,
                    int64_t table_stride, void* gx, void* gw, char* base, cudaStream_t s) {
     const int dt = h->c.dtype;
@@ -422,42 +457,33 @@ int backward_fused(const tbe_softmax_loss* h, const Plan& L, LossFused p, const 
     Table w{h, table, table_stride, p.V, L.span, 1, L.pitch, direct(h, table, table_stride, p.V), base + L.w, L.w_bytes};
     const int64_t whole = w.is_direct ? p.V : std::min(p.V, L.span);
     const int walked = loss_fused_walk(p.D);  // lines of a tile along the sum
-    const int x_slices = choose_slices(L.row_tiles, (whole + walked - 1) / walked, h->num_sms);
+    p.x.tiles = gx ? (int)L.row_tiles : 0;
+    p.x.others = (int)((whole + walked - 1) / walked);
+    p.x.part = at<float4>(base, L.x_part);
+    p.x.out = gx;
+    p.w.others = (int)((p.N + walked - 1) / walked);
+    p.w.part = at<float4>(base, L.w_part);
+    p.w.first = p.w.last = 1;
+    p.w.tiles = gw ? (int)((whole + 127) / 128) : 0;
+    choose_sides(&p.x, &p.w, p.D, h->num_sms);
     for (p.v0 = 0; p.v0 < p.V; p.v0 = p.v1) {
         p.v1 = std::min(p.V, p.v0 + whole);
         p.w0 = w.first(p.v0);
         e = w.fetch(p.v0, s);
         if (e != cudaSuccess) return cuda_fail(e);
         if (!w.map(&maps.w, p.v0)) return TBE_ERR_CUDA;
-        const int64_t item_tiles = (p.v1 - p.v0 + 127) / 128;
-        if (gx) {
-            LossFused q = p;
-            q.tiles = (int)L.row_tiles;
-            q.others = (int)((p.v1 - p.v0 + walked - 1) / walked);
-            q.slices = x_slices;
-            q.first = p.v0 == 0;
-            q.last = p.v1 == p.V;
-            q.part = at<float4>(base, L.x_part);
-            q.out = gx;
-            e = launch_loss_fused(q, maps, dt, false, q.tiles * q.slices, s);
-            if (e == cudaSuccess && q.last && !(q.slices == 1 && q.first))
-                e = launch_loss_finish(LossFinish{q.part, p.range, gx, p.N, q.tiles, q.slices, p.D, L.cols4}, dt, s);
-            if (e != cudaSuccess) return cuda_fail(e);
-        }
-        if (gw) {
-            LossFused q = p;
-            q.tiles = (int)item_tiles;
-            q.others = (int)((p.N + walked - 1) / walked);
-            q.slices = choose_slices(item_tiles, q.others, h->num_sms);
-            q.first = q.last = 1;
-            q.part = at<float4>(base, L.w_part);
-            q.out = static_cast<char*>(gw) + p.v0 * p.D * 2;
-            e = launch_loss_fused(q, maps, dt, true, q.tiles * q.slices, s);
-            if (e == cudaSuccess && q.slices > 1)
-                e = launch_loss_finish(LossFinish{q.part, p.range, q.out, p.v1 - p.v0, q.tiles, q.slices, p.D, L.cols4},
-                                       dt, s);
-            if (e != cudaSuccess) return cuda_fail(e);
-        }
+        p.x.others = (int)((p.v1 - p.v0 + walked - 1) / walked);
+        p.x.first = p.v0 == 0;
+        p.x.last = p.v1 == p.V;
+        p.w.tiles = gw ? (int)((p.v1 - p.v0 + 127) / 128) : 0;
+        p.w.out = gw ? static_cast<char*>(gw) + p.v0 * p.D * 2 : nullptr;
+        e = launch_loss_fused(p, maps, dt, s);
+        if (e != cudaSuccess) return cuda_fail(e);
+        LossFinish f{p.x, p.w, p.N, p.v1 - p.v0, p.range, p.D, L.cols4};
+        if (!(p.x.last && !(p.x.slices == 1 && p.x.first))) f.x.tiles = 0;
+        if (p.w.slices == 1) f.w.tiles = 0;
+        if (f.x.tiles + f.w.tiles > 0) e = launch_loss_finish(f, dt, s);
+        if (e != cudaSuccess) return cuda_fail(e);
     }
     return TBE_OK;
 }

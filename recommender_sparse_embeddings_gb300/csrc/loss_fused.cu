@@ -95,42 +95,15 @@ __device__ __forceinline__ void gradients(float (&x)[32], float c2, float minus_
 }
 
 template <int DT, int DP, bool ITEMS>
-__global__ void __launch_bounds__(kFusedThreads, 1)
-    loss_fused_kernel(const LossFused p, const __grid_constant__ LossFusedMaps maps) {
+__device__ __forceinline__ bool fused_body(const LossFused& p, const LossSide& side, const LossFusedMaps& maps, int cta,
+                                           unsigned char* smem, FusedBars& bars, uint32_t tmem) {
     using L = Fused<DP>;
     constexpr int kStages = L::kStages, BN = L::BN;
-    extern __shared__ unsigned char smem_raw[];
-    unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    __shared__ FusedBars bars;
-    __shared__ uint32_t slot;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    if (threadIdx.x == 0) {
-        mbar_init(&bars.held, 1);
-        mbar_init(&bars.last, 1);
-        for (int i = 0; i < kStages; ++i) {
-            mbar_init(&bars.full[i], 1);
-            mbar_init(&bars.empty[i], 1);
-        }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&bars.s_full[i], 1);
-            mbar_init(&bars.s_read[i], 8);
-            mbar_init(&bars.d_full[i], 8);
-            mbar_init(&bars.done[i], 1);
-        }
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        fence_proxy_async_smem();
-    }
-    if (warp == 17) tmem_alloc(&slot, 512);
-    tcgen05_before_sync();
-    __syncthreads();
-    tcgen05_after_sync();
-    const uint32_t tmem = slot;
-    chain_wait();
-
     // the CTA's tile and the n tiles from `from` on that it walks
-    const int tile = blockIdx.x % p.tiles, slice = blockIdx.x / p.tiles;
-    const int from = (int)((int64_t)p.others * slice / p.slices);
-    const int n = (int)((int64_t)p.others * (slice + 1) / p.slices) - from;
+    const int tile = cta % side.tiles, slice = cta / side.tiles;
+    const int from = (int)((int64_t)side.others * slice / side.slices);
+    const int n = (int)((int64_t)side.others * (slice + 1) / side.slices) - from;
     bool ok = true;
     if (n == 0) {  // (a last span of fewer tiles than slices)
     } else if (warp == 16) {
@@ -292,13 +265,50 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
             const uint32_t acc = tmem + L::sums + lanes;
             const int wide = (p.D + 15) / 16 * 16;
             const int64_t row = (int64_t)tile * 128 + line;
-            if (p.slices == 1 && p.first && p.last)
-                store_rows<DT, 4>(p.out, row * p.D, acc, wide, warp / 4, row < (ITEMS ? p.v1 - p.v0 : p.N), p.D, p.D % 8 == 0,
-                               1.f / __ldg(p.range));
+            if (side.slices == 1 && side.first && side.last)
+                store_rows<DT, 4>(side.out, row * p.D, acc, wide, warp / 4, row < (ITEMS ? p.v1 - p.v0 : p.N), p.D,
+                                  p.D % 8 == 0, 1.f / __ldg(p.range));
             else
-                add_slab<4>(p.part + ((int64_t)slice * p.tiles + tile) * p.cols4 * 128 + line, acc, wide, warp / 4, p.first);
+                add_slab<4>(side.part + ((int64_t)slice * side.tiles + tile) * p.cols4 * 128 + line, acc, wide, warp / 4,
+                            side.first);
         }
     }
+    return ok;
+}
+
+template <int DT, int DP>
+__global__ void __launch_bounds__(kFusedThreads, 1)
+    loss_fused_kernel(const LossFused p, const __grid_constant__ LossFusedMaps maps) {
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    __shared__ FusedBars bars;
+    __shared__ uint32_t slot;
+    const int warp = threadIdx.x / 32;
+    if (threadIdx.x == 0) {
+        mbar_init(&bars.held, 1);
+        mbar_init(&bars.last, 1);
+        for (int i = 0; i < Fused<DP>::kStages; ++i) {
+            mbar_init(&bars.full[i], 1);
+            mbar_init(&bars.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars.s_full[i], 1);
+            mbar_init(&bars.s_read[i], 8);
+            mbar_init(&bars.d_full[i], 8);
+            mbar_init(&bars.done[i], 1);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        fence_proxy_async_smem();
+    }
+    if (warp == 17) tmem_alloc(&slot, 512);
+    tcgen05_before_sync();
+    __syncthreads();
+    tcgen05_after_sync();
+    const uint32_t tmem = slot;
+    chain_wait();
+    const int x_ctas = p.x.tiles * p.x.slices, cta = blockIdx.x;
+    const bool ok = cta < x_ctas ? fused_body<DT, DP, false>(p, p.x, maps, cta, smem, bars, tmem)
+                                 : fused_body<DT, DP, true>(p, p.w, maps, cta - x_ctas, smem, bars, tmem);
     if (!ok) atomicOr(p.error, ERR_TIMEOUT);
     tcgen05_before_sync();
     __syncthreads();
@@ -309,40 +319,39 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
 template <int OUT>
 __global__ void __launch_bounds__(256) loss_finish_kernel(const LossFinish p) {
     chain_wait();
-    const int blocks = (p.D + 31) / 32, tile = blockIdx.x / blocks;
-    finish<OUT>(p.part + (int64_t)tile * p.cols4 * 128, (int64_t)p.tiles * p.cols4 * 128, p.slabs, p.out,
-                (int64_t)tile * 128, (int)tmin<int64_t>(128, p.rows - (int64_t)tile * 128), p.D,
+    const int blocks = (p.D + 31) / 32;
+    int tile = blockIdx.x / blocks;
+    const bool x = tile < p.x.tiles;
+    const LossSide& side = x ? p.x : p.w;
+    if (!x) tile -= p.x.tiles;
+    finish<OUT>(side.part + (int64_t)tile * p.cols4 * 128, (int64_t)side.tiles * p.cols4 * 128, side.slices, side.out,
+                (int64_t)tile * 128, (int)tmin<int64_t>(128, (x ? p.x_rows : p.w_rows) - (int64_t)tile * 128), p.D,
                 (int)(blockIdx.x % blocks) * 32, 1.f / __ldg(p.range), threadIdx.x);
 }
 
 template <int DT, int DP>
 cudaError_t configure() {
-    cudaError_t e = cudaFuncSetAttribute(loss_fused_kernel<DT, DP, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         Fused<DP>::bytes);
-    if (e != cudaSuccess) return e;
-    return cudaFuncSetAttribute(loss_fused_kernel<DT, DP, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                Fused<DP>::bytes);
+    return cudaFuncSetAttribute(loss_fused_kernel<DT, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, Fused<DP>::bytes);
 }
 
 template <int DT, int DP>
-cudaError_t launch(const LossFused& p, const LossFusedMaps& maps, bool items, int grid, cudaStream_t s) {
-    return launch_chained_smem(items ? loss_fused_kernel<DT, DP, true> : loss_fused_kernel<DT, DP, false>, dim3(grid),
-                               dim3(kFusedThreads), Fused<DP>::bytes, s, p, maps);
+cudaError_t launch(const LossFused& p, const LossFusedMaps& maps, cudaStream_t s) {
+    const int grid = p.x.tiles * p.x.slices + p.w.tiles * p.w.slices;
+    return launch_chained_smem(loss_fused_kernel<DT, DP>, dim3(grid), dim3(kFusedThreads), Fused<DP>::bytes, s, p, maps);
 }
 
 template <int DT>
-cudaError_t launch_width(const LossFused& p, const LossFusedMaps& maps, bool items, int grid, cudaStream_t s) {
-    if (p.D <= 64) return launch<DT, 64>(p, maps, items, grid, s);
-    if (p.D <= 128) return launch<DT, 128>(p, maps, items, grid, s);
-    if (p.D <= 192) return launch<DT, 192>(p, maps, items, grid, s);
-    return launch<DT, 256>(p, maps, items, grid, s);
+cudaError_t launch_width(const LossFused& p, const LossFusedMaps& maps, cudaStream_t s) {
+    if (p.D <= 64) return launch<DT, 64>(p, maps, s);
+    if (p.D <= 128) return launch<DT, 128>(p, maps, s);
+    if (p.D <= 192) return launch<DT, 192>(p, maps, s);
+    return launch<DT, 256>(p, maps, s);
 }
 
 }  // namespace
 
 cudaError_t loss_fused_configure() {
-    cudaError_t e = cudaSuccess;
-    if (e == cudaSuccess) e = configure<DT_F16, 64>();
+    cudaError_t e = configure<DT_F16, 64>();
     if (e == cudaSuccess) e = configure<DT_F16, 128>();
     if (e == cudaSuccess) e = configure<DT_F16, 192>();
     if (e == cudaSuccess) e = configure<DT_F16, 256>();
@@ -353,17 +362,14 @@ cudaError_t loss_fused_configure() {
     return e;
 }
 
-cudaError_t launch_loss_fused(const LossFused& p, const LossFusedMaps& maps, int dtype, bool items, int grid,
-                              cudaStream_t s) {
-    return dtype == DT_F16 ? launch_width<DT_F16>(p, maps, items, grid, s)
-                           : launch_width<DT_BF16>(p, maps, items, grid, s);
+cudaError_t launch_loss_fused(const LossFused& p, const LossFusedMaps& maps, int dtype, cudaStream_t s) {
+    return dtype == DT_F16 ? launch_width<DT_F16>(p, maps, s) : launch_width<DT_BF16>(p, maps, s);
 }
 
 cudaError_t launch_loss_finish(const LossFinish& p, int dtype, cudaStream_t s) {
-    const dim3 grid((unsigned)p.tiles * ((p.D + 31) / 32));
-    return dtype == DT_F32   ? launch_chained(loss_finish_kernel<DT_F32>, grid, dim3(256), s, p)
-           : dtype == DT_F16 ? launch_chained(loss_finish_kernel<DT_F16>, grid, dim3(256), s, p)
-                             : launch_chained(loss_finish_kernel<DT_BF16>, grid, dim3(256), s, p);
+    const dim3 grid((unsigned)(p.x.tiles + p.w.tiles) * ((p.D + 31) / 32));
+    return dtype == DT_F16 ? launch_chained(loss_finish_kernel<DT_F16>, grid, dim3(256), s, p)
+                           : launch_chained(loss_finish_kernel<DT_BF16>, grid, dim3(256), s, p);
 }
 
 }  // namespace tbe

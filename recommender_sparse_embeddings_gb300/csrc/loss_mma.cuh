@@ -197,18 +197,24 @@ struct LossMaps {
     CUtensorMap x, w, pw, d_in, d_out;
 };
 
-// One gradient of 16-bit operands of up to 256 columns, d never leaving the
-// SM: tiles of 128 rows (grad_x) or items (grad_table) by slices of the others.
+// The work of one gradient in a fused launch: a CTA for each of `tiles` tiles
+// of 128 lines and each slice of the `others` tiles along the sum.
+struct LossSide {
+    int32_t tiles, others, slices;
+    int32_t first, last;  // over spans of the table: the sums begin, end here
+    float4* part;         // [slices][tiles][cols4][128]; a whole sum goes to `out` at once
+    void* out;
+};
+
+// Both gradients of 16-bit operands of up to 256 columns, d never leaving the
+// SM: grad_x's CTAs come first, then grad_table's.
 struct LossFused {
     int64_t N, V, v0, v1;  // the call's items and this launch's
     int64_t w0;            // the item at the table map's first row
-    int32_t D, tiles, others, slices;  // others: tiles along the sum
-    int32_t first, last;   // grad_x over spans of the table: its sums begin, end here
+    int32_t D, cols4;
     float c2;
     const float *rows, *range;
-    float4* part;  // [slices][tiles][cols4][128]; one slice goes to `out` at once
-    void* out;
-    int32_t cols4;
+    LossSide x, w;
     uint32_t* error;
 };
 
@@ -216,20 +222,18 @@ struct LossFusedMaps {
     CUtensorMap x, w;
 };
 
-// A result's sums of slabs: [slabs][tiles][cols4][128] float4.
+// The results whose sums lie in several slabs.
 struct LossFinish {
-    const float4* part;
+    LossSide x, w;  // tiles 0: nothing to do
+    int64_t x_rows, w_rows;
     const float* range;
-    void* out;
-    int64_t rows;
-    int32_t tiles, slabs, D, cols4;
+    int32_t D, cols4;
 };
 
 cudaError_t loss_mma_configure();
 cudaError_t loss_fused_configure();
 constexpr int loss_fused_walk(int D) { return D <= 128 ? 128 : 64; }
-cudaError_t launch_loss_fused(const LossFused& p, const LossFusedMaps& maps, int dtype, bool items, int grid,
-                              cudaStream_t s);
+cudaError_t launch_loss_fused(const LossFused& p, const LossFusedMaps& maps, int dtype, cudaStream_t s);
 cudaError_t launch_loss_finish(const LossFinish& p, int dtype, cudaStream_t s);
 cudaError_t launch_loss_forward(const LossForward& p, const LossMaps& maps, int dtype, int grid, cudaStream_t s);
 cudaError_t launch_loss_step(const LossStep& p, const LossMaps& maps, int dtype, int grid, cudaStream_t s);
