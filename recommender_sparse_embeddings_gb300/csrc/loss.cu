@@ -202,9 +202,12 @@ T* at(void* base, size_t offset) {
 
 int64_t up_to(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
-// Elements of a piece of d: two pieces of this size, the rows and the piece of
-// the table stay in L2 (129 MB).
-constexpr int64_t kPieceBytes = 48 << 20;
+// Bytes of a piece of d (per plane of fp32's three).  Long pieces make few
+// launches, each with a start and an end in which SMs idle; shorter ones would
+// stay in L2 (129 MB), which gains less.  4096 x 32768 x 512 bf16 in pieces of 48
+// MB 445 us, 64 MB 412, 100 MB 353, 150 MB 380; 8192 x 20000 x 256 fp32 1543, 1424,
+// 1404, 1398.
+constexpr int64_t kPieceBytes = 96 << 20;
 // Work items that the sums' parts make at most.
 constexpr int kMostParts = 608;
 constexpr int kRowCtas = 1024;
@@ -218,9 +221,10 @@ struct Plan {
     size_t w_bytes, d_bytes, w_part_bytes;              // of one of two
 };
 
-// Whether the fused kernels take the call (their accumulators are 256 columns
-// wide); others go through pieces of d in memory.
-bool takes_fused(const tbe_softmax_loss* h) { return h->c.dtype != TBE_F32 && h->c.dim <= 256; }
+// Whether the fused kernel takes the call (its sums are up to 256 columns wide,
+// and of fp32's three planes 128 columns fill shared memory); others go through
+// pieces of d in memory.
+bool takes_fused(const tbe_softmax_loss* h) { return h->c.dim <= (h->c.dtype == TBE_F32 ? 128 : 256); }
 
 // Sized so that a workspace serves every smaller call: each size grows with N
 // and V although the piece shrinks with N.
@@ -424,17 +428,17 @@ void choose_sides(LossSide* x, LossSide* w, int D, int ctas) {
         return slices == 1 || (slices <= s.others && (int64_t)slices * s.tiles <= kMostParts);
     };
     for (int i : kTry) {
-        if (x->tiles == 0 ? i > 1 : !allowed(*x, i)) continue;
+        if (!allowed(*x, i)) continue;
         a.slices = i;
-        const int ca = x->tiles ? cost(a) : 0;
+        const int ca = cost(a);
         for (int j : kTry) {
-            if (w->tiles == 0 ? j > 1 : !allowed(*w, j)) continue;
+            if (!allowed(*w, j)) continue;
             b.slices = j;
-            const int cb = w->tiles ? cost(b) : 0;
+            const int cb = cost(b);
             const int64_t na = (int64_t)x->tiles * i, nb = (int64_t)w->tiles * j, n = na + nb;
             double time = std::max(ca, cb);
             if (n > ctas)
-                time = std::max(time, ((double)na * ca + (double)nb * cb) / ctas + 0.5 * (nb ? cb : ca));
+                time = std::max(time, ((double)na * ca + (double)nb * cb) / ctas + 0.5 * cb);
             if (time < least) {
                 least = time;
                 x->slices = i;
@@ -453,19 +457,20 @@ int backward_fused(const tbe_softmax_loss* h, const Plan& L, LossFused p, const 
     p.rows = at<float>(base, L.rows);
     p.range = at<float>(base, L.range);
     p.cols4 = L.cols4;
-    if (!encode(&maps.x, dt, base + L.x, p.D, p.N, 1, L.pitch, 64)) return TBE_ERR_CUDA;
-    Table w{h, table, table_stride, p.V, L.span, 1, L.pitch, direct(h, table, table_stride, p.V), base + L.w, L.w_bytes};
+    if (!encode(&maps.x, dt, base + L.x, p.D, p.N, L.planes, L.pitch, 64)) return TBE_ERR_CUDA;
+    Table w{h, table, table_stride, p.V, L.span, L.planes, L.pitch, direct(h, table, table_stride, p.V), base + L.w, L.w_bytes};
     const int64_t whole = w.is_direct ? p.V : std::min(p.V, L.span);
-    const int walked = loss_fused_walk(p.D);  // lines of a tile along the sum
-    p.x.tiles = gx ? (int)L.row_tiles : 0;
+    const int walked = loss_fused_walk(p.D, L.planes);  // lines of a tile along the sum
+    p.x.tiles = (int)L.row_tiles;
     p.x.others = (int)((whole + walked - 1) / walked);
     p.x.part = at<float4>(base, L.x_part);
     p.x.out = gx;
     p.w.others = (int)((p.N + walked - 1) / walked);
     p.w.part = at<float4>(base, L.w_part);
     p.w.first = p.w.last = 1;
-    p.w.tiles = gw ? (int)((whole + 127) / 128) : 0;
-    choose_sides(&p.x, &p.w, p.D, h->num_sms);
+    p.w.tiles = (int)((whole + 127) / 128);
+    choose_sides(&p.x, &p.w, p.D, h->num_sms);  // (of both, so that one alone has the same bits)
+    if (!gx) p.x.tiles = 0;
     for (p.v0 = 0; p.v0 < p.V; p.v0 = p.v1) {
         p.v1 = std::min(p.V, p.v0 + whole);
         p.w0 = w.first(p.v0);
@@ -476,7 +481,7 @@ int backward_fused(const tbe_softmax_loss* h, const Plan& L, LossFused p, const 
         p.x.first = p.v0 == 0;
         p.x.last = p.v1 == p.V;
         p.w.tiles = gw ? (int)((p.v1 - p.v0 + 127) / 128) : 0;
-        p.w.out = gw ? static_cast<char*>(gw) + p.v0 * p.D * 2 : nullptr;
+        p.w.out = gw ? static_cast<char*>(gw) + p.v0 * p.D * elem_bytes(dt) : nullptr;
         e = launch_loss_fused(p, maps, dt, s);
         if (e != cudaSuccess) return cuda_fail(e);
         LossFinish f{p.x, p.w, p.N, p.v1 - p.v0, p.range, p.D, L.cols4};
@@ -508,8 +513,7 @@ int backward(const tbe_softmax_loss* h, const Plan& L, LossStep p, const RowsIn&
     // share of a launch, so that none is waited for at its end.
     const int64_t piece = std::min(L.piece, p.V), item_tiles = (piece + 127) / 128;
     const int64_t row_blocks = (p.N + 63) / 64, piece_blocks = (piece + 63) / 64;
-    const int64_t products = (p.gx ? L.row_tiles * L.col_tiles * piece_blocks : 0) +
-                             (p.gw ? item_tiles * L.col_tiles * row_blocks : 0);
+    const int64_t products = L.row_tiles * L.col_tiles * piece_blocks + item_tiles * L.col_tiles * row_blocks;
     const int64_t share = std::max<int64_t>(4, products / (h->num_sms * 2));
     auto slabs = [&](int64_t blocks, int64_t tiles) {
         const int64_t most = std::max<int64_t>(1, kMostParts / std::max<int64_t>(tiles, 1));

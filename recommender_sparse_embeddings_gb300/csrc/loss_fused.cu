@@ -1,5 +1,5 @@
-// The softmax loss's gradients for 16-bit operands of up to 256 columns: the
-// logits' gradients d never leave the SM.
+// The softmax loss's gradients for operands of up to 256 columns (fp32: 128):
+// the logits' gradients d never leave the SM.
 //
 // A CTA holds 128 rows (grad_x) or 128 items (grad_table) in shared memory and
 // walks tiles of the others, 128 at a time or, above 128 columns, 64 (shared
@@ -18,7 +18,8 @@
 // instructions, a wait takes 100 cycles or more), warps 0 to 15 compute d, eight
 // those of the even tiles and eight those of the odd ones: a thread has one line
 // of S and half of its columns.  S and d are double buffered beside each other:
-// the scores after next are computed as soon as these are read.
+// the scores after next are computed as soon as these are read.  fp32's three
+// planes of each operand lie in shared memory side by side, d's in tensor memory.
 #include "loss_mma.cuh"
 
 namespace tbe {
@@ -27,16 +28,18 @@ namespace {
 
 constexpr int kFusedThreads = 608;
 
-template <int DP>
+template <int DP, int P>
 struct Fused {
-    static constexpr int BN = loss_fused_walk(DP);  // lines of a walked tile
-    static constexpr int kHeld = 128 * DP * 2, kTile = BN * DP * 2;
-    static constexpr int kStages = DP == 64 ? 6 : DP == 128 ? 5 : DP == 192 ? 5 : 4;
+    static constexpr int BN = loss_fused_walk(DP, P);  // lines of a walked tile
+    static constexpr int kHeldPlane = 128 * DP * 2, kTilePlane = BN * DP * 2;
+    static constexpr int kHeld = P * kHeldPlane, kTile = P * kTilePlane;
+    static constexpr int kStages = P == 3 ? (DP == 64 ? 5 : 2) : DP == 64 ? 6 : DP == 256 ? 4 : 5;
     static constexpr int kStats = 3 * BN * 4;  // bytes of a tile's rows' values
     static constexpr int ring = kHeld, stats = ring + kStages * kTile;
     static constexpr int bytes = stats + kStages * kStats + 1024;
-    // tensor memory: two S, two d (16-bit), the sums
-    static constexpr int d = 2 * BN, sums = BN == 128 ? 384 : 256;
+    // tensor memory: two S, two d (16-bit, plane by plane), the sums
+    static constexpr int d = 2 * BN, kD = P * BN / 2, sums = BN == 128 || P == 3 ? 384 : 256;
+    static_assert(d + 2 * kD <= sums && sums + DP <= 512, "");
 };
 
 struct FusedBars {
@@ -94,10 +97,10 @@ __device__ __forceinline__ void gradients(float (&x)[32], float c2, float minus_
     }
 }
 
-template <int DT, int DP, bool ITEMS>
+template <int DT, int DP, int P, bool ITEMS>
 __device__ __forceinline__ bool fused_body(const LossFused& p, const LossSide& side, const LossFusedMaps& maps, int cta,
                                            unsigned char* smem, FusedBars& bars, uint32_t tmem) {
-    using L = Fused<DP>;
+    using L = Fused<DP, P>;
     constexpr int kStages = L::kStages, BN = L::BN;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     // the CTA's tile and the n tiles from `from` on that it walks
@@ -112,10 +115,12 @@ __device__ __forceinline__ bool fused_body(const LossFused& p, const LossSide& s
         const int64_t item0 = p.v0 - p.w0;
         auto load = [&](uint32_t dst, const CUtensorMap& map, int64_t row, int boxes, uint64_t* bar) {
 #pragma unroll
-            for (int c = 0; c < DP / 64; ++c)
+            for (int plane = 0; plane < P; ++plane)
 #pragma unroll
-                for (int r = 0; r < boxes; ++r)
-                    load_box(dst + (c * boxes + r) * kBox, map, c * 64, row + r * 64, 0, bar);
+                for (int c = 0; c < DP / 64; ++c)
+#pragma unroll
+                    for (int r = 0; r < boxes; ++r)
+                        load_box(dst + ((plane * (DP / 64) + c) * boxes + r) * kBox, map, c * 64, row + r * 64, plane, bar);
         };
         if (elect_one()) {
             mbar_expect_tx(&bars.held, L::kHeld);
@@ -171,10 +176,16 @@ __device__ __forceinline__ bool fused_body(const LossFused& p, const LossSide& s
                 if (elect_one()) {
                     const uint64_t b = walk + (uint64_t)(st * (L::kTile / 16));
 #pragma unroll
-                    for (int k = 0; k < DP / 16; ++k)
-                        if (k < ksteps)
-                            mma_f16(tmem + buf * BN, held + (k / 4) * (2 * kBox / 16) + (k % 4) * 2,
-                                    b + (k / 4) * (BN * 128 / 16) + (k % 4) * 2, idesc, k > 0);
+                    for (int sum = P - 1; sum >= 0; --sum)  // of the planes' numbers: the small products first
+#pragma unroll
+                        for (int pa = sum; pa >= 0; --pa)
+#pragma unroll
+                            for (int k = 0; k < DP / 16; ++k)
+                                if (k < ksteps)
+                                    mma_f16(tmem + buf * BN,
+                                            held + pa * (L::kHeldPlane / 16) + (k / 4) * (2 * kBox / 16) + (k % 4) * 2,
+                                            b + (sum - pa) * (L::kTilePlane / 16) + (k / 4) * (BN * 128 / 16) + (k % 4) * 2,
+                                            idesc, sum + 1 < P || pa < sum || k > 0);
                     mma_commit(&bars.s_full[buf]);
                 }
                 __syncwarp();
@@ -189,9 +200,14 @@ __device__ __forceinline__ bool fused_body(const LossFused& p, const LossSide& s
                 if (elect_one()) {
                     const uint64_t b = walk + (uint64_t)(st * (L::kTile / 16));
 #pragma unroll
-                    for (int k = 0; k < BN / 16; ++k)
-                        mma_f16_ts(tmem + L::sums, tmem + L::d + buf * (BN / 2) + k * 8, b + k * (2048 / 16), idesc,
-                                   i > 0 || k > 0);
+                    for (int sum = P - 1; sum >= 0; --sum)
+#pragma unroll
+                        for (int pa = sum; pa >= 0; --pa)
+#pragma unroll
+                            for (int k = 0; k < BN / 16; ++k)
+                                mma_f16_ts(tmem + L::sums, tmem + L::d + buf * L::kD + pa * (BN / 2) + k * 8,
+                                           b + (sum - pa) * (L::kTilePlane / 16) + k * (2048 / 16), idesc,
+                                           i > 0 || sum + 1 < P || pa < sum || k > 0);
                     // (the tile's scores are done with it: d was computed from them)
                     mma_commit(&bars.empty[st]);
                     mma_commit(&bars.done[buf]);
@@ -241,15 +257,24 @@ __device__ __forceinline__ bool fused_body(const LossFused& p, const LossSide& s
                     if (lane == 0) mbar_arrive(&bars.s_read[buf]);
                 }
                 gradients<ITEMS, BN>(x, p.c2, minus_lse2, coef, at - h, left - h, stats + h, mine);
-                uint32_t pk[16];
-#pragma unroll
-                for (int c = 0; c < 16; ++c) pk[c] = pack2<DT>(x[2 * c], x[2 * c + 1]);
                 if (h == 0 && i >= 2) {  // d's columns are free of the product before last
                     ok = mbar_wait_tight(&bars.done[buf], (i / 2 - 1) & 1);
                     ok = __all_sync(0xffffffffu, ok);
                     tcgen05_after_sync();
                 }
-                tmem_st16(tmem + L::d + buf * (BN / 2) + group * (BN / 4) + h / 2 + lanes, pk);
+#pragma unroll
+                for (int plane = 0; plane < P; ++plane) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) {
+                        pk[c] = pack2<DT>(x[2 * c], x[2 * c + 1]);
+                        if (plane + 1 < P) {
+                            x[2 * c] -= __uint_as_float(pk[c] << 16);
+                            x[2 * c + 1] -= __uint_as_float(pk[c] & 0xffff0000u);
+                        }
+                    }
+                    tmem_st16(tmem + L::d + buf * L::kD + plane * (BN / 2) + group * (BN / 4) + h / 2 + lanes, pk);
+                }
             }
             if (!ok) break;
             tmem_wait_st();
@@ -266,7 +291,7 @@ __device__ __forceinline__ bool fused_body(const LossFused& p, const LossSide& s
             const int wide = (p.D + 15) / 16 * 16;
             const int64_t row = (int64_t)tile * 128 + line;
             if (side.slices == 1 && side.first && side.last)
-                store_rows<DT, 4>(side.out, row * p.D, acc, wide, warp / 4, row < (ITEMS ? p.v1 - p.v0 : p.N), p.D,
+                store_rows<P == 3 ? DT_F32 : DT, 4>(side.out, row * p.D, acc, wide, warp / 4, row < (ITEMS ? p.v1 - p.v0 : p.N), p.D,
                                   p.D % 8 == 0, 1.f / __ldg(p.range));
             else
                 add_slab<4>(side.part + ((int64_t)slice * side.tiles + tile) * p.cols4 * 128 + line, acc, wide, warp / 4,
@@ -276,7 +301,7 @@ __device__ __forceinline__ bool fused_body(const LossFused& p, const LossSide& s
     return ok;
 }
 
-template <int DT, int DP>
+template <int DT, int DP, int P>
 __global__ void __launch_bounds__(kFusedThreads, 1)
     loss_fused_kernel(const LossFused p, const __grid_constant__ LossFusedMaps maps) {
     extern __shared__ unsigned char smem_raw[];
@@ -287,7 +312,7 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
     if (threadIdx.x == 0) {
         mbar_init(&bars.held, 1);
         mbar_init(&bars.last, 1);
-        for (int i = 0; i < Fused<DP>::kStages; ++i) {
+        for (int i = 0; i < Fused<DP, P>::kStages; ++i) {
             mbar_init(&bars.full[i], 1);
             mbar_init(&bars.empty[i], 1);
         }
@@ -307,8 +332,8 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
     const uint32_t tmem = slot;
     chain_wait();
     const int x_ctas = p.x.tiles * p.x.slices, cta = blockIdx.x;
-    const bool ok = cta < x_ctas ? fused_body<DT, DP, false>(p, p.x, maps, cta, smem, bars, tmem)
-                                 : fused_body<DT, DP, true>(p, p.w, maps, cta - x_ctas, smem, bars, tmem);
+    const bool ok = cta < x_ctas ? fused_body<DT, DP, P, false>(p, p.x, maps, cta, smem, bars, tmem)
+                                 : fused_body<DT, DP, P, true>(p, p.w, maps, cta - x_ctas, smem, bars, tmem);
     if (!ok) atomicOr(p.error, ERR_TIMEOUT);
     tcgen05_before_sync();
     __syncthreads();
@@ -329,15 +354,17 @@ __global__ void __launch_bounds__(256) loss_finish_kernel(const LossFinish p) {
                 (int)(blockIdx.x % blocks) * 32, 1.f / __ldg(p.range), threadIdx.x);
 }
 
-template <int DT, int DP>
+template <int DT, int DP, int P>
 cudaError_t configure() {
-    return cudaFuncSetAttribute(loss_fused_kernel<DT, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, Fused<DP>::bytes);
+    return cudaFuncSetAttribute(loss_fused_kernel<DT, DP, P>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                Fused<DP, P>::bytes);
 }
 
-template <int DT, int DP>
+template <int DT, int DP, int P = 1>
 cudaError_t launch(const LossFused& p, const LossFusedMaps& maps, cudaStream_t s) {
     const int grid = p.x.tiles * p.x.slices + p.w.tiles * p.w.slices;
-    return launch_chained_smem(loss_fused_kernel<DT, DP>, dim3(grid), dim3(kFusedThreads), Fused<DP>::bytes, s, p, maps);
+    return launch_chained_smem(loss_fused_kernel<DT, DP, P>, dim3(grid), dim3(kFusedThreads), Fused<DP, P>::bytes, s, p,
+                               maps);
 }
 
 template <int DT>
@@ -351,25 +378,29 @@ cudaError_t launch_width(const LossFused& p, const LossFusedMaps& maps, cudaStre
 }  // namespace
 
 cudaError_t loss_fused_configure() {
-    cudaError_t e = configure<DT_F16, 64>();
-    if (e == cudaSuccess) e = configure<DT_F16, 128>();
-    if (e == cudaSuccess) e = configure<DT_F16, 192>();
-    if (e == cudaSuccess) e = configure<DT_F16, 256>();
-    if (e == cudaSuccess) e = configure<DT_BF16, 64>();
-    if (e == cudaSuccess) e = configure<DT_BF16, 128>();
-    if (e == cudaSuccess) e = configure<DT_BF16, 192>();
-    if (e == cudaSuccess) e = configure<DT_BF16, 256>();
+    cudaError_t e = configure<DT_F16, 64, 1>();
+    if (e == cudaSuccess) e = configure<DT_F16, 128, 1>();
+    if (e == cudaSuccess) e = configure<DT_F16, 192, 1>();
+    if (e == cudaSuccess) e = configure<DT_F16, 256, 1>();
+    if (e == cudaSuccess) e = configure<DT_BF16, 64, 1>();
+    if (e == cudaSuccess) e = configure<DT_BF16, 128, 1>();
+    if (e == cudaSuccess) e = configure<DT_BF16, 192, 1>();
+    if (e == cudaSuccess) e = configure<DT_BF16, 256, 1>();
+    if (e == cudaSuccess) e = configure<DT_BF16, 64, 3>();
+    if (e == cudaSuccess) e = configure<DT_BF16, 128, 3>();
     return e;
 }
 
 cudaError_t launch_loss_fused(const LossFused& p, const LossFusedMaps& maps, int dtype, cudaStream_t s) {
+    if (dtype == DT_F32) return p.D <= 64 ? launch<DT_BF16, 64, 3>(p, maps, s) : launch<DT_BF16, 128, 3>(p, maps, s);
     return dtype == DT_F16 ? launch_width<DT_F16>(p, maps, s) : launch_width<DT_BF16>(p, maps, s);
 }
 
 cudaError_t launch_loss_finish(const LossFinish& p, int dtype, cudaStream_t s) {
     const dim3 grid((unsigned)(p.x.tiles + p.w.tiles) * ((p.D + 31) / 32));
-    return dtype == DT_F16 ? launch_chained(loss_finish_kernel<DT_F16>, grid, dim3(256), s, p)
-                           : launch_chained(loss_finish_kernel<DT_BF16>, grid, dim3(256), s, p);
+    return dtype == DT_F32   ? launch_chained(loss_finish_kernel<DT_F32>, grid, dim3(256), s, p)
+           : dtype == DT_F16 ? launch_chained(loss_finish_kernel<DT_F16>, grid, dim3(256), s, p)
+                             : launch_chained(loss_finish_kernel<DT_BF16>, grid, dim3(256), s, p);
 }
 
 }  // namespace tbe

@@ -9,14 +9,8 @@ constexpr int kForwardThreads = 576;
 constexpr float kLazyMax = 8.f;
 
 struct LossBars {
-    uint64_t full[kLossStages], empty[kLossStages], acc_full[2], acc_empty[2];
+    uint64_t full[kLossStages], empty[kLossStages], a_full[2], a_empty[2], acc_full[2], acc_empty[2];
 };
-
-// Plane pairs of an fp32 product, small ones first.
-template <int P>
-constexpr int kTerms = P == 3 ? 6 : 1;
-__device__ __forceinline__ int plane_a(int term) { return (0x001012 >> (4 * term)) & 15; }
-__device__ __forceinline__ int plane_b(int term) { return (0x010210 >> (4 * term)) & 15; }
 
 __device__ __forceinline__ void store_box(const CUtensorMap& map, uint32_t src, int col, int row, int plane) {
     asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(&map),
@@ -36,12 +30,13 @@ struct Product {
     int k0, kblocks;  // along the sum, blocks of 64
     int wide;
     int slab;
+    int last_steps;  // scores: steps of 16 columns in the last block
 };
 
 __device__ __forceinline__ int columns_of(int64_t left) { return (int)tmin<int64_t>(256, (left + 15) / 16 * 16); }
 
 __device__ __forceinline__ Product score_tile(int64_t V, int D, int row0, int64_t item) {
-    return Product{ITEM_D, row0, item, 0, (D + 63) / 64, columns_of(V - item), 0};
+    return Product{ITEM_D, row0, item, 0, (D + 63) / 64, columns_of(V - item), 0, ((D - 1) % 64 + 16) / 16};
 }
 
 // Work item i of a backward launch: the long ones first.
@@ -83,54 +78,93 @@ __device__ __forceinline__ Product step_item(const LossStep& p, int i) {
     return t;
 }
 
-// Warp roles' shared counters: steps through the ring and accumulators used.
+// The operands' way through shared memory.  One plane: stages of a tile of A (2
+// boxes) and of B (4).  fp32's three: A's planes of a block stay for the block's
+// six products, twice 3 tiles; B's planes pass in three stages, each meeting the
+// planes of A that matter beside it.  That is 144 KB for what 288 KB of single
+// products would be: at 2 x 96 bytes a cycle and SM the L2 cache's reads bounded
+// fp32's passes.
+template <int P>
+struct Ring {
+    static constexpr int kStages = P == 3 ? 3 : 4;
+    static constexpr int kStage = P == 3 ? 4 * kBox : 6 * kBox;
+    static constexpr int b = P == 3 ? 2 * 3 * 2 * kBox : 2 * kBox;  // of the first stage
+};
+static_assert(Ring<3>::b + Ring<3>::kStages * Ring<3>::kStage <= kLossStages * kStageBytes, "");
+
 template <int P, typename Next>
 __device__ bool produce(unsigned char* smem, LossBars& bars, const LossMaps& maps, int64_t w0, int64_t p_row, Next next) {
-    int n = 0;
+    using R = Ring<P>;
+    int n = 0, blocks = 0;  // stages and (P = 3) blocks so far
     bool ok = true;
     Product t;
+    const uint32_t base = smem_u32(smem);
     while (ok && next(t)) {
         if (t.kind >= ITEM_FIN_W) continue;
-        const int steps = t.kblocks * kTerms<P>, slabs = (t.wide + 63) / 64;
-        for (int s = 0; s < steps && ok; ++s, ++n) {
-            const int st = n % kLossStages;
-            if (n >= kLossStages) ok = mbar_wait_tight(&bars.empty[st], (n / kLossStages - 1) & 1);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            if (elect_one()) {
-                uint64_t* bar = &bars.full[st];
-                const uint32_t a = smem_u32(smem) + st * kStageBytes, b = a + 2 * kBox;
-                const int term = P == 3 ? s / t.kblocks : 0, k = (t.k0 + (P == 3 ? s % t.kblocks : s)) * 64;
-                const int pa = P == 3 ? plane_a(term) : 0, pb = P == 3 ? plane_b(term) : 0;
-                mbar_expect_tx(bar, (2 + slabs) * kBox);
-                if (t.kind == ITEM_D) {
-                    load_box(a, maps.x, k, t.row0, pa, bar);
-                    load_box(a + kBox, maps.x, k, t.row0 + 64, pa, bar);
-                    for (int j = 0; j < slabs; ++j) load_box(b + j * kBox, maps.w, k, t.col0 - w0 + j * 64, pb, bar);
-                } else if (t.kind == ITEM_GX) {
-                    load_box(a, maps.d_in, k, t.row0, pa, bar);
-                    load_box(a + kBox, maps.d_in, k, t.row0 + 64, pa, bar);
-                    for (int j = 0; j < slabs; ++j)
-                        load_box(b + j * kBox, maps.pw, (int)t.col0 + j * 64, p_row + k, pb, bar);
-                } else {
-                    load_box(a, maps.d_in, t.row0, k, pa, bar);
-                    load_box(a + kBox, maps.d_in, t.row0 + 64, k, pa, bar);
-                    for (int j = 0; j < slabs; ++j) load_box(b + j * kBox, maps.x, (int)t.col0 + j * 64, k, pb, bar);
-                }
+        const int slabs = (t.wide + 63) / 64;
+        auto load_a = [&](uint32_t a, int k, int plane, uint64_t* bar) {
+            if (t.kind == ITEM_D) {
+                load_box(a, maps.x, k, t.row0, plane, bar);
+                load_box(a + kBox, maps.x, k, t.row0 + 64, plane, bar);
+            } else if (t.kind == ITEM_GX) {
+                load_box(a, maps.d_in, k, t.row0, plane, bar);
+                load_box(a + kBox, maps.d_in, k, t.row0 + 64, plane, bar);
+            } else {
+                load_box(a, maps.d_in, t.row0, k, plane, bar);
+                load_box(a + kBox, maps.d_in, t.row0 + 64, k, plane, bar);
             }
-            __syncwarp();
+        };
+        auto load_b = [&](uint32_t b, int k, int plane, uint64_t* bar) {
+            for (int j = 0; j < slabs; ++j)
+                if (t.kind == ITEM_D)
+                    load_box(b + j * kBox, maps.w, k, t.col0 - w0 + j * 64, plane, bar);
+                else if (t.kind == ITEM_GX)
+                    load_box(b + j * kBox, maps.pw, (int)t.col0 + j * 64, p_row + k, plane, bar);
+                else
+                    load_box(b + j * kBox, maps.x, (int)t.col0 + j * 64, k, plane, bar);
+        };
+        for (int s = 0; s < t.kblocks && ok; ++s) {
+            const int k = (t.k0 + s) * 64;
+            if constexpr (P == 3) {
+                const int ab = blocks & 1;
+                if (blocks >= 2) ok = mbar_wait_tight(&bars.a_empty[ab], (blocks / 2 - 1) & 1);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                if (elect_one()) {
+                    mbar_expect_tx(&bars.a_full[ab], 3 * 2 * kBox);
+                    for (int plane = 0; plane < 3; ++plane)
+                        load_a(base + (ab * 3 + plane) * 2 * kBox, k, plane, &bars.a_full[ab]);
+                }
+                __syncwarp();
+                ++blocks;
+            }
+            for (int plane = P - 1; plane >= 0 && ok; --plane, ++n) {
+                const int st = n % R::kStages;
+                if (n >= R::kStages) ok = mbar_wait_tight(&bars.empty[st], (n / R::kStages - 1) & 1);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                if (elect_one()) {
+                    mbar_expect_tx(&bars.full[st], ((P == 3 ? 0 : 2) + slabs) * kBox);
+                    if constexpr (P == 1) load_a(base + st * R::kStage, k, 0, &bars.full[st]);
+                    load_b(base + R::b + st * R::kStage, k, plane, &bars.full[st]);
+                }
+                __syncwarp();
+            }
         }
     }
     // where a wait ran out: this CTA's copies in flight land before it ends
-    if (!ok)
-        for (int i = tmax(0, n - kLossStages); i < n; ++i)
-            mbar_wait_tight(&bars.full[i % kLossStages], (i / kLossStages) & 1);
+    if (!ok) {
+        for (int i = tmax(0, n - R::kStages); i < n; ++i)
+            mbar_wait_tight(&bars.full[i % R::kStages], (i / R::kStages) & 1);
+        for (int i = tmax(0, blocks - 2); i < blocks; ++i) mbar_wait_tight(&bars.a_full[i & 1], (i / 2) & 1);
+    }
     return ok;
 }
 
 template <int DT, int P, typename Next>
 __device__ bool multiply(unsigned char* smem, LossBars& bars, uint32_t tmem, Next next) {
-    int n = 0, tile = 0;
+    using R = Ring<P>;
+    int n = 0, blocks = 0, tile = 0;
     bool ok = true;
     auto wait = [&](uint64_t* bar, int parity) {
         const bool in = mbar_wait_tight(bar, parity & 1);
@@ -148,27 +182,43 @@ __device__ bool multiply(unsigned char* smem, LossBars& bars, uint32_t tmem, Nex
         const uint32_t idesc =
             mma_idesc(DT == DT_BF16, 128, t.wide) | (a_mn ? 1u << 15 : 0u) | (b_mn ? kMnMajorB : 0u);
         const uint64_t da = a_mn ? smem_desc_mn(base, kBox) : smem_desc_sw128(base, 1024);
-        const uint64_t db = b_mn ? smem_desc_mn(base + 2 * kBox, kBox) : smem_desc_sw128(base + 2 * kBox, 1024);
+        const uint64_t db = b_mn ? smem_desc_mn(base + R::b, kBox) : smem_desc_sw128(base + R::b, 1024);
         const int ka = a_mn ? 2048 / 16 : 2, kb = b_mn ? 2048 / 16 : 2;
-        const int steps = t.kblocks * kTerms<P>;
-        for (int s = 0; s < steps && ok; ++s, ++n) {
-            const int st = n % kLossStages;
-            ok = wait(&bars.full[st], n / kLossStages);
-            if (!ok) break;
-            if (elect_one()) {
-                const uint64_t at = (uint64_t)(st * (kStageBytes / 16));
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    mma_f16(tmem + buf * 256, da + at + k * ka, db + at + k * kb, idesc, s > 0 || k > 0);
-                mma_commit(&bars.empty[st]);
-                if (s + 1 == steps) mma_commit(&bars.acc_full[buf]);
+        for (int s = 0; s < t.kblocks && ok; ++s) {
+            const int steps = t.kind == ITEM_D && s + 1 == t.kblocks ? t.last_steps : 4;  // of 16 along the sum
+            const int ab = blocks & 1;
+            if constexpr (P == 3) {
+                ok = wait(&bars.a_full[ab], blocks / 2);
+                ++blocks;
             }
-            __syncwarp();
+            for (int plane = P - 1; plane >= 0 && ok; --plane, ++n) {
+                const int st = n % R::kStages;
+                ok = wait(&bars.full[st], n / R::kStages);
+                if (!ok) break;
+                if (elect_one()) {
+                    const uint64_t b = db + (uint64_t)(st * (R::kStage / 16));
+                    for (int pa = P - 1 - plane; pa >= 0; --pa) {
+                        const uint64_t a = da + (uint64_t)(P == 3 ? (ab * 3 + pa) * (2 * kBox / 16) : st * (R::kStage / 16));
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (k < steps)
+                                mma_f16(tmem + buf * 256, a + k * ka, b + k * kb, idesc,
+                                        s > 0 || plane + 1 < P || pa + 1 + plane < P || k > 0);
+                    }
+                    mma_commit(&bars.empty[st]);
+                    if (plane == 0) {
+                        if constexpr (P == 3) mma_commit(&bars.a_empty[ab]);
+                        if (s + 1 == t.kblocks) mma_commit(&bars.acc_full[buf]);
+                    }
+                }
+                __syncwarp();
+            }
         }
         ++tile;
     }
     // nothing of this CTA arrives on a barrier after its end
-    if (ok && n > 0) ok = wait(&bars.empty[(n - 1) % kLossStages], (n - 1) / kLossStages);
+    if (ok && n > 0) ok = wait(&bars.empty[(n - 1) % R::kStages], (n - 1) / R::kStages);
+    if (P == 3 && ok && blocks > 0) ok = wait(&bars.a_empty[(blocks - 1) & 1], (blocks - 1) / 2);
     return ok;
 }
 
@@ -237,6 +287,8 @@ __device__ __forceinline__ uint32_t begin(LossBars& bars, uint32_t* slot) {
             mbar_init(&bars.empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars.a_full[i], 1);
+            mbar_init(&bars.a_empty[i], 1);
             mbar_init(&bars.acc_full[i], 1);
             mbar_init(&bars.acc_empty[i], READERS);
         }

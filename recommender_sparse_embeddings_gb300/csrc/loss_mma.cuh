@@ -15,8 +15,8 @@
 // fp32.  An fp32 number is the sum of three bf16 numbers exactly (8 bits each,
 // rounded to nearest, the rest carried on).  fp32 operands are kept as three
 // such planes, and a product is the sum of the six plane products of at least
-// 2^-18 of the whole, added small ones first; the three left out are below
-// 2^-26, less than an fp32 rounding.
+// 2^-18 of the whole; the three left out are below 2^-26, less than an fp32
+// rounding.
 #pragma once
 
 #include <cuda.h>
@@ -206,8 +206,8 @@ struct LossSide {
     void* out;
 };
 
-// Both gradients of 16-bit operands of up to 256 columns, d never leaving the
-// SM: grad_x's CTAs come first, then grad_table's.
+// Both gradients of operands of up to 256 columns (fp32: 128), d never leaving
+// the SM: grad_x's CTAs come first, then grad_table's.
 struct LossFused {
     int64_t N, V, v0, v1;  // the call's items and this launch's
     int64_t w0;            // the item at the table map's first row
@@ -232,7 +232,8 @@ struct LossFinish {
 
 cudaError_t loss_mma_configure();
 cudaError_t loss_fused_configure();
-constexpr int loss_fused_walk(int D) { return D <= 128 ? 128 : 64; }
+// Lines of the tiles that the fused kernel walks.
+constexpr int loss_fused_walk(int D, int planes) { return D <= 128 && planes == 1 ? 128 : 64; }
 cudaError_t launch_loss_fused(const LossFused& p, const LossFusedMaps& maps, int dtype, cudaStream_t s);
 cudaError_t launch_loss_finish(const LossFinish& p, int dtype, cudaStream_t s);
 cudaError_t launch_loss_forward(const LossForward& p, const LossMaps& maps, int dtype, int grid, cudaStream_t s);
