@@ -493,6 +493,42 @@ int backward_fused(const tbe_softmax_loss* h, const Plan& L, LossFused p, const 
     return TBE_OK;
 }
 
+// Shares d's work items among the CTAs so that each ends at about the same
+// time: the products are given out in turn, whose items are long, and d's fill
+// up.  In blocks of 64 along the sum; an item of d is bound by its arithmetic, as
+// long as ten of them, where it has fewer.
+void share_d(LossStep* q, int ctas) {
+    const int64_t x_cost = ((q->p_items + 63) / 64 + q->x_slabs - 1) / q->x_slabs;
+    const int64_t w_cost = ((q->N + 63) / 64 + q->w_slabs - 1) / q->w_slabs;
+    const int64_t d_cost = std::max((q->D + 63) / 64, 10);
+    auto given = [&](int64_t items, int c) { return items / ctas + (c < items % ctas ? 1 : 0); };
+    auto long_cost = [&](int c) {
+        const int64_t w = given(q->n_gw, c);
+        return w * w_cost + (given((int64_t)q->n_gw + q->n_gx, c) - w) * x_cost;
+    };
+    // the least level at which d's items find room, by halving
+    int64_t lo = 0, hi = (int64_t)q->n_d * d_cost + 1;
+    for (int c = 0; c < ctas; ++c) hi = std::max(hi, long_cost(c) + (int64_t)q->n_d * d_cost + 1);
+    auto room = [&](int64_t level) {
+        int64_t items = 0;
+        for (int c = 0; c < ctas; ++c) items += std::max<int64_t>(0, level - long_cost(c)) / d_cost;
+        return items;
+    };
+    while (lo < hi) {
+        const int64_t mid = (lo + hi) / 2;
+        if (room(mid) >= q->n_d)
+            hi = mid;
+        else
+            lo = mid + 1;
+    }
+    int64_t at = 0;
+    for (int c = 0; c < ctas; ++c) {
+        q->d_from[c] = (int32_t)at;
+        at = std::min<int64_t>(q->n_d, at + std::max<int64_t>(0, lo - long_cost(c)) / d_cost);
+    }
+    q->d_from[ctas] = q->n_d;
+}
+
 int backward(const tbe_softmax_loss* h, const Plan& L, LossStep p, const RowsIn& rows, const void* table, int64_t table_stride,
              char* base, cudaStream_t s) {
     LossMaps maps{};
@@ -522,6 +558,7 @@ int backward(const tbe_softmax_loss* h, const Plan& L, LossStep p, const RowsIn&
     p.x_slabs = slabs(piece_blocks, L.row_tiles * L.col_tiles);
     p.w_slabs = slabs(row_blocks, item_tiles * L.col_tiles);
     const int64_t pieces = (p.V + L.piece - 1) / L.piece;
+    const int most_ctas = std::min(h->num_sms, kMaxStepCtas);
     for (int64_t j = 0; j <= pieces + 1; ++j) {
         LossStep q = p;
         q.n_d = q.n_gx = q.n_gw = q.n_fin_w = q.n_fin_x = 0;
@@ -557,7 +594,9 @@ int backward(const tbe_softmax_loss* h, const Plan& L, LossStep p, const RowsIn&
         if (j == pieces + 1 && p.gx) q.n_fin_x = (int)L.row_tiles * ((p.D + 31) / 32);
         const int64_t n = (int64_t)q.n_d + q.n_gx + q.n_gw + q.n_fin_w + q.n_fin_x;
         if (n == 0) continue;
-        e = launch_loss_step(q, maps, dt, (int)std::min<int64_t>(n, h->num_sms), s);
+        const int ctas = (int)std::min<int64_t>(n, most_ctas);
+        share_d(&q, ctas);
+        e = launch_loss_step(q, maps, dt, ctas, s);
         if (e != cudaSuccess) return cuda_fail(e);
     }
     return TBE_OK;

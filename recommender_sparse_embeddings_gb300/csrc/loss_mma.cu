@@ -322,15 +322,28 @@ __global__ void __launch_bounds__(kLossThreads, 1)
     const uint32_t tmem = begin<9, 8>(bars, &slot);
     chain_wait();
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int n_items = p.n_gw + p.n_gx + p.n_d + p.n_fin_w + p.n_fin_x;
-    int item = blockIdx.x;
+    // the products in turn (the long items first), then this CTA's share of d,
+    // the results in turn
+    const int products = p.n_gw + p.n_gx, results = products + p.n_d, n_items = results + p.n_fin_w + p.n_fin_x;
+    int a = blockIdx.x, b = products + p.d_from[blockIdx.x], f = results + blockIdx.x;
+    const int b_end = products + p.d_from[blockIdx.x + 1];
     auto next = [&](Product& t) {
-        do {
-            if (item >= n_items) return false;
-            t = step_item(p, item);
-            item += gridDim.x;
-        } while (t.kind <= ITEM_GX && t.kblocks == 0);  // (the last piece has fewer blocks than slabs)
-        return true;
+        for (;;) {
+            int i;
+            if (a < products) {
+                i = a;
+                a += gridDim.x;
+            } else if (b < b_end) {
+                i = b++;
+            } else if (f < n_items) {
+                i = f;
+                f += gridDim.x;
+            } else {
+                return false;
+            }
+            t = step_item(p, i);
+            if (t.kind > ITEM_GX || t.kblocks > 0) return true;  // (the last piece has fewer blocks than slabs)
+        }
     };
     bool ok = true;
     if (warp == 8) {

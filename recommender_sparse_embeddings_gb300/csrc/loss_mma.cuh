@@ -163,6 +163,9 @@ struct LossForward {
     uint32_t* error;
 };
 
+// CTAs of a backward launch at most.
+constexpr int kMaxStepCtas = 256;
+
 // One launch of the backward pass: d of a piece of the table, the products of
 // the piece before it, the results of the piece before that.
 struct LossStep {
@@ -171,8 +174,9 @@ struct LossStep {
     float c2;
     const float* rows;   // [row_tiles][kRowValues]
     const float* range;  // the power of two in the rows' second values
-    // d of the items from d0 on
+    // d of the items from d0 on, its work items d_from[c] .. d_from[c + 1] by CTA c
     int32_t n_d;
+    int32_t d_from[kMaxStepCtas + 1];
     int64_t d0, dw0;  // dw0, pw0: the items at the first row of the maps w and pw
     // products of the piece [p0, p0 + p_items)
     int32_t n_gx, n_gw;
