@@ -76,13 +76,13 @@ __global__ void __launch_bounds__(256) loss_copy_kernel(const Copy c) {
 struct RowsIn {
     Copy x;
     const void* targets;
-    int32_t index64;
+    int32_t index64, parts;  // parts: of gmax; 0: each CTA looks through the rows by itself
     int64_t V, tiles;
     const float *lse, *g;
     float scale;
-    float* rows;   // [tiles][kRowValues]
-    float* range;  // the power of two that fp16's d is multiplied by, else 1
-    float* gmax;   // fp16: kMaxCtas partial maxima
+    float* rows;  // [tiles][kRowValues]
+    float* unit;  // what the rows' second values are taken relative to
+    float* gmax;  // [kMaxCtas] partial maxima
     uint32_t* error;
 };
 
@@ -93,13 +93,11 @@ __device__ __forceinline__ int64_t row_target(const RowsIn& p, int64_t row) {
     return t >= 0 && t < p.V ? t : -1;
 }
 
-// fp16: the largest finite |g scale| of the rows, in parts.
-constexpr int kMaxCtas = 64;
-__global__ void __launch_bounds__(256) loss_max_kernel(const RowsIn p) {
-    chain_wait();
+// The largest finite |g scale| of the rows from `first` on, in steps.
+__device__ __forceinline__ float row_max(const RowsIn& p, int64_t first, int64_t step) {
     __shared__ float most[8];
     float m = 0.f;
-    for (int64_t row = (int64_t)blockIdx.x * 256 + threadIdx.x; row < p.x.rows; row += (int64_t)gridDim.x * 256) {
+    for (int64_t row = first; row < p.x.rows; row += step) {
         const float a = fabsf(p.g[row] * p.scale);
         if (a <= FLT_MAX && row_target(p, row) >= 0) m = fmaxf(m, a);
     }
@@ -107,45 +105,60 @@ __global__ void __launch_bounds__(256) loss_max_kernel(const RowsIn p) {
     for (int o = 16; o > 0; o /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     if (threadIdx.x % 32 == 0) most[threadIdx.x / 32] = m;
     __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int w = 1; w < 8; ++w) m = fmaxf(m, most[w]);
-        p.gmax[blockIdx.x] = m;
-    }
+    for (int w = 0; w < 8; ++w) m = fmaxf(m, most[w]);
+    return m;
+}
+
+// It in parts, where there are many rows.
+constexpr int kMaxCtas = 64, kFewRows = 2048;
+__global__ void __launch_bounds__(256) loss_max_kernel(const RowsIn p) {
+    chain_wait();
+    const float m = row_max(p, (int64_t)blockIdx.x * 256 + threadIdx.x, (int64_t)gridDim.x * 256);
+    if (threadIdx.x == 0) p.gmax[blockIdx.x] = m;
 }
 
 // The backward pass's rows, one warp each: x copied with zeros in the rows left
-// out, and what each row brings.  fp16's range is narrow (6e-8 to 65504) and d
-// moves with g and with the weights, 1 / V each: it is held times the power of
-// two that brings the largest |g scale| into [2^14, 2^15), so that weights down
-// to 2^-28 keep all their bits; the results are divided by it, exactly.
+// out, and what each row brings.
+//
+// 16-bit types hold d relative to the largest |g scale|.  So where all rows have
+// the same g (a mean), d is p - [target] itself: -1 for a target of little weight
+// has no rounding, where -g would be off by the same 2^-9 in every row (grad_table
+// of 300 rows over 5000 items in bf16: 0.0025 off, so 0.0017).  fp16's range is
+// narrow besides (6e-8 to 65504): there the largest is 2^14, and weights down to
+// 2^-28 keep all their bits.
 template <int DT>
 __global__ void __launch_bounds__(256) loss_rows_kernel(const RowsIn p) {
     chain_wait();
     const int lane = threadIdx.x % 32;
-    float up = 1.f;
-    if constexpr (DT == DT_F16) {
-        float m = fmaxf(p.gmax[lane], p.gmax[lane + 32]);
+    float unit = 1.f;
+    if constexpr (DT != DT_F32) {
+        float m = 0.f;
+        if (p.parts == 0) {
+            m = row_max(p, threadIdx.x, 256);
+        } else {
+            m = fmaxf(p.gmax[lane], p.gmax[lane + 32]);
 #pragma unroll
-        for (int o = 16; o > 0; o /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        // (27: the power stays below 2^115)
-        const int e = tmax((int)(__float_as_uint(m) >> 23), 27);
-        if (m > 0.f) up = __uint_as_float((uint32_t)(127 + 14 + 127 - e) << 23);
+            for (int o = 16; o > 0; o /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        }
+        if (DT == DT_F16) m *= 0x1p-14f;
+        if (m > 0.f) unit = m;
     }
-    if (blockIdx.x == 0 && threadIdx.x == 0) *p.range = up;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.unit = unit;
     for (int64_t row = ((int64_t)blockIdx.x * 256 + threadIdx.x) / 32; row < p.tiles * 128;
          row += (int64_t)gridDim.x * 8) {
         float* to = p.rows + row / 128 * kRowValues + row % 128;
         const int64_t t = row < p.x.rows ? row_target(p, row) : -1;
         if (row < p.x.rows) copy_row<DT>(p.x, row, t < 0, lane);
         if (lane == 0) {
-            to[0] = t < 0 ? 0.f : -p.lse[row] * kLog2e;
-            to[128] = t < 0 ? 0.f : p.g[row] * p.scale * up;
+            to[0] = t < 0 ? 0.f : -p.lse[row] * (DT == DT_F32 ? 1.f : kLog2e);
+            to[128] = t < 0 ? 0.f : p.g[row] * p.scale / unit;
             to[256] = __int_as_float((int)t);
         }
     }
 }
 
 // The slices' sums of a row joined, by one warp.
+template <int DT>
 __global__ void __launch_bounds__(256)
     loss_join_kernel(const float2* part, int parts, const float* picked, const void* targets, int index64, int64_t N,
                      int64_t V, float* loss, float* lse) {
@@ -160,17 +173,17 @@ __global__ void __launch_bounds__(256)
     float l = 0.f;
     for (int i = lane; i < parts; i += 32) {
         const float2 y = part[row * parts + i];
-        // (a half of a tile that no item reaches: -inf and 0)
-        if (!(y.y == 0.f)) l = fmaf(y.y, ex2(y.x - m), l);
+        // (a part that no item reaches: -inf and 0)
+        if (!(y.y == 0.f)) l = fmaf(y.y, ex2(DT == DT_F32 ? (y.x - m) * kLog2e : y.x - m), l);
     }
 #pragma unroll
     for (int o = 16; o > 0; o /= 2) l += __shfl_xor_sync(0xffffffffu, l, o);
     if (lane != 0) return;
     const int64_t t = index64 ? static_cast<const int64_t*>(targets)[row] : static_cast<const int32_t*>(targets)[row];
-    constexpr float kLn2 = 0.6931471805599453f;
+    constexpr float kNatural = DT == DT_F32 ? 1.f : 0.6931471805599453f;
     const float log_l = logf(l);
-    lse[row] = fmaf(m, kLn2, log_l);
-    loss[row] = t >= 0 && t < V ? fmaf(m - picked[row], kLn2, log_l) : 0.f;
+    lse[row] = fmaf(m, kNatural, log_l);
+    loss[row] = t >= 0 && t < V ? fmaf(m - picked[row], kNatural, log_l) : 0.f;
 }
 
 size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
@@ -217,9 +230,12 @@ struct Plan {
     int64_t row_tiles;
     int64_t piece;  // items
     int64_t span;   // items of a copied part of the table, whole pieces
-    size_t rows, range, x, w, d, x_part, w_part, total;  // offsets
+    size_t rows, unit, x, w, d, x_part, w_part, total;  // offsets
     size_t w_bytes, d_bytes, w_part_bytes;              // of one of two
 };
+
+// What a product is multiplied by on its way into the softmax.
+float argument_scale(const tbe_softmax_loss* h) { return h->c.dtype == TBE_F32 ? h->c.scale : h->c.scale * kLog2e; }
 
 // Whether the fused kernel takes the call (its sums are up to 256 columns wide,
 // and of fp32's three planes 128 columns fill shared memory); others go through
@@ -258,7 +274,7 @@ Plan make_plan(const tbe_softmax_loss* h, int64_t N, int64_t V, bool backward, b
     }
     if (backward) {
         L.rows = take(sizeof(float) * kRowValues * L.row_tiles);
-        L.range = take(sizeof(float) * (1 + kMaxCtas));
+        L.unit = take(sizeof(float) * (1 + kMaxCtas));
         const size_t tile = (size_t)L.cols4 * 128 * sizeof(float4);
         // (one sum over all items needs no slabs, and several make kMostParts tiles at most)
         L.x_part = take(std::max<int64_t>(L.row_tiles, kMostParts / L.col_tiles + 1) * tile);
@@ -395,22 +411,27 @@ int forward(const tbe_softmax_loss* h, const Plan& L, LossForward p, const void*
         e = launch_loss_forward(p, maps, h->c.dtype, (int)std::min<int64_t>(items, h->num_sms), s);
         if (e != cudaSuccess) return cuda_fail(e);
     }
-    return status(launch_chained(loss_join_kernel, dim3((unsigned)((p.N + 7) / 8)), dim3(256), s,
+    auto* join = h->c.dtype == TBE_F32 ? loss_join_kernel<DT_F32> : loss_join_kernel<DT_BF16>;
+    return status(launch_chained(join, dim3((unsigned)((p.N + 7) / 8)), dim3(256), s,
                                  (const float2*)p.part, 4 * p.slices, (const float*)p.picked, p.targets, p.index64, p.N,
                                  p.V, loss, lse));
 }
 
 cudaError_t launch_rows(const tbe_softmax_loss* h, const Plan& L, RowsIn rows, char* base, cudaStream_t s) {
     rows.rows = at<float>(base, L.rows);
-    rows.range = at<float>(base, L.range);
-    rows.gmax = rows.range + 1;
+    rows.unit = at<float>(base, L.unit);
+    rows.gmax = rows.unit + 1;
     rows.tiles = L.row_tiles;
     rows.x.to = at<uint16_t>(base, L.x);
     const dim3 grid((unsigned)std::min<int64_t>(rows.tiles * 16, kRowCtas));
+    rows.parts = rows.x.rows > kFewRows ? kMaxCtas : 0;
     if (h->c.dtype == TBE_F32) return launch_chained(loss_rows_kernel<DT_F32>, grid, dim3(256), s, rows);
-    if (h->c.dtype == TBE_BF16) return launch_chained(loss_rows_kernel<DT_BF16>, grid, dim3(256), s, rows);
-    const cudaError_t e = launch_chained(loss_max_kernel, dim3(kMaxCtas), dim3(256), s, rows);
-    return e != cudaSuccess ? e : launch_chained(loss_rows_kernel<DT_F16>, grid, dim3(256), s, rows);
+    if (rows.parts > 0) {
+        const cudaError_t e = launch_chained(loss_max_kernel, dim3(kMaxCtas), dim3(256), s, rows);
+        if (e != cudaSuccess) return e;
+    }
+    return h->c.dtype == TBE_BF16 ? launch_chained(loss_rows_kernel<DT_BF16>, grid, dim3(256), s, rows)
+                                  : launch_chained(loss_rows_kernel<DT_F16>, grid, dim3(256), s, rows);
 }
 
 // Slices of the fused launch's sums, x's and w's: those of the least estimated
@@ -455,7 +476,7 @@ int backward_fused(const tbe_softmax_loss* h, const Plan& L, LossFused p, const 
     cudaError_t e = launch_rows(h, L, rows, base, s);
     if (e != cudaSuccess) return cuda_fail(e);
     p.rows = at<float>(base, L.rows);
-    p.range = at<float>(base, L.range);
+    p.unit = at<float>(base, L.unit);
     p.cols4 = L.cols4;
     if (!encode(&maps.x, dt, base + L.x, p.D, p.N, L.planes, L.pitch, 64)) return TBE_ERR_CUDA;
     Table w{h, table, table_stride, p.V, L.span, L.planes, L.pitch, direct(h, table, table_stride, p.V), base + L.w, L.w_bytes};
@@ -480,13 +501,16 @@ int backward_fused(const tbe_softmax_loss* h, const Plan& L, LossFused p, const 
         p.x.others = (int)((p.v1 - p.v0 + walked - 1) / walked);
         p.x.first = p.v0 == 0;
         p.x.last = p.v1 == p.V;
+        // (fp32's results take the parts of a sum as they come)
+        p.x.direct = p.x.slices == 1 && (L.planes == 3 || (p.x.first && p.x.last));
+        p.w.direct = p.w.slices == 1;
         p.w.tiles = gw ? (int)((p.v1 - p.v0 + 127) / 128) : 0;
         p.w.out = gw ? static_cast<char*>(gw) + p.v0 * p.D * elem_bytes(dt) : nullptr;
         e = launch_loss_fused(p, maps, dt, s);
         if (e != cudaSuccess) return cuda_fail(e);
-        LossFinish f{p.x, p.w, p.N, p.v1 - p.v0, p.range, p.D, L.cols4};
-        if (!(p.x.last && !(p.x.slices == 1 && p.x.first))) f.x.tiles = 0;
-        if (p.w.slices == 1) f.w.tiles = 0;
+        LossFinish f{p.x, p.w, p.N, p.v1 - p.v0, p.unit, p.D, L.cols4};
+        if (!p.x.last || p.x.direct) f.x.tiles = 0;
+        if (p.w.direct) f.w.tiles = 0;
         if (f.x.tiles + f.w.tiles > 0) e = launch_loss_finish(f, dt, s);
         if (e != cudaSuccess) return cuda_fail(e);
     }
@@ -536,7 +560,7 @@ int backward(const tbe_softmax_loss* h, const Plan& L, LossStep p, const RowsIn&
     cudaError_t e = launch_rows(h, L, rows, base, s);
     if (e != cudaSuccess) return cuda_fail(e);
     p.rows = at<float>(base, L.rows);
-    p.range = at<float>(base, L.range);
+    p.unit = at<float>(base, L.unit);
     p.row_tiles = (int)L.row_tiles;
     p.col_tiles = L.col_tiles;
     p.cols4 = L.cols4;
@@ -655,7 +679,7 @@ int tbe_softmax_loss_forward(tbe_softmax_loss* h, const void* x, int64_t x_strid
     if (workspace_bytes < tbe_softmax_loss_workspace_bytes(h, N, V, 0)) return TBE_ERR_WORKSPACE_TOO_SMALL;
     if (N == 0) return TBE_OK;
     LossForward p{};
-    p.N = N, p.V = V, p.D = h->c.dim, p.c2 = h->c.scale * kLog2e;
+    p.N = N, p.V = V, p.D = h->c.dim, p.c2 = argument_scale(h);
     p.targets = targets, p.index64 = index_dtype == TBE_I64, p.error = h->error;
     char* base = reinterpret_cast<char*>(align_up(reinterpret_cast<uintptr_t>(workspace)));
     return forward(h, make_plan(h, N, V, false, !direct(h, table, table_stride, V)), p, x, x_stride, table, table_stride, loss, lse, base,
@@ -685,11 +709,11 @@ int tbe_softmax_loss_backward(tbe_softmax_loss* h, const void* x, int64_t x_stri
     char* base = reinterpret_cast<char*>(align_up(reinterpret_cast<uintptr_t>(workspace)));
     if (takes_fused(h)) {
         LossFused p{};
-        p.N = N, p.V = V, p.D = h->c.dim, p.c2 = h->c.scale * kLog2e, p.error = h->error;
+        p.N = N, p.V = V, p.D = h->c.dim, p.c2 = argument_scale(h), p.error = h->error;
         return backward_fused(h, L, p, rows, table, table_stride, grad_x, grad_table, base, s);
     }
     LossStep p{};
-    p.N = N, p.V = V, p.D = h->c.dim, p.c2 = h->c.scale * kLog2e;
+    p.N = N, p.V = V, p.D = h->c.dim, p.c2 = argument_scale(h);
     p.gx = grad_x, p.gw = grad_table, p.error = h->error;
     return backward(h, L, p, rows, table, table_stride, base, s);
 }

@@ -19,7 +19,8 @@
 // those of the even tiles and eight those of the odd ones: a thread has one line
 // of S and half of its columns.  S and d are double buffered beside each other:
 // the scores after next are computed as soon as these are read.  fp32's three
-// planes of each operand lie in shared memory side by side, d's in tensor memory.
+// planes of each operand lie in shared memory side by side, d's in tensor memory
+// (one d: its products take longer than the next d).
 #include "loss_mma.cuh"
 
 namespace tbe {
@@ -37,25 +38,24 @@ struct Fused {
     static constexpr int kStats = 3 * BN * 4;  // bytes of a tile's rows' values
     static constexpr int ring = kHeld, stats = ring + kStages * kTile;
     static constexpr int bytes = stats + kStages * kStats + 1024;
-    // tensor memory: two S, two d (16-bit, plane by plane), the sums
-    static constexpr int d = 2 * BN, kD = P * BN / 2, sums = BN == 128 || P == 3 ? 384 : 256;
-    static_assert(d + 2 * kD <= sums && sums + DP <= 512, "");
+    // tensor memory: two S; two d (16-bit; fp32 one, of three planes); the sums
+    // (fp32: of the first planes' products, and 128 columns on of the others)
+    static constexpr int d = 2 * BN, kD = P == 3 ? 0 : BN / 2, sums = BN == 128 ? 384 : 256;
+    static_assert(d + (P == 3 ? 3 * BN / 2 : BN) <= sums && sums + (P == 3 ? 128 : 0) + DP <= 512, "");
 };
 
 struct FusedBars {
-    uint64_t held, full[6], empty[6], s_full[2], s_read[2], d_full[2], done[2], last;
+    uint64_t held, full[6], empty[6], s_full[2], s_read[2], d_full[2], done[2], last, sums_full, sums_free;
 };
 
 // 32 columns of the thread's line: x = S in, d out.
-template <bool ITEMS, int BN>
-__device__ __forceinline__ void gradients(float (&x)[32], float c2, float minus_lse2, float coef, int at, int left,
+template <int P, bool ITEMS, int BN>
+__device__ __forceinline__ void gradients(float (&x)[32], float c2, float minus_lse, float coef, int at, int left,
                                           const float* stats, int line) {
     if constexpr (!ITEMS) {
 #pragma unroll
         for (int c = 0; c < 32; c += 2) {
-            fma2(x[c], x[c + 1], c2, minus_lse2, minus_lse2);
-            x[c] = ex2(x[c]);
-            x[c + 1] = ex2(x[c + 1]);
+            powers<P>(x[c], x[c + 1], c2, minus_lse, minus_lse);
         }
         if (__any_sync(0xffffffffu, at >= 0 && at < 32)) {
 #pragma unroll
@@ -74,10 +74,8 @@ __device__ __forceinline__ void gradients(float (&x)[32], float c2, float minus_
 #pragma unroll
         for (int c = 0; c < 32; c += 4) {
             const float4 l = *reinterpret_cast<const float4*>(stats + c);
-            fma2(x[c], x[c + 1], c2, l.x, l.y);
-            fma2(x[c + 2], x[c + 3], c2, l.z, l.w);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[c + e] = ex2(x[c + e]);
+            powers<P>(x[c], x[c + 1], c2, l.x, l.y);
+            powers<P>(x[c + 2], x[c + 3], c2, l.z, l.w);
         }
         const int lane = threadIdx.x % 32;
         const int t = __float_as_int(stats[2 * BN + lane]) - (line - lane);  // among the warp's items?
@@ -93,6 +91,38 @@ __device__ __forceinline__ void gradients(float (&x)[32], float c2, float minus_
             const float4 g = *reinterpret_cast<const float4*>(stats + BN + c);
             mul2(x[c], x[c + 1], g.x, g.y);
             mul2(x[c + 2], x[c + 3], g.z, g.w);
+        }
+    }
+}
+
+// fp32's two sums of the thread's line, added (or, `first`, stored) to its row of
+// the result or to a slab as add_slab lays it out.
+__device__ __forceinline__ void put_fp32(float* out, float4* part, uint32_t acc, int wide, int group, bool valid, int D,
+                                         bool first) {
+    const bool vec = D % 4 == 0 && (uintptr_t)out % 16 == 0;
+    for (int c = group * 16; c < wide; c += 64) {
+        float x[16], y[16];
+        tmem_ld16_pair(acc + c, acc + 128 + c, x, y);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[e] += y[e];
+        if (!out || vec) {
+            float4* to = out ? reinterpret_cast<float4*>(out + c) : part + c / 4 * 128;
+            const int step = out ? 1 : 128;
+            float4 old[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                old[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (!first && (!out || (valid && c + 4 * q < D))) old[q] = to[q * step];
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (!out || (valid && c + 4 * q < D))
+                    to[q * step] = make_float4(x[4 * q] + old[q].x, x[4 * q + 1] + old[q].y, x[4 * q + 2] + old[q].z,
+                                               x[4 * q + 3] + old[q].w);
+        } else if (valid) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                if (c + e < D) out[c + e] = x[e] + (first ? 0.f : out[c + e]);
         }
     }
 }
@@ -196,6 +226,9 @@ __device__ __forceinline__ bool fused_body(const LossFused& p, const LossSide& s
             for (int i = 0; i < n && ok; ++i) {
                 const int st = i % kStages, buf = i & 1;
                 ok = wait(&bars.d_full[buf], i / 2);
+                // fp32: the sums begin anew every kFusedFlush tiles, once these are in memory
+                const bool begins = P == 3 ? i % kFusedFlush == 0 : i == 0;
+                if (ok && begins && i > 0) ok = wait(&bars.sums_free, i / kFusedFlush - 1);
                 if (!ok) break;
                 if (elect_one()) {
                     const uint64_t b = walk + (uint64_t)(st * (L::kTile / 16));
@@ -205,13 +238,17 @@ __device__ __forceinline__ bool fused_body(const LossFused& p, const LossSide& s
                         for (int pa = sum; pa >= 0; --pa)
 #pragma unroll
                             for (int k = 0; k < BN / 16; ++k)
-                                mma_f16_ts(tmem + L::sums, tmem + L::d + buf * L::kD + pa * (BN / 2) + k * 8,
+                                mma_f16_ts(tmem + L::sums + (sum > 0 ? 128 : 0),
+                                           tmem + L::d + buf * L::kD + pa * (BN / 2) + k * 8,
                                            b + (sum - pa) * (L::kTilePlane / 16) + k * (2048 / 16), idesc,
-                                           i > 0 || sum + 1 < P || pa < sum || k > 0);
+                                           !begins || (sum > 0 && (sum + 1 < P || pa < sum)) || k > 0);
                     // (the tile's scores are done with it: d was computed from them)
                     mma_commit(&bars.empty[st]);
                     mma_commit(&bars.done[buf]);
-                    if (i + 1 == n) mma_commit(&bars.last);
+                    if (i + 1 == n)
+                        mma_commit(&bars.last);
+                    else if (P == 3 && i % kFusedFlush == kFusedFlush - 1)
+                        mma_commit(&bars.sums_full);
                 }
                 __syncwarp();
             }
@@ -222,14 +259,42 @@ __device__ __forceinline__ bool fused_body(const LossFused& p, const LossSide& s
         // ---- d, then the sums
         const int quarter = warp % 4, group = warp / 4 % 2, buf = warp / 8, line = quarter * 32 + lane;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-        float minus_lse2 = 0.f, coef = 0.f;
+        float minus_lse = 0.f, coef = 0.f;
         int target = -1;
         if constexpr (!ITEMS) {
             const float* r = p.rows + (int64_t)tile * kRowValues + line;
-            minus_lse2 = __ldg(r);
+            minus_lse = __ldg(r);
             coef = __ldg(r + 128);
             target = __float_as_int(__ldg(r + 256));
         }
+        const uint32_t acc = tmem + L::sums + lanes;
+        const int wide = (p.D + 15) / 16 * 16;
+        const int64_t row = (int64_t)tile * 128 + line;
+        const float unit = __ldg(p.unit);
+        int flushed = 0;
+        auto put = [&]() {
+            const bool first = side.first && flushed == 0;
+            const bool valid = row < (ITEMS ? p.v1 - p.v0 : p.N);
+            float4* part = side.part + ((int64_t)slice * side.tiles + tile) * p.cols4 * 128 + line;
+            if constexpr (P == 3)
+                put_fp32(side.direct ? static_cast<float*>(side.out) + row * p.D : nullptr, part, acc, wide, warp / 4,
+                         valid, p.D, first);
+            else if (side.direct)
+                store_rows<DT, 4>(side.out, row * p.D, acc, wide, warp / 4, valid, p.D, p.D % 8 == 0, unit);
+            else
+                add_slab<4>(part, acc, wide, warp / 4, first);
+            ++flushed;
+        };
+        auto flush = [&]() {
+            ok = mbar_wait_tight(&bars.sums_full, flushed & 1);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) return;
+            tcgen05_after_sync();
+            put();
+            tcgen05_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.sums_free);
+        };
         // the first tile's first item of the thread's half (V < 2^31)
         const int item0 = (int)(p.v0 + (int64_t)(from + buf) * BN) + group * (BN / 2);
         int left = (int)p.v1 - item0, at = target - item0, st = buf;
@@ -237,6 +302,11 @@ __device__ __forceinline__ bool fused_body(const LossFused& p, const LossSide& s
         const int mine = (int)(p.v0 + (int64_t)tile * 128) + line;
 #pragma unroll 1
         for (int i = buf; i < n; i += 2, left -= 2 * BN, at -= 2 * BN) {
+            // (before this tile's d, whose place the product behind the flush frees)
+            if (P == 3 && i / kFusedFlush > flushed) {
+                flush();
+                if (!ok) break;
+            }
             ok = mbar_wait_tight(&bars.s_full[buf], (i / 2) & 1);
             if (ITEMS && ok) ok = mbar_wait_tight(&bars.full[st], (i / kStages) & 1);  // the rows' values
             if (!__all_sync(0xffffffffu, ok)) {
@@ -256,9 +326,11 @@ __device__ __forceinline__ bool fused_body(const LossFused& p, const LossSide& s
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bars.s_read[buf]);
                 }
-                gradients<ITEMS, BN>(x, p.c2, minus_lse2, coef, at - h, left - h, stats + h, mine);
-                if (h == 0 && i >= 2) {  // d's columns are free of the product before last
-                    ok = mbar_wait_tight(&bars.done[buf], (i / 2 - 1) & 1);
+                gradients<P, ITEMS, BN>(x, p.c2, minus_lse, coef, at - h, left - h, stats + h, mine);
+                // d's columns are free of the last but one product (fp32: of the last)
+                if (h == 0 && (P == 3 ? i >= 1 : i >= 2)) {
+                    ok = P == 3 ? mbar_wait_tight(&bars.done[buf ^ 1], ((i - 1) / 2) & 1)
+                                : mbar_wait_tight(&bars.done[buf], (i / 2 - 1) & 1);
                     ok = __all_sync(0xffffffffu, ok);
                     tcgen05_after_sync();
                 }
@@ -282,20 +354,14 @@ __device__ __forceinline__ bool fused_body(const LossFused& p, const LossSide& s
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars.d_full[buf]);
         }
+        if (P == 3)
+            while (ok && (n - 1) / kFusedFlush > flushed) flush();
         // (a barrier of its own: `done` of the other buffer may be two phases back)
         if (ok) ok = mbar_wait_tight(&bars.last, 0);
         ok = __all_sync(0xffffffffu, ok);
         if (ok) {
             tcgen05_after_sync();
-            const uint32_t acc = tmem + L::sums + lanes;
-            const int wide = (p.D + 15) / 16 * 16;
-            const int64_t row = (int64_t)tile * 128 + line;
-            if (side.slices == 1 && side.first && side.last)
-                store_rows<P == 3 ? DT_F32 : DT, 4>(side.out, row * p.D, acc, wide, warp / 4, row < (ITEMS ? p.v1 - p.v0 : p.N), p.D,
-                                  p.D % 8 == 0, 1.f / __ldg(p.range));
-            else
-                add_slab<4>(side.part + ((int64_t)slice * side.tiles + tile) * p.cols4 * 128 + line, acc, wide, warp / 4,
-                            side.first);
+            put();
         }
     }
     return ok;
@@ -312,6 +378,8 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
     if (threadIdx.x == 0) {
         mbar_init(&bars.held, 1);
         mbar_init(&bars.last, 1);
+        mbar_init(&bars.sums_full, 1);
+        mbar_init(&bars.sums_free, 16);
         for (int i = 0; i < Fused<DP, P>::kStages; ++i) {
             mbar_init(&bars.full[i], 1);
             mbar_init(&bars.empty[i], 1);
@@ -351,7 +419,7 @@ __global__ void __launch_bounds__(256) loss_finish_kernel(const LossFinish p) {
     if (!x) tile -= p.x.tiles;
     finish<OUT>(side.part + (int64_t)tile * p.cols4 * 128, (int64_t)side.tiles * p.cols4 * 128, side.slices, side.out,
                 (int64_t)tile * 128, (int)tmin<int64_t>(128, (x ? p.x_rows : p.w_rows) - (int64_t)tile * 128), p.D,
-                (int)(blockIdx.x % blocks) * 32, 1.f / __ldg(p.range), threadIdx.x);
+                (int)(blockIdx.x % blocks) * 32, __ldg(p.unit), threadIdx.x);
 }
 
 template <int DT, int DP, int P>

@@ -31,17 +31,19 @@ struct Product {
     int wide;
     int slab;
     int last_steps;  // scores: steps of 16 columns in the last block
+    bool begins;     // a sum's first part
 };
 
 __device__ __forceinline__ int columns_of(int64_t left) { return (int)tmin<int64_t>(256, (left + 15) / 16 * 16); }
 
 __device__ __forceinline__ Product score_tile(int64_t V, int D, int row0, int64_t item) {
-    return Product{ITEM_D, row0, item, 0, (D + 63) / 64, columns_of(V - item), 0, ((D - 1) % 64 + 16) / 16};
+    return Product{ITEM_D, row0, item, 0, (D + 63) / 64, columns_of(V - item), 0, ((D - 1) % 64 + 16) / 16, true};
 }
 
 // Work item i of a backward launch: the long ones first.
 __device__ __forceinline__ Product step_item(const LossStep& p, int i) {
     Product t{};
+    t.begins = true;
     if (i < p.n_gw) {
         const int tiles = (p.p_items + 127) / 128, blocks = (int)((p.N + 63) / 64);
         const int tile = i % tiles, rest = i / tiles, ct = rest % p.col_tiles;
@@ -81,9 +83,9 @@ __device__ __forceinline__ Product step_item(const LossStep& p, int i) {
 // The operands' way through shared memory.  One plane: stages of a tile of A (2
 // boxes) and of B (4).  fp32's three: A's planes of a block stay for the block's
 // six products, twice 3 tiles; B's planes pass in three stages, each meeting the
-// planes of A that matter beside it.  That is 144 KB for what 288 KB of single
-// products would be: at 2 x 96 bytes a cycle and SM the L2 cache's reads bounded
-// fp32's passes.
+// planes of A that matter beside it; the first planes come once more for the
+// large products.  That is 192 KB for what 288 KB of single products would be (the
+// L2 cache's reads bound fp32's passes).
 template <int P>
 struct Ring {
     static constexpr int kStages = P == 3 ? 3 : 4;
@@ -123,34 +125,37 @@ __device__ bool produce(unsigned char* smem, LossBars& bars, const LossMaps& map
                 else
                     load_box(b + j * kBox, maps.x, (int)t.col0 + j * 64, k, plane, bar);
         };
-        for (int s = 0; s < t.kblocks && ok; ++s) {
-            const int k = (t.k0 + s) * 64;
-            if constexpr (P == 3) {
-                const int ab = blocks & 1;
-                if (blocks >= 2) ok = mbar_wait_tight(&bars.a_empty[ab], (blocks / 2 - 1) & 1);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                if (elect_one()) {
-                    mbar_expect_tx(&bars.a_full[ab], 3 * 2 * kBox);
-                    for (int plane = 0; plane < 3; ++plane)
-                        load_a(base + (ab * 3 + plane) * 2 * kBox, k, plane, &bars.a_full[ab]);
+        // (P = 3: a pass for the small products and one for the large)
+        for (int pass = P == 3 ? 0 : 1; pass < 2 && ok; ++pass)
+            for (int s = 0; s < t.kblocks && ok; ++s) {
+                const int k = (t.k0 + s) * 64;
+                if constexpr (P == 3) {
+                    const int ab = blocks & 1;
+                    if (blocks >= 2) ok = mbar_wait_tight(&bars.a_empty[ab], (blocks / 2 - 1) & 1);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    if (elect_one()) {
+                        const int planes = pass == 0 ? 3 : 1;
+                        mbar_expect_tx(&bars.a_full[ab], planes * 2 * kBox);
+                        for (int plane = 0; plane < planes; ++plane)
+                            load_a(base + (ab * 3 + plane) * 2 * kBox, k, plane, &bars.a_full[ab]);
+                    }
+                    __syncwarp();
+                    ++blocks;
                 }
-                __syncwarp();
-                ++blocks;
-            }
-            for (int plane = P - 1; plane >= 0 && ok; --plane, ++n) {
-                const int st = n % R::kStages;
-                if (n >= R::kStages) ok = mbar_wait_tight(&bars.empty[st], (n / R::kStages - 1) & 1);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                if (elect_one()) {
-                    mbar_expect_tx(&bars.full[st], ((P == 3 ? 0 : 2) + slabs) * kBox);
-                    if constexpr (P == 1) load_a(base + st * R::kStage, k, 0, &bars.full[st]);
-                    load_b(base + R::b + st * R::kStage, k, plane, &bars.full[st]);
+                for (int plane = pass == 0 ? 2 : 0; plane >= 0 && ok; --plane, ++n) {
+                    const int st = n % R::kStages;
+                    if (n >= R::kStages) ok = mbar_wait_tight(&bars.empty[st], (n / R::kStages - 1) & 1);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    if (elect_one()) {
+                        mbar_expect_tx(&bars.full[st], ((P == 3 ? 0 : 2) + slabs) * kBox);
+                        if constexpr (P == 1) load_a(base + st * R::kStage, k, 0, &bars.full[st]);
+                        load_b(base + R::b + st * R::kStage, k, plane, &bars.full[st]);
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
             }
-        }
     }
     // where a wait ran out: this CTA's copies in flight land before it ends
     if (!ok) {
@@ -184,36 +189,38 @@ __device__ bool multiply(unsigned char* smem, LossBars& bars, uint32_t tmem, Nex
         const uint64_t da = a_mn ? smem_desc_mn(base, kBox) : smem_desc_sw128(base, 1024);
         const uint64_t db = b_mn ? smem_desc_mn(base + R::b, kBox) : smem_desc_sw128(base + R::b, 1024);
         const int ka = a_mn ? 2048 / 16 : 2, kb = b_mn ? 2048 / 16 : 2;
-        for (int s = 0; s < t.kblocks && ok; ++s) {
-            const int steps = t.kind == ITEM_D && s + 1 == t.kblocks ? t.last_steps : 4;  // of 16 along the sum
-            const int ab = blocks & 1;
-            if constexpr (P == 3) {
-                ok = wait(&bars.a_full[ab], blocks / 2);
-                ++blocks;
-            }
-            for (int plane = P - 1; plane >= 0 && ok; --plane, ++n) {
-                const int st = n % R::kStages;
-                ok = wait(&bars.full[st], n / R::kStages);
-                if (!ok) break;
-                if (elect_one()) {
-                    const uint64_t b = db + (uint64_t)(st * (R::kStage / 16));
-                    for (int pa = P - 1 - plane; pa >= 0; --pa) {
-                        const uint64_t a = da + (uint64_t)(P == 3 ? (ab * 3 + pa) * (2 * kBox / 16) : st * (R::kStage / 16));
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            if (k < steps)
-                                mma_f16(tmem + buf * 256, a + k * ka, b + k * kb, idesc,
-                                        s > 0 || plane + 1 < P || pa + 1 + plane < P || k > 0);
-                    }
-                    mma_commit(&bars.empty[st]);
-                    if (plane == 0) {
-                        if constexpr (P == 3) mma_commit(&bars.a_empty[ab]);
-                        if (s + 1 == t.kblocks) mma_commit(&bars.acc_full[buf]);
-                    }
+        for (int pass = P == 3 ? 0 : 1; pass < 2 && ok; ++pass)
+            for (int s = 0; s < t.kblocks && ok; ++s) {
+                const int steps = t.kind == ITEM_D && s + 1 == t.kblocks ? t.last_steps : 4;  // of 16 along the sum
+                const int ab = blocks & 1;
+                if constexpr (P == 3) {
+                    ok = wait(&bars.a_full[ab], blocks / 2);
+                    ++blocks;
                 }
-                __syncwarp();
+                for (int plane = pass == 0 ? 2 : 0; plane >= 0 && ok; --plane, ++n) {
+                    const int st = n % R::kStages;
+                    ok = wait(&bars.full[st], n / R::kStages);
+                    if (!ok) break;
+                    if (elect_one()) {
+                        const uint64_t b = db + (uint64_t)(st * (R::kStage / 16));
+                        // A's planes that matter beside this one of B; the first ones' product comes last
+                        for (int pa = pass == 0 ? 2 - plane : 0; pa >= (pass == 0 && plane == 0 ? 1 : 0); --pa) {
+                            const uint64_t a =
+                                da + (uint64_t)(P == 3 ? (ab * 3 + pa) * (2 * kBox / 16) : st * (R::kStage / 16));
+                            const bool begins = s == 0 && (P == 1 || (pass == 0 && plane == 2));
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                if (k < steps) mma_f16(tmem + buf * 256, a + k * ka, b + k * kb, idesc, !begins || k > 0);
+                        }
+                        mma_commit(&bars.empty[st]);
+                        if (plane == 0) {
+                            if constexpr (P == 3) mma_commit(&bars.a_empty[ab]);
+                            if (pass == 1 && s + 1 == t.kblocks) mma_commit(&bars.acc_full[buf]);
+                        }
+                    }
+                    __syncwarp();
+                }
             }
-        }
         ++tile;
     }
     // nothing of this CTA arrives on a barrier after its end
@@ -233,14 +240,12 @@ __device__ __forceinline__ void stage_row(unsigned char* staging, int lane, int 
 
 // d of the warp's 32 rows and one of its two slabs of 64 items.
 template <int DT, int P>
-__device__ __forceinline__ void d_slab(float* x, float minus_lse2, float coef, int target, float c2, int64_t item0, int64_t V,
+__device__ __forceinline__ void d_slab(float* x, float minus_lse, float coef, int target, float c2, int64_t item0, int64_t V,
                                        unsigned char* staging, const CUtensorMap& map, int col, int row, int64_t rows,
                                        int lane) {
 #pragma unroll
     for (int c = 0; c < 64; c += 2) {
-        fma2(x[c], x[c + 1], c2, minus_lse2, minus_lse2);
-        x[c] = ex2(x[c]);
-        x[c + 1] = ex2(x[c + 1]);
+        powers<P>(x[c], x[c + 1], c2, minus_lse, minus_lse);
     }
     const int at = (int)tmin<int64_t>(tmax<int64_t>(target - item0, -1), 64);  // (target -1: before any item)
     if (__any_sync(0xffffffffu, at >= 0 && at < 64)) {
@@ -327,9 +332,17 @@ __global__ void __launch_bounds__(kLossThreads, 1)
     const int products = p.n_gw + p.n_gx, results = products + p.n_d, n_items = results + p.n_fin_w + p.n_fin_x;
     int a = blockIdx.x, b = products + p.d_from[blockIdx.x], f = results + blockIdx.x;
     const int b_end = products + p.d_from[blockIdx.x + 1];
+    int rest = 0;  // blocks of the item that are still to come (fp32: its sum goes to memory in parts)
     auto next = [&](Product& t) {
         for (;;) {
             int i;
+            if (P == 3 && rest > 0) {
+                t.k0 += t.kblocks;
+                t.kblocks = tmin(rest, kFlush);
+                t.begins = false;
+                rest -= t.kblocks;
+                return true;
+            }
             if (a < products) {
                 i = a;
                 a += gridDim.x;
@@ -342,7 +355,13 @@ __global__ void __launch_bounds__(kLossThreads, 1)
                 return false;
             }
             t = step_item(p, i);
-            if (t.kind > ITEM_GX || t.kblocks > 0) return true;  // (the last piece has fewer blocks than slabs)
+            if (t.kind > ITEM_GX) return true;
+            if (t.kblocks == 0) continue;  // (the last piece has fewer blocks than slabs)
+            if (P == 3) {
+                rest = tmax(0, t.kblocks - kFlush);
+                t.kblocks -= rest;
+            }
+            return true;
         }
     };
     bool ok = true;
@@ -354,7 +373,7 @@ __global__ void __launch_bounds__(kLossThreads, 1)
         constexpr int OUT = P == 3 ? DT_F32 : DT;
         unsigned char* staging = smem + kLossStages * kStageBytes + warp * kStagingBytes;
         const int quarter = warp % 4, group = warp / 4;
-        const float down = 1.f / __ldg(p.range);
+        const float unit = __ldg(p.unit);
         int tile = 0;
         Product t;
         while (next(t)) {
@@ -364,15 +383,15 @@ __global__ void __launch_bounds__(kLossThreads, 1)
                 finish<OUT>((w ? p.f_part : p.x_part) + (int64_t)(t.row0 / 128) * p.cols4 * 128,
                             (int64_t)tiles * p.cols4 * 128, w ? p.w_slabs : p.x_slabs, w ? p.gw : p.gx,
                             (w ? p.f0 : 0) + t.row0, (int)tmin<int64_t>(128, (w ? p.f_items : p.N) - t.row0), p.D,
-                            (int)t.col0, down, threadIdx.x);
+                            (int)t.col0, unit, threadIdx.x);
                 continue;
             }
             const int buf = tile & 1;
-            float minus_lse2 = 0.f, coef = 0.f;
+            float minus_lse = 0.f, coef = 0.f;
             int target = -1;
             if (t.kind == ITEM_D) {
                 const float* r = p.rows + (int64_t)(t.row0 / 128) * kRowValues + quarter * 32 + lane;
-                minus_lse2 = __ldg(r);
+                minus_lse = __ldg(r);
                 coef = __ldg(r + 128);
                 target = __float_as_int(__ldg(r + 256));
             }
@@ -390,19 +409,19 @@ __global__ void __launch_bounds__(kLossThreads, 1)
                     tmem_ld32_issue(acc + c, x);
                     tmem_ld32_issue(acc + c + 32, x + 32);
                     tmem_wait_ld(x, 64);
-                    d_slab<DT, P>(x, minus_lse2, coef, target, p.c2, t.col0 + c, p.V, staging, maps.d_out, (int)(t.col0 - p.d0) + c,
+                    d_slab<DT, P>(x, minus_lse, coef, target, p.c2, t.col0 + c, p.V, staging, maps.d_out, (int)(t.col0 - p.d0) + c,
                                   t.row0 + quarter * 32, p.N, lane);
                 }
             } else if (t.kind == ITEM_GW && p.w_slabs == 1) {
                 const int r = t.row0 + quarter * 32 + lane;
                 store_rows<OUT, 2>(p.gw, (p.p0 + r) * p.D + t.col0, acc, t.wide, group, r < p.p_items,
-                                (int)(p.D - t.col0), p.D % 8 == 0, down);
+                                (int)(p.D - t.col0), p.D % 8 == 0, unit, !t.begins);
             } else {
                 const int tiles = t.kind == ITEM_GX ? p.row_tiles : (p.p_items + 127) / 128;
                 float4* to = (t.kind == ITEM_GX ? p.x_part : p.w_part) +
                              ((int64_t)t.slab * tiles + t.row0 / 128) * p.cols4 * 128 + t.col0 / 4 * 128 +
                              quarter * 32 + lane;
-                add_slab<2>(to, acc, t.wide, group, t.kind == ITEM_GW || p.first);
+                add_slab<2>(to, acc, t.wide, group, t.begins && (t.kind == ITEM_GW || p.first));
             }
             tcgen05_before_sync();
             __syncwarp();
@@ -503,14 +522,14 @@ __global__ void __launch_bounds__(kForwardThreads, 1)
                     const float top = fmaxf(max3(max3(u[0], u[1], u[2]), u[3], u[4]), max3(u[5], u[6], u[7])) * p.c2;
                     if (__any_sync(0xffffffffu, top > m + kLazyMax)) {
                         const float to = fmaxf(m, top);
-                        l *= ex2(m - to);  // (m = -inf: 0)
+                        l *= ex2(P == 3 ? (m - to) * kLog2e : m - to);  // (m = -inf: 0)
                         m = to;
                     }
                     float s0 = 0.f, s1 = 0.f;
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
-                        fma2(x[e], x[e + 1], p.c2, -m, -m);
-                        add2(s0, s1, ex2(x[e]), ex2(x[e + 1]));
+                        powers<P>(x[e], x[e + 1], p.c2, -m, -m);
+                        add2(s0, s1, x[e], x[e + 1]);
                     }
                     l += s0 + s1;
                 };

@@ -15,8 +15,12 @@
 // fp32.  An fp32 number is the sum of three bf16 numbers exactly (8 bits each,
 // rounded to nearest, the rest carried on).  fp32 operands are kept as three
 // such planes, and a product is the sum of the six plane products of at least
-// 2^-18 of the whole; the three left out are below 2^-26, less than an fp32
-// rounding.
+// 2^-18 of the whole, the small ones first; the three left out are below 2^-26,
+// less than an fp32 rounding.  The tensor units cut an fp32 sum at every addition
+// instead of rounding it, so long sums drift: 20,011 items in one accumulator
+// made grad_x 2.2e-5 off.  fp32's large products (of the first planes) therefore
+// come last or have an accumulator of their own, which is added, rounded, to a sum
+// in memory every kFlush (fused: kFusedFlush) blocks of 64 along the sum.
 #pragma once
 
 #include <cuda.h>
@@ -71,10 +75,11 @@ __device__ __forceinline__ void add_slab(float4* to, uint32_t acc, int wide, int
 }
 
 // The same chunks, times `times`, as columns of the thread's row of a result
-// that starts at element `at` and has `left` columns.
+// that starts at element `at` and has `left` columns; added to an fp32 result
+// where `add` says so.
 template <int OUT, int GROUPS>
 __device__ __forceinline__ void store_rows(void* out, int64_t at, uint32_t acc, int wide, int group, bool valid,
-                                           int left, bool vec, float times) {
+                                           int left, bool vec, float times, bool add = false) {
     vec = vec && (uintptr_t)out % 16 == 0;
     for (int c = group * 32; c < wide; c += 32 * GROUPS) {
         float x[32];
@@ -83,6 +88,12 @@ __device__ __forceinline__ void store_rows(void* out, int64_t at, uint32_t acc, 
         if (!valid) continue;
 #pragma unroll
         for (int e = 0; e < 32; ++e) x[e] *= times;
+        if (OUT == DT_F32 && add) {
+            const float* old = static_cast<const float*>(out) + at + c;
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+                if (c + e < left) x[e] += old[e];
+        }
         if (vec) {
 #pragma unroll
             for (int e = 0; e < 32; e += 8) {
@@ -137,6 +148,7 @@ __device__ __forceinline__ void finish(const float4* part, int64_t slab_stride, 
 
 constexpr int kLossThreads = 320;
 constexpr int kLossStages = 4;
+constexpr int kFlush = 8, kFusedFlush = 16;
 constexpr int kBox = 64 * 64 * 2;  // bytes of a TMA box: 64 columns x 64 rows
 constexpr int kStageBytes = 6 * kBox;  // A: 2 boxes, B: 4
 constexpr int kStagingBytes = 4096;    // of a warp: 32 rows x 64 columns of d
@@ -144,8 +156,20 @@ constexpr int kLossSmem = kLossStages * kStageBytes + 8 * kStagingBytes + 1024;
 
 enum : int32_t { ITEM_GW = 0, ITEM_GX = 1, ITEM_D = 2, ITEM_FIN_W = 3, ITEM_FIN_X = 4 };
 
+// The softmax's arguments.  16-bit types work in base 2 (one multiply-add before
+// ex2).  fp32 takes the difference to lse (or to the maximum) in natural units and
+// multiplies then: rounding lse log2(e) would move a whole row by 2^-24 of it,
+// 1e-6 at a lse of 14, which is more than the rest of fp32's errors.
+template <int P>
+__device__ __forceinline__ void powers(float& a, float& b, float scale, float less_a, float less_b) {
+    fma2(a, b, scale, less_a, less_b);
+    if (P == 3) mul2(a, b, kLog2e, kLog2e);
+    a = ex2(a);
+    b = ex2(b);
+}
+
 // What the rows bring into the backward pass: per tile of 128 rows 128 values
-// each of -lse log2(e), of g * scale (times a power of two with fp16) and of the
+// each of -lse (times log2(e) but for fp32), of g * scale (16-bit types: over its `unit`) and of the
 // target as an int32; 0, 0 and -1 in rows that are left out or behind the last.
 constexpr int kRowValues = 3 * 128;
 
@@ -154,12 +178,12 @@ struct LossForward {
     int64_t w0;         // the item at the table map's first row
     int32_t D, row_tiles, item_tiles, slices;
     int32_t first;  // else the sums go on from `part`
-    float c2;       // scale * log2(e)
+    float c2;       // scale, times log2(e) but for fp32
     const void* targets;
     int32_t index64;
     int64_t V;
-    float2* part;   // [N][slices][4]: maximum and sum (base 2) of a quarter of a slice's columns
-    float* picked;  // [N]: the target's logit (base 2)
+    float2* part;   // [N][slices][4]: maximum and sum of a quarter of a slice's columns
+    float* picked;  // [N]: the target's logit
     uint32_t* error;
 };
 
@@ -173,7 +197,7 @@ struct LossStep {
     int32_t D, row_tiles, col_tiles;  // col_tiles: of 256 columns
     float c2;
     const float* rows;   // [row_tiles][kRowValues]
-    const float* range;  // the power of two in the rows' second values
+    const float* unit;   // what the rows' second values are taken relative to
     // d of the items from d0 on, its work items d_from[c] .. d_from[c + 1] by CTA c
     int32_t n_d;
     int32_t d_from[kMaxStepCtas + 1];
@@ -206,7 +230,8 @@ struct LossMaps {
 struct LossSide {
     int32_t tiles, others, slices;
     int32_t first, last;  // over spans of the table: the sums begin, end here
-    float4* part;         // [slices][tiles][cols4][128]; a whole sum goes to `out` at once
+    int32_t direct;       // a CTA's sums are the result's (fp32: are added there)
+    float4* part;         // [slices][tiles][cols4][128] else
     void* out;
 };
 
@@ -217,7 +242,7 @@ struct LossFused {
     int64_t w0;            // the item at the table map's first row
     int32_t D, cols4;
     float c2;
-    const float *rows, *range;
+    const float *rows, *unit;
     LossSide x, w;
     uint32_t* error;
 };
@@ -230,7 +255,7 @@ struct LossFusedMaps {
 struct LossFinish {
     LossSide x, w;  // tiles 0: nothing to do
     int64_t x_rows, w_rows;
-    const float* range;
+    const float* unit;
     int32_t D, cols4;
 };
 
