@@ -94,6 +94,18 @@ struct Ring {
 };
 static_assert(Ring<3>::b + Ring<3>::kStages * Ring<3>::kStage <= kLossStages * kStageBytes, "");
 
+// fp32's passes over a sum: the small products, then the large; both at once
+// where the sum is one block.
+enum : int { kSmall = 0, kLarge = 1, kBoth = 2 };
+template <int P>
+__device__ __forceinline__ int first_pass(const Product& t) {
+    return P == 1 ? kLarge : t.kblocks == 1 ? kBoth : kSmall;
+}
+template <int P>
+__device__ __forceinline__ int last_pass(const Product& t) {
+    return P == 3 && t.kblocks == 1 ? kBoth : kLarge;
+}
+
 template <int P, typename Next>
 __device__ bool produce(unsigned char* smem, LossBars& bars, const LossMaps& maps, int64_t w0, int64_t p_row, Next next) {
     using R = Ring<P>;
@@ -125,8 +137,7 @@ __device__ bool produce(unsigned char* smem, LossBars& bars, const LossMaps& map
                 else
                     load_box(b + j * kBox, maps.x, (int)t.col0 + j * 64, k, plane, bar);
         };
-        // (P = 3: a pass for the small products and one for the large)
-        for (int pass = P == 3 ? 0 : 1; pass < 2 && ok; ++pass)
+        for (int pass = first_pass<P>(t); pass <= last_pass<P>(t) && ok; ++pass)
             for (int s = 0; s < t.kblocks && ok; ++s) {
                 const int k = (t.k0 + s) * 64;
                 if constexpr (P == 3) {
@@ -135,7 +146,7 @@ __device__ bool produce(unsigned char* smem, LossBars& bars, const LossMaps& map
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     if (elect_one()) {
-                        const int planes = pass == 0 ? 3 : 1;
+                        const int planes = pass == kLarge ? 1 : 3;
                         mbar_expect_tx(&bars.a_full[ab], planes * 2 * kBox);
                         for (int plane = 0; plane < planes; ++plane)
                             load_a(base + (ab * 3 + plane) * 2 * kBox, k, plane, &bars.a_full[ab]);
@@ -143,7 +154,7 @@ __device__ bool produce(unsigned char* smem, LossBars& bars, const LossMaps& map
                     __syncwarp();
                     ++blocks;
                 }
-                for (int plane = pass == 0 ? 2 : 0; plane >= 0 && ok; --plane, ++n) {
+                for (int plane = pass == kLarge ? 0 : 2; plane >= 0 && ok; --plane, ++n) {
                     const int st = n % R::kStages;
                     if (n >= R::kStages) ok = mbar_wait_tight(&bars.empty[st], (n / R::kStages - 1) & 1);
                     ok = __all_sync(0xffffffffu, ok);
@@ -189,7 +200,7 @@ __device__ bool multiply(unsigned char* smem, LossBars& bars, uint32_t tmem, Nex
         const uint64_t da = a_mn ? smem_desc_mn(base, kBox) : smem_desc_sw128(base, 1024);
         const uint64_t db = b_mn ? smem_desc_mn(base + R::b, kBox) : smem_desc_sw128(base + R::b, 1024);
         const int ka = a_mn ? 2048 / 16 : 2, kb = b_mn ? 2048 / 16 : 2;
-        for (int pass = P == 3 ? 0 : 1; pass < 2 && ok; ++pass)
+        for (int pass = first_pass<P>(t); pass <= last_pass<P>(t) && ok; ++pass)
             for (int s = 0; s < t.kblocks && ok; ++s) {
                 const int steps = t.kind == ITEM_D && s + 1 == t.kblocks ? t.last_steps : 4;  // of 16 along the sum
                 const int ab = blocks & 1;
@@ -197,17 +208,17 @@ __device__ bool multiply(unsigned char* smem, LossBars& bars, uint32_t tmem, Nex
                     ok = wait(&bars.a_full[ab], blocks / 2);
                     ++blocks;
                 }
-                for (int plane = pass == 0 ? 2 : 0; plane >= 0 && ok; --plane, ++n) {
+                for (int plane = pass == kLarge ? 0 : 2; plane >= 0 && ok; --plane, ++n) {
                     const int st = n % R::kStages;
                     ok = wait(&bars.full[st], n / R::kStages);
                     if (!ok) break;
                     if (elect_one()) {
                         const uint64_t b = db + (uint64_t)(st * (R::kStage / 16));
                         // A's planes that matter beside this one of B; the first ones' product comes last
-                        for (int pa = pass == 0 ? 2 - plane : 0; pa >= (pass == 0 && plane == 0 ? 1 : 0); --pa) {
+                        for (int pa = pass == kLarge ? 0 : 2 - plane; pa >= (pass == kSmall && plane == 0 ? 1 : 0); --pa) {
                             const uint64_t a =
                                 da + (uint64_t)(P == 3 ? (ab * 3 + pa) * (2 * kBox / 16) : st * (R::kStage / 16));
-                            const bool begins = s == 0 && (P == 1 || (pass == 0 && plane == 2));
+                            const bool begins = s == 0 && (P == 1 || (pass != kLarge && plane == 2));
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
                                 if (k < steps) mma_f16(tmem + buf * 256, a + k * ka, b + k * kb, idesc, !begins || k > 0);
@@ -215,7 +226,7 @@ __device__ bool multiply(unsigned char* smem, LossBars& bars, uint32_t tmem, Nex
                         mma_commit(&bars.empty[st]);
                         if (plane == 0) {
                             if constexpr (P == 3) mma_commit(&bars.a_empty[ab]);
-                            if (pass == 1 && s + 1 == t.kblocks) mma_commit(&bars.acc_full[buf]);
+                            if (pass != kSmall && s + 1 == t.kblocks) mma_commit(&bars.acc_full[buf]);
                         }
                     }
                     __syncwarp();
