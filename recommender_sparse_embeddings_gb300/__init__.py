@@ -744,6 +744,15 @@ def _matrix(t: torch.Tensor, rows: int, dim: int, dtype, name: str):
     return t.data_ptr(), s0
 
 
+def _result(t: Optional[torch.Tensor], shape, dtype, like: torch.Tensor, stream, name: str):
+    """(tensor, address) of a result: the caller's, or memory of the call's own
+    beside ``like``."""
+    if t is None:
+        t = _new(shape, dtype, like.device, stream)
+        return t, t.data_ptr()
+    return t, _packed(t, shape, dtype, name)
+
+
 def _param(t: Optional[torch.Tensor], has: bool, dim: int, dtype, name: str):
     if (t is not None) != has:
         raise ValueError(f"{name} must be given exactly where the handle has one")
@@ -762,21 +771,16 @@ def tbe_layer_norm_forward(h: LayerNormHandle, x: torch.Tensor, weight: Optional
     n, d, dt = x.shape[0], h.dim, h.dtype
     px, sx = _matrix(x, n, d, dt, "x")
     pr, sr, pt = None, 0, None
-    if out is None:
-        out = _new((n, d), dt, x.device, stream)
-    if stats is None:
-        stats = _new((2, n), torch.float32, x.device, stream)
+    pw, pb = _param(weight, h.weight, d, dt, "weight"), _param(bias, h.bias, d, dt, "bias")
+    _on_device(h, x, residual, weight, bias, out, total, stats)
+    out, po = _result(out, (n, d), dt, x, stream, "out")
+    stats, ps = _result(stats, (2, n), torch.float32, x, stream, "stats")
     if residual is not None:
         pr, sr = _matrix(residual, n, d, dt, "residual")
-        if total is None:
-            total = _new((n, d), dt, x.device, stream)
-        pt = _packed(total, (n, d), dt, "total")
+        total, pt = _result(total, (n, d), dt, x, stream, "total")
     elif total is not None:
         raise ValueError("total without residual")
-    _on_device(h, x, residual, weight, bias, out, total, stats)
-    rc = load_library().tbe_layer_norm_forward(
-        h.ptr, px, sx, pr, sr, _param(weight, h.weight, d, dt, "weight"), _param(bias, h.bias, d, dt, "bias"), n,
-        _packed(out, (n, d), dt, "out"), pt, _packed(stats, (2, n), torch.float32, "stats"), _stream(stream))
+    rc = load_library().tbe_layer_norm_forward(h.ptr, px, sx, pr, sr, pw, pb, n, po, pt, ps, _stream(stream))
     _check(rc, "tbe_layer_norm_forward")
     return out, x if residual is None else total, stats
 
@@ -809,20 +813,22 @@ def tbe_layer_norm_backward(h: LayerNormHandle, total: torch.Tensor, stats: torc
     pt, st = _matrix(total, n, d, dt, "total")
     pg, sg = _matrix(grad_out, n, d, dt, "grad_out")
     pu, su = (None, 0) if grad_total is None else _matrix(grad_total, n, d, dt, "grad_total")
-    if grad_x is None:
-        grad_x = _new((n, d), dt, total.device, stream)
-    if grad_weight is None and h.weight:
-        grad_weight = _new((d,), dt, total.device, stream)
-    if grad_bias is None and h.bias:
-        grad_bias = _new((d,), dt, total.device, stream)
+    pw, ps = _param(weight, h.weight, d, dt, "weight"), _packed(stats, (2, n), torch.float32, "stats")
+    _on_device(h, total, stats, grad_out, grad_total, weight, grad_x, grad_weight, grad_bias, workspace)
+    px = pgw = pgb = None
+    grad_x, px = _result(grad_x, (n, d), dt, total, stream, "grad_x")
+    if h.weight:
+        grad_weight, pgw = _result(grad_weight, (d,), dt, total, stream, "grad_weight")
+    elif grad_weight is not None:
+        raise ValueError("grad_weight without weight")
+    if h.bias:
+        grad_bias, pgb = _result(grad_bias, (d,), dt, total, stream, "grad_bias")
+    elif grad_bias is not None:
+        raise ValueError("grad_bias without bias")
     if workspace is None:
         workspace = make_layer_norm_workspace(h, n, total.device, stream)
-    _on_device(h, total, stats, grad_out, grad_total, weight, grad_x, grad_weight, grad_bias, workspace)
-    rc = load_library().tbe_layer_norm_backward(
-        h.ptr, pt, st, _packed(stats, (2, n), torch.float32, "stats"), pg, sg, pu, su,
-        _param(weight, h.weight, d, dt, "weight"), n, _packed(grad_x, (n, d), dt, "grad_x"),
-        _param(grad_weight, h.weight, d, dt, "grad_weight"), _param(grad_bias, h.bias, d, dt, "grad_bias"),
-        _space(workspace), workspace.numel(), _stream(stream))
+    rc = load_library().tbe_layer_norm_backward(h.ptr, pt, st, ps, pg, sg, pu, su, pw, n, px, pgw, pgb,
+                                                _space(workspace), workspace.numel(), _stream(stream))
     _check(rc, "tbe_layer_norm_backward")
     return grad_x, grad_weight, grad_bias
 
@@ -909,16 +915,13 @@ def tbe_softmax_loss_forward(h: SoftmaxLossHandle, x: torch.Tensor, table: torch
     both fp32 [N]."""
     ops = _loss_operands(h, x, table, targets)
     n, v = ops[-2:]
-    if loss is None:
-        loss = _new((n,), torch.float32, x.device, stream)
-    if lse is None:
-        lse = _new((n,), torch.float32, x.device, stream)
+    _on_device(h, x, table, targets, loss, lse, workspace)
+    loss, po = _result(loss, (n,), torch.float32, x, stream, "loss")
+    lse, pl = _result(lse, (n,), torch.float32, x, stream, "lse")
     if workspace is None:
         workspace = make_softmax_loss_workspace(h, n, v, False, x.device, stream)
-    _on_device(h, x, table, targets, loss, lse, workspace)
-    rc = load_library().tbe_softmax_loss_forward(
-        h.ptr, *ops, _packed(loss, (n,), torch.float32, "loss"), _packed(lse, (n,), torch.float32, "lse"),
-        _space(workspace), workspace.numel(), _stream(stream))
+    rc = load_library().tbe_softmax_loss_forward(h.ptr, *ops, po, pl, _space(workspace), workspace.numel(),
+                                                 _stream(stream))
     _check(rc, "tbe_softmax_loss_forward")
     return loss, lse
 
@@ -932,18 +935,17 @@ def tbe_softmax_loss_backward(h: SoftmaxLossHandle, x: torch.Tensor, table: torc
     are computed (the other is None)."""
     ops = _loss_operands(h, x, table, targets)
     n, v = ops[-2:]
-    if grad_x is None and want[0]:
-        grad_x = _new((n, h.dim), h.dtype, x.device, stream)
-    if grad_table is None and want[1]:
-        grad_table = _new((v, h.dim), h.dtype, x.device, stream)
+    pl, pg = _packed(lse, (n,), torch.float32, "lse"), _packed(grad_loss, (n,), torch.float32, "grad_loss")
+    _on_device(h, x, table, targets, lse, grad_loss, grad_x, grad_table, workspace)
+    px = pt = None
+    if want[0] or grad_x is not None:
+        grad_x, px = _result(grad_x, (n, h.dim), h.dtype, x, stream, "grad_x")
+    if want[1] or grad_table is not None:
+        grad_table, pt = _result(grad_table, (v, h.dim), h.dtype, x, stream, "grad_table")
     if workspace is None:
         workspace = make_softmax_loss_workspace(h, n, v, True, x.device, stream)
-    _on_device(h, x, table, targets, lse, grad_loss, grad_x, grad_table, workspace)
-    rc = load_library().tbe_softmax_loss_backward(
-        h.ptr, *ops, _packed(lse, (n,), torch.float32, "lse"), _packed(grad_loss, (n,), torch.float32, "grad_loss"),
-        None if grad_x is None else _packed(grad_x, (n, h.dim), h.dtype, "grad_x"),
-        None if grad_table is None else _packed(grad_table, (v, h.dim), h.dtype, "grad_table"),
-        _space(workspace), workspace.numel(), _stream(stream))
+    rc = load_library().tbe_softmax_loss_backward(h.ptr, *ops, pl, pg, px, pt, _space(workspace), workspace.numel(),
+                                                  _stream(stream))
     _check(rc, "tbe_softmax_loss_backward")
     return grad_x, grad_table
 

@@ -19,6 +19,15 @@ struct tbe_softmax_loss {
     int num_sms = 0;
     tbe_softmax_loss_config c{};
     uint32_t* error = nullptr;
+    // the last sizes' slices (the choice takes the host 5 us, as long as a launch)
+    mutable struct {
+        int64_t rows = -1, items = -1;
+        int slices;
+    } forward_choice;
+    mutable struct {
+        int64_t rows = -1, items = -1;
+        int x, w;
+    } backward_choice;
 };
 
 namespace {
@@ -396,7 +405,13 @@ int forward(const tbe_softmax_loss* h, const Plan& L, LossForward p, const void*
             L.w_bytes};
     const int64_t whole = w.is_direct ? p.V : std::min(p.V, L.span);
     p.row_tiles = (int)L.row_tiles;
-    p.slices = choose_slices(L.row_tiles, (whole + 255) / 256, h->num_sms);
+    auto& last = h->forward_choice;
+    if (last.rows != L.row_tiles || last.items != whole) {
+        last.slices = choose_slices(L.row_tiles, (whole + 255) / 256, h->num_sms);
+        last.rows = L.row_tiles;
+        last.items = whole;
+    }
+    p.slices = last.slices;
     p.part = at<float2>(base, L.d);
     p.picked = at<float>(base, L.rows);
     for (p.v0 = 0; p.v0 < p.V; p.v0 = p.v1) {
@@ -490,7 +505,16 @@ int backward_fused(const tbe_softmax_loss* h, const Plan& L, LossFused p, const 
     p.w.part = at<float4>(base, L.w_part);
     p.w.first = p.w.last = 1;
     p.w.tiles = (int)((whole + 127) / 128);
-    choose_sides(&p.x, &p.w, p.D, h->num_sms);  // (of both, so that one alone has the same bits)
+    auto& last = h->backward_choice;
+    if (last.rows != p.N || last.items != whole) {
+        choose_sides(&p.x, &p.w, p.D, h->num_sms);  // (of both, so that one alone has the same bits)
+        last.x = p.x.slices;
+        last.w = p.w.slices;
+        last.rows = p.N;
+        last.items = whole;
+    }
+    p.x.slices = last.x;
+    p.w.slices = last.w;
     if (!gx) p.x.tiles = 0;
     for (p.v0 = 0; p.v0 < p.V; p.v0 = p.v1) {
         p.v1 = std::min(p.V, p.v0 + whole);
