@@ -25,7 +25,7 @@ namespace {
 constexpr int kMaxNormDim = 16384;
 // CTAs of the backward kernel per SM at most: bounds its partial sums (the
 // wide rows' CTAs are large, fewer fit).
-constexpr int most_ctas(int D) { return D <= 2048 ? 8 : D <= 4096 ? 4 : 2; }
+constexpr int most_ctas(int D) { return D <= 512 ? 8 : 2; }
 
 struct CallRange {
     explicit CallRange(const char* name) { nvtxRangePushA(name); }
@@ -52,12 +52,12 @@ struct NormBackward {
     float* part;  // [CTAs][2][D]: sums of g xhat and of g over a CTA's rows
 };
 
-// Both kernels stream rows that stay in registers from the load to the store:
-// T threads hold a row, thread t the accesses t, t + T, ... (K of them) of E
+// Both kernels stream rows that stay in registers from the first sum to the
+// store: T threads hold a row, thread t the accesses t, t + T, ... (K of them) of E
 // consecutive elements (16 bytes, or one element where rows are not aligned).
-// A group of T <= 32 lanes sums by shuffles alone and a CTA holds several; a
-// wider row is a CTA's.  Groups take rows in turn (the grid fills the GPU
-// once), so weights stay in registers and the next row is fetched before this
+// A group of T <= 32 lanes sums by shuffles alone, a larger one through shared
+// memory and a barrier of its own.  Groups take rows in turn (the grid fills the GPU
+// once), so weights stay in registers and the next rows are fetched before this
 // one's sums.
 template <int DT, int E>
 struct Access {
@@ -145,24 +145,115 @@ struct RowPart {
     }
 };
 
+// Threads of a CTA: several groups where a row leaves room for them (they share
+// the backward pass's partial sums of the weights; the forward pass wants the
+// registers).
+constexpr int forward_threads(int T) { return T <= 32 ? 256 : T; }
+constexpr int backward_threads(int T) { return T <= 32 ? 256 : T < 512 ? 512 : T; }
+
+// The backward pass's rows that a group takes in turn, fetched ahead.  16-byte
+// accesses go through shared memory, S rows deep: a thread copies its own accesses
+// there (cp.async) and reads them back, so nothing has to wait for another
+// thread, and rows in flight take no registers (50,523 x 512 bf16 54 -> 44 us; the
+// forward pass has registers for the next row and lost 5 % by it).  Single elements
+// and the widest rows are held in registers, one row ahead.
+template <int DT, int E, int K, int T>
+struct Feed {
+    using Part = RowPart<DT, E, K, T>;
+    static constexpr int kThreads = backward_threads(T), kAccess = kThreads * 16;
+    static constexpr bool kRing = E > 1 && T < 512;
+    static constexpr int S = K == 1 ? 5 : K == 2 ? 4 : 2;
+    static constexpr size_t kBytes = kRing ? (size_t)S * 3 * K * kAccess : 0;
+    const NormBackward& p;
+    const int64_t step;
+    const int t;
+    int at;
+    uint32_t room;  // of this thread
+    Part x, g, u;   // without the ring: the next row
+
+    __device__ __forceinline__ Feed(const NormBackward& args, int64_t step, int t)
+        : p(args), step(step), t(t), at(0), room(0) {}
+
+    __device__ __forceinline__ void copy_one(const void* base, int64_t at, uint32_t to) {
+        const char* from = static_cast<const char*>(base) + at * elem_bytes(DT);
+#pragma unroll
+        for (int k = 0; k < K; ++k)  // (behind the row's end: nothing read, zeros)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + k * kAccess),
+                         "l"((k * T + t) * E < p.D ? from + (k * T + t) * 16 : from), "r"((k * T + t) * E < p.D ? 16 : 0)
+                         : "memory");
+    }
+
+    __device__ __forceinline__ void copy(int64_t row, int slot) {
+        if (row < p.rows) {
+            const uint32_t to = room + slot * (3 * K * kAccess);
+            copy_one(p.total, row * p.total_stride, to);
+            copy_one(p.g, row * p.g_stride, to + K * kAccess);
+            if (p.u) copy_one(p.u, row * p.u_stride, to + 2 * K * kAccess);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+
+    __device__ __forceinline__ void load(int64_t row) {
+        if (row >= p.rows) {  // a group without a row adds nothing to the sums
+            x = g = Part{};
+            return;
+        }
+        x.load(p.total, row * p.total_stride, p.D, t);
+        g.load(p.g, row * p.g_stride, p.D, t);
+        if (p.u) u.load(p.u, row * p.u_stride, p.D, t);
+    }
+
+    __device__ __forceinline__ void start(unsigned char* smem, int64_t row) {
+        if constexpr (kRing) {
+            room = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + threadIdx.x * 16;
+#pragma unroll
+            for (int i = 0; i < S - 1; ++i) copy(row + i * step, i);
+        } else {
+            load(row);
+        }
+    }
+
+    // The ring's row `row` is there.
+    __device__ __forceinline__ void take(int64_t row) {
+        copy(row + (S - 1) * step, (at + S - 1) % S);
+        asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
+    }
+    __device__ __forceinline__ void get(int i, float* f) const {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            uint4 v;
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                         : "r"(room + ((at * 3 + i) * K + k) * kAccess)
+                         : "memory");
+            unpack16<DT>(v, f + k * E);
+        }
+    }
+    __device__ __forceinline__ void leave() { at = (at + 1) % S; }
+};
+
 // Sums of N values over the T threads of a row, in all of them.  Wider groups
 // than a warp join through shared memory; `turn` alternates between its two
 // halves, so one barrier a sum is enough.
-template <int T, int N>
+template <int T, int kGroups, int N>
 __device__ __forceinline__ void row_sums(float (&v)[N], int& turn) {
 #pragma unroll
     for (int o = (T < 32 ? T : 32) / 2; o > 0; o /= 2)
 #pragma unroll
         for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
     if constexpr (T > 32) {
-        __shared__ float part[2][N][T / 32];
+        __shared__ float part[2][kGroups][N][T / 32];
+        const int group = threadIdx.x / T;
         if (threadIdx.x % 32 == 0)
 #pragma unroll
-            for (int i = 0; i < N; ++i) part[turn][i][threadIdx.x / 32] = v[i];
-        __syncthreads();
+            for (int i = 0; i < N; ++i) part[turn][group][i][threadIdx.x % T / 32] = v[i];
+        if constexpr (kGroups > 1)
+            asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(T) : "memory");
+        else
+            __syncthreads();
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            float s = part[turn][i][threadIdx.x % (T / 32)];
+            float s = part[turn][group][i][threadIdx.x % (T / 32)];
 #pragma unroll
             for (int o = T / 64; o > 0; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
             v[i] = s;
@@ -171,15 +262,13 @@ __device__ __forceinline__ void row_sums(float (&v)[N], int& turn) {
     }
 }
 
-constexpr int cta_threads(int T) { return T > 32 ? T : 256; }
-
 template <int DT, int E, int K, int T>
-__global__ void __launch_bounds__(cta_threads(T)) norm_forward_kernel(const NormForward p) {
+__global__ void __launch_bounds__(forward_threads(T)) norm_forward_kernel(const NormForward p) {
     using Part = RowPart<DT, E, K, T>;
-    constexpr int kGroups = cta_threads(T) / T, M = E * K;
+    constexpr int kGroups = forward_threads(T) / T, M = E * K;
     const int t = threadIdx.x % T;
     const int64_t step = (int64_t)gridDim.x * kGroups;
-    const float width = p.D;
+    const float width = p.D, per = 1.f / width;
     Part w{}, b{};
     if (p.weight) w.load(p.weight, 0, p.D, t);
     if (p.bias) b.load(p.bias, 0, p.D, t);
@@ -208,8 +297,9 @@ __global__ void __launch_bounds__(cta_threads(T)) norm_forward_kernel(const Norm
         fetch(row + step);
 #pragma unroll
         for (int i = 0; i < M; ++i) s[0] += f[i];
-        row_sums<T>(s, turn);
-        const float mean = s[0] / width;  // (exact where all elements are the same)
+        row_sums<T, kGroups>(s, turn);
+        const float about = s[0] * per;
+        const float mean = fmaf(fmaf(-width, about, s[0]), per, about);  // (exact where all elements are the same)
         s[0] = 0.f;
 #pragma unroll
         for (int k = 0; k < K; ++k)
@@ -219,8 +309,8 @@ __global__ void __launch_bounds__(cta_threads(T)) norm_forward_kernel(const Norm
                     f[i] -= mean;
                     s[0] = fmaf(f[i], f[i], s[0]);
                 }
-        row_sums<T>(s, turn);
-        const float rstd = rsqrtf(s[0] / width + p.eps);
+        row_sums<T, kGroups>(s, turn);
+        const float rstd = rsqrtf(fmaf(s[0], per, p.eps));
         if (row >= p.rows) continue;
         if (p.residual) keep.store(p.total, row * p.D, p.D, t);
         float q[M];
@@ -253,31 +343,27 @@ constexpr bool sums_in_smem() {
 }
 
 template <int DT, int E, int K, int T>
-__global__ void __launch_bounds__(cta_threads(T)) norm_backward_kernel(const NormBackward p) {
+__global__ void __launch_bounds__(backward_threads(T)) norm_backward_kernel(const NormBackward p) {
     using Part = RowPart<DT, E, K, T>;
-    constexpr int kThreads = cta_threads(T), kGroups = kThreads / T, M = E * K;
+    constexpr int kThreads = backward_threads(T), kGroups = kThreads / T, M = E * K;
     constexpr bool kSmem = sums_in_smem<E, K, T>();
-    extern __shared__ float room[];  // kSmem: [2 M][threads]; several groups: [M][threads]
+    using Rows = Feed<DT, E, K, T>;
+    extern __shared__ __align__(16) unsigned char smem[];
+    // behind the rows ahead (kSmem: [2 M][threads]) or, after them, in their place (several groups: [M][threads])
+    float* room = reinterpret_cast<float*>(smem + (kSmem ? Rows::kBytes : 0));
     const int t = threadIdx.x % T;
     const int64_t step = (int64_t)gridDim.x * kGroups;
-    const float width = p.D;
+    const float per = 1.f / p.D;
     const bool params = p.gw || p.gb;
     Part w{};
     if (p.weight) w.load(p.weight, 0, p.D, t);
     int64_t row = (int64_t)blockIdx.x * kGroups + threadIdx.x / T;
-    Part x{}, g{}, u{};
+    Rows feed(p, step, t);
+    feed.start(smem, row);
     float mean = 0.f, rstd = 0.f;
     auto fetch = [&](int64_t i) {
-        if (i >= p.rows) {  // a group without a row adds nothing to the sums
-            x = g = Part{};
-            mean = rstd = 0.f;
-            return;
-        }
-        x.load(p.total, i * p.total_stride, p.D, t);
-        g.load(p.g, i * p.g_stride, p.D, t);
-        if (p.u) u.load(p.u, i * p.u_stride, p.D, t);
-        mean = __ldg(p.stats + i);
-        rstd = __ldg(p.stats + p.rows + i);
+        mean = i < p.rows ? __ldg(p.stats + i) : 0.f;
+        rstd = i < p.rows ? __ldg(p.stats + p.rows + i) : 0.f;
     };
     float sw[kSmem ? 1 : M], sb[kSmem ? 1 : M];
     if constexpr (kSmem) {
@@ -291,10 +377,22 @@ __global__ void __launch_bounds__(cta_threads(T)) norm_backward_kernel(const Nor
     int turn = 0;
     for (; row - threadIdx.x % 32 / T < p.rows; row += step) {
         float h[M], a[M], q[M], s[2] = {0.f, 0.f};
-        x.get(h);
-        g.get(a);
         const float m = mean, is = rstd;
-        Part on = u;
+        const bool valid = row < p.rows;
+        Part on{};
+        if constexpr (Rows::kRing) {
+            feed.take(row);
+            feed.get(0, h);
+            feed.get(1, a);
+            if (T < 32 && !valid)
+#pragma unroll
+                for (int i = 0; i < M; ++i) a[i] = h[i] = 0.f;
+        } else {
+            feed.x.get(h);
+            feed.g.get(a);
+            on = feed.u;
+            feed.load(row + step);
+        }
         fetch(row + step);
         // (accesses behind the row's end hold g = 0, and their xhat meets nothing else)
 #pragma unroll
@@ -320,21 +418,25 @@ __global__ void __launch_bounds__(cta_threads(T)) norm_backward_kernel(const Nor
             s[0] += a[i];
             s[1] = fmaf(a[i], h[i], s[1]);
         }
-        row_sums<T>(s, turn);
-        s[0] /= width;
-        s[1] /= width;
-        if (row >= p.rows) continue;
+        row_sums<T, kGroups>(s, turn);
+        s[0] *= per;
+        s[1] *= per;
         if (p.u) {
-            on.get(q);
+            if constexpr (Rows::kRing)
+                feed.get(2, q);
+            else
+                on.get(q);
 #pragma unroll
             for (int i = 0; i < M; ++i) a[i] = fmaf(is, (a[i] - s[0]) - h[i] * s[1], q[i]);
         } else {
 #pragma unroll
             for (int i = 0; i < M; ++i) a[i] = is * ((a[i] - s[0]) - h[i] * s[1]);
         }
+        if constexpr (Rows::kRing) feed.leave();
         on.set(a);
-        on.store(p.gx, row * p.D, p.D, t);
+        if (valid) on.store(p.gx, row * p.D, p.D, t);
     }
+    if constexpr (Rows::kRing) asm volatile("cp.async.wait_group 0;" ::: "memory");
     if (!params) return;
     // the CTA's sums of both kinds, its groups in order
     float* part = p.part + (int64_t)blockIdx.x * 2 * p.D;
@@ -414,7 +516,7 @@ int resident(F kernel, int threads, size_t smem) {
 
 template <int DT, int E, int K, int T>
 cudaError_t forward(const NormForward& p, const tbe_layer_norm* h, cudaStream_t s) {
-    constexpr int threads = cta_threads(T);
+    constexpr int threads = forward_threads(T);
     auto* kernel = norm_forward_kernel<DT, E, K, T>;
     static const int per_sm = resident(kernel, threads, 0);
     kernel<<<fill(h, per_sm, threads / T, p.rows), threads, 0, s>>>(p);
@@ -423,12 +525,13 @@ cudaError_t forward(const NormForward& p, const tbe_layer_norm* h, cudaStream_t 
 
 template <int DT, int E, int K, int T>
 cudaError_t backward(const NormBackward& p, const tbe_layer_norm* h, cudaStream_t s) {
-    constexpr int threads = cta_threads(T), M = E * K;
-    constexpr size_t smem = sizeof(float) * threads * (sums_in_smem<E, K, T>() ? 2 * M : threads > T ? M : 0);
+    constexpr int threads = backward_threads(T), M = E * K;
+    constexpr size_t ahead = Feed<DT, E, K, T>::kBytes, sums = sizeof(float) * threads * M;
+    constexpr size_t smem = sums_in_smem<E, K, T>() ? ahead + 2 * sums : threads > T ? std::max(ahead, sums) : ahead;
     auto* kernel = norm_backward_kernel<DT, E, K, T>;
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
+    if (smem > 48 * 1024) {  // (an attribute of the device's copy of the kernel, so set at every call)
+        const cudaError_t f = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (f != cudaSuccess) return f;
     }
     static const int per_sm = resident(kernel, threads, smem);
     const unsigned grid = fill(h, std::min(per_sm, most_ctas(p.D)), threads / T, p.rows);
