@@ -12,7 +12,12 @@ q, k, v and the bias table, ``tbe_backward_sgd`` for the item table.
 Serving keeps the keys and values in a paged cache: the histories are appended
 once, then each new event is appended and attends to its user's cache.
 
-    python examples/history_model.py [--users 64] [--steps 20]
+``NextItemModel`` predicts the next event's item instead: the pooled rows are a
+stream that is normalised on its way into attention, attention's output is added
+to it, and the normalised sum is scored against the item table itself
+(``tbe_softmax_loss_forward``; the table gets the gradients of both its uses).
+
+    python examples/history_model.py [--users 64] [--steps 20] [--next-item]
 """
 
 from __future__ import annotations
@@ -80,6 +85,102 @@ class HistoryModel:
         self.attention.close()
 
 
+class NextItemModel:
+    """One pre-norm attention block over pooled rows, and the loss of the next
+    item over the table that the rows come from."""
+
+    def __init__(self, items=5000, dim=64, heads=4, kv_heads=2, head_dim=32, window=64, sinks=2, buckets=16,
+                 dtype=torch.bfloat16, device="cuda", seed=0):
+        g = torch.Generator(device="cpu").manual_seed(seed)
+
+        def weight(*shape, std, mean=0.0):
+            return (torch.randn(shape, generator=g) * std + mean).to(device)
+
+        self.dtype, self.heads, self.kv_heads, self.head_dim = dtype, heads, kv_heads, head_dim
+        self.table = weight(items, dim, std=0.3).to(dtype)
+        self.bags = tbe.tbe_create([self.table], "sum")
+        self.params = {"w": weight(dim, (heads + 2 * kv_heads) * head_dim, std=dim ** -0.5),
+                       "w_out": weight(heads * head_dim, dim, std=(heads * head_dim) ** -0.5),
+                       "bias": weight(buckets, heads, std=0.1)}
+        for i in ("1", "2"):
+            self.params |= {"norm_w" + i: weight(dim, std=0.1, mean=1.0), "norm_b" + i: weight(dim, std=0.1)}
+        self.attention = tbe.tbe_attention_create(heads, kv_heads, head_dim, dtype, window, sinks,
+                                                  tbe.tbe_relative_buckets(buckets, window))
+        self.norm = tbe.tbe_layer_norm_create(dim, dtype)
+        self.loss = tbe.tbe_softmax_loss_create(dim, dtype)
+
+    def gradients(self, ids, bag_offsets, offsets, targets, scale=1.0):
+        """(loss, gradients of the parameters and of the pooled rows) of the mean
+        loss over the labelled events, times ``scale``; the table's gradient as a
+        table of items is "table", its lookups' come from "rows"."""
+        events, p = bag_offsets.numel() - 1, {k: v.to(self.dtype) for k, v in self.params.items()}
+        h, k, dt = self.heads, self.kv_heads, self.dtype
+        stream = tbe.tbe_forward(self.bags, ids, bag_offsets, events).to(dt)
+        y1, _, stats1 = tbe.tbe_layer_norm_forward(self.norm, stream, p["norm_w1"], p["norm_b1"])
+        qkv = (y1 @ p["w"]).view(events, h + 2 * k, self.head_dim)
+        q, key, v = qkv[:, :h], qkv[:, h:h + k], qkv[:, h + k:]
+        out, lse = tbe.tbe_attention_forward(self.attention, q, key, v, offsets, p["bias"])
+        flat = out.view(events, -1)
+        y2, total, stats2 = tbe.tbe_layer_norm_forward(self.norm, flat @ p["w_out"], p["norm_w2"], p["norm_b2"],
+                                                       residual=stream)
+        loss, lse2 = tbe.tbe_softmax_loss_forward(self.loss, y2, self.table, targets)
+        labelled = (targets >= 0).sum().clamp(min=1)
+
+        up = (scale / labelled.float()).expand(events).contiguous()
+        g = {}
+        gy2, g["table"] = tbe.tbe_softmax_loss_backward(self.loss, y2, self.table, targets, lse2, up)
+        ga, g["norm_w2"], g["norm_b2"] = tbe.tbe_layer_norm_backward(self.norm, total, stats2, gy2, p["norm_w2"])
+        g["w_out"] = flat.t() @ ga
+        d_out = (ga @ p["w_out"].t()).view_as(out)
+        gq, gk, gv, g["bias"] = tbe.tbe_attention_backward(self.attention, q, key, v, offsets, out, lse, d_out, p["bias"])
+        d_qkv = torch.cat([gq, gk, gv], 1).view(events, -1)
+        g["w"] = y1.t() @ d_qkv
+        g["rows"], g["norm_w1"], g["norm_b1"] = tbe.tbe_layer_norm_backward(
+            self.norm, stream, stats1, d_qkv @ p["w"].t(), p["norm_w1"], grad_total=ga)
+        return loss.sum() / labelled, g
+
+    def step(self, ids, bag_offsets, offsets, targets, lr):
+        """One training step on a batch of histories; returns the loss."""
+        scale = float(offsets[-1])  # the 16-bit gradients carry the sum, the updates divide
+        loss, g = self.gradients(ids, bag_offsets, offsets, targets, scale)
+        for name, x in self.params.items():
+            x -= lr / scale * g[name].float()
+        events = bag_offsets.numel() - 1
+        workspace = tbe.make_workspace(self.bags, ids.numel(), events)
+        tbe.tbe_backward_sgd(self.bags, ids, bag_offsets, events, g["rows"].float() / scale, lr, workspace)
+        self.table -= (lr / scale * g["table"].float()).to(self.dtype)
+        return float(loss)
+
+    def check(self):
+        codes = (tbe.tbe_get_error(self.bags), tbe.tbe_attention_get_error(self.attention),
+                 tbe.tbe_softmax_loss_get_error(self.loss))
+        if any(c != tbe.TBE_OK for c in codes):
+            raise RuntimeError(f"device error {codes}")
+
+    def close(self):
+        for h in (self.bags, self.attention, self.norm, self.loss):
+            h.close()
+
+
+def next_items(ids, offsets):
+    """The first id of the event after each one (three ids an event); -1 for a history's last."""
+    targets = ids[::3].roll(-1)
+    targets[offsets[1:] - 1] = -1
+    return targets
+
+
+def train_next_item(users=64, steps=20, items=500, lr=2.0, verbose=True):
+    model = NextItemModel(items=items)
+    ids, bags, offsets, _ = make_histories(users, items, "cuda", 1)
+    targets = next_items(ids, offsets)
+    losses = [model.step(ids, bags, offsets, targets, lr) for _ in range(steps)]
+    model.check()
+    if verbose:
+        print(f"next item: loss {losses[0]:.4f} -> {losses[-1]:.4f} in {steps} steps")
+    model.close()
+    return losses
+
+
 class Cache:
     """A paged cache of a batch of users' keys and values."""
 
@@ -140,5 +241,9 @@ if __name__ == "__main__":
     p = argparse.ArgumentParser()
     p.add_argument("--users", type=int, default=64)
     p.add_argument("--steps", type=int, default=20)
+    p.add_argument("--next-item", action="store_true", help="train the next item's loss over the item table")
     a = p.parse_args()
-    main(a.users, a.steps)
+    if a.next_item:
+        train_next_item(a.users, a.steps)
+    else:
+        main(a.users, a.steps)
