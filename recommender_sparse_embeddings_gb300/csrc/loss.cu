@@ -90,7 +90,7 @@ struct RowsIn {
     const float *lse, *g;
     float scale;
     float* rows;  // [tiles][kRowValues]
-    float* unit;  // what the rows' second values are taken relative to
+    float* unit;  // what the products of d are multiplied by
     float* gmax;  // [kMaxCtas] partial maxima
     uint32_t* error;
 };
@@ -129,38 +129,34 @@ __global__ void __launch_bounds__(256) loss_max_kernel(const RowsIn p) {
 // The backward pass's rows, one warp each: x copied with zeros in the rows left
 // out, and what each row brings.
 //
-// 16-bit types hold d relative to the largest |g scale|.  So where all rows have
-// the same g (a mean), d is p - [target] itself: -1 for a target of little weight
-// has no rounding, where -g would be off by the same 2^-9 in every row (grad_table
-// of 300 rows over 5000 items in bf16: 0.0025 off, so 0.0017).  fp16's range is
-// narrow besides (6e-8 to 65504): there the largest is 2^14, and weights down to
-// 2^-28 keep all their bits.
+// d is held relative to the largest |g scale|.  So where all rows have the same g
+// (a mean), d is p - [target] itself: nothing has to be multiplied, and -1 for a
+// target of little weight has no rounding, where -g would be off by the same 2^-9
+// in every row (grad_table of 300 rows over 5000 items in bf16: 0.0025 off, so
+// 0.0017).  fp16's range is narrow besides (6e-8 to 65504): there d comes times
+// kTargetUnit = 2^14, and weights down to 2^-28 keep all their bits.
 template <int DT>
 __global__ void __launch_bounds__(256) loss_rows_kernel(const RowsIn p) {
     chain_wait();
     const int lane = threadIdx.x % 32;
-    float unit = 1.f;
-    if constexpr (DT != DT_F32) {
-        float m = 0.f;
-        if (p.parts == 0) {
-            m = row_max(p, threadIdx.x, 256);
-        } else {
-            m = fmaxf(p.gmax[lane], p.gmax[lane + 32]);
+    float m = 0.f;
+    if (p.parts == 0) {
+        m = row_max(p, threadIdx.x, 256);
+    } else {
+        m = fmaxf(p.gmax[lane], p.gmax[lane + 32]);
 #pragma unroll
-            for (int o = 16; o > 0; o /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        }
-        if (DT == DT_F16) m *= 0x1p-14f;
-        if (m > 0.f) unit = m;
+        for (int o = 16; o > 0; o /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     }
-    if (blockIdx.x == 0 && threadIdx.x == 0) *p.unit = unit;
+    if (!(m > 0.f)) m = 1.f;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.unit = m / target_unit<DT>();
     for (int64_t row = ((int64_t)blockIdx.x * 256 + threadIdx.x) / 32; row < p.tiles * 128;
          row += (int64_t)gridDim.x * 8) {
         float* to = p.rows + row / 128 * kRowValues + row % 128;
         const int64_t t = row < p.x.rows ? row_target(p, row) : -1;
         if (row < p.x.rows) copy_row<DT>(p.x, row, t < 0, lane);
         if (lane == 0) {
-            to[0] = t < 0 ? 0.f : -p.lse[row] * (DT == DT_F32 ? 1.f : kLog2e);
-            to[128] = t < 0 ? 0.f : p.g[row] * p.scale / unit;
+            to[0] = t < 0 ? -INFINITY : DT == DT_F32 ? -p.lse[row] : log2f(target_unit<DT>()) - p.lse[row] * kLog2e;
+            to[128] = t < 0 ? 1.f : p.g[row] * p.scale / m;
             to[256] = __int_as_float((int)t);
         }
     }
@@ -440,13 +436,13 @@ cudaError_t launch_rows(const tbe_softmax_loss* h, const Plan& L, RowsIn rows, c
     rows.x.to = at<uint16_t>(base, L.x);
     const dim3 grid((unsigned)std::min<int64_t>(rows.tiles * 16, kRowCtas));
     rows.parts = rows.x.rows > kFewRows ? kMaxCtas : 0;
-    if (h->c.dtype == TBE_F32) return launch_chained(loss_rows_kernel<DT_F32>, grid, dim3(256), s, rows);
     if (rows.parts > 0) {
         const cudaError_t e = launch_chained(loss_max_kernel, dim3(kMaxCtas), dim3(256), s, rows);
         if (e != cudaSuccess) return e;
     }
-    return h->c.dtype == TBE_BF16 ? launch_chained(loss_rows_kernel<DT_BF16>, grid, dim3(256), s, rows)
-                                  : launch_chained(loss_rows_kernel<DT_F16>, grid, dim3(256), s, rows);
+    return h->c.dtype == TBE_F32   ? launch_chained(loss_rows_kernel<DT_F32>, grid, dim3(256), s, rows)
+           : h->c.dtype == TBE_F16 ? launch_chained(loss_rows_kernel<DT_F16>, grid, dim3(256), s, rows)
+                                   : launch_chained(loss_rows_kernel<DT_BF16>, grid, dim3(256), s, rows);
 }
 
 // Slices of the fused launch's sums, x's and w's: those of the least estimated

@@ -49,7 +49,7 @@ struct FusedBars {
 };
 
 // 32 columns of the thread's line: x = S in, d out.
-template <int P, bool ITEMS, int BN>
+template <int DT, int P, bool ITEMS, int BN>
 __device__ __forceinline__ void gradients(float (&x)[32], float c2, float minus_lse, float coef, int at, int left,
                                           const float* stats, int line) {
     if constexpr (!ITEMS) {
@@ -60,15 +60,17 @@ __device__ __forceinline__ void gradients(float (&x)[32], float c2, float minus_
         if (__any_sync(0xffffffffu, at >= 0 && at < 32)) {
 #pragma unroll
             for (int c = 0; c < 32; ++c)
-                if (c == at) x[c] -= 1.f;
+                if (c == at) x[c] -= target_unit<DT>();
         }
         if (left < 32) {
 #pragma unroll
             for (int c = 0; c < 32; ++c)
                 if (c >= left) x[c] = 0.f;
         }
+        if (!__all_sync(0xffffffffu, coef == 1.f)) {
 #pragma unroll
-        for (int c = 0; c < 32; c += 2) mul2(x[c], x[c + 1], coef, coef);
+            for (int c = 0; c < 32; c += 2) mul2(x[c], x[c + 1], coef, coef);
+        }
     } else {
         // columns are rows of x: their values lie in shared memory
 #pragma unroll
@@ -84,27 +86,29 @@ __device__ __forceinline__ void gradients(float (&x)[32], float c2, float minus_
 #pragma unroll
             for (int c = 0; c < 32; ++c)
                 if (hit >> c & 1)
-                    if (__float_as_int(stats[2 * BN + c]) == line) x[c] -= 1.f;
+                    if (__float_as_int(stats[2 * BN + c]) == line) x[c] -= target_unit<DT>();
         }
+        if (!__all_sync(0xffffffffu, stats[BN + lane] == 1.f)) {
 #pragma unroll
-        for (int c = 0; c < 32; c += 4) {
-            const float4 g = *reinterpret_cast<const float4*>(stats + BN + c);
-            mul2(x[c], x[c + 1], g.x, g.y);
-            mul2(x[c + 2], x[c + 3], g.z, g.w);
+            for (int c = 0; c < 32; c += 4) {
+                const float4 g = *reinterpret_cast<const float4*>(stats + BN + c);
+                mul2(x[c], x[c + 1], g.x, g.y);
+                mul2(x[c + 2], x[c + 3], g.z, g.w);
+            }
         }
     }
 }
 
 // fp32's two sums of the thread's line, added (or, `first`, stored) to its row of
-// the result or to a slab as add_slab lays it out.
+// the result, times `unit`, or to a slab as add_slab lays it out.
 __device__ __forceinline__ void put_fp32(float* out, float4* part, uint32_t acc, int wide, int group, bool valid, int D,
-                                         bool first) {
+                                         bool first, float unit) {
     const bool vec = D % 4 == 0 && (uintptr_t)out % 16 == 0;
     for (int c = group * 16; c < wide; c += 64) {
         float x[16], y[16];
         tmem_ld16_pair(acc + c, acc + 128 + c, x, y);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] += y[e];
+        for (int e = 0; e < 16; ++e) x[e] = out ? (x[e] + y[e]) * unit : x[e] + y[e];
         if (!out || vec) {
             float4* to = out ? reinterpret_cast<float4*>(out + c) : part + c / 4 * 128;
             const int step = out ? 1 : 128;
@@ -278,7 +282,7 @@ __device__ __forceinline__ bool fused_body(const LossFused& p, const LossSide& s
             float4* part = side.part + ((int64_t)slice * side.tiles + tile) * p.cols4 * 128 + line;
             if constexpr (P == 3)
                 put_fp32(side.direct ? static_cast<float*>(side.out) + row * p.D : nullptr, part, acc, wide, warp / 4,
-                         valid, p.D, first);
+                         valid, p.D, first, unit);
             else if (side.direct)
                 store_rows<DT, 4>(side.out, row * p.D, acc, wide, warp / 4, valid, p.D, p.D % 8 == 0, unit);
             else
@@ -326,7 +330,7 @@ __device__ __forceinline__ bool fused_body(const LossFused& p, const LossSide& s
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bars.s_read[buf]);
                 }
-                gradients<P, ITEMS, BN>(x, p.c2, minus_lse, coef, at - h, left - h, stats + h, mine);
+                gradients<DT, P, ITEMS, BN>(x, p.c2, minus_lse, coef, at - h, left - h, stats + h, mine);
                 // d's columns are free of the last but one product (fp32: of the last)
                 if (h == 0 && (P == 3 ? i >= 1 : i >= 2)) {
                     ok = P == 3 ? mbar_wait_tight(&bars.done[buf ^ 1], ((i - 1) / 2) & 1)

@@ -6,7 +6,7 @@ namespace tbe {
 namespace {
 
 constexpr int kForwardThreads = 576;
-constexpr float kLazyMax = 8.f;
+constexpr float kLargeSum = 8192.f;
 
 struct LossBars {
     uint64_t full[kLossStages], empty[kLossStages], a_full[2], a_empty[2], acc_full[2], acc_empty[2];
@@ -262,7 +262,7 @@ __device__ __forceinline__ void d_slab(float* x, float minus_lse, float coef, in
     if (__any_sync(0xffffffffu, at >= 0 && at < 64)) {
 #pragma unroll
         for (int c = 0; c < 64; ++c)
-            if (c == at) x[c] -= 1.f;
+            if (c == at) x[c] -= target_unit<DT>();
     }
     const int64_t left = V - item0;
     if (left < 64) {
@@ -446,8 +446,9 @@ __global__ void __launch_bounds__(kLossThreads, 1)
 
 // Forward pass: a CTA's item is a tile of 128 rows and a slice of the table,
 // whose maximum and sum its threads (a row and a quarter of a tile's columns
-// each) carry in registers.  The running maximum moves only when a logit exceeds it
-// by 2^8 (terms below 2^8 lose nothing in an fp32 sum).
+// each) carry in registers.  The maximum moves only when 32 terms' sum against the
+// last one exceeds 2^13 (below, an fp32 sum loses nothing by it); otherwise no
+// maximum is looked for (a third of the loop's instructions).
 template <int DT, int P>
 __global__ void __launch_bounds__(kForwardThreads, 1)
     loss_forward_kernel(const LossForward p, const __grid_constant__ LossMaps maps) {
@@ -527,22 +528,29 @@ __global__ void __launch_bounds__(kForwardThreads, 1)
                                          : "r"(mine - c - e), "f"(x[e]));
                         found |= mine >= c && mine < c + 32;
                     }
-                    float u[8];
+                    auto sum = [&]() {
+                        float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) u[e] = fmaxf(max3(x[e], x[e + 8], x[e + 16]), x[e + 24]);
-                    const float top = fmaxf(max3(max3(u[0], u[1], u[2]), u[3], u[4]), max3(u[5], u[6], u[7])) * p.c2;
-                    if (__any_sync(0xffffffffu, top > m + kLazyMax)) {
-                        const float to = fmaxf(m, top);
+                        for (int e = 0; e < 32; e += 2) {
+                            float y0 = x[e], y1 = x[e + 1];
+                            powers<P>(y0, y1, p.c2, -m, -m);
+                            add2(s0, s1, y0, y1);
+                        }
+                        return s0 + s1;
+                    };
+                    float s = sum();
+                    if (__any_sync(0xffffffffu, !(s <= kLargeSum))) {  // (m = -inf, at first, too)
+                        float u[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) u[e] = fmaxf(max3(x[e], x[e + 8], x[e + 16]), x[e + 24]);
+                        const float top = fmaxf(max3(max3(u[0], u[1], u[2]), u[3], u[4]), max3(u[5], u[6], u[7])) * p.c2;
+                        // (only where it is the row's own: a neighbour's logits change no bits)
+                        const float to = s <= kLargeSum ? m : fmaxf(m, top);
                         l *= ex2(P == 3 ? (m - to) * kLog2e : m - to);  // (m = -inf: 0)
                         m = to;
+                        s = sum();
                     }
-                    float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        powers<P>(x[e], x[e + 1], p.c2, -m, -m);
-                        add2(s0, s1, x[e], x[e + 1]);
-                    }
-                    l += s0 + s1;
+                    l += s;
                 };
                 auto release = [&]() {
                     tcgen05_before_sync();

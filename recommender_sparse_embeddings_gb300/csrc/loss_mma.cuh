@@ -172,9 +172,16 @@ __device__ __forceinline__ void powers(float& a, float& b, float scale, float le
 }
 
 // What the rows bring into the backward pass: per tile of 128 rows 128 values
-// each of -lse (times log2(e) but for fp32), of g * scale (16-bit types: over its `unit`) and of the
-// target as an int32; 0, 0 and -1 in rows that are left out or behind the last.
+// each of -lse (times log2(e) but for fp32; fp16: + 14), of g over the largest |g|,
+// and of the target as an int32; -inf, 1 and -1 in rows that are left out or
+// behind the last.
 constexpr int kRowValues = 3 * 128;
+
+// What d has of the target: 1, or with fp16 2^14.
+template <int DT>
+__host__ __device__ constexpr float target_unit() {
+    return DT == DT_F16 ? 16384.f : 1.f;
+}
 
 struct LossForward {
     int64_t N, v0, v1;  // rows; the items of this launch
@@ -200,7 +207,7 @@ struct LossStep {
     int32_t D, row_tiles, col_tiles;  // col_tiles: of 256 columns
     float c2;
     const float* rows;   // [row_tiles][kRowValues]
-    const float* unit;   // what the rows' second values are taken relative to
+    const float* unit;   // what the products of d are multiplied by
     // d of the items from d0 on, its work items d_from[c] .. d_from[c + 1] by CTA c
     int32_t n_d;
     int32_t d_from[kMaxStepCtas + 1];
