@@ -512,7 +512,8 @@ void tbe_layer_norm_destroy(tbe_layer_norm* h);
  * contiguous, receives t; NULL exactly where residual is.  stats: device fp32
  * [2, rows], every row's mean and rstd, kept for the backward call.  weight and
  * bias: device dtype [D], NULL exactly where the handle has none.  out or total
- * may be x or residual itself (contiguous, the same rows) but not each other. */
+ * may be x or residual itself (contiguous, the same rows) but not each other
+ * (INVALID_ARG).  A row without spread gives 0 * rstd: with eps 0 that is NaN. */
 int tbe_layer_norm_forward(tbe_layer_norm* h, const void* x, int64_t x_stride, const void* residual,
                            int64_t residual_stride, const void* weight, const void* bias, int64_t num_rows,
                            void* out, void* total, float* stats, void* stream);
@@ -550,15 +551,16 @@ int tbe_layer_norm_backward(tbe_layer_norm* h, const void* total, int64_t total_
  * target >= V leaves the row out too and raises TBE_ERR_INDEX_OOB.
  *
  * The logits are never kept as a whole: the forward call carries a running
- * maximum and sum, the backward call computes them again in pieces of the
- * table.  dtype (fp32, fp16 or bf16) is that of x, the table and the gradients;
- * loss, lse and g are fp32.  Logits, statistics and sums are fp32.  With 16-bit
- * types d is rounded to dtype where it enters the gradients' products; fp16's
- * range holds it relative to the largest finite |g| (g itself may be of any
- * size, the gradients have to fit fp16).  fp32 operands enter the products as
- * three bf16 terms that sum to them exactly; the six products of those terms
- * that matter to fp32 are summed.  x and the table are expected to be finite
- * in rows that are not left out.
+ * maximum and sum, the backward call computes them again, tile by tile or in
+ * pieces of the table.  dtype (fp32, fp16 or bf16) is that of x, the table and
+ * the gradients; loss, lse and g are fp32.  Logits, statistics and sums are fp32.
+ * With 16-bit types d, relative to the largest finite |g|, is rounded to dtype
+ * where it enters the gradients' products (with fp16 times 2^14: g may be of any
+ * size and the weights down to 2^-28, the gradients have to fit fp16).  fp32
+ * operands enter the products as three bf16 terms that sum to them exactly; the
+ * six products of those terms that matter to fp32 are summed, and long sums are
+ * added up in parts.  x and the table are expected to be finite (fp32: below
+ * 3.39e38), x in rows that are not left out.
  *
  * Results are deterministic.  Rows start at data + row * stride (elements,
  * >= D for the table, >= 0 for x).  The fastest path wants 16-bit rows that are
@@ -593,7 +595,7 @@ int tbe_softmax_loss_forward(tbe_softmax_loss* h, const void* x, int64_t x_strid
 
 /* lse: the forward call's.  grad_loss: device fp32 [N].  grad_x: device dtype
  * [N, D], grad_table: device dtype [V, D], both contiguous and written, not
- * added to; either may be NULL (not wanted). */
+ * added to; either may be NULL (not wanted; the other has the same bits). */
 int tbe_softmax_loss_backward(tbe_softmax_loss* h, const void* x, int64_t x_stride, const void* table,
                               int64_t table_stride, const void* targets, int32_t index_dtype, int64_t num_rows,
                               int64_t num_items, const float* lse, const float* grad_loss, void* grad_x,

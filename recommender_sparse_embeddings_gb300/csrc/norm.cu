@@ -633,7 +633,7 @@ int tbe_layer_norm_forward(tbe_layer_norm* h, const void* x, int64_t x_stride, c
         return TBE_ERR_INVALID_ARG;
     if (rows >= (int64_t(1) << 31)) return TBE_ERR_UNSUPPORTED;
     if (rows == 0) return TBE_OK;
-    if (!x || !out || !stats || (residual != nullptr) != (total != nullptr)) return TBE_ERR_INVALID_ARG;
+    if (!x || !out || !stats || (residual != nullptr) != (total != nullptr) || out == total) return TBE_ERR_INVALID_ARG;
     const NormForward p{x, residual, weight, bias, x_stride, residual_stride, rows, h->c.dim, h->c.eps, out, total, stats};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool vec = vec_rows(h, x, x_stride) && vec_rows(h, out, 0) && (!weight || aligned16(weight)) &&

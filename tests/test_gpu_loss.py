@@ -174,6 +174,50 @@ def test_small_gradients_of_fp16_beside_many_items():
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n,d", [(150, 64), (2100, 40), (300, 300)])
+def test_upstream_gradients_of_all_sizes(dtype, n, d):
+    """One row's is far the largest, one is infinite in a row that is left out, some are 0, some are negative; beyond
+    2048 rows another launch looks for the largest."""
+    c = Case(dtype, n, 200, d, seed=8)
+    c.grad = torch.linspace(-1.0, 1.0, n, device="cuda") ** 3
+    c.grad[n // 3] = 8.0
+    c.targets[n // 3] = 3
+    c.grad[5::50] = 0.0
+    c.targets[7], c.grad[7] = -1, float("inf")
+    got = c.run()
+    c.grad[7] = 0.0
+    c.check(got)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_results_off_16_byte_boundaries(dtype):
+    """Results in views that begin anywhere: written element by element."""
+    for d in (64, 72, 264):
+        c = Case(dtype, 140, 300, d, seed=d)
+        want = c.run()
+        gx, gw = (torch.full((r * d + 3,), 7.0, dtype=dtype, device="cuda") for r in (140, 300))
+        tbe.tbe_softmax_loss_backward(c.h, c.x, c.table, c.targets, want["lse"], c.grad, grad_x=gx[1:-2].view(140, d),
+                                      grad_table=gw[1:-2].view(300, d))
+        assert torch.equal(gx[1:-2].view(140, d), want["grad_x"]) and torch.equal(gw[1:-2].view(300, d), want["grad_table"])
+        for t in (gx, gw):  # what lies around them is left as it was
+            assert t[0] == 7.0 and (t[-2:] == 7.0).all()
+
+
+def test_two_handles_on_two_streams():
+    """Calls of two handles whose work overlaps share nothing."""
+    a, b = Case(torch.bfloat16, 900, 6000, 128, seed=1), Case(torch.float32, 400, 3001, 96, seed=2)
+    want = a.run(), b.run()
+    torch.cuda.synchronize()
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    got = [[c.run(stream=s) for c, s in zip((a, b), streams)] for _ in range(5)]
+    torch.cuda.synchronize()
+    for pair in got:
+        for g, w in zip(pair, want):
+            for x in w:
+                assert torch.equal(g[x], w[x]), x
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 def test_one_gradient_wanted(dtype):
     c = Case(dtype, 200, 700, 72, seed=1)
     both = c.run()

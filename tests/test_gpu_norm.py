@@ -231,6 +231,24 @@ def test_refusals():
     with pytest.raises(tbe.TBEError) as e:
         backward(workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     assert e.value.code == tbe.TBE_ERR_WORKSPACE_TOO_SMALL
+    with pytest.raises(tbe.TBEError) as e:  # both results in one place
+        forward(out=total, total=total)
+    assert e.value.code == tbe.TBE_ERR_INVALID_ARG
+    for t in (c.x, total):
+        with pytest.raises(ValueError):
+            tbe.tbe_layer_norm_forward(tbe.tbe_layer_norm_create(32, c.dtype), t, c.weight, c.bias)
     c.h.close()
     with pytest.raises(RuntimeError):
         forward()
+
+
+def test_handles_without_parameters_refuse_them():
+    h = tbe.tbe_layer_norm_create(64, torch.bfloat16, weight=False, bias=False)
+    x = torch.zeros((4, 64), dtype=torch.bfloat16, device="cuda")
+    out, total, stats = tbe.tbe_layer_norm_forward(h, x)
+    for kw in (dict(weight=x[0]), dict(bias=x[0])):
+        with pytest.raises(ValueError):
+            tbe.tbe_layer_norm_forward(h, x, **kw)
+    for kw in (dict(weight=x[0]), dict(grad_weight=x[0].clone()), dict(grad_bias=x[0].clone())):
+        with pytest.raises(ValueError):
+            tbe.tbe_layer_norm_backward(h, total, stats, x, **kw)
