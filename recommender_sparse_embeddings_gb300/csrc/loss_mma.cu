@@ -1,4 +1,5 @@
-// The softmax loss's tensor-core kernel; see loss_mma.cuh.
+// The softmax loss's forward kernel and the backward pass's for wide operands, on
+// the tensor cores; see loss_mma.cuh.
 #include "loss_mma.cuh"
 
 namespace tbe {

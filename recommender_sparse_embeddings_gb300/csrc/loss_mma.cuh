@@ -5,11 +5,13 @@
 //   scores   S = X W^T            (rows x items, over the D columns)
 //   gx       dX += d W            (rows x columns, over the items)
 //   gw       dW = d^T X           (items x columns, over the rows)
-// and one kernel runs them all.  A persistent CTA per SM takes work items in
-// turn; warp 8 fetches operand tiles by TMA, warp 9 issues the products (128 x
-// up to 256, fp32 in tensor memory, two accumulators of 256 columns), warps 0
-// to 7 read the accumulators: one item's arithmetic runs under the next item's
-// products.  X, W and d lie row by row in memory; the products read them
+// The forward pass takes the scores alone; the backward pass all three, up to 256
+// columns (fp32: 128) in the fused kernel and above in the step kernel, with d in
+// memory.  The forward and the step kernel: a persistent CTA per SM takes work items
+// in turn; one warp fetches operand tiles by TMA, one issues the products (128 x up
+// to 256, fp32 in tensor memory, two accumulators of 256 columns), and the first 16
+// (step kernel: 8) read the accumulators: one item's arithmetic runs under the next
+// item's products.  X, W and d lie row by row in memory; the products read them
 // K-major or MN-major by the descriptor alone, so nothing is transposed.
 //
 // fp32.  An fp32 number is the sum of three bf16 numbers exactly (8 bits each,
@@ -150,7 +152,7 @@ constexpr int kLossThreads = 320;
 constexpr int kLossStages = 4;
 // Blocks between two such additions: the drift grows with them and so does the
 // time without (2050 x 20011 x 96 fp32, plain fp32 torch 7.2e-7 off; fused: 4 235 us
-// and 4.8e-7, 6 211 us and 6.5e-7, 8 203 us and 8.8e-7, 16 189 us and 1.7e-6).
+// and 4.8e-7, 6 211 us and 6.7e-7, 8 203 us and 8.8e-7, 16 189 us and 1.7e-6).
 constexpr int kFlush = 8, kFusedFlush = 6;
 constexpr int kBox = 64 * 64 * 2;  // bytes of a TMA box: 64 columns x 64 rows
 constexpr int kStageBytes = 6 * kBox;  // A: 2 boxes, B: 4
