@@ -595,7 +595,9 @@ int tbe_softmax_loss_forward(tbe_softmax_loss* h, const void* x, int64_t x_strid
 
 /* lse: the forward call's.  grad_loss: device fp32 [N].  grad_x: device dtype
  * [N, D], grad_table: device dtype [V, D], both contiguous and written, not
- * added to; either may be NULL (not wanted; the other has the same bits). */
+ * added to; either may be NULL (not wanted; the other has the same bits).
+ * Neither may share memory with the table or the other (INVALID_ARG); grad_x may
+ * be x itself. */
 int tbe_softmax_loss_backward(tbe_softmax_loss* h, const void* x, int64_t x_stride, const void* table,
                               int64_t table_stride, const void* targets, int32_t index_dtype, int64_t num_rows,
                               int64_t num_items, const float* lse, const float* grad_loss, void* grad_x,

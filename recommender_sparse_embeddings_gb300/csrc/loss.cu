@@ -1,6 +1,7 @@
 // Softmax cross entropy of rows over a table of items, and its gradients.
 // Declarations, formulas and contracts are in include/tbe.h.
 #include <algorithm>
+#include <mutex>
 #include <new>
 
 #include <nvtx3/nvToolsExt.h>
@@ -19,7 +20,10 @@ struct tbe_softmax_loss {
     int num_sms = 0;
     tbe_softmax_loss_config c{};
     uint32_t* error = nullptr;
-    // the last sizes' slices (the choice takes the host 5 us, as long as a launch)
+    // the last sizes' slices (the choice takes the host 5 us, as long as a launch).
+    // Under a lock: workspaces are laid out for the slices of their own sizes, so a
+    // handle used from two host threads against the rules must not mix them up.
+    mutable std::mutex choice_mu;
     mutable struct {
         int64_t rows = -1, items = -1;
         int slices;
@@ -209,6 +213,12 @@ int check(const tbe_softmax_loss* h, const void* x, int64_t x_stride, const void
     if (N < 0 || V < 0 || (N > 0 && (V == 0 || !x || !table || !targets))) return TBE_ERR_INVALID_ARG;
     if (x_stride < 0 || (V > 1 && table_stride < h->c.dim)) return TBE_ERR_INVALID_ARG;
     return within_limits(N, V) ? TBE_OK : TBE_ERR_UNSUPPORTED;
+}
+
+// Whether two blocks share bytes (either may be NULL).
+bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+    return a && b && x < y + (uintptr_t)b_bytes && y < x + (uintptr_t)a_bytes;
 }
 
 // ---- workspaces and plans
@@ -401,13 +411,16 @@ int forward(const tbe_softmax_loss* h, const Plan& L, LossForward p, const void*
             L.w_bytes};
     const int64_t whole = w.is_direct ? p.V : std::min(p.V, L.span);
     p.row_tiles = (int)L.row_tiles;
-    auto& last = h->forward_choice;
-    if (last.rows != L.row_tiles || last.items != whole) {
-        last.slices = choose_slices(L.row_tiles, (whole + 255) / 256, h->num_sms);
-        last.rows = L.row_tiles;
-        last.items = whole;
+    {
+        std::lock_guard<std::mutex> lock(h->choice_mu);
+        auto& last = h->forward_choice;
+        if (last.rows != L.row_tiles || last.items != whole) {
+            last.slices = choose_slices(L.row_tiles, (whole + 255) / 256, h->num_sms);
+            last.rows = L.row_tiles;
+            last.items = whole;
+        }
+        p.slices = last.slices;
     }
-    p.slices = last.slices;
     p.part = at<float2>(base, L.d);
     p.picked = at<float>(base, L.rows);
     for (p.v0 = 0; p.v0 < p.V; p.v0 = p.v1) {
@@ -501,16 +514,19 @@ int backward_fused(const tbe_softmax_loss* h, const Plan& L, LossFused p, const 
     p.w.part = at<float4>(base, L.w_part);
     p.w.first = p.w.last = 1;
     p.w.tiles = (int)((whole + 127) / 128);
-    auto& last = h->backward_choice;
-    if (last.rows != p.N || last.items != whole) {
-        choose_sides(&p.x, &p.w, p.D, h->num_sms);  // (of both, so that one alone has the same bits)
-        last.x = p.x.slices;
-        last.w = p.w.slices;
-        last.rows = p.N;
-        last.items = whole;
+    {
+        std::lock_guard<std::mutex> lock(h->choice_mu);
+        auto& last = h->backward_choice;
+        if (last.rows != p.N || last.items != whole) {
+            choose_sides(&p.x, &p.w, p.D, h->num_sms);  // (of both, so that one alone has the same bits)
+            last.x = p.x.slices;
+            last.w = p.w.slices;
+            last.rows = p.N;
+            last.items = whole;
+        }
+        p.x.slices = last.x;
+        p.w.slices = last.w;
     }
-    p.x.slices = last.x;
-    p.w.slices = last.w;
     if (!gx) p.x.tiles = 0;
     for (p.v0 = 0; p.v0 < p.V; p.v0 = p.v1) {
         p.v1 = std::min(p.V, p.v0 + whole);
@@ -721,6 +737,12 @@ int tbe_softmax_loss_backward(tbe_softmax_loss* h, const void* x, int64_t x_stri
         return status(cudaMemsetAsync(grad_table, 0, (size_t)V * h->c.dim * elem_bytes(h->c.dtype), s));
     }
     if (!grad_x && !grad_table) return TBE_OK;
+    // (x is copied before a gradient is written; the table is read where it is)
+    const int64_t bytes = elem_bytes(h->c.dtype), x_bytes = N * h->c.dim * bytes, w_bytes = V * h->c.dim * bytes;
+    const int64_t table_bytes = ((V - 1) * table_stride + h->c.dim) * bytes;
+    if (overlap(grad_x, x_bytes, table, table_bytes) || overlap(grad_table, w_bytes, table, table_bytes) ||
+        overlap(grad_x, x_bytes, grad_table, w_bytes))
+        return TBE_ERR_INVALID_ARG;
     const Plan L = make_plan(h, N, V, true, !direct(h, table, table_stride, V));
     RowsIn rows{};
     rows.x = make_copy(h, x, x_stride, N, L.pitch, nullptr);

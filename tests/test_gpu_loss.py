@@ -203,6 +203,25 @@ def test_results_off_16_byte_boundaries(dtype):
             assert t[0] == 7.0 and (t[-2:] == 7.0).all()
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("d", [64, 264])
+def test_results_in_the_place_of_operands(dtype, d):
+    """grad_x may be x; a gradient over the table, or both in one place, are refused before anything is written."""
+    c = Case(dtype, 150, 150, d, seed=d)
+    want = c.run()
+    for kw in (dict(grad_x=c.table), dict(grad_table=c.table), dict(grad_x=c.x, grad_table=c.x),
+               dict(grad_x=c.table, want=(True, False)), dict(grad_table=c.table, want=(False, True))):
+        with pytest.raises(tbe.TBEError) as e:
+            tbe.tbe_softmax_loss_backward(c.h, c.x, c.table, c.targets, want["lse"], c.grad, **kw)
+        assert e.value.code == tbe.TBE_ERR_INVALID_ARG
+    both = torch.empty((299, d), dtype=dtype, device="cuda")  # (they share a row)
+    with pytest.raises(tbe.TBEError) as e:
+        tbe.tbe_softmax_loss_backward(c.h, c.x, c.table, c.targets, want["lse"], c.grad, both[:150], both[149:])
+    assert e.value.code == tbe.TBE_ERR_INVALID_ARG
+    gx, gw = tbe.tbe_softmax_loss_backward(c.h, c.x, c.table, c.targets, want["lse"], c.grad, grad_x=c.x)
+    assert gx is c.x and torch.equal(gx, want["grad_x"]) and torch.equal(gw, want["grad_table"])
+
+
 def test_two_handles_on_two_streams():
     """Calls of two handles whose work overlaps share nothing."""
     a, b = Case(torch.bfloat16, 900, 6000, 128, seed=1), Case(torch.float32, 400, 3001, 96, seed=2)
