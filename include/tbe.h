@@ -558,9 +558,10 @@ int tbe_layer_norm_backward(tbe_layer_norm* h, const void* total, int64_t total_
  * where it enters the gradients' products (with fp16 times 2^14: g may be of any
  * size and the weights down to 2^-28, the gradients have to fit fp16).  fp32
  * operands enter the products as three bf16 terms that sum to them exactly; the
- * six products of those terms that matter to fp32 are summed, and long sums are
- * added up in parts.  x and the table are expected to be finite (fp32: below
- * 3.39e38), x in rows that are not left out.
+ * six products of those terms that matter to fp32 are summed.  The gradients' long
+ * sums are added up in fp32 in parts, of 32,768 rows or items at most (fp32: 512).
+ * x and the table are expected to be finite (fp32: below 3.39e38), x in rows that
+ * are not left out.
  *
  * Results are deterministic.  Rows start at data + row * stride (elements,
  * >= D for the table, >= 0 for x).  The fastest path wants 16-bit rows that are

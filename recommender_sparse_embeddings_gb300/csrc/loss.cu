@@ -293,7 +293,10 @@ Plan make_plan(const tbe_softmax_loss* h, int64_t N, int64_t V, bool backward, b
         const size_t tile = (size_t)L.cols4 * 128 * sizeof(float4);
         // (one sum over all items needs no slabs, and several make kMostParts tiles at most)
         L.x_part = take(std::max<int64_t>(L.row_tiles, kMostParts / L.col_tiles + 1) * tile);
-        L.w_part_bytes = (kMostParts / L.col_tiles + 1) * tile;
+        // (the fused kernel's long sums of 16-bit types over the rows: a slab of each tile of items)
+        const int64_t long_tiles =
+            fused && L.planes == 1 && N > kLongSum ? (copied ? std::min(padded, L.span) : padded) / 128 : 0;
+        L.w_part_bytes = (size_t)std::max<int64_t>(kMostParts / L.col_tiles + 1, long_tiles) * tile;
         L.w_part = take((fused ? 1 : 2) * L.w_part_bytes);
         if (!fused) {
             L.d_bytes = align_up((size_t)std::min(std::max(room, 256 * N), N * padded) * 2 * L.planes);
@@ -506,6 +509,7 @@ int backward_fused(const tbe_softmax_loss* h, const Plan& L, LossFused p, const 
     Table w{h, table, table_stride, p.V, L.span, L.planes, L.pitch, direct(h, table, table_stride, p.V), base + L.w, L.w_bytes};
     const int64_t whole = w.is_direct ? p.V : std::min(p.V, L.span);
     const int walked = loss_fused_walk(p.D, L.planes);  // lines of a tile along the sum
+    const int flush = loss_fused_flush(p.D, L.planes);
     p.x.tiles = (int)L.row_tiles;
     p.x.others = (int)((whole + walked - 1) / walked);
     p.x.part = at<float4>(base, L.x_part);
@@ -537,9 +541,9 @@ int backward_fused(const tbe_softmax_loss* h, const Plan& L, LossFused p, const 
         p.x.others = (int)((p.v1 - p.v0 + walked - 1) / walked);
         p.x.first = p.v0 == 0;
         p.x.last = p.v1 == p.V;
-        // (fp32's results take the parts of a sum as they come)
-        p.x.direct = p.x.slices == 1 && (L.planes == 3 || (p.x.first && p.x.last));
-        p.w.direct = p.w.slices == 1;
+        // (fp32's results take the parts of a sum as they come, 16-bit ones a whole sum)
+        p.x.direct = p.x.slices == 1 && (L.planes == 3 || (p.x.first && p.x.last && p.x.others <= flush));
+        p.w.direct = p.w.slices == 1 && (L.planes == 3 || p.w.others <= flush);
         p.w.tiles = gw ? (int)((p.v1 - p.v0 + 127) / 128) : 0;
         p.w.out = gw ? static_cast<char*>(gw) + p.v0 * p.D * elem_bytes(dt) : nullptr;
         e = launch_loss_fused(p, maps, dt, s);
@@ -610,7 +614,7 @@ int backward(const tbe_softmax_loss* h, const Plan& L, LossStep p, const RowsIn&
     const int64_t piece = std::min(L.piece, p.V), item_tiles = (piece + 127) / 128;
     const int64_t row_blocks = (p.N + 63) / 64, piece_blocks = (piece + 63) / 64;
     const int64_t products = L.row_tiles * L.col_tiles * piece_blocks + item_tiles * L.col_tiles * row_blocks;
-    const int64_t share = std::max<int64_t>(4, products / (h->num_sms * 2));
+    const int64_t share = std::clamp<int64_t>(products / (h->num_sms * 2), 4, kLongSum / 64);
     auto slabs = [&](int64_t blocks, int64_t tiles) {
         const int64_t most = std::max<int64_t>(1, kMostParts / std::max<int64_t>(tiles, 1));
         return (int)std::min({most, blocks, (blocks + share - 1) / share});

@@ -32,6 +32,7 @@ constexpr int kFusedThreads = 608;
 template <int DP, int P>
 struct Fused {
     static constexpr int BN = loss_fused_walk(DP, P);  // lines of a walked tile
+    static constexpr int kFlushTiles = loss_fused_flush(DP, P);
     static constexpr int kHeldPlane = 128 * DP * 2, kTilePlane = BN * DP * 2;
     static constexpr int kHeld = P * kHeldPlane, kTile = P * kTilePlane;
     static constexpr int kStages = P == 3 ? (DP == 64 ? 5 : 2) : DP == 64 ? 6 : DP == 256 ? 4 : 5;
@@ -135,7 +136,7 @@ template <int DT, int DP, int P, bool ITEMS>
 __device__ __forceinline__ bool fused_body(const LossFused& p, const LossSide& side, const LossFusedMaps& maps, int cta,
                                            unsigned char* smem, FusedBars& bars, uint32_t tmem) {
     using L = Fused<DP, P>;
-    constexpr int kStages = L::kStages, BN = L::BN;
+    constexpr int kStages = L::kStages, BN = L::BN, kFlushTiles = L::kFlushTiles;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     // the CTA's tile and the n tiles from `from` on that it walks
     const int tile = cta % side.tiles, slice = cta / side.tiles;
@@ -230,9 +231,9 @@ __device__ __forceinline__ bool fused_body(const LossFused& p, const LossSide& s
             for (int i = 0; i < n && ok; ++i) {
                 const int st = i % kStages, buf = i & 1;
                 ok = wait(&bars.d_full[buf], i / 2);
-                // fp32: the sums begin anew every kFusedFlush tiles, once these are in memory
-                const bool begins = P == 3 ? i % kFusedFlush == 0 : i == 0;
-                if (ok && begins && i > 0) ok = wait(&bars.sums_free, i / kFusedFlush - 1);
+                // the sums begin anew every kFlushTiles tiles, once these are in memory
+                const bool begins = i % kFlushTiles == 0;
+                if (ok && begins && i > 0) ok = wait(&bars.sums_free, i / kFlushTiles - 1);
                 if (!ok) break;
                 if (elect_one()) {
                     const uint64_t b = walk + (uint64_t)(st * (L::kTile / 16));
@@ -251,7 +252,7 @@ __device__ __forceinline__ bool fused_body(const LossFused& p, const LossSide& s
                     mma_commit(&bars.done[buf]);
                     if (i + 1 == n)
                         mma_commit(&bars.last);
-                    else if (P == 3 && i % kFusedFlush == kFusedFlush - 1)
+                    else if (i % kFlushTiles == kFlushTiles - 1)
                         mma_commit(&bars.sums_full);
                 }
                 __syncwarp();
@@ -286,86 +287,77 @@ __device__ __forceinline__ bool fused_body(const LossFused& p, const LossSide& s
             else if (side.direct)
                 store_rows<DT, 4>(side.out, row * p.D, acc, wide, warp / 4, valid, p.D, p.D % 8 == 0, unit);
             else
-                add_slab<4>(part, acc, wide, warp / 4, first);
+                add_slab<4, 16>(part, acc, wide, warp / 4, first);
             ++flushed;
-        };
-        auto flush = [&]() {
-            ok = mbar_wait_tight(&bars.sums_full, flushed & 1);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) return;
-            tcgen05_after_sync();
-            put();
-            tcgen05_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars.sums_free);
         };
         // the first tile's first item of the thread's half (V < 2^31)
         const int item0 = (int)(p.v0 + (int64_t)(from + buf) * BN) + group * (BN / 2);
         int left = (int)p.v1 - item0, at = target - item0, st = buf;
         if (target < 0) at = -1;
         const int mine = (int)(p.v0 + (int64_t)tile * 128) + line;
+        int i = buf;
 #pragma unroll 1
-        for (int i = buf; i < n; i += 2, left -= 2 * BN, at -= 2 * BN) {
-            // (before this tile's d, whose place the product behind the flush frees)
-            if (P == 3 && i / kFusedFlush > flushed) {
-                flush();
-                if (!ok) break;
-            }
-            ok = mbar_wait_tight(&bars.s_full[buf], (i / 2) & 1);
-            if (ITEMS && ok) ok = mbar_wait_tight(&bars.full[st], (i / kStages) & 1);  // the rows' values
-            if (!__all_sync(0xffffffffu, ok)) {
-                ok = false;
-                break;
-            }
-            tcgen05_after_sync();
-            const float* stats = reinterpret_cast<const float*>(smem + L::stats + st * L::kStats) + group * (BN / 2);
-            st = st + 2 < kStages ? st + 2 : st + 2 - kStages;
-#pragma unroll
-            for (int h = 0; h < BN / 2; h += 32) {
-                float x[32];
-                tmem_ld32_issue(tmem + buf * BN + group * (BN / 2) + h + lanes, x);
-                tmem_wait_ld(x, 32);
-                if (h + 32 == BN / 2) {
-                    tcgen05_before_sync();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bars.s_read[buf]);
+        while (ok) {  // the tiles of one accumulator, then its way to memory
+            const int end = tmin(n, (flushed + 1) * kFlushTiles);
+#pragma unroll 1
+            for (; i < end; i += 2, left -= 2 * BN, at -= 2 * BN) {
+                ok = mbar_wait_tight(&bars.s_full[buf], (i / 2) & 1);
+                if (ITEMS && ok) ok = mbar_wait_tight(&bars.full[st], (i / kStages) & 1);  // the rows' values
+                if (!__all_sync(0xffffffffu, ok)) {
+                    ok = false;
+                    break;
                 }
-                gradients<DT, P, ITEMS, BN>(x, p.c2, minus_lse, coef, at - h, left - h, stats + h, mine);
-                // d's columns are free of the last but one product (fp32: of the last)
-                if (h == 0 && (P == 3 ? i >= 1 : i >= 2)) {
-                    ok = P == 3 ? mbar_wait_tight(&bars.done[buf ^ 1], ((i - 1) / 2) & 1)
-                                : mbar_wait_tight(&bars.done[buf], (i / 2 - 1) & 1);
-                    ok = __all_sync(0xffffffffu, ok);
-                    tcgen05_after_sync();
-                }
+                tcgen05_after_sync();
+                const float* stats = reinterpret_cast<const float*>(smem + L::stats + st * L::kStats) + group * (BN / 2);
+                st = st + 2 < kStages ? st + 2 : st + 2 - kStages;
 #pragma unroll
-                for (int plane = 0; plane < P; ++plane) {
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int c = 0; c < 16; ++c) {
-                        pk[c] = pack2<DT>(x[2 * c], x[2 * c + 1]);
-                        if (plane + 1 < P) {
-                            x[2 * c] -= __uint_as_float(pk[c] << 16);
-                            x[2 * c + 1] -= __uint_as_float(pk[c] & 0xffff0000u);
-                        }
+                for (int h = 0; h < BN / 2; h += 32) {
+                    float x[32];
+                    tmem_ld32_issue(tmem + buf * BN + group * (BN / 2) + h + lanes, x);
+                    tmem_wait_ld(x, 32);
+                    if (h + 32 == BN / 2) {
+                        tcgen05_before_sync();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bars.s_read[buf]);
                     }
-                    tmem_st16(tmem + L::d + buf * L::kD + plane * (BN / 2) + group * (BN / 4) + h / 2 + lanes, pk);
+                    gradients<DT, P, ITEMS, BN>(x, p.c2, minus_lse, coef, at - h, left - h, stats + h, mine);
+                    // d's columns are free of the last but one product (fp32: of the last)
+                    if (h == 0 && (P == 3 ? i >= 1 : i >= 2)) {
+                        ok = P == 3 ? mbar_wait_tight(&bars.done[buf ^ 1], ((i - 1) / 2) & 1)
+                                    : mbar_wait_tight(&bars.done[buf], (i / 2 - 1) & 1);
+                        ok = __all_sync(0xffffffffu, ok);
+                        tcgen05_after_sync();
+                    }
+#pragma unroll
+                    for (int plane = 0; plane < P; ++plane) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) {
+                            pk[c] = pack2<DT>(x[2 * c], x[2 * c + 1]);
+                            if (plane + 1 < P) {
+                                x[2 * c] -= __uint_as_float(pk[c] << 16);
+                                x[2 * c + 1] -= __uint_as_float(pk[c] & 0xffff0000u);
+                            }
+                        }
+                        tmem_st16(tmem + L::d + buf * L::kD + plane * (BN / 2) + group * (BN / 4) + h / 2 + lanes, pk);
+                    }
                 }
+                if (!ok) break;
+                tmem_wait_st();
+                tcgen05_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars.d_full[buf]);
             }
+            // (barriers of their own: `done` of the other buffer may be two phases back)
+            if (ok) ok = end == n ? mbar_wait_tight(&bars.last, 0) : mbar_wait_tight(&bars.sums_full, flushed & 1);
+            ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
-            tmem_wait_st();
-            tcgen05_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars.d_full[buf]);
-        }
-        if (P == 3)
-            while (ok && (n - 1) / kFusedFlush > flushed) flush();
-        // (a barrier of its own: `done` of the other buffer may be two phases back)
-        if (ok) ok = mbar_wait_tight(&bars.last, 0);
-        ok = __all_sync(0xffffffffu, ok);
-        if (ok) {
             tcgen05_after_sync();
             put();
+            if (end == n) break;
+            tcgen05_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.sums_free);
         }
     }
     return ok;

@@ -344,13 +344,16 @@ __global__ void __launch_bounds__(kLossThreads, 1)
     const int products = p.n_gw + p.n_gx, results = products + p.n_d, n_items = results + p.n_fin_w + p.n_fin_x;
     int a = blockIdx.x, b = products + p.d_from[blockIdx.x], f = results + blockIdx.x;
     const int b_end = products + p.d_from[blockIdx.x + 1];
-    int rest = 0;  // blocks of the item that are still to come (fp32: its sum goes to memory in parts)
+    // blocks of the item that are still to come: its sum goes to memory in parts (with
+    // 16-bit types a sum that goes to the result at once is short enough)
+    constexpr int kPart = P == 3 ? kFlush : kLongSum / 64;
+    int rest = 0;
     auto next = [&](Product& t) {
         for (;;) {
             int i;
-            if (P == 3 && rest > 0) {
+            if (rest > 0) {
                 t.k0 += t.kblocks;
-                t.kblocks = tmin(rest, kFlush);
+                t.kblocks = tmin(rest, kPart);
                 t.begins = false;
                 rest -= t.kblocks;
                 return true;
@@ -369,10 +372,8 @@ __global__ void __launch_bounds__(kLossThreads, 1)
             t = step_item(p, i);
             if (t.kind > ITEM_GX) return true;
             if (t.kblocks == 0) continue;  // (the last piece has fewer blocks than slabs)
-            if (P == 3) {
-                rest = tmax(0, t.kblocks - kFlush);
-                t.kblocks -= rest;
-            }
+            rest = tmax(0, t.kblocks - kPart);
+            t.kblocks -= rest;
             return true;
         }
     };

@@ -18,11 +18,15 @@
 // rounded to nearest, the rest carried on).  fp32 operands are kept as three
 // such planes, and a product is the sum of the six plane products of at least
 // 2^-18 of the whole, the small ones first; the three left out are below 2^-26,
-// less than an fp32 rounding.  The tensor units cut an fp32 sum at every addition
-// instead of rounding it, so long sums drift: 20,011 items in one accumulator
-// made grad_x 2.2e-5 off.  fp32's large products (of the first planes) therefore
-// come last or have an accumulator of their own, which is added, rounded, to a sum
-// in memory every kFlush (fused: kFusedFlush) blocks of 64 along the sum.
+// less than an fp32 rounding.
+//
+// Long sums.  The tensor units cut an fp32 sum at every addition instead of
+// rounding it, so long sums drift towards 0: 20,011 items in one accumulator made
+// fp32's grad_x 2.2e-5 off, 1,000,000 made fp16's 1.2e-3 off, where its rounding is
+// 2.1e-4.  An accumulator is therefore added, rounded, to a sum in memory and begun
+// anew every kFlush (fused: kFusedFlush) blocks of 64 along the sum with fp32, whose
+// large products (of the first planes) come last or have an accumulator of their
+// own, and every kLongSum rows or items with 16-bit types.
 #pragma once
 
 #include <cuda.h>
@@ -53,22 +57,25 @@ __device__ __forceinline__ void store8(void* out, int64_t at, const float* x) {
     }
 }
 
-// The accumulator's 32-column chunks of this warpgroup (one of GROUPS) into
+// The accumulator's chunks of W columns of this warpgroup (one of GROUPS) into
 // a slab of partial sums: [columns / 4][128 rows] of float4, so that a warp's
 // 32 rows are 512 consecutive bytes.
-template <int GROUPS>
+template <int GROUPS, int W = 32>
 __device__ __forceinline__ void add_slab(float4* to, uint32_t acc, int wide, int group, bool first) {
-    for (int c = group * 32; c < wide; c += 32 * GROUPS) {
-        float x[32];
-        tmem_ld32_issue(acc + c, x);
-        float4 old[8];
+    for (int c = group * W; c < wide; c += W * GROUPS) {
+        float x[W];
+        if constexpr (W == 32)
+            tmem_ld32_issue(acc + c, x);
+        else
+            tmem_ld16(acc + c, x);
+        float4 old[W / 4];
         if (!first) {
 #pragma unroll
-            for (int q = 0; q < 8; ++q) old[q] = to[(c / 4 + q) * 128];
+            for (int q = 0; q < W / 4; ++q) old[q] = to[(c / 4 + q) * 128];
         }
-        tmem_wait_ld(x, 32);
+        if (W == 32) tmem_wait_ld(x, W);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
+        for (int q = 0; q < W / 4; ++q) {
             float4 v = make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
             if (!first) v.x += old[q].x, v.y += old[q].y, v.z += old[q].z, v.w += old[q].w;
             to[(c / 4 + q) * 128] = v;
@@ -154,6 +161,11 @@ constexpr int kLossStages = 4;
 // time without (2050 x 20011 x 96 fp32, plain fp32 torch 7.2e-7 off; fused: 4 235 us
 // and 4.8e-7, 6 211 us and 6.7e-7, 8 203 us and 8.8e-7, 16 189 us and 1.7e-6).
 constexpr int kFlush = 8, kFusedFlush = 6;
+// 16-bit types: rows or items, 16 of them a product; a cut loses 2^-25 of the final
+// sum on average, so 32,768 drift by 6e-5, a third of fp16's rounding.
+// (10,000 x 1,000,000 x 128 f16: 1.18e-3 off without, 2.1e-4 with, 5.39 and 5.34 ms;
+// 131,072 x 40,000 x 64 f16: 2.81 and 2.89 ms.)
+constexpr int kLongSum = 32768;
 constexpr int kBox = 64 * 64 * 2;  // bytes of a TMA box: 64 columns x 64 rows
 constexpr int kStageBytes = 6 * kBox;  // A: 2 boxes, B: 4
 constexpr int kStagingBytes = 4096;    // of a warp: 32 rows x 64 columns of d
@@ -275,6 +287,10 @@ cudaError_t loss_mma_configure();
 cudaError_t loss_fused_configure();
 // Lines of the tiles that the fused kernel walks.
 constexpr int loss_fused_walk(int D, int planes) { return D <= 128 && planes == 1 ? 128 : 64; }
+// Such tiles that one of its accumulators takes.
+constexpr int loss_fused_flush(int D, int planes) {
+    return planes == 3 ? kFusedFlush : kLongSum / loss_fused_walk(D, planes);
+}
 cudaError_t launch_loss_fused(const LossFused& p, const LossFusedMaps& maps, int dtype, cudaStream_t s);
 cudaError_t launch_loss_finish(const LossFinish& p, int dtype, cudaStream_t s);
 cudaError_t launch_loss_forward(const LossForward& p, const LossMaps& maps, int dtype, int grid, cudaStream_t s);

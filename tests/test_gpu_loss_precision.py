@@ -1,0 +1,103 @@
+"""How exact the softmax loss is, by the 2-norm of its errors against 64 bits (the element by element bounds of the
+other tests have to allow for the worst case of every sum).
+
+Bounds, of the norm of the result.  A result rounded to fp16 is 2.1e-4 off (2^-11 / sqrt(3), values within a factor of
+two of each other: times 0.75 on average), and no more comes from d's rounding: together sqrt(2) of that, 3.0e-4; bf16
+eight times that, 2.4e-3.  The tensor units cut each sum of 16 products' terms by up to 2^-23 of the sum so far, which
+for a sum that grows evenly is 2^-25 of its final value on average (half the cut, half the sum): k products in one
+accumulator shrink the result by k 2^-25.
+"""
+
+import pytest
+import torch
+
+import recommender_sparse_embeddings_gb300 as tbe
+
+pytestmark = pytest.mark.gpu
+FP16, BF16, FP32 = torch.float16, torch.bfloat16, torch.float32
+
+
+class Case:
+    def __init__(self, dtype, n, v, d, seed=1, targets_from=0):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        self.x = torch.randn((n, d), generator=g, device="cuda").to(dtype)
+        self.table = (torch.randn((v, d), generator=g, device="cuda") * 1.5 * d ** -0.5).to(dtype)
+        self.targets = torch.randint(targets_from, v, (n,), generator=g, device="cuda")
+        self.grad = torch.full((n,), 1024.0 if dtype == FP16 else 1.0, device="cuda")
+        self.h = tbe.tbe_softmax_loss_create(d, dtype)
+
+    def run(self):
+        self.loss, self.lse = tbe.tbe_softmax_loss_forward(self.h, self.x, self.table, self.targets)
+        self.grad_x, self.grad_table = tbe.tbe_softmax_loss_backward(self.h, self.x, self.table, self.targets, self.lse,
+                                                                     self.grad)
+        assert tbe.tbe_softmax_loss_get_error(self.h) == tbe.TBE_OK
+
+    def rows(self, at):
+        """loss, lse and grad_x of the rows `at` in 64 bits, and the target's own term of grad_x."""
+        w, t = self.table.double(), self.targets[at]
+        s = self.x[at].double() @ w.t()
+        lse = torch.logsumexp(s, 1)
+        hot = w[t] * self.grad[at].double()[:, None]
+        return lse - s.gather(1, t[:, None])[:, 0], lse, torch.softmax(s, 1) @ w * self.grad[at].double()[:, None] - hot, hot
+
+    def items(self, at):
+        """grad_table of the items `at`, the rows in parts."""
+        got = torch.zeros((len(at), self.x.shape[1]), dtype=torch.float64, device="cuda")
+        w = self.table[at].double()
+        for lo in range(0, self.x.shape[0], 65536):
+            x, t = self.x[lo:lo + 65536].double(), self.targets[lo:lo + 65536]
+            p = torch.exp(x @ w.t() - self.lse[lo:lo + 65536].double()[:, None]) - (t[:, None] == at[None, :]).double()
+            got += (p * self.grad[lo:lo + 65536].double()[:, None]).t() @ x
+        return got
+
+
+def off(got, want):
+    return ((got.double() - want).norm() / want.norm()).item()
+
+
+def shrunk(got, want):
+    return 1.0 - ((got.double() * want).sum() / (want * want).sum()).item()
+
+
+@pytest.mark.parametrize("dtype,n,v,d", [(FP16, 10000, 1000000, 128), (FP16, 16384, 400000, 256), (BF16, 10000, 1000000, 40)])
+def test_long_sums_over_the_items(dtype, n, v, d):
+    """Accumulators take 32,768 items at most: 2^-14, twice that for a cut's size within a power of two (1,000,000 in one
+    would be 2e-3).  What is left beside the target's own term, which would cover it, is compared."""
+    c = Case(dtype, n, v, d)
+    c.run()
+    at = torch.arange(0, n, n // 48, device="cuda")
+    _, _, want, hot = c.rows(at)
+    assert off(c.grad_x[at], want) < (3.0e-4 if dtype == FP16 else 2.4e-3) + 2 ** -13
+    if dtype == FP16:  # (bf16's rounding of 48 x 40 results leaves 2e-3 / 44 in the mean, times hot's size beside the rest)
+        assert abs(shrunk(c.grad_x[at].double() + hot, want + hot)) < 2 ** -13
+
+
+@pytest.mark.parametrize("dtype,n,v,d", [(FP16, 262144, 40000, 64), (FP16, 262144, 20000, 256), (FP16, 140000, 30001, 200),
+                                         (FP16, 33000, 60000, 64)])
+def test_long_sums_over_the_rows(dtype, n, v, d):
+    """The same of the table's gradient, of items that are nobody's target and of some that are; 30,001 x 200 columns
+    is copied in parts (its rows lie off 16-byte boundaries)."""
+    c = Case(dtype, n, v, d, targets_from=64)
+    if d == 200:
+        c.table = torch.cat([c.table, c.table[:, :1]], 1)[:, :d]
+    c.run()
+    at = torch.cat([torch.arange(64, device="cuda"), torch.tensor([v - 1, v - 200, v // 2], device="cuda")])
+    want = c.items(at)
+    assert abs(shrunk(c.grad_table[at[:64]], want[:64])) < 2 ** -13
+    assert off(c.grad_table[at], want) < 3.0e-4 + 2 ** -13
+    at = torch.arange(0, n, n // 20, device="cuda")
+    assert off(c.grad_x[at], c.rows(at)[2]) < 3.0e-4 + 2 ** -13
+
+
+def test_long_sums_over_the_rows_of_wide_operands():
+    """Above 256 columns d passes through memory in pieces; here of 256 items, whose sums go over 36,864 rows each."""
+    c = Case(FP16, 700000, 250, 4096, targets_from=16)
+    c.run()
+    at = torch.tensor([0, 1, 7, 15, 16, 17, 128, 249], device="cuda")
+    got, want = c.grad_table[at], c.items(at)
+    # (1024 times a sum of 700,000 rows: results from 65520 on round to an infinity of fp16.  Within 1 % of it, 20 times
+    # the errors' norm below, either is right)
+    fits, beyond = want.abs() < 64865.0, want.abs() > 66175.0
+    assert torch.equal(got[beyond].double(), torch.copysign(torch.full_like(want, float("inf")), want)[beyond])
+    assert abs(shrunk(got[:4][fits[:4]], want[:4][fits[:4]])) < 2 ** -13
+    assert off(got[fits], want[fits]) < 3.0e-4 + 2 ** -13
