@@ -560,6 +560,8 @@ int tbe_layer_norm_backward(tbe_layer_norm* h, const void* total, int64_t total_
  * operands enter the products as three bf16 terms that sum to them exactly; the
  * six products of those terms that matter to fp32 are summed.  The gradients' long
  * sums are added up in fp32 in parts, of 32,768 rows or items at most (fp32: 512).
+ * A score of more than 512 columns is added up in parts of as many (but where it
+ * only serves a d of 16 bits).
  * x and the table are expected to be finite (fp32: below 3.39e38), x in rows that
  * are not left out.
  *

@@ -41,6 +41,15 @@ __device__ __forceinline__ Product score_tile(int64_t V, int D, int row0, int64_
     return Product{ITEM_D, row0, item, 0, (D + 63) / 64, columns_of(V - item), 0, ((D - 1) % 64 + 16) / 16, true};
 }
 
+// Its first part, or the one after t, of `part` blocks; `rest` are still to come then.
+__device__ __forceinline__ void score_part(Product& t, int D, int part, bool first, int& rest) {
+    t.k0 = first ? 0 : t.k0 + t.kblocks;
+    if (first) rest = (D + 63) / 64;
+    t.kblocks = tmin(rest, part);
+    rest -= t.kblocks;
+    t.last_steps = rest > 0 ? 4 : ((D - 1) % 64 + 16) / 16;
+}
+
 // Work item i of a backward launch: the long ones first.
 __device__ __forceinline__ Product step_item(const LossStep& p, int i) {
     Product t{};
@@ -241,6 +250,18 @@ __device__ bool multiply(unsigned char* smem, LossBars& bars, uint32_t tmem, Nex
     return ok;
 }
 
+// N columns of the thread's line of a part of the scores, added to x or stored there.
+template <bool ADD, int N>
+__device__ __forceinline__ void take_scores(float (&x)[N], uint32_t acc) {
+#pragma unroll
+    for (int c = 0; c < N; c += 16) {
+        float y[16];
+        tmem_ld16(acc + c, y);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[c + e] = ADD ? x[c + e] + y[e] : y[e];
+    }
+}
+
 // 32 columns of one row in staging: the warp's tile of 32 rows x 128 bytes in
 // the 128-byte swizzle.
 __device__ __forceinline__ void stage_row(unsigned char* staging, int lane, int half, const uint32_t* pk) {
@@ -328,8 +349,9 @@ __device__ __forceinline__ void end(uint32_t tmem, bool ok, uint32_t* error) {
     if (threadIdx.x / 32 == WARP) tmem_dealloc(tmem, 512);
 }
 
-// Backward pass: one launch's work items.
-template <int DT, int P>
+// Backward pass: one launch's work items.  PARTS (fp32, above 512 columns): a tile of
+// scores has several accumulators.
+template <int DT, int P, bool PARTS = false>
 __global__ void __launch_bounds__(kLossThreads, 1)
     loss_step_kernel(const LossStep p, const __grid_constant__ LossMaps maps) {
     extern __shared__ unsigned char smem_raw[];
@@ -347,10 +369,15 @@ __global__ void __launch_bounds__(kLossThreads, 1)
     // blocks of the item that are still to come: its sum goes to memory in parts (with
     // 16-bit types a sum that goes to the result at once is short enough)
     constexpr int kPart = P == 3 ? kFlush : kLongSum / 64;
+    const int part = PARTS ? score_part_blocks(p.D) : 0;
     int rest = 0;
     auto next = [&](Product& t) {
         for (;;) {
             int i;
+            if (PARTS && rest > 0 && t.kind == ITEM_D) {
+                score_part(t, p.D, part, false, rest);
+                return true;
+            }
             if (rest > 0) {
                 t.k0 += t.kblocks;
                 t.kblocks = tmin(rest, kPart);
@@ -370,6 +397,7 @@ __global__ void __launch_bounds__(kLossThreads, 1)
                 return false;
             }
             t = step_item(p, i);
+            if (PARTS && t.kind == ITEM_D) score_part(t, p.D, part, true, rest);
             if (t.kind > ITEM_GX) return true;
             if (t.kblocks == 0) continue;  // (the last piece has fewer blocks than slabs)
             rest = tmax(0, t.kblocks - kPart);
@@ -413,6 +441,35 @@ __global__ void __launch_bounds__(kLossThreads, 1)
             if (!ok) break;
             tcgen05_after_sync();
             const uint32_t acc = tmem + buf * 256 + ((uint32_t)(quarter * 32) << 16);
+            auto release = [&]() {
+                tcgen05_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars.acc_empty[tile & 1]);
+                ++tile;
+            };
+            if (PARTS && t.kind == ITEM_D) {
+                float x[128];
+                take_scores<false>(x, acc + group * 128);
+                release();
+                while (rest > 0) {
+                    next(t);
+                    ok = mbar_wait_tight(&bars.acc_full[tile & 1], (tile / 2) & 1);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    tcgen05_after_sync();
+                    take_scores<true>(x, tmem + (tile & 1) * 256 + ((uint32_t)(quarter * 32) << 16) + group * 128);
+                    release();
+                }
+                if (!ok) break;
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    const int c = group * 128 + s * 64;
+                    if (t.col0 + c >= p.V) break;
+                    d_slab<DT, P>(x + s * 64, minus_lse, coef, target, p.c2, t.col0 + c, p.V, staging, maps.d_out,
+                                  (int)(t.col0 - p.d0) + c, t.row0 + quarter * 32, p.N, lane);
+                }
+                continue;
+            }
             if (t.kind == ITEM_D) {
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
@@ -436,10 +493,7 @@ __global__ void __launch_bounds__(kLossThreads, 1)
                              quarter * 32 + lane;
                 add_slab<2>(to, acc, t.wide, group, t.begins && (t.kind == ITEM_GW || p.first));
             }
-            tcgen05_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars.acc_empty[buf]);
-            ++tile;
+            release();
         }
         if (lane == 0) store_wait();
     }
@@ -451,7 +505,8 @@ __global__ void __launch_bounds__(kLossThreads, 1)
 // each) carry in registers.  The maximum moves only when 32 terms' sum against the
 // last one exceeds 2^13 (below, an fp32 sum loses nothing by it); otherwise no
 // maximum is looked for (a third of the loop's instructions).
-template <int DT, int P>
+// PARTS: above 512 columns, a tile has several accumulators.
+template <int DT, int P, bool PARTS>
 __global__ void __launch_bounds__(kForwardThreads, 1)
     loss_forward_kernel(const LossForward p, const __grid_constant__ LossMaps maps) {
     extern __shared__ unsigned char smem_raw[];
@@ -462,9 +517,14 @@ __global__ void __launch_bounds__(kForwardThreads, 1)
     chain_wait();
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int n_items = p.row_tiles * p.slices;
-    int item = blockIdx.x, tiles = 0;  // tiles: left of the item
+    const int part = PARTS ? score_part_blocks(p.D) : 0;
+    int item = blockIdx.x, tiles = 0, rest = 0;  // tiles: left of the item, rest: blocks of the tile
     // (called with the same t: all but an item's first tile only move it on)
     auto next = [&](Product& t) {
+        if (PARTS && rest > 0) {
+            score_part(t, p.D, part, false, rest);
+            return true;
+        }
         while (tiles == 0) {
             if (item >= n_items) return false;
             const int slice = item / p.row_tiles;
@@ -476,6 +536,7 @@ __global__ void __launch_bounds__(kForwardThreads, 1)
         }
         t.col0 += 256;
         t.wide = --tiles == 0 ? columns_of(p.v1 - t.col0) : 256;
+        if (PARTS) score_part(t, p.D, part, true, rest);
         return true;
     };
     bool ok = true;
@@ -491,7 +552,7 @@ __global__ void __launch_bounds__(kForwardThreads, 1)
         Product t;
         while (ok && next(t)) {
             const int count = tiles + 1;
-            tiles = 0;
+            tiles = rest = 0;
             const int64_t row = t.row0 + quarter * 32 + lane;
             float m = -INFINITY, l = 0.f, picked = 0.f;
             int left = (int)(p.v1 - t.col0) - group * 64;  // items from the quarter on
@@ -513,12 +574,17 @@ __global__ void __launch_bounds__(kForwardThreads, 1)
             const uint32_t acc0 = tmem + group * 64 + ((uint32_t)(quarter * 32) << 16);
 #pragma unroll 1
             for (int j = 0; j < count; ++j, ++tile, left -= 256, mine -= 256) {
-                const int buf = tile & 1;
-                ok = mbar_wait_tight(&bars.acc_full[buf], (tile / 2) & 1);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                tcgen05_after_sync();
-                const uint32_t acc = acc0 + buf * 256;
+                auto arrived = [&]() {
+                    ok = mbar_wait_tight(&bars.acc_full[tile & 1], (tile / 2) & 1);
+                    ok = __all_sync(0xffffffffu, ok);
+                    tcgen05_after_sync();
+                    return ok;
+                };
+                auto release = [&]() {
+                    tcgen05_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars.acc_empty[tile & 1]);
+                };
                 const bool picks = __any_sync(0xffffffffu, mine >= 0 && mine < 64);
                 // 32 columns from c on
                 auto take = [&](float (&x)[32], int c) {
@@ -554,11 +620,34 @@ __global__ void __launch_bounds__(kForwardThreads, 1)
                     }
                     l += s;
                 };
-                auto release = [&]() {
-                    tcgen05_before_sync();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bars.acc_empty[buf]);
-                };
+                if constexpr (PARTS) {
+                    float x[32], y[32];
+                    if (!arrived()) break;
+                    take_scores<false>(x, acc0 + (tile & 1) * 256);
+                    take_scores<false>(y, acc0 + (tile & 1) * 256 + 32);
+#pragma unroll 1
+                    for (int k = part; k < (p.D + 63) / 64; k += part) {
+                        release();
+                        ++tile;
+                        if (!arrived()) break;
+                        take_scores<true>(x, acc0 + (tile & 1) * 256);
+                        take_scores<true>(y, acc0 + (tile & 1) * 256 + 32);
+                    }
+                    if (!ok) break;
+                    release();
+                    if (left < 64) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            if (e >= left) x[e] = -INFINITY;
+                            if (e + 32 >= left) y[e] = -INFINITY;
+                        }
+                    }
+                    if (left > 0) take(x, 0);
+                    if (left > 32) take(y, 32);
+                    continue;
+                }
+                if (!arrived()) break;
+                const uint32_t acc = acc0 + (tile & 1) * 256;
                 if (left >= 64) {
                     float x[32], y[32];
                     tmem_ld32_issue(acc, x);
@@ -594,8 +683,12 @@ __global__ void __launch_bounds__(kForwardThreads, 1)
 template <int DT, int P>
 cudaError_t configure() {
     cudaError_t e = cudaFuncSetAttribute(loss_step_kernel<DT, P>, cudaFuncAttributeMaxDynamicSharedMemorySize, kLossSmem);
+    if (e == cudaSuccess && P == 3)
+        e = cudaFuncSetAttribute(loss_step_kernel<DT, P, P == 3>, cudaFuncAttributeMaxDynamicSharedMemorySize, kLossSmem);
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(loss_forward_kernel<DT, P>, cudaFuncAttributeMaxDynamicSharedMemorySize, kLossSmem);
+        e = cudaFuncSetAttribute(loss_forward_kernel<DT, P, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kLossSmem);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(loss_forward_kernel<DT, P, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kLossSmem);
     return e;
 }
 
@@ -608,17 +701,24 @@ cudaError_t loss_mma_configure() {
     return e;
 }
 
-cudaError_t launch_loss_forward(const LossForward& p, const LossMaps& maps, int dtype, int grid, cudaStream_t s) {
-    auto* kernel = dtype == DT_F32   ? loss_forward_kernel<DT_BF16, 3>
-                   : dtype == DT_F16 ? loss_forward_kernel<DT_F16, 1>
-                                     : loss_forward_kernel<DT_BF16, 1>;
+template <bool PARTS>
+static cudaError_t launch_forward(const LossForward& p, const LossMaps& maps, int dtype, int grid, cudaStream_t s) {
+    auto* kernel = dtype == DT_F32   ? loss_forward_kernel<DT_BF16, 3, PARTS>
+                   : dtype == DT_F16 ? loss_forward_kernel<DT_F16, 1, PARTS>
+                                     : loss_forward_kernel<DT_BF16, 1, PARTS>;
     return launch_chained_smem(kernel, dim3(grid), dim3(kForwardThreads), kLossSmem, s, p, maps);
 }
 
+cudaError_t launch_loss_forward(const LossForward& p, const LossMaps& maps, int dtype, int grid, cudaStream_t s) {
+    return p.D > kScorePart * 64 ? launch_forward<true>(p, maps, dtype, grid, s)
+                                 : launch_forward<false>(p, maps, dtype, grid, s);
+}
+
 cudaError_t launch_loss_step(const LossStep& p, const LossMaps& maps, int dtype, int grid, cudaStream_t s) {
-    auto* kernel = dtype == DT_F32   ? loss_step_kernel<DT_BF16, 3>
-                   : dtype == DT_F16 ? loss_step_kernel<DT_F16, 1>
-                                     : loss_step_kernel<DT_BF16, 1>;
+    auto* kernel = dtype == DT_F16          ? loss_step_kernel<DT_F16, 1>
+                   : dtype == DT_BF16       ? loss_step_kernel<DT_BF16, 1>
+                   : p.D <= kScorePart * 64 ? loss_step_kernel<DT_BF16, 3>
+                                            : loss_step_kernel<DT_BF16, 3, true>;
     return launch_chained_smem(kernel, dim3(grid), dim3(kLossThreads), kLossSmem, s, p, maps);
 }
 

@@ -26,7 +26,10 @@
 // 2.1e-4.  An accumulator is therefore added, rounded, to a sum in memory and begun
 // anew every kFlush (fused: kFusedFlush) blocks of 64 along the sum with fp32, whose
 // large products (of the first planes) come last or have an accumulator of their
-// own, and every kLongSum rows or items with 16-bit types.
+// own, and every kLongSum rows or items with 16-bit types.  A score is such a sum
+// too: above 512 columns it is taken in parts of up to kScorePart blocks of 64, which
+// are added up in registers (but for the d of 16-bit types, which is rounded to 8 or
+// 11 bits: its parts changed no error and took 8 to 12 % of the backward pass).
 #pragma once
 
 #include <cuda.h>
@@ -166,6 +169,14 @@ constexpr int kFlush = 8, kFusedFlush = 6;
 // (10,000 x 1,000,000 x 128 f16: 1.18e-3 off without, 2.1e-4 with, 5.39 and 5.34 ms;
 // 131,072 x 40,000 x 64 f16: 2.81 and 2.89 ms.)
 constexpr int kLongSum = 32768;
+// Blocks of 64 columns that a part of the scores has at most (an accumulator's error
+// of lse at 4096 columns: in one 8e-7, in parts of 8 1e-7), and has: equal parts.
+// Below, the kernels are built without parts (with them they lost 5 % at 512 columns).
+constexpr int kScorePart = 8;
+__host__ __device__ constexpr int score_part_blocks(int D) {
+    const int blocks = (D + 63) / 64, parts = (blocks + kScorePart - 1) / kScorePart;
+    return (blocks + parts - 1) / parts;
+}
 constexpr int kBox = 64 * 64 * 2;  // bytes of a TMA box: 64 columns x 64 rows
 constexpr int kStageBytes = 6 * kBox;  // A: 2 boxes, B: 4
 constexpr int kStagingBytes = 4096;    // of a warp: 32 rows x 64 columns of d

@@ -101,3 +101,23 @@ def test_long_sums_over_the_rows_of_wide_operands():
     assert torch.equal(got[beyond].double(), torch.copysign(torch.full_like(want, float("inf")), want)[beyond])
     assert abs(shrunk(got[:4][fits[:4]], want[:4][fits[:4]])) < 2 ** -13
     assert off(got[fits], want[fits]) < 3.0e-4 + 2 ** -13
+
+
+# A score of 4096 columns in parts of 512: 32 products each, cut by 32 2^-25 = 1e-6 of the part's size, which grows as a
+# random walk's (2/3 of its final value on average) and has a sign of its own: 6e-7 of a score's size, 1.5.  Of a loss
+# and lse of about 11 that is 1e-7 by the target's score and, as every score shrinks, E_p[s] 6e-7 / 11 = 1.2e-7 by lse:
+# 2e-7 together, and 1e-7 for fp32's roundings and the sum's.  In one accumulator it was 8e-7 to 1e-6.
+@pytest.mark.parametrize("dtype", [FP32, BF16, FP16])
+@pytest.mark.parametrize("n,v,d", [(300, 30000, 4096), (140, 9000, 2500), (300, 20000, 1000), (200, 5001, 577)])
+def test_scores_over_many_columns(dtype, n, v, d):
+    c = Case(dtype, n, v, d)
+    c.run()
+    at = torch.arange(n, device="cuda")
+    loss, lse, grad_x, _ = c.rows(at)
+    assert off(c.loss, loss) < 3e-7 and off(c.lse, lse) < 3e-7
+    # 16 bits: d's and the result's rounding.  fp32: weights off by their scores' 6e-7 times 1.5 and lse's 1e-6, one of
+    # which follows the other, and the sums' 32 products 1e-6
+    bound = {FP16: 3.0e-4, BF16: 2.4e-3, FP32: 2e-6}[dtype] + 2 ** -13 * (dtype != FP32)
+    assert off(c.grad_x, grad_x) < bound
+    at = torch.arange(0, v, 97, device="cuda")
+    assert off(c.grad_table[at], c.items(at)) < bound
