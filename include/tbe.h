@@ -554,16 +554,18 @@ int tbe_layer_norm_backward(tbe_layer_norm* h, const void* total, int64_t total_
  * maximum and sum, the backward call computes them again, tile by tile or in
  * pieces of the table.  dtype (fp32, fp16 or bf16) is that of x, the table and
  * the gradients; loss, lse and g are fp32.  Logits, statistics and sums are fp32.
- * With 16-bit types d, relative to the largest finite |g|, is rounded to dtype
- * where it enters the gradients' products (with fp16 times 2^14: g may be of any
- * size and the weights down to 2^-28, the gradients have to fit fp16).  fp32
- * operands enter the products as three bf16 terms that sum to them exactly; the
- * six products of those terms that matter to fp32 are summed.  The gradients' long
- * sums are added up in fp32 in parts, of 32,768 rows or items at most (fp32: 512).
- * A score of more than 512 columns is added up in parts of as many (but where it
- * only serves a d of 16 bits).
- * x and the table are expected to be finite (fp32: below 3.39e38), x in rows that
- * are not left out.
+ * With 16-bit types d is rounded to dtype where it enters the gradients' products
+ * (with fp16 times 2^14: weights down to 2^-28 keep all their bits; the gradients
+ * have to fit fp16): for grad_table relative to the largest finite |g|; for grad_x
+ * up to 256 columns without g, which multiplies the finished row, so g may be of any
+ * size, and above 256 columns as for grad_table, so with fp16 a row whose g is r
+ * times the largest keeps weights down to 2^-28 / r.  fp32 operands enter the
+ * products as three bf16 terms that sum to them exactly; the six products of those
+ * terms that matter to fp32 are summed.  The gradients' long sums are added up in
+ * fp32 in parts, of 32,768 rows or items at most (fp32: 512); a score of more than
+ * 512 columns in parts of as many (but where it only serves a d of 16 bits).  x and
+ * the table are expected to be finite (fp32: below 3.39e38), x in rows that are not
+ * left out.
  *
  * Results are deterministic.  Rows start at data + row * stride (elements,
  * >= D for the table, >= 0 for x).  The fastest path wants 16-bit rows that are

@@ -133,8 +133,10 @@ __global__ void __launch_bounds__(256) loss_max_kernel(const RowsIn p) {
 // The backward pass's rows, one warp each: x copied with zeros in the rows left
 // out, and what each row brings.
 //
-// d is held relative to the largest |g scale|.  So where all rows have the same g
-// (a mean), d is p - [target] itself: nothing has to be multiplied, and -1 for a
+// The fused kernel's grad_x sums p - [target] and multiplies the row's sum by its own
+// g.  In sums over the rows (and in the step kernel, whose d serves both gradients) d
+// is held relative to the largest |g scale|.  So where all rows have the same g (a
+// mean), d is p - [target] itself: nothing has to be multiplied, and -1 for a
 // target of little weight has no rounding, where -g would be off by the same 2^-9
 // in every row (grad_table of 300 rows over 5000 items in bf16: 0.0025 off, so
 // 0.0017).  fp16's range is narrow besides (6e-8 to 65504): there d comes times
@@ -162,6 +164,7 @@ __global__ void __launch_bounds__(256) loss_rows_kernel(const RowsIn p) {
             to[0] = t < 0 ? -INFINITY : DT == DT_F32 ? -p.lse[row] : log2f(target_unit<DT>()) - p.lse[row] * kLog2e;
             to[128] = t < 0 ? 1.f : p.g[row] * p.scale / m;
             to[256] = __int_as_float((int)t);
+            to[384] = t < 0 ? 0.f : p.g[row] * p.scale / target_unit<DT>();
         }
     }
 }
@@ -548,7 +551,7 @@ int backward_fused(const tbe_softmax_loss* h, const Plan& L, LossFused p, const 
         p.w.out = gw ? static_cast<char*>(gw) + p.v0 * p.D * elem_bytes(dt) : nullptr;
         e = launch_loss_fused(p, maps, dt, s);
         if (e != cudaSuccess) return cuda_fail(e);
-        LossFinish f{p.x, p.w, p.N, p.v1 - p.v0, p.unit, p.D, L.cols4};
+        LossFinish f{p.x, p.w, p.N, p.v1 - p.v0, p.rows, p.unit, p.D, L.cols4};
         if (!p.x.last || p.x.direct) f.x.tiles = 0;
         if (p.w.direct) f.w.tiles = 0;
         if (f.x.tiles + f.w.tiles > 0) e = launch_loss_finish(f, dt, s);

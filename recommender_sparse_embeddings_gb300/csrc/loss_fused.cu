@@ -5,8 +5,9 @@
 // walks tiles of the others, 128 at a time or, above 128 columns, 64 (shared
 // memory holds four of those, but two of 128: the products then waited for
 // each tile's fetch, 4150 cycles per 128 of them at 256 columns):
-//   grad_x:      S = X W^T,  d = coef (2^(S c - lse) - [target]),  dX += d W
-//   grad_table:  S = W X^T,  d likewise, transposed,               dW += d X
+//   grad_x:      S = X W^T,  d = 2^(S c - lse) - [target],           dX += d W
+//   grad_table:  S = W X^T,  d likewise, transposed, times g / max,  dW += d X
+// (a row's g multiplies its finished grad_x, so rows of any g have all their bits).
 // S (fp32) and d (16-bit, the second product's first operand) live in tensor
 // memory; the walked tile serves both products, K-major in the first and
 // MN-major in the second, so it is fetched once.  That is four products of
@@ -51,7 +52,7 @@ struct FusedBars {
 
 // 32 columns of the thread's line: x = S in, d out.
 template <int DT, int P, bool ITEMS, int BN>
-__device__ __forceinline__ void gradients(float (&x)[32], float c2, float minus_lse, float coef, int at, int left,
+__device__ __forceinline__ void gradients(float (&x)[32], float c2, float minus_lse, int at, int left,
                                           const float* stats, int line) {
     if constexpr (!ITEMS) {
 #pragma unroll
@@ -67,10 +68,6 @@ __device__ __forceinline__ void gradients(float (&x)[32], float c2, float minus_
 #pragma unroll
             for (int c = 0; c < 32; ++c)
                 if (c >= left) x[c] = 0.f;
-        }
-        if (!__all_sync(0xffffffffu, coef == 1.f)) {
-#pragma unroll
-            for (int c = 0; c < 32; c += 2) mul2(x[c], x[c + 1], coef, coef);
         }
     } else {
         // columns are rows of x: their values lie in shared memory
@@ -264,28 +261,27 @@ __device__ __forceinline__ bool fused_body(const LossFused& p, const LossSide& s
         // ---- d, then the sums
         const int quarter = warp % 4, group = warp / 4 % 2, buf = warp / 8, line = quarter * 32 + lane;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-        float minus_lse = 0.f, coef = 0.f;
+        float minus_lse = 0.f;
         int target = -1;
+        const float* values = p.rows + (int64_t)tile * kRowValues + line;  // (of the held row)
         if constexpr (!ITEMS) {
-            const float* r = p.rows + (int64_t)tile * kRowValues + line;
-            minus_lse = __ldg(r);
-            coef = __ldg(r + 128);
-            target = __float_as_int(__ldg(r + 256));
+            minus_lse = __ldg(values);
+            target = __float_as_int(__ldg(values + 256));
         }
         const uint32_t acc = tmem + L::sums + lanes;
         const int wide = (p.D + 15) / 16 * 16;
         const int64_t row = (int64_t)tile * 128 + line;
-        const float unit = __ldg(p.unit);
         int flushed = 0;
         auto put = [&]() {
             const bool first = side.first && flushed == 0;
             const bool valid = row < (ITEMS ? p.v1 - p.v0 : p.N);
+            const float times = __ldg(ITEMS ? p.unit : values + 384);
             float4* part = side.part + ((int64_t)slice * side.tiles + tile) * p.cols4 * 128 + line;
             if constexpr (P == 3)
                 put_fp32(side.direct ? static_cast<float*>(side.out) + row * p.D : nullptr, part, acc, wide, warp / 4,
-                         valid, p.D, first, unit);
+                         valid, p.D, first, times);
             else if (side.direct)
-                store_rows<DT, 4>(side.out, row * p.D, acc, wide, warp / 4, valid, p.D, p.D % 8 == 0, unit);
+                store_rows<DT, 4>(side.out, row * p.D, acc, wide, warp / 4, valid, p.D, p.D % 8 == 0, times);
             else
                 add_slab<4, 16>(part, acc, wide, warp / 4, first);
             ++flushed;
@@ -320,7 +316,7 @@ __device__ __forceinline__ bool fused_body(const LossFused& p, const LossSide& s
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&bars.s_read[buf]);
                     }
-                    gradients<DT, P, ITEMS, BN>(x, p.c2, minus_lse, coef, at - h, left - h, stats + h, mine);
+                    gradients<DT, P, ITEMS, BN>(x, p.c2, minus_lse, at - h, left - h, stats + h, mine);
                     // d's columns are free of the last but one product (fp32: of the last)
                     if (h == 0 && (P == 3 ? i >= 1 : i >= 2)) {
                         ok = P == 3 ? mbar_wait_tight(&bars.done[buf ^ 1], ((i - 1) / 2) & 1)
@@ -415,7 +411,8 @@ __global__ void __launch_bounds__(256) loss_finish_kernel(const LossFinish p) {
     if (!x) tile -= p.x.tiles;
     finish<OUT>(side.part + (int64_t)tile * p.cols4 * 128, (int64_t)side.tiles * p.cols4 * 128, side.slices, side.out,
                 (int64_t)tile * 128, (int)tmin<int64_t>(128, (x ? p.x_rows : p.w_rows) - (int64_t)tile * 128), p.D,
-                (int)(blockIdx.x % blocks) * 32, __ldg(p.unit), threadIdx.x);
+                (int)(blockIdx.x % blocks) * 32,
+                __ldg(x ? p.rows + (int64_t)tile * kRowValues + 384 + threadIdx.x % 128 : p.unit), threadIdx.x);
 }
 
 template <int DT, int DP, int P>

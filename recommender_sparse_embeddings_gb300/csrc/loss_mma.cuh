@@ -198,9 +198,9 @@ __device__ __forceinline__ void powers(float& a, float& b, float scale, float le
 
 // What the rows bring into the backward pass: per tile of 128 rows 128 values
 // each of -lse (times log2(e) but for fp32; fp16: + 14), of g over the largest |g|,
-// and of the target as an int32; -inf, 1 and -1 in rows that are left out or
-// behind the last.
-constexpr int kRowValues = 3 * 128;
+// of the target as an int32, and of what a row's own sum is multiplied by (g scale;
+// fp16: 2^-14 of it); -inf, 1, -1 and 0 in rows that are left out or behind the last.
+constexpr int kRowValues = 4 * 128;
 
 // What d has of the target: 1, or with fp16 2^14.
 template <int DT>
@@ -290,7 +290,7 @@ struct LossFusedMaps {
 struct LossFinish {
     LossSide x, w;  // tiles 0: nothing to do
     int64_t x_rows, w_rows;
-    const float* unit;
+    const float *rows, *unit;
     int32_t D, cols4;
 };
 

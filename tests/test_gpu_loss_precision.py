@@ -12,6 +12,7 @@ import pytest
 import torch
 
 import recommender_sparse_embeddings_gb300 as tbe
+import rows_reference as ref
 
 pytestmark = pytest.mark.gpu
 FP16, BF16, FP32 = torch.float16, torch.bfloat16, torch.float32
@@ -121,3 +122,23 @@ def test_scores_over_many_columns(dtype, n, v, d):
     assert off(c.grad_x, grad_x) < bound
     at = torch.arange(0, v, 97, device="cuda")
     assert off(c.grad_table[at], c.items(at)) < bound
+
+
+@pytest.mark.parametrize("dtype", [FP32, BF16, FP16])
+@pytest.mark.parametrize("n,v,d", [(64, 5000, 64), (300, 700, 250), (2300, 3000, 40)])
+def test_rows_of_small_upstream_gradients(dtype, n, v, d):
+    """Each row's grad_x is as exact as if it were alone: d enters its sum without g.  The largest g is 2^27 times the
+    smallest (they are powers of two, so that scaling them back is exact); fp16's results stay above its smallest
+    normal number's neighbourhood by the table's size, and what is below loses half a step of 2^-24."""
+    c = Case(dtype, n, v, d)
+    c.grad = torch.exp2(-(torch.arange(n, device="cuda") % 28).float() + (10 if dtype == FP16 else 0))
+    c.grad[1::2] *= -1.0
+    c.run()
+    got = c.grad_x.double() / c.grad.double()[:, None]
+    want, bound = ref.loss(ref.f64(c.x), ref.f64(c.table), c.targets.cpu().numpy(), 1.0, torch.ones(n).double().numpy(), dtype)
+    # (the bound of rows whose g is 1, and what the result's rounding in the subnormals loses)
+    half_step = 2.0 ** -25 if dtype == FP16 else 2.0 ** -134
+    room = torch.from_numpy(bound["grad_x"]).cuda() + half_step / c.grad.double().abs()[:, None]
+    assert bool(((got - torch.from_numpy(want["grad_x"]).cuda()).abs() <= room).all())
+    at = torch.arange(v, device="cuda")
+    assert off(c.grad_table, c.items(at)) < {FP32: 2e-6, BF16: 2.4e-3, FP16: 3.0e-4}[dtype] + 2 ** -13 * (dtype != FP32)
