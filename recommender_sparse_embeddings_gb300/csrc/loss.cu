@@ -218,10 +218,10 @@ int check(const tbe_softmax_loss* h, const void* x, int64_t x_stride, const void
     return within_limits(N, V) ? TBE_OK : TBE_ERR_UNSUPPORTED;
 }
 
-// Whether two blocks share bytes (either may be NULL).
+// Whether two blocks share bytes (either may be NULL or empty).
 bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
     const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
-    return a && b && x < y + (uintptr_t)b_bytes && y < x + (uintptr_t)a_bytes;
+    return a && b && a_bytes > 0 && b_bytes > 0 && x < y + (uintptr_t)b_bytes && y < x + (uintptr_t)a_bytes;
 }
 
 // ---- workspaces and plans
@@ -739,17 +739,17 @@ int tbe_softmax_loss_backward(tbe_softmax_loss* h, const void* x, int64_t x_stri
     if (!workspace || !aligned16(workspace) || (N > 0 && (!lse || !grad_loss))) return TBE_ERR_INVALID_ARG;
     if (workspace_bytes < tbe_softmax_loss_workspace_bytes(h, N, V, 1)) return TBE_ERR_WORKSPACE_TOO_SMALL;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (N == 0) {
-        if (!grad_table || V == 0) return TBE_OK;
-        return status(cudaMemsetAsync(grad_table, 0, (size_t)V * h->c.dim * elem_bytes(h->c.dtype), s));
-    }
-    if (!grad_x && !grad_table) return TBE_OK;
     // (x is copied before a gradient is written; the table is read where it is)
     const int64_t bytes = elem_bytes(h->c.dtype), x_bytes = N * h->c.dim * bytes, w_bytes = V * h->c.dim * bytes;
-    const int64_t table_bytes = ((V - 1) * table_stride + h->c.dim) * bytes;
+    const int64_t table_bytes = V > 0 ? ((V - 1) * table_stride + h->c.dim) * bytes : 0;
     if (overlap(grad_x, x_bytes, table, table_bytes) || overlap(grad_table, w_bytes, table, table_bytes) ||
         overlap(grad_x, x_bytes, grad_table, w_bytes))
         return TBE_ERR_INVALID_ARG;
+    if (N == 0) {
+        if (!grad_table || V == 0) return TBE_OK;
+        return status(cudaMemsetAsync(grad_table, 0, (size_t)w_bytes, s));
+    }
+    if (!grad_x && !grad_table) return TBE_OK;
     const Plan L = make_plan(h, N, V, true, !direct(h, table, table_stride, V));
     RowsIn rows{};
     rows.x = make_copy(h, x, x_stride, N, L.pitch, nullptr);
