@@ -512,8 +512,10 @@ void tbe_layer_norm_destroy(tbe_layer_norm* h);
  * contiguous, receives t; NULL exactly where residual is.  stats: device fp32
  * [2, rows], every row's mean and rstd, kept for the backward call.  weight and
  * bias: device dtype [D], NULL exactly where the handle has none.  out or total
- * may be x or residual itself (contiguous, the same rows) but not each other
- * (INVALID_ARG).  A row without spread gives 0 * rstd: with eps 0 that is NaN. */
+ * may be x or residual itself (contiguous, the same rows).  Results that share
+ * memory with each other, with other rows of x or residual, with weight or with
+ * bias are refused (INVALID_ARG).  A row without spread gives 0 * rstd: with eps 0
+ * that is NaN. */
 int tbe_layer_norm_forward(tbe_layer_norm* h, const void* x, int64_t x_stride, const void* residual,
                            int64_t residual_stride, const void* weight, const void* bias, int64_t num_rows,
                            void* out, void* total, float* stats, void* stream);

@@ -218,12 +218,6 @@ int check(const tbe_softmax_loss* h, const void* x, int64_t x_stride, const void
     return within_limits(N, V) ? TBE_OK : TBE_ERR_UNSUPPORTED;
 }
 
-// Whether two blocks share bytes (either may be NULL or empty).
-bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
-    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
-    return a && b && a_bytes > 0 && b_bytes > 0 && x < y + (uintptr_t)b_bytes && y < x + (uintptr_t)a_bytes;
-}
-
 // ---- workspaces and plans
 
 template <typename T>

@@ -496,6 +496,24 @@ bool on_device(const tbe_layer_norm* h) {
     return cudaGetDevice(&d) == cudaSuccess && d == h->device;
 }
 
+// Whether a block shares bytes with one of `rows` rows of `row` bytes, `stride` apart.
+bool over_rows(const void* block, int64_t bytes, const void* base, int64_t stride, int64_t row, int64_t rows) {
+    if (!block || !base || (uintptr_t)base >= (uintptr_t)block + (uintptr_t)bytes) return false;
+    const int64_t behind = (int64_t)((uintptr_t)block - (uintptr_t)base) - row;  // its start from the first row's end
+    if (behind < 0) return true;
+    const int64_t first = stride > 0 ? behind / stride + 1 : rows;  // the first row that ends behind its start
+    return first < rows && (uintptr_t)base + (uintptr_t)(first * stride) < (uintptr_t)block + (uintptr_t)bytes;
+}
+
+// Whether a result of contiguous rows may not lie where it does beside an operand:
+// over the same rows it may (a row is read before it is written, by the same
+// threads), over others of them it may not.
+bool misplaced(const tbe_layer_norm* h, const void* result, const void* operand, int64_t stride, int64_t rows) {
+    const int64_t e = elem_bytes(h->c.dtype), row = h->c.dim * e;
+    if (result == operand && (stride == h->c.dim || rows == 1)) return false;
+    return over_rows(result, rows * row, operand, stride * e, row, rows);
+}
+
 bool aligned16(const void* p) { return (uintptr_t)p % 16 == 0; }
 
 bool vec_rows(const tbe_layer_norm* h, const void* p, int64_t stride) {
@@ -633,7 +651,17 @@ int tbe_layer_norm_forward(tbe_layer_norm* h, const void* x, int64_t x_stride, c
         return TBE_ERR_INVALID_ARG;
     if (rows >= (int64_t(1) << 31)) return TBE_ERR_UNSUPPORTED;
     if (rows == 0) return TBE_OK;
-    if (!x || !out || !stats || (residual != nullptr) != (total != nullptr) || out == total) return TBE_ERR_INVALID_ARG;
+    if (!x || !out || !stats || (residual != nullptr) != (total != nullptr)) return TBE_ERR_INVALID_ARG;
+    const int64_t e_bytes = elem_bytes(h->c.dtype), row = h->c.dim * e_bytes, stats_bytes = 2 * rows * (int64_t)sizeof(float);
+    if (overlap(out, rows * row, total, rows * row) || over_rows(stats, stats_bytes, x, x_stride * e_bytes, row, rows) ||
+        over_rows(stats, stats_bytes, residual, residual_stride * e_bytes, row, rows))
+        return TBE_ERR_INVALID_ARG;
+    for (const void* result : {static_cast<const void*>(out), static_cast<const void*>(total)})
+        if (misplaced(h, result, x, x_stride, rows) || misplaced(h, result, residual, residual_stride, rows) ||
+            overlap(result, rows * row, weight, row) || overlap(result, rows * row, bias, row) ||
+            overlap(result, rows * row, stats, stats_bytes))
+            return TBE_ERR_INVALID_ARG;
+    if (overlap(stats, stats_bytes, weight, row) || overlap(stats, stats_bytes, bias, row)) return TBE_ERR_INVALID_ARG;
     const NormForward p{x, residual, weight, bias, x_stride, residual_stride, rows, h->c.dim, h->c.eps, out, total, stats};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool vec = vec_rows(h, x, x_stride) && vec_rows(h, out, 0) && (!weight || aligned16(weight)) &&

@@ -196,6 +196,12 @@ inline cudaError_t launch_chained(void (*kernel)(KArgs...), dim3 grid, dim3 bloc
     return launch_chained_smem(kernel, grid, block, 0, s, args...);
 }
 
+// Whether two blocks share bytes (either may be NULL or empty).
+inline bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+    return a && b && a_bytes > 0 && b_bytes > 0 && x < y + (uintptr_t)b_bytes && y < x + (uintptr_t)a_bytes;
+}
+
 template <typename IDX>
 __device__ __forceinline__ int64_t ld_index(const IDX* p, int64_t k) {
     return (int64_t)__ldg(p + k);

@@ -29,3 +29,61 @@ def test_no_rows_leave_a_table_given_as_its_gradient(dtype, d):
     assert gw.shape == table.shape and not gw.any()
     # no rows and no items: nothing is written wherever the results lie
     tbe.tbe_softmax_loss_backward(h, x, table[:0], targets, lse, grad, grad_x=x, grad_table=table[:0])
+
+
+def norm(dtype, rows, d, weight=True):
+    g = torch.Generator(device="cuda").manual_seed(rows + d)
+    h = tbe.tbe_layer_norm_create(d, dtype, weight=weight, bias=weight)
+    return h, *(torch.randn((n, d), generator=g, device="cuda").to(dtype) for n in (rows, rows, 1, 1))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("d", [64, 77])
+def test_norm_results_over_each_other_or_over_operands(dtype, d):
+    n = 40
+    h, x, r, w, b = norm(dtype, n, d)
+    room = torch.full(((2 * n + 8) * d + 64,), 7.0, dtype=dtype, device="cuda")
+    was = room.clone()
+
+    def at(first, rows=n):
+        return room[first:first + rows * d].view(rows, d)
+
+    def call(x=x, r=r, **kw):
+        return tbe.tbe_layer_norm_forward(h, x, kw.pop("w", w)[0], kw.pop("b", b)[0], r, **kw)
+
+    for first in (0, 1, d, (n - 1) * d, n * d - 1):  # out and total: the same, an element, rows apart, the last shared
+        refused(call, out=at(0), total=at(first))
+        refused(call, out=at(first), total=at(0))
+    call(out=at(0), total=at(n * d))
+    room.copy_(was)
+    for first in (1, d, (n - 1) * d):  # results over other rows of an operand
+        for kw in (dict(x=at(0), out=at(first)), dict(x=at(first), out=at(0)), dict(r=at(0), out=at(first)),
+                   dict(x=at(0), total=at(first)), dict(r=at(first), total=at(0))):
+            refused(call, **kw)
+    wide = room[:n * 2 * d].view(n, 2 * d)  # over strided rows, a broadcast one, and the gaps between them
+    refused(call, x=wide[:, :d], out=at(0))
+    refused(call, r=wide[:, d:], total=at(0))
+    refused(call, x=room[:d].expand(n, d), out=at(0))
+    refused(call, w=at(3 * d), out=at(0))
+    refused(call, b=at(n * d - d, 1), total=at(0))
+    stats = room[:4 * n].view(torch.float32)[:2 * n].view(2, n)
+    for kw in (dict(out=at(0)), dict(total=at(0)), dict(x=at(0)), dict(r=at(0)), dict(w=at(0, 1))):
+        refused(call, stats=stats, **kw)
+    assert torch.equal(room, was)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_norm_results_beside_operands(dtype):
+    """What shares no byte is taken: a result in a gap between strided rows, behind them, and the same row of one."""
+    n, d = 3, 64
+    h, x, r, w, b = norm(dtype, n, d)
+    want = [t.clone() for t in tbe.tbe_layer_norm_forward(h, x, w[0], b[0], r)]
+    wide = torch.zeros((n, 16 * d), dtype=dtype, device="cuda")
+    wide[:, :d] = x
+    flat = wide.view(-1)
+    for first in (d, 12 * d, (2 * 16 + 1) * d):
+        got = tbe.tbe_layer_norm_forward(h, wide[:, :d], w[0], b[0], r, out=flat[first:first + n * d].view(n, d))
+        assert torch.equal(got[0], want[0]) and torch.equal(wide[:, :d], x)
+    one = wide[:1, :d]  # a single row: its stride says nothing
+    tbe.tbe_layer_norm_forward(h, one, w[0], b[0], r[:1], out=flat[:d].view(1, d))
+    assert torch.equal(one, want[0][:1])
