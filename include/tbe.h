@@ -527,10 +527,12 @@ size_t tbe_layer_norm_workspace_bytes(const tbe_layer_norm* h, int64_t num_rows)
 
 /* Gradients from the kept stream (t; x where there was no residual), the
  * forward call's stats, the upstream gradient grad_out and grad_total (u; NULL:
- * none).  grad_x: device dtype [rows, D], contiguous, may be grad_out or
- * grad_total itself.  grad_weight and grad_bias: device dtype [D], written, not
- * added to (zeros where there are no rows); NULL exactly where the handle has
- * no weight (bias). */
+ * none).  grad_x: device dtype [rows, D], contiguous, may be total, grad_out or
+ * grad_total itself (contiguous, the same rows).  grad_weight and grad_bias:
+ * device dtype [D], written, not added to (zeros where there are no rows); NULL
+ * exactly where the handle has no weight (bias).  Results that share memory with
+ * each other, or grad_x with other rows of an operand, with stats or with weight,
+ * are refused (INVALID_ARG). */
 int tbe_layer_norm_backward(tbe_layer_norm* h, const void* total, int64_t total_stride, const float* stats,
                             const void* grad_out, int64_t grad_out_stride, const void* grad_total,
                             int64_t grad_total_stride, const void* weight, int64_t num_rows, void* grad_x,

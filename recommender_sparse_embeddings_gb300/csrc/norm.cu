@@ -688,6 +688,13 @@ int tbe_layer_norm_backward(tbe_layer_norm* h, const void* total, int64_t total_
     if (!workspace || !aligned16(workspace)) return TBE_ERR_INVALID_ARG;
     if (rows > 0 && (!total || !stats || !grad_out || !grad_x)) return TBE_ERR_INVALID_ARG;
     if (workspace_bytes < tbe_layer_norm_workspace_bytes(h, rows)) return TBE_ERR_WORKSPACE_TOO_SMALL;
+    // (grad_weight and grad_bias are written after all operands are read)
+    const int64_t row = h->c.dim * elem_bytes(h->c.dtype);
+    if (misplaced(h, grad_x, total, total_stride, rows) || misplaced(h, grad_x, grad_out, grad_out_stride, rows) ||
+        misplaced(h, grad_x, grad_total, grad_total_stride, rows) || overlap(grad_x, rows * row, weight, row) ||
+        overlap(grad_x, rows * row, stats, 2 * rows * (int64_t)sizeof(float)) || overlap(grad_weight, row, grad_bias, row) ||
+        overlap(grad_x, rows * row, grad_weight, row) || overlap(grad_x, rows * row, grad_bias, row))
+        return TBE_ERR_INVALID_ARG;
     const NormBackward p{total, grad_out, grad_total, weight, total_stride, grad_out_stride, grad_total_stride, rows,
                          stats, h->c.dim, grad_x, grad_weight, grad_bias, static_cast<float*>(workspace)};
     cudaStream_t s = static_cast<cudaStream_t>(stream);

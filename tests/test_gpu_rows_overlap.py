@@ -87,3 +87,41 @@ def test_norm_results_beside_operands(dtype):
     one = wide[:1, :d]  # a single row: its stride says nothing
     tbe.tbe_layer_norm_forward(h, one, w[0], b[0], r[:1], out=flat[:d].view(1, d))
     assert torch.equal(one, want[0][:1])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("d", [64, 77])
+def test_norm_gradients_over_each_other_or_over_operands(dtype, d):
+    n = 40
+    h, x, g, w, b = norm(dtype, n, d)
+    _, total, stats = tbe.tbe_layer_norm_forward(h, x, w[0], b[0])
+    want = [t.clone() for t in tbe.tbe_layer_norm_backward(h, total, stats, g, w[0], g)]
+    room = torch.full(((2 * n + 8) * d + 64,), 7.0, dtype=dtype, device="cuda")
+    was = room.clone()
+
+    def at(first, rows=n):
+        return room[first:first + rows * d].view(rows, d)
+
+    def call(total=total, stats=stats, g=g, w=w, u=g, **kw):
+        return tbe.tbe_layer_norm_backward(h, total, stats, g, w[0], u, **kw)
+
+    for first in (1, d, (n - 1) * d):
+        for name in ("total", "g", "u"):
+            refused(call, **{name: at(0)}, grad_x=at(first))
+            refused(call, **{name: at(first)}, grad_x=at(0))
+    refused(call, g=room[:n * 2 * d].view(n, 2 * d)[:, :d], grad_x=at(0))
+    refused(call, u=room[:d].expand(n, d), grad_x=at(0))
+    refused(call, w=at(5 * d), grad_x=at(0))
+    refused(call, stats=room[:4 * n].view(torch.float32)[:2 * n].view(2, n), grad_x=at(0))
+    one = room[:d]
+    refused(call, grad_weight=one, grad_bias=one)
+    refused(call, grad_weight=one, grad_bias=room[d - 1:2 * d - 1])
+    refused(call, grad_x=at(0), grad_weight=room[d * (n - 1) + 3:d * n + 3])
+    refused(call, grad_x=at(0), grad_bias=one)
+    assert torch.equal(room, was)
+    for place in ("total", "g", "u"):  # the same rows in place, the weights' gradients over the weights
+        at(0).copy_(total if place == "total" else g)
+        ww = w.clone()
+        got = call(**{place: at(0)}, w=ww, grad_x=at(0), grad_weight=ww[0], grad_bias=at(n * d, 1)[0])
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), place
+        assert torch.equal(ww[0], want[1])
