@@ -596,7 +596,8 @@ void tbe_softmax_loss_destroy(tbe_softmax_loss* h);
 size_t tbe_softmax_loss_workspace_bytes(const tbe_softmax_loss* h, int64_t num_rows, int64_t num_items,
                                         int32_t backward);
 
-/* targets: device int32 or int64 [N].  loss, lse: device fp32 [N]. */
+/* targets: device int32 or int64 [N].  loss, lse: device fp32 [N], neither sharing
+ * memory with the other or with targets (INVALID_ARG). */
 int tbe_softmax_loss_forward(tbe_softmax_loss* h, const void* x, int64_t x_stride, const void* table,
                              int64_t table_stride, const void* targets, int32_t index_dtype, int64_t num_rows,
                              int64_t num_items, float* loss, float* lse, void* workspace, size_t workspace_bytes,

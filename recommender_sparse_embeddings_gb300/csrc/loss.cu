@@ -714,6 +714,10 @@ int tbe_softmax_loss_forward(tbe_softmax_loss* h, const void* x, int64_t x_strid
     if (rc) return rc;
     if (!workspace || !aligned16(workspace) || (N > 0 && (!loss || !lse))) return TBE_ERR_INVALID_ARG;
     if (workspace_bytes < tbe_softmax_loss_workspace_bytes(h, N, V, 0)) return TBE_ERR_WORKSPACE_TOO_SMALL;
+    const int64_t row_bytes = N * (int64_t)sizeof(float), target_bytes = N * (index_dtype == TBE_I64 ? 8 : 4);
+    if (overlap(loss, row_bytes, lse, row_bytes) || overlap(loss, row_bytes, targets, target_bytes) ||
+        overlap(lse, row_bytes, targets, target_bytes))
+        return TBE_ERR_INVALID_ARG;
     if (N == 0) return TBE_OK;
     LossForward p{};
     p.N = N, p.V = V, p.D = h->c.dim, p.c2 = argument_scale(h);

@@ -125,3 +125,17 @@ def test_norm_gradients_over_each_other_or_over_operands(dtype, d):
         got = call(**{place: at(0)}, w=ww, grad_x=at(0), grad_weight=ww[0], grad_bias=at(n * d, 1)[0])
         assert all(torch.equal(a, b) for a, b in zip(got, want)), place
         assert torch.equal(ww[0], want[1])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("index", [torch.int32, torch.int64])
+def test_loss_over_lse_or_over_the_targets(dtype, index):
+    n, h = 30, tbe.tbe_softmax_loss_create(48, dtype)
+    x, table = torch.randn((n, 48), device="cuda").to(dtype), torch.randn((100, 48), device="cuda").to(dtype)
+    targets, room = torch.arange(n, device="cuda").to(index), torch.full((2 * n,), 7.0, device="cuda")
+    was = targets.clone()
+    for kw in (dict(loss=room[:n], lse=room[:n]), dict(loss=room[:n], lse=room[n - 1:2 * n - 1]),
+               dict(loss=targets.view(torch.float32)[:n]), dict(lse=targets.view(torch.float32)[-n:])):
+        refused(tbe.tbe_softmax_loss_forward, h, x, table, targets, **kw)
+    assert torch.equal(targets, was) and bool((room == 7.0).all())
+    tbe.tbe_softmax_loss_forward(h, x, table, targets, loss=room[:n], lse=room[n:])
