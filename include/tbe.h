@@ -512,7 +512,8 @@ void tbe_layer_norm_destroy(tbe_layer_norm* h);
  * contiguous, receives t; NULL exactly where residual is.  stats: device fp32
  * [2, rows], every row's mean and rstd, kept for the backward call.  weight and
  * bias: device dtype [D], NULL exactly where the handle has none.  out or total
- * may be x or residual itself (contiguous, the same rows).  Results that share
+ * may be x or residual itself (contiguous, the same rows; out over x without a
+ * residual leaves no t for a backward call).  Results that share
  * memory with each other, with other rows of x or residual, with weight or with
  * bias are refused (INVALID_ARG).  A row without spread gives 0 * rstd: with eps 0
  * that is NaN. */

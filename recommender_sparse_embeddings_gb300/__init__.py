@@ -765,7 +765,8 @@ def tbe_layer_norm_forward(h: LayerNormHandle, x: torch.Tensor, weight: Optional
                            stats: Optional[torch.Tensor] = None, stream=None):
     """x [N, D] and residual [N, D] (strided rows are fine); returns (out,
     total, stats): the normalised rows, the kept stream x + residual (x itself
-    without a residual) and fp32 [2, N] of the rows' mean and 1 / deviation."""
+    without a residual, None where ``out`` has taken its place: there is nothing
+    left for a backward call) and fp32 [2, N] of the rows' mean and 1 / deviation."""
     if x.dim() != 2:
         raise ValueError("x must be [N, D]")
     n, d, dt = x.shape[0], h.dim, h.dtype
@@ -782,7 +783,9 @@ def tbe_layer_norm_forward(h: LayerNormHandle, x: torch.Tensor, weight: Optional
         raise ValueError("total without residual")
     rc = load_library().tbe_layer_norm_forward(h.ptr, px, sx, pr, sr, pw, pb, n, po, pt, ps, _stream(stream))
     _check(rc, "tbe_layer_norm_forward")
-    return out, x if residual is None else total, stats
+    if residual is None:
+        total = None if n > 0 and po == px else x
+    return out, total, stats
 
 
 def tbe_layer_norm_workspace_bytes(h: LayerNormHandle, num_rows: int) -> int:
@@ -807,7 +810,7 @@ def tbe_layer_norm_backward(h: LayerNormHandle, total: torch.Tensor, stats: torc
     and stats and the upstream gradients of its out and (optionally) its total;
     grad_x is the residual's gradient too.  What the handle has no parameter
     for is None."""
-    if total.dim() != 2:
+    if total is None or total.dim() != 2:
         raise ValueError("total must be [N, D]")
     n, d, dt = total.shape[0], h.dim, h.dtype
     pt, st = _matrix(total, n, d, dt, "total")

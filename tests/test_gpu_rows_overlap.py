@@ -139,3 +139,22 @@ def test_loss_over_lse_or_over_the_targets(dtype, index):
         refused(tbe.tbe_softmax_loss_forward, h, x, table, targets, **kw)
     assert torch.equal(targets, was) and bool((room == 7.0).all())
     tbe.tbe_softmax_loss_forward(h, x, table, targets, loss=room[:n], lse=room[n:])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_norm_in_place_without_a_residual_keeps_no_stream(dtype):
+    """What the call returns as the kept stream is the stream, or nothing: not the normalised rows in its place."""
+    h, x, r, w, b = norm(dtype, 20, 72)
+    was = x.clone()
+    out, total, stats = tbe.tbe_layer_norm_forward(h, x, w[0], b[0])
+    assert total is x and torch.equal(x, was)
+    again, total, stats = tbe.tbe_layer_norm_forward(h, x, w[0], b[0], out=x)
+    assert total is None and again is x and torch.equal(x, out)
+    with pytest.raises(ValueError):
+        tbe.tbe_layer_norm_backward(h, total, stats, out, w[0])
+    x.copy_(was)
+    want = tbe.tbe_layer_norm_forward(h, x, w[0], b[0], r)
+    got = tbe.tbe_layer_norm_forward(h, x, w[0], b[0], r, out=x)  # with a residual the stream has a place of its own
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    empty = tbe.tbe_layer_norm_forward(h, x[:0], w[0], b[0])
+    assert empty[1] is not None and empty[1].shape == (0, 72)
