@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(forward_threads(T)) norm_forward_kernel(const 
 
 // Wide rows of 1024 threads keep the weights' sums in shared memory (64
 // registers a thread hold the row alone).
-template <int E, int K, int T>
+template <int T>
 constexpr bool sums_in_smem() {
     return T == 1024;
 }
@@ -348,7 +348,7 @@ template <int DT, int E, int K, int T>
 __global__ void __launch_bounds__(backward_threads(T)) norm_backward_kernel(const NormBackward p) {
     using Part = RowPart<DT, E, K, T>;
     constexpr int kThreads = backward_threads(T), kGroups = kThreads / T, M = E * K;
-    constexpr bool kSmem = sums_in_smem<E, K, T>();
+    constexpr bool kSmem = sums_in_smem<T>();
     using Rows = Feed<DT, E, K, T>;
     extern __shared__ __align__(16) unsigned char smem[];
     // behind the rows ahead (kSmem: [2 M][threads]) or, after them, in their place (several groups: [M][threads])
@@ -551,7 +551,7 @@ template <int DT, int E, int K, int T>
 cudaError_t backward(const NormBackward& p, const tbe_layer_norm* h, cudaStream_t s) {
     constexpr int threads = backward_threads(T), M = E * K;
     constexpr size_t ahead = Feed<DT, E, K, T>::kBytes, sums = sizeof(float) * threads * M;
-    constexpr size_t smem = sums_in_smem<E, K, T>() ? ahead + 2 * sums : threads > T ? std::max(ahead, sums) : ahead;
+    constexpr size_t smem = sums_in_smem<T>() ? ahead + 2 * sums : threads > T ? std::max(ahead, sums) : ahead;
     auto* kernel = norm_backward_kernel<DT, E, K, T>;
     if (smem > 48 * 1024) {  // (an attribute of the device's copy of the kernel, so set at every call)
         const cudaError_t f = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -605,8 +605,11 @@ cudaError_t launch_backward(const NormBackward& p, bool vec, const tbe_layer_nor
     if (p.D <= 16 * E) return backward<DT, E, 1, 16>(p, h, s);
     if (p.D <= 32 * E) return backward<DT, E, 1, 32>(p, h, s);
     if (p.D <= 64 * E) return backward<DT, E, 2, 32>(p, h, s);
-    if (p.D <= 512) return backward<DT, E, K2, 32>(p, h, s);
-    if (p.D <= 128 * E) return backward<DT, E, 1, 128>(p, h, s);
+    if constexpr (DT == DT_F32) {
+        if (p.D <= 512) return backward<DT, E, K2, 32>(p, h, s);
+    } else {
+        if (p.D <= 1024) return backward<DT, E, 1, 128>(p, h, s);
+    }
     if (p.D <= 2048) return backward<DT, E, K2, 128>(p, h, s);
     if (p.D <= 4096) return backward<DT, E, K2, 256>(p, h, s);
     if (p.D <= 8192) return backward<DT, E, K2 / 2, 1024>(p, h, s);
