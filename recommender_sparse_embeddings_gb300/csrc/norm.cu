@@ -24,8 +24,9 @@ struct tbe_layer_norm {
 namespace {
 
 constexpr int kMaxNormDim = 16384;
-// CTAs of the backward kernel per SM at most: bounds its partial sums (the
-// wide rows' CTAs are large, fewer fit).
+// CTAs of the backward kernel per SM at most: bounds its partial sums.  Wide rows'
+// CTAs are large: two fit (8192 x 4096 f16 with one 73 us, with two 60); of narrow
+// rows 4, 8 and 16 take the same time.
 constexpr int most_ctas(int D) { return D <= 512 ? 8 : 2; }
 
 struct CallRange {
@@ -301,7 +302,7 @@ __global__ void __launch_bounds__(forward_threads(T)) norm_forward_kernel(const 
         for (int i = 0; i < M; ++i) s[0] += f[i];
         row_sums<T, kGroups>(s, turn);
         const float about = s[0] * per;
-        const float mean = fmaf(fmaf(-width, about, s[0]), per, about);  // (exact where all elements are the same)
+        const float mean = fmaf(fmaf(-width, about, s[0]), per, about);  // (the sum / D, rounded once)
         s[0] = 0.f;
 #pragma unroll
         for (int k = 0; k < K; ++k)
@@ -337,8 +338,10 @@ __global__ void __launch_bounds__(forward_threads(T)) norm_forward_kernel(const 
     }
 }
 
-// Wide rows of 1024 threads keep the weights' sums in shared memory (64
-// registers a thread hold the row alone).
+// Wide rows of 1024 threads keep the weights' sums in shared memory: they have at
+// most 64 registers a thread, and those of more than 8 elements spill as it is (164 to
+// 268 bytes with 16-bit accesses of 16 bytes, 0.4 to 1.6 KB with fp32's or single
+// elements, as do other variants of single elements above 512 columns by 0.1 to 0.4).
 template <int T>
 constexpr bool sums_in_smem() {
     return T == 1024;
@@ -565,9 +568,11 @@ cudaError_t backward(const NormBackward& p, const tbe_layer_norm* h, cudaStream_
     return launch_chained(norm_join_kernel<DT>, dim3((2 * p.D + 31) / 32), dim3(1024), s, p, (int)grid);
 }
 
-// The fewest threads a row whose registers hold it: 32 elements a thread in
-// the forward pass, 16 in the backward pass (whose sums take two registers an
-// element besides; 8 for 4096 to 8192 columns, 4000 x 8192 fp32 119 -> 101 us).
+// The fewest threads a row whose registers hold it: at most 32 elements a thread
+// of 16-bit rows in the forward pass (16 of 1025 to 2048 columns), 16 of fp32 and of
+// rows off 16 bytes, and 16 in the backward pass, whose sums take two registers an
+// element besides.  fp32's backward pass of 4097 to 8192 columns has 8 (4000 x 8192
+// 119 -> 101 us; 16-bit rows lost by it: 8000 x 5000 bf16 110 -> 127, x 8192 131 -> 138).
 template <int DT>
 cudaError_t launch_forward(const NormForward& p, bool vec, const tbe_layer_norm* h, cudaStream_t s) {
     constexpr int E = DT == DT_F32 ? 4 : 8;
@@ -612,7 +617,11 @@ cudaError_t launch_backward(const NormBackward& p, bool vec, const tbe_layer_nor
     }
     if (p.D <= 2048) return backward<DT, E, K2, 128>(p, h, s);
     if (p.D <= 4096) return backward<DT, E, K2, 256>(p, h, s);
-    if (p.D <= 8192) return backward<DT, E, K2 / 2, 1024>(p, h, s);
+    if constexpr (DT == DT_F32) {
+        if (p.D <= 8192) return backward<DT, E, K2 / 2, 1024>(p, h, s);
+    } else {
+        if (p.D <= 8192) return backward<DT, E, K2, 512>(p, h, s);
+    }
     return backward<DT, E, K2, 1024>(p, h, s);
 }
 
