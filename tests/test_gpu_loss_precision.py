@@ -142,3 +142,85 @@ def test_rows_of_small_upstream_gradients(dtype, n, v, d):
     assert bool(((got - torch.from_numpy(want["grad_x"]).cuda()).abs() <= room).all())
     at = torch.arange(v, device="cuda")
     assert off(c.grad_table, c.items(at)) < {FP32: 2e-6, BF16: 2.4e-3, FP16: 3.0e-4}[dtype] + 2 ** -13 * (dtype != FP32)
+
+
+def check_all(c, tolerance):
+    """loss, lse and both gradients of all rows and items, and each element (the norm would not show a single one): none
+    is off by more than 16 roundings of the largest, in fp32 64: a weight of 1 is off by lse's error, which may be 3e-7
+    of 11, 55 of fp32's roundings of 2^-24, and half a step of an lse of 8 to 16, 8 of them."""
+    n, v = c.targets.numel(), c.table.shape[0]
+    parts = [c.rows(torch.arange(lo, min(n, lo + 2048), device="cuda")) for lo in range(0, n, 2048)]
+    loss, lse, grad_x = (torch.cat([p[i] for p in parts]) for i in range(3))
+    # fp32's roundings of sums of up to 40,000 terms in 64 parts or more, one of loss itself, 2^-22 of each exponential
+    assert off(c.loss, loss) < 3e-7 and off(c.lse, lse) < 3e-7
+    grad_table = torch.cat([c.items(torch.arange(lo, min(v, lo + 2048), device="cuda")) for lo in range(0, v, 2048)])
+    for got, want in ((c.grad_x, grad_x), (c.grad_table, grad_table)):
+        assert off(got, want) < tolerance
+        assert (got.double() - want).abs().max() <= (64 if got.dtype == FP32 else 16) * ref.UNIT[got.dtype] * want.abs().max()
+
+
+# fp32: 24 to 32 products in an accumulator, 7e-7 to 1e-6 by their cuts, 5e-7 by the scores of up to 264 columns (17
+# products, half of their cuts' 5e-7 times 1.5 follows lse's), roundings 1e-7: 1.5e-6 and, above 128 columns, 1.8e-6.
+# Two bf16 terms of each operand instead of three are 3.2e-6 off; sums of 313 blocks in one accumulator 2.2e-5.
+@pytest.mark.parametrize("dtype,n,v,d,tolerance", [
+    (FP32, 2050, 20011, 96, 1.5e-6),     # fused, sums in many parts
+    (FP32, 300, 9000, 60, 1.5e-6),
+    (FP32, 5000, 8000, 136, 1.8e-6),     # three pieces of d, seven slabs of rows, sums in parts of 8 blocks
+    (FP32, 900, 30000, 264, 1.8e-6),     # the table's gradient added to in place
+    (BF16, 3000, 40000, 264, 2.4e-3),    # three pieces, the table read in place
+    (FP16, 12000, 9001, 264, 3.0e-4),    # three pieces and three slabs of rows: joined two launches later
+    (BF16, 12000, 9001, 320, 2.4e-3),
+    (FP16, 4096, 20000, 512, 3.0e-4),
+    (FP16, 2500, 30000, 128, 3.0e-4),    # fused
+    (BF16, 2500, 30000, 250, 2.4e-3)])
+def test_all_results(dtype, n, v, d, tolerance):
+    c = Case(dtype, n, v, d, seed=n)
+    c.run()
+    check_all(c, tolerance)
+
+
+@pytest.mark.parametrize("dtype,n,v,d", [(FP32, 2600, 9000, 192), (BF16, 9000, 6000, 264), (FP16, 9000, 6000, 300)])
+def test_pieces_again_alone_in_a_used_workspace_and_in_graphs(dtype, n, v, d):
+    """What the fused kernel's tests ask of it, of d in memory: two pieces, several slabs of rows and of items."""
+    c, o = Case(dtype, n, v, d, seed=5), Case(FP32 if dtype == BF16 else BF16, 2000, 9001, 264, seed=6)
+    c.targets[::7] = -1
+    c.run(), o.run()
+    want = [c.loss, c.lse, c.grad_x, c.grad_table]
+    other = [o.grad_x, o.grad_table]
+    assert not c.grad_x[::7].any()
+    ws = tbe.make_softmax_loss_workspace(c.h, n, v, True)
+
+    def call(workspace=ws, stream=None, **kw):
+        loss, lse = tbe.tbe_softmax_loss_forward(c.h, c.x, c.table, c.targets, workspace=workspace, stream=stream)
+        return [loss, lse, *tbe.tbe_softmax_loss_backward(c.h, c.x, c.table, c.targets, lse, c.grad, workspace=workspace,
+                                                          stream=stream, **kw)]
+
+    for byte in (255, 0):
+        ws.fill_(byte)
+        assert all(torch.equal(a, b) for a, b in zip(call(), want))
+    ws.fill_(255)  # a smaller call in the same workspace, then the large one again
+    small = tbe.tbe_softmax_loss_forward(c.h, c.x[:100], c.table[:777], c.targets[:100] % 777, workspace=ws)
+    gx, _ = tbe.tbe_softmax_loss_backward(c.h, c.x[:100], c.table[:777], c.targets[:100] % 777, small[1], c.grad[:100],
+                                          workspace=ws)
+    assert bool(gx.isfinite().all()) and all(torch.equal(a, b) for a, b in zip(call(), want))
+    assert torch.equal(call(want=(True, False))[2], want[2]) and torch.equal(call(want=(False, True))[3], want[3])
+    graphs, results = [], []
+    for _ in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            results.append(call())
+        graphs.append(graph)
+    for graph in graphs + graphs:
+        graph.replay()
+    torch.cuda.synchronize()
+    for got in results:
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    streams = torch.cuda.Stream(), torch.cuda.Stream()  # two handles whose calls overlap
+    got = []
+    for _ in range(3):
+        got.append((call(workspace=None, stream=streams[0]),
+                    tbe.tbe_softmax_loss_backward(o.h, o.x, o.table, o.targets, o.lse, o.grad, stream=streams[1])))
+    torch.cuda.synchronize()
+    for a, b in got:
+        assert all(torch.equal(x, y) for x, y in zip(a, want)) and all(torch.equal(x, y) for x, y in zip(b, other))
+    assert tbe.tbe_softmax_loss_get_error(c.h) == tbe.TBE_OK and tbe.tbe_softmax_loss_get_error(o.h) == tbe.TBE_OK

@@ -34,3 +34,30 @@ def test_gradients_of_huge_rows_without_spread(dtype, dim):
     assert bool(((gx.double() - want).abs() <= room).all())
     assert not gw.any()
     assert bool(((gb.double() - up.double().sum(0)).abs() <= u * up.double().sum(0).abs() + 8 * ref.F * up.double().abs().sum(0)).all())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,dim", [(40000, 8), (40011, 24), (30007, 64), (20003, 77), (9001, 512), (6007, 1100),
+                                      (3001, 4096)])
+def test_in_place_of_many_rows(dtype, rows, dim):
+    """Every thread takes many rows in turn, so rows fetched ahead lie beside others that are already overwritten (narrow
+    ones in one cache line with them)."""
+    g = torch.Generator(device="cuda").manual_seed(dim)
+    h = tbe.tbe_layer_norm_create(dim, dtype)
+    x, r, grad, up = (torch.randn((rows, dim), generator=g, device="cuda").to(dtype) for _ in range(4))
+    w, b = torch.randn((2, dim), generator=g, device="cuda").to(dtype)
+    out, total, stats = tbe.tbe_layer_norm_forward(h, x, w, b, r)
+    for names in (("out", "total"), ("total", "out")):
+        places = dict(zip(names, (x.clone(), r.clone())))
+        first, second = places[names[0]], places[names[1]]
+        got = tbe.tbe_layer_norm_forward(h, first, w, b, second, **places)
+        assert torch.equal(got[0], out) and torch.equal(got[1], total) and torch.equal(got[2], stats), names
+    y = x.clone()
+    want = tbe.tbe_layer_norm_forward(h, x, w, b)
+    assert torch.equal(tbe.tbe_layer_norm_forward(h, y, w, b, out=y)[0], want[0])
+    want = tbe.tbe_layer_norm_backward(h, total, stats, grad, w, up)
+    for place in ("total", "grad_out", "grad_total"):
+        args = dict(total=total, grad_out=grad, grad_total=up)
+        args[place] = args[place].clone()
+        got = tbe.tbe_layer_norm_backward(h, stats=stats, weight=w, grad_x=args[place], **args)
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), place
