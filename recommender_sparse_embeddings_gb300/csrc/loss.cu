@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(256) loss_max_kernel(const RowsIn p) {
 // target of little weight has no rounding, where -g would be off by the same 2^-9
 // in every row (grad_table of 300 rows over 5000 items in bf16: 0.0025 off, so
 // 0.0017).  fp16's range is narrow besides (6e-8 to 65504): there d comes times
-// kTargetUnit = 2^14, and weights down to 2^-28 keep all their bits.
+// target_unit = 2^14, and weights down to 2^-28 keep all their bits.
 template <int DT>
 __global__ void __launch_bounds__(256) loss_rows_kernel(const RowsIn p) {
     chain_wait();
@@ -229,11 +229,14 @@ int64_t up_to(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
 // Bytes of a piece of d (per plane of fp32's three).  Long pieces make few
 // launches, each with a start and an end in which SMs idle; shorter ones would
-// stay in L2 (129 MB), which gains less.  4096 x 32768 x 512 bf16 in pieces of 48
-// MB 445 us, 64 MB 412, 100 MB 353, 150 MB 380; 8192 x 20000 x 256 fp32 1543, 1424,
-// 1404, 1398.
+// stay in L2 (129 MB), which gains less.  Pieces of 48, 64, 96 and 150 MB: 4096 x
+// 32768 x 512 bf16 473, 442, 379 and 369 us, 8192 x 20000 x 256 fp32 1733, 1537, 1384
+// and 1426, 2048 x 30000 x 4096 bf16 1215, 1174, 1269 and 1380.
 constexpr int64_t kPieceBytes = 96 << 20;
-// Work items that the sums' parts make at most.
+// Work items that the sums' parts make at most: four a SM of the 152, as many and
+// as few as even out (forward 8192 x 131072 x 256 bf16 338 us; 304 items 387, 1216 337,
+// with twice the room).  The slices tried below are a few small numbers and the SMs'
+// count, its half and multiples; a GPU of other counts would be served, less evenly.
 constexpr int kMostParts = 608;
 constexpr int kRowCtas = 1024;
 

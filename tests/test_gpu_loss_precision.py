@@ -90,6 +90,20 @@ def test_long_sums_over_the_rows(dtype, n, v, d):
     assert off(c.grad_x[at], c.rows(at)[2]) < 3.0e-4 + 2 ** -13
 
 
+@pytest.mark.parametrize("copied", [False, True])
+def test_long_sums_over_the_rows_of_many_items(copied):
+    """More tiles of items than the sums' parts otherwise have room for; copied, in two spans of the table."""
+    c = Case(FP16, 33000, 200000, 64)
+    if copied:
+        c.table = torch.cat([c.table, c.table[:, :1]], 1)[:, :64]
+    c.run()
+    for at in (0, 65536, 131000, 131072, 199900):
+        at = torch.arange(at, at + 100, device="cuda")
+        assert off(c.grad_table[at], c.items(at)) < 3.0e-4 + 2 ** -13
+    at = torch.arange(0, 33000, 1100, device="cuda")
+    assert off(c.grad_x[at], c.rows(at)[2]) < 3.0e-4 + 2 ** -13
+
+
 def test_long_sums_over_the_rows_of_wide_operands():
     """Above 256 columns d passes through memory in pieces; here of 256 items, whose sums go over 36,864 rows each."""
     c = Case(FP16, 700000, 250, 4096, targets_from=16)
